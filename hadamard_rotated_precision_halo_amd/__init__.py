@@ -33,7 +33,9 @@ EXPORTS = ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
            "halo_gemm_i8", "halo_gemm_fp8", "halo_linear_workspace_bytes",
            "halo_linear_workspace_bytes_ex", "halo_linear_fwd", "halo_linear_fwd_ex",
            "halo_linear_bwd", "halo_linear_bwd_ex", "halo_fwht_quant_dual",
-           "halo_fwht_quant_dual_workspace_bytes", "halo_mfma_rate_probe", "halo_status_str")
+           "halo_fwht_quant_dual_workspace_bytes", "halo_mfma_rate_probe", "halo_status_str",
+           "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_block_norm_bwd_workspace_bytes",
+           "halo_distill_fwd", "halo_distill_bwd", "halo_distill_fwd_bwd")
 
 
 class QuantOpts(ctypes.Structure):
@@ -97,12 +99,28 @@ def lib():
         L.halo_fwht_quant_dual_workspace_bytes.restype = sz
         L.halo_fwht_quant_dual.argtypes = [vp, e, i64, i64, i64, i32, e, vp, i64, vp, vp, i64, vp,
                                            qo, qo, vp, sz, vp]
+        f32 = ctypes.c_float
+        L.halo_block_norm_fwd.argtypes = [vp, i64, vp, i64, vp, i64, i64, vp, vp, e, i64, i64, f32,
+                                          f32, vp, i64, vp, i64, vp, vp, vp]
+        L.halo_block_norm_bwd_workspace_bytes.argtypes = [i64, i64, i64, e]
+        L.halo_block_norm_bwd_workspace_bytes.restype = sz
+        L.halo_block_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, vp,
+                                          vp, vp, e, i64, i64, f32, vp, i64, vp, i64, vp, vp, vp,
+                                          vp, sz, vp]
+        L.halo_distill_fwd.argtypes = [vp, e, i64, vp, i64, vp, e, i64, i64, i64, i64, f32, vp, vp,
+                                       vp]
+        L.halo_distill_bwd.argtypes = [vp, vp, e, i64, vp, vp, i64, vp, e, i64, i64, i64, i64, f32,
+                                       vp, i64, vp]
+        L.halo_distill_fwd_bwd.argtypes = [vp, e, i64, vp, i64, vp, e, i64, vp, i64, i64, i64, f32,
+                                           vp, vp, vp, i64, vp]
         L.halo_status_str.argtypes = [e]
         L.halo_status_str.restype = ctypes.c_char_p
         for f in ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
                   "halo_gemm_i8", "halo_gemm_fp8",
                   "halo_linear_fwd", "halo_linear_fwd_ex", "halo_linear_bwd",
-                  "halo_linear_bwd_ex", "halo_fwht_quant_dual", "halo_mfma_rate_probe"):
+                  "halo_linear_bwd_ex", "halo_fwht_quant_dual", "halo_mfma_rate_probe",
+                  "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_distill_fwd",
+                  "halo_distill_bwd", "halo_distill_fwd_bwd"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -527,3 +545,242 @@ def linear_bwd(dy, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, want_dx=T
                                   ws.numel() * ws.element_size(), _stream(stream))
     _check(st, "halo_linear_bwd_ex")
     return (dx if want_dx else None), (dw if want_dw else None)
+
+
+# ---------------------------------------------------------------------------
+# the join between two blocks, and the distillation loss
+# ---------------------------------------------------------------------------
+
+def _rows(t, name, shape, dtype, device):
+    """A 2-D argument of exactly shape and dtype with unit column stride and any row stride of
+    at least its width; returns the row stride."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and tuple(t.shape) == shape
+            and t.dtype == dtype and t.device == device):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
+    ld = t.stride(0)
+    if t.shape[0] <= 1:  # one row: its stride says nothing
+        ld = max(ld, shape[1])
+    if t.numel() and ((shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]):
+        raise ValueError(f"{name} must be row-major with unit column stride")
+    return max(ld, shape[1])
+
+
+def _vec(t, name, n, dtype, device):
+    """A contiguous 1-D argument of exactly n entries."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 1 and t.shape[0] == n and t.dtype == dtype
+            and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on {device}")
+
+
+def _io_2d(t, name):
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2):
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError("the inputs must be GPU tensors")
+    return t.dtype, t.device
+
+
+def _current_stream(device, stream):
+    """The HIP stream of a call on tensors of `device`: `stream`, or that device's current one."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scale=1.0, eps=1e-6,
+                   r_out=None, h=None, stream=None):
+    """The join between two blocks (halo_block_norm_fwd): the block output y enters the residual
+    stream r under a norm, a gate and a residual scale, and the next block's input is normalised,
+
+        a = 1 / sqrt(mean(y^2) + eps),      r_out = r + scale * gate * (y * a * post_weight),
+        b = 1 / sqrt(mean(r_out^2) + eps),  h = r_out * b * pre_weight,
+
+    each mean over the features of a token (a row of r and y, bf16 or fp32).  y None: only
+    h = norm(r).  gate: [groups, dim] (or [dim]), row g for the g-th run of tokens / groups
+    consecutive tokens, or None.  post_weight None: y joins without a norm; pre_weight None: no
+    norm after the join.  Returns (r_out, h, rstd_post, rstd_pre): r itself without y, None for h
+    and for the fp32 factors of norms that were not asked for.
+    """
+    dt, dev = _io_2d(r, "r")
+    t, d = shape = tuple(r.shape)
+    ldr = _rows(r, "r", shape, dt, dev)
+    ldy = ldro = ldh = ldg = 0
+    groups = 1
+    rstd_post = rstd_pre = None
+    if y is not None:
+        ldy = _rows(y, "y", shape, dt, dev)
+        if gate is not None:
+            if gate.dim() == 1:
+                gate = gate.unsqueeze(0)
+            groups = gate.shape[0]
+            ldg = _rows(gate, "gate", (groups, d), dt, dev)
+        if post_weight is not None:
+            _vec(post_weight, "post_weight", d, dt, dev)
+            rstd_post = torch.empty(t, dtype=torch.float32, device=dev)
+        if r_out is None:
+            r_out = torch.empty(shape, dtype=dt, device=dev)
+        ldro = _rows(r_out, "r_out", shape, dt, dev)
+    elif gate is not None or post_weight is not None or r_out is not None:
+        raise ValueError("gate, post_weight and r_out need y")
+    if pre_weight is not None:
+        _vec(pre_weight, "pre_weight", d, dt, dev)
+        rstd_pre = torch.empty(t, dtype=torch.float32, device=dev)
+        if h is None:
+            h = torch.empty(shape, dtype=dt, device=dev)
+        ldh = _rows(h, "h", shape, dt, dev)
+    elif h is not None:
+        raise ValueError("h needs pre_weight")
+    st = lib().halo_block_norm_fwd(_p(r), ldr, _p(y), ldy, _p(gate), ldg, groups, _p(post_weight),
+                                   _p(pre_weight), _TORCH_CODE[dt], t, d, scale, eps, _p(r_out),
+                                   ldro, _p(h), ldh, _p(rstd_post), _p(rstd_pre),
+                                   _current_stream(dev, stream))
+    _check(st, "halo_block_norm_fwd")
+    return (r if y is None else r_out), h, rstd_post, rstd_pre
+
+
+def block_norm_bwd_workspace_bytes(tokens, dim, groups=1, dtype=torch.bfloat16):
+    return int(lib().halo_block_norm_bwd_workspace_bytes(tokens, dim, groups, _code(dtype)))
+
+
+def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_weight=None,
+                   rstd_post=None, rstd_pre=None, scale=1.0, dr=None, dy=None, want_dgate=True,
+                   want_dpost=True, want_dpre=True, workspace=None, stream=None):
+    """Gradient of block_norm_fwd: from dr_out (the gradient arriving at the residual stream, or
+    None) and dh, with the forward's r_out, y, weights and factors, returns (dr, dy, dgate,
+    dpost_weight, dpre_weight); None for what does not exist or is not wanted.  dgate is
+    [groups, dim].  The parameter gradients are fp32 sums in a fixed order, rounded once."""
+    ref = dr_out if dr_out is not None else dh
+    dt, dev = _io_2d(ref, "dr_out" if dr_out is not None else "dh")
+    t, d = shape = tuple(ref.shape)
+    if t == 0:
+        raise ValueError("the gradient needs at least one token")
+    lddro = lddh = ldro = ldy = ldg = lddy = 0
+    groups = 1
+    dgate = dpost = dpre = None
+    if dr_out is not None:
+        lddro = _rows(dr_out, "dr_out", shape, dt, dev)
+    if pre_weight is not None:
+        _vec(pre_weight, "pre_weight", d, dt, dev)
+        _vec(rstd_pre, "rstd_pre", t, torch.float32, dev)
+        lddh = _rows(dh, "dh", shape, dt, dev)
+        ldro = _rows(r_out, "r_out", shape, dt, dev)
+        if want_dpre:
+            dpre = torch.empty(d, dtype=dt, device=dev)
+    elif dh is not None:
+        raise ValueError("dh needs pre_weight")
+    if y is not None:
+        ldy = _rows(y, "y", shape, dt, dev)
+        if gate is not None:
+            if gate.dim() == 1:
+                gate = gate.unsqueeze(0)
+            groups = gate.shape[0]
+            ldg = _rows(gate, "gate", (groups, d), dt, dev)
+            if want_dgate:
+                dgate = torch.empty((groups, d), dtype=dt, device=dev)
+        if post_weight is not None:
+            _vec(post_weight, "post_weight", d, dt, dev)
+            _vec(rstd_post, "rstd_post", t, torch.float32, dev)
+            if want_dpost:
+                dpost = torch.empty(d, dtype=dt, device=dev)
+        if dy is None:
+            dy = torch.empty(shape, dtype=dt, device=dev)
+        lddy = _rows(dy, "dy", shape, dt, dev)
+    elif gate is not None or post_weight is not None or dy is not None:
+        raise ValueError("gate, post_weight and dy need y")
+    if dr is None:
+        dr = torch.empty(shape, dtype=dt, device=dev)
+    lddr = _rows(dr, "dr", shape, dt, dev)
+    L = lib()
+    code = _TORCH_CODE[dt]
+    if workspace is None:
+        need = L.halo_block_norm_bwd_workspace_bytes(t, d, groups, code)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        _bytes(workspace, "workspace")
+        _same_gpu(ref, workspace=workspace)
+    st = L.halo_block_norm_bwd(_p(dr_out), lddro, _p(dh), lddh,
+                               _p(r_out) if pre_weight is not None else None, ldro, _p(y), ldy,
+                               _p(gate), ldg, groups, _p(post_weight), _p(pre_weight),
+                               _p(rstd_post) if post_weight is not None else None, _p(rstd_pre),
+                               code, t, d, scale, _p(dr), lddr, _p(dy), lddy, _p(dgate),
+                               _p(dpost), _p(dpre), _p(workspace), workspace.numel(),
+                               _current_stream(dev, stream))
+    _check(st, "halo_block_norm_bwd")
+    return dr, dy, dgate, dpost, dpre
+
+
+def _distill_args(logits, idx, tlogits):
+    dt, dev = _io_2d(logits, "logits")
+    t, v = logits.shape
+    ldl = _rows(logits, "logits", (t, v), dt, dev)
+    if not (isinstance(tlogits, torch.Tensor) and tlogits.dim() == 2):
+        raise ValueError("tlogits must be a 2-D tensor")
+    tt = tlogits.dtype
+    if tt is not torch.float32 and tt is not torch.bfloat16:
+        raise TypeError(f"unsupported dtype {tt}")
+    top = tlogits.shape[1]
+    ldt = _rows(tlogits, "tlogits", (t, top), tt, dev)
+    ldi = _rows(idx, "idx", (t, top), torch.int32, dev)
+    return dt, dev, t, v, top, ldl, ldi, ldt, _TORCH_CODE[tt]
+
+
+def distill_fwd(logits, idx, tlogits, temperature=1.0, loss=None, lse=None, stream=None):
+    """Distillation loss of every token from a teacher's top logits (halo_distill_fwd):
+    temperature^2 * sum_k p_k (log p_k - log q[idx_k]) with p the softmax of the kept teacher
+    logits (tlogits [tokens, top], at vocabulary indices idx, int32; an index outside the
+    vocabulary, such as -1, is no entry) and q the softmax of the student's logits, both at the
+    temperature.  Returns (loss, lse), fp32 per token; lse = log sum exp(logits / temperature)."""
+    dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
+    loss = _out_vec(loss, "loss", t, dev)
+    lse = _out_vec(lse, "lse", t, dev)
+    st = lib().halo_distill_fwd(_p(logits), _TORCH_CODE[dt], ldl, _p(idx), ldi, _p(tlogits), tc,
+                                ldt, t, v, top, temperature, _p(loss), _p(lse),
+                                _current_stream(dev, stream))
+    _check(st, "halo_distill_fwd")
+    return loss, lse
+
+
+def _out_vec(t, name, n, dev):
+    if t is None:
+        return torch.empty(n, dtype=torch.float32, device=dev)
+    _vec(t, name, n, torch.float32, dev)
+    return t
+
+
+def distill_bwd(dloss, logits, lse, idx, tlogits, temperature=1.0, dlogits=None, stream=None):
+    """Gradient of distill_fwd for the logits: dloss[t] * temperature * (q - p) per token, from
+    the forward's lse.  dlogits may be logits itself."""
+    dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
+    _vec(dloss, "dloss", t, torch.float32, dev)
+    _vec(lse, "lse", t, torch.float32, dev)
+    if dlogits is None:
+        dlogits = torch.empty((t, v), dtype=dt, device=dev)
+    ldd = _rows(dlogits, "dlogits", (t, v), dt, dev)
+    st = lib().halo_distill_bwd(_p(dloss), _p(logits), _TORCH_CODE[dt], ldl, _p(lse), _p(idx), ldi,
+                                _p(tlogits), tc, ldt, t, v, top, temperature, _p(dlogits), ldd,
+                                _current_stream(dev, stream))
+    _check(st, "halo_distill_bwd")
+    return dlogits
+
+
+def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse=None,
+                    dlogits=None, stream=None):
+    """distill_fwd and distill_bwd from one read of the logits, for training steps that know each
+    token's weight in the loss beforehand (dloss; 0 leaves a token out).  Returns (loss, lse,
+    dlogits); dlogits may be logits itself."""
+    dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
+    _vec(dloss, "dloss", t, torch.float32, dev)
+    loss = _out_vec(loss, "loss", t, dev)
+    lse = _out_vec(lse, "lse", t, dev)
+    if dlogits is None:
+        dlogits = torch.empty((t, v), dtype=dt, device=dev)
+    ldd = _rows(dlogits, "dlogits", (t, v), dt, dev)
+    st = lib().halo_distill_fwd_bwd(_p(logits), _TORCH_CODE[dt], ldl, _p(idx), ldi, _p(tlogits),
+                                    tc, ldt, _p(dloss), t, v, top, temperature, _p(loss), _p(lse),
+                                    _p(dlogits), ldd, _current_stream(dev, stream))
+    _check(st, "halo_distill_fwd_bwd")
+    return loss, lse, dlogits

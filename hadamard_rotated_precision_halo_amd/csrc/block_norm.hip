@@ -1,0 +1,626 @@
+// block_norm.hip -- the join between two blocks of a model, forward and backward (gfx950).
+//
+// Forward.  A block's output y joins the residual stream r and the next block's input is
+// normalised (every mean over the D elements of a token's row):
+//   a = 1 / sqrt(mean(y^2) + eps),     r' = r + scale gate (y a post_weight)
+//   b = 1 / sqrt(mean(r'^2) + eps),    h  = r' b pre_weight
+// r' stays in fp32 between the two norms; each output is rounded once.
+//
+// Backward, with rhat = r' b, yhat = y a, u = dh pre_weight, c = scale gate post_weight:
+//   G  = dr' + b (u - rhat mean(u rhat))              (dr = G)
+//   dy = a (c G - yhat mean(c G yhat))
+//   dgate = sum scale G yhat post_weight,  dpost = sum scale gate G yhat,  dpre = sum dh rhat
+// The second mean is linear in the first: mean(c G yhat) = mean(c yhat (dr' + b u)) -
+// mean(u rhat) mean(c yhat b rhat), so one pass over the row and one joint reduction of three
+// sums give both, and a row is read once.
+//
+// Mapping.  Both directions are bound by memory: a row (or several) is held in registers as
+// 16-byte chunks by a team of NW waves, CH chunks per lane, read once and written once.  A row
+// whose length the chunk does not divide ends in a chunk that is moved back to end at the row's
+// last element; the elements it shares with the chunk before are computed twice (the same
+// values) and counted once.
+// The backward's parameter gradients are sums over tokens: a team keeps its columns' sums in
+// registers over its rows, a workgroup folds its teams through the LDS and writes one partial
+// row per sum, and a second launch adds the partial rows in a fixed order (no atomics: the
+// results do not change between runs).
+#include "halo_kernels.h"
+#include "rowops.h"
+
+namespace halo {
+
+namespace {
+
+// One chunk's place in a row of d elements: chunk c starts at element min(c VEC, d - VEC) and
+// counts its elements from c VEC on (`from`: elements below are the chunk before's).
+template <int VEC>
+struct Place {
+  int at, from;
+  bool in;
+};
+template <int VEC, bool ODD>
+__device__ __forceinline__ Place<VEC> place_of(int c, int d) {
+  Place<VEC> p;
+  const int start = c * VEC;
+  p.in = start < d;
+  p.at = p.in ? (ODD ? min(start, d - VEC) : start) : 0;
+  p.from = ODD ? start - p.at : 0;
+  return p;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ uint4 get(const T* row, int at) {
+  if constexpr (VEC == 1) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (sizeof(T) == 2) w.x = *reinterpret_cast<const uint16_t*>(row + at);
+    else w.x = *reinterpret_cast<const uint32_t*>(row + at);
+    return w;
+  } else {
+    return load16u(row + at);
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void val(uint4 w, float* o) {
+  if constexpr (VEC == 1) o[0] = sizeof(T) == 2 ? __uint_as_float(w.x << 16) : __uint_as_float(w.x);
+  else unpack16<T>(w, o);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void put(T* row, int at, const float* v) {
+  if constexpr (VEC == 1) elem_store<T>(row + at, v[0]);
+  else store16u(row + at, pack16<T>(v));
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+
+// Sum over the NW waves of a team (NW == 1: the wave).  `s` holds one float per wave of the
+// workgroup; each call uses its own slot array, so one barrier per call is enough.
+template <int NW>
+__device__ __forceinline__ float team_sum(float v, float* s, int wave, int team) {
+  v = wave_sum(v);
+  if constexpr (NW > 1) {
+    if ((threadIdx.x & 63) == 0) s[wave] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) v += s[team * NW + i];
+  }
+  return v;
+}
+
+// NW waves per token, 4 waves (or NW) per workgroup.
+template <typename T, int VEC, bool ODD, int NW, int CH>
+__global__ __launch_bounds__(64 * (NW > 4 ? NW : 4)) void norm_fwd_kernel(NormFwdArgs a) {
+  constexpr int WAVES = NW > 4 ? NW : 4, TEAMS = WAVES / NW;
+  __shared__ float s_post[WAVES], s_pre[WAVES];
+  const int wave = threadIdx.x >> 6, team = wave / NW;
+  const int tl = threadIdx.x - team * NW * 64;  // thread within the team
+  const int64_t tok = (int64_t)blockIdx.x * TEAMS + team;
+  if (tok >= a.tokens) return;  // only where a wave is a team: no barrier follows
+  const int64_t t = tok;
+  const int d = a.dim;
+  const T* r = reinterpret_cast<const T*>(a.r) + t * a.ldr;
+  const T* y = reinterpret_cast<const T*>(a.y) + t * a.ldy;
+  Place<VEC> pl[CH];
+  uint4 rr[CH], yr[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
+  if (a.y) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) yr[j] = get<T, VEC>(y, pl[j].at);
+  }
+#pragma unroll
+  for (int j = 0; j < CH; ++j) rr[j] = get<T, VEC>(r, pl[j].at);
+
+  float x[CH][VEC];
+  float inv_post = 1.f;
+  if (a.y) {
+    if (a.post) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        float v[VEC];
+        val<T, VEC>(yr[j], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (pl[j].in && (!ODD || e >= pl[j].from)) ss = __builtin_fmaf(v[e], v[e], ss);
+      }
+      ss = team_sum<NW>(ss, s_post, wave, team);
+      inv_post = 1.f / sqrtf(ss * a.inv_dim + a.eps);
+      if (a.rstd_post && tl == 0) a.rstd_post[t] = inv_post;
+    }
+    const T* gate = reinterpret_cast<const T*>(a.gate) + (a.gate ? (t / a.group_len) * a.ldg : 0);
+    const T* post = reinterpret_cast<const T*>(a.post);
+    const float k = a.scale * inv_post;
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float yv[VEC], rv[VEC], c[VEC];
+      val<T, VEC>(yr[j], yv);
+      val<T, VEC>(rr[j], rv);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) c[e] = k;
+      if (post) {
+        float w[VEC];
+        val<T, VEC>(get<T, VEC>(post, pl[j].at), w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) c[e] *= w[e];
+      }
+      if (a.gate) {
+        float w[VEC];
+        val<T, VEC>(get<T, VEC>(gate, pl[j].at), w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) c[e] *= w[e];
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[j][e] = __builtin_fmaf(c[e], yv[e], rv[e]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) val<T, VEC>(rr[j], x[j]);
+  }
+  // with no norm on either side no reduction has ordered this row's loads before its stores,
+  // which may overlap them (r_out may be r, and a moved-back chunk shares elements)
+  if (NW > 1 && !a.pre && !a.post) __syncthreads();
+  float inv_pre = 1.f;
+  if (a.pre) {
+    float ss = 0.f;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (pl[j].in && (!ODD || e >= pl[j].from)) ss = __builtin_fmaf(x[j][e], x[j][e], ss);
+    ss = team_sum<NW>(ss, s_pre, wave, team);
+    inv_pre = 1.f / sqrtf(ss * a.inv_dim + a.eps);
+    if (a.rstd_pre && tl == 0) a.rstd_pre[t] = inv_pre;
+  }
+  if (a.y) {
+    T* ro = reinterpret_cast<T*>(a.r_out) + t * a.ldro;
+#pragma unroll
+    for (int j = 0; j < CH; ++j)
+      if (pl[j].in) put<T, VEC>(ro, pl[j].at, x[j]);
+  }
+  if (a.pre) {
+    T* h = reinterpret_cast<T*>(a.h) + t * a.ldh;
+    const T* pre = reinterpret_cast<const T*>(a.pre);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float w[VEC];
+      val<T, VEC>(get<T, VEC>(pre, pl[j].at), w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] *= x[j][e] * inv_pre;
+      if (pl[j].in) put<T, VEC>(h, pl[j].at, w);
+    }
+  }
+}
+
+template <typename T, int VEC, bool ODD, int NW, int CH>
+hipError_t run_fwd(const NormFwdArgs& a, hipStream_t st) {
+  constexpr int WAVES = NW > 4 ? NW : 4, TEAMS = WAVES / NW;
+  const int64_t grid = (a.tokens + TEAMS - 1) / TEAMS;
+  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, ODD, NW, CH>), dim3((unsigned)grid),
+                     dim3(64 * WAVES), 0, st, a);
+  return hipGetLastError();
+}
+
+// Waves per token: the fewest that hold a row in at most 8 chunks per lane; 4 or 16 when the
+// tokens alone would leave most of the device idle (fewer than one 4-wave workgroup per compute
+// unit): a row then arrives in one or two loads per lane and its latency is the call's.
+template <typename T, int VEC, bool ODD>
+hipError_t pick_fwd(const NormFwdArgs& a, hipStream_t st) {
+  const int64_t chunks = (a.dim + VEC - 1) / VEC;
+  const bool few = a.tokens <= 1024;
+  const int64_t per = (chunks + 63) / 64;  // chunks per lane of one wave
+  if (per <= 1) return run_fwd<T, VEC, ODD, 1, 1>(a, st);
+  if (few) {
+    if (per <= 4) return run_fwd<T, VEC, ODD, 4, 1>(a, st);
+    if (per <= 16) return run_fwd<T, VEC, ODD, 16, 1>(a, st);
+  }
+  if (per <= 2) return run_fwd<T, VEC, ODD, 1, 2>(a, st);
+  if (per <= 4) return run_fwd<T, VEC, ODD, 1, 4>(a, st);
+  if (per <= 8) return run_fwd<T, VEC, ODD, 1, 8>(a, st);
+  if (per <= 16) return run_fwd<T, VEC, ODD, 4, 4>(a, st);
+  if (per <= 32) return run_fwd<T, VEC, ODD, 4, 8>(a, st);
+  if (per <= 64) return run_fwd<T, VEC, ODD, 16, 4>(a, st);
+  return run_fwd<T, VEC, ODD, 16, 8>(a, st);
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
+
+// Row plan of the backward: workgroup i handles rows_per_wg consecutive rows of one gate group
+// (chunks_per_group workgroups per group), its teams taking rows in turn; or, where groups are
+// shorter than a team's share (whole_groups > 0), whole_groups consecutive groups, its teams
+// taking groups in turn and writing their gate gradients themselves.
+struct NormPlan {
+  int64_t wgs, rows_per_wg, chunks_per_group, whole_groups;
+};
+
+constexpr int kBwdWaves = 8;
+
+// Waves per token and chunks per lane of the backward for a row of `chunks` chunks.
+void bwd_shape(int64_t chunks, int* nw, int* ch) {
+  const int64_t per = (chunks + 63) / 64;
+  *nw = per <= 1 ? 1 : per <= 2 ? 1 : per <= 4 ? 2 : per <= 8 ? 4 : 8;
+  *ch = per <= 1 ? 1 : per <= 16 ? 2 : per <= 32 ? 4 : 8;
+}
+
+NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
+  NormPlan p{};
+  // one workgroup per compute unit: its teams keep enough rows in flight, and the partial sums
+  // (one row per workgroup) stay few
+  int64_t rows = (tokens + 255) / 256;
+  if (rows < teams) rows = teams;
+  if (group_len * teams <= rows) {
+    p.whole_groups = rows / group_len;
+    const int64_t groups = tokens / group_len;
+    p.rows_per_wg = p.whole_groups * group_len;
+    p.wgs = (groups + p.whole_groups - 1) / p.whole_groups;
+    p.chunks_per_group = 0;
+    return p;
+  }
+  p.chunks_per_group = (group_len + rows - 1) / rows;
+  p.rows_per_wg = (group_len + p.chunks_per_group - 1) / p.chunks_per_group;
+  p.chunks_per_group = (group_len + p.rows_per_wg - 1) / p.rows_per_wg;
+  p.wgs = p.chunks_per_group * (tokens / group_len);
+  return p;
+}
+
+template <typename T, int VEC, bool ODD, int NW, int CH>
+__global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a, NormPlan pn) {
+  constexpr int TEAMS = kBwdWaves / NW;
+  __shared__ float s_red[2][3][kBwdWaves];
+  extern __shared__ float s_fold[];  // TEAMS > 1: (TEAMS - 1) x (columns) x 3 floats, see below
+  const int wave = threadIdx.x >> 6, team = wave / NW;
+  const int tl = threadIdx.x - team * NW * 64;
+  const int d = a.dim;
+  const T* gate = reinterpret_cast<const T*>(a.gate);
+  const T* post = reinterpret_cast<const T*>(a.post);
+  const T* pre = reinterpret_cast<const T*>(a.pre);
+
+  Place<VEC> pl[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
+  // the weights of the lane's columns, in their stored form
+  uint4 wpost[CH], wpre[CH], wgate[CH];
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    if (post) wpost[j] = get<T, VEC>(post, pl[j].at);
+    if (pre) wpre[j] = get<T, VEC>(pre, pl[j].at);
+  }
+  float spost[CH][VEC], spre[CH][VEC], sgate[CH][VEC];
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) spost[j][e] = spre[j][e] = sgate[j][e] = 0.f;
+
+  // the team's rows
+  int64_t row0, nrows, step, iters, group = 0;
+  if (pn.whole_groups > 0) {
+    const int64_t groups = a.tokens / a.group_len;
+    const int64_t g0 = (int64_t)blockIdx.x * pn.whole_groups;
+    const int64_t ng = min(pn.whole_groups, groups - g0);
+    row0 = g0 * a.group_len;
+    nrows = ng * a.group_len;
+    step = 0;
+    iters = (ng + TEAMS - 1) / TEAMS * a.group_len;
+    group = g0;
+  } else {
+    group = (int64_t)blockIdx.x / pn.chunks_per_group;
+    const int64_t c = (int64_t)blockIdx.x % pn.chunks_per_group;
+    row0 = group * a.group_len + c * pn.rows_per_wg;
+    nrows = min(pn.rows_per_wg, a.group_len - c * pn.rows_per_wg);
+    step = TEAMS;
+    iters = (nrows + TEAMS - 1) / TEAMS;
+    if (gate) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) wgate[j] = get<T, VEC>(gate + group * a.ldg, pl[j].at);
+    }
+  }
+  for (int64_t it = 0; it < iters; ++it) {
+    int64_t off;  // row within the workgroup's range
+    if (step > 0) {
+      off = it * step + team;
+    } else {  // whole groups: team q takes groups q, q + TEAMS, ...
+      const int64_t gi = it / a.group_len * TEAMS + team;
+      off = gi * a.group_len + it % a.group_len;
+      if (gate && it % a.group_len == 0 && off < nrows) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j) wgate[j] = get<T, VEC>(gate + (group + gi) * a.ldg, pl[j].at);
+      }
+    }
+    const bool live = off < nrows;
+    const int64_t t = row0 + (live ? off : 0);
+    uint4 gr[CH], hr[CH], rr[CH], yr[CH];
+    if (a.dr_out) {
+      const T* p = reinterpret_cast<const T*>(a.dr_out) + t * a.lddro;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) gr[j] = get<T, VEC>(p, pl[j].at);
+    }
+    if (pre) {
+      const T* p = reinterpret_cast<const T*>(a.dh) + t * a.lddh;
+      const T* q = reinterpret_cast<const T*>(a.r_out) + t * a.ldro;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) hr[j] = get<T, VEC>(p, pl[j].at);
+#pragma unroll
+      for (int j = 0; j < CH; ++j) rr[j] = get<T, VEC>(q, pl[j].at);
+    }
+    if (a.y) {
+      const T* p = reinterpret_cast<const T*>(a.y) + t * a.ldy;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) yr[j] = get<T, VEC>(p, pl[j].at);
+    }
+    const float b = pre ? a.rstd_pre[t] : 0.f;
+    const float ar = post ? a.rstd_post[t] : 1.f;
+    // the three sums: m1 = sum u rhat, A = sum c yhat (dr' + b u), B = sum c yhat b rhat
+    float m1 = 0.f, sa = 0.f, sb = 0.f;
+    float G[CH][VEC];  // dr' + b u, then G
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      float u[VEC], rv[VEC], yv[VEC], c[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) G[j][e] = 0.f;
+      if (a.dr_out) val<T, VEC>(gr[j], G[j]);
+      if (pre) {
+        float w[VEC];
+        val<T, VEC>(hr[j], u);
+        val<T, VEC>(rr[j], rv);
+        val<T, VEC>(wpre[j], w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          rv[e] *= b;
+          u[e] *= w[e];
+          G[j][e] = __builtin_fmaf(b, u[e], G[j][e]);
+          if (pl[j].in && (!ODD || e >= pl[j].from)) m1 = __builtin_fmaf(u[e], rv[e], m1);
+        }
+      }
+      if (post) {
+        float w[VEC];
+        val<T, VEC>(yr[j], yv);
+        val<T, VEC>(wpost[j], c);
+        if (gate) {
+          val<T, VEC>(wgate[j], w);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) c[e] *= w[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float cy = c[e] * (yv[e] * ar);
+          if (pl[j].in && (!ODD || e >= pl[j].from)) {
+            sa = __builtin_fmaf(cy, G[j][e], sa);
+            if (pre) sb = __builtin_fmaf(cy * b, rv[e], sb);
+          }
+        }
+      }
+    }
+    m1 = wave_sum(m1);
+    sa = wave_sum(sa);
+    sb = wave_sum(sb);
+    if constexpr (NW > 1) {
+      float(*s)[kBwdWaves] = s_red[it & 1];  // the other buffer is still being read
+      if ((tl & 63) == 0) {
+        s[0][wave] = m1;
+        s[1][wave] = sa;
+        s[2][wave] = sb;
+      }
+      __syncthreads();
+      m1 = sa = sb = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        m1 += s[0][team * NW + i];
+        sa += s[1][team * NW + i];
+        sb += s[2][team * NW + i];
+      }
+    }
+    m1 *= a.inv_dim;
+    const float bm = b * m1;
+    const float m2 = (sa - m1 * sb) * a.scale * a.inv_dim;
+    if (live) {
+      T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
+      T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+        if (pre) {
+          float u[VEC], rv[VEC];
+          val<T, VEC>(hr[j], u);
+          val<T, VEC>(rr[j], rv);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float rhat = rv[e] * b;
+            G[j][e] = __builtin_fmaf(-bm, rhat, G[j][e]);
+            spre[j][e] = __builtin_fmaf(u[e], rhat, spre[j][e]);
+          }
+        }
+        if (pl[j].in) put<T, VEC>(dr, pl[j].at, G[j]);
+        if (a.y) {
+          float yv[VEC], wp[VEC], wg[VEC], o[VEC];
+          val<T, VEC>(yr[j], yv);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) wp[e] = wg[e] = 1.f;
+          if (post) val<T, VEC>(wpost[j], wp);
+          if (gate) val<T, VEC>(wgate[j], wg);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float yhat = yv[e] * ar, sG = a.scale * G[j][e];
+            const float gy = sG * yhat;
+            sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
+            spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
+            const float cG = sG * wg[e] * wp[e];
+            o[e] = post ? ar * __builtin_fmaf(-m2, yhat, cG) : cG;
+          }
+          if (pl[j].in) put<T, VEC>(dy, pl[j].at, o);
+        }
+      }
+      // whole groups: the group's last row writes its gate gradient
+      if (step == 0 && it % a.group_len == a.group_len - 1) {
+        if (a.dgate) {
+          T* dg = reinterpret_cast<T*>(a.dgate) + (t / a.group_len) * (int64_t)d;
+#pragma unroll
+          for (int j = 0; j < CH; ++j)
+            if (pl[j].in) put<T, VEC>(dg, pl[j].at, sgate[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) sgate[j][e] = 0.f;
+      }
+    }
+  }
+  // fold the teams: team q's sums are added in team order, one sum at a time, through
+  // (TEAMS - 1) x 64 NW CH VEC floats of LDS, and the workgroup's partial rows are written
+  constexpr int COLS = NW * 64 * CH * VEC;
+  const bool want[3] = {a.part_post != nullptr, a.part_pre != nullptr,
+                        a.part_gate != nullptr && step > 0};
+  float* out[3] = {a.part_post, a.part_pre, a.part_gate};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (!want[k]) continue;
+    float(*s)[VEC] = k == 0 ? spost : k == 1 ? spre : sgate;
+    if constexpr (TEAMS > 1) {
+      __syncthreads();
+      if (team > 0) {
+#pragma unroll
+        for (int j = 0; j < CH; ++j)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            s_fold[(team - 1) * COLS + (j * VEC + e) * NW * 64 + tl] = s[j][e];
+      }
+      __syncthreads();
+    }
+    if (team == 0) {
+      float* o = out[k] + (int64_t)blockIdx.x * d;
+#pragma unroll
+      for (int j = 0; j < CH; ++j) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float v = s[j][e];
+          for (int q = 0; q < TEAMS - 1; ++q) v += s_fold[q * COLS + (j * VEC + e) * NW * 64 + tl];
+          if (pl[j].in && (!ODD || e >= pl[j].from)) o[pl[j].at + e] = v;
+        }
+      }
+    }
+  }
+}
+
+// Second launch of the backward: the partial rows of each sum, added in a fixed order.  Sum
+// rows: 0 dpost and 1 dpre over all workgroups, then the gate groups over their chunks.  A
+// workgroup takes 64 columns of one sum row; its 4 waves take the partial rows in turn and are
+// added in wave order.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_sum_kernel(NormBwdArgs a, NormPlan pn) {
+  __shared__ float s[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+  int64_t which = blockIdx.y;
+  const float* p;
+  T* o;
+  int64_t n;
+  const int nw = (a.part_post ? 1 : 0) + (a.part_pre ? 1 : 0);
+  if (which < nw) {
+    const bool is_post = a.part_post && which == 0;
+    p = is_post ? a.part_post : a.part_pre;
+    o = reinterpret_cast<T*>(is_post ? a.dpost : a.dpre);
+    n = pn.wgs;
+  } else {
+    const int64_t g = which - nw;
+    p = a.part_gate + g * pn.chunks_per_group * (int64_t)a.dim;
+    o = reinterpret_cast<T*>(a.dgate) + g * (int64_t)a.dim;
+    n = pn.chunks_per_group;
+  }
+  float v = 0.f;
+  if (col < a.dim) {
+#pragma unroll 8
+    for (int64_t i = w; i < n; i += 4) v += p[i * a.dim + col];
+  }
+  s[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && col < a.dim)
+    elem_store<T>(o + col, (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]));
+}
+
+struct BwdLayout {
+  NormPlan plan;
+  int nw, ch, vec;
+  size_t post, pre, gate, total;  // byte offsets of the partial rows
+};
+
+BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16, bool post,
+                     bool pre, bool gate) {
+  BwdLayout l{};
+  l.vec = in_bf16 ? 8 : 4;
+  if (dim < l.vec) l.vec = 1;
+  bwd_shape((dim + l.vec - 1) / l.vec, &l.nw, &l.ch);
+  l.plan = plan_bwd(tokens, group_len, kBwdWaves / l.nw);
+  const size_t rows = (size_t)l.plan.wgs * (size_t)dim * 4;
+  l.post = 0;
+  l.pre = post ? rows : 0;
+  l.gate = l.pre + (pre ? rows : 0);
+  l.total = l.gate + (gate && l.plan.whole_groups == 0 ? rows : 0);
+  return l;
+}
+
+template <typename T, int VEC, bool ODD, int NW, int CH>
+hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
+  constexpr int TEAMS = kBwdWaves / NW;
+  constexpr int LDS = (TEAMS - 1) * NW * 64 * CH * VEC * 4;
+  static_assert(LDS < 60000, "the fold's LDS fits a workgroup's default limit");
+  hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH>), dim3((unsigned)pn.wgs),
+                     dim3(64 * kBwdWaves), LDS, st, a, pn);
+  return hipGetLastError();
+}
+
+template <typename T, int VEC, bool ODD>
+hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
+  if (l.ch == 1) return run_bwd<T, VEC, ODD, 1, 1>(a, l.plan, st);
+  if (l.nw == 1) return run_bwd<T, VEC, ODD, 1, 2>(a, l.plan, st);
+  if (l.nw == 2) return run_bwd<T, VEC, ODD, 2, 2>(a, l.plan, st);
+  if (l.nw == 4) return run_bwd<T, VEC, ODD, 4, 2>(a, l.plan, st);
+  if (l.ch == 2) return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
+  if (l.ch == 4) return run_bwd<T, VEC, ODD, 8, 4>(a, l.plan, st);
+  return run_bwd<T, VEC, ODD, 8, 8>(a, l.plan, st);
+}
+
+template <typename T>
+hipError_t bwd_type(NormBwdArgs a, const BwdLayout& l, hipStream_t st) {
+  constexpr int VEC = RowType<T>::VEC;
+  hipError_t e = l.vec == 1          ? run_bwd<T, 1, false, 1, 1>(a, l.plan, st)
+                 : a.dim % VEC == 0 ? pick_bwd<T, VEC, false>(a, l, st)
+                                    : pick_bwd<T, VEC, true>(a, l, st);
+  if (e != hipSuccess) return e;
+  const int64_t sums = (a.part_post ? 1 : 0) + (a.part_pre ? 1 : 0) +
+                       (a.part_gate ? a.tokens / a.group_len : 0);
+  if (sums == 0) return hipSuccess;
+  hipLaunchKernelGGL((norm_sum_kernel<T>), dim3((unsigned)((a.dim + 63) / 64), (unsigned)sums),
+                     dim3(256), 0, st, a, l.plan);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t norm_max_dim(int in_bf16) { return in_bf16 ? 32768 : 16384; }
+
+hipError_t launch_norm_fwd(const NormFwdArgs& a, int in_bf16, hipStream_t st) {
+  if (in_bf16) {
+    if (a.dim < 8) return run_fwd<uint16_t, 1, false, 1, 1>(a, st);
+    return a.dim % 8 == 0 ? pick_fwd<uint16_t, 8, false>(a, st) : pick_fwd<uint16_t, 8, true>(a, st);
+  }
+  if (a.dim < 4) return run_fwd<float, 1, false, 1, 1>(a, st);
+  return a.dim % 4 == 0 ? pick_fwd<float, 4, false>(a, st) : pick_fwd<float, 4, true>(a, st);
+}
+
+size_t norm_bwd_ws_bytes(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16, bool post,
+                         bool pre, bool gate) {
+  return bwd_layout(tokens, dim, group_len, in_bf16, post, pre, gate).total;
+}
+
+hipError_t launch_norm_bwd(NormBwdArgs a, int in_bf16, void* ws, hipStream_t st) {
+  const BwdLayout l = bwd_layout(a.tokens, a.dim, a.group_len, in_bf16, a.dpost != nullptr,
+                                 a.dpre != nullptr, a.dgate != nullptr);
+  char* base = static_cast<char*>(ws);
+  a.part_post = a.dpost ? reinterpret_cast<float*>(base + l.post) : nullptr;
+  a.part_pre = a.dpre ? reinterpret_cast<float*>(base + l.pre) : nullptr;
+  a.part_gate = a.dgate && l.plan.whole_groups == 0 ? reinterpret_cast<float*>(base + l.gate) : nullptr;
+  return in_bf16 ? bwd_type<uint16_t>(a, l, st) : bwd_type<float>(a, l, st);
+}
+
+}  // namespace halo

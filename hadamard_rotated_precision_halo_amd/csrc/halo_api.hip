@@ -300,6 +300,52 @@ bool layer_dims_ok(int64_t m, int64_t n, int64_t k) {
   return m >= 0 && n >= 0 && k >= 0 && m < kMaxDim && n < kMaxDim && k < kMaxDim;
 }
 
+// Row operators take any stride and any alignment of whole elements.
+bool aligned_to(const void* p, int e) { return (reinterpret_cast<uintptr_t>(p) & (e - 1)) == 0; }
+
+bool norm_dims_ok(int64_t tokens, int64_t dim, int64_t groups, halo_dtype io) {
+  return tokens >= 0 && tokens < kMaxDim && dim > 0 && dim <= norm_max_dim(io == HALO_BF16) &&
+         groups > 0 && (tokens == 0 || groups <= tokens) && tokens % groups == 0;
+}
+
+halo_status check_distill(const void* logits, const halo_dtype& lt, int64_t ldl,
+                          const int32_t* idx, int64_t ldi, const void* tlogits,
+                          const halo_dtype& tt, int64_t ldt, int64_t tokens, int64_t vocab,
+                          int64_t top, float temperature) {
+  if (!dtype_ok(lt) || !dtype_ok(tt)) return HALO_ERR_DTYPE;
+  if ((lt != HALO_F32 && lt != HALO_BF16) || (tt != HALO_F32 && tt != HALO_BF16))
+    return HALO_ERR_DTYPE;
+  if (tokens < 0 || tokens >= kMaxDim || vocab <= 0 || vocab >= kMaxDim || top <= 0 ||
+      top > kDistillMaxTop)
+    return HALO_ERR_SHAPE;
+  if (ldl < vocab || ldi < top || ldt < top) return HALO_ERR_SHAPE;
+  if (!(temperature > 0.f) || std::isinf(temperature) || std::isinf(1.f / temperature))
+    return HALO_ERR_OPTION;
+  if (tokens > 0 && (!logits || !idx || !tlogits)) return HALO_ERR_NULL;
+  if (!aligned_to(logits, esize(lt)) || !aligned_to(idx, 4) || !aligned_to(tlogits, esize(tt)))
+    return HALO_ERR_ALIGN;
+  return HALO_OK;
+}
+
+DistillArgs make_distill(const void* logits, int64_t ldl, const int32_t* idx, int64_t ldi,
+                         const void* tlogits, halo_dtype tt, int64_t ldt, int64_t tokens,
+                         int64_t vocab, int64_t top, float temperature) {
+  DistillArgs a{};
+  a.logits = logits;
+  a.idx = idx;
+  a.tlogits = tlogits;
+  a.ldl = ldl;
+  a.ldi = ldi;
+  a.ldt = ldt;
+  a.tokens = tokens;
+  a.vocab = (int)vocab;
+  a.top = (int)top;
+  a.t_bf16 = tt == HALO_BF16 ? 1 : 0;
+  a.tau = temperature;
+  a.inv_tau = 1.f / temperature;
+  return a;
+}
+
 }  // namespace
 
 extern "C" {
@@ -327,6 +373,161 @@ const char* halo_status_str(halo_status s) {
     case HALO_ERR_OPTION: return "invalid rounding option";
   }
   return "unknown status";
+}
+
+// ---- block norms ------------------------------------------------------------------------
+
+size_t halo_block_norm_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t groups,
+                                           halo_dtype io_type) {
+  if (!dtype_ok(io_type) || (io_type != HALO_F32 && io_type != HALO_BF16)) return 0;
+  if (tokens <= 0 || dim <= 0 || groups <= 0 || tokens >= kMaxDim || tokens % groups != 0 ||
+      dim > norm_max_dim(io_type == HALO_BF16))
+    return 0;
+  return norm_bwd_ws_bytes(tokens, dim, tokens / groups, io_type == HALO_BF16, true, true, true);
+}
+
+halo_status halo_block_norm_fwd(const void* r, int64_t ldr, const void* y, int64_t ldy,
+                                const void* gate, int64_t ldg, int64_t groups,
+                                const void* post_weight, const void* pre_weight,
+                                halo_dtype io_type, int64_t tokens, int64_t dim, float scale,
+                                float eps, void* r_out, int64_t ldr_out, void* h, int64_t ldh,
+                                float* rstd_post, float* rstd_pre, void* stream) {
+  if (!dtype_ok(io_type)) return HALO_ERR_DTYPE;
+  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
+  if (!norm_dims_ok(tokens, dim, groups, io_type)) return HALO_ERR_SHAPE;
+  if (!(eps >= 0.f)) return HALO_ERR_OPTION;
+  if (tokens == 0) return HALO_OK;  // empty tensors may come with NULL pointers
+  if ((gate || post_weight || r_out || rstd_post) && !y) return HALO_ERR_NULL;
+  if (rstd_post && !post_weight) return HALO_ERR_NULL;
+  if ((h || rstd_pre) && !pre_weight) return HALO_ERR_NULL;
+  if (!r || (y && !r_out) || (pre_weight && !h) || (!y && !pre_weight)) return HALO_ERR_NULL;
+  if (ldr < dim || (y && (ldy < dim || ldr_out < dim)) || (pre_weight && ldh < dim) ||
+      (gate && ldg < dim))
+    return HALO_ERR_SHAPE;
+  const int e = esize(io_type);
+  if (!aligned_to(r, e) || !aligned_to(y, e) || !aligned_to(gate, e) ||
+      !aligned_to(post_weight, e) || !aligned_to(pre_weight, e) || !aligned_to(r_out, e) ||
+      !aligned_to(h, e) || !aligned_to(rstd_post, 4) || !aligned_to(rstd_pre, 4))
+    return HALO_ERR_ALIGN;
+  NormFwdArgs a{};
+  a.r = r; a.y = y; a.gate = gate; a.post = post_weight; a.pre = pre_weight;
+  a.r_out = r_out; a.h = h; a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.ldr = ldr; a.ldy = ldy; a.ldg = ldg; a.ldro = ldr_out; a.ldh = ldh;
+  a.tokens = tokens; a.group_len = tokens / groups; a.dim = (int)dim;
+  a.scale = scale; a.eps = eps; a.inv_dim = (float)(1.0 / (double)dim);
+  return from_hip(launch_norm_fwd(a, io_type == HALO_BF16 ? 1 : 0, (hipStream_t)stream));
+}
+
+halo_status halo_block_norm_bwd(const void* dr_out, int64_t lddr_out, const void* dh,
+                                int64_t lddh, const void* r_out, int64_t ldr_out, const void* y,
+                                int64_t ldy, const void* gate, int64_t ldg, int64_t groups,
+                                const void* post_weight, const void* pre_weight,
+                                const float* rstd_post, const float* rstd_pre,
+                                halo_dtype io_type, int64_t tokens, int64_t dim, float scale,
+                                void* dr, int64_t lddr, void* dy, int64_t lddy, void* dgate,
+                                void* dpost_weight, void* dpre_weight, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!dtype_ok(io_type)) return HALO_ERR_DTYPE;
+  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
+  if (!norm_dims_ok(tokens, dim, groups, io_type) || tokens == 0) return HALO_ERR_SHAPE;
+  if (!dr || (!dr_out && !dh)) return HALO_ERR_NULL;
+  if (pre_weight ? (!dh || !r_out || !rstd_pre) : (dh || dpre_weight)) return HALO_ERR_NULL;
+  if ((gate || post_weight || dy || dgate || dpost_weight) && !y) return HALO_ERR_NULL;
+  if (y && !dy) return HALO_ERR_NULL;
+  if (post_weight ? !rstd_post : dpost_weight != nullptr) return HALO_ERR_NULL;
+  if (dgate && !gate) return HALO_ERR_NULL;
+  if ((dr_out && lddr_out < dim) || (pre_weight && (lddh < dim || ldr_out < dim)) ||
+      (y && (ldy < dim || lddy < dim)) || (gate && ldg < dim) || lddr < dim)
+    return HALO_ERR_SHAPE;
+  const int e = esize(io_type);
+  if (!aligned_to(dr_out, e) || !aligned_to(dh, e) || !aligned_to(r_out, e) ||
+      !aligned_to(y, e) || !aligned_to(gate, e) || !aligned_to(post_weight, e) ||
+      !aligned_to(pre_weight, e) || !aligned_to(rstd_post, 4) || !aligned_to(rstd_pre, 4) ||
+      !aligned_to(dr, e) || !aligned_to(dy, e) || !aligned_to(dgate, e) ||
+      !aligned_to(dpost_weight, e) || !aligned_to(dpre_weight, e))
+    return HALO_ERR_ALIGN;
+  const size_t need =
+      norm_bwd_ws_bytes(tokens, dim, tokens / groups, io_type == HALO_BF16,
+                        dpost_weight != nullptr, dpre_weight != nullptr, dgate != nullptr);
+  if (need > 0 && (!ws || ws_bytes < need)) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  NormBwdArgs a{};
+  a.dr_out = dr_out; a.dh = dh; a.r_out = r_out; a.y = y;
+  a.gate = gate; a.post = post_weight; a.pre = pre_weight;
+  a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  a.dr = dr; a.dy = dy; a.dgate = dgate; a.dpost = dpost_weight; a.dpre = dpre_weight;
+  a.lddro = lddr_out; a.lddh = lddh; a.ldro = ldr_out; a.ldy = ldy; a.ldg = ldg;
+  a.lddr = lddr; a.lddy = lddy;
+  a.tokens = tokens; a.group_len = tokens / groups; a.dim = (int)dim;
+  a.scale = scale; a.inv_dim = (float)(1.0 / (double)dim);
+  return from_hip(launch_norm_bwd(a, io_type == HALO_BF16 ? 1 : 0, ws, (hipStream_t)stream));
+}
+
+// ---- distillation -----------------------------------------------------------------------
+
+halo_status halo_distill_fwd(const void* logits, halo_dtype logits_type, int64_t ldl,
+                             const int32_t* idx, int64_t ldi, const void* tlogits,
+                             halo_dtype t_type, int64_t ldt, int64_t tokens, int64_t vocab,
+                             int64_t top, float temperature, float* loss, float* lse,
+                             void* stream) {
+  halo_status s = check_distill(logits, logits_type, ldl, idx, ldi, tlogits, t_type, ldt, tokens,
+                                vocab, top, temperature);
+  if (s != HALO_OK) return s;
+  if (tokens > 0 && !loss) return HALO_ERR_NULL;
+  if (!aligned_to(loss, 4) || !aligned_to(lse, 4)) return HALO_ERR_ALIGN;
+  if (tokens == 0) return HALO_OK;
+  DistillArgs a = make_distill(logits, ldl, idx, ldi, tlogits, t_type, ldt, tokens, vocab, top,
+                               temperature);
+  a.loss = loss;
+  a.lse = lse;
+  return from_hip(launch_distill(a, logits_type == HALO_BF16 ? 1 : 0, (hipStream_t)stream));
+}
+
+halo_status halo_distill_bwd(const float* dloss, const void* logits, halo_dtype logits_type,
+                             int64_t ldl, const float* lse, const int32_t* idx, int64_t ldi,
+                             const void* tlogits, halo_dtype t_type, int64_t ldt, int64_t tokens,
+                             int64_t vocab, int64_t top, float temperature, void* dlogits,
+                             int64_t ldd, void* stream) {
+  halo_status s = check_distill(logits, logits_type, ldl, idx, ldi, tlogits, t_type, ldt, tokens,
+                                vocab, top, temperature);
+  if (s != HALO_OK) return s;
+  if (tokens > 0 && (!dloss || !lse || !dlogits)) return HALO_ERR_NULL;
+  if (ldd < vocab || (dlogits == logits && ldd != ldl)) return HALO_ERR_SHAPE;
+  if (!aligned_to(dloss, 4) || !aligned_to(lse, 4) || !aligned_to(dlogits, esize(logits_type)))
+    return HALO_ERR_ALIGN;
+  if (tokens == 0) return HALO_OK;
+  DistillArgs a = make_distill(logits, ldl, idx, ldi, tlogits, t_type, ldt, tokens, vocab, top,
+                               temperature);
+  a.dloss = dloss;
+  a.lse_in = lse;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  return from_hip(launch_distill(a, logits_type == HALO_BF16 ? 1 : 0, (hipStream_t)stream));
+}
+
+halo_status halo_distill_fwd_bwd(const void* logits, halo_dtype logits_type, int64_t ldl,
+                                 const int32_t* idx, int64_t ldi, const void* tlogits,
+                                 halo_dtype t_type, int64_t ldt, const float* dloss,
+                                 int64_t tokens, int64_t vocab, int64_t top, float temperature,
+                                 float* loss, float* lse, void* dlogits, int64_t ldd,
+                                 void* stream) {
+  halo_status s = check_distill(logits, logits_type, ldl, idx, ldi, tlogits, t_type, ldt, tokens,
+                                vocab, top, temperature);
+  if (s != HALO_OK) return s;
+  if (tokens > 0 && (!dloss || !loss || !dlogits)) return HALO_ERR_NULL;
+  if (ldd < vocab || (dlogits == logits && ldd != ldl)) return HALO_ERR_SHAPE;
+  if (!aligned_to(dloss, 4) || !aligned_to(loss, 4) || !aligned_to(lse, 4) ||
+      !aligned_to(dlogits, esize(logits_type)))
+    return HALO_ERR_ALIGN;
+  if (tokens == 0) return HALO_OK;
+  DistillArgs a = make_distill(logits, ldl, idx, ldi, tlogits, t_type, ldt, tokens, vocab, top,
+                               temperature);
+  a.dloss = dloss;
+  a.loss = loss;
+  a.lse = lse;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  return from_hip(launch_distill(a, logits_type == HALO_BF16 ? 1 : 0, (hipStream_t)stream));
 }
 
 size_t halo_fwht_quant_workspace_bytes(int64_t rows, int64_t cols, halo_axis axis,

@@ -112,6 +112,51 @@ hipError_t launch_gemm(const GemmArgs& g, int kind, int afmt, int bfmt, int out,
 hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs* g1, int kind, int afmt, int bfmt,
                             int out, hipStream_t st);
 
+// The join between two blocks (block_norm.hip).  Optional tensors are NULL; leading dimensions
+// in elements; group_len = tokens / gate rows.
+struct NormFwdArgs {
+  const void *r, *y, *gate, *post, *pre;
+  void *r_out, *h;
+  float *rstd_post, *rstd_pre;
+  int64_t ldr, ldy, ldg, ldro, ldh;
+  int64_t tokens, group_len;
+  int dim;
+  float scale, eps, inv_dim;
+};
+struct NormBwdArgs {
+  const void *dr_out, *dh, *r_out, *y, *gate, *post, *pre;
+  const float *rstd_post, *rstd_pre;
+  void *dr, *dy, *dgate, *dpost, *dpre;
+  int64_t lddro, lddh, ldro, ldy, ldg, lddr, lddy;
+  int64_t tokens, group_len;
+  int dim;
+  float scale, inv_dim;
+  float *part_post, *part_pre, *part_gate;  // partial sums, set by the launcher
+};
+int64_t norm_max_dim(int in_bf16);
+hipError_t launch_norm_fwd(const NormFwdArgs& a, int in_bf16, hipStream_t st);
+size_t norm_bwd_ws_bytes(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16, bool post,
+                         bool pre, bool gate);
+hipError_t launch_norm_bwd(NormBwdArgs a, int in_bf16, void* ws, hipStream_t st);
+
+// Distillation loss over a teacher's top logits (distill.hip).
+constexpr int kDistillMaxTop = 1024;
+struct DistillArgs {
+  const void* logits;    // [tokens x vocab], ldl
+  const int32_t* idx;    // [tokens x top], ldi
+  const void* tlogits;   // [tokens x top], ldt
+  const float* dloss;    // NULL: no gradient
+  const float* lse_in;   // NULL: computed
+  float *loss, *lse;     // NULL: not written
+  void* dlogits;         // [tokens x vocab], ldd; may be logits
+  int64_t ldl, ldi, ldt, ldd;
+  int64_t tokens;
+  int vocab, top;
+  int t_bf16;            // tlogits are bf16
+  float tau, inv_tau;
+};
+hipError_t launch_distill(const DistillArgs& a, int in_bf16, hipStream_t st);
+
 // Matrix-core rate probe (mfma_probe.hip): kind 0 INT8 32x32x32, 1 FP8 32x32x64, 2 FP8
 // 16x16x128; mfma_probe_ops gives the operations one launch performs.
 hipError_t launch_mfma_probe(int kind, int iters, hipStream_t st);

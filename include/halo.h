@@ -347,6 +347,100 @@ halo_status halo_fwht_quant_dual(const void* x, halo_dtype x_type, int64_t rows,
                                  void* stream);
 
 /*
+ * Row operators: the join between two blocks of a model and the distillation loss.  Unlike the
+ * rotation and the products they take any leading dimension (at least the row's width) and any
+ * pointer aligned to its own element.
+ *
+ * halo_block_norm_fwd: a block's output y joins the residual stream r and the next block's
+ * input is normalised.  Over the `dim` elements of each of `tokens` rows:
+ *   a = 1 / sqrt(mean(y^2) + eps),   r_out = r + scale gate (y a post_weight),
+ *   b = 1 / sqrt(mean(r_out^2) + eps),   h = r_out b pre_weight.
+ * Sums and r_out between the two norms are fp32; each output is rounded once.
+ *   r, y         HALO_F32 or HALO_BF16 (io_type, also of gate, weights and outputs).  y NULL: no
+ *                join (a first block): only h is written, r_out must be NULL.
+ *   gate         [groups x dim] or NULL (ones): row g gates the g-th run of tokens / groups
+ *                consecutive tokens; groups divides tokens (1: one gate per channel, tokens: one
+ *                per token).  groups is 1 when gate is NULL.
+ *   post_weight  [dim], or NULL: y joins without a norm.
+ *   pre_weight   [dim], or NULL: no norm after the join (h must be NULL).
+ *   r_out, h     outputs; r_out may be r or y, h may be y or r (with the same leading dimension).
+ *   rstd_post, rstd_pre  [tokens] fp32, the factors a and b (the backward takes them); may be NULL.
+ * dim is 1 .. 32768 (bf16) or 16384 (fp32).  A row of zeros with eps 0 gives infinities, as the
+ * formula does.
+ */
+halo_status halo_block_norm_fwd(const void* r, int64_t ldr, const void* y, int64_t ldy,
+                                const void* gate, int64_t ldg, int64_t groups,
+                                const void* post_weight, const void* pre_weight,
+                                halo_dtype io_type, int64_t tokens, int64_t dim, float scale,
+                                float eps, void* r_out, int64_t ldr_out, void* h, int64_t ldh,
+                                float* rstd_post, float* rstd_pre, void* stream);
+
+/*
+ * Gradient of halo_block_norm_fwd.  With rhat = r_out b, yhat = y a, u = dh pre_weight,
+ * c = scale gate post_weight (means over a row):
+ *   dr = dr_out + b (u - rhat mean(u rhat)),      dy = a (c dr - yhat mean(c dr yhat)),
+ *   dgate = sum scale dr yhat post_weight (over the tokens of a gate row),
+ *   dpost_weight = sum scale gate dr yhat,        dpre_weight = sum dh rhat.
+ *   dr_out   gradient arriving at the residual stream, or NULL (zero).
+ *   dh, r_out, rstd_pre    with pre_weight; NULL without it.
+ *   y, dy, rstd_post       y and dy NULL when the forward had no y; rstd_post with post_weight.
+ *   dr       may be dr_out or dh; dy may be y or dh (same leading dimension).
+ *   dgate [groups x dim], dpost_weight, dpre_weight [dim] (dense, io_type): each may be NULL.
+ *   ws       at least halo_block_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (the
+ *            partial sums of the parameter gradients; not read when all three are NULL).
+ * Sums over tokens are fp32 in a fixed order: equal inputs give equal bits.
+ */
+size_t halo_block_norm_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t groups,
+                                           halo_dtype io_type);
+halo_status halo_block_norm_bwd(const void* dr_out, int64_t lddr_out, const void* dh,
+                                int64_t lddh, const void* r_out, int64_t ldr_out, const void* y,
+                                int64_t ldy, const void* gate, int64_t ldg, int64_t groups,
+                                const void* post_weight, const void* pre_weight,
+                                const float* rstd_post, const float* rstd_pre,
+                                halo_dtype io_type, int64_t tokens, int64_t dim, float scale,
+                                void* dr, int64_t lddr, void* dy, int64_t lddy, void* dgate,
+                                void* dpost_weight, void* dpre_weight, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  For a token with student logits s[vocab] and the
+ * teacher's `top` kept logits t_k at vocabulary indices idx_k:
+ *   p = softmax(t / temperature) over the kept entries,
+ *   q = softmax(s / temperature) over the vocabulary, lse = log sum exp(s / temperature),
+ *   loss = temperature^2 sum_k p_k (log p_k - log q[idx_k]),
+ *   dlogits[j] = dloss temperature (q_j - sum_k p_k [idx_k = j]).
+ * An index outside [0, vocab) is no entry (use -1 for tokens with fewer of them); equal indices
+ * add their p.  Entries with p_k = 0 (t_k = -inf) add nothing.  A token without an entry, or
+ * whose logits are all -inf, has loss 0 and gradient 0; a token with dloss 0 has gradient 0
+ * whatever its logits.  An entry at a logit of -inf gives loss +inf.  NaN and +inf give NaN.
+ *   logits   HALO_F32 or HALO_BF16 [tokens x vocab], ldl >= vocab.
+ *   idx      int32 [tokens x top], ldi >= top;  tlogits HALO_F32 or HALO_BF16, ldt >= top;
+ *            top is 1 .. 1024.
+ *   temperature  positive and finite (HALO_ERR_OPTION otherwise).
+ *   loss, lse    fp32 [tokens]; lse may be NULL.
+ *   dloss    fp32 [tokens], the gradient of the token's loss (a mean over n tokens: 1 / n).
+ *   dlogits  [tokens x vocab] of the logits' type, ldd >= vocab; may be logits (then ldd = ldl).
+ * halo_distill_bwd takes the lse that the forward wrote; halo_distill_fwd_bwd does both from one
+ * read of the logits.
+ */
+halo_status halo_distill_fwd(const void* logits, halo_dtype logits_type, int64_t ldl,
+                             const int32_t* idx, int64_t ldi, const void* tlogits,
+                             halo_dtype t_type, int64_t ldt, int64_t tokens, int64_t vocab,
+                             int64_t top, float temperature, float* loss, float* lse,
+                             void* stream);
+halo_status halo_distill_bwd(const float* dloss, const void* logits, halo_dtype logits_type,
+                             int64_t ldl, const float* lse, const int32_t* idx, int64_t ldi,
+                             const void* tlogits, halo_dtype t_type, int64_t ldt, int64_t tokens,
+                             int64_t vocab, int64_t top, float temperature, void* dlogits,
+                             int64_t ldd, void* stream);
+halo_status halo_distill_fwd_bwd(const void* logits, halo_dtype logits_type, int64_t ldl,
+                                 const int32_t* idx, int64_t ldi, const void* tlogits,
+                                 halo_dtype t_type, int64_t ldt, const float* dloss,
+                                 int64_t tokens, int64_t vocab, int64_t top, float temperature,
+                                 float* loss, float* lse, void* dlogits, int64_t ldd,
+                                 void* stream);
+
+/*
  * Measurement aid, not part of the layer: the sustained rate of the matrix-core instruction a
  * product uses, on the whole device, to set the products' measured rates beside what the
  * instruction alone reaches under a sustained load (the published dense peaks assume the

@@ -1,0 +1,209 @@
+"""The distillation loss over a teacher's top logits and its gradient against the formula in 64
+bits.
+
+Tolerances, in units of u = 2^-24.  lse: the logits scaled by 1 / temperature carry 3 u |z| each
+(the factor, the product, the maximum they are compared with), a row's sum of exponentials has a
+chain of at most 256 additions, each exponential 8 u.  p: the same with the teacher's logits.  The
+loss adds (|log p| + |z| + |lse|) u per entry.  A gradient element is off by its exponent's error,
+relative, plus its rounding to the output type."""
+import pytest
+import torch
+
+import hadamard_rotated_precision_halo_amd as H
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+U = 2.0 ** -24
+ROUND = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def ref64(logits, idx, tl, tau, dloss=None, lse=None):
+    """Loss, lse, gradient in 64 bits and the tolerances of each."""
+    z, v = logits.double() / tau, logits.shape[1]
+    there = (idx >= 0) & (idx < v)
+    u = torch.where(there, tl.double() / tau, float("-inf"))
+    zmax = torch.where(z.isinf(), 0.0, z).abs().amax(1)
+    own = torch.logsumexp(z, 1)
+    lse_tol = U * (4 * zmax + 300 + 8)
+    if lse is not None:
+        own, lse_tol = lse.double(), torch.zeros_like(lse_tol)
+    dead = (own == float("-inf")) | (u == float("-inf")).all(1)
+    p = torch.softmax(torch.where(dead[:, None], 0.0, u), 1) * there
+    at = idx.clamp(0, v - 1).long()
+    logp = torch.where(p > 0, p, 1.0).log()
+    zk = z.gather(1, at)
+    term = torch.where((p > 0) & ~dead[:, None], p * (logp - zk + own[:, None]), 0.0)
+    loss = tau ** 2 * term.sum(1)
+    umax = torch.where(u.isinf(), 0.0, u).abs().amax(1)
+    p_tol = U * (64 + 8 * umax + idx.shape[1] / 4)
+    size = torch.where(p > 0, p * (logp.abs() + zk.abs() + own.abs()[:, None] + 1), 0.0).sum(1)
+    loss_tol = tau ** 2 * (lse_tol + (p_tol + 8 * U) * size)
+    out = [loss, torch.where(dead, 0.0, loss_tol), own, lse_tol]
+    if dloss is not None:
+        by = torch.where(dead | (dloss == 0), 0.0, dloss.double() * tau)[:, None]
+        zz = torch.where(by == 0, 0.0, z)
+        q = torch.exp(zz - torch.where(by[:, 0] == 0, 0.0, own)[:, None])
+        spread = torch.zeros_like(q).scatter_add_(1, at, torch.where(there, p, 0.0))
+        grad = by * (q - spread)
+        e = U * (4 * torch.where(zz.isinf(), 0.0, zz).abs() + 4 * own.abs()[:, None].nan_to_num(0, 0, 0) + 16) + lse_tol[:, None]
+        tol = by.abs() * (q * e + spread * p_tol[:, None]) + ROUND[logits.dtype] * 1.01 * grad.abs() + 1e-37
+        out += [grad, tol]
+    return out
+
+
+def make(t, v, k, dt, seed, tdt=F32, pad=0, missing=True):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    full = (2.5 * torch.randn((t, v + pad), generator=g, device=DEV)).to(dt)
+    logits = full[:, :v] if pad else full
+    idx = torch.randint(0, v, (t, k), generator=g, device=DEV, dtype=torch.int32)   # repeats occur
+    if missing:
+        drop = torch.rand((t, k), generator=g, device=DEV) < 0.2
+        idx = torch.where(drop, torch.randint(-3, 0, (t, k), generator=g, device=DEV, dtype=torch.int32), idx)
+    tl = (4 * torch.randn((t, k), generator=g, device=DEV)).to(tdt)
+    dloss = torch.rand(t, generator=g, device=DEV) * (torch.rand(t, generator=g, device=DEV) < 0.8)
+    return logits, idx, tl, dloss
+
+
+def within(got, ref, tol, what):
+    got = got.double()
+    same = (got == ref) | ((got - ref).abs() <= tol)
+    assert same.all(), (what, int((~same).sum()), got[~same][:4], ref[~same][:4])
+
+
+def check_all(logits, idx, tl, dloss, tau):
+    loss, lse = H.distill_fwd(logits, idx, tl, temperature=tau)
+    rl, tl_, re, te, rg, tg = ref64(logits, idx, tl, tau, dloss)
+    within(lse, re, te, "lse")
+    within(loss, rl, tl_, "loss")
+    both = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=tau)
+    assert torch.equal(both[0], loss) and torch.equal(both[1], lse)
+    within(both[2], rg, tg, "gradient of the joint call")
+    grad = H.distill_bwd(dloss, logits, lse, idx, tl, temperature=tau)
+    g2 = ref64(logits, idx, tl, tau, dloss, lse)
+    within(grad, g2[4], g2[5], "gradient")
+    assert torch.equal(grad, both[2])
+
+
+# tokens, vocabulary, kept entries, row padding: every size of the held row and the longer ones
+SHAPES = [(1, 1, 1, 0), (3, 7, 4, 0), (2, 8, 8, 3), (5, 1000, 33, 0), (4, 4100, 128, 5),
+          (3, 8192, 5, 0), (3, 8200, 64, 0), (2, 32771, 300, 1), (3, 50257, 20, 0),
+          (2, 65536, 16, 0), (1, 131072, 1024, 0), (2, 131075, 64, 0), (1, 262147, 7, 0)]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("t,v,k,pad", SHAPES)
+def test_loss_and_gradient(t, v, k, pad, dt):
+    print(f"tokens {t} vocabulary {v} kept {k} padding {pad} {dt}", flush=True)
+    for seed, tau in ((1, 1.0), (2, 2.5)):
+        check_all(*make(t, v, k, dt, seed, pad=pad), tau)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_teacher_in_bf16_and_strided(dt):
+    logits, idx, tl, dloss = make(33, 2000, 24, dt, 5, tdt=BF16)
+    wide_i = torch.full((33, 31), 7, dtype=torch.int32, device=DEV)
+    wide_t = torch.zeros((33, 40), dtype=BF16, device=DEV)
+    wide_i[:, :24], wide_t[:, :24] = idx, tl
+    check_all(logits, wide_i[:, :24], wide_t[:, :24], dloss, 3.0)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("v", [1003, 140000])
+def test_masked_places(v, dt):
+    inf = float("inf")
+    lowest = torch.finfo(dt).min
+    logits, idx, tl, dloss = make(8, v, 16, dt, 9, missing=False)
+    dloss = dloss + 0.25
+    logits[0, v // 2:] = -inf              # half the vocabulary masked
+    idx[0] = torch.arange(16, device=DEV, dtype=torch.int32)
+    logits[1, 1:] = lowest                 # masked with the type's lowest value
+    idx[1, :], idx[1, 0] = -1, 0           # one entry, at the only live logit: loss 0
+    tl[2, 3:] = -inf                       # most of the teacher's entries without weight
+    idx[3, :] = -1                         # no entry
+    tl[4, :] = -inf                        # entries, none with weight
+    idx[5, :] = v                          # outside the vocabulary: no entry
+    logits[6, :] = -inf                    # nothing left of the student
+    idx[7] = 5                             # one index sixteen times
+    check_all(logits, idx, tl, dloss, 1.5)
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=1.5)
+    for row in (3, 4, 5, 6):
+        assert loss[row] == 0 and (grad[row] == 0).all()
+    assert lse[6] == -inf
+    assert (grad[0, v // 2:] == 0).all()
+    # an entry with weight at a masked logit: infinite loss, finite gradient
+    idx[0, 0] = v - 1
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=1.5)
+    assert loss[0] == inf and torch.isfinite(grad[0]).all() and grad[0, v - 1] < 0
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_nan_stays_in_its_token(dt):
+    nan, inf = float("nan"), float("inf")
+    logits, idx, tl, dloss = make(6, 777, 9, dt, 3, missing=False)
+    dloss = torch.ones_like(dloss)
+    clean = H.distill_fwd_bwd(logits, idx, tl, dloss)
+    logits[0, 5], logits[1, :], logits[2, 3], tl[3, 0], tl[4, :] = nan, nan, inf, nan, nan
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss)
+    assert loss[:5].isnan().all() and lse[:3].isnan().all() and not lse[3:].isnan().any()
+    assert grad[0].isnan().all() and grad[1].isnan().all()
+    for a, b in zip((loss, lse, grad), clean):
+        assert torch.equal(a[5], b[5])
+    # a token with dloss 0 has gradient 0 whatever its logits
+    dloss[:5] = 0
+    assert (H.distill_fwd_bwd(logits, idx, tl, dloss)[2][:5] == 0).all()
+    assert (H.distill_bwd(dloss, logits, lse, idx, tl)[:5] == 0).all()
+
+
+@pytest.mark.parametrize("dt,v", [(BF16, 5001), (F32, 40000), (BF16, 150001)])
+def test_in_place_on_another_stream(dt, v):
+    logits, idx, tl, dloss = make(9, v, 40, dt, 7)
+    want = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=2.0)
+    a, b = logits.clone(), logits.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = H.distill_fwd_bwd(a, idx, tl, dloss, temperature=2.0, dlogits=a, stream=s)
+    g = H.distill_bwd(dloss, b, want[1], idx, tl, temperature=2.0, dlogits=b, stream=s)
+    s.synchronize()
+    assert got[2].data_ptr() == a.data_ptr()
+    assert torch.equal(got[0], want[0]) and torch.equal(a, want[2]) and torch.equal(g, want[2])
+
+
+def test_gradient_against_differences():
+    # the sum of the weighted losses of the 64-bit formula by central differences
+    logits, idx, tl, dloss = make(6, 301, 12, F32, 13)
+    tau, step = 1.7, 1e-4
+    grad = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=tau)[2].double()
+    g = torch.Generator(device=DEV)
+    g.manual_seed(3)
+    for _ in range(4):
+        v = torch.randn(logits.shape, generator=g, device=DEV, dtype=torch.float64)
+        up, down = (float((ref64(logits.double() + s * v, idx, tl, tau)[0] * dloss).sum())
+                    for s in (step, -step))
+        num, ours = (up - down) / (2 * step), float((grad * v).sum())
+        assert abs(num - ours) <= 1e-5 * float((grad * v).abs().sum()), (num, ours)
+
+
+def test_offsets_past_32_bits():
+    # the last tokens of a batch whose logits span more than 2^32 bytes, each checked alone
+    t, v = 20000, 120001
+    logits = torch.zeros((t, v), dtype=BF16, device=DEV)
+    small = make(3, v, 10, BF16, 1)
+    logits[-3:] = small[0]
+    idx = torch.full((t, 10), -1, dtype=torch.int32, device=DEV)
+    tl = torch.zeros((t, 10), device=DEV)
+    dloss = torch.zeros(t, device=DEV)
+    idx[-3:], tl[-3:], dloss[-3:] = small[1], small[2], small[3]
+    want = H.distill_fwd_bwd(*small)
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss, dlogits=logits)
+    assert torch.equal(loss[-3:], want[0]) and torch.equal(grad[-3:], want[2])
+    assert (loss[:-3] == 0).all() and (grad[:-3].view(torch.int16).amax(1) == 0).all()
+
+
+def test_no_tokens():
+    e = torch.empty((0, 100), dtype=BF16, device=DEV)
+    i = torch.empty((0, 4), dtype=torch.int32, device=DEV)
+    loss, lse, grad = H.distill_fwd_bwd(e, i, torch.empty((0, 4), device=DEV),
+                                        torch.empty(0, device=DEV))
+    assert loss.numel() == 0 and grad.shape == (0, 100)
