@@ -35,7 +35,10 @@ EXPORTS = ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
            "halo_linear_bwd", "halo_linear_bwd_ex", "halo_fwht_quant_dual",
            "halo_fwht_quant_dual_workspace_bytes", "halo_mfma_rate_probe", "halo_status_str",
            "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_block_norm_bwd_workspace_bytes",
-           "halo_distill_fwd", "halo_distill_bwd", "halo_distill_fwd_bwd")
+           "halo_distill_fwd", "halo_distill_bwd", "halo_distill_fwd_bwd",
+           "halo_linear_act_fwd", "halo_linear_act_q", "halo_linear_act_q_workspace_bytes",
+           "halo_linear_act_bwd", "halo_linear_act_bwd_workspace_bytes")
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu_erf": 4}  # halo_activation
 
 
 class QuantOpts(ctypes.Structure):
@@ -51,6 +54,13 @@ class LinearOpts(ctypes.Structure):
                 ("signs_m", ctypes.c_void_p), ("grad_rounding", ctypes.c_int32),
                 ("seed", ctypes.c_uint32 * 2), ("counter", ctypes.c_uint32 * 2),
                 ("exchange_polls", ctypes.c_uint32)]
+
+
+class Epilogue(ctypes.Structure):
+    """halo_epilogue of include/halo.h."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("z", ctypes.c_void_p),
+                ("activation", ctypes.c_int32)]
+
 
 _TORCH_CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8,
                torch.float8_e4m3fn: E4M3, torch.float8_e5m2: E5M2, torch.int32: I32}
@@ -113,6 +123,17 @@ def lib():
                                        vp, i64, vp]
         L.halo_distill_fwd_bwd.argtypes = [vp, e, i64, vp, i64, vp, e, i64, vp, i64, i64, i64, f32,
                                            vp, vp, vp, i64, vp]
+        ep = ctypes.POINTER(Epilogue)
+        L.halo_linear_act_fwd.argtypes = [vp, vp, e, i64, i64, i64, i32, e, vp, e, ep, lo, vp, sz,
+                                          vp]
+        L.halo_linear_act_q_workspace_bytes.argtypes = [i64, i64, i32]
+        L.halo_linear_act_q_workspace_bytes.restype = sz
+        L.halo_linear_act_q.argtypes = [vp, e, vp, e, vp, i64, i64, i64, i32, vp, e, ep, vp, vp, sz,
+                                        vp]
+        L.halo_linear_act_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, e]
+        L.halo_linear_act_bwd_workspace_bytes.restype = sz
+        L.halo_linear_act_bwd.argtypes = [vp, vp, e, vp, vp, e, i64, i64, i64, i32, e, e, vp, vp,
+                                          vp, lo, vp, sz, vp]
         L.halo_status_str.argtypes = [e]
         L.halo_status_str.restype = ctypes.c_char_p
         for f in ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
@@ -120,7 +141,8 @@ def lib():
                   "halo_linear_fwd", "halo_linear_fwd_ex", "halo_linear_bwd",
                   "halo_linear_bwd_ex", "halo_fwht_quant_dual", "halo_mfma_rate_probe",
                   "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_distill_fwd",
-                  "halo_distill_bwd", "halo_distill_fwd_bwd"):
+                  "halo_distill_bwd", "halo_distill_fwd_bwd", "halo_linear_act_fwd",
+                  "halo_linear_act_q", "halo_linear_act_bwd"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -784,3 +806,169 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
                                     _p(dlogits), ldd, _current_stream(dev, stream))
     _check(st, "halo_distill_fwd_bwd")
     return loss, lse, dlogits
+
+
+# ---------------------------------------------------------------------------
+# the layer with its epilogue
+# ---------------------------------------------------------------------------
+
+def _dense(t, name, shape, dtype, device):
+    """A contiguous 2-D argument of exactly shape and dtype."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and tuple(t.shape) == shape
+            and t.dtype == dtype and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError(f"activation must be one of {tuple(ACTIVATIONS)}, not {name!r}") from None
+
+
+def _epilogue(bias, activation, residual, z, shape, dtype, device):
+    if bias is not None:
+        _vec(bias, "bias", shape[1], dtype, device)
+    if residual is not None:
+        _dense(residual, "residual", shape, dtype, device)
+    if z is not None:
+        _dense(z, "z", shape, dtype, device)
+    return Epilogue(_p(bias), _p(residual), _p(z), _activation(activation))
+
+
+def _scratch(workspace, need, ref):
+    if workspace is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=ref.device)
+    _bytes(workspace, "workspace")
+    _same_gpu(ref, workspace=workspace)
+    return workspace
+
+
+def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none", residual=None,
+                   y=None, y_dtype=None, want_z=False, z=None, workspace=None, stream=None,
+                   signs_k=None):
+    """The layer with its epilogue (halo_linear_act_fwd): z = X W^T + bias (rotated 8-bit product,
+    as linear_fwd), y = act(z) + residual, rounded once.  activation: "none", "relu", "silu",
+    "gelu_tanh" or "gelu_erf"; bias [n], residual, y and z [m, n] share y's type.  Returns y, or
+    (y, z) when the pre-activation is wanted (want_z or a z to write it to): linear_act_bwd takes
+    it.  residual may be y itself."""
+    dt, dev = _io_2d(x, "x")
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2):
+        raise ValueError("w must be a 2-D tensor")
+    m, k = x.shape
+    n = w.shape[0]
+    _dense(x, "x", (m, k), dt, dev)
+    _dense(w, "w", (n, k), dt, dev)
+    yt = y.dtype if y is not None else (y_dtype or dt)
+    if y is None:
+        y = torch.empty((m, n), dtype=yt, device=dev)
+    _dense(y, "y", (m, n), yt, dev)
+    if want_z and z is None:
+        z = torch.empty((m, n), dtype=yt, device=dev)
+    ep = _epilogue(bias, activation, residual, z, (m, n), yt, dev)
+    opts = None
+    if signs_k is not None:
+        _vector(signs_k, "signs_k", _sign_words(contraction_len(k, block)), torch.int32)
+        _same_gpu(x, signs_k=signs_k)
+        opts = ctypes.byref(LinearOpts(_p(signs_k), None, None, NEAREST))
+    L, qc = lib(), _code(q_dtype)
+    ws = _scratch(workspace, L.halo_linear_workspace_bytes_ex(m, n, k, int(block), qc, 0)
+                  if workspace is None else 0, x)
+    st = L.halo_linear_act_fwd(_p(x), _p(w), _TORCH_CODE[dt], m, n, k, int(block), qc, _p(y),
+                               _code(yt), ctypes.byref(ep), opts, _p(ws), ws.numel(),
+                               _current_stream(dev, stream))
+    _check(st, "halo_linear_act_fwd")
+    return y if z is None else (y, z)
+
+
+def linear_act_q_workspace_bytes(m, k, block):
+    return int(lib().halo_linear_act_q_workspace_bytes(m, k, int(block)))
+
+
+def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, y=None,
+                 y_dtype=None, z=None, workspace=None, stream=None, signs_k=None):
+    """linear_act_fwd on weights quantised once, for serving: (qw, sw) = fwht_quant(w, ROWS, block,
+    q_dtype[, signs=signs_k]) of the weights [n, k] (k padded to a multiple of block, of 32 at
+    least).  Only x is rotated and quantised here; up to 64 rows of x take a kernel bound by
+    reading qw once.  Returns y (and z when a z to write it to is given)."""
+    dt, dev = _io_2d(x, "x")
+    m, k = x.shape
+    if not (isinstance(qw, torch.Tensor) and qw.dim() == 2):
+        raise ValueError("qw must be a 2-D tensor")
+    n, block = qw.shape[0], int(block)
+    _dense(x, "x", (m, k), dt, dev)
+    if qw.dtype is not torch.int8 and qw.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"unsupported dtype {qw.dtype}")
+    kq = contraction_len(k, block) if block > 0 else k  # the library refuses a bad block
+    _dense(qw, "qw", (n, kq), qw.dtype, dev)
+    _vec(sw, "sw", n, torch.float32, dev)
+    yt = y.dtype if y is not None else (y_dtype or dt)
+    if y is None:
+        y = torch.empty((m, n), dtype=yt, device=dev)
+    _dense(y, "y", (m, n), yt, dev)
+    ep = _epilogue(bias, activation, residual, z, (m, n), yt, dev)
+    if signs_k is not None:
+        _vector(signs_k, "signs_k", _sign_words(kq), torch.int32)
+        _same_gpu(x, signs_k=signs_k)
+    L = lib()
+    ws = _scratch(workspace, L.halo_linear_act_q_workspace_bytes(m, k, block)
+                  if workspace is None else 0, x)
+    st = L.halo_linear_act_q(_p(x), _TORCH_CODE[dt], _p(qw), _TORCH_CODE[qw.dtype], _p(sw), m, n, k,
+                             block, _p(y), _code(yt), ctypes.byref(ep), _p(signs_k), _p(ws),
+                             ws.numel(), _current_stream(dev, stream))
+    _check(st, "halo_linear_act_q")
+    return y if z is None else (y, z)
+
+
+def linear_act_bwd_workspace_bytes(m, n, k, block, q_dtype=torch.int8):
+    return int(lib().halo_linear_act_bwd_workspace_bytes(m, n, k, int(block), _code(q_dtype)))
+
+
+def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, activation="none",
+                   want_dx=True, want_dw=True, want_db=True, dx=None, dw=None, db=None,
+                   workspace=None, stream=None, signs_n=None, signs_m=None,
+                   grad_rounding="nearest", seed=0, counter=0, exchange_polls=0):
+    """Gradient of linear_act_fwd: dz = dy act'(z) (fp32 until its codes), then linear_bwd's
+    products dX = dz W and dW = dz^T X, and db = dz summed over the rows.  z may be None with
+    activation "none".  The residual's gradient is dy.  Returns (dx, dw, db), None where not
+    wanted; options as linear_bwd."""
+    dt, dev = _io_2d(dy, "dy")
+    if not all(isinstance(t, torch.Tensor) and t.dim() == 2 for t in (x, w)):
+        raise ValueError("x and w must be 2-D tensors")
+    m, k = x.shape
+    n = w.shape[0]
+    _dense(dy, "dy", (m, n), dt, dev)
+    _dense(x, "x", (m, k), dt, dev)
+    _dense(w, "w", (n, k), dt, dev)
+    act = _activation(activation)
+    if act != 0 or z is not None:
+        _dense(z, "z", (m, n), dt, dev)
+    if want_dx:
+        dx = torch.empty((m, k), dtype=dt, device=dev) if dx is None else dx
+        _dense(dx, "dx", (m, k), dt, dev)
+    if want_dw:
+        dw = torch.empty((n, k), dtype=dt, device=dev) if dw is None else dw
+        _dense(dw, "dw", (n, k), dt, dev)
+    if want_db:
+        db = torch.empty(n, dtype=dt, device=dev) if db is None else db
+        _vec(db, "db", n, dt, dev)
+    if signs_n is not None:
+        _vector(signs_n, "signs_n", _sign_words(contraction_len(n, block)), torch.int32)
+    if signs_m is not None:
+        _vector(signs_m, "signs_m", _sign_words(contraction_len(m, block)), torch.int32)
+    _same_gpu(dy, signs_n=signs_n, signs_m=signs_m)
+    rnd = _rounding(grad_rounding)
+    opts = None
+    if signs_n is not None or signs_m is not None or rnd != NEAREST or exchange_polls:
+        opts = ctypes.byref(LinearOpts(None, _p(signs_n), _p(signs_m), rnd, _u32x2(seed),
+                                       _u32x2(counter), int(exchange_polls)))
+    L, qc = lib(), _code(q_dtype)
+    ws = _scratch(workspace, L.halo_linear_act_bwd_workspace_bytes(m, n, k, int(block), qc)
+                  if workspace is None else 0, dy)
+    st = L.halo_linear_act_bwd(_p(dy), _p(z), act, _p(x), _p(w), _TORCH_CODE[dt], m, n, k,
+                               int(block), qc, _code(grad_q_dtype or q_dtype),
+                               _p(dx) if want_dx else None, _p(dw) if want_dw else None,
+                               _p(db) if want_db else None, opts, _p(ws), ws.numel(),
+                               _current_stream(dev, stream))
+    _check(st, "halo_linear_act_bwd")
+    return (dx if want_dx else None), (dw if want_dw else None), (db if want_db else None)

@@ -1,0 +1,116 @@
+// epilogue.h -- activations of the layer's epilogue and their slopes, and the loads and stores of
+// an epilogue's columns.
+#pragma once
+
+#include "rowops.h"
+
+namespace halo {
+
+enum Act { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGeluTanh = 3, kActGeluErf = 4 };
+
+// 1 / (1 + exp(-x)): v_exp_f32 and v_rcp_f32, 1 ulp each; the argument's scaling to base 2 adds
+// |x| 2^-24 relative.
+__device__ __forceinline__ float sigmoid_fast(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+}
+
+// 2 sqrt(2 / pi) (z + 0.044715 z^3): gelu's tanh form is z (1 + tanh u) / 2 = z sigmoid(2 u)
+__device__ __forceinline__ float gelu_arg(float z) {
+  const float t = z * z;
+  return z * __builtin_fmaf(t, 0.07135481627159f, 1.5957691216057308f);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
+  if constexpr (ACT == kActSilu) return z * sigmoid_fast(z);
+  if constexpr (ACT == kActGeluTanh) return z * sigmoid_fast(gelu_arg(z));
+  if constexpr (ACT == kActGeluErf) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+  return z;
+}
+
+// d act / dz.  silu: p + z p (1 - p); gelu's tanh form the same with p = sigmoid(2 u) and the
+// slope of 2 u; gelu: the normal distribution plus z times its density.
+template <int ACT>
+__device__ __forceinline__ float slope_of(float z) {
+  if constexpr (ACT == kActRelu) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  if constexpr (ACT == kActSilu) {
+    const float p = sigmoid_fast(z);
+    return __builtin_fmaf(z * p, 1.f - p, p);
+  }
+  if constexpr (ACT == kActGeluTanh) {
+    const float p = sigmoid_fast(gelu_arg(z));
+    const float du = __builtin_fmaf(z * z, 3.f * 0.07135481627159f, 1.5957691216057308f);
+    return __builtin_fmaf(z * (p * (1.f - p)), du, p);
+  }
+  if constexpr (ACT == kActGeluErf) {
+    const float cdf = 0.5f * (1.f + erff(z * 0.7071067811865476f));
+    const float pdf = 0.3989422804014327f * __builtin_amdgcn_exp2f(z * z * -0.7213475204444817f);
+    return __builtin_fmaf(z, pdf, cdf);
+  }
+  return 1.f;
+}
+
+// The activation (a wave-uniform choice) of 8 values.
+__device__ __forceinline__ void act8(int act, const float* z, float* y) {
+#define HALO_ACT8(A) \
+  _Pragma("unroll") for (int e = 0; e < 8; ++e) y[e] = act_of<A>(z[e])
+  switch (act) {
+    case kActRelu: HALO_ACT8(kActRelu); break;
+    case kActSilu: HALO_ACT8(kActSilu); break;
+    case kActGeluTanh: HALO_ACT8(kActGeluTanh); break;
+    case kActGeluErf: HALO_ACT8(kActGeluErf); break;
+    default: HALO_ACT8(kActNone); break;
+  }
+#undef HALO_ACT8
+}
+
+// d[e] *= slope(z[e]) for N values.
+template <int N>
+__device__ __forceinline__ void slope_mul(int act, const float* z, float* d) {
+#define HALO_SLOPE(A) \
+  _Pragma("unroll") for (int e = 0; e < N; ++e) d[e] *= slope_of<A>(z[e])
+  switch (act) {
+    case kActRelu: HALO_SLOPE(kActRelu); break;
+    case kActSilu: HALO_SLOPE(kActSilu); break;
+    case kActGeluTanh: HALO_SLOPE(kActGeluTanh); break;
+    case kActGeluErf: HALO_SLOPE(kActGeluErf); break;
+    default: break;
+  }
+#undef HALO_SLOPE
+}
+
+// 8 columns of an epilogue row, of which cnt (1 .. 8) exist.  Rows start 16-byte aligned and
+// lanes take multiples of 8 columns, so a whole group is one 16-byte access (two for fp32).
+template <typename T>
+__device__ __forceinline__ void load_cols(const T* p, int cnt, float* o) {
+  if (cnt == 8) {
+    load8<T>(p, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = e < cnt ? elem_f32<T>(p + e) : 0.f;
+  }
+}
+
+// Whole groups are stored non-temporally: the outputs are not read back here.
+template <typename T>
+__device__ __forceinline__ void store_cols(T* p, int cnt, const float* v) {
+  if (cnt == 8) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 w = pack16<uint16_t>(v);
+      const v4i o = {(int)w.x, (int)w.y, (int)w.z, (int)w.w};
+      __builtin_nontemporal_store(o, reinterpret_cast<v4i*>(p));
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const v4i o = {__float_as_int(v[4 * h]), __float_as_int(v[4 * h + 1]),
+                       __float_as_int(v[4 * h + 2]), __float_as_int(v[4 * h + 3])};
+        __builtin_nontemporal_store(o, reinterpret_cast<v4i*>(p + 4 * h));
+      }
+    }
+  } else {
+    for (int e = 0; e < cnt; ++e) elem_store<T>(p + e, v[e]);
+  }
+}
+
+}  // namespace halo

@@ -300,6 +300,242 @@ bool layer_dims_ok(int64_t m, int64_t n, int64_t k) {
   return m >= 0 && n >= 0 && k >= 0 && m < kMaxDim && n < kMaxDim && k < kMaxDim;
 }
 
+halo_status check_epilogue(const halo_epilogue* ep) {
+  if (!ep) return HALO_OK;
+  if (ep->activation < HALO_ACT_NONE || ep->activation > HALO_ACT_GELU_ERF) return HALO_ERR_OPTION;
+  if (!aligned16(ep->bias) || !aligned16(ep->residual) || !aligned16(ep->z)) return HALO_ERR_ALIGN;
+  return HALO_OK;
+}
+
+// The product with its epilogue.
+halo_status act_product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
+                        const float* sb, int64_t m, int64_t n, int64_t k, halo_dtype qt, void* y,
+                        halo_dtype yt, const halo_epilogue* ep, hipStream_t st) {
+  GemmArgs g{a, lda, b, ldb, sa, sb, y, n, m, n, k};
+  g.bias = ep->bias;
+  g.res = ep->residual;
+  g.z = ep->z;
+  g.act = ep->activation;
+  return from_hip(launch_gemm_act(g, qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
+}
+
+// Validation of a layer forward.
+halo_status check_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m, int64_t n,
+                      int64_t k, int32_t block, halo_dtype q_type, const void* y,
+                      halo_dtype y_type, const halo_linear_opts* opts) {
+  if (!layer_dims_ok(m, n, k) || k == 0) return HALO_ERR_SHAPE;
+  if ((m > 0 && !x) || (n > 0 && !w) || (m > 0 && n > 0 && !y)) return HALO_ERR_NULL;
+  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
+  if (q_type != HALO_I8 && q_type != HALO_E4M3) return HALO_ERR_DTYPE;
+  if (y_type != HALO_F32 && y_type != HALO_BF16) return HALO_ERR_DTYPE;
+  if (!valid_block(block)) return HALO_ERR_BLOCK;
+  const int64_t kq = contraction_len(k, block);
+  if (k % 8 != 0 || !rows_len_ok(kq, block, io_type == HALO_BF16, false)) return HALO_ERR_SHAPE;
+  if (!operand_fits(m, kq, kq) || !operand_fits(n, kq, kq)) return HALO_ERR_SHAPE;
+  if (opts && (opts->grad_rounding != HALO_ROUND_NEAREST_EVEN &&
+               opts->grad_rounding != HALO_ROUND_STOCHASTIC))
+    return HALO_ERR_OPTION;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return HALO_ERR_ALIGN;
+  if ((n * esize(y_type)) % 16 != 0) return HALO_ERR_ALIGN;
+  if (opts && check_signs(opts->signs_k) != HALO_OK) return HALO_ERR_ALIGN;
+  return HALO_OK;
+}
+
+// The layer forward on validated arguments; ep: the epilogue's part of the product's arguments
+// (NULL: the bare product).  ws holds plan_ws(m, n, k, 0, block).total bytes.
+halo_status run_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m, int64_t n,
+                    int64_t k, int32_t block, halo_dtype q_type, void* y, halo_dtype y_type,
+                    const halo_epilogue* ep, const halo_linear_opts* opts, void* ws,
+                    hipStream_t st) {
+  const WsPlan p = plan_ws(m, n, k, 0, block);
+  const int64_t kq = contraction_len(k, block);
+  char* base = static_cast<char*>(ws);
+  void* qx = base + p.off[0];
+  float* sx = reinterpret_cast<float*>(base + p.off[1]);
+  void* qw = base + p.off[2];
+  float* sw = reinterpret_cast<float*>(base + p.off[3]);
+  PassOpts po;  // X and W: the signs along k, nearest-even codes
+  if (opts) po.signs = opts->signs_k;
+  const FqArgs ax = make_fq(x, m, k, k, HALO_ALONG_ROWS, block, q_type, qx, kq, sx, po, kq);
+  const FqArgs aw = make_fq(w, n, k, k, HALO_ALONG_ROWS, block, q_type, qw, kq, sw, po, kq);
+  halo_status s = HALO_OK;
+  if (fq_rows2_supported(kq, block)) {  // X and W rows in one launch
+    FqPair pp{};
+    pp.p0 = ax;
+    pp.p1 = aw;
+    pp.has1 = 1;
+    s = from_hip(launch_fq_rows2_pair(pp, io_type == HALO_BF16 ? 1 : 0, qt_index(q_type), st));
+  } else {
+    s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
+    if (s == HALO_OK) s = run_fa(aw, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
+  }
+  if (s == HALO_OK && ep) return act_product(qx, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep, st);
+  if (s == HALO_OK)
+    s = gemm_any(qx, q_type, kq, sx, qw, q_type, kq, sw, m, n, kq, y, y_type, n, st);
+  return s;
+}
+
+// Validation of a layer backward; rot_type: the type dY's rows are rotated in.
+halo_status check_bwd(const void* dy, halo_dtype rot_type, const void* x, const void* w,
+                      halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
+                      halo_dtype q_type, halo_dtype grad_q_type, const void* dx, const void* dw,
+                      const halo_linear_opts* opts) {
+  if (!dy || !x || !w) return HALO_ERR_NULL;
+  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
+  if (q_type == HALO_I8) {
+    if (grad_q_type != HALO_I8) return HALO_ERR_DTYPE;
+  } else if (q_type == HALO_E4M3) {
+    if (grad_q_type != HALO_E5M2 && grad_q_type != HALO_E4M3) return HALO_ERR_DTYPE;
+  } else {
+    return HALO_ERR_DTYPE;
+  }
+  if (!layer_dims_ok(m, n, k) || m == 0 || n == 0 || k == 0) return HALO_ERR_SHAPE;
+  if (!valid_block(block)) return HALO_ERR_BLOCK;
+  const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
+  if (n % 8 != 0 || k % 8 != 0) return HALO_ERR_SHAPE;
+  const bool sr_dy = opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC;
+  if (dx && !rows_len_ok(nq, block, rot_type == HALO_BF16, sr_dy)) return HALO_ERR_SHAPE;
+  if (!operand_fits(m, nq, nq) || !operand_fits(k, nq, nq) || !operand_fits(n, mq, mq) ||
+      !operand_fits(k, mq, mq))
+    return HALO_ERR_SHAPE;
+  if (opts && (opts->grad_rounding != HALO_ROUND_NEAREST_EVEN &&
+               opts->grad_rounding != HALO_ROUND_STOCHASTIC))
+    return HALO_ERR_OPTION;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(w)) return HALO_ERR_ALIGN;
+  if ((dx && !aligned16(dx)) || (dw && !aligned16(dw))) return HALO_ERR_ALIGN;
+  if (opts && (check_signs(opts->signs_n) != HALO_OK || check_signs(opts->signs_m) != HALO_OK))
+    return HALO_ERR_ALIGN;
+  return HALO_OK;
+}
+
+// The layer backward on validated arguments: the rotation passes of dY (of type dy_type), W and X
+// (io_type), then the products.  ws holds plan_ws(m, n, k, 1, block).total bytes.
+halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const void* w,
+                    halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
+                    halo_dtype q_type, halo_dtype grad_q_type, void* dx, void* dw,
+                    const halo_linear_opts* opts, void* ws, hipStream_t st) {
+  const WsPlan p = plan_ws(m, n, k, 1, block);
+  const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
+  char* base = static_cast<char*>(ws);
+  char* scr = base + p.scratch_off;
+  void* scr_w = scr;
+  void* scr_dy = scr + p.scr_w;
+  void* scr_x = scr + p.scr_w + p.scr_dy;
+  const int inb = io_type == HALO_BF16 ? 1 : 0, inb_dy = dy_type == HALO_BF16 ? 1 : 0;
+  halo_status s = HALO_OK;
+
+  // pass options: the signs along each contraction dimension; the dY codes' rounding (its
+  // columns pass draws at counter word 3 ^ 2^31)
+  PassOpts on, om, gn, gm;
+  if (opts) {
+    on.signs = gn.signs = opts->signs_n;
+    om.signs = gm.signs = opts->signs_m;
+    gn.sr = gm.sr = opts->grad_rounding == HALO_ROUND_STOCHASTIC ? 1 : 0;
+    gn.key0 = gm.key0 = opts->seed[0];
+    gn.key1 = gm.key1 = opts->seed[1];
+    gn.ctr2 = gm.ctr2 = opts->counter[0];
+    gn.ctr3 = opts->counter[1];
+    gm.ctr3 = opts->counter[1] ^ 0x80000000u;
+    on.polls = om.polls = gn.polls = gm.polls = opts->exchange_polls;
+  }
+  void* qdy = base + p.off[0];
+  float* sdy = reinterpret_cast<float*>(base + p.off[1]);
+  void* qwt = base + p.off[2];
+  float* swt = reinterpret_cast<float*>(base + p.off[3]);
+  void* qdyt = base + p.off[4];
+  float* sdyt = reinterpret_cast<float*>(base + p.off[5]);
+  void* qxt = base + p.off[6];
+  float* sxt = reinterpret_cast<float*>(base + p.off[7]);
+  // dX = dY W: rows of dY and columns of W along n; dW = dY^T X: columns of dY and X along m
+  const FqArgs rows = make_fq(dy, m, n, n, HALO_ALONG_ROWS, block, grad_q_type, qdy, nq, sdy, gn, nq);
+  const FqArgs cw = make_fq(w, n, k, k, HALO_ALONG_COLS, block, q_type, qwt, nq, swt, on, nq);
+  const FqArgs cdy = make_fq(dy, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
+  const FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
+
+  // the single-read column passes need their scratch cleared: folded into the first kernel
+  // when that is a rows pass, else one fill
+  bool zero_pending = p.scratch_bytes > 0;
+  auto clear_scratch = [&]() {
+    if (!zero_pending || s != HALO_OK) return;
+    s = from_hip(launch_fill_zero(reinterpret_cast<float*>(scr), (int64_t)(p.scratch_bytes / 4), st));
+    zero_pending = false;
+  };
+  // one column pass: single-read when covered (its scratch already clear), else two reads
+  auto cols_pass = [&](const FqArgs& a, halo_dtype at, halo_dtype qt, void* sws, size_t sbytes) {
+    if (s != HALO_OK) return;
+    const int ib = at == HALO_BF16 ? 1 : 0;
+    if (fq_cols2_supported(a.len, a.nvec, block, ib, a.sr != 0, sbytes))
+      s = from_hip(launch_fq_cols2_pair(a, sws, nullptr, nullptr, ib, qt_index(qt), 1, st));
+    else
+      s = run_fa(a, at, HALO_ALONG_COLS, qt, nullptr, 0, st);
+  };
+  // the rows pass of dY, clearing the scratch as a side job when it runs as the wave kernel
+  auto rows_pass = [&]() {
+    if (s != HALO_OK) return;
+    if (fq_rows2_supported(nq, block) && (inb_dy || !rows.sr)) {
+      FqPair pp{};
+      pp.p0 = rows;
+      if (zero_pending) {
+        pp.zero = reinterpret_cast<uint32_t*>(scr);
+        pp.nzero = (int64_t)(p.scratch_bytes / 4);
+        zero_pending = false;
+      }
+      s = from_hip(launch_fq_rows2_pair(pp, inb_dy, qt_index(grad_q_type), st));
+    } else {
+      s = run_fa(rows, dy_type, HALO_ALONG_ROWS, grad_q_type, nullptr, 0, st);
+    }
+  };
+  const int qg = qt_index(grad_q_type), qw = qt_index(q_type);
+  const bool pair_ok = (qg == 0 && qw == 0) || (qg == 2 && qw == 1) || (qg == 1 && qw == 1);
+  if (dx && dw && inb && inb_dy && pair_ok && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
+      fq_cols2_supported(mq, n, block, 1, cdy.sr != 0, p.scr_dy) &&
+      fq_cols2_supported(mq, k, block, 1, false, p.scr_x)) {
+    // every rotation pass of the backward in one launch (or two, when the dY rows are long):
+    // the passes overlap on the device, then the two products
+    const bool rows_in = fq_batch_rows_ok(nq);
+    if (rows_in) {
+      clear_scratch();
+    } else {
+      rows_pass();
+      clear_scratch();
+    }
+    if (s == HALO_OK)
+      s = from_hip(launch_fq_batch(rows_in ? &rows : nullptr, cw, scr_w, cdy, scr_dy, cx, scr_x,
+                                   qg, qw, st));
+  } else {
+    if (dx) rows_pass();
+    clear_scratch();
+    if (dx) cols_pass(cw, io_type, q_type, scr_w, p.scr_w);
+    if (dw) {
+      const bool c1 = fq_cols2_supported(mq, n, block, inb_dy, cdy.sr != 0, p.scr_dy);
+      const bool c2 = fq_cols2_supported(mq, k, block, inb, cx.sr != 0, p.scr_x);
+      if (s == HALO_OK && c1 && c2 && inb == inb_dy && grad_q_type == q_type && cdy.sr == cx.sr) {
+        // dY and X columns in one launch
+        s = from_hip(launch_fq_cols2_pair(cdy, scr_dy, &cx, scr_x, inb, qt_index(q_type), 1, st));
+      } else {
+        cols_pass(cdy, dy_type, grad_q_type, scr_dy, p.scr_dy);
+        cols_pass(cx, io_type, q_type, scr_x, p.scr_x);
+      }
+    }
+  }
+  if (s == HALO_OK && dx && dw) {  // both products in one launch
+    const GemmArgs gx{qdy, nq, qwt, nq, sdy, swt, dx, k, m, k, nq};
+    const GemmArgs gw{qdyt, mq, qxt, mq, sdyt, sxt, dw, k, n, k, mq};
+    const int out = io_type == HALO_F32 ? 1 : 2;
+    if (grad_q_type == HALO_I8)
+      s = from_hip(launch_gemm_pair(gx, &gw, 0, 0, 0, out, st));
+    else
+      s = from_hip(launch_gemm_pair(gx, &gw, 1, gemm_kind_fmt(grad_q_type), gemm_kind_fmt(q_type),
+                                    out, st));
+    return s;
+  }
+  if (s == HALO_OK && dx)
+    s = gemm_any(qdy, grad_q_type, nq, sdy, qwt, q_type, nq, swt, m, k, nq, dx, io_type, k, st);
+  if (s == HALO_OK && dw)
+    s = gemm_any(qdyt, grad_q_type, mq, sdyt, qxt, q_type, mq, sxt, n, k, mq, dw, io_type, k, st);
+  return s;
+}
+
 // Row operators take any stride and any alignment of whole elements.
 bool aligned_to(const void* p, int e) { return (reinterpret_cast<uintptr_t>(p) & (e - 1)) == 0; }
 
@@ -669,48 +905,12 @@ halo_status halo_linear_fwd_ex(const void* x, const void* w, halo_dtype io_type,
                                halo_dtype y_type, const halo_linear_opts* opts, void* ws,
                                size_t ws_bytes, void* stream) {
   if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
-  if (!layer_dims_ok(m, n, k) || k == 0) return HALO_ERR_SHAPE;
-  if ((m > 0 && !x) || (n > 0 && !w) || (m > 0 && n > 0 && !y)) return HALO_ERR_NULL;
-  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
-  if (q_type != HALO_I8 && q_type != HALO_E4M3) return HALO_ERR_DTYPE;
-  if (y_type != HALO_F32 && y_type != HALO_BF16) return HALO_ERR_DTYPE;
-  if (!valid_block(block)) return HALO_ERR_BLOCK;
-  const int64_t kq = contraction_len(k, block);
-  if (k % 8 != 0 || !rows_len_ok(kq, block, io_type == HALO_BF16, false)) return HALO_ERR_SHAPE;
-  if (!operand_fits(m, kq, kq) || !operand_fits(n, kq, kq)) return HALO_ERR_SHAPE;
-  if (opts && (opts->grad_rounding != HALO_ROUND_NEAREST_EVEN &&
-               opts->grad_rounding != HALO_ROUND_STOCHASTIC))
-    return HALO_ERR_OPTION;
-  if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return HALO_ERR_ALIGN;
-  if ((n * esize(y_type)) % 16 != 0) return HALO_ERR_ALIGN;
-  if (opts && check_signs(opts->signs_k) != HALO_OK) return HALO_ERR_ALIGN;
-  const WsPlan p = plan_ws(m, n, k, 0, block);
-  if (!ws || ws_bytes < p.total) return HALO_ERR_WORKSPACE;
+  const halo_status s = check_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, opts);
+  if (s != HALO_OK) return s;
+  if (!ws || ws_bytes < plan_ws(m, n, k, 0, block).total) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
-  char* base = static_cast<char*>(ws);
-  void* qx = base + p.off[0];
-  float* sx = reinterpret_cast<float*>(base + p.off[1]);
-  void* qw = base + p.off[2];
-  float* sw = reinterpret_cast<float*>(base + p.off[3]);
-  hipStream_t st = (hipStream_t)stream;
-  PassOpts po;  // X and W: the signs along k, nearest-even codes
-  if (opts) po.signs = opts->signs_k;
-  const FqArgs ax = make_fq(x, m, k, k, HALO_ALONG_ROWS, block, q_type, qx, kq, sx, po, kq);
-  const FqArgs aw = make_fq(w, n, k, k, HALO_ALONG_ROWS, block, q_type, qw, kq, sw, po, kq);
-  halo_status s = HALO_OK;
-  if (fq_rows2_supported(kq, block)) {  // X and W rows in one launch
-    FqPair pp{};
-    pp.p0 = ax;
-    pp.p1 = aw;
-    pp.has1 = 1;
-    s = from_hip(launch_fq_rows2_pair(pp, io_type == HALO_BF16 ? 1 : 0, qt_index(q_type), st));
-  } else {
-    s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
-    if (s == HALO_OK) s = run_fa(aw, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
-  }
-  if (s == HALO_OK)
-    s = gemm_any(qx, q_type, kq, sx, qw, q_type, kq, sw, m, n, kq, y, y_type, n, st);
-  return s;
+  return run_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, nullptr, opts, ws,
+                 (hipStream_t)stream);
 }
 
 halo_status halo_linear_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
@@ -727,152 +927,13 @@ halo_status halo_linear_bwd_ex(const void* dy, const void* x, const void* w, hal
                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
                                void* stream) {
   if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
-  if (!dy || !x || !w) return HALO_ERR_NULL;
-  if (io_type != HALO_F32 && io_type != HALO_BF16) return HALO_ERR_DTYPE;
-  if (q_type == HALO_I8) {
-    if (grad_q_type != HALO_I8) return HALO_ERR_DTYPE;
-  } else if (q_type == HALO_E4M3) {
-    if (grad_q_type != HALO_E5M2 && grad_q_type != HALO_E4M3) return HALO_ERR_DTYPE;
-  } else {
-    return HALO_ERR_DTYPE;
-  }
-  if (!layer_dims_ok(m, n, k) || m == 0 || n == 0 || k == 0) return HALO_ERR_SHAPE;
-  if (!valid_block(block)) return HALO_ERR_BLOCK;
-  const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
-  if (n % 8 != 0 || k % 8 != 0) return HALO_ERR_SHAPE;
-  const bool sr_dy = opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC;
-  if (dx && !rows_len_ok(nq, block, io_type == HALO_BF16, sr_dy)) return HALO_ERR_SHAPE;
-  if (!operand_fits(m, nq, nq) || !operand_fits(k, nq, nq) || !operand_fits(n, mq, mq) ||
-      !operand_fits(k, mq, mq))
-    return HALO_ERR_SHAPE;
-  if (opts && (opts->grad_rounding != HALO_ROUND_NEAREST_EVEN &&
-               opts->grad_rounding != HALO_ROUND_STOCHASTIC))
-    return HALO_ERR_OPTION;
-  if (!aligned16(dy) || !aligned16(x) || !aligned16(w)) return HALO_ERR_ALIGN;
-  if ((dx && !aligned16(dx)) || (dw && !aligned16(dw))) return HALO_ERR_ALIGN;
-  if (opts && (check_signs(opts->signs_n) != HALO_OK || check_signs(opts->signs_m) != HALO_OK))
-    return HALO_ERR_ALIGN;
-  const WsPlan p = plan_ws(m, n, k, 1, block);
-  if (!ws || ws_bytes < p.total) return HALO_ERR_WORKSPACE;
+  const halo_status s = check_bwd(dy, io_type, x, w, io_type, m, n, k, block, q_type, grad_q_type,
+                                  dx, dw, opts);
+  if (s != HALO_OK) return s;
+  if (!ws || ws_bytes < plan_ws(m, n, k, 1, block).total) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
-  char* base = static_cast<char*>(ws);
-  char* scr = base + p.scratch_off;
-  void* scr_w = scr;
-  void* scr_dy = scr + p.scr_w;
-  void* scr_x = scr + p.scr_w + p.scr_dy;
-  const int inb = io_type == HALO_BF16 ? 1 : 0;
-  hipStream_t st = (hipStream_t)stream;
-  halo_status s = HALO_OK;
-
-  // pass options: the signs along each contraction dimension; the dY codes' rounding (its
-  // columns pass draws at counter word 3 ^ 2^31)
-  PassOpts on, om, gn, gm;
-  if (opts) {
-    on.signs = gn.signs = opts->signs_n;
-    om.signs = gm.signs = opts->signs_m;
-    gn.sr = gm.sr = opts->grad_rounding == HALO_ROUND_STOCHASTIC ? 1 : 0;
-    gn.key0 = gm.key0 = opts->seed[0];
-    gn.key1 = gm.key1 = opts->seed[1];
-    gn.ctr2 = gm.ctr2 = opts->counter[0];
-    gn.ctr3 = opts->counter[1];
-    gm.ctr3 = opts->counter[1] ^ 0x80000000u;
-    on.polls = om.polls = gn.polls = gm.polls = opts->exchange_polls;
-  }
-  void* qdy = base + p.off[0];
-  float* sdy = reinterpret_cast<float*>(base + p.off[1]);
-  void* qwt = base + p.off[2];
-  float* swt = reinterpret_cast<float*>(base + p.off[3]);
-  void* qdyt = base + p.off[4];
-  float* sdyt = reinterpret_cast<float*>(base + p.off[5]);
-  void* qxt = base + p.off[6];
-  float* sxt = reinterpret_cast<float*>(base + p.off[7]);
-  // dX = dY W: rows of dY and columns of W along n; dW = dY^T X: columns of dY and X along m
-  const FqArgs rows = make_fq(dy, m, n, n, HALO_ALONG_ROWS, block, grad_q_type, qdy, nq, sdy, gn, nq);
-  const FqArgs cw = make_fq(w, n, k, k, HALO_ALONG_COLS, block, q_type, qwt, nq, swt, on, nq);
-  const FqArgs cdy = make_fq(dy, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
-  const FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
-
-  // the single-read column passes need their scratch cleared: folded into the first kernel
-  // when that is a rows pass, else one fill
-  bool zero_pending = p.scratch_bytes > 0;
-  auto clear_scratch = [&]() {
-    if (!zero_pending || s != HALO_OK) return;
-    s = from_hip(launch_fill_zero(reinterpret_cast<float*>(scr), (int64_t)(p.scratch_bytes / 4), st));
-    zero_pending = false;
-  };
-  // one column pass: single-read when covered (its scratch already clear), else two reads
-  auto cols_pass = [&](const FqArgs& a, halo_dtype qt, void* sws, size_t sbytes) {
-    if (s != HALO_OK) return;
-    if (fq_cols2_supported(a.len, a.nvec, block, inb, a.sr != 0, sbytes))
-      s = from_hip(launch_fq_cols2_pair(a, sws, nullptr, nullptr, inb, qt_index(qt), 1, st));
-    else
-      s = run_fa(a, io_type, HALO_ALONG_COLS, qt, nullptr, 0, st);
-  };
-  // the rows pass of dY, clearing the scratch as a side job when it runs as the wave kernel
-  auto rows_pass = [&]() {
-    if (s != HALO_OK) return;
-    if (fq_rows2_supported(nq, block) && (inb || !rows.sr)) {
-      FqPair pp{};
-      pp.p0 = rows;
-      if (zero_pending) {
-        pp.zero = reinterpret_cast<uint32_t*>(scr);
-        pp.nzero = (int64_t)(p.scratch_bytes / 4);
-        zero_pending = false;
-      }
-      s = from_hip(launch_fq_rows2_pair(pp, inb, qt_index(grad_q_type), st));
-    } else {
-      s = run_fa(rows, io_type, HALO_ALONG_ROWS, grad_q_type, nullptr, 0, st);
-    }
-  };
-  const int qg = qt_index(grad_q_type), qw = qt_index(q_type);
-  const bool pair_ok = (qg == 0 && qw == 0) || (qg == 2 && qw == 1) || (qg == 1 && qw == 1);
-  if (dx && dw && inb && pair_ok && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
-      fq_cols2_supported(mq, n, block, 1, cdy.sr != 0, p.scr_dy) &&
-      fq_cols2_supported(mq, k, block, 1, false, p.scr_x)) {
-    // every rotation pass of the backward in one launch (or two, when the dY rows are long):
-    // the passes overlap on the device, then the two products
-    const bool rows_in = fq_batch_rows_ok(nq);
-    if (rows_in) {
-      clear_scratch();
-    } else {
-      rows_pass();
-      clear_scratch();
-    }
-    if (s == HALO_OK)
-      s = from_hip(launch_fq_batch(rows_in ? &rows : nullptr, cw, scr_w, cdy, scr_dy, cx, scr_x,
-                                   qg, qw, st));
-  } else {
-    if (dx) rows_pass();
-    clear_scratch();
-    if (dx) cols_pass(cw, q_type, scr_w, p.scr_w);
-    if (dw) {
-      const bool c1 = fq_cols2_supported(mq, n, block, inb, cdy.sr != 0, p.scr_dy);
-      const bool c2 = fq_cols2_supported(mq, k, block, inb, cx.sr != 0, p.scr_x);
-      if (s == HALO_OK && c1 && c2 && grad_q_type == q_type && cdy.sr == cx.sr) {
-        // dY and X columns in one launch
-        s = from_hip(launch_fq_cols2_pair(cdy, scr_dy, &cx, scr_x, inb, qt_index(q_type), 1, st));
-      } else {
-        cols_pass(cdy, grad_q_type, scr_dy, p.scr_dy);
-        cols_pass(cx, q_type, scr_x, p.scr_x);
-      }
-    }
-  }
-  if (s == HALO_OK && dx && dw) {  // both products in one launch
-    const GemmArgs gx{qdy, nq, qwt, nq, sdy, swt, dx, k, m, k, nq};
-    const GemmArgs gw{qdyt, mq, qxt, mq, sdyt, sxt, dw, k, n, k, mq};
-    const int out = io_type == HALO_F32 ? 1 : 2;
-    if (grad_q_type == HALO_I8)
-      s = from_hip(launch_gemm_pair(gx, &gw, 0, 0, 0, out, st));
-    else
-      s = from_hip(launch_gemm_pair(gx, &gw, 1, gemm_kind_fmt(grad_q_type), gemm_kind_fmt(q_type),
-                                    out, st));
-    return s;
-  }
-  if (s == HALO_OK && dx)
-    s = gemm_any(qdy, grad_q_type, nq, sdy, qwt, q_type, nq, swt, m, k, nq, dx, io_type, k, st);
-  if (s == HALO_OK && dw)
-    s = gemm_any(qdyt, grad_q_type, mq, sdyt, qxt, q_type, mq, sxt, n, k, mq, dw, io_type, k, st);
-  return s;
+  return run_bwd(dy, io_type, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw, opts, ws,
+                 (hipStream_t)stream);
 }
 
 halo_status halo_linear_bwd(const void* dy, const void* x, const void* w, halo_dtype io_type,
@@ -882,6 +943,93 @@ halo_status halo_linear_bwd(const void* dy, const void* x, const void* w, halo_d
   if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
   return halo_linear_bwd_ex(dy, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw,
                             nullptr, ws, ws_bytes, stream);
+}
+
+// ---- the layer with its epilogue ------------------------------------------------------------
+
+halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type, void* y,
+                                halo_dtype y_type, const halo_epilogue* ep,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, opts);
+  if (s == HALO_OK) s = check_epilogue(ep);
+  if (s != HALO_OK) return s;
+  if (!ws || ws_bytes < plan_ws(m, n, k, 0, block).total) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  const halo_epilogue none{};
+  return run_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, ep ? ep : &none, opts, ws,
+                 (hipStream_t)stream);
+}
+
+size_t halo_linear_act_q_workspace_bytes(int64_t m, int64_t k, int32_t block) {
+  if (!layer_dims_ok(m, 0, k) || !valid_block(block)) return 0;
+  return round256((size_t)m * contraction_len(k, block)) + round256((size_t)m * 4);
+}
+
+halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
+                              void* y, halo_dtype y_type, const halo_epilogue* ep,
+                              const uint32_t* signs_k, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_fwd(x, qw, io_type, m, n, k, block, q_type, y, y_type, nullptr);
+  if (s == HALO_OK) s = check_epilogue(ep);
+  if (s != HALO_OK) return s;
+  const int64_t kq = contraction_len(k, block);
+  if (kq != padded_len(k, block)) return HALO_ERR_SHAPE;
+  if (n > 0 && !sw) return HALO_ERR_NULL;
+  if (!aligned16(sw) || check_signs(signs_k) != HALO_OK) return HALO_ERR_ALIGN;
+  if (m == 0 || n == 0) return HALO_OK;
+  if (!ws || ws_bytes < halo_linear_act_q_workspace_bytes(m, k, block)) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  const hipStream_t st = (hipStream_t)stream;
+  char* base = static_cast<char*>(ws);
+  float* sx = reinterpret_cast<float*>(base + round256((size_t)m * kq));
+  PassOpts po;
+  po.signs = signs_k;
+  const FqArgs ax = make_fq(x, m, k, k, HALO_ALONG_ROWS, block, q_type, base, kq, sx, po, kq);
+  s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
+  if (s != HALO_OK) return s;
+  const halo_epilogue none{};
+  return act_product(base, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep ? ep : &none, st);
+}
+
+size_t halo_linear_act_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                           halo_dtype q_type) {
+  const size_t layer = halo_linear_workspace_bytes_ex(m, n, k, block, q_type, 1);
+  if (layer == 0) return 0;
+  return layer + round256((size_t)m * n * 4) + round256((size_t)act_grad_parts(m, n) * n * 4);
+}
+
+halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation activation,
+                                const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                halo_dtype grad_q_type, void* dx, void* dw, void* db,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
+  if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return HALO_ERR_OPTION;
+  const bool act = activation != HALO_ACT_NONE;
+  halo_status s = check_bwd(dy, act ? HALO_F32 : io_type, x, w, io_type, m, n, k, block, q_type,
+                            grad_q_type, dx, dw, opts);
+  if (s != HALO_OK) return s;
+  if (act && !z) return HALO_ERR_NULL;
+  if (!aligned16(z) || !aligned16(db)) return HALO_ERR_ALIGN;
+  if (!ws || ws_bytes < halo_linear_act_bwd_workspace_bytes(m, n, k, block, q_type))
+    return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  const hipStream_t st = (hipStream_t)stream;
+  char* tail = static_cast<char*>(ws) + plan_ws(m, n, k, 1, block).total;
+  float* dz = reinterpret_cast<float*>(tail);
+  float* part = reinterpret_cast<float*>(tail + round256((size_t)m * n * 4));
+  if (act || db) {
+    const hipError_t e = launch_act_grad(dy, z, (int)activation, io_type == HALO_BF16 ? 1 : 0, m, n,
+                                         act ? dz : nullptr, db, part, st);
+    if (e != hipSuccess) return HALO_ERR_HIP;
+  }
+  return run_bwd(act ? dz : dy, act ? HALO_F32 : io_type, x, w, io_type, m, n, k, block, q_type,
+                 grad_q_type, dx, dw, opts, ws, st);
 }
 
 }  // extern "C"

@@ -104,6 +104,12 @@ struct GemmArgs {
   void* c;        // [m x n], ldc (elements)
   int64_t ldc;
   int64_t m, n, k;
+  // the layer's epilogue (launch_gemm_act only): bias [n], residual and z [m x n] (ldc), of the
+  // output's type, each may be NULL; act: an Act of epilogue.h
+  const void* bias = nullptr;
+  const void* res = nullptr;
+  void* z = nullptr;
+  int act = 0;
 };
 
 // kind: 0 INT8, 1 FP8.  afmt/bfmt (FP8 only): 0 E4M3, 1 E5M2.  out: 0 int32, 1 fp32, 2 bf16.
@@ -111,6 +117,19 @@ hipError_t launch_gemm(const GemmArgs& g, int kind, int afmt, int bfmt, int out,
 // Two products of the same kind, formats and output type in one launch (g1 may be NULL).
 hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs* g1, int kind, int afmt, int bfmt,
                             int out, hipStream_t st);
+
+// One product with the layer's epilogue: y = act(z) + residual, z = (acc sa) sb + bias.  kind: 0
+// INT8, 1 FP8 (E4M3 both).  out: 1 fp32, 2 bf16.  c, res and z rows and bias 16-byte aligned.
+hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st);
+// The same for up to kSkinnyRows rows of a (gemm_skinny.hip).
+constexpr int kSkinnyRows = 64;
+hipError_t launch_gemm_skinny(const GemmArgs& g, int kind, int out, hipStream_t st);
+
+// dz = dy act'(z) in fp32 and, when db is not NULL, db = its sums over the m rows (bias type:
+// that of dy).  part: act_grad_parts(m, n) x n floats of scratch (db only).
+int64_t act_grad_parts(int64_t m, int64_t n);
+hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
+                           int64_t n, float* dz, void* db, float* part, hipStream_t st);
 
 // The join between two blocks (block_norm.hip).  Optional tensors are NULL; leading dimensions
 // in elements; group_len = tokens / gate rows.

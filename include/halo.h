@@ -63,8 +63,9 @@ typedef enum {
     HALO_ERR_ALIGN = 5,     /* pointer or leading dimension not 16-byte aligned            */
     HALO_ERR_WORKSPACE = 6, /* workspace NULL or smaller than the size query returns       */
     HALO_ERR_HIP = 7,       /* the HIP runtime refused a launch                            */
-    HALO_ERR_OPTION = 8     /* invalid option: unknown rounding mode, or stochastic        */
-                            /* rounding asked of the fp32 value mode                       */
+    HALO_ERR_OPTION = 8     /* invalid option: unknown rounding mode or activation,        */
+                            /* stochastic rounding asked of the fp32 value mode, eps < 0   */
+                            /* or a temperature that is not positive and finite            */
 } halo_status;
 
 typedef enum {
@@ -345,6 +346,68 @@ halo_status halo_fwht_quant_dual(const void* x, halo_dtype x_type, int64_t rows,
                                  float* scale_c, const halo_quant_opts* row_opts,
                                  const halo_quant_opts* col_opts, void* ws, size_t ws_bytes,
                                  void* stream);
+
+/*
+ * The layer with its epilogue: halo_linear_fwd's product, then
+ *   z = X W^T + bias,   y = act(z) + residual
+ * in one pass over the accumulators (fp32 until the stores; y and z are rounded once each).
+ */
+typedef enum {
+    HALO_ACT_NONE = 0,
+    HALO_ACT_RELU = 1,      /* max(z, 0)                                            */
+    HALO_ACT_SILU = 2,      /* z / (1 + exp(-z))                                    */
+    HALO_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2    */
+    HALO_ACT_GELU_ERF = 4   /* z (1 + erf(z / sqrt 2)) / 2                          */
+} halo_activation;
+
+typedef struct {
+    const void* bias;     /* [n] of y_type, or NULL                                     */
+    const void* residual; /* [m x n] of y_type, dense, or NULL; may be y                */
+    void* z;              /* [m x n] of y_type, dense: receives z (for the backward), or NULL */
+    int32_t activation;   /* halo_activation                                            */
+} halo_epilogue;
+
+/* Arguments, workspace (halo_linear_workspace_bytes[_ex], backward 0) and errors as
+ * halo_linear_fwd_ex; ep NULL: the bare product.  Pointers of ep 16-byte aligned; an unknown
+ * activation gives HALO_ERR_OPTION.  y, z and residual must not overlap except residual = y. */
+halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type, void* y,
+                                halo_dtype y_type, const halo_epilogue* ep,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/*
+ * The same on weights quantised once (serving): qw [n x kq] and sw [n] are the codes and scales
+ * that halo_fwht_quant gives along the rows of W (with the same block, signs and q_type), dense,
+ * kq = k rounded up to a multiple of block, which must be a multiple of 32.  Only x is rotated
+ * and quantised here.  One to 64 rows of x run a kernel bound by reading qw once.
+ *   ws   at least halo_linear_act_q_workspace_bytes(m, k, block) bytes, 16-byte aligned.
+ */
+size_t halo_linear_act_q_workspace_bytes(int64_t m, int64_t k, int32_t block);
+halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
+                              void* y, halo_dtype y_type, const halo_epilogue* ep,
+                              const uint32_t* signs_k, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the layer with its epilogue, for dy of y (the residual's gradient is dy itself):
+ *   dz = dy act'(z),   dX = dz W,   dW = dz^T X (as halo_linear_bwd),   db = sum over rows of dz.
+ * dz is fp32 from the activation to its rotation; only the 8-bit codes round it.  db sums in
+ * fp32 in a fixed order and is rounded once to io_type.
+ *   z            the forward's z (io_type, dense); not read with HALO_ACT_NONE (may be NULL).
+ *   dx, dw, db   each may be NULL to skip it; db [n].
+ *   ws           at least halo_linear_act_bwd_workspace_bytes(...) bytes.
+ * Everything else as halo_linear_bwd_ex (with an activation, the dX product's padded n is limited
+ * under stochastic rounding as for fp32 dY).
+ */
+size_t halo_linear_act_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                           halo_dtype q_type);
+halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation activation,
+                                const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                halo_dtype grad_q_type, void* dx, void* dw, void* db,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream);
 
 /*
  * Row operators: the join between two blocks of a model and the distillation loss.  Unlike the
