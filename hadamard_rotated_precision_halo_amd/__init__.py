@@ -576,20 +576,21 @@ def linear_bwd(dy, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, want_dx=T
 def _rows(t, name, shape, dtype, device):
     """A 2-D argument of exactly shape and dtype with unit column stride and any row stride of
     at least its width; returns the row stride."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and tuple(t.shape) == shape
-            and t.dtype == dtype and t.device == device):
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}")
-    ld = t.stride(0)
-    if t.shape[0] <= 1:  # one row: its stride says nothing
-        ld = max(ld, shape[1])
-    if t.numel() and ((shape[1] > 1 and t.stride(1) != 1) or ld < shape[1]):
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == device):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    rows, cols = shape
+    if t.is_contiguous():
+        return cols
+    ld = t.stride(0) if rows > 1 else cols  # one row: its stride says nothing
+    if t.numel() and ((cols > 1 and t.stride(1) != 1) or ld < cols):
         raise ValueError(f"{name} must be row-major with unit column stride")
-    return max(ld, shape[1])
+    return max(ld, cols)
 
 
 def _vec(t, name, n, dtype, device):
     """A contiguous 1-D argument of exactly n entries."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 1 and t.shape[0] == n and t.dtype == dtype
+    if not (isinstance(t, torch.Tensor) and t.dim() == 1 and t.shape[0] == n and t.dtype is dtype
             and t.device == device and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries on {device}")
 
@@ -597,16 +598,31 @@ def _vec(t, name, n, dtype, device):
 def _io_2d(t, name):
     if not (isinstance(t, torch.Tensor) and t.dim() == 2):
         raise ValueError(f"{name} must be a 2-D tensor")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
-        raise TypeError(f"unsupported dtype {t.dtype}")
+    dt = t.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
+        raise TypeError(f"unsupported dtype {dt}")
     if not t.is_cuda:
         raise ValueError("the inputs must be GPU tensors")
-    return t.dtype, t.device
+    return dt, t.device
+
+
+# torch's raw handle of a device's current stream: a twentieth of the time of building the
+# torch.cuda.Stream object for it, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _current_stream(device, stream):
     """The HIP stream of a call on tensors of `device`: `stream`, or that device's current one."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _dense_like(t):
+    """A new contiguous tensor of t's shape, type and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _p(t):
@@ -628,7 +644,7 @@ def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scal
     and for the fp32 factors of norms that were not asked for.
     """
     dt, dev = _io_2d(r, "r")
-    t, d = shape = tuple(r.shape)
+    t, d = shape = r.shape
     ldr = _rows(r, "r", shape, dt, dev)
     ldy = ldro = ldh = ldg = 0
     groups = 1
@@ -644,16 +660,18 @@ def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scal
             _vec(post_weight, "post_weight", d, dt, dev)
             rstd_post = torch.empty(t, dtype=torch.float32, device=dev)
         if r_out is None:
-            r_out = torch.empty(shape, dtype=dt, device=dev)
-        ldro = _rows(r_out, "r_out", shape, dt, dev)
+            r_out, ldro = _dense_like(r), d
+        else:
+            ldro = _rows(r_out, "r_out", shape, dt, dev)
     elif gate is not None or post_weight is not None or r_out is not None:
         raise ValueError("gate, post_weight and r_out need y")
     if pre_weight is not None:
         _vec(pre_weight, "pre_weight", d, dt, dev)
         rstd_pre = torch.empty(t, dtype=torch.float32, device=dev)
         if h is None:
-            h = torch.empty(shape, dtype=dt, device=dev)
-        ldh = _rows(h, "h", shape, dt, dev)
+            h, ldh = _dense_like(r), d
+        else:
+            ldh = _rows(h, "h", shape, dt, dev)
     elif h is not None:
         raise ValueError("h needs pre_weight")
     st = lib().halo_block_norm_fwd(_p(r), ldr, _p(y), ldy, _p(gate), ldg, groups, _p(post_weight),
@@ -677,7 +695,7 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
     [groups, dim].  The parameter gradients are fp32 sums in a fixed order, rounded once."""
     ref = dr_out if dr_out is not None else dh
     dt, dev = _io_2d(ref, "dr_out" if dr_out is not None else "dh")
-    t, d = shape = tuple(ref.shape)
+    t, d = shape = ref.shape
     if t == 0:
         raise ValueError("the gradient needs at least one token")
     lddro = lddh = ldro = ldy = ldg = lddy = 0
@@ -709,13 +727,15 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
             if want_dpost:
                 dpost = torch.empty(d, dtype=dt, device=dev)
         if dy is None:
-            dy = torch.empty(shape, dtype=dt, device=dev)
-        lddy = _rows(dy, "dy", shape, dt, dev)
+            dy, lddy = _dense_like(y), d
+        else:
+            lddy = _rows(dy, "dy", shape, dt, dev)
     elif gate is not None or post_weight is not None or dy is not None:
         raise ValueError("gate, post_weight and dy need y")
     if dr is None:
-        dr = torch.empty(shape, dtype=dt, device=dev)
-    lddr = _rows(dr, "dr", shape, dt, dev)
+        dr, lddr = _dense_like(ref), d
+    else:
+        lddr = _rows(dr, "dr", shape, dt, dev)
     L = lib()
     code = _TORCH_CODE[dt]
     if workspace is None:
@@ -737,16 +757,17 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
 
 def _distill_args(logits, idx, tlogits):
     dt, dev = _io_2d(logits, "logits")
-    t, v = logits.shape
-    ldl = _rows(logits, "logits", (t, v), dt, dev)
+    t, v = shape = logits.shape
+    ldl = _rows(logits, "logits", shape, dt, dev)
     if not (isinstance(tlogits, torch.Tensor) and tlogits.dim() == 2):
         raise ValueError("tlogits must be a 2-D tensor")
     tt = tlogits.dtype
     if tt is not torch.float32 and tt is not torch.bfloat16:
         raise TypeError(f"unsupported dtype {tt}")
     top = tlogits.shape[1]
-    ldt = _rows(tlogits, "tlogits", (t, top), tt, dev)
-    ldi = _rows(idx, "idx", (t, top), torch.int32, dev)
+    shape = (t, top)
+    ldt = _rows(tlogits, "tlogits", shape, tt, dev)
+    ldi = _rows(idx, "idx", shape, torch.int32, dev)
     return dt, dev, t, v, top, ldl, ldi, ldt, _TORCH_CODE[tt]
 
 
@@ -780,8 +801,9 @@ def distill_bwd(dloss, logits, lse, idx, tlogits, temperature=1.0, dlogits=None,
     _vec(dloss, "dloss", t, torch.float32, dev)
     _vec(lse, "lse", t, torch.float32, dev)
     if dlogits is None:
-        dlogits = torch.empty((t, v), dtype=dt, device=dev)
-    ldd = _rows(dlogits, "dlogits", (t, v), dt, dev)
+        dlogits, ldd = _dense_like(logits), v
+    else:
+        ldd = _rows(dlogits, "dlogits", logits.shape, dt, dev)
     st = lib().halo_distill_bwd(_p(dloss), _p(logits), _TORCH_CODE[dt], ldl, _p(lse), _p(idx), ldi,
                                 _p(tlogits), tc, ldt, t, v, top, temperature, _p(dlogits), ldd,
                                 _current_stream(dev, stream))
@@ -799,8 +821,9 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
     loss = _out_vec(loss, "loss", t, dev)
     lse = _out_vec(lse, "lse", t, dev)
     if dlogits is None:
-        dlogits = torch.empty((t, v), dtype=dt, device=dev)
-    ldd = _rows(dlogits, "dlogits", (t, v), dt, dev)
+        dlogits, ldd = _dense_like(logits), v
+    else:
+        ldd = _rows(dlogits, "dlogits", logits.shape, dt, dev)
     st = lib().halo_distill_fwd_bwd(_p(logits), _TORCH_CODE[dt], ldl, _p(idx), ldi, _p(tlogits),
                                     tc, ldt, _p(dloss), t, v, top, temperature, _p(loss), _p(lse),
                                     _p(dlogits), ldd, _current_stream(dev, stream))
@@ -814,9 +837,9 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
 
 def _dense(t, name, shape, dtype, device):
     """A contiguous 2-D argument of exactly shape and dtype."""
-    if not (isinstance(t, torch.Tensor) and t.dim() == 2 and tuple(t.shape) == shape
-            and t.dtype == dtype and t.device == device and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == device and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
 
 
 def _activation(name):
@@ -862,7 +885,8 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
     yt = y.dtype if y is not None else (y_dtype or dt)
     if y is None:
         y = torch.empty((m, n), dtype=yt, device=dev)
-    _dense(y, "y", (m, n), yt, dev)
+    else:
+        _dense(y, "y", (m, n), yt, dev)
     if want_z and z is None:
         z = torch.empty((m, n), dtype=yt, device=dev)
     ep = _epilogue(bias, activation, residual, z, (m, n), yt, dev)
@@ -896,7 +920,7 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
     if not (isinstance(qw, torch.Tensor) and qw.dim() == 2):
         raise ValueError("qw must be a 2-D tensor")
     n, block = qw.shape[0], int(block)
-    _dense(x, "x", (m, k), dt, dev)
+    _dense(x, "x", x.shape, dt, dev)
     if qw.dtype is not torch.int8 and qw.dtype is not torch.float8_e4m3fn:
         raise TypeError(f"unsupported dtype {qw.dtype}")
     kq = contraction_len(k, block) if block > 0 else k  # the library refuses a bad block
@@ -905,7 +929,8 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
     yt = y.dtype if y is not None else (y_dtype or dt)
     if y is None:
         y = torch.empty((m, n), dtype=yt, device=dev)
-    _dense(y, "y", (m, n), yt, dev)
+    else:
+        _dense(y, "y", (m, n), yt, dev)
     ep = _epilogue(bias, activation, residual, z, (m, n), yt, dev)
     if signs_k is not None:
         _vector(signs_k, "signs_k", _sign_words(kq), torch.int32)

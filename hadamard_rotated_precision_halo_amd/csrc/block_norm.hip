@@ -58,6 +58,15 @@ __device__ __forceinline__ uint4 get(const T* row, int at) {
     return load16u(row + at);
   }
 }
+// A row that is read once and not again, past the caches: not where rows start anywhere (ODD),
+// whose boundary lines two rows share (2310 x 2049 fp32 backward: 39.6 us against 43.0 us with
+// these loads; 8192 x 4096 bf16: 93.7 us with, 96.8 us without).
+template <typename T, int VEC, bool ODD>
+__device__ __forceinline__ uint4 get_once(const T* row, int at) {
+  if constexpr (VEC == 1 || ODD) return get<T, VEC>(row, at);
+  else return load16u_nt(row + at);
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void val(uint4 w, float* o) {
   if constexpr (VEC == 1) o[0] = sizeof(T) == 2 ? __uint_as_float(w.x << 16) : __uint_as_float(w.x);
@@ -96,8 +105,10 @@ __global__ __launch_bounds__(64 * (NW > 4 ? NW : 4)) void norm_fwd_kernel(NormFw
   const int wave = threadIdx.x >> 6, team = wave / NW;
   const int tl = threadIdx.x - team * NW * 64;  // thread within the team
   const int64_t tok = (int64_t)blockIdx.x * TEAMS + team;
-  if (tok >= a.tokens) return;  // only where a wave is a team: no barrier follows
-  const int64_t t = tok;
+  // a workgroup of several teams may end past the last token; a team of one wave meets no
+  // barrier and leaves, one of more waves repeats the last token (its stores write the same)
+  if (NW == 1 && tok >= a.tokens) return;
+  const int64_t t = min(tok, a.tokens - 1);
   const int d = a.dim;
   const T* r = reinterpret_cast<const T*>(a.r) + t * a.ldr;
   const T* y = reinterpret_cast<const T*>(a.y) + t * a.ldy;
@@ -202,24 +213,24 @@ hipError_t run_fwd(const NormFwdArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Waves per token: the fewest that hold a row in at most 8 chunks per lane; 4 or 16 when the
-// tokens alone would leave most of the device idle (fewer than one 4-wave workgroup per compute
-// unit): a row then arrives in one or two loads per lane and its latency is the call's.
+// Waves per token: so many that a lane holds at most two chunks of r and of y, since few registers
+// leave many rows in flight (8192 x 4096 bf16, 268 MB: 48.5 us with 4 waves of 2 chunks, 55 us
+// with 2 of 4, 72 us with 1 of 8); and up to one chunk where the tokens alone would not fill the
+// device (8 x 4096: latency counts).
 template <typename T, int VEC, bool ODD>
 hipError_t pick_fwd(const NormFwdArgs& a, hipStream_t st) {
   const int64_t chunks = (a.dim + VEC - 1) / VEC;
-  const bool few = a.tokens <= 1024;
   const int64_t per = (chunks + 63) / 64;  // chunks per lane of one wave
   if (per <= 1) return run_fwd<T, VEC, ODD, 1, 1>(a, st);
-  if (few) {
+  if (a.tokens <= 1024) {
     if (per <= 4) return run_fwd<T, VEC, ODD, 4, 1>(a, st);
     if (per <= 16) return run_fwd<T, VEC, ODD, 16, 1>(a, st);
   }
   if (per <= 2) return run_fwd<T, VEC, ODD, 1, 2>(a, st);
-  if (per <= 4) return run_fwd<T, VEC, ODD, 1, 4>(a, st);
-  if (per <= 8) return run_fwd<T, VEC, ODD, 1, 8>(a, st);
-  if (per <= 16) return run_fwd<T, VEC, ODD, 4, 4>(a, st);
-  if (per <= 32) return run_fwd<T, VEC, ODD, 4, 8>(a, st);
+  if (per <= 4) return run_fwd<T, VEC, ODD, 2, 2>(a, st);
+  if (per <= 8) return run_fwd<T, VEC, ODD, 4, 2>(a, st);
+  if (per <= 16) return run_fwd<T, VEC, ODD, 8, 2>(a, st);
+  if (per <= 32) return run_fwd<T, VEC, ODD, 16, 2>(a, st);
   if (per <= 64) return run_fwd<T, VEC, ODD, 16, 4>(a, st);
   return run_fwd<T, VEC, ODD, 16, 8>(a, st);
 }
@@ -247,8 +258,9 @@ void bwd_shape(int64_t chunks, int* nw, int* ch) {
 
 NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
   NormPlan p{};
-  // one workgroup per compute unit: its teams keep enough rows in flight, and the partial sums
-  // (one row per workgroup) stay few
+  // one workgroup per compute unit: its teams keep enough rows in flight (each prefetches its
+  // next row), and the partial sums, one row per workgroup, stay few (8192 x 4096 bf16: 96.8 us
+  // with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9 us)
   int64_t rows = (tokens + 255) / 256;
   if (rows < teams) rows = teams;
   if (group_len * teams <= rows) {
@@ -317,39 +329,55 @@ __global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a,
       for (int j = 0; j < CH; ++j) wgate[j] = get<T, VEC>(gate + group * a.ldg, pl[j].at);
     }
   }
-  for (int64_t it = 0; it < iters; ++it) {
-    int64_t off;  // row within the workgroup's range
-    if (step > 0) {
-      off = it * step + team;
-    } else {  // whole groups: team q takes groups q, q + TEAMS, ...
-      const int64_t gi = it / a.group_len * TEAMS + team;
-      off = gi * a.group_len + it % a.group_len;
-      if (gate && it % a.group_len == 0 && off < nrows) {
-#pragma unroll
-        for (int j = 0; j < CH; ++j) wgate[j] = get<T, VEC>(gate + (group + gi) * a.ldg, pl[j].at);
-      }
-    }
-    const bool live = off < nrows;
-    const int64_t t = row0 + (live ? off : 0);
-    uint4 gr[CH], hr[CH], rr[CH], yr[CH];
+  // row of iteration `it` within the workgroup's range
+  auto row_of = [&](int64_t it) -> int64_t {
+    if (step > 0) return it * step + team;
+    // whole groups: team q takes groups q, q + TEAMS, ...
+    return (it / a.group_len * TEAMS + team) * a.group_len + it % a.group_len;
+  };
+  // the next row's loads are in flight while this row is reduced and stored
+  uint4 ngr[CH], nhr[CH], nrr[CH], nyr[CH];
+  auto fetch = [&](int64_t it) __attribute__((always_inline)) {
+    const int64_t off = it < iters ? row_of(it) : 0;
+    const int64_t t = row0 + (off < nrows ? off : 0);
     if (a.dr_out) {
       const T* p = reinterpret_cast<const T*>(a.dr_out) + t * a.lddro;
 #pragma unroll
-      for (int j = 0; j < CH; ++j) gr[j] = get<T, VEC>(p, pl[j].at);
+      for (int j = 0; j < CH; ++j) ngr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
     }
     if (pre) {
       const T* p = reinterpret_cast<const T*>(a.dh) + t * a.lddh;
       const T* q = reinterpret_cast<const T*>(a.r_out) + t * a.ldro;
 #pragma unroll
-      for (int j = 0; j < CH; ++j) hr[j] = get<T, VEC>(p, pl[j].at);
+      for (int j = 0; j < CH; ++j) nhr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
 #pragma unroll
-      for (int j = 0; j < CH; ++j) rr[j] = get<T, VEC>(q, pl[j].at);
+      for (int j = 0; j < CH; ++j) nrr[j] = get_once<T, VEC, ODD>(q, pl[j].at);
     }
     if (a.y) {
       const T* p = reinterpret_cast<const T*>(a.y) + t * a.ldy;
 #pragma unroll
-      for (int j = 0; j < CH; ++j) yr[j] = get<T, VEC>(p, pl[j].at);
+      for (int j = 0; j < CH; ++j) nyr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
     }
+  };
+  fetch(0);
+  for (int64_t it = 0; it < iters; ++it) {
+    const int64_t off = row_of(it);
+    if (step == 0 && gate && it % a.group_len == 0 && off < nrows) {
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+        wgate[j] = get<T, VEC>(gate + (group + off / a.group_len) * a.ldg, pl[j].at);
+    }
+    const bool live = off < nrows;
+    const int64_t t = row0 + (live ? off : 0);
+    uint4 gr[CH], hr[CH], rr[CH], yr[CH];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      gr[j] = ngr[j];
+      hr[j] = nhr[j];
+      rr[j] = nrr[j];
+      yr[j] = nyr[j];
+    }
+    fetch(it + 1);
     const float b = pre ? a.rstd_pre[t] : 0.f;
     const float ar = post ? a.rstd_post[t] : 1.f;
     // the three sums: m1 = sum u rhat, A = sum c yhat (dr' + b u), B = sum c yhat b rhat
@@ -504,11 +532,11 @@ __global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a,
 
 // Second launch of the backward: the partial rows of each sum, added in a fixed order.  Sum
 // rows: 0 dpost and 1 dpre over all workgroups, then the gate groups over their chunks.  A
-// workgroup takes 64 columns of one sum row; its 4 waves take the partial rows in turn and are
+// workgroup takes 64 columns of one sum row; its 16 waves take the partial rows in turn and are
 // added in wave order.
 template <typename T>
-__global__ __launch_bounds__(256) void norm_sum_kernel(NormBwdArgs a, NormPlan pn) {
-  __shared__ float s[4][64];
+__global__ __launch_bounds__(1024) void norm_sum_kernel(NormBwdArgs a, NormPlan pn) {
+  __shared__ float s[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t col = (int64_t)blockIdx.x * 64 + lane;
   int64_t which = blockIdx.y;
@@ -529,13 +557,17 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(NormBwdArgs a, NormPlan p
   }
   float v = 0.f;
   if (col < a.dim) {
-#pragma unroll 8
-    for (int64_t i = w; i < n; i += 4) v += p[i * a.dim + col];
+#pragma unroll 16
+    for (int64_t i = w; i < n; i += 16) v += p[i * a.dim + col];
   }
   s[w][lane] = v;
   __syncthreads();
-  if (w == 0 && col < a.dim)
-    elem_store<T>(o + col, (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]));
+  if (w == 0 && col < a.dim) {
+    v = s[0][lane];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) v += s[i][lane];
+    elem_store<T>(o + col, v);
+  }
 }
 
 struct BwdLayout {
@@ -591,7 +623,7 @@ hipError_t bwd_type(NormBwdArgs a, const BwdLayout& l, hipStream_t st) {
                        (a.part_gate ? a.tokens / a.group_len : 0);
   if (sums == 0) return hipSuccess;
   hipLaunchKernelGGL((norm_sum_kernel<T>), dim3((unsigned)((a.dim + 63) / 64), (unsigned)sums),
-                     dim3(256), 0, st, a, l.plan);
+                     dim3(1024), 0, st, a, l.plan);
   return hipGetLastError();
 }
 

@@ -8,14 +8,21 @@
 // A token without a kept entry, or whose logits are all -inf, has loss 0 and gradient 0; so has,
 // for its gradient, a token with dloss 0.  A kept entry with p_k = 0 adds nothing.
 //
-// Bound by memory: the logits are read once and the gradient written once.  A workgroup holds a
-// token's row in registers in its stored form (CH 16-byte chunks per lane) between the softmax
-// statistics and the gradient; rows longer than a workgroup holds are read again, which their
-// size makes a cache read for all but the first bytes.  Statistics, exponents and sums are fp32;
-// every thread keeps the sum of its own chunks and the threads are added in a fixed order.
-// The gradient is written for the whole row as dloss tau q; then the K entries, computed apart
-// from their own logits, are written over it (duplicated indices sum their p first, so every
-// writer of a position writes the same value).
+// Bound by memory: the logits are read once and the gradient written once, past the caches.
+//   Held      loss and gradient of a row that fits a workgroup's registers in its stored form (CH
+//             16-byte chunks per lane): between the softmax statistics and the gradient it is not
+//             read again.
+//   Streamed  the loss alone (a running maximum and sum per lane, few registers, many rows in
+//             flight), and loss and gradient of longer rows, which read them twice.
+//   Parts     the gradient alone under a given lse: no statistics, so a row is split over
+//             workgroups.
+// Every lane keeps a running (maximum, sum) over groups of 4 chunks of its part of the row, and the
+// first 256 threads one of the teacher's entries; waves combine theirs in a fixed order after one
+// barrier.  The order depends on the vocabulary alone (its thread count), so the three calls give
+// the same bits and a token's values do not depend on the others in its batch.  Statistics,
+// exponents and sums are fp32.  The gradient is written for the whole row as dloss tau q; after a second barrier the
+// entries, computed apart from their own logits, are written over it (duplicated indices sum their
+// p first, so every writer of a position writes the same value).
 #include "halo_kernels.h"
 #include "rowops.h"
 
@@ -48,137 +55,181 @@ struct Exponent {
   }
 };
 
-// Sum and maximum over a workgroup of NW waves; s: NW floats, not in use by an earlier call.
-template <int NW>
-__device__ __forceinline__ float wg_sum(float v, float* s) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < NW; ++i) v += s[i];
-  return v;
+__device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.f : m; }
+
+// A (maximum, sum of exp(. - maximum)) pair over the lanes of a wave.  A part that is -inf
+// everywhere has maximum -inf and sum 0; NaN stays in the sum.
+__device__ __forceinline__ void wave_pair(float& m, float& s) {
+  const float top = wave_max(m);
+  s = wave_sum(s * exp2_fast((m - finite_ref(top)) * kLog2e));
+  m = top;
 }
+// The same over the pairs of NW waves.
 template <int NW>
-__device__ __forceinline__ float wg_max(float v, float* s) {
-  v = wave_max(v);
-  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = s[0];
+__device__ __forceinline__ void pair_of(const float (*p)[2], float& m, float& s) {
+  m = p[0][0];
 #pragma unroll
-  for (int i = 1; i < NW; ++i) v = fmaxf(v, s[i]);
-  return v;
+  for (int i = 1; i < NW; ++i) m = fmaxf(m, p[i][0]);
+  const float ref = finite_ref(m);
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NW; ++i) s += p[i][1] * exp2_fast((p[i][0] - ref) * kLog2e);
 }
 
-// HELD: the row is in registers (vocab <= NT CH VEC); else it is read twice.
-template <typename T, int NT, int CH, bool HELD>
-__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
+// Keeps a row's chunks in their stored form from here on: the compiler would otherwise keep the
+// fp32 values of an earlier pass over them, twice the registers.
+template <int CH>
+__device__ __forceinline__ void keep_raw(uint4 (&raw)[CH]) {
+#pragma unroll
+  for (int j = 0; j < CH; ++j)
+    asm volatile("" : "+v"(raw[j].x), "+v"(raw[j].y), "+v"(raw[j].z), "+v"(raw[j].w));
+}
+
+enum Mode { kHeld, kStreamed, kParts };
+
+// One token's row (kParts: the part blockIdx.y of it, NT CH chunks).
+template <typename T, int NT, int CH, int MODE>
+__global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
-  __shared__ float s_max[NW], s_sum[NW], s_tmax[NW], s_tsum[NW], s_loss[NW];
-  extern __shared__ float s_top[];  // p[K], logit[K] (fp32), then index[K]
-  const int tid = threadIdx.x;
+  __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
+  extern __shared__ float s_top[];  // t / tau, then p [K]; logit [K]; index [K]
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t tok = blockIdx.x;
-  const int V = a.vocab, K = a.top;
+  const int K = a.top;
+  const int first = MODE == kParts ? (int)blockIdx.y * (NT * CH * VEC) : 0;
+  const int V = MODE == kParts ? min(a.vocab - first, NT * CH * VEC) : a.vocab;  // this part's
   const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ldl;
   T* out = reinterpret_cast<T*>(a.dlogits) + tok * a.ldd;
+  const T* in = row + first;
   float* s_p = s_top;
   float* s_z = s_top + K;
   int* s_i = reinterpret_cast<int*>(s_top + 2 * K);
   const int whole = V / VEC;  // full chunks; the V % VEC elements after them go one per thread
   const int rest0 = whole * VEC;
-  const float dl = a.dloss ? a.dloss[tok] : 0.f;
+  const bool has_rest = rest0 + tid < V;
   const bool grad = a.dlogits != nullptr;
+  const float dl = a.dloss ? a.dloss[tok] : 0.f;
 
-  if (a.lse_in && dl == 0.f) {  // gradient alone, of a token that takes no part
+  if (MODE == kParts && dl == 0.f) {  // a token that takes no part
     const float z[VEC] = {};
-    for (int c = tid; c < whole; c += NT) store16u(out + c * VEC, pack16<T>(z));
-    if (rest0 + tid < V) elem_store<T>(out + rest0 + tid, 0.f);
+    for (int c = tid; c < whole; c += NT) store16u_nt(out + first + c * VEC, pack16<T>(z));
+    if (has_rest) elem_store<T>(out + first + rest0 + tid, 0.f);
     return;
   }
 
-  uint4 raw[HELD ? CH : 1];
-  float rest = -__builtin_inff();
-  if constexpr (HELD) {
+  // the teacher's first entries are asked for before the row, so that the loads of their logits
+  // need not wait for it
+  constexpr int TT = 256;  // threads that reduce the teacher's entries
+  const int32_t* idx = a.idx + tok * a.ldi;
+  auto teacher = [&](int k) {
+    return a.t_bf16 ? elem_f32(reinterpret_cast<const uint16_t*>(a.tlogits) + tok * a.ldt + k)
+                    : reinterpret_cast<const float*>(a.tlogits)[tok * a.ldt + k];
+  };
+  const bool mine = tid < TT && tid < K;
+  const int i0 = mine ? idx[tid] : -1;
+  const float t0 = mine ? teacher(tid) : 0.f;
+
+  uint4 raw[MODE == kStreamed ? 1 : CH];
+  if constexpr (MODE != kStreamed) {
+    if (whole > 0) {  // chunks past the row read its first one
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = j * NT + tid;
-      raw[j] = load16u(row + (c < whole ? c : 0) * VEC);
+      for (int j = 0; j < CH; ++j) {
+        const int c = j * NT + tid;
+        raw[j] = load16u_nt(in + (c < whole ? c : 0) * VEC);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < CH; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  if (rest0 + tid < V) rest = elem_f32<T>(row + rest0 + tid);
+  const float rest = has_rest ? elem_f32<T>(in + rest0 + tid) : -__builtin_inff();
 
-  // the teacher's entries
-  float tm = -__builtin_inff();
-  for (int k = tid; k < K; k += NT) {
-    const int i = a.idx[tok * a.ldi + k];
-    const bool in = i >= 0 && i < V;
-    float t = a.t_bf16 ? elem_f32(reinterpret_cast<const uint16_t*>(a.tlogits) + tok * a.ldt + k)
-                       : reinterpret_cast<const float*>(a.tlogits)[tok * a.ldt + k];
-    t = in ? t * a.inv_tau : -__builtin_inff();
-    s_i[k] = in ? i : -1;
-    s_p[k] = t;
-    s_z[k] = in ? elem_f32<T>(row + i) : 0.f;
-    tm = fmaxf(tm, t != t ? __builtin_inff() : t);  // a NaN entry keeps the token in, as NaN
+  // the teacher's entries: kept in LDS, and their (maximum, sum)
+  if (tid < TT) {
+    float tm = -__builtin_inff();
+    for (int k = tid; k < K; k += TT) {
+      const int i = k == tid ? i0 : idx[k];
+      const bool there = i >= 0 && i < a.vocab;
+      const float t = there ? (k == tid ? t0 : teacher(k)) * a.inv_tau : -__builtin_inff();
+      s_i[k] = there ? i : -1;
+      s_z[k] = there ? elem_f32<T>(row + i) : 0.f;
+      s_p[k] = t;
+      tm = fmaxf(tm, t != t ? __builtin_inff() : t);  // a NaN entry keeps the token in, as NaN
+    }
+    float ts = 0.f;
+    const float ref = finite_ref(tm);
+    for (int k = tid; k < K; k += TT) ts += exp2_fast((s_p[k] - ref) * kLog2e);
+    wave_pair(tm, ts);
+    if (lane == 0) {
+      s_tea[wave][0] = tm;
+      s_tea[wave][1] = ts;
+    }
   }
-  tm = wg_max<NW>(tm, s_tmax);
-  const bool some = tm != -__builtin_inff();
-  float ts = 0.f;
-  for (int k = tid; k < K; k += NT) ts += some ? exp2_fast((s_p[k] - tm) * kLog2e) : 0.f;
-  ts = wg_sum<NW>(ts, s_tsum);
 
-  // statistics of the row
-  float lse;
-  if (a.lse_in) {
+  // the row's (maximum, sum), of logits / tau
+  if constexpr (MODE != kParts) {
+    float m = rest * a.inv_tau, sum = 0.f;
+    if (has_rest) sum = Exponent<T>(a.inv_tau, finite_ref(m))(rest);
+    // chunks c0, c0 + NT, .. (4 of them): their maximum first, then the running sum moves to it
+    auto group = [&](const uint4* w, int c0) __attribute__((always_inline)) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[VEC], t = -__builtin_inff();
+        unpack16<T>(w[j], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) t = fmaxf(t, v[e]);
+        if (c0 + j * NT < whole) top = fmaxf(top, t);
+      }
+      top = fmaxf(m, top * a.inv_tau);
+      const float ref = finite_ref(top);
+      const Exponent<T> ex(a.inv_tau, ref);
+      sum *= exp2_fast((m - ref) * kLog2e);
+      m = top;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[VEC], part = 0.f;
+        unpack16<T>(w[j], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) part += ex(v[e]);
+        sum += c0 + j * NT < whole ? part : 0.f;
+      }
+    };
+    if constexpr (MODE == kHeld) {
+#pragma unroll
+      for (int j = 0; j < CH; j += 4) group(&raw[j], j * NT + tid);
+      keep_raw(raw);
+    } else {
+      for (int c0 = tid; c0 < whole; c0 += NT * 4) {
+        uint4 w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + j * NT;
+          w[j] = load16u_nt(in + (c < whole ? c : c0) * VEC);
+        }
+        group(w, c0);
+      }
+    }
+    wave_pair(m, sum);
+    if (lane == 0) {
+      s_row[wave][0] = m;
+      s_row[wave][1] = sum;
+    }
+  }
+  __syncthreads();
+  float tm, ts, lse;
+  pair_of<TT / 64>(s_tea, tm, ts);
+  if (MODE == kParts) {
     lse = a.lse_in[tok];
   } else {
-    float m = rest;
-    if constexpr (HELD) {
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        float v[VEC];
-        unpack16<T>(raw[j], v);
-        if (j * NT + tid < whole) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) m = fmaxf(m, v[e]);
-        }
-      }
-    } else {
-      for (int c = tid; c < whole; c += NT) {
-        float v[VEC];
-        unpack16<T>(load16u(row + c * VEC), v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) m = fmaxf(m, v[e]);
-      }
-    }
-    m = wg_max<NW>(m, s_max) * a.inv_tau;
-    if (m == -__builtin_inff()) m = 0.f;  // all -inf (sum 0), or all NaN (sum NaN)
-    const Exponent<T> ex(a.inv_tau, m);
-    float sum = rest0 + tid < V ? ex(rest) : 0.f;
-    if constexpr (HELD) {
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        float v[VEC];
-        unpack16<T>(raw[j], v);
-        if (j * NT + tid < whole) {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sum += ex(v[e]);
-        }
-      }
-    } else {
-      for (int c = tid; c < whole; c += NT) {
-        float v[VEC];
-        unpack16<T>(load16u(row + c * VEC), v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sum += ex(v[e]);
-      }
-    }
-    sum = wg_sum<NW>(sum, s_sum);
-    lse = sum == 0.f ? -__builtin_inff() : m + logf(sum);
+    float m, sum;
+    pair_of<NW>(s_row, m, sum);
+    lse = sum == 0.f ? -__builtin_inff() : finite_ref(m) + logf(sum);
     if (a.lse && tid == 0) a.lse[tok] = lse;
   }
-  const bool empty = !some || lse == -__builtin_inff();
+  const bool empty = tm == -__builtin_inff() || lse == -__builtin_inff();
 
-  // the loss, and each entry's p
+  // each entry's p, and the loss
   float l = 0.f;
   const float logts = logf(ts);
   for (int k = tid; k < K; k += NT) {
@@ -187,61 +238,72 @@ __global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
     s_p[k] = p;
     if (p != 0.f) l += p * (lp - (__builtin_fmaf(s_z[k], a.inv_tau, -lse)));
   }
-  if (a.loss) {
-    l = wg_sum<NW>(l, s_loss);
-    if (tid == 0) a.loss[tok] = l * a.tau * a.tau;
+  if (MODE != kParts) {
+    l = wave_sum(l);
+    if (lane == 0) s_loss[wave] = l;
   }
-  if (!grad) return;
   const float by = empty ? 0.f : dl * a.tau;
   const bool zero = by == 0.f;
   const Exponent<T> ex(a.inv_tau, zero ? 0.f : lse);
-  if constexpr (HELD) {
+  if (grad) {
+    T* o = out + first;
+    if constexpr (MODE == kStreamed) {
+      for (int c = tid; c < whole; c += NT) {
+        float v[VEC];
+        unpack16<T>(load16u(in + c * VEC), v);
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = j * NT + tid;
-      float v[VEC];
-      unpack16<T>(raw[j], v);
+        for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
+        store16u_nt(o + c * VEC, pack16<T>(v));
+      }
+    } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
-      if (c < whole) store16u(out + c * VEC, pack16<T>(v));
+      for (int j = 0; j < CH; ++j) {
+        const int c = j * NT + tid;
+        float v[VEC];
+        unpack16<T>(raw[j], v);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
+        if (c < whole) store16u_nt(o + c * VEC, pack16<T>(v));
+      }
     }
-  } else {
-    for (int c = tid; c < whole; c += NT) {
-      float v[VEC];
-      unpack16<T>(load16u(row + c * VEC), v);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
-      store16u(out + c * VEC, pack16<T>(v));
-    }
+    if (has_rest) elem_store<T>(o + rest0 + tid, zero ? 0.f : by * ex(rest));
   }
-  if (rest0 + tid < V) elem_store<T>(out + rest0 + tid, zero ? 0.f : by * ex(rest));
-  if (zero) return;
-  // the entries, over the row (the barrier orders the two stores of a position)
-  __syncthreads();
+  __syncthreads();  // the losses and the p are in LDS; the row's stores come before the entries'
+  if (MODE != kParts && tid == 0) {
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) l += s_loss[i];
+    a.loss[tok] = l * a.tau * a.tau;
+  }
+  if (!grad || zero) return;
   for (int k = tid; k < K; k += NT) {
     const int i = s_i[k];
-    if (i < 0) continue;
+    if (i < first || i >= first + V) continue;
     float p = 0.f;
     for (int o = 0; o < K; ++o) p += s_i[o] == i ? s_p[o] : 0.f;
     elem_store<T>(out + i, by * (ex(s_z[k]) - p));
   }
 }
 
-template <typename T, int NT, int CH, bool HELD>
+template <typename T, int NT, int CH, int MODE>
 hipError_t run(const DistillArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((distill_kernel<T, NT, CH, HELD>), dim3((unsigned)a.tokens), dim3(NT),
-                     (size_t)a.top * 12, st, a);
+  constexpr int64_t part = (int64_t)NT * CH * RowType<T>::VEC;
+  const dim3 grid((unsigned)a.tokens, MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
+  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT), (size_t)a.top * 12, st, a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t pick(const DistillArgs& a, hipStream_t st) {
   const int64_t chunks = a.vocab / RowType<T>::VEC;
-  if (chunks <= 256 * 4) return run<T, 256, 4, true>(a, st);
-  if (chunks <= 512 * 8) return run<T, 512, 8, true>(a, st);
-  if (chunks <= 1024 * 8) return run<T, 1024, 8, true>(a, st);
-  if (chunks <= 1024 * 16) return run<T, 1024, 16, true>(a, st);
-  return run<T, 1024, 1, false>(a, st);
+  if (a.lse_in) return run<T, 256, 8, kParts>(a, st);
+  if (chunks <= 256 * 4)
+    return a.dlogits ? run<T, 256, 4, kHeld>(a, st) : run<T, 256, 4, kStreamed>(a, st);
+  if (!a.dlogits) return run<T, 1024, 4, kStreamed>(a, st);
+  if (chunks <= 1024 * 4) return run<T, 1024, 4, kHeld>(a, st);
+  if (chunks <= 1024 * 8) return run<T, 1024, 8, kHeld>(a, st);
+  if (chunks <= 1024 * 16) return run<T, 1024, 16, kHeld>(a, st);
+  return run<T, 1024, 4, kStreamed>(a, st);
 }
 
 }  // namespace

@@ -31,6 +31,16 @@ __device__ __forceinline__ void store16u(void* p, uint4 v) {
   *reinterpret_cast<v4i_any*>(p) = w;
 }
 
+// The same past the caches, for what is read or written once.
+__device__ __forceinline__ uint4 load16u_nt(const void* p) {
+  const v4i_any w = __builtin_nontemporal_load(reinterpret_cast<const v4i_any*>(p));
+  return make_uint4((uint32_t)w.x, (uint32_t)w.y, (uint32_t)w.z, (uint32_t)w.w);
+}
+__device__ __forceinline__ void store16u_nt(void* p, uint4 v) {
+  const v4i_any w = {(int)v.x, (int)v.y, (int)v.z, (int)v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<v4i_any*>(p));
+}
+
 typedef __bf16 bf16v2 __attribute__((ext_vector_type(2)));
 typedef float f32v2 __attribute__((ext_vector_type(2)));
 
