@@ -936,11 +936,17 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
         _vector(signs_k, "signs_k", _sign_words(kq), torch.int32)
         _same_gpu(x, signs_k=signs_k)
     L = lib()
-    ws = _scratch(workspace, L.halo_linear_act_q_workspace_bytes(m, k, block)
-                  if workspace is None else 0, x)
-    st = L.halo_linear_act_q(_p(x), _TORCH_CODE[dt], _p(qw), _TORCH_CODE[qw.dtype], _p(sw), m, n, k,
-                             block, _p(y), _code(yt), ctypes.byref(ep), _p(signs_k), _p(ws),
-                             ws.numel(), _current_stream(dev, stream))
+    if workspace is None:
+        need = L.halo_linear_act_q_workspace_bytes(m, k, block)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _scratch(workspace, 0, x)
+    st = L.halo_linear_act_q(x.data_ptr(), _TORCH_CODE[dt], qw.data_ptr(), _TORCH_CODE[qw.dtype],
+                             sw.data_ptr(), m, n, k, block, y.data_ptr(), _code(yt),
+                             ctypes.byref(ep), _p(signs_k), _p(workspace),
+                             0 if workspace is None else workspace.numel(),
+                             _current_stream(dev, stream))
     _check(st, "halo_linear_act_q")
     return y if z is None else (y, z)
 

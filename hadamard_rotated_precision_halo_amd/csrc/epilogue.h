@@ -20,12 +20,34 @@ __device__ __forceinline__ float gelu_arg(float z) {
   return z * __builtin_fmaf(t, 0.07135481627159f, 1.5957691216057308f);
 }
 
+// erfc(x) / 2 for x >= 0 and exp(-x^2), by formula 7.1.26 of Abramowitz and Stegun, "Handbook of
+// Mathematical Functions" (absolute error of erf below 1.5e-7, 2.5 units of 2^-24): one exponential,
+// one reciprocal and five multiply-adds, a quarter of the library erf's time.
+__device__ __forceinline__ float half_erfc(float x, float* gauss) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
+  float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+  p = __builtin_fmaf(p, t, 1.421413741f);
+  p = __builtin_fmaf(p, t, -0.284496736f);
+  p = __builtin_fmaf(p, t, 0.254829592f);
+  *gauss = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+  return 0.5f * p * t * *gauss;
+}
+
+// The normal distribution at z and exp(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float* gauss) {
+  const float h = half_erfc(fabsf(z) * 0.7071067811865476f, gauss);
+  return z < 0.f ? h : 1.f - h;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (ACT == kActSilu) return z * sigmoid_fast(z);
   if constexpr (ACT == kActGeluTanh) return z * sigmoid_fast(gelu_arg(z));
-  if constexpr (ACT == kActGeluErf) return 0.5f * z * (1.f + erff(z * 0.7071067811865476f));
+  if constexpr (ACT == kActGeluErf) {
+    float gauss;
+    return z * normal_cdf(z, &gauss);
+  }
   return z;
 }
 
@@ -44,9 +66,9 @@ __device__ __forceinline__ float slope_of(float z) {
     return __builtin_fmaf(z * (p * (1.f - p)), du, p);
   }
   if constexpr (ACT == kActGeluErf) {
-    const float cdf = 0.5f * (1.f + erff(z * 0.7071067811865476f));
-    const float pdf = 0.3989422804014327f * __builtin_amdgcn_exp2f(z * z * -0.7213475204444817f);
-    return __builtin_fmaf(z, pdf, cdf);
+    float gauss;
+    const float cdf = normal_cdf(z, &gauss);
+    return __builtin_fmaf(z * 0.3989422804014327f, gauss, cdf);
   }
   return 1.f;
 }

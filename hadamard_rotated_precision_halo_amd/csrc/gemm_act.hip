@@ -6,9 +6,11 @@ namespace halo {
 
 namespace {
 
-// 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit.
+// 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit; the 64 x 64 tile also
+// with a ring of 8 slabs, for one workgroup per unit.
 using MidTile = TileCfg<128, 2, 2, 2>;
 using SmallTile = TileCfg<64, 2, 2, 4>;
+using DeepTile = TileCfg<64, 2, 2, 8>;
 
 template <int KIND, int OUT, bool MASK, typename CFG>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
@@ -33,7 +35,8 @@ hipError_t pick(const GemmArgs& g, hipStream_t st) {
   auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((g.n + bt - 1) / bt); };
   if (tiles(256) >= 224) return run<KIND, OUT, MASK, BigTile>(g, st);
   if (tiles(128) >= 224) return run<KIND, OUT, MASK, MidTile>(g, st);
-  return run<KIND, OUT, MASK, SmallTile>(g, st);
+  if (tiles(64) > 256) return run<KIND, OUT, MASK, SmallTile>(g, st);
+  return run<KIND, OUT, MASK, DeepTile>(g, st);
 }
 
 template <int KIND, int OUT>

@@ -307,16 +307,22 @@ halo_status check_epilogue(const halo_epilogue* ep) {
   return HALO_OK;
 }
 
-// The product with its epilogue.
-halo_status act_product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
-                        const float* sb, int64_t m, int64_t n, int64_t k, halo_dtype qt, void* y,
-                        halo_dtype yt, const halo_epilogue* ep, hipStream_t st) {
+GemmArgs act_args(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
+                  const float* sb, int64_t m, int64_t n, int64_t k, void* y,
+                  const halo_epilogue* ep) {
   GemmArgs g{a, lda, b, ldb, sa, sb, y, n, m, n, k};
   g.bias = ep->bias;
   g.res = ep->residual;
   g.z = ep->z;
   g.act = ep->activation;
-  return from_hip(launch_gemm_act(g, qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
+  return g;
+}
+
+// The product with its epilogue.
+halo_status act_product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
+                        const float* sb, int64_t m, int64_t n, int64_t k, halo_dtype qt, void* y,
+                        halo_dtype yt, const halo_epilogue* ep, hipStream_t st) {
+  return from_hip(launch_gemm_act(act_args(a, lda, sa, b, ldb, sb, m, n, k, y, ep), qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
 }
 
 // Validation of a layer forward.
@@ -965,6 +971,7 @@ halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type
 
 size_t halo_linear_act_q_workspace_bytes(int64_t m, int64_t k, int32_t block) {
   if (!layer_dims_ok(m, 0, k) || !valid_block(block)) return 0;
+  if (skinny_fused_ok(m, contraction_len(k, block), block)) return 0;
   return round256((size_t)m * contraction_len(k, block)) + round256((size_t)m * 4);
 }
 
@@ -981,17 +988,23 @@ halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw,
   if (n > 0 && !sw) return HALO_ERR_NULL;
   if (!aligned16(sw) || check_signs(signs_k) != HALO_OK) return HALO_ERR_ALIGN;
   if (m == 0 || n == 0) return HALO_OK;
-  if (!ws || ws_bytes < halo_linear_act_q_workspace_bytes(m, k, block)) return HALO_ERR_WORKSPACE;
+  const size_t need = halo_linear_act_q_workspace_bytes(m, k, block);
+  if (need > 0 && (!ws || ws_bytes < need)) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
   const hipStream_t st = (hipStream_t)stream;
   char* base = static_cast<char*>(ws);
-  float* sx = reinterpret_cast<float*>(base + round256((size_t)m * kq));
+  float* sx = reinterpret_cast<float*>(need > 0 ? base + round256((size_t)m * kq) : nullptr);
   PassOpts po;
   po.signs = signs_k;
   const FqArgs ax = make_fq(x, m, k, k, HALO_ALONG_ROWS, block, q_type, base, kq, sx, po, kq);
+  const halo_epilogue none{};
+  if (need == 0) {
+    const GemmArgs g = act_args(nullptr, kq, nullptr, qw, kq, sw, m, n, kq, y, ep ? ep : &none);
+    return from_hip(launch_skinny_fused(g, ax, io_type == HALO_BF16 ? 1 : 0, q_type == HALO_I8 ? 0 : 1,
+                                        y_type == HALO_F32 ? 1 : 2, st));
+  }
   s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
   if (s != HALO_OK) return s;
-  const halo_epilogue none{};
   return act_product(base, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep ? ep : &none, st);
 }
 

@@ -117,6 +117,38 @@ __device__ __forceinline__ uint32_t fp8_pair(float a, float b) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false) & 0xffffu;
 }
 
+// Encoders for 8 consecutive values (one chunk) -> 8 bytes of codes.
+template <int QT>
+__device__ __forceinline__ uint2 encode8(const float* y, float m) {
+  uint2 w;
+  if constexpr (QT == 0) {
+    uint32_t t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = __float_as_uint(__builtin_fmaf(y[e], m, 12582912.0f));
+    // v_perm_b32: byte 0 of each of two dwords -> bytes 0 and 1 (selector 0x0c zeroes)
+    const uint32_t p01 = __builtin_amdgcn_perm(t[1], t[0], 0x0c0c0400u);
+    const uint32_t p23 = __builtin_amdgcn_perm(t[3], t[2], 0x0c0c0400u);
+    const uint32_t p45 = __builtin_amdgcn_perm(t[5], t[4], 0x0c0c0400u);
+    const uint32_t p67 = __builtin_amdgcn_perm(t[7], t[6], 0x0c0c0400u);
+    w.x = __builtin_amdgcn_perm(p23, p01, 0x05040100u);
+    w.y = __builtin_amdgcn_perm(p67, p45, 0x05040100u);
+  } else {
+    // v_cvt_pk_{fp8,bf8}_f32 writes one 16-bit half of its destination and keeps the other
+    if constexpr (QT == 1) {
+      w.x = __builtin_amdgcn_cvt_pk_fp8_f32(mulz(y[2], m), mulz(y[3], m),
+                                            __builtin_amdgcn_cvt_pk_fp8_f32(mulz(y[0], m), mulz(y[1], m), 0, false), true);
+      w.y = __builtin_amdgcn_cvt_pk_fp8_f32(mulz(y[6], m), mulz(y[7], m),
+                                            __builtin_amdgcn_cvt_pk_fp8_f32(mulz(y[4], m), mulz(y[5], m), 0, false), true);
+    } else {
+      w.x = __builtin_amdgcn_cvt_pk_bf8_f32(mulz(y[2], m), mulz(y[3], m),
+                                            __builtin_amdgcn_cvt_pk_bf8_f32(mulz(y[0], m), mulz(y[1], m), 0, false), true);
+      w.y = __builtin_amdgcn_cvt_pk_bf8_f32(mulz(y[6], m), mulz(y[7], m),
+                                            __builtin_amdgcn_cvt_pk_bf8_f32(mulz(y[4], m), mulz(y[5], m), 0, false), true);
+    }
+  }
+  return w;
+}
+
 // ---------------------------------------------------------------------------
 // randomised transform and stochastic rounding
 // ---------------------------------------------------------------------------

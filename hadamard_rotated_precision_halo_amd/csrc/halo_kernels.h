@@ -124,6 +124,10 @@ hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st)
 // The same for up to kSkinnyRows rows of a (gemm_skinny.hip).
 constexpr int kSkinnyRows = 64;
 hipError_t launch_gemm_skinny(const GemmArgs& g, int kind, int out, hipStream_t st);
+// The same with the rows pass f (its codes and scales stay inside) of m rows in one launch.
+bool skinny_fused_ok(int64_t m, int64_t kq, int block);
+hipError_t launch_skinny_fused(const GemmArgs& g, const FqArgs& f, int in_bf16, int kind, int out,
+                               hipStream_t st);
 
 // dz = dy act'(z) in fp32 and, when db is not NULL, db = its sums over the m rows (bias type:
 // that of dy).  part: act_grad_parts(m, n) x n floats of scratch (db only).

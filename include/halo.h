@@ -381,7 +381,8 @@ halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type
  * that halo_fwht_quant gives along the rows of W (with the same block, signs and q_type), dense,
  * kq = k rounded up to a multiple of block, which must be a multiple of 32.  Only x is rotated
  * and quantised here.  One to 64 rows of x run a kernel bound by reading qw once.
- *   ws   at least halo_linear_act_q_workspace_bytes(m, k, block) bytes, 16-byte aligned.
+ *   ws   at least halo_linear_act_q_workspace_bytes(m, k, block) bytes, 16-byte aligned (0 bytes
+ *        for the fewest rows, which are quantised inside the product's kernel: ws may be NULL).
  */
 size_t halo_linear_act_q_workspace_bytes(int64_t m, int64_t k, int32_t block);
 halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,

@@ -2,7 +2,7 @@
 
 Forward.  The codes are those of fwht_quant (held to the oracle by its own tests), so the product
 has an exact value in 64 bits.  INT8 sums are exact integers: z carries at most 5 roundings of
-2^-24 of |product| + |bias|; FP8 sums carry the matrix core's documented bound on top.  An
+2^-24 of |product| + |bias| (or of a subnormal unit); FP8 sums carry the matrix core's documented bound on top.  An
 activation passes an error of z on by at most its largest slope (1.13) and adds 2^-24 (16 + 4 |z|)
 of |z| (exponent scaled to base 2, two units in the last place of exp and rcp, erf).  y and z are
 rounded once (2^-8 for bf16).
@@ -22,6 +22,7 @@ BF16, F32, I8, E4M3, E5M2 = (torch.bfloat16, torch.float32, torch.int8, torch.fl
                              torch.float8_e5m2)
 ROUND = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
 U = 2.0 ** -24
+ETA = 2.0 ** -149   # a rounding in the subnormal range, where no relative bound holds
 ACTS = ["none", "relu", "silu", "gelu_tanh", "gelu_erf"]
 
 
@@ -68,7 +69,7 @@ def check_fwd(x, w, block, q, act, bias, res, y, z, yt):
     prod = (a @ b.t()) * s
     bz = bias.double() if bias is not None else torch.zeros(w.shape[0], dtype=torch.float64, device=DEV)
     ref_z = prod + bz
-    err = 5 * U * (prod.abs() + bz.abs())
+    err = 5 * U * (prod.abs() + bz.abs()) + 5 * ETA
     if q != I8:
         n = a.shape[1] / 8 + 2
         err = err + (2.0 ** -10 + n * U / (1 - n * U)) * (a.abs() @ b.abs().t()) * s
@@ -249,3 +250,36 @@ def test_streams_graph_and_empty():
     e = torch.empty((0, k), dtype=BF16, device=DEV)
     assert H.linear_act_fwd(e, w, block, bias=bias).shape == (0, n)
     assert H.linear_act_q(e, qw, sw, block).shape == (0, n)
+
+
+# rows, columns, contraction, block: rows quantised inside the product's kernel (up to 16 rows, 32
+# slices of 512), and the shapes just past it
+INSIDE = [(1, 16, 512, 512), (1, 40, 544, 32), (1, 4096, 4096, 256), (2, 24, 4064, 32),
+          (3, 1000, 1536, 8), (4, 136, 4096, 2), (8, 80, 2048, 128), (16, 264, 992, 16),
+          (1, 56, 16384, 64), (1, 48, 16448, 32), (16, 40, 1056, 32), (2, 32, 1024, 1024),
+          (1, 64, 5504, 1)]
+
+
+@pytest.mark.parametrize("q", [I8, E4M3])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("m,n,k,block", INSIDE)
+def test_serving_form_equals_the_forward(m, n, k, block, dt, q):
+    print(f"m {m} n {n} k {k} block {block} {dt} {q}", flush=True)
+    x, w = rnd((m, k), dt, 1), rnd((n, k), dt, 2, k ** -0.5)
+    x[:, 3] *= 40
+    if m > 1:
+        x[1] = 0                       # zero codes
+    if m > 2 and dt == F32:
+        x[2] *= 1e-40                  # so small that the quantiser's multiplier overflows
+    bias, res = rnd((n,), dt, 3), rnd((m, n), dt, 4)
+    for signs in (None, H.hadamard_signs(kq_of(k, block), 3, DEV)):
+        qw, sw = H.fwht_quant(w, H.ROWS, block, q, signs=signs)
+        y, z = H.linear_act_fwd(x, w, block, q, bias=bias, activation="silu", residual=res,
+                                want_z=True, signs_k=signs)
+        z2 = torch.empty_like(z)
+        y2, _ = H.linear_act_q(x, qw, sw, block, bias=bias, activation="silu", residual=res, z=z2,
+                               signs_k=signs)
+        assert torch.equal(y2, y) and torch.equal(z2, z)
+    if signs is not None:
+        y = H.linear_act_fwd(x, w, block, q, activation="relu")
+        check_fwd(x, w, block, q, "relu", None, None, y, None, dt)
