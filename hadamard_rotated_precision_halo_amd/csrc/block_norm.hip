@@ -25,6 +25,9 @@
 // results do not change between runs).
 #include "halo_kernels.h"
 #include "rowops.h"
+#ifndef BCH
+#define BCH 1
+#endif
 
 namespace halo {
 
@@ -58,9 +61,10 @@ __device__ __forceinline__ uint4 get(const T* row, int at) {
     return load16u(row + at);
   }
 }
-// A row that is read once and not again, past the caches: not where rows start anywhere (ODD),
-// whose boundary lines two rows share (2310 x 2049 fp32 backward: 39.6 us against 43.0 us with
-// these loads; 8192 x 4096 bf16: 93.7 us with, 96.8 us without).
+// A row that is read once and not again, past the caches (8192 x 4096 bf16: forward 48.8 us with,
+// 51.8 us without; backward 91.8 and 98.3 us): not where rows start anywhere (ODD), whose boundary
+// lines two rows share (2310 x 2049 fp32 backward: 43.0 us with, 39.6 us without).  The outputs
+// are stored through the caches: the next layer reads them.
 template <typename T, int VEC, bool ODD>
 __device__ __forceinline__ uint4 get_once(const T* row, int at) {
   if constexpr (VEC == 1 || ODD) return get<T, VEC>(row, at);
@@ -71,6 +75,18 @@ template <typename T, int VEC>
 __device__ __forceinline__ void val(uint4 w, float* o) {
   if constexpr (VEC == 1) o[0] = sizeof(T) == 2 ? __uint_as_float(w.x << 16) : __uint_as_float(w.x);
   else unpack16<T>(w, o);
+}
+// Only the elements of a moved-back chunk that are its own (see place_of).
+template <typename T, int VEC>
+__device__ __forceinline__ void put_own(T* row, int at, int from, const float* v) {
+  if (from == 0) {
+    if constexpr (VEC == 1) elem_store<T>(row + at, v[0]);
+    else store16u(row + at, pack16<T>(v));
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e)
+      if (e >= from) elem_store<T>(row + at + e, v[e]);
+  }
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void put(T* row, int at, const float* v) {
@@ -97,10 +113,14 @@ __device__ __forceinline__ float team_sum(float v, float* s, int wave, int team)
   return v;
 }
 
-// NW waves per token, 4 waves (or NW) per workgroup.
+// NW waves per token; workgroups of at least 3 waves.
+template <int NW>
+struct FwdGeo {
+  static constexpr int TEAMS = NW == 1 ? 4 : NW == 2 ? 2 : 1, WAVES = TEAMS * NW;
+};
 template <typename T, int VEC, bool ODD, int NW, int CH>
-__global__ __launch_bounds__(64 * (NW > 4 ? NW : 4)) void norm_fwd_kernel(NormFwdArgs a) {
-  constexpr int WAVES = NW > 4 ? NW : 4, TEAMS = WAVES / NW;
+__global__ __launch_bounds__(64 * FwdGeo<NW>::WAVES) void norm_fwd_kernel(NormFwdArgs a) {
+  constexpr int WAVES = FwdGeo<NW>::WAVES, TEAMS = FwdGeo<NW>::TEAMS;
   __shared__ float s_post[WAVES], s_pre[WAVES];
   const int wave = threadIdx.x >> 6, team = wave / NW;
   const int tl = threadIdx.x - team * NW * 64;  // thread within the team
@@ -118,10 +138,10 @@ __global__ __launch_bounds__(64 * (NW > 4 ? NW : 4)) void norm_fwd_kernel(NormFw
   for (int j = 0; j < CH; ++j) pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
   if (a.y) {
 #pragma unroll
-    for (int j = 0; j < CH; ++j) yr[j] = get<T, VEC>(y, pl[j].at);
+    for (int j = 0; j < CH; ++j) yr[j] = get_once<T, VEC, ODD>(y, pl[j].at);
   }
 #pragma unroll
-  for (int j = 0; j < CH; ++j) rr[j] = get<T, VEC>(r, pl[j].at);
+  for (int j = 0; j < CH; ++j) rr[j] = get_once<T, VEC, ODD>(r, pl[j].at);
 
   float x[CH][VEC];
   float inv_post = 1.f;
@@ -206,7 +226,7 @@ __global__ __launch_bounds__(64 * (NW > 4 ? NW : 4)) void norm_fwd_kernel(NormFw
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
 hipError_t run_fwd(const NormFwdArgs& a, hipStream_t st) {
-  constexpr int WAVES = NW > 4 ? NW : 4, TEAMS = WAVES / NW;
+  constexpr int WAVES = FwdGeo<NW>::WAVES, TEAMS = FwdGeo<NW>::TEAMS;
   const int64_t grid = (a.tokens + TEAMS - 1) / TEAMS;
   hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, ODD, NW, CH>), dim3((unsigned)grid),
                      dim3(64 * WAVES), 0, st, a);
@@ -226,10 +246,16 @@ hipError_t pick_fwd(const NormFwdArgs& a, hipStream_t st) {
     if (per <= 4) return run_fwd<T, VEC, ODD, 4, 1>(a, st);
     if (per <= 16) return run_fwd<T, VEC, ODD, 16, 1>(a, st);
   }
-  if (per <= 2) return run_fwd<T, VEC, ODD, 1, 2>(a, st);
-  if (per <= 4) return run_fwd<T, VEC, ODD, 2, 2>(a, st);
-  if (per <= 8) return run_fwd<T, VEC, ODD, 4, 2>(a, st);
-  if (per <= 16) return run_fwd<T, VEC, ODD, 8, 2>(a, st);
+  switch ((per + 1) / 2) {
+    case 1: return run_fwd<T, VEC, ODD, 1, 2>(a, st);
+    case 2: return run_fwd<T, VEC, ODD, 2, 2>(a, st);
+    case 3: return run_fwd<T, VEC, ODD, 3, 2>(a, st);
+    case 4: return run_fwd<T, VEC, ODD, 4, 2>(a, st);
+    case 5: return run_fwd<T, VEC, ODD, 5, 2>(a, st);
+    case 6: return run_fwd<T, VEC, ODD, 6, 2>(a, st);
+    case 7: return run_fwd<T, VEC, ODD, 7, 2>(a, st);
+    case 8: return run_fwd<T, VEC, ODD, 8, 2>(a, st);
+  }
   if (per <= 32) return run_fwd<T, VEC, ODD, 16, 2>(a, st);
   if (per <= 64) return run_fwd<T, VEC, ODD, 16, 4>(a, st);
   return run_fwd<T, VEC, ODD, 16, 8>(a, st);
@@ -247,13 +273,24 @@ struct NormPlan {
   int64_t wgs, rows_per_wg, chunks_per_group, whole_groups;
 };
 
-constexpr int kBwdWaves = 8;
-
-// Waves per token and chunks per lane of the backward for a row of `chunks` chunks.
+// Waves per token and chunks per lane of the backward for a row of `chunks` chunks: one chunk per
+// lane (a lane also holds three fp32 sums for each of its columns), as many waves as the row has
+// 64 chunks (rounded up to one of the instantiated counts), and 16 waves of two or four for the
+// widest rows.
 void bwd_shape(int64_t chunks, int* nw, int* ch) {
   const int64_t per = (chunks + 63) / 64;
-  *nw = per <= 1 ? 1 : per <= 2 ? 1 : per <= 4 ? 2 : per <= 8 ? 4 : 8;
-  *ch = per <= 1 ? 1 : per <= 16 ? 2 : per <= 32 ? 4 : 8;
+#if BCH == 2
+  *ch = per <= 1 ? 1 : per <= 32 ? 2 : 4;
+  *nw = per <= 16 ? (int)((per + 1) / 2) : 16;
+#else
+  *ch = per <= 16 ? 1 : per <= 32 ? 2 : 4;
+  *nw = per > 8 ? (int)(per > 14 ? 16 : (per + 1) / 2 * 2) : (int)per;
+#endif
+}
+// Teams of a workgroup: at most 16 waves together.
+constexpr int bwd_teams(int nw, int ch, int vec) {
+  const int waves = ch == 1 ? (vec == 8 ? 12 : 16) : 8;
+  return waves / nw > 0 ? waves / nw : 1;
 }
 
 NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
@@ -278,10 +315,14 @@ NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
   return p;
 }
 
-template <typename T, int VEC, bool ODD, int NW, int CH>
-__global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a, NormPlan pn) {
-  constexpr int TEAMS = kBwdWaves / NW;
-  __shared__ float s_red[2][3][kBwdWaves];
+// FULL: every optional input is there (the gate may be missing: ones), so the loop over the rows
+// has no branch on them and its loads and stores stay in flight across it; otherwise each is
+// looked up.
+template <typename T, int VEC, bool ODD, int NW, int CH, bool FULL>
+__global__ __launch_bounds__(64 * NW * bwd_teams(NW, CH, VEC)) void norm_bwd_kernel(NormBwdArgs a,
+                                                                               NormPlan pn) {
+  constexpr int TEAMS = bwd_teams(NW, CH, VEC), WAVES = NW * TEAMS;
+  __shared__ float s_red[2][3][WAVES];
   extern __shared__ float s_fold[];  // TEAMS > 1: (TEAMS - 1) x (columns) x 3 floats, see below
   const int wave = threadIdx.x >> 6, team = wave / NW;
   const int tl = threadIdx.x - team * NW * 64;
@@ -289,25 +330,34 @@ __global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a,
   const T* gate = reinterpret_cast<const T*>(a.gate);
   const T* post = reinterpret_cast<const T*>(a.post);
   const T* pre = reinterpret_cast<const T*>(a.pre);
+  const bool has_in = FULL || a.dr_out, has_pre = FULL || pre, has_y = FULL || a.y,
+             has_post = FULL || post;
 
   Place<VEC> pl[CH];
 #pragma unroll
   for (int j = 0; j < CH; ++j) pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
-  // the weights of the lane's columns, in their stored form
+  // A lane keeps its weights in their stored form and has the next row's loads in flight while a
+  // row is reduced and stored.  In the widest rows a lane of several chunks has not the registers:
+  // it loads a chunk and its weights when it needs them, and once more (from the caches) after
+  // the reduction.
+  constexpr bool AHEAD = NW < 16 || CH == 1;
+  const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+  const uint4 ones4 = make_uint4(one, one, one, one);
   uint4 wpost[CH], wpre[CH], wgate[CH];
-#pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    if (post) wpost[j] = get<T, VEC>(post, pl[j].at);
-    if (pre) wpre[j] = get<T, VEC>(pre, pl[j].at);
-  }
   float spost[CH][VEC], spre[CH][VEC], sgate[CH][VEC];
 #pragma unroll
   for (int j = 0; j < CH; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) spost[j][e] = spre[j][e] = sgate[j][e] = 0.f;
+  auto load_weights = [&](int64_t t, int j) __attribute__((always_inline)) {
+    wpost[j] = has_post ? get<T, VEC>(post, pl[j].at) : ones4;
+    wpre[j] = has_pre ? get<T, VEC>(pre, pl[j].at) : ones4;
+    wgate[j] = gate ? get<T, VEC>(gate + t / a.group_len * a.ldg, pl[j].at) : ones4;
+  };
 
   // the team's rows
-  int64_t row0, nrows, step, iters, group = 0;
+  int64_t row0, nrows, step, iters;
   if (pn.whole_groups > 0) {
     const int64_t groups = a.tokens / a.group_len;
     const int64_t g0 = (int64_t)blockIdx.x * pn.whole_groups;
@@ -316,18 +366,13 @@ __global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a,
     nrows = ng * a.group_len;
     step = 0;
     iters = (ng + TEAMS - 1) / TEAMS * a.group_len;
-    group = g0;
   } else {
-    group = (int64_t)blockIdx.x / pn.chunks_per_group;
+    const int64_t group = (int64_t)blockIdx.x / pn.chunks_per_group;
     const int64_t c = (int64_t)blockIdx.x % pn.chunks_per_group;
     row0 = group * a.group_len + c * pn.rows_per_wg;
     nrows = min(pn.rows_per_wg, a.group_len - c * pn.rows_per_wg);
     step = TEAMS;
     iters = (nrows + TEAMS - 1) / TEAMS;
-    if (gate) {
-#pragma unroll
-      for (int j = 0; j < CH; ++j) wgate[j] = get<T, VEC>(gate + group * a.ldg, pl[j].at);
-    }
   }
   // row of iteration `it` within the workgroup's range
   auto row_of = [&](int64_t it) -> int64_t {
@@ -335,163 +380,187 @@ __global__ __launch_bounds__(64 * kBwdWaves) void norm_bwd_kernel(NormBwdArgs a,
     // whole groups: team q takes groups q, q + TEAMS, ...
     return (it / a.group_len * TEAMS + team) * a.group_len + it % a.group_len;
   };
-  // the next row's loads are in flight while this row is reduced and stored
-  uint4 ngr[CH], nhr[CH], nrr[CH], nyr[CH];
-  auto fetch = [&](int64_t it) __attribute__((always_inline)) {
+  auto token_of = [&](int64_t it) {
     const int64_t off = it < iters ? row_of(it) : 0;
-    const int64_t t = row0 + (off < nrows ? off : 0);
-    if (a.dr_out) {
-      const T* p = reinterpret_cast<const T*>(a.dr_out) + t * a.lddro;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) ngr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
-    }
-    if (pre) {
-      const T* p = reinterpret_cast<const T*>(a.dh) + t * a.lddh;
-      const T* q = reinterpret_cast<const T*>(a.r_out) + t * a.ldro;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) nhr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
-#pragma unroll
-      for (int j = 0; j < CH; ++j) nrr[j] = get_once<T, VEC, ODD>(q, pl[j].at);
-    }
-    if (a.y) {
-      const T* p = reinterpret_cast<const T*>(a.y) + t * a.ldy;
-#pragma unroll
-      for (int j = 0; j < CH; ++j) nyr[j] = get_once<T, VEC, ODD>(p, pl[j].at);
-    }
+    return row0 + (off < nrows ? off : 0);
   };
-  fetch(0);
+  struct Row {
+    uint4 g, h, r, y;
+  };
+  // chunk j of row t (once: past the caches); lanes past the row get zeros, which add nothing
+  auto load = [&](int64_t t, int j, bool once, Row& w) __attribute__((always_inline)) {
+    const int at = pl[j].at;
+    auto part = [&](const void* base, int64_t ld) {
+      const T* p = reinterpret_cast<const T*>(base) + t * ld;
+      return once ? get_once<T, VEC, ODD>(p, at) : get<T, VEC>(p, at);
+    };
+    w.g = has_in ? part(a.dr_out, a.lddro) : zero4;
+    w.h = has_pre ? part(a.dh, a.lddh) : zero4;
+    w.r = has_pre ? part(a.r_out, a.ldro) : zero4;
+    w.y = has_y ? part(a.y, a.ldy) : zero4;
+  };
+  Row cur[CH], nxt[CH];
+  float nb = 0.f, na = 1.f;
+  auto ahead = [&](int64_t it) __attribute__((always_inline)) {
+    const int64_t t = token_of(it);
+    if (has_pre) nb = a.rstd_pre[t];
+    if (has_post) na = a.rstd_post[t];
+#pragma unroll
+    for (int j = 0; j < CH; ++j) load(t, j, true, nxt[j]);
+  };
+  if constexpr (AHEAD) {
+#pragma unroll
+    for (int j = 0; j < CH; ++j) load_weights(row0, j);
+    ahead(0);
+  }
   for (int64_t it = 0; it < iters; ++it) {
-    const int64_t off = row_of(it);
-    if (step == 0 && gate && it % a.group_len == 0 && off < nrows) {
+    const bool live = row_of(it) < nrows;
+    const int64_t t = token_of(it);
+    float b, ar;
+    if constexpr (AHEAD) {
+      if (step == 0 && gate && it % a.group_len == 0) {
 #pragma unroll
-      for (int j = 0; j < CH; ++j)
-        wgate[j] = get<T, VEC>(gate + (group + off / a.group_len) * a.ldg, pl[j].at);
-    }
-    const bool live = off < nrows;
-    const int64_t t = row0 + (live ? off : 0);
-    uint4 gr[CH], hr[CH], rr[CH], yr[CH];
+        for (int j = 0; j < CH; ++j)
+          wgate[j] = get<T, VEC>(gate + t / a.group_len * a.ldg, pl[j].at);
+      }
+      keep_raw(wpost);
+      keep_raw(wpre);
+      keep_raw(wgate);
 #pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      gr[j] = ngr[j];
-      hr[j] = nhr[j];
-      rr[j] = nrr[j];
-      yr[j] = nyr[j];
+      for (int j = 0; j < CH; ++j) {
+        cur[j].g = pl[j].in ? nxt[j].g : zero4;
+        cur[j].h = pl[j].in ? nxt[j].h : zero4;
+        cur[j].r = pl[j].in ? nxt[j].r : zero4;
+        cur[j].y = pl[j].in ? nxt[j].y : zero4;
+      }
+      b = nb;
+      ar = na;
+      ahead(it + 1);
+    } else {
+      b = has_pre ? a.rstd_pre[t] : 0.f;
+      ar = has_post ? a.rstd_post[t] : 1.f;
     }
-    fetch(it + 1);
-    const float b = pre ? a.rstd_pre[t] : 0.f;
-    const float ar = post ? a.rstd_post[t] : 1.f;
     // the three sums: m1 = sum u rhat, A = sum c yhat (dr' + b u), B = sum c yhat b rhat
     float m1 = 0.f, sa = 0.f, sb = 0.f;
-    float G[CH][VEC];  // dr' + b u, then G
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      float u[VEC], rv[VEC], yv[VEC], c[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) G[j][e] = 0.f;
-      if (a.dr_out) val<T, VEC>(gr[j], G[j]);
-      if (pre) {
-        float w[VEC];
-        val<T, VEC>(hr[j], u);
-        val<T, VEC>(rr[j], rv);
-        val<T, VEC>(wpre[j], w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          rv[e] *= b;
-          u[e] *= w[e];
-          G[j][e] = __builtin_fmaf(b, u[e], G[j][e]);
-          if (pl[j].in && (!ODD || e >= pl[j].from)) m1 = __builtin_fmaf(u[e], rv[e], m1);
-        }
+      if constexpr (!AHEAD) {
+        __builtin_amdgcn_sched_barrier(0);  // one chunk's registers at a time
+        load(t, j, false, cur[j]);
+        load_weights(t, j);
+        if (!pl[j].in) cur[j].h = cur[j].y = zero4;
       }
-      if (post) {
-        float w[VEC];
-        val<T, VEC>(yr[j], yv);
-        val<T, VEC>(wpost[j], c);
-        if (gate) {
-          val<T, VEC>(wgate[j], w);
+      float g[VEC], u[VEC], rv[VEC], yv[VEC], wp[VEC], wq[VEC], wg[VEC];
+      val<T, VEC>(cur[j].g, g);
+      val<T, VEC>(cur[j].h, u);
+      val<T, VEC>(cur[j].r, rv);
+      val<T, VEC>(cur[j].y, yv);
+      val<T, VEC>(wpre[j], wq);
+      val<T, VEC>(wpost[j], wp);
+      val<T, VEC>(wgate[j], wg);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) c[e] *= w[e];
+      for (int e = 0; e < VEC; ++e) {
+        u[e] *= wq[e];
+        rv[e] *= b;
+        float cy = (wp[e] * wg[e]) * (yv[e] * ar);
+        if (ODD) {  // the chunk before counts the shared elements
+          u[e] = e >= pl[j].from ? u[e] : 0.f;
+          cy = e >= pl[j].from ? cy : 0.f;
         }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float cy = c[e] * (yv[e] * ar);
-          if (pl[j].in && (!ODD || e >= pl[j].from)) {
-            sa = __builtin_fmaf(cy, G[j][e], sa);
-            if (pre) sb = __builtin_fmaf(cy * b, rv[e], sb);
-          }
-        }
+        m1 = __builtin_fmaf(u[e], rv[e], m1);
+        sa = __builtin_fmaf(cy, __builtin_fmaf(b, u[e], g[e]), sa);
+        sb = __builtin_fmaf(cy * b, rv[e], sb);
       }
     }
     m1 = wave_sum(m1);
     sa = wave_sum(sa);
     sb = wave_sum(sb);
     if constexpr (NW > 1) {
-      float(*s)[kBwdWaves] = s_red[it & 1];  // the other buffer is still being read
+      float(*s)[WAVES] = s_red[it & 1];  // the other buffer is still being read
       if ((tl & 63) == 0) {
         s[0][wave] = m1;
         s[1][wave] = sa;
         s[2][wave] = sb;
       }
       __syncthreads();
-      m1 = sa = sb = 0.f;
+      if constexpr (NW <= 4) {
+        m1 = sa = sb = 0.f;
 #pragma unroll
-      for (int i = 0; i < NW; ++i) {
-        m1 += s[0][team * NW + i];
-        sa += s[1][team * NW + i];
-        sb += s[2][team * NW + i];
+        for (int i = 0; i < NW; ++i) {
+          m1 += s[0][team * NW + i];
+          sa += s[1][team * NW + i];
+          sb += s[2][team * NW + i];
+        }
+      } else {  // a lane per wave's sum: few registers
+        const int i = team * NW + min(tl & 63, NW - 1);
+        const bool mine = (tl & 63) < NW;
+        m1 = wave_sum(mine ? s[0][i] : 0.f);
+        sa = wave_sum(mine ? s[1][i] : 0.f);
+        sb = wave_sum(mine ? s[2][i] : 0.f);
       }
     }
     m1 *= a.inv_dim;
     const float bm = b * m1;
-    const float m2 = (sa - m1 * sb) * a.scale * a.inv_dim;
-    if (live) {
-      T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
-      T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
+    const float m2 = has_post ? (sa - m1 * sb) * a.scale * a.inv_dim : 0.f;
+    if constexpr (AHEAD) {
+      keep_raw(wpost);
+      keep_raw(wpre);
+      keep_raw(wgate);
+    }
+    T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
+    T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
+    const float on = live ? 1.f : 0.f;
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        if (pre) {
-          float u[VEC], rv[VEC];
-          val<T, VEC>(hr[j], u);
-          val<T, VEC>(rr[j], rv);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float rhat = rv[e] * b;
-            G[j][e] = __builtin_fmaf(-bm, rhat, G[j][e]);
-            spre[j][e] = __builtin_fmaf(u[e], rhat, spre[j][e]);
-          }
-        }
-        if (pl[j].in) put<T, VEC>(dr, pl[j].at, G[j]);
-        if (a.y) {
-          float yv[VEC], wp[VEC], wg[VEC], o[VEC];
-          val<T, VEC>(yr[j], yv);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) wp[e] = wg[e] = 1.f;
-          if (post) val<T, VEC>(wpost[j], wp);
-          if (gate) val<T, VEC>(wgate[j], wg);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float yhat = yv[e] * ar, sG = a.scale * G[j][e];
-            const float gy = sG * yhat;
-            sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
-            spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
-            const float cG = sG * wg[e] * wp[e];
-            o[e] = post ? ar * __builtin_fmaf(-m2, yhat, cG) : cG;
-          }
-          if (pl[j].in) put<T, VEC>(dy, pl[j].at, o);
-        }
+    for (int j = 0; j < CH; ++j) {
+      if constexpr (!AHEAD) {
+        __builtin_amdgcn_sched_barrier(0);
+        load(t, j, false, cur[j]);
+        load_weights(t, j);
+      } else {
+        keep_raw1(cur[j].g);
+        keep_raw1(cur[j].h);
+        keep_raw1(cur[j].r);
+        keep_raw1(cur[j].y);
       }
-      // whole groups: the group's last row writes its gate gradient
-      if (step == 0 && it % a.group_len == a.group_len - 1) {
-        if (a.dgate) {
-          T* dg = reinterpret_cast<T*>(a.dgate) + (t / a.group_len) * (int64_t)d;
+      float g[VEC], u[VEC], rv[VEC], yv[VEC], wp[VEC], wq[VEC], wg[VEC], o[VEC];
+      val<T, VEC>(cur[j].g, g);
+      val<T, VEC>(cur[j].h, u);
+      val<T, VEC>(cur[j].r, rv);
+      val<T, VEC>(cur[j].y, yv);
+      val<T, VEC>(wpre[j], wq);
+      val<T, VEC>(wpost[j], wp);
+      val<T, VEC>(wgate[j], wg);
 #pragma unroll
-          for (int j = 0; j < CH; ++j)
-            if (pl[j].in) put<T, VEC>(dg, pl[j].at, sgate[j]);
-        }
+      for (int e = 0; e < VEC; ++e) {
+        const float rhat = rv[e] * b, yhat = yv[e] * ar;
+        g[e] = __builtin_fmaf(-bm, rhat, __builtin_fmaf(b, u[e] * wq[e], g[e]));
+        spre[j][e] = __builtin_fmaf(u[e] * on, rhat, spre[j][e]);
+        const float sG = a.scale * g[e];
+        const float gy = sG * yhat * on;
+        sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
+        spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
+        o[e] = ar * __builtin_fmaf(-m2, yhat, sG * wg[e] * wp[e]);
+      }
+      // where a row is loaded again its chunks do not store each other's elements: dr may be
+      // dr_out or dh
+      const int from = AHEAD ? 0 : pl[j].from;
+      if (live && pl[j].in) {
+        put_own<T, VEC>(dr, pl[j].at, from, g);
+        if (has_y) put_own<T, VEC>(dy, pl[j].at, from, o);
+      }
+    }
+    // whole groups: the group's last row writes its gate gradient
+    if (step == 0 && it % a.group_len == a.group_len - 1) {
+      if (a.dgate && live) {
+        T* dg = reinterpret_cast<T*>(a.dgate) + (t / a.group_len) * (int64_t)d;
 #pragma unroll
         for (int j = 0; j < CH; ++j)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) sgate[j][e] = 0.f;
+          if (pl[j].in) put<T, VEC>(dg, pl[j].at, sgate[j]);
       }
+#pragma unroll
+      for (int j = 0; j < CH; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sgate[j][e] = 0.f;
     }
   }
   // fold the teams: team q's sums are added in team order, one sum at a time, through
@@ -582,7 +651,7 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
   l.vec = in_bf16 ? 8 : 4;
   if (dim < l.vec) l.vec = 1;
   bwd_shape((dim + l.vec - 1) / l.vec, &l.nw, &l.ch);
-  l.plan = plan_bwd(tokens, group_len, kBwdWaves / l.nw);
+  l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw, l.ch, l.vec));
   const size_t rows = (size_t)l.plan.wgs * (size_t)dim * 4;
   l.post = 0;
   l.pre = post ? rows : 0;
@@ -593,23 +662,40 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
 hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
-  constexpr int TEAMS = kBwdWaves / NW;
+  constexpr int TEAMS = bwd_teams(NW, CH, VEC);
   constexpr int LDS = (TEAMS - 1) * NW * 64 * CH * VEC * 4;
   static_assert(LDS < 60000, "the fold's LDS fits a workgroup's default limit");
-  hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH>), dim3((unsigned)pn.wgs),
-                     dim3(64 * kBwdWaves), LDS, st, a, pn);
+  const dim3 grid((unsigned)pn.wgs), block(64 * NW * TEAMS);
+  if (a.dr_out && a.pre && a.y && a.post)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true>), grid, block, LDS, st, a, pn);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false>), grid, block, LDS, st, a, pn);
   return hipGetLastError();
 }
 
 template <typename T, int VEC, bool ODD>
 hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
+  if (l.nw == 16 && l.ch == 2) return run_bwd<T, VEC, ODD, 16, 2>(a, l.plan, st);
+  if (l.ch == 4) return run_bwd<T, VEC, ODD, 16, 4>(a, l.plan, st);
+#if BCH == 2
   if (l.ch == 1) return run_bwd<T, VEC, ODD, 1, 1>(a, l.plan, st);
-  if (l.nw == 1) return run_bwd<T, VEC, ODD, 1, 2>(a, l.plan, st);
-  if (l.nw == 2) return run_bwd<T, VEC, ODD, 2, 2>(a, l.plan, st);
-  if (l.nw == 4) return run_bwd<T, VEC, ODD, 4, 2>(a, l.plan, st);
-  if (l.ch == 2) return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
-  if (l.ch == 4) return run_bwd<T, VEC, ODD, 8, 4>(a, l.plan, st);
-  return run_bwd<T, VEC, ODD, 8, 8>(a, l.plan, st);
+#endif
+  switch (l.nw) {
+    case 1: return run_bwd<T, VEC, ODD, 1, BCH>(a, l.plan, st);
+    case 2: return run_bwd<T, VEC, ODD, 2, BCH>(a, l.plan, st);
+    case 3: return run_bwd<T, VEC, ODD, 3, BCH>(a, l.plan, st);
+    case 4: return run_bwd<T, VEC, ODD, 4, BCH>(a, l.plan, st);
+    case 5: return run_bwd<T, VEC, ODD, 5, BCH>(a, l.plan, st);
+    case 6: return run_bwd<T, VEC, ODD, 6, BCH>(a, l.plan, st);
+    case 7: return run_bwd<T, VEC, ODD, 7, BCH>(a, l.plan, st);
+    case 8: return run_bwd<T, VEC, ODD, 8, BCH>(a, l.plan, st);
+#if BCH == 1
+    case 10: return run_bwd<T, VEC, ODD, 10, 1>(a, l.plan, st);
+    case 12: return run_bwd<T, VEC, ODD, 12, 1>(a, l.plan, st);
+    case 14: return run_bwd<T, VEC, ODD, 14, 1>(a, l.plan, st);
+#endif
+  }
+  return run_bwd<T, VEC, ODD, 16, 1>(a, l.plan, st);
 }
 
 template <typename T>

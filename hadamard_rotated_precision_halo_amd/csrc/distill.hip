@@ -76,29 +76,10 @@ __device__ __forceinline__ void pair_of(const float (*p)[2], float& m, float& s)
   for (int i = 0; i < NW; ++i) s += p[i][1] * exp2_fast((p[i][0] - ref) * kLog2e);
 }
 
-// A chunk of the gradient: past the caches where rows start on 16 bytes; the chunks of other rows
-// share lines, which the caches put together (777 x 50257 fp32, the gradient alone: 73.5 us with
-// every chunk past the caches, 63.8 us so).
-template <bool CACHED>
-__device__ __forceinline__ void store_grad(void* p, uint4 v) {
-  if constexpr (CACHED) store16u(p, v);
-  else store16u_nt(p, v);
-}
-
-// Keeps a row's chunks in their stored form from here on: the compiler would otherwise keep the
-// fp32 values of an earlier pass over them, twice the registers.
-template <int CH>
-__device__ __forceinline__ void keep_raw(uint4 (&raw)[CH]) {
-#pragma unroll
-  for (int j = 0; j < CH; ++j)
-    asm volatile("" : "+v"(raw[j].x), "+v"(raw[j].y), "+v"(raw[j].z), "+v"(raw[j].w));
-}
-
 enum Mode { kHeld, kStreamed, kParts };
 
 // One token's row (kParts: the part blockIdx.y of it, NT CH chunks).
-// ODD: rows of the gradient that start anywhere.
-template <typename T, int NT, int CH, int MODE, bool ODD>
+template <typename T, int NT, int CH, int MODE>
 __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
   __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
@@ -122,7 +103,7 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
 
   if (MODE == kParts && dl == 0.f) {  // a token that takes no part
     const float z[VEC] = {};
-    for (int c = tid; c < whole; c += NT) store_grad<ODD>(out + first + c * VEC, pack16<T>(z));
+    for (int c = tid; c < whole; c += NT) store16u_nt(out + first + c * VEC, pack16<T>(z));
     if (has_rest) elem_store<T>(out + first + rest0 + tid, 0.f);
     return;
   }
@@ -263,7 +244,7 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
         unpack16<T>(load16u(in + c * VEC), v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
-        store_grad<ODD>(o + c * VEC, pack16<T>(v));
+        store16u_nt(o + c * VEC, pack16<T>(v));
       }
     } else {
 #pragma unroll
@@ -273,7 +254,7 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
         unpack16<T>(raw[j], v);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) v[e] = zero ? 0.f : by * ex(v[e]);
-        if (c < whole) store_grad<ODD>(o + c * VEC, pack16<T>(v));
+        if (c < whole) store16u_nt(o + c * VEC, pack16<T>(v));
       }
     }
     if (has_rest) elem_store<T>(o + rest0 + tid, zero ? 0.f : by * ex(rest));
@@ -295,15 +276,11 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
   }
 }
 
-template <typename T, int NT, int CH, int MODE, bool ODD = false>
+template <typename T, int NT, int CH, int MODE>
 hipError_t run(const DistillArgs& a, hipStream_t st) {
-  if constexpr (!ODD) {
-    if (a.dlogits && ((reinterpret_cast<uintptr_t>(a.dlogits) | (a.ldd * sizeof(T))) & 15) != 0)
-      return run<T, NT, CH, MODE, true>(a, st);
-  }
   constexpr int64_t part = (int64_t)NT * CH * RowType<T>::VEC;
   const dim3 grid((unsigned)a.tokens, MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
-  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE, ODD>), grid, dim3(NT), (size_t)a.top * 12, st, a);
+  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT), (size_t)a.top * 12, st, a);
   return hipGetLastError();
 }
 

@@ -97,6 +97,17 @@ __device__ __forceinline__ uint4 pack16<float>(const float* v) {
                     __float_as_uint(v[3]));
 }
 
+// Keeps chunks in their stored form from here on: the compiler would otherwise keep the fp32 values
+// of an earlier pass over them, twice the registers.
+__device__ __forceinline__ void keep_raw1(uint4& w) {
+  asm volatile("" : "+v"(w.x), "+v"(w.y), "+v"(w.z), "+v"(w.w));
+}
+template <int CH>
+__device__ __forceinline__ void keep_raw(uint4 (&raw)[CH]) {
+#pragma unroll
+  for (int j = 0; j < CH; ++j) keep_raw1(raw[j]);
+}
+
 // Sum and maximum over the 64 lanes of a wave (every lane receives it; fixed order).
 __device__ __forceinline__ float wave_sum(float v) {
   v += partner<0>(v);
