@@ -25,9 +25,6 @@
 // results do not change between runs).
 #include "halo_kernels.h"
 #include "rowops.h"
-#ifndef BCH
-#define BCH 1
-#endif
 
 namespace halo {
 
@@ -273,31 +270,24 @@ struct NormPlan {
   int64_t wgs, rows_per_wg, chunks_per_group, whole_groups;
 };
 
-// Waves per token and chunks per lane of the backward for a row of `chunks` chunks: one chunk per
-// lane (a lane also holds three fp32 sums for each of its columns), as many waves as the row has
-// 64 chunks (rounded up to one of the instantiated counts), and 16 waves of two or four for the
-// widest rows.
+// Waves per token and chunks per lane of the backward for a row of `chunks` chunks: two chunks per
+// lane and as many waves as that takes, so that few lanes idle whatever the width (8192 x 4096
+// and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us);
+// 16 waves of two or four for the widest rows.
 void bwd_shape(int64_t chunks, int* nw, int* ch) {
   const int64_t per = (chunks + 63) / 64;
-#if BCH == 2
   *ch = per <= 1 ? 1 : per <= 32 ? 2 : 4;
   *nw = per <= 16 ? (int)((per + 1) / 2) : 16;
-#else
-  *ch = per <= 16 ? 1 : per <= 32 ? 2 : 4;
-  *nw = per > 8 ? (int)(per > 14 ? 16 : (per + 1) / 2 * 2) : (int)per;
-#endif
 }
-// Teams of a workgroup: at most 16 waves together.
-constexpr int bwd_teams(int nw, int ch, int vec) {
-  const int waves = ch == 1 ? (vec == 8 ? 12 : 16) : 8;
-  return waves / nw > 0 ? waves / nw : 1;
-}
+// Teams of a workgroup: about 8 waves together, whose lanes then have 256 registers each.
+constexpr int bwd_teams(int nw) { return nw <= 8 ? 8 / nw : 1; }
 
 NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
   NormPlan p{};
   // one workgroup per compute unit: its teams keep enough rows in flight (each prefetches its
   // next row), and the partial sums, one row per workgroup, stay few (8192 x 4096 bf16: 96.8 us
-  // with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9 us)
+  // with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9 us, each before
+  // the loop lost its branches)
   int64_t rows = (tokens + 255) / 256;
   if (rows < teams) rows = teams;
   if (group_len * teams <= rows) {
@@ -319,9 +309,9 @@ NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
 // has no branch on them and its loads and stores stay in flight across it; otherwise each is
 // looked up.
 template <typename T, int VEC, bool ODD, int NW, int CH, bool FULL>
-__global__ __launch_bounds__(64 * NW * bwd_teams(NW, CH, VEC)) void norm_bwd_kernel(NormBwdArgs a,
+__global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormBwdArgs a,
                                                                                NormPlan pn) {
-  constexpr int TEAMS = bwd_teams(NW, CH, VEC), WAVES = NW * TEAMS;
+  constexpr int TEAMS = bwd_teams(NW), WAVES = NW * TEAMS;
   __shared__ float s_red[2][3][WAVES];
   extern __shared__ float s_fold[];  // TEAMS > 1: (TEAMS - 1) x (columns) x 3 floats, see below
   const int wave = threadIdx.x >> 6, team = wave / NW;
@@ -340,7 +330,7 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, CH, VEC)) void norm_bwd_ker
   // row is reduced and stored.  In the widest rows a lane of several chunks has not the registers:
   // it loads a chunk and its weights when it needs them, and once more (from the caches) after
   // the reduction.
-  constexpr bool AHEAD = NW < 16 || CH == 1;
+  constexpr bool AHEAD = NW < 16;
   const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
   const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
   const uint4 ones4 = make_uint4(one, one, one, one);
@@ -651,7 +641,7 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
   l.vec = in_bf16 ? 8 : 4;
   if (dim < l.vec) l.vec = 1;
   bwd_shape((dim + l.vec - 1) / l.vec, &l.nw, &l.ch);
-  l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw, l.ch, l.vec));
+  l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw));
   const size_t rows = (size_t)l.plan.wgs * (size_t)dim * 4;
   l.post = 0;
   l.pre = post ? rows : 0;
@@ -662,7 +652,7 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
 hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
-  constexpr int TEAMS = bwd_teams(NW, CH, VEC);
+  constexpr int TEAMS = bwd_teams(NW);
   constexpr int LDS = (TEAMS - 1) * NW * 64 * CH * VEC * 4;
   static_assert(LDS < 60000, "the fold's LDS fits a workgroup's default limit");
   const dim3 grid((unsigned)pn.wgs), block(64 * NW * TEAMS);
@@ -675,27 +665,19 @@ hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
 
 template <typename T, int VEC, bool ODD>
 hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
-  if (l.nw == 16 && l.ch == 2) return run_bwd<T, VEC, ODD, 16, 2>(a, l.plan, st);
   if (l.ch == 4) return run_bwd<T, VEC, ODD, 16, 4>(a, l.plan, st);
-#if BCH == 2
   if (l.ch == 1) return run_bwd<T, VEC, ODD, 1, 1>(a, l.plan, st);
-#endif
   switch (l.nw) {
-    case 1: return run_bwd<T, VEC, ODD, 1, BCH>(a, l.plan, st);
-    case 2: return run_bwd<T, VEC, ODD, 2, BCH>(a, l.plan, st);
-    case 3: return run_bwd<T, VEC, ODD, 3, BCH>(a, l.plan, st);
-    case 4: return run_bwd<T, VEC, ODD, 4, BCH>(a, l.plan, st);
-    case 5: return run_bwd<T, VEC, ODD, 5, BCH>(a, l.plan, st);
-    case 6: return run_bwd<T, VEC, ODD, 6, BCH>(a, l.plan, st);
-    case 7: return run_bwd<T, VEC, ODD, 7, BCH>(a, l.plan, st);
-    case 8: return run_bwd<T, VEC, ODD, 8, BCH>(a, l.plan, st);
-#if BCH == 1
-    case 10: return run_bwd<T, VEC, ODD, 10, 1>(a, l.plan, st);
-    case 12: return run_bwd<T, VEC, ODD, 12, 1>(a, l.plan, st);
-    case 14: return run_bwd<T, VEC, ODD, 14, 1>(a, l.plan, st);
-#endif
+    case 1: return run_bwd<T, VEC, ODD, 1, 2>(a, l.plan, st);
+    case 2: return run_bwd<T, VEC, ODD, 2, 2>(a, l.plan, st);
+    case 3: return run_bwd<T, VEC, ODD, 3, 2>(a, l.plan, st);
+    case 4: return run_bwd<T, VEC, ODD, 4, 2>(a, l.plan, st);
+    case 5: return run_bwd<T, VEC, ODD, 5, 2>(a, l.plan, st);
+    case 6: return run_bwd<T, VEC, ODD, 6, 2>(a, l.plan, st);
+    case 7: return run_bwd<T, VEC, ODD, 7, 2>(a, l.plan, st);
+    case 8: return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
   }
-  return run_bwd<T, VEC, ODD, 16, 1>(a, l.plan, st);
+  return run_bwd<T, VEC, ODD, 16, 2>(a, l.plan, st);
 }
 
 template <typename T>
