@@ -913,7 +913,7 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
                  y_dtype=None, z=None, workspace=None, stream=None, signs_k=None):
     """linear_act_fwd on weights quantised once, for serving: (qw, sw) = fwht_quant(w, ROWS, block,
     q_dtype[, signs=signs_k]) of the weights [n, k] (k padded to a multiple of block, of 32 at
-    least).  Only x is rotated and quantised here; up to 64 rows of x take a kernel bound by
+    least).  Only x is rotated and quantised here; up to 16 rows of x take a kernel bound by
     reading qw once.  Returns y (and z when a z to write it to is given)."""
     dt, dev = _io_2d(x, "x")
     m, k = x.shape

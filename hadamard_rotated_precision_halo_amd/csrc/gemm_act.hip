@@ -6,11 +6,9 @@ namespace halo {
 
 namespace {
 
-// 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit; the 64 x 64 tile also
-// with a ring of 8 slabs, for one workgroup per unit.
+// 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit.
 using MidTile = TileCfg<128, 2, 2, 2>;
 using SmallTile = TileCfg<64, 2, 2, 4>;
-using DeepTile = TileCfg<64, 2, 2, 8>;
 
 template <int KIND, int OUT, bool MASK, typename CFG>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
@@ -27,16 +25,19 @@ hipError_t run(const GemmArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The largest tile that still gives the 256 compute units a tile each (with 64 x 64 below that):
-// a workgroup of the 256 tile needs a whole unit, so fewer tiles leave units idle for the whole
-// contraction, while smaller tiles read each operand more often from the L2.
+// The largest tile that still gives the 256 compute units a tile each, since a workgroup of the
+// 256 tile needs a whole unit and fewer tiles leave units idle for the whole contraction, while
+// smaller tiles read each operand more often from the L2.  Below that 64 x 64 tiles: two
+// workgroups per unit, or, where there is not even one tile per unit, the kernel whose waves
+// split the contraction (256 x 4096 x 4096 INT8: 16.3 us a call against 18.4 us; but 400 rows:
+// 24.3 against 21.7 us).
 template <int KIND, int OUT, bool MASK>
 hipError_t pick(const GemmArgs& g, hipStream_t st) {
   auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((g.n + bt - 1) / bt); };
   if (tiles(256) >= 224) return run<KIND, OUT, MASK, BigTile>(g, st);
   if (tiles(128) >= 224) return run<KIND, OUT, MASK, MidTile>(g, st);
   if (tiles(64) > 256) return run<KIND, OUT, MASK, SmallTile>(g, st);
-  return run<KIND, OUT, MASK, DeepTile>(g, st);
+  return launch_gemm_ksplit(g, KIND, OUT, st);
 }
 
 template <int KIND, int OUT>

@@ -66,77 +66,10 @@ __device__ __forceinline__ void finish(const GemmArgs& g, float acc, float sa, i
   if (g.z) elem_store<T>(reinterpret_cast<T*>(g.z) + at, z);
 }
 
-template <int KIND, int OUT, int MT>
-__global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
-  using S = Step<KIND>;
-  using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
-  constexpr int UN = MT <= 2 ? 8 / S::CH : 4 / S::CH;  // steps whose loads are in flight together
-  __shared__ typename S::Acc s_acc[kWaves][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r16 = lane & 15, q16 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const char* pb = static_cast<const char*>(g.b) + min(n0 + r16, g.n - 1) * g.ldb + q16 * 16;
-  const char* pa[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-    pa[t] = static_cast<const char*>(g.a) + min((int64_t)(t * 16 + r16), g.m - 1) * g.lda + q16 * 16;
-
-  typename S::Acc acc[MT] = {};
-  const int steps = (int)((g.k + S::K - 1) / S::K);
-  const int s0 = (int)((int64_t)steps * wave / kWaves), s1 = (int)((int64_t)steps * (wave + 1) / kWaves);
-  for (int s = s0; s < s1; s += UN) {
-    v4i fb[UN][S::CH], fa[UN][MT][S::CH];
-#pragma unroll
-    for (int u = 0; u < UN; ++u)
-#pragma unroll
-      for (int h = 0; h < S::CH; ++h) {
-        // a chunk past the contraction or the wave's steps reads the row's first bytes
-        const int64_t k = (int64_t)(s + u) * S::K + h * 64;
-        const bool in = s + u < s1 && k + q16 * 16 < g.k;
-        fb[u][h] = *reinterpret_cast<const v4i*>(pb + (in ? k : -(int64_t)q16 * 16));
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-          fa[u][t][h] = *reinterpret_cast<const v4i*>(pa[t] + (in ? k : -(int64_t)q16 * 16));
-      }
-#pragma unroll
-    for (int u = 0; u < UN; ++u) {
-#pragma unroll
-      for (int h = 0; h < S::CH; ++h) {
-        const int64_t k = (int64_t)(s + u) * S::K + h * 64;
-        const int keep = s + u < s1 && k + q16 * 16 < g.k ? -1 : 0;
-        fb[u][h] &= keep;
-        if constexpr (KIND == 1) {  // 0 x NaN is not 0
-#pragma unroll
-          for (int t = 0; t < MT; ++t) fa[u][t][h] &= keep;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = S::mul(fb[u], fa[u][t], acc[t]);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) s_acc[wave][t][lane] = acc[t];
-  __syncthreads();
-  // lane (r16, q16) of tile t holds row t * 16 + r16 and columns n0 + q16 * 4 + [0, 4)
-  for (int i = threadIdx.x; i < MT * 64; i += 64 * kWaves) {
-    const int t = i >> 6, l = i & 63;
-    typename S::Acc v = s_acc[0][t][l];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += s_acc[w][t][l];
-    const int64_t row = t * 16 + (l & 15), col = n0 + (l >> 4) * 4;
-    if (row >= g.m) continue;
-    const float sa = g.sa[row];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (col + e >= g.n) break;
-      finish<T>(g, (float)v[e], sa, row, col + e);
-    }
-  }
-}
-
-// One step's operands of b for UN steps from s on, 0 past the contraction or the wave's steps.
+// An operand's fragments of UN steps from s on; chunks past the contraction or the wave's steps
+// read the row's first bytes (the caller zeroes them).
 template <int KIND, int UN>
-__device__ __forceinline__ void load_b(v4i (&fb)[UN][Step<KIND>::CH], const char* pb, int s, int s1,
+__device__ __forceinline__ void load_steps(v4i (&f)[UN][Step<KIND>::CH], const char* p, int s, int s1,
                                        int64_t k_end, int q16) {
   using S = Step<KIND>;
 #pragma unroll
@@ -145,8 +78,59 @@ __device__ __forceinline__ void load_b(v4i (&fb)[UN][Step<KIND>::CH], const char
     for (int h = 0; h < S::CH; ++h) {
       const int64_t k = (int64_t)(s + u) * S::K + h * 64;
       const bool in = s + u < s1 && k + q16 * 16 < k_end;
-      fb[u][h] = *reinterpret_cast<const v4i*>(pb + (in ? k : -(int64_t)q16 * 16));
+      f[u][h] = *reinterpret_cast<const v4i*>(p + (in ? k : -(int64_t)q16 * 16));
     }
+}
+
+// The waves' partial tiles, added in wave order, and the epilogue: element (row i % 16, column
+// i / 16) of thread i is value column % 4 of lane (row, column / 4).
+template <typename T, int KIND, typename Scale>
+__device__ __forceinline__ void join(const GemmArgs& g, const typename Step<KIND>::Acc (*s_acc)[64],
+                                     int64_t n0, Scale scale) {
+  using E = typename std::conditional<KIND == 0, int, float>::type;
+  const int i = threadIdx.x, row = i & 15, cl = i >> 4;
+  const int64_t col = n0 + cl;
+  if (i >= 256 || row >= g.m || col >= g.n) return;
+  E sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) sum += s_acc[w][(cl >> 2) * 16 + row][cl & 3];
+  finish<T>(g, (float)sum, scale(row), row, col);
+}
+
+template <int KIND, int OUT>
+__global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
+  using S = Step<KIND>;
+  using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
+  constexpr int UN = 8 / S::CH;  // steps whose loads are in flight together
+  __shared__ typename S::Acc s_acc[kWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r16 = lane & 15, q16 = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const char* pb = static_cast<const char*>(g.b) + min(n0 + r16, g.n - 1) * g.ldb + q16 * 16;
+  const char* pa = static_cast<const char*>(g.a) + min((int64_t)r16, g.m - 1) * g.lda + q16 * 16;
+
+  typename S::Acc acc = {};
+  const int steps = (int)((g.k + S::K - 1) / S::K);
+  const int s0 = (int)((int64_t)steps * wave / kWaves), s1 = (int)((int64_t)steps * (wave + 1) / kWaves);
+  for (int s = s0; s < s1; s += UN) {
+    v4i fb[UN][S::CH], fa[UN][S::CH];
+    load_steps<KIND, UN>(fb, pb, s, s1, g.k, q16);
+    load_steps<KIND, UN>(fa, pa, s, s1, g.k, q16);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+#pragma unroll
+      for (int h = 0; h < S::CH; ++h) {
+        const int64_t k = (int64_t)(s + u) * S::K + h * 64;
+        const int keep = s + u < s1 && k + q16 * 16 < g.k ? -1 : 0;
+        fb[u][h] &= keep;
+        if constexpr (KIND == 1) fa[u][h] &= keep;  // 0 x NaN is not 0
+      }
+      acc = S::mul(fb[u], fa[u], acc);
+    }
+  }
+  s_acc[wave][lane] = acc;
+  __syncthreads();
+  join<T, KIND>(g, s_acc, n0, [&](int row) { return g.sa[row]; });
 }
 
 // Butterflies of one stage across lanes at distance 2^S where the block spans them.
@@ -208,7 +192,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   const int steps = (kq + S::K - 1) / S::K;
   const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
   v4i fb[UN][S::CH];
-  load_b<KIND, UN>(fb, pb, s0, s1, g.k, q16);
+  load_steps<KIND, UN>(fb, pb, s0, s1, g.k, q16);
 
   // ---- the rows of x ---------------------------------------------------------------------
   const int slices = (kq + 511) / 512, units = m * slices;
@@ -260,7 +244,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   typename S::Acc acc = {};
   const char* la = s_codes + min(r16, m - 1) * pitch + q16 * 16;
   for (int s = s0; s < s1; s += UN) {
-    if (s > s0) load_b<KIND, UN>(fb, pb, s, s1, g.k, q16);
+    if (s > s0) load_steps<KIND, UN>(fb, pb, s, s1, g.k, q16);
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
       v4i fa[S::CH];
@@ -278,16 +262,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   }
   s_acc[wave][lane] = acc;
   __syncthreads();
-  // element (row i % 16, column i / 16), of 16 x 16: lane (row, column / 4), value column % 4
-  const int i = threadIdx.x;
-  const int row = i & 15, cl = i >> 4;
-  const int64_t col = n0 + cl;
-  if (i >= 256 || row >= m || col >= g.n) return;
-  using E = typename std::conditional<KIND == 0, int, float>::type;
-  E sum = 0;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) sum += s_acc[w][(cl >> 2) * 16 + row][cl & 3];
-  finish<T>(g, (float)sum, s_sa[row], row, col);
+  join<T, KIND>(g, s_acc, n0, [&](int row) { return s_sa[row]; });
 }
 
 template <typename TX, int KIND, int OUT>
@@ -306,10 +281,8 @@ hipError_t run_fused_x(const GemmArgs& g, const FqArgs& f, int kind, int out, hi
 
 template <int KIND, int OUT>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
-  const dim3 grid((unsigned)((g.n + 15) / 16)), block(64 * kWaves);
-  if (g.m <= 16) hipLaunchKernelGGL((skinny_kernel<KIND, OUT, 1>), grid, block, 0, st, g);
-  else if (g.m <= 32) hipLaunchKernelGGL((skinny_kernel<KIND, OUT, 2>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((skinny_kernel<KIND, OUT, 4>), grid, block, 0, st, g);
+  hipLaunchKernelGGL((skinny_kernel<KIND, OUT>), dim3((unsigned)((g.n + 15) / 16)),
+                     dim3(64 * kWaves), 0, st, g);
   return hipGetLastError();
 }
 

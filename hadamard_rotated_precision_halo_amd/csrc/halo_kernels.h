@@ -121,8 +121,10 @@ hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs* g1, int kind, int
 // One product with the layer's epilogue: y = act(z) + residual, z = (acc sa) sb + bias.  kind: 0
 // INT8, 1 FP8 (E4M3 both).  out: 1 fp32, 2 bf16.  c, res and z rows and bias 16-byte aligned.
 hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st);
+// The same with the contraction split over a workgroup's waves, for few tiles (gemm_ksplit.hip).
+hipError_t launch_gemm_ksplit(const GemmArgs& g, int kind, int out, hipStream_t st);
 // The same for up to kSkinnyRows rows of a (gemm_skinny.hip).
-constexpr int kSkinnyRows = 64;
+constexpr int kSkinnyRows = 16;
 hipError_t launch_gemm_skinny(const GemmArgs& g, int kind, int out, hipStream_t st);
 // The same with the rows pass f (its codes and scales stay inside) of m rows in one launch.
 bool skinny_fused_ok(int64_t m, int64_t kq, int block);

@@ -380,7 +380,7 @@ halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type
  * The same on weights quantised once (serving): qw [n x kq] and sw [n] are the codes and scales
  * that halo_fwht_quant gives along the rows of W (with the same block, signs and q_type), dense,
  * kq = k rounded up to a multiple of block, which must be a multiple of 32.  Only x is rotated
- * and quantised here.  One to 64 rows of x run a kernel bound by reading qw once.
+ * and quantised here.  One to 16 rows of x run a kernel bound by reading qw once.
  *   ws   at least halo_linear_act_q_workspace_bytes(m, k, block) bytes, 16-byte aligned (0 bytes
  *        for the fewest rows, which are quantised inside the product's kernel: ws may be NULL).
  */
