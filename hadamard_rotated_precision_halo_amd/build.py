@@ -8,7 +8,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libhalo.so")
-SOURCES = ["halo_api.hip", "fwht_quant.hip", "fwht_wave.hip", "fwht_wave_sr.hip", "fwht_dual.hip",
+SOURCES = ["halo_api.hip", "fwht_quant.hip", "fwht_wave.hip", "fwht_wave_sr.hip", "fwht_wave_act.hip",
+           "fwht_dual.hip",
            "gemm.hip", "gemm_act.hip", "gemm_skinny.hip", "gemm_ksplit.hip", "act_grad.hip", "block_norm.hip",
            "distill.hip", "mfma_probe.hip"]
 HEADERS = ["halo_device.h", "halo_kernels.h", "fwht_wave.h", "rowops.h", "gemm_tile.h", "epilogue.h"]

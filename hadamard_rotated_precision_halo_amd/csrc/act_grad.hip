@@ -102,6 +102,13 @@ hipError_t run(const void* dy, const void* z, int act, int64_t m, int64_t n, flo
 
 }  // namespace
 
+hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t* db,
+                           hipStream_t st) {
+  hipLaunchKernelGGL((part_sum_kernel<uint16_t>), dim3((unsigned)((n + 63) / 64)), dim3(256), 0, st,
+                     part, parts, n, db);
+  return hipGetLastError();
+}
+
 int64_t act_grad_parts(int64_t m, int64_t n) {
   const int64_t rows = rows_per(m, n);
   return (m + rows - 1) / rows;

@@ -46,6 +46,7 @@
 // a template parameter, instantiated in fwht_wave_sr.hip).
 #pragma once
 
+#include "epilogue.h"
 #include "halo_device.h"
 #include "halo_kernels.h"
 
@@ -301,15 +302,35 @@ __device__ __forceinline__ void store_slice_staged(const FqArgs& a, const float*
 // Load the 8 chunks of a lane: chunk j at position pos0 + off(lane, j) of the vector whose
 // element 0 is at vp.  The loads are unconditional (a chunk of the zero padding, at and past
 // in_len, reads chunk 0 instead), so they issue back to back; only passes with padding then
-// zero those chunks.  Then the transform's signs.
-template <typename Tin, int B>
+// zero those chunks.  Then the transform's signs.  ACT: the vector is dz = dy act'(z), z at the
+// same place of a.z as dy of a.x.
+template <typename Tin, int B, bool ACT = false>
 __device__ __forceinline__ void load_slice(const FqArgs& a, const Tin* vp, int64_t pos0, int lane,
                                            bool valid, float* v) {
   using S = Slice<B>;
+  if constexpr (ACT) {
+    const Tin* zp = a.z + (vp - reinterpret_cast<const Tin*>(a.x));
+    uint4 d[8], z[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int64_t pos = pos0 + S::off(lane, j);
-    load8<Tin>(vp + (valid && pos < a.in_len ? pos : 0), &v[j * 8]);
+    for (int j = 0; j < 8; ++j) {
+      const int64_t pos = pos0 + S::off(lane, j);
+      const int64_t at = valid && pos < a.in_len ? pos : 0;
+      d[j] = *reinterpret_cast<const uint4*>(vp + at);
+      z[j] = *reinterpret_cast<const uint4*>(zp + at);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float zv[8];
+      unpack_bf16x8(d[j], &v[j * 8]);
+      unpack_bf16x8(z[j], zv);
+      slope_mul<8>(a.act, zv, &v[j * 8]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t pos = pos0 + S::off(lane, j);
+      load8<Tin>(vp + (valid && pos < a.in_len ? pos : 0), &v[j * 8]);
+    }
   }
   if (a.in_len < a.len) {
 #pragma unroll
@@ -353,7 +374,7 @@ __device__ __forceinline__ float stored_scale(const FqArgs& a, float mx) {
 
 // One wave's slice of a rows pass with L <= 4096 and 4096 % L == 0: wave `gw` of the pass owns
 // rows [gw * 4096 / L, (gw + 1) * 4096 / L).  Lanes past the last row idle.
-template <typename Tin, int B, int QT, bool SR>
+template <typename Tin, int B, int QT, bool SR, bool ACT = false>
 __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane) {
   using S = Slice<B>;
   const int L = (int)a.len;
@@ -367,7 +388,7 @@ __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane)
   // idle lanes read the first chunk of row 0
   const Tin* rp = xin + (valid ? row : 0) * a.ldx;
   float v[64];
-  load_slice<Tin, B>(a, rp, col0, lane, valid, v);
+  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, v);
   const float sgn = rotate64<B>(v, lane);
   float mx = valid ? absmax64(v) : 0.f;
   mx = lane_max(mx, row_lanes_log2);
@@ -383,7 +404,7 @@ __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane)
 // multi = 0: 4096 % L == 0, each wave owns 4096 / L whole rows.
 // One launch serves up to two passes of the same geometry (workgroups below pp.split run the
 // first), and can clear a scratch range for the column passes that follow it on the stream.
-template <typename Tin, int B, int QT, bool SR>
+template <typename Tin, int B, int QT, bool SR, bool ACT = false>
 __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   using S = Slice<B>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
@@ -406,7 +427,7 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
       if (row >= a.nvec) return;
       const Tin* rp = reinterpret_cast<const Tin*>(a.x) + row * a.ldx;
       float v[64];
-      load_slice<Tin, B>(a, rp, 0, lane, true, v);
+      load_slice<Tin, B, ACT>(a, rp, 0, lane, true, v);
       const float sgn = rotate64<B>(v, lane);
       const float mx = lane_max(absmax64(v), 6);
       if (lane == 0) a.scale[row] = stored_scale<QT>(a, mx);
@@ -414,7 +435,7 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
       store_slice_staged<B, QT, SR>(a, v, mul, row * a.ldq, lane, row, 0, 4096, st);
       return;
     }
-    rows_wave<Tin, B, QT, SR>(a, (int64_t)bid * nw + w, lane);
+    rows_wave<Tin, B, QT, SR, ACT>(a, (int64_t)bid * nw + w, lane);
     return;
   }
   const int64_t row = bid;
@@ -423,7 +444,7 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   const Tin* __restrict__ xin = reinterpret_cast<const Tin*>(a.x);
   const Tin* rp = xin + row * a.ldx;
   float v[64];
-  load_slice<Tin, B>(a, rp, col0, lane, valid, v);
+  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, v);
   const float sgn = rotate64<B>(v, lane);
   float mx = valid ? absmax64(v) : 0.f;
   mx = lane_max(mx, 6);
@@ -460,7 +481,7 @@ static int64_t rows2_grid(const FqArgs& a) {
   return (waves + 3) / 4;
 }
 
-template <typename Tin, int B, int QT, bool SR>
+template <typename Tin, int B, int QT, bool SR, bool ACT = false>
 static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
   const int64_t L = pp.p0.len;
   const int64_t g0 = rows2_grid(pp.p0), g1 = pp.has1 ? rows2_grid(pp.p1) : 0;
@@ -476,10 +497,10 @@ static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
   const int nw = multi ? (int)((L + 4095) / 4096) : 4;
   const int lds = QT != 3 && (multi || L == 4096) ? nw * kStageBytes : 0;
   if (lds > 65536) {
-    const hipError_t e = allow_dynamic_lds<&fq_rows2_kernel<Tin, B, QT, SR>>(16 * kStageBytes);
+    const hipError_t e = allow_dynamic_lds<&fq_rows2_kernel<Tin, B, QT, SR, ACT>>(16 * kStageBytes);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((fq_rows2_kernel<Tin, B, QT, SR>), dim3((unsigned)grid), dim3(64 * nw), lds,
+  hipLaunchKernelGGL((fq_rows2_kernel<Tin, B, QT, SR, ACT>), dim3((unsigned)grid), dim3(64 * nw), lds,
                      st, pp, multi);
   return hipGetLastError();
 }
@@ -638,6 +659,92 @@ __device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, in
   }
 }
 
+// The activation-gradient pass: dz = dy act'(z) of bf16 dy and z, in fp32, through the fp32 tile.
+// Both rounds' loads of both inputs (8 bytes: 4 columns of a row) are issued first.
+template <int B>
+__device__ __forceinline__ void cols_load_act(const ColsProb& pr, int64_t c0, int part, int t,
+                                              uint2 (&d)[2][8], uint2 (&z)[2][8]) {
+  const FqArgs& a = pr.a;
+  const int R = pr.R, CC = pr.C / 4;
+  const int cc = t % CC, i = t / CC;
+  const int64_t col = c0 + cc * 4;
+  const int64_t p0 = col < a.nvec ? col : 0;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t at = p0 + (r0 + e < a.in_len ? (r0 + e) * a.ldx : 0);
+      d[h][e] = *reinterpret_cast<const uint2*>(x + at);
+      z[h][e] = *reinterpret_cast<const uint2*>(a.z + at);
+    }
+  }
+}
+
+// One round's dz (8 rows of 4 columns), its sums over the rows added to sum, the transform's signs
+// last.
+template <int B>
+__device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, int h,
+                                         const uint2 (&d)[8], const uint2 (&z)[8], float (&sum)[4],
+                                         uint4 (&raw)[8]) {
+  const FqArgs& a = pr.a;
+  const int i = t / (pr.C / 4);
+  const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(i, h) * 8;
+  const uint32_t flip = a.signs ? a.signs[r0 >> 5] >> (r0 & 31) : 0u;
+  // a row at a time: few values live beside the tile's
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float v[4] = {__uint_as_float(d[e].x << 16), __uint_as_float(d[e].x & 0xffff0000u),
+                  __uint_as_float(d[e].y << 16), __uint_as_float(d[e].y & 0xffff0000u)};
+    const float zv[4] = {__uint_as_float(z[e].x << 16), __uint_as_float(z[e].x & 0xffff0000u),
+                         __uint_as_float(z[e].y << 16), __uint_as_float(z[e].y & 0xffff0000u)};
+    slope_mul<4>(a.act, zv, v);
+    const bool in = r0 + e < a.in_len;  // rows of the zero padding
+    const uint32_t f = ((flip >> e) & 1u) ? 0x80000000u : 0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      v[c] = in ? v[c] : 0.f;
+      sum[c] += v[c];
+    }
+    raw[e] = make_uint4(__float_as_uint(v[0]) ^ f, __float_as_uint(v[1]) ^ f,
+                        __float_as_uint(v[2]) ^ f, __float_as_uint(v[3]) ^ f);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// The task's column sums from its threads' (4 columns each): lanes of the same columns first,
+// then the waves in order, into row `part` of db_part or db itself.
+__device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
+                                        float (&sum)[4]) {
+  __shared__ float s_db[16][256];
+  const FqArgs& a = pr.a;
+  const int CC = pr.C / 4, lane = t & 63, w = t >> 6;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    if (CC <= 1) sum[c] += partner<0>(sum[c]);
+    if (CC <= 2) sum[c] += partner<1>(sum[c]);
+    if (CC <= 4) sum[c] += partner<2>(sum[c]);
+    if (CC <= 8) sum[c] += partner<3>(sum[c]);
+    if (CC <= 16) sum[c] += partner<4>(sum[c]);
+    if (CC <= 32) sum[c] += partner<5>(sum[c]);
+  }
+  const int width = CC < 64 ? CC : 64;  // column chunks of a wave
+  if (lane < width) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s_db[w][lane * 4 + c] = sum[c];
+  }
+  __syncthreads();
+  // waves w, w + CC / 64, .. hold the same columns where a row of the tile spans several waves
+  const int same = CC <= 64 ? 1 : CC / 64;
+  if (t < pr.C && c0 + t < a.nvec) {
+    float v = 0.f;
+    for (int i = t / 256; i < 16; i += same) v += s_db[i][t & 255];
+    if (a.db) a.db[c0 + t] = (uint16_t)bf16x2_of(v, 0.f);
+    else if (a.db_part) a.db_part[(int64_t)part * a.nvec + c0 + t] = v;
+  }
+}
+
 __device__ __forceinline__ uint32_t word_of(const uint4& u, int e) {
   return e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w;
 }
@@ -668,7 +775,8 @@ __device__ __forceinline__ void cols_stage_f32(const ColsProb& pr, int t, int h,
 // REPAIR: the second launch of an exchanging pass (see below): only the tasks of strips marked
 // late run, with the column maxima complete by then.
 // F32: fp32 input (two LDS rounds, see cols_load_f32); else bf16.
-template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false>
+// ACT: the activation-gradient pass (see cols_load_act; F32 with it).
+template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false, bool ACT = false>
 __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uint4* lds) {
   using S = Slice<B>;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -714,11 +822,15 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   // ---- load R rows x C columns, transposed into LDS, into the wave's slices ---------------
   float v[64];
   if constexpr (F32) {
-    uint4 raw[2][8];
-    cols_load_f32<B>(pr, c0, part, t, raw);
+    uint4 raw[ACT ? 1 : 2][8];
+    uint2 ad[ACT ? 2 : 1][8], az[ACT ? 2 : 1][8];
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (ACT) cols_load_act<B>(pr, c0, part, t, ad, az);
+    else cols_load_f32<B>(pr, c0, part, t, raw);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      cols_stage_f32<B>(pr, t, h, raw[h], lds);
+      if constexpr (ACT) cols_act<B>(pr, part, t, h, ad[h], az[h], sum, raw[0]);
+      cols_stage_f32<B>(pr, t, h, raw[ACT ? 0 : h], lds);
       __syncthreads();
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
@@ -732,6 +844,7 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       }
       if (h == 0) __syncthreads();  // round 1 overwrites the LDS tile
     }
+    if constexpr (ACT && !REPAIR) cols_db(pr, c0, part, t, sum);
   } else {
     cols_load<B>(pr, c0, part, t, lds);
     __syncthreads();
@@ -855,7 +968,8 @@ struct FqBatch {
 
 // SR: stochastic rounding of the dY codes (the W and X codes are rounded to nearest).
 // REPAIR: the follow-up launch of the column passes (rows tasks excluded from its grid).
-template <int B, int QG, int QW, bool SR, bool REPAIR = false>
+// ACT: dY's passes take dz = dy act'(z).
+template <int B, int QG, int QW, bool SR, bool REPAIR = false, bool ACT = false>
 __global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
   extern __shared__ __attribute__((aligned(16))) uint4 lds[];
   if constexpr (REPAIR) {
@@ -868,7 +982,7 @@ __global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
       __syncthreads();  // the next task overwrites the LDS tile
     }
     for (int64_t t = blockIdx.x; t < fb.end_dy - fb.end_w; t += gridDim.x) {
-      cols_task<B, QG, SR, true>(fb.cdy, t, lds);
+      cols_task<B, QG, SR, true, ACT, ACT>(fb.cdy, t, lds);
       __syncthreads();
     }
     for (int64_t t = blockIdx.x; t < fb.end_x - fb.end_dy; t += gridDim.x) {
@@ -881,11 +995,11 @@ __global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
   if (bid < fb.end_w) {
     cols_task<B, QW, false>(fb.cw, bid, lds);
   } else if (bid < fb.end_dy) {
-    cols_task<B, QG, SR>(fb.cdy, bid - fb.end_w, lds);
+    cols_task<B, QG, SR, false, ACT, ACT>(fb.cdy, bid - fb.end_w, lds);
   } else if (bid < fb.end_x) {
     cols_task<B, QW, false>(fb.cx, bid - fb.end_dy, lds);
   } else {
-    rows_wave<uint16_t, B, QG, SR>(fb.rows, (bid - fb.end_x) * 16 + (threadIdx.x >> 6),
+    rows_wave<uint16_t, B, QG, SR, ACT>(fb.rows, (bid - fb.end_x) * 16 + (threadIdx.x >> 6),
                                    threadIdx.x & 63);
   }
 }
@@ -1029,12 +1143,12 @@ static hipError_t cols2_block(const FqArgs& a0, void* ws0, const FqArgs* a1, voi
 // backward batch
 // ---------------------------------------------------------------------------
 
-template <int B, int QG, int QW, bool SR>
+template <int B, int QG, int QW, bool SR, bool ACT = false>
 static hipError_t launch_batch_t(const FqArgs* rows, const FqArgs& cw, void* ws_w,
                                  const FqArgs& cdy, void* ws_dy, const FqArgs& cx, void* ws_x,
                                  hipStream_t st) {
-  auto* fn = &fq_batch_kernel<B, QG, QW, SR>;
-  hipError_t e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR>>(kColsLdsBytes);
+  auto* fn = &fq_batch_kernel<B, QG, QW, SR, false, ACT>;
+  hipError_t e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, false, ACT>>(kColsLdsBytes);
   if (e != hipSuccess) return e;
   FqBatch fb{};
   int64_t tw = 0, tdy = 0, tx = 0, scratch = 0;
@@ -1061,16 +1175,16 @@ static hipError_t launch_batch_t(const FqArgs* rows, const FqArgs& cw, void* ws_
     fb.cdy.gs = cols2_group(fb.cdy.P, cap);
     fb.cx.gs = cols2_group(fb.cx.P, cap);
   }
-  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR>), dim3((unsigned)grid), dim3(1024),
+  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, false, ACT>), dim3((unsigned)grid), dim3(1024),
                      kColsLdsBytes, st, fb);
   e = hipGetLastError();
   if (e != hipSuccess || P == 1) return e;
   // the repair launch over the column tasks (see launch_cols2_t)
-  e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, true>>(kColsLdsBytes);
+  e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, true, ACT>>(kColsLdsBytes);
   if (e != hipSuccess) return e;
   const int cap = cols2_capacity(reinterpret_cast<const void*>(fn));
   const int64_t rgrid = fb.end_x < cap ? fb.end_x : cap;
-  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, true>), dim3((unsigned)rgrid),
+  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, true, ACT>), dim3((unsigned)rgrid),
                      dim3(1024), kColsLdsBytes, st, fb);
   return hipGetLastError();
 }

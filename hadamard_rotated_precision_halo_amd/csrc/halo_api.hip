@@ -414,12 +414,37 @@ halo_status check_bwd(const void* dy, halo_dtype rot_type, const void* x, const 
   return HALO_OK;
 }
 
+// The activation whose gradient the backward's dY passes take in (fused into their loads).
+struct ActGrad {
+  const void* z = nullptr;
+  int act = 0;
+  void* db = nullptr;    // bf16 [n] or NULL
+  float* part = nullptr; // scratch of its partial sums
+};
+
+// Whether the backward forms dz = dy act'(z) inside its rotation passes: the one-launch batch of
+// bf16 passes, both products, nearest rounding.
+bool act_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
+                  halo_dtype q_type, halo_dtype grad_q_type, const void* dx, const void* dw,
+                  const halo_linear_opts* opts) {
+  const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
+  const WsPlan p = plan_ws(m, n, k, 1, block);
+  return dx && dw && io_type == HALO_BF16 && fq_act_block_ok(block) &&
+         !(opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC) &&
+         fq_rows2_supported(nq, block) && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
+         fq_cols2_supported(mq, n, block, 1, false, p.scr_dy) &&
+         fq_cols2_supported(mq, k, block, 1, false, p.scr_x) &&
+         act_grad_parts(m, n) >= (fq_act_parts(mq, block) > 1 ? fq_act_parts(mq, block) : 1);
+}
+
 // The layer backward on validated arguments: the rotation passes of dY (of type dy_type), W and X
 // (io_type), then the products.  ws holds plan_ws(m, n, k, 1, block).total bytes.
+// act: NULL, or the activation dY's passes take in (act_fused_ok).
 halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const void* w,
                     halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
                     halo_dtype q_type, halo_dtype grad_q_type, void* dx, void* dw,
-                    const halo_linear_opts* opts, void* ws, hipStream_t st) {
+                    const halo_linear_opts* opts, void* ws, hipStream_t st,
+                    const ActGrad* act = nullptr) {
   const WsPlan p = plan_ws(m, n, k, 1, block);
   const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
   char* base = static_cast<char*>(ws);
@@ -453,10 +478,18 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
   void* qxt = base + p.off[6];
   float* sxt = reinterpret_cast<float*>(base + p.off[7]);
   // dX = dY W: rows of dY and columns of W along n; dW = dY^T X: columns of dY and X along m
-  const FqArgs rows = make_fq(dy, m, n, n, HALO_ALONG_ROWS, block, grad_q_type, qdy, nq, sdy, gn, nq);
+  FqArgs rows = make_fq(dy, m, n, n, HALO_ALONG_ROWS, block, grad_q_type, qdy, nq, sdy, gn, nq);
   const FqArgs cw = make_fq(w, n, k, k, HALO_ALONG_COLS, block, q_type, qwt, nq, swt, on, nq);
-  const FqArgs cdy = make_fq(dy, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
+  FqArgs cdy = make_fq(dy, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
   const FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
+
+  const int64_t db_parts = act ? fq_act_parts(mq, block) : 0;
+  if (act) {
+    rows.z = cdy.z = static_cast<const uint16_t*>(act->z);
+    rows.act = cdy.act = act->act;
+    if (act->db && db_parts == 1) cdy.db = static_cast<uint16_t*>(act->db);
+    if (act->db && db_parts > 1) cdy.db_part = act->part;
+  }
 
   // the single-read column passes need their scratch cleared: folded into the first kernel
   // when that is a rows pass, else one fill
@@ -486,7 +519,8 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
         pp.nzero = (int64_t)(p.scratch_bytes / 4);
         zero_pending = false;
       }
-      s = from_hip(launch_fq_rows2_pair(pp, inb_dy, qt_index(grad_q_type), st));
+      s = from_hip(act ? launch_fq_rows2_act(pp, qt_index(grad_q_type), st)
+                       : launch_fq_rows2_pair(pp, inb_dy, qt_index(grad_q_type), st));
     } else {
       s = run_fa(rows, dy_type, HALO_ALONG_ROWS, grad_q_type, nullptr, 0, st);
     }
@@ -506,8 +540,10 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
       clear_scratch();
     }
     if (s == HALO_OK)
-      s = from_hip(launch_fq_batch(rows_in ? &rows : nullptr, cw, scr_w, cdy, scr_dy, cx, scr_x,
-                                   qg, qw, st));
+      s = from_hip((act ? launch_fq_batch_act : launch_fq_batch)(
+          rows_in ? &rows : nullptr, cw, scr_w, cdy, scr_dy, cx, scr_x, qg, qw, st));
+    if (s == HALO_OK && cdy.db_part)
+      s = from_hip(launch_part_sum(cdy.db_part, db_parts, n, static_cast<uint16_t*>(act->db), st));
   } else {
     if (dx) rows_pass();
     clear_scratch();
@@ -1036,6 +1072,15 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
   char* tail = static_cast<char*>(ws) + plan_ws(m, n, k, 1, block).total;
   float* dz = reinterpret_cast<float*>(tail);
   float* part = reinterpret_cast<float*>(tail + round256((size_t)m * n * 4));
+  if (act && act_fused_ok(io_type, m, n, k, block, q_type, grad_q_type, dx, dw, opts)) {
+    ActGrad ag;
+    ag.z = z;
+    ag.act = (int)activation;
+    ag.db = db;
+    ag.part = part;
+    return run_bwd(dy, io_type, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw, opts, ws,
+                   st, &ag);
+  }
   if (act || db) {
     const hipError_t e = launch_act_grad(dy, z, (int)activation, io_type == HALO_BF16 ? 1 : 0, m, n,
                                          act ? dz : nullptr, db, part, st);

@@ -30,6 +30,14 @@ struct FqArgs {
   uint32_t ctr2, ctr3;    // Philox counter words 2 and 3 (word 0: position / 4, word 1: vector)
   uint32_t polls;         // columns passes that exchange maxima: polls of a waiting task
                           // before it stops waiting (0: the default, 2^20)
+  // activation-gradient passes only (launch_fq_*_act): the input is dy = x and the vectors rotated
+  // are those of dz = dy act'(z), z [rows x cols] with x's leading dimension (bf16); db_part: the
+  // columns pass's sums of dz over each task's rows, [parts x nvec] fp32, or, where a task holds
+  // whole columns and db is not NULL, db [nvec] bf16 itself
+  const uint16_t* z;
+  int act;
+  float* db_part;
+  uint16_t* db;
 };
 
 // in_bf16: 1 for bf16 input, 0 for fp32.  qt: 0 INT8, 1 E4M3, 2 E5M2, 3 fp32 values.
@@ -55,6 +63,15 @@ bool fq_batch_rows_ok(int64_t len);
 hipError_t launch_fq_batch(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
                            void* ws_dy, const FqArgs& cx, void* ws_x, int qg, int qw,
                            hipStream_t st);
+
+// The same with dY's passes taken from dy and z (see FqArgs::z), nearest rounding, blocks
+// fq_act_block_ok: the rows of dz (NULL, or fq_batch_rows_ok(len)) and the columns of W, dz and X
+// in one launch; and the rows of dz alone.  fq_act_parts: rows of db_part (1: whole columns).
+bool fq_act_block_ok(int block);
+int64_t fq_act_parts(int64_t rows, int block);
+hipError_t launch_fq_batch_act(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
+                               void* ws_dy, const FqArgs& cx, void* ws_x, int qg, int qw,
+                               hipStream_t st);
 
 // Both passes of one bf16 matrix from a single read (fwht_dual.hip): the rows pass ar and
 // the columns pass ac of the same x (same block and code type qt), with one scratch whose
@@ -84,6 +101,7 @@ struct FqPair {
   int64_t nzero;
 };
 hipError_t launch_fq_rows2_pair(const FqPair& a, int in_bf16, int qt, hipStream_t st);
+hipError_t launch_fq_rows2_act(const FqPair& a, int qt, hipStream_t st);
 
 // Up to two single-read column passes over columns of the same length, block, input type
 // (in_bf16) and code type in one launch (a1 may be NULL).  prezeroed: the scratch of both was
@@ -134,6 +152,9 @@ hipError_t launch_skinny_fused(const GemmArgs& g, const FqArgs& f, int in_bf16, 
 // dz = dy act'(z) in fp32 and, when db is not NULL, db = its sums over the m rows (bias type:
 // that of dy).  part: act_grad_parts(m, n) x n floats of scratch (db only).
 int64_t act_grad_parts(int64_t m, int64_t n);
+// db (bf16) = the sum of `parts` rows of part, in order.
+hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t* db,
+                           hipStream_t st);
 hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
                            int64_t n, float* dz, void* db, float* part, hipStream_t st);
 

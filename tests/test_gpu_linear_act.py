@@ -283,3 +283,36 @@ def test_serving_form_equals_the_forward(m, n, k, block, dt, q):
     if signs is not None:
         y = H.linear_act_fwd(x, w, block, q, activation="relu")
         check_fwd(x, w, block, q, "relu", None, None, y, None, dt)
+
+
+@pytest.mark.parametrize("q,gq", [(I8, I8), (E4M3, E5M2)])
+@pytest.mark.parametrize("act", ["silu", "gelu_erf"])
+@pytest.mark.parametrize("m,n,k,block", [(256, 512, 256, 64), (4096, 64, 72, 1024), (128, 4096, 64, 128),
+                                         (8192, 200, 64, 256), (5120, 520, 136, 512),
+                                         (2000, 8192, 128, 128), (64, 12288, 64, 64),
+                                         (448, 640, 64, 64), (1000, 1000, 256, 256)])
+def test_backward_inside_the_rotations(m, n, k, block, act, q, gq):
+    # shapes whose dz is formed as the rotation passes load it (whole columns, columns split over
+    # workgroups, rows of one and of several waves, padded ends) against the same passes of an fp32
+    # dz, and against the form that stores dz (random signs of a zero word: the same transform)
+    print(f"m {m} n {n} k {k} block {block} {act} {q}", flush=True)
+    x, w = rnd((m, k), BF16, 1), rnd((n, k), BF16, 2, k ** -0.5)
+    z, dy = rnd((m, n), BF16, 3, 1.5), rnd((m, n), BF16, 4, 1e-3)
+    z[0, :4], dy[-1] = 30.0, 0.0
+    sn = torch.randint(-2 ** 31, 2 ** 31, (-(-H.contraction_len(n, block) // 32),), dtype=torch.int32).to(DEV)
+    sm = torch.randint(-2 ** 31, 2 ** 31, (-(-H.contraction_len(m, block) // 32),), dtype=torch.int32).to(DEV)
+    dz = dy.double() * slope64(z.double(), act)
+    for kw in ({}, {"signs_n": sn, "signs_m": sm}):
+        dx, dw, db = H.linear_act_bwd(dy, z, x, w, block, q, gq, activation=act, **kw)
+        tol = ROUND[BF16] * 1.01 * dz.sum(0).abs() + 2100 * U * dz.abs().sum(0)
+        assert ((db.double() - dz.sum(0)).abs() <= tol).all()
+        rx, rw = H.linear_bwd(dz.float(), x.float(), w.float(), block, q, gq, **kw)
+        for got, ref, name in ((dx, rx, "dx"), (dw, rw, "dw")):
+            rel = float((got.double() - ref.double()).norm() / ref.double().norm())
+            assert rel <= ROUND[BF16] / 3 ** 0.5 + 1e-3, (name, rel)
+        again = H.linear_act_bwd(dy, z, x, w, block, q, gq, activation=act, **kw)
+        only = H.linear_act_bwd(dy, z, x, w, block, q, gq, activation=act, want_dx=False, **kw)
+        for u, v in zip(again, (dx, dw, db)):
+            assert torch.equal(u, v)
+        rel = float((only[1].double() - dw.double()).norm() / dw.double().norm())
+        assert rel <= 1e-3   # the stored dz: the same fp32 values, the same codes
