@@ -68,6 +68,22 @@ __device__ __forceinline__ uint4 get_once(const T* row, int at) {
   else return load16u_nt(row + at);
 }
 
+// 16 bytes at offset off of a row of row_bytes bytes (16-byte aligned, the same for the wave) through
+// a buffer resource over the row: zeros past its end, and a store there is dropped.  Loads past the
+// caches, as get_once.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* row, uint32_t row_bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, (int)row_bytes, 0x00020000);
+}
+__device__ __forceinline__ uint4 buffer_load16(const void* row, uint32_t row_bytes, uint32_t off) {
+  const auto w = __builtin_amdgcn_raw_buffer_load_b128(row_rsrc(row, row_bytes), (int)off, 0, 2);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void buffer_store16(void* row, uint32_t row_bytes, uint32_t off, uint4 v) {
+  typedef unsigned v4u __attribute__((ext_vector_type(4)));
+  const v4u w = {v.x, v.y, v.z, v.w};
+  __builtin_amdgcn_raw_buffer_store_b128(w, row_rsrc(row, row_bytes), (int)off, 0, 0);
+}
+
 template <typename T, int VEC>
 __device__ __forceinline__ void val(uint4 w, float* o) {
   if constexpr (VEC == 1) o[0] = sizeof(T) == 2 ? __uint_as_float(w.x << 16) : __uint_as_float(w.x);
@@ -272,23 +288,25 @@ struct NormPlan {
 
 // Waves per token and chunks per lane of the backward for a row of `chunks` chunks: two chunks per
 // lane and as many waves as that takes, so that few lanes idle whatever the width (8192 x 4096
-// and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us);
-// 16 waves of two or four for the widest rows.
+// and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us).
+// Rows of more than 16 x 64 chunks (nw 0) go by column strips, see norm_strip_kernel.
 void bwd_shape(int64_t chunks, int* nw, int* ch) {
   const int64_t per = (chunks + 63) / 64;
-  *ch = per <= 1 ? 1 : per <= 32 ? 2 : 4;
-  *nw = per <= 16 ? (int)((per + 1) / 2) : 16;
+  *ch = per <= 1 ? 1 : 2;
+  *nw = per <= 16 ? (int)((per + 1) / 2) : 0;
 }
 // Teams of a workgroup: about 8 waves together, whose lanes then have 256 registers each.
-constexpr int bwd_teams(int nw) { return nw <= 8 ? 8 / nw : 1; }
+constexpr int bwd_teams(int nw) { return 8 / nw; }
+constexpr int kStripTeams = 4;
 
-NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
+// wgs: the workgroups to aim at.
+NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams, int64_t wgs) {
   NormPlan p{};
-  // one workgroup per compute unit: its teams keep enough rows in flight (each prefetches its
-  // next row), and the partial sums, one row per workgroup, stay few (8192 x 4096 bf16: 96.8 us
+  // whole rows: one workgroup per compute unit, whose teams keep enough rows in flight (each
+  // prefetches its next row), so that the partial sums, one row per workgroup, stay few (8192 x 4096 bf16: 96.8 us
   // with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9 us, each before
   // the loop lost its branches)
-  int64_t rows = (tokens + 255) / 256;
+  int64_t rows = (tokens + wgs - 1) / wgs;
   if (rows < teams) rows = teams;
   if (group_len * teams <= rows) {
     p.whole_groups = rows / group_len;
@@ -305,32 +323,81 @@ NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams) {
   return p;
 }
 
-// FULL: every optional input is there (the gate may be missing: ones), so the loop over the rows
-// has no branch on them and its loads and stores stay in flight across it; otherwise each is
-// looked up.
-template <typename T, int VEC, bool ODD, int NW, int CH, bool FULL>
+// The rows of a team in workgroup `wg`'s range (nrows from row0 on), one per iteration: whole
+// groups: team q takes groups q, q + teams, ..; else rows q, q + teams, ...
+struct TeamRows {
+  int64_t row0, nrows, iters, row, in_group, group_len;
+  int teams;
+  bool whole;
+  // token of the current row; the range's first where there is none
+  __device__ __forceinline__ int64_t token() const { return row0 + (row < nrows ? row : 0); }
+  __device__ __forceinline__ bool live() const { return row < nrows; }
+  __device__ __forceinline__ bool first_of_group() const { return whole && in_group == 0; }
+  __device__ __forceinline__ bool last_of_group() const { return whole && in_group == group_len - 1; }
+  __device__ __forceinline__ void advance() {
+    if (!whole) {
+      row += teams;
+    } else {
+      const bool wrap = ++in_group == group_len;
+      row += wrap ? (teams - 1) * group_len + 1 : 1;
+      in_group = wrap ? 0 : in_group;
+    }
+  }
+};
+__device__ __forceinline__ TeamRows team_rows(const NormBwdArgs& a, const NormPlan& pn, int teams,
+                                              int team, int64_t wg) {
+  TeamRows r;
+  r.group_len = a.group_len;
+  r.teams = teams;
+  r.whole = pn.whole_groups > 0;
+  r.in_group = 0;
+  if (r.whole) {
+    const int64_t groups = a.tokens / a.group_len;
+    const int64_t g0 = wg * pn.whole_groups, ng = min(pn.whole_groups, groups - g0);
+    r.row0 = g0 * a.group_len;
+    r.nrows = ng * a.group_len;
+    r.iters = (ng + teams - 1) / teams * a.group_len;
+    r.row = team * a.group_len;
+  } else {
+    const int64_t group = wg / pn.chunks_per_group, c = wg % pn.chunks_per_group;
+    r.row0 = group * a.group_len + c * pn.rows_per_wg;
+    r.nrows = min(pn.rows_per_wg, a.group_len - c * pn.rows_per_wg);
+    r.iters = (r.nrows + teams - 1) / teams;
+    r.row = team;
+  }
+  return r;
+}
+
+// FAST: every optional input is there (the gate may be missing: ones) and every row starts on 16
+// bytes.  Loads and stores then go through buffer resources of one row, which give zeros (that add
+// nothing) past its end and drop what is stored there, or of no bytes where a team has no row: the
+// loop has no branch around a memory access, and no wait covers more than the row it needs.
+// WHOLE: the plan's whole groups, whose gate rows are loaded with each row.
+template <typename T, int VEC, bool ODD, int NW, int CH, bool FAST, bool WHOLE>
 __global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormBwdArgs a,
-                                                                               NormPlan pn) {
+                                                                           NormPlan pn) {
   constexpr int TEAMS = bwd_teams(NW), WAVES = NW * TEAMS;
   __shared__ float s_red[2][3][WAVES];
   extern __shared__ float s_fold[];  // TEAMS > 1: (TEAMS - 1) x (columns) x 3 floats, see below
-  const int wave = threadIdx.x >> 6, team = wave / NW;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / NW;
   const int tl = threadIdx.x - team * NW * 64;
   const int d = a.dim;
   const T* gate = reinterpret_cast<const T*>(a.gate);
   const T* post = reinterpret_cast<const T*>(a.post);
   const T* pre = reinterpret_cast<const T*>(a.pre);
-  const bool has_in = FULL || a.dr_out, has_pre = FULL || pre, has_y = FULL || a.y,
-             has_post = FULL || post;
+  const bool has_in = FAST || a.dr_out, has_pre = FAST || pre, has_y = FAST || a.y,
+             has_post = FAST || post;
 
   Place<VEC> pl[CH];
+  uint32_t off[CH];  // byte offset of a chunk in its row (FAST; past the row for idle lanes)
 #pragma unroll
-  for (int j = 0; j < CH; ++j) pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
+  for (int j = 0; j < CH; ++j) {
+    pl[j] = place_of<VEC, ODD>(j * NW * 64 + tl, d);
+    off[j] = (uint32_t)(j * NW * 64 + tl) * (uint32_t)(VEC * sizeof(T));
+  }
+  const uint32_t row_bytes = (uint32_t)d * (uint32_t)sizeof(T);
   // A lane keeps its weights in their stored form and has the next row's loads in flight while a
-  // row is reduced and stored.  In the widest rows a lane of several chunks has not the registers:
-  // it loads a chunk and its weights when it needs them, and once more (from the caches) after
-  // the reduction.
-  constexpr bool AHEAD = NW < 16;
+  // row is reduced and stored.
   const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
   const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
   const uint4 ones4 = make_uint4(one, one, one, one);
@@ -340,106 +407,60 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormB
   for (int j = 0; j < CH; ++j)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) spost[j][e] = spre[j][e] = sgate[j][e] = 0.f;
-  auto load_weights = [&](int64_t t, int j) __attribute__((always_inline)) {
-    wpost[j] = has_post ? get<T, VEC>(post, pl[j].at) : ones4;
-    wpre[j] = has_pre ? get<T, VEC>(pre, pl[j].at) : ones4;
-    wgate[j] = gate ? get<T, VEC>(gate + t / a.group_len * a.ldg, pl[j].at) : ones4;
-  };
 
-  // the team's rows
-  int64_t row0, nrows, step, iters;
-  if (pn.whole_groups > 0) {
-    const int64_t groups = a.tokens / a.group_len;
-    const int64_t g0 = (int64_t)blockIdx.x * pn.whole_groups;
-    const int64_t ng = min(pn.whole_groups, groups - g0);
-    row0 = g0 * a.group_len;
-    nrows = ng * a.group_len;
-    step = 0;
-    iters = (ng + TEAMS - 1) / TEAMS * a.group_len;
-  } else {
-    const int64_t group = (int64_t)blockIdx.x / pn.chunks_per_group;
-    const int64_t c = (int64_t)blockIdx.x % pn.chunks_per_group;
-    row0 = group * a.group_len + c * pn.rows_per_wg;
-    nrows = min(pn.rows_per_wg, a.group_len - c * pn.rows_per_wg);
-    step = TEAMS;
-    iters = (nrows + TEAMS - 1) / TEAMS;
-  }
-  // row of iteration `it` within the workgroup's range
-  auto row_of = [&](int64_t it) -> int64_t {
-    if (step > 0) return it * step + team;
-    // whole groups: team q takes groups q, q + TEAMS, ...
-    return (it / a.group_len * TEAMS + team) * a.group_len + it % a.group_len;
-  };
-  auto token_of = [&](int64_t it) {
-    const int64_t off = it < iters ? row_of(it) : 0;
-    return row0 + (off < nrows ? off : 0);
-  };
+  TeamRows now = team_rows(a, pn, TEAMS, team, blockIdx.x);
+  TeamRows then = now;  // one row ahead
+  const int64_t iters = now.iters;
   struct Row {
-    uint4 g, h, r, y;
+    uint4 g, h, r, y, w;
   };
-  // chunk j of row t (once: past the caches); lanes past the row get zeros, which add nothing
-  auto load = [&](int64_t t, int j, bool once, Row& w) __attribute__((always_inline)) {
-    const int at = pl[j].at;
-    auto part = [&](const void* base, int64_t ld) {
-      const T* p = reinterpret_cast<const T*>(base) + t * ld;
-      return once ? get_once<T, VEC, ODD>(p, at) : get<T, VEC>(p, at);
-    };
-    w.g = has_in ? part(a.dr_out, a.lddro) : zero4;
-    w.h = has_pre ? part(a.dh, a.lddh) : zero4;
-    w.r = has_pre ? part(a.r_out, a.ldro) : zero4;
-    w.y = has_y ? part(a.y, a.ldy) : zero4;
+  auto part = [&](const void* base, int64_t ld, int64_t t, int j) __attribute__((always_inline)) {
+    const T* row = reinterpret_cast<const T*>(base) + t * ld;
+    if constexpr (FAST) return buffer_load16(row, row_bytes, off[j]);
+    else return get_once<T, VEC, ODD>(row, pl[j].at);
   };
   Row cur[CH], nxt[CH];
   float nb = 0.f, na = 1.f;
-  auto ahead = [&](int64_t it) __attribute__((always_inline)) {
-    const int64_t t = token_of(it);
+  auto ahead = [&]() __attribute__((always_inline)) {
+    const int64_t t = then.token();
     if (has_pre) nb = a.rstd_pre[t];
     if (has_post) na = a.rstd_post[t];
 #pragma unroll
-    for (int j = 0; j < CH; ++j) load(t, j, true, nxt[j]);
-  };
-  if constexpr (AHEAD) {
-#pragma unroll
-    for (int j = 0; j < CH; ++j) load_weights(row0, j);
-    ahead(0);
-  }
-  for (int64_t it = 0; it < iters; ++it) {
-    const bool live = row_of(it) < nrows;
-    const int64_t t = token_of(it);
-    float b, ar;
-    if constexpr (AHEAD) {
-      if (step == 0 && gate && it % a.group_len == 0) {
-#pragma unroll
-        for (int j = 0; j < CH; ++j)
-          wgate[j] = get<T, VEC>(gate + t / a.group_len * a.ldg, pl[j].at);
-      }
-      keep_raw(wpost);
-      keep_raw(wpre);
-      keep_raw(wgate);
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        cur[j].g = pl[j].in ? nxt[j].g : zero4;
-        cur[j].h = pl[j].in ? nxt[j].h : zero4;
-        cur[j].r = pl[j].in ? nxt[j].r : zero4;
-        cur[j].y = pl[j].in ? nxt[j].y : zero4;
-      }
-      b = nb;
-      ar = na;
-      ahead(it + 1);
-    } else {
-      b = has_pre ? a.rstd_pre[t] : 0.f;
-      ar = has_post ? a.rstd_post[t] : 1.f;
+    for (int j = 0; j < CH; ++j) {
+      nxt[j].g = has_in ? part(a.dr_out, a.lddro, t, j) : zero4;
+      nxt[j].h = has_pre ? part(a.dh, a.lddh, t, j) : zero4;
+      nxt[j].r = has_pre ? part(a.r_out, a.ldro, t, j) : zero4;
+      nxt[j].y = has_y ? part(a.y, a.ldy, t, j) : zero4;
+      if (WHOLE)
+        nxt[j].w = gate ? get<T, VEC>(gate + t / a.group_len * a.ldg, pl[j].at) : ones4;
     }
+    then.advance();
+  };
+#pragma unroll
+  for (int j = 0; j < CH; ++j) {
+    wpost[j] = has_post ? get<T, VEC>(post, pl[j].at) : ones4;
+    wpre[j] = has_pre ? get<T, VEC>(pre, pl[j].at) : ones4;
+    wgate[j] = gate ? get<T, VEC>(gate + now.token() / a.group_len * a.ldg, pl[j].at) : ones4;
+  }
+  ahead();
+  for (int64_t it = 0; it < iters; ++it) {
+    const bool live = now.live();
+    const int64_t t = now.token();
+    keep_raw(wpost);
+    keep_raw(wpre);
+    keep_raw(wgate);
+#pragma unroll
+    for (int j = 0; j < CH; ++j) {
+      cur[j] = nxt[j];
+      if (WHOLE) wgate[j] = nxt[j].w;
+      if (!FAST && !pl[j].in) cur[j].g = cur[j].h = cur[j].r = cur[j].y = zero4;
+    }
+    const float b = nb, ar = na;
+    ahead();
     // the three sums: m1 = sum u rhat, A = sum c yhat (dr' + b u), B = sum c yhat b rhat
     float m1 = 0.f, sa = 0.f, sb = 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      if constexpr (!AHEAD) {
-        __builtin_amdgcn_sched_barrier(0);  // one chunk's registers at a time
-        load(t, j, false, cur[j]);
-        load_weights(t, j);
-        if (!pl[j].in) cur[j].h = cur[j].y = zero4;
-      }
       float g[VEC], u[VEC], rv[VEC], yv[VEC], wp[VEC], wq[VEC], wg[VEC];
       val<T, VEC>(cur[j].g, g);
       val<T, VEC>(cur[j].h, u);
@@ -492,26 +513,18 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormB
     m1 *= a.inv_dim;
     const float bm = b * m1;
     const float m2 = has_post ? (sa - m1 * sb) * a.scale * a.inv_dim : 0.f;
-    if constexpr (AHEAD) {
-      keep_raw(wpost);
-      keep_raw(wpre);
-      keep_raw(wgate);
-    }
+    keep_raw(wpost);
+    keep_raw(wpre);
+    keep_raw(wgate);
     T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
     T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
     const float on = live ? 1.f : 0.f;
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
-      if constexpr (!AHEAD) {
-        __builtin_amdgcn_sched_barrier(0);
-        load(t, j, false, cur[j]);
-        load_weights(t, j);
-      } else {
-        keep_raw1(cur[j].g);
-        keep_raw1(cur[j].h);
-        keep_raw1(cur[j].r);
-        keep_raw1(cur[j].y);
-      }
+      keep_raw1(cur[j].g);
+      keep_raw1(cur[j].h);
+      keep_raw1(cur[j].r);
+      keep_raw1(cur[j].y);
       float g[VEC], u[VEC], rv[VEC], yv[VEC], wp[VEC], wq[VEC], wg[VEC], o[VEC];
       val<T, VEC>(cur[j].g, g);
       val<T, VEC>(cur[j].h, u);
@@ -531,33 +544,35 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormB
         spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
         o[e] = ar * __builtin_fmaf(-m2, yhat, sG * wg[e] * wp[e]);
       }
-      // where a row is loaded again its chunks do not store each other's elements: dr may be
-      // dr_out or dh
-      const int from = AHEAD ? 0 : pl[j].from;
-      if (live && pl[j].in) {
-        put_own<T, VEC>(dr, pl[j].at, from, g);
-        if (has_y) put_own<T, VEC>(dy, pl[j].at, from, o);
+      if constexpr (FAST) {
+        buffer_store16(dr, live ? row_bytes : 0u, off[j], pack16<T>(g));
+        buffer_store16(dy, live ? row_bytes : 0u, off[j], pack16<T>(o));
+      } else if (live && pl[j].in) {
+        put<T, VEC>(dr, pl[j].at, g);
+        if (has_y) put<T, VEC>(dy, pl[j].at, o);
       }
     }
-    // whole groups: the group's last row writes its gate gradient
-    if (step == 0 && it % a.group_len == a.group_len - 1) {
-      if (a.dgate && live) {
-        T* dg = reinterpret_cast<T*>(a.dgate) + (t / a.group_len) * (int64_t)d;
+    if (WHOLE) {  // the group's last row writes its gate gradient
+      const bool last = now.last_of_group();
+      const bool put_gate = last && live && a.dgate;
+      T* dg = reinterpret_cast<T*>(a.dgate) + t / a.group_len * (int64_t)d;
 #pragma unroll
-        for (int j = 0; j < CH; ++j)
-          if (pl[j].in) put<T, VEC>(dg, pl[j].at, sgate[j]);
+      for (int j = 0; j < CH; ++j) {
+        if constexpr (FAST)
+          buffer_store16(dg, put_gate ? row_bytes : 0u, off[j], pack16<T>(sgate[j]));
+        else if (put_gate && pl[j].in)
+          put<T, VEC>(dg, pl[j].at, sgate[j]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) sgate[j][e] = last ? 0.f : sgate[j][e];
       }
-#pragma unroll
-      for (int j = 0; j < CH; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) sgate[j][e] = 0.f;
     }
+    now.advance();
   }
   // fold the teams: team q's sums are added in team order, one sum at a time, through
   // (TEAMS - 1) x 64 NW CH VEC floats of LDS, and the workgroup's partial rows are written
   constexpr int COLS = NW * 64 * CH * VEC;
   const bool want[3] = {a.part_post != nullptr, a.part_pre != nullptr,
-                        a.part_gate != nullptr && step > 0};
+                        a.part_gate != nullptr};
   float* out[3] = {a.part_post, a.part_pre, a.part_gate};
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
@@ -632,7 +647,7 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(NormBwdArgs a, NormPlan 
 struct BwdLayout {
   NormPlan plan;
   int nw, ch, vec;
-  size_t post, pre, gate, total;  // byte offsets of the partial rows
+  size_t post, pre, gate, stats, total;  // byte offsets of the partial rows and row statistics
 };
 
 BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16, bool post,
@@ -641,13 +656,199 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
   l.vec = in_bf16 ? 8 : 4;
   if (dim < l.vec) l.vec = 1;
   bwd_shape((dim + l.vec - 1) / l.vec, &l.nw, &l.ch);
-  l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw));
+  if (l.nw > 0) {
+    l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw), 256);
+  } else {
+    const int64_t strips = (dim + 64 * l.vec - 1) / (64 * l.vec);
+    l.plan = plan_bwd(tokens, group_len, kStripTeams, (1024 + strips - 1) / strips);
+  }
   const size_t rows = (size_t)l.plan.wgs * (size_t)dim * 4;
   l.post = 0;
   l.pre = post ? rows : 0;
   l.gate = l.pre + (pre ? rows : 0);
-  l.total = l.gate + (gate && l.plan.whole_groups == 0 ? rows : 0);
+  l.stats = l.gate + (gate && l.plan.whole_groups == 0 ? rows : 0);
+  l.total = l.stats + (l.nw == 0 ? (size_t)tokens * 8 : 0);
   return l;
+}
+
+// The widest rows, which a workgroup's registers do not hold beside their columns' sums: a first
+// launch reduces each row to the two numbers that its gradient needs, bm = b mean(u rhat) and the
+// mean m2 of dy's formula; a second takes strips of 64 chunks, a wave per row of a strip, and does
+// the rest (2048 x 16384 bf16: see the launcher).  Only the second stores, so dr and dy may be
+// inputs as before; a moved-back chunk's shared elements are another workgroup's and not stored.
+template <typename T, int VEC, bool ODD>
+__global__ __launch_bounds__(512) void norm_stats_kernel(NormBwdArgs a) {
+  constexpr int WAVES = 8;
+  __shared__ float s_red[3][WAVES];
+  const int64_t t = blockIdx.x;
+  const T* dr_out = reinterpret_cast<const T*>(a.dr_out) + t * a.lddro;
+  const T* dh = reinterpret_cast<const T*>(a.dh) + t * a.lddh;
+  const T* r = reinterpret_cast<const T*>(a.r_out) + t * a.ldro;
+  const T* y = reinterpret_cast<const T*>(a.y) + t * a.ldy;
+  const T* gate = reinterpret_cast<const T*>(a.gate) + (a.gate ? t / a.group_len * a.ldg : 0);
+  const T* post = reinterpret_cast<const T*>(a.post);
+  const T* pre = reinterpret_cast<const T*>(a.pre);
+  const float b = a.pre ? a.rstd_pre[t] : 0.f, ar = a.post ? a.rstd_post[t] : 1.f;
+  float m1 = 0.f, sa = 0.f, sb = 0.f;
+  for (int c = threadIdx.x; c * VEC < a.dim; c += 64 * WAVES) {
+    const Place<VEC> p = place_of<VEC, ODD>(c, a.dim);
+    float g[VEC] = {}, u[VEC] = {}, rv[VEC] = {}, cy[VEC] = {}, w[VEC];
+    if (a.dr_out) val<T, VEC>(get<T, VEC>(dr_out, p.at), g);
+    if (a.pre) {
+      val<T, VEC>(get<T, VEC>(dh, p.at), u);
+      val<T, VEC>(get<T, VEC>(r, p.at), rv);
+      val<T, VEC>(get<T, VEC>(pre, p.at), w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) u[e] *= w[e];
+    }
+    if (a.post) {
+      val<T, VEC>(get<T, VEC>(y, p.at), cy);
+      val<T, VEC>(get<T, VEC>(post, p.at), w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) cy[e] *= ar * w[e];
+      if (a.gate) {
+        val<T, VEC>(get<T, VEC>(gate, p.at), w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) cy[e] *= w[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (ODD && e < p.from) continue;
+      const float rhat = rv[e] * b;
+      m1 = __builtin_fmaf(u[e], rhat, m1);
+      sa = __builtin_fmaf(cy[e], __builtin_fmaf(b, u[e], g[e]), sa);
+      sb = __builtin_fmaf(cy[e] * b, rhat, sb);
+    }
+  }
+  const float s[3] = {wave_sum(m1), wave_sum(sa), wave_sum(sb)};
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s_red[k][threadIdx.x >> 6] = s[k];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v[3] = {};
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[k] += s_red[k][i];
+    m1 = v[0] * a.inv_dim;
+    a.stats[2 * t] = b * m1;
+    a.stats[2 * t + 1] = a.post ? (v[1] - m1 * v[2]) * a.scale * a.inv_dim : 0.f;
+  }
+}
+
+template <typename T, int VEC, bool ODD>
+__global__ __launch_bounds__(64 * kStripTeams) void norm_strip_kernel(NormBwdArgs a, NormPlan pn) {
+  constexpr int TEAMS = kStripTeams;
+  __shared__ float s_fold[TEAMS - 1][VEC][64];
+  const int lane = threadIdx.x & 63;
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const T* gate = reinterpret_cast<const T*>(a.gate);
+  const Place<VEC> pl = place_of<VEC, ODD>((int)blockIdx.x * 64 + lane, a.dim);
+  const uint4 zero4 = make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t one = sizeof(T) == 2 ? 0x3f803f80u : 0x3f800000u;
+  const uint4 ones4 = make_uint4(one, one, one, one);
+  const uint4 wpost = a.post ? get<T, VEC>(reinterpret_cast<const T*>(a.post), pl.at) : ones4;
+  const uint4 wpre = a.pre ? get<T, VEC>(reinterpret_cast<const T*>(a.pre), pl.at) : ones4;
+  uint4 wgate = ones4;
+  float sums[3][VEC] = {};  // post, pre, gate
+  TeamRows now = team_rows(a, pn, TEAMS, team, blockIdx.y);
+  TeamRows then = now;
+  const int64_t iters = now.iters;
+  struct Row {
+    uint4 g, h, r, y;
+    float b, a, bm, m2;
+  } nxt;
+  auto ahead = [&]() __attribute__((always_inline)) {
+    const int64_t t = then.token();
+    then.advance();
+    auto part = [&](const void* base, int64_t ld) {
+      return get_once<T, VEC, ODD>(reinterpret_cast<const T*>(base) + t * ld, pl.at);
+    };
+    nxt.b = a.pre ? a.rstd_pre[t] : 0.f;
+    nxt.a = a.post ? a.rstd_post[t] : 1.f;
+    nxt.bm = a.stats[2 * t];
+    nxt.m2 = a.stats[2 * t + 1];
+    nxt.g = a.dr_out ? part(a.dr_out, a.lddro) : zero4;
+    nxt.h = a.pre ? part(a.dh, a.lddh) : zero4;
+    nxt.r = a.pre ? part(a.r_out, a.ldro) : zero4;
+    nxt.y = a.y ? part(a.y, a.ldy) : zero4;
+  };
+  if (gate) wgate = get<T, VEC>(gate + now.token() / a.group_len * a.ldg, pl.at);
+  ahead();
+  for (int64_t it = 0; it < iters; ++it) {
+    const bool live = now.live();
+    const int64_t t = now.token();
+    if (gate && now.first_of_group())
+      wgate = get<T, VEC>(gate + t / a.group_len * a.ldg, pl.at);
+    const Row cur = nxt;
+    ahead();
+    float g[VEC], u[VEC], rv[VEC], yv[VEC], wp[VEC], wq[VEC], wg[VEC], o[VEC];
+    val<T, VEC>(cur.g, g);
+    val<T, VEC>(cur.h, u);
+    val<T, VEC>(cur.r, rv);
+    val<T, VEC>(cur.y, yv);
+    val<T, VEC>(wpre, wq);
+    val<T, VEC>(wpost, wp);
+    val<T, VEC>(wgate, wg);
+    const float on = live ? 1.f : 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float rhat = rv[e] * cur.b, yhat = yv[e] * cur.a;
+      g[e] = __builtin_fmaf(-cur.bm, rhat, __builtin_fmaf(cur.b, u[e] * wq[e], g[e]));
+      sums[1][e] = __builtin_fmaf(u[e] * on, rhat, sums[1][e]);
+      const float sG = a.scale * g[e], gy = sG * yhat * on;
+      sums[2][e] = __builtin_fmaf(gy, wp[e], sums[2][e]);
+      sums[0][e] = __builtin_fmaf(gy, wg[e], sums[0][e]);
+      o[e] = cur.a * __builtin_fmaf(-cur.m2, yhat, sG * wg[e] * wp[e]);
+    }
+    if (live && pl.in) {
+      put_own<T, VEC>(reinterpret_cast<T*>(a.dr) + t * a.lddr, pl.at, pl.from, g);
+      if (a.y) put_own<T, VEC>(reinterpret_cast<T*>(a.dy) + t * a.lddy, pl.at, pl.from, o);
+    }
+    if (now.last_of_group()) {  // whole groups: this wave's own gate row
+      if (a.dgate && live && pl.in)
+        put_own<T, VEC>(reinterpret_cast<T*>(a.dgate) + t / a.group_len * (int64_t)a.dim, pl.at,
+                        pl.from, sums[2]);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) sums[2][e] = 0.f;
+    }
+    now.advance();
+  }
+  float* out[3] = {a.part_post, a.part_pre, a.part_gate};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    if (!out[k]) continue;
+    __syncthreads();
+    if (team > 0) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s_fold[team - 1][e][lane] = sums[k][e];
+    }
+    __syncthreads();
+    if (team == 0 && pl.in) {
+      float* o = out[k] + (int64_t)blockIdx.y * a.dim;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float v = sums[k][e];
+#pragma unroll
+        for (int q = 0; q < TEAMS - 1; ++q) v += s_fold[q][e][lane];
+        if (e >= pl.from) o[pl.at + e] = v;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, bool ODD>
+hipError_t run_strips(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
+  hipLaunchKernelGGL((norm_stats_kernel<T, VEC, ODD>), dim3((unsigned)a.tokens), dim3(512), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const unsigned strips = (unsigned)((a.dim + 64 * VEC - 1) / (64 * VEC));
+  hipLaunchKernelGGL((norm_strip_kernel<T, VEC, ODD>), dim3(strips, (unsigned)pn.wgs),
+                     dim3(64 * kStripTeams), 0, st, a, pn);
+  return hipGetLastError();
 }
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
@@ -656,16 +857,31 @@ hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
   constexpr int LDS = (TEAMS - 1) * NW * 64 * CH * VEC * 4;
   static_assert(LDS < 60000, "the fold's LDS fits a workgroup's default limit");
   const dim3 grid((unsigned)pn.wgs), block(64 * NW * TEAMS);
-  if (a.dr_out && a.pre && a.y && a.post)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true>), grid, block, LDS, st, a, pn);
+  const bool whole = pn.whole_groups > 0;
+  if constexpr (!ODD && VEC > 1) {
+    auto on16 = [](const void* p, int64_t ld) {
+      return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)ld * sizeof(T)) & 15) == 0;
+    };
+    if (a.dr_out && a.pre && a.y && a.post && on16(a.dr_out, a.lddro) && on16(a.dh, a.lddh) &&
+        on16(a.r_out, a.ldro) && on16(a.y, a.ldy) && on16(a.dr, a.lddr) && on16(a.dy, a.lddy) &&
+        on16(a.dgate, a.dim)) {
+      if (whole)
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, true>), grid, block, LDS, st, a, pn);
+      else
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, false>), grid, block, LDS, st, a, pn);
+      return hipGetLastError();
+    }
+  }
+  if (whole)
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, true>), grid, block, LDS, st, a, pn);
   else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false>), grid, block, LDS, st, a, pn);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, false>), grid, block, LDS, st, a, pn);
   return hipGetLastError();
 }
 
 template <typename T, int VEC, bool ODD>
 hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
-  if (l.ch == 4) return run_bwd<T, VEC, ODD, 16, 4>(a, l.plan, st);
+  if (l.nw == 0) return run_strips<T, VEC, ODD>(a, l.plan, st);
   if (l.ch == 1) return run_bwd<T, VEC, ODD, 1, 1>(a, l.plan, st);
   switch (l.nw) {
     case 1: return run_bwd<T, VEC, ODD, 1, 2>(a, l.plan, st);
@@ -675,9 +891,8 @@ hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
     case 5: return run_bwd<T, VEC, ODD, 5, 2>(a, l.plan, st);
     case 6: return run_bwd<T, VEC, ODD, 6, 2>(a, l.plan, st);
     case 7: return run_bwd<T, VEC, ODD, 7, 2>(a, l.plan, st);
-    case 8: return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
   }
-  return run_bwd<T, VEC, ODD, 16, 2>(a, l.plan, st);
+  return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
 }
 
 template <typename T>
@@ -720,6 +935,7 @@ hipError_t launch_norm_bwd(NormBwdArgs a, int in_bf16, void* ws, hipStream_t st)
   a.part_post = a.dpost ? reinterpret_cast<float*>(base + l.post) : nullptr;
   a.part_pre = a.dpre ? reinterpret_cast<float*>(base + l.pre) : nullptr;
   a.part_gate = a.dgate && l.plan.whole_groups == 0 ? reinterpret_cast<float*>(base + l.gate) : nullptr;
+  a.stats = reinterpret_cast<float*>(base + l.stats);
   return in_bf16 ? bwd_type<uint16_t>(a, l, st) : bwd_type<float>(a, l, st);
 }
 

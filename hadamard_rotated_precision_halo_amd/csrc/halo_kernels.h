@@ -177,7 +177,8 @@ struct NormBwdArgs {
   int64_t tokens, group_len;
   int dim;
   float scale, inv_dim;
-  float *part_post, *part_pre, *part_gate;  // partial sums, set by the launcher
+  // set by the launcher: partial sums, and the widest rows' statistics [tokens x 2]
+  float *part_post, *part_pre, *part_gate, *stats;
 };
 int64_t norm_max_dim(int in_bf16);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int in_bf16, hipStream_t st);

@@ -257,3 +257,28 @@ def test_graph_replay():
         torch.cuda.synchronize()
         for u, v in zip(got, step()):
             assert torch.equal(u, v), k
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("t,d,groups", [(300, 8200, 1), (260, 8203, 130), (600, 9216, 600), (70, 16384, 7),
+                                        (40, 12001, 0)])
+def test_widest_rows(t, d, groups, dt):
+    # rows that go by column strips, in place and out of place
+    print(f"tokens {t} dim {d} gate rows {groups} {dt}", flush=True)
+    r, y = rnd((t, d), dt, 1), rnd((t, d), dt, 2)
+    gate = rnd((groups, d), dt, 3) if groups else None
+    post, pre = rnd((d,), dt, 4) + 1, rnd((d,), dt, 5) + 1
+    out, h, a, b = H.block_norm_fwd(r, y, gate=gate, post_weight=post, pre_weight=pre, scale=0.5)
+    dr, dh = rnd((t, d), dt, 6, 0.01), rnd((t, d), dt, 7, 0.01)
+    kw = dict(gate=gate, post_weight=post, pre_weight=pre, rstd_post=a, rstd_pre=b, scale=0.5)
+    g = H.block_norm_bwd(dr, dh, out, y, **kw)
+    ref = bwd64(dr, dh, out, y, gate, post, pre, a, b, 0.5)
+    for name, v in zip(("dr", "dy", "dgate", "dpost", "dpre"), g):
+        if name != "dgate" or gate is not None:
+            check(v, *ref[name], dt, name)
+    dr2, y2 = dr.clone(), y.clone()
+    g2 = H.block_norm_bwd(dr2, dh, out, y2, dr=dr2, dy=y2, **kw)
+    for u, v in zip(g2, g):
+        assert u is None or torch.equal(u, v)
+    only = H.block_norm_bwd(dr, dh, out, y, want_dgate=False, want_dpost=False, want_dpre=False, **kw)
+    assert torch.equal(only[0], g[0]) and torch.equal(only[1], g[1]) and only[2:] == (None,) * 3
