@@ -289,14 +289,15 @@ struct NormPlan {
 // Waves per token and chunks per lane of the backward for a row of `chunks` chunks: two chunks per
 // lane and as many waves as that takes, so that few lanes idle whatever the width (8192 x 4096
 // and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us).
-// Rows of more than 16 x 64 chunks (nw 0) go by column strips, see norm_strip_kernel.
-void bwd_shape(int64_t chunks, int* nw, int* ch) {
+// bf16 lanes (256 registers, 8 waves) and fp32 lanes (160 registers, 12 waves) bound the row; longer
+// rows (nw 0) go by column strips, see norm_strip_kernel.
+void bwd_shape(int64_t chunks, int vec, int* nw, int* ch) {
   const int64_t per = (chunks + 63) / 64;
   *ch = per <= 1 ? 1 : 2;
-  *nw = per <= 16 ? (int)((per + 1) / 2) : 0;
+  *nw = per <= 2 * (vec == 8 ? 8 : 12) ? (int)((per + 1) / 2) : 0;
 }
-// Teams of a workgroup: about 8 waves together, whose lanes then have 256 registers each.
-constexpr int bwd_teams(int nw) { return 8 / nw; }
+// Teams of a workgroup, as many as its registers allow.
+constexpr int bwd_teams(int nw, int vec) { return (vec == 8 ? 8 : 12) / nw; }
 constexpr int kStripTeams = 4;
 
 // wgs: the workgroups to aim at.
@@ -374,9 +375,9 @@ __device__ __forceinline__ TeamRows team_rows(const NormBwdArgs& a, const NormPl
 // loop has no branch around a memory access, and no wait covers more than the row it needs.
 // WHOLE: the plan's whole groups, whose gate rows are loaded with each row.
 template <typename T, int VEC, bool ODD, int NW, int CH, bool FAST, bool WHOLE>
-__global__ __launch_bounds__(64 * NW * bwd_teams(NW)) void norm_bwd_kernel(NormBwdArgs a,
+__global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(NormBwdArgs a,
                                                                            NormPlan pn) {
-  constexpr int TEAMS = bwd_teams(NW), WAVES = NW * TEAMS;
+  constexpr int TEAMS = bwd_teams(NW, VEC), WAVES = NW * TEAMS;
   __shared__ float s_red[2][3][WAVES];
   extern __shared__ float s_fold[];  // TEAMS > 1: (TEAMS - 1) x (columns) x 3 floats, see below
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), team = wave / NW;
@@ -655,9 +656,9 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
   BwdLayout l{};
   l.vec = in_bf16 ? 8 : 4;
   if (dim < l.vec) l.vec = 1;
-  bwd_shape((dim + l.vec - 1) / l.vec, &l.nw, &l.ch);
+  bwd_shape((dim + l.vec - 1) / l.vec, l.vec, &l.nw, &l.ch);
   if (l.nw > 0) {
-    l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw), 256);
+    l.plan = plan_bwd(tokens, group_len, bwd_teams(l.nw, l.vec), 256);
   } else {
     const int64_t strips = (dim + 64 * l.vec - 1) / (64 * l.vec);
     l.plan = plan_bwd(tokens, group_len, kStripTeams, (1024 + strips - 1) / strips);
@@ -853,7 +854,7 @@ hipError_t run_strips(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) 
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
 hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
-  constexpr int TEAMS = bwd_teams(NW);
+  constexpr int TEAMS = bwd_teams(NW, VEC);
   constexpr int LDS = (TEAMS - 1) * NW * 64 * CH * VEC * 4;
   static_assert(LDS < 60000, "the fold's LDS fits a workgroup's default limit");
   const dim3 grid((unsigned)pn.wgs), block(64 * NW * TEAMS);
@@ -891,8 +892,17 @@ hipError_t pick_bwd(const NormBwdArgs& a, const BwdLayout& l, hipStream_t st) {
     case 5: return run_bwd<T, VEC, ODD, 5, 2>(a, l.plan, st);
     case 6: return run_bwd<T, VEC, ODD, 6, 2>(a, l.plan, st);
     case 7: return run_bwd<T, VEC, ODD, 7, 2>(a, l.plan, st);
+    case 8: return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
   }
-  return run_bwd<T, VEC, ODD, 8, 2>(a, l.plan, st);
+  if constexpr (VEC == 4) {
+    switch (l.nw) {
+      case 9: return run_bwd<T, VEC, ODD, 9, 2>(a, l.plan, st);
+      case 10: return run_bwd<T, VEC, ODD, 10, 2>(a, l.plan, st);
+      case 11: return run_bwd<T, VEC, ODD, 11, 2>(a, l.plan, st);
+      case 12: return run_bwd<T, VEC, ODD, 12, 2>(a, l.plan, st);
+    }
+  }
+  return hipErrorInvalidValue;
 }
 
 template <typename T>

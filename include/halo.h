@@ -451,8 +451,8 @@ halo_status halo_block_norm_fwd(const void* r, int64_t ldr, const void* y, int64
  *   dr       may be dr_out or dh; dy may be y or dh (same leading dimension).
  *   dgate [groups x dim], dpost_weight, dpre_weight [dim] (dense, io_type): each may be NULL.
  *   ws       at least halo_block_norm_bwd_workspace_bytes(...) bytes, 16-byte aligned (the
- *            partial sums of the parameter gradients and, for rows of more than 16 KB, two numbers
- *            per token).
+ *            partial sums of the parameter gradients and, for long rows, two numbers per
+ *            token).
  * Sums over tokens are fp32 in a fixed order: equal inputs give equal bits.
  */
 size_t halo_block_norm_bwd_workspace_bytes(int64_t tokens, int64_t dim, int64_t groups,
