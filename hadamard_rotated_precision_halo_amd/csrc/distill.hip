@@ -17,7 +17,7 @@
 //   Parts     the gradient alone under a given lse: no statistics, so a row is split over
 //             workgroups.
 // Every lane keeps a running (maximum, sum) over groups of 4 chunks of its part of the row, and the
-// first 256 threads one of the teacher's entries; waves combine theirs in a fixed order after one
+// first 256 threads (or all) one of the teacher's entries; waves combine theirs in a fixed order after one
 // barrier.  The order depends on the vocabulary alone (its thread count), so the three calls give
 // the same bits and a token's values do not depend on the others in its batch.  Statistics,
 // exponents and sums are fp32.  The gradient is written for the whole row as dloss tau q; after a second barrier the
@@ -80,10 +80,11 @@ enum Mode { kHeld, kStreamed, kParts };
 
 // One token's row (kParts: the part blockIdx.y of it, NT CH chunks).
 template <typename T, int NT, int CH, int MODE>
-__global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_kernel(DistillArgs a) {
+__global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4) void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
   __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
-  extern __shared__ float s_top[];  // t / tau, then p [K]; logit [K]; index [K]
+  // t / tau, then p [K]; logit [K]; index [K]
+  extern __shared__ __attribute__((aligned(16))) float s_top[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t tok = blockIdx.x;
   const int K = a.top;
@@ -92,9 +93,10 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
   const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ldl;
   T* out = reinterpret_cast<T*>(a.dlogits) + tok * a.ldd;
   const T* in = row + first;
+  const int Kp = (K + 3) & ~3;  // the entries are also read 4 at a time
   float* s_p = s_top;
-  float* s_z = s_top + K;
-  int* s_i = reinterpret_cast<int*>(s_top + 2 * K);
+  float* s_z = s_top + Kp;
+  int* s_i = reinterpret_cast<int*>(s_top + 2 * Kp);
   const int whole = V / VEC;  // full chunks; the V % VEC elements after them go one per thread
   const int rest0 = whole * VEC;
   const bool has_rest = rest0 + tid < V;
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
 
   // the teacher's first entries are asked for before the row, so that the loads of their logits
   // need not wait for it
-  constexpr int TT = 256;  // threads that reduce the teacher's entries
+  constexpr int TT = NT < 256 ? NT : 256;  // threads that reduce the teacher's entries
   const int32_t* idx = a.idx + tok * a.ldi;
   auto teacher = [&](int k) {
     return a.t_bf16 ? elem_f32(reinterpret_cast<const uint16_t*>(a.tlogits) + tok * a.ldt + k)
@@ -146,6 +148,10 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
       s_z[k] = there ? elem_f32<T>(row + i) : 0.f;
       s_p[k] = t;
       tm = fmaxf(tm, t != t ? __builtin_inff() : t);  // a NaN entry keeps the token in, as NaN
+    }
+    if (tid < Kp - K) {
+      s_i[K + tid] = -1;
+      s_p[K + tid] = 0.f;
     }
     float ts = 0.f;
     const float ref = finite_ref(tm);
@@ -271,7 +277,14 @@ __global__ __launch_bounds__(NT, NT == 1024 && CH <= 4 ? 8 : 4) void distill_ker
     const int i = s_i[k];
     if (i < first || i >= first + V) continue;
     float p = 0.f;
-    for (int o = 0; o < K; ++o) p += s_i[o] == i ? s_p[o] : 0.f;
+    for (int o = 0; o < Kp; o += 4) {
+      const int4 oi = *reinterpret_cast<const int4*>(s_i + o);
+      const float4 op = *reinterpret_cast<const float4*>(s_p + o);
+      p += oi.x == i ? op.x : 0.f;
+      p += oi.y == i ? op.y : 0.f;
+      p += oi.z == i ? op.z : 0.f;
+      p += oi.w == i ? op.w : 0.f;
+    }
     elem_store<T>(out + i, by * (ex(s_z[k]) - p));
   }
 }
@@ -280,19 +293,30 @@ template <typename T, int NT, int CH, int MODE>
 hipError_t run(const DistillArgs& a, hipStream_t st) {
   constexpr int64_t part = (int64_t)NT * CH * RowType<T>::VEC;
   const dim3 grid((unsigned)a.tokens, MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
-  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT), (size_t)a.top * 12, st, a);
+  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT),
+                     (size_t)((a.top + 3) & ~3) * 12, st, a);
   return hipGetLastError();
 }
 
+// Threads per token, by the vocabulary alone: so few that a compute unit holds several rows, one of
+// which loads while another is reduced or stored, and so many that a row fits their registers.
+// 8192 x 2000 bf16, loss and gradient: 17.8 us with a wave per token, 33.0 us with 256 threads;
+// 4096 x 16000: 58 us with 512 threads, 69 us with 1024; 2048 x 65536: 95 and 107 us.
 template <typename T>
 hipError_t pick(const DistillArgs& a, hipStream_t st) {
   const int64_t chunks = a.vocab / RowType<T>::VEC;
+  if (chunks <= 64 * 4) {
+    if (a.lse_in) return run<T, 64, 4, kParts>(a, st);
+    return a.dlogits ? run<T, 64, 4, kHeld>(a, st) : run<T, 64, 4, kStreamed>(a, st);
+  }
   if (a.lse_in) return run<T, 256, 8, kParts>(a, st);
   if (chunks <= 256 * 4)
     return a.dlogits ? run<T, 256, 4, kHeld>(a, st) : run<T, 256, 4, kStreamed>(a, st);
+  if (chunks <= 512 * 16) {
+    if (!a.dlogits) return run<T, 512, 4, kStreamed>(a, st);
+    return chunks <= 512 * 8 ? run<T, 512, 8, kHeld>(a, st) : run<T, 512, 16, kHeld>(a, st);
+  }
   if (!a.dlogits) return run<T, 1024, 4, kStreamed>(a, st);
-  if (chunks <= 1024 * 4) return run<T, 1024, 4, kHeld>(a, st);
-  if (chunks <= 1024 * 8) return run<T, 1024, 8, kHeld>(a, st);
   if (chunks <= 1024 * 16) return run<T, 1024, 16, kHeld>(a, st);
   return run<T, 1024, 4, kStreamed>(a, st);
 }
