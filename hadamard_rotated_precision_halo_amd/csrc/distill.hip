@@ -78,7 +78,7 @@ __device__ __forceinline__ void pair_of(const float (*p)[2], float& m, float& s)
 
 enum Mode { kHeld, kStreamed, kParts };
 
-// One token's row (kParts: the part blockIdx.y of it, NT CH chunks).
+// One token's row (kParts: the part blockIdx.y of it).
 template <typename T, int NT, int CH, int MODE>
 __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4) void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
@@ -88,25 +88,32 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t tok = blockIdx.x;
   const int K = a.top;
-  const int first = MODE == kParts ? (int)blockIdx.y * (NT * CH * VEC) : 0;
-  const int V = MODE == kParts ? min(a.vocab - first, NT * CH * VEC) : a.vocab;  // this part's
   const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ldl;
   T* out = reinterpret_cast<T*>(a.dlogits) + tok * a.ldd;
-  const T* in = row + first;
   const int Kp = (K + 3) & ~3;  // the entries are also read 4 at a time
   float* s_p = s_top;
   float* s_z = s_top + Kp;
   int* s_i = reinterpret_cast<int*>(s_top + 2 * Kp);
-  const int whole = V / VEC;  // full chunks; the V % VEC elements after them go one per thread
-  const int rest0 = whole * VEC;
-  const bool has_rest = rest0 + tid < V;
+  // This workgroup's elements [lo, hi): full chunks from base on, then fewer than VEC more, one per
+  // thread.  A part's chunks start on 64 bytes (777 x 50257 fp32: 212 MB fetched for 156 MB of rows
+  // where they start anywhere); the elements before the first part's also go one per thread.
+  constexpr int SPAN = NT * CH * VEC;
+  const int part = MODE == kParts ? (int)blockIdx.y : 0;
+  const int head = MODE == kParts ? min(a.vocab, (int)((-reinterpret_cast<uintptr_t>(row) & 63) / sizeof(T))) : 0;
+  const int base = head + part * SPAN;
+  const int n = MODE == kParts ? max(0, min(a.vocab - base, SPAN)) : a.vocab;
+  const int lo = part == 0 ? 0 : base, hi = base + n;
+  const int whole = n / VEC, tail = n - whole * VEC;
+  const int lone = tid < tail ? base + whole * VEC + tid
+                   : part == 0 && tid - tail < head ? tid - tail : -1;
+  const T* in = row + base;
   const bool grad = a.dlogits != nullptr;
   const float dl = a.dloss ? a.dloss[tok] : 0.f;
 
   if (MODE == kParts && dl == 0.f) {  // a token that takes no part
     const float z[VEC] = {};
-    for (int c = tid; c < whole; c += NT) store16u_nt(out + first + c * VEC, pack16<T>(z));
-    if (has_rest) elem_store<T>(out + first + rest0 + tid, 0.f);
+    for (int c = tid; c < whole; c += NT) store16u_nt(out + base + c * VEC, pack16<T>(z));
+    if (lone >= 0) elem_store<T>(out + lone, 0.f);
     return;
   }
 
@@ -135,7 +142,7 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
       for (int j = 0; j < CH; ++j) raw[j] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  const float rest = has_rest ? elem_f32<T>(in + rest0 + tid) : -__builtin_inff();
+  const float rest = lone >= 0 ? elem_f32<T>(row + lone) : -__builtin_inff();
 
   // the teacher's entries: kept in LDS, and their (maximum, sum)
   if (tid < TT) {
@@ -166,7 +173,7 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
   // the row's (maximum, sum), of logits / tau
   if constexpr (MODE != kParts) {
     float m = rest * a.inv_tau, sum = 0.f;
-    if (has_rest) sum = Exponent<T>(a.inv_tau, finite_ref(m))(rest);
+    if (lone >= 0) sum = Exponent<T>(a.inv_tau, finite_ref(m))(rest);
     // chunks c0, c0 + NT, .. (4 of them): their maximum first, then the running sum moves to it
     auto group = [&](const uint4* w, int c0) __attribute__((always_inline)) {
       float top = -__builtin_inff();
@@ -243,7 +250,7 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
   const bool zero = by == 0.f;
   const Exponent<T> ex(a.inv_tau, zero ? 0.f : lse);
   if (grad) {
-    T* o = out + first;
+    T* o = out + base;
     if constexpr (MODE == kStreamed) {
       for (int c = tid; c < whole; c += NT) {
         float v[VEC];
@@ -263,7 +270,7 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
         if (c < whole) store16u_nt(o + c * VEC, pack16<T>(v));
       }
     }
-    if (has_rest) elem_store<T>(o + rest0 + tid, zero ? 0.f : by * ex(rest));
+    if (lone >= 0) elem_store<T>(out + lone, zero ? 0.f : by * ex(rest));
   }
   __syncthreads();  // the losses and the p are in LDS; the row's stores come before the entries'
   if (MODE != kParts && tid == 0) {
@@ -275,7 +282,7 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
   if (!grad || zero) return;
   for (int k = tid; k < K; k += NT) {
     const int i = s_i[k];
-    if (i < first || i >= first + V) continue;
+    if (i < lo || i >= hi) continue;
     float p = 0.f;
     for (int o = 0; o < Kp; o += 4) {
       const int4 oi = *reinterpret_cast<const int4*>(s_i + o);

@@ -207,3 +207,25 @@ def test_no_tokens():
     loss, lse, grad = H.distill_fwd_bwd(e, i, torch.empty((0, 4), device=DEV),
                                         torch.empty(0, device=DEV))
     assert loss.numel() == 0 and grad.shape == (0, 100)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("v", [5, 33, 1001, 2055, 16383, 16401, 33000])
+def test_rows_that_start_anywhere(v, dt):
+    # every start of a row within 64 bytes, in place and out of place: the gradient alone works on
+    # parts that start on 64 bytes, and gives the joint call's bits
+    step = 4 if dt == F32 else 2
+    for shift in range(0, 64 // step, 3):
+        logits, idx, tl, dloss = make(3, v, 6, dt, 11 + shift, missing=False)
+        idx[0, 0], idx[0, 1], idx[1, 0] = 0, v - 1, min(v - 1, 40)
+        room = torch.zeros(3 * (v + 5) + 64, dtype=dt, device=DEV)
+        view = room[shift:shift + 3 * (v + 5)].view(3, v + 5)[:, :v]
+        view.copy_(logits)
+        guard = room.clone()
+        loss, lse, want = H.distill_fwd_bwd(logits, idx, tl, dloss + 0.5, temperature=1.5)
+        got = H.distill_bwd(dloss + 0.5, view, lse, idx, tl, temperature=1.5)
+        assert torch.equal(got, want), shift
+        H.distill_bwd(dloss + 0.5, view, lse, idx, tl, temperature=1.5, dlogits=view)
+        assert torch.equal(view, want), shift
+        view.copy_(logits)
+        assert torch.equal(room, guard), shift   # nothing written outside the rows
