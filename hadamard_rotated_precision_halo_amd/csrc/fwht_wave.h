@@ -660,25 +660,23 @@ __device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, in
 }
 
 // The activation-gradient pass: dz = dy act'(z) of bf16 dy and z, in fp32, through the fp32 tile.
-// Both rounds' loads of both inputs (8 bytes: 4 columns of a row) are issued first.
+// A round's loads of both inputs (8 bytes: 4 columns of a row); the second round's are issued
+// before the first is staged, when the first's registers are free.
 template <int B>
 __device__ __forceinline__ void cols_load_act(const ColsProb& pr, int64_t c0, int part, int t,
-                                              uint2 (&d)[2][8], uint2 (&z)[2][8]) {
+                                              int h, uint2 (&d)[8], uint2 (&z)[8]) {
   const FqArgs& a = pr.a;
   const int R = pr.R, CC = pr.C / 4;
   const int cc = t % CC, i = t / CC;
   const int64_t col = c0 + cc * 4;
   const int64_t p0 = col < a.nvec ? col : 0;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+  const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int64_t at = p0 + (r0 + e < a.in_len ? (r0 + e) * a.ldx : 0);
-      d[h][e] = *reinterpret_cast<const uint2*>(x + at);
-      z[h][e] = *reinterpret_cast<const uint2*>(a.z + at);
-    }
+  for (int e = 0; e < 8; ++e) {
+    const int64_t at = p0 + (r0 + e < a.in_len ? (r0 + e) * a.ldx : 0);
+    d[e] = *reinterpret_cast<const uint2*>(x + at);
+    z[e] = *reinterpret_cast<const uint2*>(a.z + at);
   }
 }
 
@@ -823,13 +821,16 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   float v[64];
   if constexpr (F32) {
     uint4 raw[ACT ? 1 : 2][8];
-    uint2 ad[ACT ? 2 : 1][8], az[ACT ? 2 : 1][8];
+    uint2 ad[8], az[8];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (ACT) cols_load_act<B>(pr, c0, part, t, ad, az);
+    if constexpr (ACT) cols_load_act<B>(pr, c0, part, t, 0, ad, az);
     else cols_load_f32<B>(pr, c0, part, t, raw);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if constexpr (ACT) cols_act<B>(pr, part, t, h, ad[h], az[h], sum, raw[0]);
+      if constexpr (ACT) {
+        cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
+        if (h == 0) cols_load_act<B>(pr, c0, part, t, 1, ad, az);
+      }
       cols_stage_f32<B>(pr, t, h, raw[ACT ? 0 : h], lds);
       __syncthreads();
 #pragma unroll
