@@ -68,9 +68,9 @@ __device__ __forceinline__ uint4 get_once(const T* row, int at) {
   else return load16u_nt(row + at);
 }
 
-// 16 bytes at offset off of a row of row_bytes bytes (16-byte aligned, the same for the wave) through
-// a buffer resource over the row: zeros past its end, and a store there is dropped.  Loads past the
-// caches, as get_once.
+// 16 bytes at offset off of a row of row_bytes bytes (16-byte aligned, the same for the wave)
+// through a buffer resource over the row: zeros past its end, and a store there is dropped.  Loads
+// past the caches, as get_once.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_rsrc(const void* row, uint32_t row_bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(row), 0, (int)row_bytes, 0x00020000);
 }
@@ -289,8 +289,8 @@ struct NormPlan {
 // Waves per token and chunks per lane of the backward for a row of `chunks` chunks: two chunks per
 // lane and as many waves as that takes, so that few lanes idle whatever the width (8192 x 4096
 // and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us).
-// bf16 lanes (256 registers, 8 waves) and fp32 lanes (160 registers, 12 waves) bound the row; longer
-// rows (nw 0) go by column strips, see norm_strip_kernel.
+// bf16 lanes (256 registers, 8 waves) and fp32 lanes (160 registers, 12 waves) bound the row;
+// longer rows (nw 0) go by column strips, see norm_strip_kernel.
 void bwd_shape(int64_t chunks, int vec, int* nw, int* ch) {
   const int64_t per = (chunks + 63) / 64;
   *ch = per <= 1 ? 1 : 2;
@@ -304,9 +304,9 @@ constexpr int kStripTeams = 4;
 NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams, int64_t wgs) {
   NormPlan p{};
   // whole rows: one workgroup per compute unit, whose teams keep enough rows in flight (each
-  // prefetches its next row), so that the partial sums, one row per workgroup, stay few (8192 x 4096 bf16: 96.8 us
-  // with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9 us, each before
-  // the loop lost its branches)
+  // prefetches its next row), so that the partial sums, one row per workgroup, stay few (8192 x
+  // 4096 bf16: 96.8 us with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9
+  // us, each before the loop lost its branches)
   int64_t rows = (tokens + wgs - 1) / wgs;
   if (rows < teams) rows = teams;
   if (group_len * teams <= rows) {
@@ -519,7 +519,8 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
     keep_raw(wgate);
     T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
     T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
-    const float on = live ? 1.f : 0.f;
+    // without a row (!live) nothing is added: selected, not multiplied by zero, since the row read
+    // in its place may hold infinities
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       keep_raw1(cur[j].g);
@@ -538,9 +539,9 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
       for (int e = 0; e < VEC; ++e) {
         const float rhat = rv[e] * b, yhat = yv[e] * ar;
         g[e] = __builtin_fmaf(-bm, rhat, __builtin_fmaf(b, u[e] * wq[e], g[e]));
-        spre[j][e] = __builtin_fmaf(u[e] * on, rhat, spre[j][e]);
+        spre[j][e] = __builtin_fmaf(live ? u[e] : 0.f, rhat, spre[j][e]);
         const float sG = a.scale * g[e];
-        const float gy = sG * yhat * on;
+        const float gy = live ? sG * yhat : 0.f;
         sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
         spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
         o[e] = ar * __builtin_fmaf(-m2, yhat, sG * wg[e] * wp[e]);
@@ -794,13 +795,12 @@ __global__ __launch_bounds__(64 * kStripTeams) void norm_strip_kernel(NormBwdArg
     val<T, VEC>(wpre, wq);
     val<T, VEC>(wpost, wp);
     val<T, VEC>(wgate, wg);
-    const float on = live ? 1.f : 0.f;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
+    for (int e = 0; e < VEC; ++e) {  // !live: see norm_bwd_kernel
       const float rhat = rv[e] * cur.b, yhat = yv[e] * cur.a;
       g[e] = __builtin_fmaf(-cur.bm, rhat, __builtin_fmaf(cur.b, u[e] * wq[e], g[e]));
-      sums[1][e] = __builtin_fmaf(u[e] * on, rhat, sums[1][e]);
-      const float sG = a.scale * g[e], gy = sG * yhat * on;
+      sums[1][e] = __builtin_fmaf(live ? u[e] : 0.f, rhat, sums[1][e]);
+      const float sG = a.scale * g[e], gy = live ? sG * yhat : 0.f;
       sums[2][e] = __builtin_fmaf(gy, wp[e], sums[2][e]);
       sums[0][e] = __builtin_fmaf(gy, wg[e], sums[0][e]);
       o[e] = cur.a * __builtin_fmaf(-cur.m2, yhat, sG * wg[e] * wp[e]);
@@ -867,16 +867,20 @@ hipError_t run_bwd(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
         on16(a.r_out, a.ldro) && on16(a.y, a.ldy) && on16(a.dr, a.lddr) && on16(a.dy, a.lddy) &&
         on16(a.dgate, a.dim)) {
       if (whole)
-        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, true>), grid, block, LDS, st, a, pn);
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, true>), grid, block,
+                           LDS, st, a, pn);
       else
-        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, false>), grid, block, LDS, st, a, pn);
+        hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, true, false>), grid, block,
+                           LDS, st, a, pn);
       return hipGetLastError();
     }
   }
   if (whole)
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, true>), grid, block, LDS, st, a, pn);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, true>), grid, block,
+                           LDS, st, a, pn);
   else
-    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, false>), grid, block, LDS, st, a, pn);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, VEC, ODD, NW, CH, false, false>), grid, block,
+                           LDS, st, a, pn);
   return hipGetLastError();
 }
 

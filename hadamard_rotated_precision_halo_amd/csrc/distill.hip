@@ -17,12 +17,12 @@
 //   Parts     the gradient alone under a given lse: no statistics, so a row is split over
 //             workgroups.
 // Every lane keeps a running (maximum, sum) over groups of 4 chunks of its part of the row, and the
-// first 256 threads (or all) one of the teacher's entries; waves combine theirs in a fixed order after one
-// barrier.  The order depends on the vocabulary alone (its thread count), so the three calls give
-// the same bits and a token's values do not depend on the others in its batch.  Statistics,
-// exponents and sums are fp32.  The gradient is written for the whole row as dloss tau q; after a second barrier the
-// entries, computed apart from their own logits, are written over it (duplicated indices sum their
-// p first, so every writer of a position writes the same value).
+// first 256 threads (or all) one of the teacher's entries; waves combine theirs in a fixed order
+// after one barrier.  The order depends on the vocabulary alone (its thread count), so the three
+// calls give the same bits and a token's values do not depend on the others in its batch.
+// Statistics, exponents and sums are fp32.  The gradient is written for the whole row as dloss tau
+// q; after a second barrier the entries, computed apart from their own logits, are written over it
+// (duplicated indices sum their p first, so every writer of a position writes the same value).
 #include "halo_kernels.h"
 #include "rowops.h"
 
@@ -80,7 +80,9 @@ enum Mode { kHeld, kStreamed, kParts };
 
 // One token's row (kParts: the part blockIdx.y of it).
 template <typename T, int NT, int CH, int MODE>
-__global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4) void distill_kernel(DistillArgs a) {
+__global__
+__launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4)
+void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
   __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
   // t / tau, then p [K]; logit [K]; index [K]
@@ -99,7 +101,8 @@ __global__ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8
   // where they start anywhere); the elements before the first part's also go one per thread.
   constexpr int SPAN = NT * CH * VEC;
   const int part = MODE == kParts ? (int)blockIdx.y : 0;
-  const int head = MODE == kParts ? min(a.vocab, (int)((-reinterpret_cast<uintptr_t>(row) & 63) / sizeof(T))) : 0;
+  const int to_line = (int)((-reinterpret_cast<uintptr_t>(row) & 63) / sizeof(T));
+  const int head = MODE == kParts ? min(a.vocab, to_line) : 0;
   const int base = head + part * SPAN;
   const int n = MODE == kParts ? max(0, min(a.vocab - base, SPAN)) : a.vocab;
   const int lo = part == 0 ? 0 : base, hi = base + n;

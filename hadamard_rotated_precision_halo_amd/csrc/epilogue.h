@@ -21,8 +21,8 @@ __device__ __forceinline__ float gelu_arg(float z) {
 }
 
 // erfc(x) / 2 for x >= 0 and exp(-x^2), by formula 7.1.26 of Abramowitz and Stegun, "Handbook of
-// Mathematical Functions" (absolute error of erf below 1.5e-7, 2.5 units of 2^-24): one exponential,
-// one reciprocal and five multiply-adds, a quarter of the library erf's time.
+// Mathematical Functions" (absolute error of erf below 1.5e-7, 2.5 units of 2^-24): one
+// exponential, one reciprocal and five multiply-adds, a quarter of the library erf's time.
 __device__ __forceinline__ float half_erfc(float x, float* gauss) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
   float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);

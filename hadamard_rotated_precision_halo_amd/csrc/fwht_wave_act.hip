@@ -1,7 +1,7 @@
 // fwht_wave_act.hip -- the activation-gradient instantiations of the wave-slice rotation kernels
-// (fwht_wave.h): the rotation passes of a layer backward whose gradient is dz = dy act'(z), formed in
-// fp32 as dy and z are loaded, so that dz never goes to memory, and the bias gradient beside them
-// from the columns pass.  bf16 input, nearest rounding, blocks 64 .. 1024.
+// (fwht_wave.h): the rotation passes of a layer backward whose gradient is dz = dy act'(z), formed
+// in fp32 as dy and z are loaded, so that dz never goes to memory, and the bias gradient beside
+// them from the columns pass.  bf16 input, nearest rounding, blocks 64 .. 1024.
 #include "fwht_wave.h"
 
 namespace halo {

@@ -7,10 +7,10 @@
 // two waves), and accumulates the whole tile.  So every staged byte is read from LDS once (waves
 // that share a slab and split the tile read each byte twice, and the LDS was their bound), and no
 // wave waits for another before the end, where the four partial tiles meet in LDS and are added in
-// wave order.  Bound by the loads: a tile reads 128 bytes for each K byte, 1.4 MB per compute unit at
-// 203 x 4096 x 11008 FP8, 12 to 14 us at the 100 to 120 bytes/ns that a unit loads of data in its
-// L2; the product takes 20.6 us (19.7 us with its LDS reads and MFMAs left out; touching the lines
-// of b ahead of their loads made it 30 us).
+// wave order.  Bound by the loads: a tile reads 128 bytes for each K byte, 1.4 MB per compute unit
+// at 203 x 4096 x 11008 FP8, 12 to 14 us at the 100 to 120 bytes/ns that a unit loads of data in
+// its L2; the product takes 20.6 us (19.7 us with its LDS reads and MFMAs left out; touching the
+// lines of b ahead of their loads made it 30 us).
 #include "gemm_tile.h"
 
 namespace halo {

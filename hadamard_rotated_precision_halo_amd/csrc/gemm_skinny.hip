@@ -8,8 +8,8 @@
 // split the contraction, so a 4096 x 4096 layer keeps all 256 compute units busy and every byte
 // of b is asked for at the start; the codes go from memory into MFMA operands directly (16 rows x
 // 64 bytes per load, no LDS), since no other wave uses them.  MT 16-row tiles of a are read from
-// the L2.  The waves' partial sums meet in LDS and are added in wave order.  For the fewest rows the
-// rotation and quantisation of a run in the same kernel (skinny_fused_kernel).
+// the L2.  The waves' partial sums meet in LDS and are added in wave order.  For the fewest rows
+// the rotation and quantisation of a run in the same kernel (skinny_fused_kernel).
 #include "epilogue.h"
 #include "halo_kernels.h"
 

@@ -322,7 +322,8 @@ GemmArgs act_args(const void* a, int64_t lda, const float* sa, const void* b, in
 halo_status act_product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
                         const float* sb, int64_t m, int64_t n, int64_t k, halo_dtype qt, void* y,
                         halo_dtype yt, const halo_epilogue* ep, hipStream_t st) {
-  return from_hip(launch_gemm_act(act_args(a, lda, sa, b, ldb, sb, m, n, k, y, ep), qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
+  return from_hip(launch_gemm_act(act_args(a, lda, sa, b, ldb, sb, m, n, k, y, ep),
+                                  qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
 }
 
 // Validation of a layer forward.
@@ -375,7 +376,8 @@ halo_status run_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
     s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
     if (s == HALO_OK) s = run_fa(aw, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
   }
-  if (s == HALO_OK && ep) return act_product(qx, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep, st);
+  if (s == HALO_OK && ep)
+    return act_product(qx, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep, st);
   if (s == HALO_OK)
     s = gemm_any(qx, q_type, kq, sx, qw, q_type, kq, sw, m, n, kq, y, y_type, n, st);
   return s;

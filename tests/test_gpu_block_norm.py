@@ -282,3 +282,29 @@ def test_widest_rows(t, d, groups, dt):
         assert u is None or torch.equal(u, v)
     only = H.block_norm_bwd(dr, dh, out, y, want_dgate=False, want_dpost=False, want_dpre=False, **kw)
     assert torch.equal(only[0], g[0]) and torch.equal(only[1], g[1]) and only[2:] == (None,) * 3
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("t,d,pad", [(2, 64, 0), (1, 1000, 0), (2, 513, 1), (3, 8193, 0), (1, 4096, 8)])
+def test_an_infinite_gradient_stays_in_its_column(t, d, pad, dt):
+    """An infinity in a row's incoming gradient gives that column's sums over tokens an infinity of
+    its sign; the other columns' sums do not see it."""
+    print(f"tokens {t} dim {d} padding {pad} {dt}", flush=True)
+    col = d // 2
+    r, y = rnd((t, d), dt, 1, 3.0, pad), rnd((t, d), dt, 2, 0.7, pad)
+    r[0, col], y[0, col] = 2.0, 0.5
+    gate, post, pre = rnd((1, d), dt, 3).abs() + 1, rnd((d,), dt, 4).abs() + 1, rnd((d,), dt, 5) + 1
+    out, h, a, b = H.block_norm_fwd(r, y, gate=gate, post_weight=post, pre_weight=pre, scale=1.0,
+                                    eps=1e-5)
+    assert out[0, col] > 0
+    for inf_in in ("dr", "dh"):
+        dr, dh = rnd((t, d), dt, 6, 0.01, pad), rnd((t, d), dt, 7, 0.01)
+        (dr if inf_in == "dr" else dh)[0, col] = float("inf")
+        _, _, dgate, dpost, dpre = H.block_norm_bwd(
+            dr, dh, out, y, gate=gate, post_weight=post, pre_weight=pre, rstd_post=a, rstd_pre=b,
+            scale=1.0)
+        sums = (dgate[0], dpost) if inf_in == "dr" else (dpre,)
+        for v in sums:
+            assert v[col] == float("inf"), inf_in
+            v[col] = 0
+            assert torch.isfinite(v).all(), inf_in
