@@ -76,6 +76,38 @@ __device__ __forceinline__ void pair_of(const float (*p)[2], float& m, float& s)
   for (int i = 0; i < NW; ++i) s += p[i][1] * exp2_fast((p[i][0] - ref) * kLog2e);
 }
 
+// Which of a token's entries share their index with another.  Up to kSearch entries: each one's p is
+// summed over all of them.  With more, the indices go into an open table in the LDS of at least
+// two slots per entry (so a free one ends every walk) whose top bit marks an index that came twice,
+// and only marked ones are summed over: the same terms in the same order, as p + 0 = p.  A table
+// costs two short walks and its clearing for each entry.  2048 x
+// 32000 bf16, loss and gradient: 62.5 us for 68.1 us at 256 entries, 123 for 213 us at 1024; 8192 x
+// 2000 at 128 entries 27.0 for 33.4 us; at 32 entries (no table) 20.1 for 21.4 us, at 64 equal.
+constexpr int kSearch = 64;
+__host__ __device__ constexpr int entry_slots(int top) {
+  int n = 4 * kSearch;
+  while (n < 2 * top) n *= 2;
+  return top <= kSearch ? 0 : n;
+}
+__device__ __forceinline__ int first_slot(int i, int slots) {  // multiplicative hash, top bits
+  return (int)(((uint32_t)i * 2654435769u) >> (__clz(slots) + 1));
+}
+__device__ __forceinline__ void enter(int* key, int slots, int i) {
+  for (int at = first_slot(i, slots);; at = (at + 1) & (slots - 1)) {
+    const int was = atomicCAS(key + at, -1, i);
+    if (was == -1) return;
+    if ((was & 0x7fffffff) == i) {
+      atomicOr(key + at, (int)0x80000000u);
+      return;
+    }
+  }
+}
+__device__ __forceinline__ bool entered_twice(const int* key, int slots, int i) {
+  int at = first_slot(i, slots);
+  while ((key[at] & 0x7fffffff) != i) at = (at + 1) & (slots - 1);
+  return key[at] < 0;
+}
+
 enum Mode { kHeld, kStreamed, kParts };
 
 // One token's row (kParts: the part blockIdx.y of it).
@@ -85,7 +117,7 @@ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4)
 void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
   __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
-  // t / tau, then p [K]; logit [K]; index [K]
+  // t / tau, then p [K]; logit [K]; index [K]; with many entries, a table of indices [slots]
   extern __shared__ __attribute__((aligned(16))) float s_top[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t tok = blockIdx.x;
@@ -96,6 +128,8 @@ void distill_kernel(DistillArgs a) {
   float* s_p = s_top;
   float* s_z = s_top + Kp;
   int* s_i = reinterpret_cast<int*>(s_top + 2 * Kp);
+  int* s_key = s_i + Kp;
+  const int slots = entry_slots(K);
   // This workgroup's elements [lo, hi): full chunks from base on, then fewer than VEC more, one per
   // thread.  A part's chunks start on 64 bytes (777 x 50257 fp32: 212 MB fetched for 156 MB of rows
   // where they start anywhere); the elements before the first part's also go one per thread.
@@ -150,14 +184,36 @@ void distill_kernel(DistillArgs a) {
   // the teacher's entries: kept in LDS, and their (maximum, sum)
   if (tid < TT) {
     float tm = -__builtin_inff();
-    for (int k = tid; k < K; k += TT) {
-      const int i = k == tid ? i0 : idx[k];
+    auto keep = [&](int k, int i, float t, float z) __attribute__((always_inline)) {
       const bool there = i >= 0 && i < a.vocab;
-      const float t = there ? (k == tid ? t0 : teacher(k)) * a.inv_tau : -__builtin_inff();
+      t = there ? t * a.inv_tau : -__builtin_inff();
       s_i[k] = there ? i : -1;
-      s_z[k] = there ? elem_f32<T>(row + i) : 0.f;
+      s_z[k] = there ? z : 0.f;
       s_p[k] = t;
       tm = fmaxf(tm, t != t ? __builtin_inff() : t);  // a NaN entry keeps the token in, as NaN
+    };
+    // a part takes the logits of its own entries, the others' of the row's first element
+    const int from = MODE == kParts ? lo : 0, to = MODE == kParts ? hi : a.vocab;
+    auto logit = [&](int i) { return elem_f32<T>(row + (i >= from && i < to ? i : 0)); };
+    if (mine) keep(tid, i0, t0, logit(i0));
+    // DEEP entries in flight.  4 where many fall on a thread (8192 x 2000 bf16 with 512 entries:
+    // 53 us, 68 us with 1) and for parts; 1 beside a longer row in registers (4096 x 131072 with 64
+    // entries: 398 us, 418 us with 4).
+    constexpr int DEEP = NT <= 64 || MODE == kParts ? 4 : 1;
+    for (int k0 = tid + TT; k0 < K; k0 += DEEP * TT) {
+      int i[DEEP];
+      float t[DEEP], z[DEEP];
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j) {
+        const int k = min(k0 + j * TT, K - 1);
+        i[j] = idx[k];
+        t[j] = teacher(k);
+      }
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j) z[j] = logit(i[j]);
+#pragma unroll
+      for (int j = 0; j < DEEP; ++j)
+        if (k0 + j * TT < K) keep(k0 + j * TT, i[j], t[j], z[j]);
     }
     if (tid < Kp - K) {
       s_i[K + tid] = -1;
@@ -172,6 +228,8 @@ void distill_kernel(DistillArgs a) {
       s_tea[wave][1] = ts;
     }
   }
+
+  for (int k = tid; k < slots; k += NT) s_key[k] = -1;
 
   // the row's (maximum, sum), of logits / tau
   if constexpr (MODE != kParts) {
@@ -244,6 +302,8 @@ void distill_kernel(DistillArgs a) {
     const float p = empty ? 0.f : exp2_fast(lp * kLog2e);
     s_p[k] = p;
     if (p != 0.f) l += p * (lp - (__builtin_fmaf(s_z[k], a.inv_tau, -lse)));
+    const int i = s_i[k];
+    if (slots && grad && i >= lo && i < hi) enter(s_key, slots, i);
   }
   if (MODE != kParts) {
     l = wave_sum(l);
@@ -286,6 +346,10 @@ void distill_kernel(DistillArgs a) {
   for (int k = tid; k < K; k += NT) {
     const int i = s_i[k];
     if (i < lo || i >= hi) continue;
+    if (slots && !entered_twice(s_key, slots, i)) {
+      elem_store<T>(out + i, by * (ex(s_z[k]) - s_p[k]));
+      continue;
+    }
     float p = 0.f;
     for (int o = 0; o < Kp; o += 4) {
       const int4 oi = *reinterpret_cast<const int4*>(s_i + o);
@@ -304,7 +368,7 @@ hipError_t run(const DistillArgs& a, hipStream_t st) {
   constexpr int64_t part = (int64_t)NT * CH * RowType<T>::VEC;
   const dim3 grid((unsigned)a.tokens, MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
   hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT),
-                     (size_t)((a.top + 3) & ~3) * 12, st, a);
+                     (size_t)((a.top + 3) & ~3) * 12 + (size_t)entry_slots(a.top) * 4, st, a);
   return hipGetLastError();
 }
 

@@ -229,3 +229,23 @@ def test_rows_that_start_anywhere(v, dt):
         assert torch.equal(view, want), shift
         view.copy_(logits)
         assert torch.equal(room, guard), shift   # nothing written outside the rows
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("v,k", [(1000, 64), (1000, 65), (5000, 257), (9001, 1023), (70000, 1024)])
+def test_many_entries_that_repeat(v, k, dt):
+    """Entries whose indices repeat up to k / 8 times (a sum of that many p adds k / 8 roundings, which
+    the tolerance's k / 4 covers), far apart, next to each other, or in steps of a power of two."""
+    print(f"vocabulary {v} kept {k} {dt}", flush=True)
+    logits, idx, tl, dloss = make(6, v, k, dt, 21)
+    dloss = dloss + 0.25
+    n = torch.arange(k, device=DEV, dtype=torch.int32)
+    idx[0] = n % v                                  # one each
+    idx[1] = n % 8                                  # eight indices, each k / 8 times
+    idx[2] = n.flip(0) // 2                         # neighbours, twice
+    idx[3] = (n * 64) % v
+    idx[4] = torch.where(n % 3 == 0, n // 8 * 8, -1)  # with places that are no entry between
+    idx[5] = v - 1 - (n * 4096) % v
+    repeats = torch.stack([torch.bincount(i[i >= 0].long(), minlength=v).max() for i in idx[:3]])
+    assert (repeats <= -(-k // 8)).all()
+    check_all(logits, idx, tl, dloss, 2.0)
