@@ -250,3 +250,43 @@ def test_the_binding_refuses():
         H.distill_fwd(r, i, f, temperature=0.0)
     with pytest.raises(H.HaloError):
         H.linear_act_q(r, q, s, 64, workspace=torch.zeros(16, dtype=torch.uint8, device=dev))
+
+
+@pytest.mark.gpu
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """A call given a stream allocates its outputs and workspaces on that stream: memory of another
+    stream could be handed on while the call's kernels still use it."""
+    import torch
+    dev, bf = torch.device("cuda", torch.cuda.current_device()), torch.bfloat16
+    r, w, v = (torch.ones(s, dtype=bf, device=dev) for s in ((40, 64), (32, 64), (64,)))
+    f, dloss = torch.zeros((40, 4), device=dev), torch.ones(40, device=dev)
+    i = torch.arange(4, dtype=torch.int32, device=dev).repeat(40, 1)
+    one = torch.ones(40, device=dev)
+    dy = torch.ones((40, 32), dtype=bf, device=dev)
+    q, s = H.fwht_quant(w, H.ROWS, 64)
+    calls = [lambda **k: H.block_norm_fwd(r, r, post_weight=v, pre_weight=v, **k),
+             lambda **k: H.block_norm_bwd(r, r, r, r, v, v, v, one, one, **k),
+             lambda **k: H.distill_fwd(r, i, f, **k),
+             lambda **k: H.distill_bwd(dloss, r, one, i, f, **k),
+             lambda **k: H.distill_fwd_bwd(r, i, f, dloss, **k),
+             lambda **k: H.linear_act_fwd(r, w, 64, want_z=True, activation="silu", **k),
+             lambda **k: H.linear_act_q(r, q, s, 64, **k),
+             lambda **k: H.linear_act_bwd(dy, dy, r, w, 64, activation="silu", **k)]
+    side, at = torch.cuda.Stream(), []
+    for name in ("empty", "empty_like"):
+        def spy(*a, real=getattr(torch, name), **k):
+            at.append(torch.cuda.current_stream(dev).cuda_stream)
+            return real(*a, **k)
+        monkeypatch.setattr(torch, name, spy)
+    for n, call in enumerate(calls):
+        want = call()
+        side.wait_stream(torch.cuda.current_stream())
+        at.clear()
+        got = call(stream=side)
+        assert at and set(at) == {side.cuda_stream}, n
+        side.synchronize()
+        one_or_more = lambda o: o if isinstance(o, tuple) else (o,)
+        for a, b in zip(one_or_more(got), one_or_more(want)):
+            assert (a is None and b is None) or torch.equal(a, b), n
+        with pytest.raises(ValueError):
+            call(stream=side.cuda_stream)
