@@ -19,8 +19,12 @@
 // Every lane keeps a running (maximum, sum) over groups of 4 chunks of its part of the row, and the
 // first 256 threads (or all) one of the teacher's entries; waves combine theirs in a fixed order
 // after one barrier.  The order depends on the vocabulary alone (its thread count), so the three
-// calls give the same bits and a token's values do not depend on the others in its batch.
-// Statistics, exponents and sums are fp32.  The gradient is written for the whole row as dloss tau
+// calls give the same bits (the gradient: up to |lse| = kFar) and a token's values do not depend on
+// the others in its batch.
+// Statistics, exponents and sums are fp32.  The statistics are of differences from a maximum taken
+// before they are scaled by 1 / tau: with s log2(e) / tau and the maximum's product rounded apart, a
+// part of the row that a mask fills with -1e10 or the type's lowest value would be off from its own
+// maximum by more than an exponential holds.  The gradient is written for the whole row as dloss tau
 // q; after a second barrier the entries, computed apart from their own logits, are written over it
 // (duplicated indices sum their p first, so every writer of a position writes the same value).
 #include "halo_kernels.h"
@@ -36,7 +40,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 
 // exp(s / tau - lse).  fp32 logits: s / tau - lse is rounded once (an fma) before it is scaled to
 // base 2, so the error does not grow with |s|; bf16 logits' gradients keep 8 bits, and one fma
-// with both factors merged is enough.
+// with both factors merged is enough.  For |lse| up to kFar: see FarExponent.
 template <typename T>
 struct Exponent {
   float mul, sub;  // fp32: 1 / tau, lse; bf16: log2(e) / tau, log2(e) lse
@@ -55,25 +59,37 @@ struct Exponent {
   }
 };
 
+// The same where lse is so large that its own last bit (2^-12 at kFar) shows in the exponential:
+// exp2((s - ref) mul - sub), from the row's maximum ref and sub = log2 of its sum where the call has
+// them, else from ref = lse tau and no more than 1, which q is.  NaN stays.
+constexpr float kFar = 4096.f;
+struct FarExponent {
+  float ref, mul, sub;
+  __device__ __forceinline__ float operator()(float s) const {
+    const float d = __builtin_fmaf(s - ref, mul, -sub);
+    return exp2_fast(d > 0.f ? 0.f : d);
+  }
+};
+
 __device__ __forceinline__ float finite_ref(float m) { return m == -__builtin_inff() ? 0.f : m; }
 
-// A (maximum, sum of exp(. - maximum)) pair over the lanes of a wave.  A part that is -inf
-// everywhere has maximum -inf and sum 0; NaN stays in the sum.
-__device__ __forceinline__ void wave_pair(float& m, float& s) {
+// A (maximum, sum of exp2((. - maximum) mul)) pair over the lanes of a wave, mul = log2(e) / tau.  A
+// part that is -inf everywhere has maximum -inf and sum 0; NaN stays in the sum.
+__device__ __forceinline__ void wave_pair(float& m, float& s, float mul) {
   const float top = wave_max(m);
-  s = wave_sum(s * exp2_fast((m - finite_ref(top)) * kLog2e));
+  s = wave_sum(s * exp2_fast((m - finite_ref(top)) * mul));
   m = top;
 }
 // The same over the pairs of NW waves.
 template <int NW>
-__device__ __forceinline__ void pair_of(const float (*p)[2], float& m, float& s) {
+__device__ __forceinline__ void pair_of(const float (*p)[2], float mul, float& m, float& s) {
   m = p[0][0];
 #pragma unroll
   for (int i = 1; i < NW; ++i) m = fmaxf(m, p[i][0]);
   const float ref = finite_ref(m);
   s = 0.f;
 #pragma unroll
-  for (int i = 0; i < NW; ++i) s += p[i][1] * exp2_fast((p[i][0] - ref) * kLog2e);
+  for (int i = 0; i < NW; ++i) s += p[i][1] * exp2_fast((p[i][0] - ref) * mul);
 }
 
 // Which of a token's entries share their index with another.  Up to kSearch entries: each one's p is
@@ -117,11 +133,12 @@ __launch_bounds__(NT, NT >= 512 && CH <= 4 ? 8 : NT == 512 && CH == 8 ? 6 : 4)
 void distill_kernel(DistillArgs a) {
   constexpr int VEC = RowType<T>::VEC, NW = NT / 64;
   __shared__ float s_row[NW][2], s_tea[4][2], s_loss[NW];
-  // t / tau, then p [K]; logit [K]; index [K]; with many entries, a table of indices [slots]
+  // t, then p [K]; logit [K]; index [K]; with many entries, a table of indices [slots]
   extern __shared__ __attribute__((aligned(16))) float s_top[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t tok = blockIdx.x;
   const int K = a.top;
+  const float mul = a.inv_tau * kLog2e;
   const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ldl;
   T* out = reinterpret_cast<T*>(a.dlogits) + tok * a.ldd;
   const int Kp = (K + 3) & ~3;  // the entries are also read 4 at a time
@@ -186,7 +203,7 @@ void distill_kernel(DistillArgs a) {
     float tm = -__builtin_inff();
     auto keep = [&](int k, int i, float t, float z) __attribute__((always_inline)) {
       const bool there = i >= 0 && i < a.vocab;
-      t = there ? t * a.inv_tau : -__builtin_inff();
+      t = there ? t : -__builtin_inff();
       s_i[k] = there ? i : -1;
       s_z[k] = there ? z : 0.f;
       s_p[k] = t;
@@ -221,8 +238,8 @@ void distill_kernel(DistillArgs a) {
     }
     float ts = 0.f;
     const float ref = finite_ref(tm);
-    for (int k = tid; k < K; k += TT) ts += exp2_fast((s_p[k] - ref) * kLog2e);
-    wave_pair(tm, ts);
+    for (int k = tid; k < K; k += TT) ts += exp2_fast((s_p[k] - ref) * mul);
+    wave_pair(tm, ts, mul);
     if (lane == 0) {
       s_tea[wave][0] = tm;
       s_tea[wave][1] = ts;
@@ -231,10 +248,10 @@ void distill_kernel(DistillArgs a) {
 
   for (int k = tid; k < slots; k += NT) s_key[k] = -1;
 
-  // the row's (maximum, sum), of logits / tau
+  // the row's (maximum, sum)
   if constexpr (MODE != kParts) {
-    float m = rest * a.inv_tau, sum = 0.f;
-    if (lone >= 0) sum = Exponent<T>(a.inv_tau, finite_ref(m))(rest);
+    float m = rest, sum = 0.f;
+    if (lone >= 0) sum = exp2_fast((rest - finite_ref(m)) * mul);
     // chunks c0, c0 + NT, .. (4 of them): their maximum first, then the running sum moves to it
     auto group = [&](const uint4* w, int c0) __attribute__((always_inline)) {
       float top = -__builtin_inff();
@@ -246,17 +263,16 @@ void distill_kernel(DistillArgs a) {
         for (int e = 0; e < VEC; ++e) t = fmaxf(t, v[e]);
         if (c0 + j * NT < whole) top = fmaxf(top, t);
       }
-      top = fmaxf(m, top * a.inv_tau);
+      top = fmaxf(m, top);
       const float ref = finite_ref(top);
-      const Exponent<T> ex(a.inv_tau, ref);
-      sum *= exp2_fast((m - ref) * kLog2e);
+      sum *= exp2_fast((m - ref) * mul);
       m = top;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float v[VEC], part = 0.f;
         unpack16<T>(w[j], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) part += ex(v[e]);
+        for (int e = 0; e < VEC; ++e) part += exp2_fast((v[e] - ref) * mul);
         sum += c0 + j * NT < whole ? part : 0.f;
       }
     };
@@ -275,21 +291,22 @@ void distill_kernel(DistillArgs a) {
         group(w, c0);
       }
     }
-    wave_pair(m, sum);
+    wave_pair(m, sum, mul);
     if (lane == 0) {
       s_row[wave][0] = m;
       s_row[wave][1] = sum;
     }
   }
   __syncthreads();
-  float tm, ts, lse;
-  pair_of<TT / 64>(s_tea, tm, ts);
+  float tm, ts, lse, m = 0.f, logsum = 0.f;
+  pair_of<TT / 64>(s_tea, mul, tm, ts);
   if (MODE == kParts) {
     lse = a.lse_in[tok];
   } else {
-    float m, sum;
-    pair_of<NW>(s_row, m, sum);
-    lse = sum == 0.f ? -__builtin_inff() : finite_ref(m) + logf(sum);
+    float sum;
+    pair_of<NW>(s_row, mul, m, sum);
+    logsum = logf(sum);
+    lse = sum == 0.f ? -__builtin_inff() : __builtin_fmaf(m, a.inv_tau, logsum);
     if (a.lse && tid == 0) a.lse[tok] = lse;
   }
   const bool empty = tm == -__builtin_inff() || lse == -__builtin_inff();
@@ -298,10 +315,10 @@ void distill_kernel(DistillArgs a) {
   float l = 0.f;
   const float logts = logf(ts);
   for (int k = tid; k < K; k += NT) {
-    const float lp = (s_p[k] - tm) - logts;
+    const float lp = __builtin_fmaf(s_p[k] - tm, a.inv_tau, -logts);
     const float p = empty ? 0.f : exp2_fast(lp * kLog2e);
     s_p[k] = p;
-    if (p != 0.f) l += p * (lp - (__builtin_fmaf(s_z[k], a.inv_tau, -lse)));
+    if (p != 0.f) l += p * (lp - __builtin_fmaf(s_z[k] - m, a.inv_tau, -logsum));
     const int i = s_i[k];
     if (slots && grad && i >= lo && i < hi) enter(s_key, slots, i);
   }
@@ -311,8 +328,14 @@ void distill_kernel(DistillArgs a) {
   }
   const float by = empty ? 0.f : dl * a.tau;
   const bool zero = by == 0.f;
-  const Exponent<T> ex(a.inv_tau, zero ? 0.f : lse);
-  if (grad) {
+  const bool far = !(fabsf(lse) <= kFar);
+  const Exponent<T> ex(a.inv_tau, lse);
+  FarExponent exf{m, mul, logsum * kLog2e};
+  if (MODE == kParts) {
+    exf.ref = fmaxf(lse * a.tau, -__FLT_MAX__);
+    exf.sub = lse == lse ? 0.f : lse;
+  }
+  auto write = [&](auto ex) __attribute__((always_inline)) {
     T* o = out + base;
     if constexpr (MODE == kStreamed) {
       for (int c = tid; c < whole; c += NT) {
@@ -334,6 +357,10 @@ void distill_kernel(DistillArgs a) {
       }
     }
     if (lone >= 0) elem_store<T>(out + lone, zero ? 0.f : by * ex(rest));
+  };
+  if (grad) {
+    if (far) write(exf);
+    else write(ex);
   }
   __syncthreads();  // the losses and the p are in LDS; the row's stores come before the entries'
   if (MODE != kParts && tid == 0) {
@@ -346,8 +373,9 @@ void distill_kernel(DistillArgs a) {
   for (int k = tid; k < K; k += NT) {
     const int i = s_i[k];
     if (i < lo || i >= hi) continue;
+    const float q = far ? exf(s_z[k]) : ex(s_z[k]);
     if (slots && !entered_twice(s_key, slots, i)) {
-      elem_store<T>(out + i, by * (ex(s_z[k]) - s_p[k]));
+      elem_store<T>(out + i, by * (q - s_p[k]));
       continue;
     }
     float p = 0.f;
@@ -359,7 +387,7 @@ void distill_kernel(DistillArgs a) {
       p += oi.z == i ? op.z : 0.f;
       p += oi.w == i ? op.w : 0.f;
     }
-    elem_store<T>(out + i, by * (ex(s_z[k]) - p));
+    elem_store<T>(out + i, by * (q - p));
   }
 }
 

@@ -478,6 +478,8 @@ halo_status halo_block_norm_bwd(const void* dr_out, int64_t lddr_out, const void
  * add their p.  Entries with p_k = 0 (t_k = -inf) add nothing.  A token without an entry, or
  * whose logits are all -inf, has loss 0 and gradient 0; a token with dloss 0 has gradient 0
  * whatever its logits.  An entry at a logit of -inf gives loss +inf.  NaN and +inf give NaN.
+ * Logits masked by a large negative value (-1e10, the type's lowest) weigh what the formula gives
+ * them: nothing beside live ones, and alike in a row that holds nothing else.
  *   logits   HALO_F32 or HALO_BF16 [tokens x vocab], ldl >= vocab.
  *   idx      int32 [tokens x top], ldi >= top;  tlogits HALO_F32 or HALO_BF16, ldt >= top;
  *            top is 1 .. 1024.
@@ -486,7 +488,8 @@ halo_status halo_block_norm_bwd(const void* dr_out, int64_t lddr_out, const void
  *   dloss    fp32 [tokens], the gradient of the token's loss (a mean over n tokens: 1 / n).
  *   dlogits  [tokens x vocab] of the logits' type, ldd >= vocab; may be logits (then ldd = ldl).
  * halo_distill_bwd takes the lse that the forward wrote; halo_distill_fwd_bwd does both from one
- * read of the logits.
+ * read of the logits.  Their gradients are the same bits while |lse| <= 4096; beyond, the joint
+ * call's q comes from the row's sum, and halo_distill_bwd's is as good as lse in fp32 (in [0, 1]).
  */
 halo_status halo_distill_fwd(const void* logits, halo_dtype logits_type, int64_t ldl,
                              const int32_t* idx, int64_t ldi, const void* tlogits,

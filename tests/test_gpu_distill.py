@@ -249,3 +249,76 @@ def test_many_entries_that_repeat(v, k, dt):
     repeats = torch.stack([torch.bincount(i[i >= 0].long(), minlength=v).max() for i in idx[:3]])
     assert (repeats <= -(-k // 8)).all()
     check_all(logits, idx, tl, dloss, 2.0)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.5, 3.0])
+@pytest.mark.parametrize("value", ["lowest", -1e30, -1e10])
+@pytest.mark.parametrize("v", [250, 2000, 9001, 70001, 140001])
+def test_most_of_the_vocabulary_masked(v, value, tau, dt):
+    """Masked places of a large negative value have weight exp(-1e10 / 3) = 0 whichever it is, so the
+    formula's values are those of -inf there, with the live logits' tolerances."""
+    print(f"vocabulary {v} value {value} temperature {tau} {dt}", flush=True)
+    logits, idx, tl, dloss = make(5, v, 12, dt, 31, missing=False)
+    dloss = dloss + 0.25
+    at = torch.arange(v, device=DEV)
+    live = torch.stack([at < 40, at >= v - 13, at % 97 == 3, (at < v // 8) | (at >= v - v // 8),
+                        (at // 8) % 2 == 0])
+    logits = torch.where(live, logits.float(), torch.finfo(dt).min if value == "lowest" else value).to(dt)
+    for row in range(5):                     # the teacher's entries are live
+        where = torch.nonzero(live[row])[:, 0]
+        idx[row] = where[torch.arange(12, device=DEV) % len(where)].to(torch.int32)
+    oracle = logits.masked_fill(~live, float("-inf"))
+    loss, lse = H.distill_fwd(logits, idx, tl, temperature=tau)
+    rl, tl_, re, te, rg, tg = ref64(oracle, idx, tl, tau, dloss)
+    within(lse, re, te, "lse")
+    within(loss, rl, tl_, "loss")
+    both = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=tau)
+    assert torch.equal(both[0], loss) and torch.equal(both[1], lse)
+    within(both[2], rg, tg, "gradient of the joint call")
+    assert (both[2][~live] == 0).all()
+    assert torch.equal(H.distill_bwd(dloss, logits, lse, idx, tl, temperature=tau), both[2])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("tau", [1.0, 1.5, 3.0])
+@pytest.mark.parametrize("v", [3, 250, 2000, 70001, 140001])
+def test_rows_of_one_value(v, tau, dt):
+    """A row whose logits are all the same has q = 1 / vocabulary, also where the value is the type's
+    lowest or so large that lse is the value itself.
+
+    Tolerances: the sum of exponentials carries at most 300 u (its chain of additions and 8 u each), so
+    log q 310 u beside u |log V| per rounding; lse rounds |value| / temperature three times.  Up to
+    4096 the gradient takes q from lse (8 u |lse|); beyond, from the sum itself."""
+    print(f"vocabulary {v} temperature {tau} {dt}", flush=True)
+    values = [torch.finfo(dt).min, -3e30, -1e10, -7.5e4, -1000.0, 0.0, 5.0, 6e4, 3e38]
+    t = len(values)
+    _, idx, tl, dloss = make(t, v, 9, dt, 41, missing=False)
+    dloss = dloss + 0.25
+    logits = torch.tensor(values, dtype=torch.float64, device=DEV)[:, None].expand(t, v).to(dt).contiguous()
+    c = logits[:, 0].double() / tau
+    logv = torch.log(torch.tensor(float(v), dtype=torch.float64)).item()
+    p = torch.softmax(tl.double() / tau, 1)
+    p_tol = (U * (64 + 8 * (tl.double() / tau).abs().amax(1) + 9 / 4))[:, None]
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=tau)
+    within(lse, c + logv, U * (4 * c.abs() + 4 * logv + 310), "lse")
+    tol = tau ** 2 * ((p * (p_tol + 16 * U) * (p.log().abs() + logv + 1)).sum(1) + 310 * U)
+    within(loss, tau ** 2 * (p * (p.log() + logv)).sum(1), tol, "loss")
+    l2, e2 = H.distill_fwd(logits, idx, tl, temperature=tau)
+    assert torch.equal(l2, loss) and torch.equal(e2, lse)
+    by = (dloss.double() * tau)[:, None]
+    spread = torch.zeros((t, v), dtype=torch.float64, device=DEV).scatter_add_(1, idx.long(), p)
+    want = by * (1 / v - spread)
+    size = lse.double().abs()[:, None]
+    e = U * (400 + 16 * logv + 8 * torch.where(size <= 4097, size, 0.0))
+    tol = by * (e / v + spread * p_tol) + ROUND[dt] * 1.01 * want.abs()
+    within(grad, want, tol, "gradient of the joint call")
+    # from lse alone: as good as lse is where that says something, and never outside 0 <= q <= 1
+    alone = H.distill_bwd(dloss, logits, lse, idx, tl, temperature=tau).double()
+    top = by * (1 - spread)
+    slack = by * spread * p_tol + ROUND[dt] * 1.01 * torch.maximum(top.abs(), (by * spread).abs())
+    assert ((alone >= -by * spread - slack) & (alone <= top + slack)).all()
+    near = size[:, 0] < 1e5
+    e = U * (400 + 16 * logv + 8 * size)
+    tol = by * (e / v * (1 + e) + spread * p_tol) + ROUND[dt] * 1.01 * (want.abs() + by * e / v)
+    within(alone[near], want[near], tol[near], "gradient")
