@@ -308,3 +308,42 @@ def test_an_infinite_gradient_stays_in_its_column(t, d, pad, dt):
             assert v[col] == float("inf"), inf_in
             v[col] = 0
             assert torch.isfinite(v).all(), inf_in
+
+
+# Widths that give every number of waves per token there is, each with whole chunks and with rows
+# that end inside one, at a prime number of tokens (the last team of a workgroup is then one too
+# many), and the widest rows.  bf16: a wave holds 512 elements per chunk of its lanes, fp32 256.
+WIDTHS = {BF16: [1000, 1003, 1600, 1603, 2600, 2603, 4000, 4003, 5000, 5003, 6000, 6003, 7000, 7003,
+                 8000, 8192, 8191],
+          F32: [500, 503, 800, 803, 1300, 1303, 2000, 2003, 2500, 2503, 3000, 3003, 3500, 3503, 4000, 4003,
+                4500, 4503, 5000, 5003, 5600, 5603, 6000, 6144, 6143]}
+
+
+@pytest.mark.parametrize("dt,d", [(dt, d) for dt in WIDTHS for d in WIDTHS[dt]])
+def test_every_number_of_waves(d, dt):
+    test_forward_and_backward(1031, d, 1, 0, dt)
+
+
+@pytest.mark.parametrize("t,d,groups,dt", [(3, 32768, 1, BF16), (5, 32767, 0, BF16), (2, 20001, 2, BF16),
+                                           (1100, 20000, 1, BF16), (1100, 9001, 1100, F32),
+                                           (1031, 1603, 1031, BF16), (1031, 2600, 1031, F32),
+                                           (2062, 800, 2, F32), (1300, 7000, 13, BF16)])
+def test_widest_rows_and_groups_of_many_tokens(t, d, groups, dt):
+    test_forward_and_backward(t, d, groups, 0, dt)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("post,pre", [(True, False), (False, True), (False, False), (True, True)])
+@pytest.mark.parametrize("d", [1600, 1603, 830])
+def test_in_place_with_a_team_too_many(d, post, pre, dt):
+    # two teams of two waves in a workgroup and an odd number of tokens, r_out in r's place
+    d = d // 2 if dt == F32 and d > 1000 else d
+    t = 1031
+    r, y = rnd((t, d), dt, 1, 3.0), rnd((t, d), dt, 2)
+    wp, wq = rnd((d,), dt, 3) if post else None, rnd((d,), dt, 4) if pre else None
+    want = H.block_norm_fwd(r, y, post_weight=wp, pre_weight=wq, scale=0.5)
+    rout, terms, rh, ra, rb = fwd64(r, y, None, wp, wq, 0.5, 1e-6)
+    check(want[0], rout, terms, dt, "r_out")
+    got = H.block_norm_fwd(r, y, post_weight=wp, pre_weight=wq, scale=0.5, r_out=r, h=y if pre else None)
+    for u, v in zip(got, want):
+        assert (u is None and v is None) or torch.equal(u, v)

@@ -85,8 +85,8 @@ def check_fwd(x, w, block, q, act, bias, res, y, z, yt):
     assert not bad.any(), ("y", int(bad.sum()), int(torch.nonzero(bad)[0][0]))
 
 
-# rows, columns, contraction, block: every kernel (few rows in 1, 2 and 4 tiles, 64, 128 and 256
-# tiles), whole and ragged tiles, whole and ragged contractions
+# rows, columns, contraction, block: up to 16 rows, waves that split the contraction, 128 and 256
+# tiles (64 ones: see the small tiles below), whole and ragged tiles, whole and ragged contractions
 SHAPES = [(1, 8, 32, 32), (1, 264, 4096, 256), (5, 40, 96, 32), (16, 512, 1000, 8), (17, 1000, 640, 64),
           (33, 72, 2048, 1024), (64, 136, 4128, 32), (65, 200, 512, 128), (203, 520, 1376, 32),
           (700, 1000, 256, 64), (1800, 2000, 160, 32), (1800, 2000, 256, 64),
@@ -316,3 +316,25 @@ def test_backward_inside_the_rotations(m, n, k, block, act, q, gq):
             assert torch.equal(u, v)
         rel = float((only[1].double() - dw.double()).norm() / dw.double().norm())
         assert rel <= 1e-3   # the stored dz: the same fp32 values, the same codes
+
+
+def tiles(m, n, t):
+    return -(-m // t) * -(-n // t)
+
+
+@pytest.mark.parametrize("q", [I8, E4M3])
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("m,n,k,block", [(400, 4096, 512, 64), (1000, 1096, 160, 32), (333, 4104, 96, 32),
+                                         (450, 2400, 256, 64), (257, 4096, 384, 128), (700, 1928, 1152, 128),
+                                         (520, 2056, 1376, 32)])
+def test_forward_on_the_small_tiles(m, n, k, block, dt, q):
+    # more 64 x 64 tiles than compute units and too few 128 x 128 ones: the 64 x 64 tile kernel;
+    # contractions of one to eleven 128-byte slabs (its ring holds four), whole and ragged
+    assert tiles(m, n, 64) > 256 and tiles(m, n, 128) < 224
+    test_forward(m, n, k, block, dt, q)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_parts_of_the_epilogue_on_the_small_tiles(act):
+    assert tiles(700, 1928, 64) > 256 and tiles(700, 1928, 128) < 224
+    test_parts_of_the_epilogue(700, act)
