@@ -62,7 +62,9 @@ __device__ __forceinline__ float slope_of(float z) {
   }
   if constexpr (ACT == kActGeluTanh) {
     const float p = sigmoid_fast(gelu_arg(z));
-    const float du = __builtin_fmaf(z * z, 3.f * 0.07135481627159f, 1.5957691216057308f);
+    // z^2 would be infinite, and zero times it NaN, from 1.8e19 on, where p (1 - p) is long 0
+    const float zz = fminf(z * z, 1e30f);
+    const float du = __builtin_fmaf(zz, 3.f * 0.07135481627159f, 1.5957691216057308f);
     return __builtin_fmaf(z * (p * (1.f - p)), du, p);
   }
   if constexpr (ACT == kActGeluErf) {

@@ -338,3 +338,34 @@ def test_forward_on_the_small_tiles(m, n, k, block, dt, q):
 def test_parts_of_the_epilogue_on_the_small_tiles(act):
     assert tiles(700, 1928, 64) > 256 and tiles(700, 1928, 128) < 224
     test_parts_of_the_epilogue(700, act)
+
+
+# finite z whose square, cube or exponential passes the type's range
+FAR = [30.0, 1e4, 1e10, 1.9e19, 1e20, 1e30, 3e38]
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("act", ACTS[1:])
+def test_activations_and_slopes_far_out(act, dt):
+    """z so large that every activation is z or 0 and every slope 1 or 0, to the last bit: the nearest,
+    gelu at -30, is 30 exp(-450)."""
+    v = torch.tensor(FAR + [-f for f in FAR], dtype=torch.float64, device=DEV).to(dt)
+    n, k, block = v.numel() + 2, 64, 64
+    bias = torch.zeros(n, dtype=dt, device=DEV)
+    bias[:v.numel()] = v
+    w = rnd((n, k), dt, 1)
+    for m in (1, 40):                      # rows of zeros: z is the bias
+        x = torch.zeros((m, k), dtype=dt, device=DEV)
+        y, z = H.linear_act_fwd(x, w, block, bias=bias, activation=act, want_z=True)
+        assert torch.equal(z, bias.expand(m, n))
+        assert ((y.double() - z.double().clamp(min=0)).abs() <= 1e-11).all()
+    want = (v > 0).to(dt)
+    for m in (1, 128):                     # 128 rows: dz inside the rotations (bf16)
+        z = bias.expand(m, n).contiguous()
+        dy = torch.zeros((m, n), dtype=dt, device=DEV)
+        dy[0] = 1
+        dx, dw, db = H.linear_act_bwd(dy, z, rnd((m, k), dt, 2), w, block, activation=act)
+        assert ((db[:v.numel()] - want).abs() <= 1e-9).all()
+        assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+        only = H.linear_act_bwd(dy, z, rnd((m, k), dt, 2), w, block, activation=act, want_dw=False)
+        assert torch.equal(only[2], db) and torch.isfinite(only[0]).all()
