@@ -172,6 +172,30 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# The current device's index; torch's own handle, where this torch has it, at a fraction of
+# torch.cuda.current_device's time.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _off_device(t):
+    """Whether a tensor is on a GPU that is not the current device: the library launches on the
+    current one."""
+    return t.is_cuda and t.device.index != _current_device()
+
+
+def _on(stream, device, call, *args, **kw):
+    """call(..) with `device` the current device and `stream` (None: the device's current one) its
+    current stream, so that the kernels run on the tensors' device and the outputs and workspaces
+    they need belong to the stream they run on: the allocator hands out memory in the order of one
+    stream's work."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif not (isinstance(stream, torch.cuda.Stream) and stream.device == device):
+        raise ValueError(f"stream must be a torch.cuda.Stream of {device}")
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
+
+
 def _check(status, what):
     if status != 0:
         raise HaloError(status, what)
@@ -296,6 +320,10 @@ def fwht_quant(x, axis=ROWS, block=256, q_dtype=torch.int8, q=None, scale=None, 
     codes); 0 = the library's default.
     """
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
+    if _off_device(x):
+        return _on(stream, x.device, fwht_quant, x, axis, block, q_dtype, q, scale, workspace,
+                   signs=signs, rounding=rounding, seed=seed, counter=counter,
+                   exchange_polls=exchange_polls)
     rows, cols = x.shape
     nvec, L = (rows, cols) if axis == ROWS else (cols, rows)
     Lp = padded_len(L, block)
@@ -355,6 +383,11 @@ def fwht_quant_dual(x, block=256, q_dtype=torch.int8, qr=None, scale_r=None, qc=
     fwht_quant (the counter of each pass its own).  `workspace`: the scratch, allocated here
     when None; False runs without it."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
+    if _off_device(x):
+        return _on(stream, x.device, fwht_quant_dual, x, block, q_dtype, qr, scale_r, qc, scale_c,
+                   workspace, row_signs=row_signs, col_signs=col_signs, rounding=rounding,
+                   seed=seed, row_counter=row_counter, col_counter=col_counter,
+                   exchange_polls=exchange_polls)
     rows, cols = x.shape
     if qr is None:
         qr = torch.empty((rows, padded_len(cols, block)), dtype=q_dtype, device=x.device)
@@ -403,6 +436,8 @@ MFMA_PROBE_KINDS = {0: "v_mfma_i32_32x32x32_i8", 1: "v_mfma_scale_f32_32x32x64_f
 def mfma_rate_probe(kind, iters, stream=None):
     """One launch of the matrix-core rate probe (halo_mfma_rate_probe) on `stream`; returns the
     operations it performs.  A measurement aid: time it with events on the same stream."""
+    if stream is not None and stream.device.index != _current_device():
+        return _on(stream, stream.device, mfma_rate_probe, kind, iters)
     ops = ctypes.c_int64(0)
     _check(lib().halo_mfma_rate_probe(int(kind), int(iters), ctypes.byref(ops), _stream(stream)),
            "halo_mfma_rate_probe")
@@ -415,6 +450,9 @@ def fwht_quant_noalloc(x, q, scale, axis=ROWS, block=256, stream=None, signs=Non
     a workspace (halo_fwht_quant_noalloc): nothing is allocated.  Calls that may overlap on one
     device share that scratch and must be ordered by the caller."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
+    if _off_device(x):
+        return _on(stream, x.device, fwht_quant_noalloc, x, q, scale, axis, block, signs=signs,
+                   rounding=rounding, seed=seed, counter=counter, exchange_polls=exchange_polls)
     rows, cols = x.shape
     nvec, L = (rows, cols) if axis == ROWS else (cols, rows)
     Lp = padded_len(L, block)
@@ -439,6 +477,8 @@ def gemm_i8(a, sa, b, sb, out_dtype=torch.bfloat16, c=None, stream=None):
     """c = (a . b^T) * sa[:, None] * sb[None, :] with int8 codes (int32 raw if out is int32)."""
     _require(isinstance(a, torch.Tensor) and a.dim() == 2 and isinstance(b, torch.Tensor)
              and b.dim() == 2, "a and b must be 2-D tensors")
+    if _off_device(a):
+        return _on(stream, a.device, gemm_i8, a, sa, b, sb, out_dtype, c)
     m, k = a.shape
     n = b.shape[0]
     _matrix(b, "b", (n, k))
@@ -459,6 +499,8 @@ def gemm_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, c=None, stream=None):
     """c = (dec(a) . dec(b)^T) * sa[:, None] * sb[None, :] with fp8 codes (E4M3 / E5M2)."""
     _require(isinstance(a, torch.Tensor) and a.dim() == 2 and isinstance(b, torch.Tensor)
              and b.dim() == 2, "a and b must be 2-D tensors")
+    if _off_device(a):
+        return _on(stream, a.device, gemm_fp8, a, sa, b, sb, out_dtype, c)
     m, k = a.shape
     n = b.shape[0]
     _matrix(b, "b", (n, k))
@@ -497,6 +539,9 @@ def linear_fwd(x, w, block, q_dtype=torch.int8, y=None, y_dtype=None, workspace=
     signs_k: the randomised transform's sign words along K (see hadamard_signs) or None."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor)
              and w.dim() == 2, "x and w must be 2-D tensors")
+    if _off_device(x):
+        return _on(stream, x.device, linear_fwd, x, w, block, q_dtype, y, y_dtype, workspace,
+                   signs_k=signs_k)
     m, k = x.shape
     n = w.shape[0]
     _matrix(x, "x", (m, k), contiguous=True)
@@ -531,6 +576,11 @@ def linear_bwd(dy, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, want_dx=T
     exchange_polls: as in fwht_quant, for the columns along m."""
     _require(all(isinstance(t, torch.Tensor) and t.dim() == 2 for t in (dy, x, w)),
              "dy, x and w must be 2-D tensors")
+    if _off_device(x):
+        return _on(stream, x.device, linear_bwd, dy, x, w, block, q_dtype, grad_q_dtype, want_dx,
+                   want_dw, dx, dw, workspace, signs_n=signs_n, signs_m=signs_m,
+                   grad_rounding=grad_rounding, seed=seed, counter=counter,
+                   exchange_polls=exchange_polls)
     m, k = x.shape
     n = w.shape[0]
     _matrix(x, "x", (m, k), contiguous=True)
@@ -618,16 +668,6 @@ def _current_stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _on(stream, device, call, *args, **kw):
-    """call(..) with `stream` as the current one of `device`, so that the outputs and workspaces
-    it allocates belong to the stream its kernels run on: the allocator hands out memory in the
-    order of one stream's work."""
-    if not (isinstance(stream, torch.cuda.Stream) and stream.device == device):
-        raise ValueError(f"stream must be a torch.cuda.Stream of {device}")
-    with torch.cuda.stream(stream):
-        return call(*args, **kw)
-
-
 def _dense_like(t):
     """A new contiguous tensor of t's shape, type and device."""
     return torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -652,7 +692,7 @@ def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scal
     and for the fp32 factors of norms that were not asked for.
     """
     dt, dev = _io_2d(r, "r")
-    if stream is not None:
+    if stream is not None or _off_device(r):
         return _on(stream, dev, block_norm_fwd, r, y, gate, post_weight, pre_weight, scale, eps,
                    r_out, h)
     t, d = shape = r.shape
@@ -706,7 +746,7 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
     [groups, dim].  The parameter gradients are fp32 sums in a fixed order, rounded once."""
     ref = dr_out if dr_out is not None else dh
     dt, dev = _io_2d(ref, "dr_out" if dr_out is not None else "dh")
-    if stream is not None:
+    if stream is not None or _off_device(ref):
         return _on(stream, dev, block_norm_bwd, dr_out, dh, r_out, y, gate, post_weight,
                    pre_weight, rstd_post, rstd_pre, scale, dr, dy, want_dgate, want_dpost,
                    want_dpre, workspace)
@@ -793,7 +833,7 @@ def distill_fwd(logits, idx, tlogits, temperature=1.0, loss=None, lse=None, stre
     vocabulary, such as -1, is no entry) and q the softmax of the student's logits, both at the
     temperature.  Returns (loss, lse), fp32 per token; lse = log sum exp(logits / temperature)."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None:
+    if stream is not None or _off_device(logits):
         return _on(stream, dev, distill_fwd, logits, idx, tlogits, temperature, loss, lse)
     loss = _out_vec(loss, "loss", t, dev)
     lse = _out_vec(lse, "lse", t, dev)
@@ -815,7 +855,7 @@ def distill_bwd(dloss, logits, lse, idx, tlogits, temperature=1.0, dlogits=None,
     """Gradient of distill_fwd for the logits: dloss[t] * temperature * (q - p) per token, from
     the forward's lse.  dlogits may be logits itself."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None:
+    if stream is not None or _off_device(logits):
         return _on(stream, dev, distill_bwd, dloss, logits, lse, idx, tlogits, temperature,
                    dlogits)
     _vec(dloss, "dloss", t, torch.float32, dev)
@@ -837,7 +877,7 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
     token's weight in the loss beforehand (dloss; 0 leaves a token out).  Returns (loss, lse,
     dlogits); dlogits may be logits itself."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None:
+    if stream is not None or _off_device(logits):
         return _on(stream, dev, distill_fwd_bwd, logits, idx, tlogits, dloss, temperature, loss,
                    lse, dlogits)
     _vec(dloss, "dloss", t, torch.float32, dev)
@@ -899,7 +939,7 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
     (y, z) when the pre-activation is wanted (want_z or a z to write it to): linear_act_bwd takes
     it.  residual may be y itself."""
     dt, dev = _io_2d(x, "x")
-    if stream is not None:
+    if stream is not None or _off_device(x):
         return _on(stream, dev, linear_act_fwd, x, w, block, q_dtype, bias, activation, residual,
                    y, y_dtype, want_z, z, workspace, signs_k=signs_k)
     if not (isinstance(w, torch.Tensor) and w.dim() == 2):
@@ -942,7 +982,7 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
     least).  Only x is rotated and quantised here; up to 16 rows of x take a kernel bound by
     reading qw once.  Returns y (and z when a z to write it to is given)."""
     dt, dev = _io_2d(x, "x")
-    if stream is not None:
+    if stream is not None or _off_device(x):
         return _on(stream, dev, linear_act_q, x, qw, sw, block, bias, activation, residual, y,
                    y_dtype, z, workspace, signs_k=signs_k)
     m, k = x.shape
@@ -993,7 +1033,7 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
     activation "none".  The residual's gradient is dy.  Returns (dx, dw, db), None where not
     wanted; options as linear_bwd."""
     dt, dev = _io_2d(dy, "dy")
-    if stream is not None:
+    if stream is not None or _off_device(dy):
         return _on(stream, dev, linear_act_bwd, dy, z, x, w, block, q_dtype, grad_q_dtype,
                    activation, want_dx, want_dw, want_db, dx, dw, db, workspace, signs_n=signs_n,
                    signs_m=signs_m, grad_rounding=grad_rounding, seed=seed, counter=counter,
