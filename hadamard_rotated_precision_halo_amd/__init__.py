@@ -320,7 +320,7 @@ def fwht_quant(x, axis=ROWS, block=256, q_dtype=torch.int8, q=None, scale=None, 
     codes); 0 = the library's default.
     """
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
-    if _off_device(x):
+    if stream is not None or _off_device(x):
         return _on(stream, x.device, fwht_quant, x, axis, block, q_dtype, q, scale, workspace,
                    signs=signs, rounding=rounding, seed=seed, counter=counter,
                    exchange_polls=exchange_polls)
@@ -383,7 +383,7 @@ def fwht_quant_dual(x, block=256, q_dtype=torch.int8, qr=None, scale_r=None, qc=
     fwht_quant (the counter of each pass its own).  `workspace`: the scratch, allocated here
     when None; False runs without it."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
-    if _off_device(x):
+    if stream is not None or _off_device(x):
         return _on(stream, x.device, fwht_quant_dual, x, block, q_dtype, qr, scale_r, qc, scale_c,
                    workspace, row_signs=row_signs, col_signs=col_signs, rounding=rounding,
                    seed=seed, row_counter=row_counter, col_counter=col_counter,
@@ -450,7 +450,7 @@ def fwht_quant_noalloc(x, q, scale, axis=ROWS, block=256, stream=None, signs=Non
     a workspace (halo_fwht_quant_noalloc): nothing is allocated.  Calls that may overlap on one
     device share that scratch and must be ordered by the caller."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor")
-    if _off_device(x):
+    if stream is not None or _off_device(x):
         return _on(stream, x.device, fwht_quant_noalloc, x, q, scale, axis, block, signs=signs,
                    rounding=rounding, seed=seed, counter=counter, exchange_polls=exchange_polls)
     rows, cols = x.shape
@@ -477,7 +477,7 @@ def gemm_i8(a, sa, b, sb, out_dtype=torch.bfloat16, c=None, stream=None):
     """c = (a . b^T) * sa[:, None] * sb[None, :] with int8 codes (int32 raw if out is int32)."""
     _require(isinstance(a, torch.Tensor) and a.dim() == 2 and isinstance(b, torch.Tensor)
              and b.dim() == 2, "a and b must be 2-D tensors")
-    if _off_device(a):
+    if stream is not None or _off_device(a):
         return _on(stream, a.device, gemm_i8, a, sa, b, sb, out_dtype, c)
     m, k = a.shape
     n = b.shape[0]
@@ -499,7 +499,7 @@ def gemm_fp8(a, sa, b, sb, out_dtype=torch.bfloat16, c=None, stream=None):
     """c = (dec(a) . dec(b)^T) * sa[:, None] * sb[None, :] with fp8 codes (E4M3 / E5M2)."""
     _require(isinstance(a, torch.Tensor) and a.dim() == 2 and isinstance(b, torch.Tensor)
              and b.dim() == 2, "a and b must be 2-D tensors")
-    if _off_device(a):
+    if stream is not None or _off_device(a):
         return _on(stream, a.device, gemm_fp8, a, sa, b, sb, out_dtype, c)
     m, k = a.shape
     n = b.shape[0]
@@ -539,7 +539,7 @@ def linear_fwd(x, w, block, q_dtype=torch.int8, y=None, y_dtype=None, workspace=
     signs_k: the randomised transform's sign words along K (see hadamard_signs) or None."""
     _require(isinstance(x, torch.Tensor) and x.dim() == 2 and isinstance(w, torch.Tensor)
              and w.dim() == 2, "x and w must be 2-D tensors")
-    if _off_device(x):
+    if stream is not None or _off_device(x):
         return _on(stream, x.device, linear_fwd, x, w, block, q_dtype, y, y_dtype, workspace,
                    signs_k=signs_k)
     m, k = x.shape
@@ -576,7 +576,7 @@ def linear_bwd(dy, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, want_dx=T
     exchange_polls: as in fwht_quant, for the columns along m."""
     _require(all(isinstance(t, torch.Tensor) and t.dim() == 2 for t in (dy, x, w)),
              "dy, x and w must be 2-D tensors")
-    if _off_device(x):
+    if stream is not None or _off_device(x):
         return _on(stream, x.device, linear_bwd, dy, x, w, block, q_dtype, grad_q_dtype, want_dx,
                    want_dw, dx, dw, workspace, signs_n=signs_n, signs_m=signs_m,
                    grad_rounding=grad_rounding, seed=seed, counter=counter,

@@ -56,7 +56,7 @@ def calls(dev):
     bf, f32, i8 = torch.bfloat16, torch.float32, torch.int8
     x, w, dy = (torch.empty(s, dtype=bf, device=dev) for s in ((64, 128), (32, 128), (64, 32)))
     v, b = torch.empty(128, dtype=bf, device=dev), torch.empty(32, dtype=bf, device=dev)
-    one, s128 = torch.empty(64, device=dev), torch.empty(128, device=dev)
+    one, sw = torch.empty(64, device=dev), torch.empty(32, device=dev)
     q, qw, e = (torch.empty(s, dtype=t, device=dev) for s, t in (((64, 128), i8), ((32, 128), i8),
                                                                  ((64, 128), torch.float8_e4m3fn)))
     idx, tl = torch.empty((64, 4), dtype=torch.int32, device=dev), torch.empty((64, 4), device=dev)
@@ -74,7 +74,7 @@ def calls(dev):
         "distill_bwd": lambda **k: H.distill_bwd(one, x, one, idx, tl, **k),
         "distill_fwd_bwd": lambda **k: H.distill_fwd_bwd(x, idx, tl, one, **k),
         "linear_act_fwd": lambda **k: H.linear_act_fwd(x, w, 64, bias=b, want_z=True, **k),
-        "linear_act_q": lambda **k: H.linear_act_q(x, qw, torch.empty(32, device=dev), 64, **k),
+        "linear_act_q": lambda **k: H.linear_act_q(x, qw, sw, 64, **k),
         "linear_act_bwd": lambda **k: H.linear_act_bwd(dy, dy, x, w, 32, activation="silu", **k),
     }
 
@@ -95,8 +95,7 @@ def machine(monkeypatch):
 @pytest.mark.parametrize("name", NAMES)
 def test_a_call_launches_on_its_tensors_device(machine, name, index):
     out = calls(f"cuda:{index}")[name]()
-    launched = [l for l in machine.launches]
-    assert [l[1:] for l in launched] == [(index, 100 + index)], launched
+    assert [l[1:] for l in machine.launches] == [(index, 100 + index)]
     assert machine.switches == (0 if index == 0 else 1)      # nothing to switch on the current device
     assert machine.device == 0                               # and the current device is the caller's again
     for t in out if isinstance(out, tuple) else (out,):
@@ -109,3 +108,24 @@ def test_the_rate_probe_launches_on_its_streams_device(machine, monkeypatch):
     H.mfma_rate_probe(0, 4, stream=other)
     H.mfma_rate_probe(0, 4)
     assert [l[1:] for l in machine.launches] == [(1, 101), (0, 100)] and machine.device == 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_call_given_a_stream_allocates_on_it(machine, monkeypatch, name):
+    """The allocator may hand on memory as soon as its stream's work reaches the point where it was
+    freed: outputs and workspaces of another stream than the kernels' could be handed on early."""
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    call, at = calls("cuda:0")[name], []
+    side = machine.current_stream("cuda:0")
+    side.cuda_stream = 777
+    for n in ("empty", "empty_like"):
+        def spy(*a, real=getattr(torch, n), **k):
+            at.append(machine.streams[machine.device])
+            return real(*a, **k)
+        monkeypatch.setattr(torch, n, spy)
+    call(stream=side)
+    assert machine.launches[-1][1:] == (0, 777) and machine.streams[0] == 100
+    assert set(at) <= {777} and (at or name == "fwht_quant_noalloc"), at
+    other = machine.current_stream("cuda:1")
+    with pytest.raises(ValueError, match="stream"):
+        call(stream=other)
