@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256) void part_sum_kernel(const float* part, int64_
 }
 
 int64_t rows_per(int64_t m, int64_t n) {
-  const int64_t strips = (n + kCols - 1) / kCols;
+  const int64_t strips = n > 0 ? (n + kCols - 1) / kCols : 1;
   const int64_t want = (2048 + strips - 1) / strips;  // about 2048 workgroups in all
   const int64_t rows = (m + want - 1) / want;
   return rows < 16 ? 16 : rows;

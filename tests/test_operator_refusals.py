@@ -290,3 +290,16 @@ def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
             assert (a is None and b is None) or torch.equal(a, b), n
         with pytest.raises(ValueError):
             call(stream=side.cuda_stream)
+
+
+def test_workspace_of_an_empty_layer(L):
+    # no rows, no outputs, no contraction: sizes, not a division by zero
+    q = L.halo_linear_act_bwd_workspace_bytes
+    for m, n, k in ((0, 128, 64), (64, 0, 64), (64, 128, 0), (0, 0, 0)):
+        assert q(m, n, k, 64, I8) == L.halo_linear_workspace_bytes_ex(m, n, k, 64, I8, 1) \
+            + (0 if m == 0 or n == 0 else 64 * 128 * 4 + 4 * 128 * 4)
+        assert L.halo_linear_act_q_workspace_bytes(m, k, 64) == 64 * ((m * k + 255) // 256 * 4) \
+            + (m * 4 + 255) // 256 * 256
+    assert L.halo_block_norm_bwd_workspace_bytes(0, 64, 1, BF16) == 0
+    assert L.halo_block_norm_bwd_workspace_bytes(4, 0, 1, BF16) == 0
+    assert L.halo_block_norm_bwd_workspace_bytes(4, 64, 0, BF16) == 0
