@@ -37,7 +37,8 @@ EXPORTS = ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
            "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_block_norm_bwd_workspace_bytes",
            "halo_distill_fwd", "halo_distill_bwd", "halo_distill_fwd_bwd",
            "halo_linear_act_fwd", "halo_linear_act_q", "halo_linear_act_q_workspace_bytes",
-           "halo_linear_act_bwd", "halo_linear_act_bwd_workspace_bytes")
+           "halo_linear_act_bwd", "halo_linear_act_bwd_workspace_bytes",
+           "halo_linear_act_bwd_workspace_bytes_ex")
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu_erf": 4}  # halo_activation
 
 
@@ -132,6 +133,8 @@ def lib():
                                         vp]
         L.halo_linear_act_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, e]
         L.halo_linear_act_bwd_workspace_bytes.restype = sz
+        L.halo_linear_act_bwd_workspace_bytes_ex.argtypes = [i64, i64, i64, i32, e, e, e, i32, e]
+        L.halo_linear_act_bwd_workspace_bytes_ex.restype = sz
         L.halo_linear_act_bwd.argtypes = [vp, vp, e, vp, vp, e, i64, i64, i64, i32, e, e, vp, vp,
                                           vp, lo, vp, sz, vp]
         L.halo_status_str.argtypes = [e]
@@ -1020,8 +1023,16 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
     return y if z is None else (y, z)
 
 
-def linear_act_bwd_workspace_bytes(m, n, k, block, q_dtype=torch.int8):
-    return int(lib().halo_linear_act_bwd_workspace_bytes(m, n, k, int(block), _code(q_dtype)))
+def linear_act_bwd_workspace_bytes(m, n, k, block, q_dtype=torch.int8, dtype=None,
+                                   activation="none", want_dx=True, want_dw=True, want_db=True,
+                                   grad_rounding="nearest"):
+    """Workspace bytes of linear_act_bwd: for a call on tensors of dtype with these arguments, or,
+    with dtype None, for every form."""
+    if dtype is None:
+        return int(lib().halo_linear_act_bwd_workspace_bytes(m, n, k, int(block), _code(q_dtype)))
+    return int(lib().halo_linear_act_bwd_workspace_bytes_ex(
+        m, n, k, int(block), _code(dtype), _code(q_dtype), _activation(activation),
+        1 * bool(want_dx) + 2 * bool(want_dw) + 4 * bool(want_db), _rounding(grad_rounding)))
 
 
 def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, activation="none",
@@ -1068,8 +1079,9 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
         opts = ctypes.byref(LinearOpts(None, _p(signs_n), _p(signs_m), rnd, _u32x2(seed),
                                        _u32x2(counter), int(exchange_polls)))
     L, qc = lib(), _code(q_dtype)
-    ws = _scratch(workspace, L.halo_linear_act_bwd_workspace_bytes(m, n, k, int(block), qc)
-                  if workspace is None else 0, dy)
+    ws = _scratch(workspace, L.halo_linear_act_bwd_workspace_bytes_ex(
+        m, n, k, int(block), _TORCH_CODE[dt], qc, act, 1 * bool(want_dx) + 2 * bool(want_dw)
+        + 4 * bool(want_db), rnd) if workspace is None else 0, dy)
     st = L.halo_linear_act_bwd(_p(dy), _p(z), act, _p(x), _p(w), _TORCH_CODE[dt], m, n, k,
                                int(block), qc, _code(grad_q_dtype or q_dtype),
                                _p(dx) if want_dx else None, _p(dw) if want_dw else None,

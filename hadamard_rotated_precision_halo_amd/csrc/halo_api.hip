@@ -426,17 +426,33 @@ struct ActGrad {
 
 // Whether the backward forms dz = dy act'(z) inside its rotation passes: the one-launch batch of
 // bf16 passes, both products, nearest rounding.
-bool act_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
-                  halo_dtype q_type, halo_dtype grad_q_type, const void* dx, const void* dw,
-                  const halo_linear_opts* opts) {
+bool act_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block, bool dx,
+                  bool dw, bool stochastic) {
   const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
   const WsPlan p = plan_ws(m, n, k, 1, block);
   return dx && dw && io_type == HALO_BF16 && fq_act_block_ok(block) &&
-         !(opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC) &&
+         !stochastic &&
          fq_rows2_supported(nq, block) && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
          fq_cols2_supported(mq, n, block, 1, false, p.scr_dy) &&
          fq_cols2_supported(mq, k, block, 1, false, p.scr_x) &&
          act_grad_parts(m, n) >= (fq_act_parts(mq, block) > 1 ? fq_act_parts(mq, block) : 1);
+}
+
+// Workspace of a layer backward with its activation: the layer's, then a stored dz (where the
+// rotation passes do not form it) and the bias gradient's partial rows.
+struct ActBwdWs {
+  bool fused;
+  size_t dz, part, total;  // byte offsets, and the whole
+};
+
+ActBwdWs act_bwd_ws(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block, bool act,
+                    bool dx, bool dw, bool db, bool stochastic) {
+  ActBwdWs w{};
+  w.fused = act && act_fused_ok(io_type, m, n, k, block, dx, dw, stochastic);
+  w.dz = plan_ws(m, n, k, 1, block).total;
+  w.part = w.dz + (act && !w.fused ? round256((size_t)m * n * 4) : 0);
+  w.total = w.part + (db ? round256((size_t)act_grad_parts(m, n) * n * 4) : 0);
+  return w;
 }
 
 // The layer backward on validated arguments: the rotation passes of dY (of type dy_type), W and X
@@ -1053,6 +1069,21 @@ size_t halo_linear_act_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int3
   return layer + round256((size_t)m * n * 4) + round256((size_t)act_grad_parts(m, n) * n * 4);
 }
 
+size_t halo_linear_act_bwd_workspace_bytes_ex(int64_t m, int64_t n, int64_t k, int32_t block,
+                                              halo_dtype io_type, halo_dtype q_type,
+                                              halo_activation activation, int32_t gradients,
+                                              halo_rounding grad_rounding) {
+  if (!dtype_ok(io_type) || (io_type != HALO_F32 && io_type != HALO_BF16)) return 0;
+  if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return 0;
+  if (!enum_in(grad_rounding, HALO_ROUND_NEAREST_EVEN, HALO_ROUND_STOCHASTIC)) return 0;
+  if (gradients & ~(HALO_GRAD_DX | HALO_GRAD_DW | HALO_GRAD_DB)) return 0;
+  if (halo_linear_workspace_bytes_ex(m, n, k, block, q_type, 1) == 0) return 0;
+  return act_bwd_ws(io_type, m, n, k, block, activation != HALO_ACT_NONE, gradients & HALO_GRAD_DX,
+                    gradients & HALO_GRAD_DW, gradients & HALO_GRAD_DB,
+                    grad_rounding == HALO_ROUND_STOCHASTIC)
+      .total;
+}
+
 halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation activation,
                                 const void* x, const void* w, halo_dtype io_type, int64_t m,
                                 int64_t n, int64_t k, int32_t block, halo_dtype q_type,
@@ -1067,14 +1098,14 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
   if (s != HALO_OK) return s;
   if (act && !z) return HALO_ERR_NULL;
   if (!aligned16(z) || !aligned16(db)) return HALO_ERR_ALIGN;
-  if (!ws || ws_bytes < halo_linear_act_bwd_workspace_bytes(m, n, k, block, q_type))
-    return HALO_ERR_WORKSPACE;
+  const ActBwdWs wl = act_bwd_ws(io_type, m, n, k, block, act, dx, dw, db,
+                                 opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC);
+  if (!ws || ws_bytes < wl.total) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
   const hipStream_t st = (hipStream_t)stream;
-  char* tail = static_cast<char*>(ws) + plan_ws(m, n, k, 1, block).total;
-  float* dz = reinterpret_cast<float*>(tail);
-  float* part = reinterpret_cast<float*>(tail + round256((size_t)m * n * 4));
-  if (act && act_fused_ok(io_type, m, n, k, block, q_type, grad_q_type, dx, dw, opts)) {
+  float* dz = reinterpret_cast<float*>(static_cast<char*>(ws) + wl.dz);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + wl.part);
+  if (wl.fused) {
     ActGrad ag;
     ag.z = z;
     ag.act = (int)activation;

@@ -397,12 +397,21 @@ halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw,
  * fp32 in a fixed order and is rounded once to io_type.
  *   z            the forward's z (io_type, dense); not read with HALO_ACT_NONE (may be NULL).
  *   dx, dw, db   each may be NULL to skip it; db [n].
- *   ws           at least halo_linear_act_bwd_workspace_bytes(...) bytes.
+ *   ws           at least halo_linear_act_bwd_workspace_bytes_ex(...) bytes for the call's own
+ *                types, activation, gradients and rounding;
+ *                halo_linear_act_bwd_workspace_bytes(...) is enough for every form.
  * Everything else as halo_linear_bwd_ex (with an activation, the dX product's padded n is limited
  * under stochastic rounding as for fp32 dY).
  */
+#define HALO_GRAD_DX 1 /* the gradients a call asks for, as bits */
+#define HALO_GRAD_DW 2
+#define HALO_GRAD_DB 4
 size_t halo_linear_act_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
                                            halo_dtype q_type);
+size_t halo_linear_act_bwd_workspace_bytes_ex(int64_t m, int64_t n, int64_t k, int32_t block,
+                                              halo_dtype io_type, halo_dtype q_type,
+                                              halo_activation activation, int32_t gradients,
+                                              halo_rounding grad_rounding);
 halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation activation,
                                 const void* x, const void* w, halo_dtype io_type, int64_t m,
                                 int64_t n, int64_t k, int32_t block, halo_dtype q_type,

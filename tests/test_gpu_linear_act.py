@@ -369,3 +369,26 @@ def test_activations_and_slopes_far_out(act, dt):
         assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
         only = H.linear_act_bwd(dy, z, rnd((m, k), dt, 2), w, block, activation=act, want_dw=False)
         assert torch.equal(only[2], db) and torch.isfinite(only[0]).all()
+
+
+@pytest.mark.parametrize("kw,dt", [(dict(activation="silu"), BF16), (dict(activation="silu"), F32),
+                                   (dict(activation="silu", want_db=False), BF16),
+                                   (dict(activation="gelu_erf", want_dw=False), BF16),
+                                   (dict(activation="gelu_erf", want_dx=False, want_db=False), BF16),
+                                   (dict(activation="relu", want_dx=False, want_dw=False), F32),
+                                   (dict(), BF16), (dict(want_db=False), F32),
+                                   (dict(activation="gelu_tanh", grad_rounding="stochastic"), BF16)])
+@pytest.mark.parametrize("m,n,k,block", [(300, 520, 264, 64), (4500, 256, 136, 128), (64, 128, 64, 32)])
+def test_backward_in_its_own_workspace(m, n, k, block, kw, dt):
+    x, w = rnd((m, k), dt, 1), rnd((n, k), dt, 2, k ** -0.5)
+    z, dy = rnd((m, n), dt, 3, 1.5), rnd((m, n), dt, 4, 1e-3)
+    need = H.linear_act_bwd_workspace_bytes(m, n, k, block, torch.int8, dt, **kw)
+    assert need <= H.linear_act_bwd_workspace_bytes(m, n, k, block)
+    room = torch.full((need + 4096,), 77, dtype=torch.uint8, device=DEV)
+    want = H.linear_act_bwd(dy, z, x, w, block, **kw)
+    got = H.linear_act_bwd(dy, z, x, w, block, workspace=room[:need], **kw)
+    for u, v in zip(got, want):
+        assert (u is None and v is None) or torch.equal(u, v)
+    assert (room[need:] == 77).all()
+    with pytest.raises(H.HaloError, match="WORKSPACE"):
+        H.linear_act_bwd(dy, z, x, w, block, workspace=room[:need - 1], **kw)

@@ -303,3 +303,31 @@ def test_workspace_of_an_empty_layer(L):
     assert L.halo_block_norm_bwd_workspace_bytes(0, 64, 1, BF16) == 0
     assert L.halo_block_norm_bwd_workspace_bytes(4, 0, 1, BF16) == 0
     assert L.halo_block_norm_bwd_workspace_bytes(4, 64, 0, BF16) == 0
+
+
+def test_workspace_of_a_gradients_own_form(L):
+    """What a call must bring: the layer's workspace, a stored dz only where the rotation passes do not
+    form it, partial rows only for a bias gradient."""
+    every, own = L.halo_linear_act_bwd_workspace_bytes, L.halo_linear_act_bwd_workspace_bytes_ex
+    m, n, k, silu, none = 512, 1024, 256, 2, 0
+    layer = L.halo_linear_workspace_bytes_ex(m, n, k, 128, I8, 1)
+    dz, parts = m * n * 4, 32 * n * 4      # 32 runs of 16 rows
+    for q in (I8, E4M3):
+        assert every(m, n, k, 128, q) == layer + dz + parts
+        assert own(m, n, k, 128, BF16, q, silu, 7, 0) == layer + parts            # inside the passes
+        assert own(m, n, k, 128, BF16, q, silu, 3, 0) == layer
+        assert own(m, n, k, 128, BF16, q, none, 7, 0) == layer + parts
+        assert own(m, n, k, 128, BF16, q, none, 3, 0) == layer
+        for form in ((128, BF16, q, silu, 5, 0), (128, BF16, q, silu, 6, 0), (128, F32, q, silu, 7, 0),
+                     (128, BF16, q, silu, 7, 1), (32, BF16, q, silu, 7, 0)):
+            assert own(m, n, k, *form) == L.halo_linear_workspace_bytes_ex(m, n, k, form[0], q, 1) \
+                + dz + parts, form
+    for bad in ((BF16, F32, silu, 7, 0), (I8, I8, silu, 7, 0), (BF16, I8, 9, 7, 0), (BF16, I8, silu, 8, 0),
+                (BF16, I8, silu, -1, 0), (BF16, I8, silu, 7, 2)):
+        assert own(m, n, k, 128, *bad) == 0
+    assert own(m, n, k, 3, BF16, I8, silu, 7, 0) == 0 and own(m, -1, k, 128, BF16, I8, silu, 7, 0) == 0
+    assert own(m, 0, k, 128, BF16, I8, silu, 7, 0) > 0
+    # a smaller one is refused, before anything is launched
+    small = layer + parts - 1
+    assert call(L.halo_linear_act_bwd, ACT_BWD, m=m, n=n, k=k, block=128, act=silu,
+                ws_bytes=small) == WORKSPACE
