@@ -271,7 +271,7 @@ hipError_t pick_fwd(const NormFwdArgs& a, hipStream_t st) {
   }
   if (per <= 32) return run_fwd<T, VEC, ODD, 16, 2>(a, st);
   if (per <= 64) return run_fwd<T, VEC, ODD, 16, 4>(a, st);
-  return run_fwd<T, VEC, ODD, 16, 8>(a, st);
+  return hipErrorInvalidValue;  // past norm_max_dim
 }
 
 // ---------------------------------------------------------------------------
