@@ -22,7 +22,9 @@ __device__ __forceinline__ float gelu_arg(float z) {
 
 // erfc(x) / 2 for x >= 0 and exp(-x^2), by formula 7.1.26 of Abramowitz and Stegun, "Handbook of
 // Mathematical Functions" (absolute error of erf below 1.5e-7, 2.5 units of 2^-24): one
-// exponential, one reciprocal and five multiply-adds, a quarter of the library erf's time.
+// exponential, one reciprocal and five multiply-adds, a quarter of the library erf's time.  For
+// bf16 outputs and for slopes; the tail's relative error (5e-5 at z = -3, 1.6e-3 at -5) would show
+// in fp32 outputs, which take the library's erfc.
 __device__ __forceinline__ float half_erfc(float x, float* gauss) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.f));
   float p = __builtin_fmaf(1.061405429f, t, -1.453152027f);
@@ -39,12 +41,14 @@ __device__ __forceinline__ float normal_cdf(float z, float* gauss) {
   return z < 0.f ? h : 1.f - h;
 }
 
-template <int ACT>
+// FULL: for fp32 outputs.
+template <int ACT, bool FULL>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == kActRelu) return z > 0.f ? z : (z != z ? z : 0.f);
   if constexpr (ACT == kActSilu) return z * sigmoid_fast(z);
   if constexpr (ACT == kActGeluTanh) return z * sigmoid_fast(gelu_arg(z));
   if constexpr (ACT == kActGeluErf) {
+    if constexpr (FULL) return z * (0.5f * erfcf(z * -0.7071067811865476f));
     float gauss;
     return z * normal_cdf(z, &gauss);
   }
@@ -75,10 +79,11 @@ __device__ __forceinline__ float slope_of(float z) {
   return 1.f;
 }
 
-// The activation (a wave-uniform choice) of 8 values.
+// The activation (a wave-uniform choice) of 8 values, for outputs of type T.
+template <typename T>
 __device__ __forceinline__ void act8(int act, const float* z, float* y) {
 #define HALO_ACT8(A) \
-  _Pragma("unroll") for (int e = 0; e < 8; ++e) y[e] = act_of<A>(z[e])
+  _Pragma("unroll") for (int e = 0; e < 8; ++e) y[e] = act_of<A, sizeof(T) == 4>(z[e])
   switch (act) {
     case kActRelu: HALO_ACT8(kActRelu); break;
     case kActSilu: HALO_ACT8(kActSilu); break;

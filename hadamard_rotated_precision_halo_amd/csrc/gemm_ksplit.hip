@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
     float z[8], y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf((float)s[e] * sar, sbv[e], bias[e]);
-    act8(g.act, z, y);
+    act8<T>(g.act, z, y);
     if (g.res) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] += res[e];

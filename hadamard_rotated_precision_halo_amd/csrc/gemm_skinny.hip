@@ -53,12 +53,13 @@ __device__ __forceinline__ void finish(const GemmArgs& g, float acc, float sa, i
   const int64_t at = row * g.ldc + col;
   float z = (acc * sa) * g.sb[col];
   if (g.bias) z += elem_f32<T>(reinterpret_cast<const T*>(g.bias) + col);
+  constexpr bool FULL = sizeof(T) == 4;
   float y;
   switch (g.act) {
-    case kActRelu: y = act_of<kActRelu>(z); break;
-    case kActSilu: y = act_of<kActSilu>(z); break;
-    case kActGeluTanh: y = act_of<kActGeluTanh>(z); break;
-    case kActGeluErf: y = act_of<kActGeluErf>(z); break;
+    case kActRelu: y = act_of<kActRelu, FULL>(z); break;
+    case kActSilu: y = act_of<kActSilu, FULL>(z); break;
+    case kActGeluTanh: y = act_of<kActGeluTanh, FULL>(z); break;
+    case kActGeluErf: y = act_of<kActGeluErf, FULL>(z); break;
     default: y = z;
   }
   if (g.res) y += elem_f32<T>(reinterpret_cast<const T*>(g.res) + at);

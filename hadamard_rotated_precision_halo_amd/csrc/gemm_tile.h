@@ -392,7 +392,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
         float z[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = __builtin_fmaf(a[e] * sar, sbv[e], bias[e]);
-        act8(g.act, z, y);
+        act8<T>(g.act, z, y);
         if (g.res) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] += res[t][e];

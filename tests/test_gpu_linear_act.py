@@ -392,3 +392,23 @@ def test_backward_in_its_own_workspace(m, n, k, block, kw, dt):
     assert (room[need:] == 77).all()
     with pytest.raises(H.HaloError, match="WORKSPACE"):
         H.linear_act_bwd(dy, z, x, w, block, workspace=room[:need - 1], **kw)
+
+
+@pytest.mark.parametrize("m", [1, 40, 300, 1100, 3900])
+def test_gelu_in_fp32_keeps_its_tail(m):
+    """gelu by its distribution in fp32 outputs, relative to its own value down to z = -12.  With x = 0
+    z is the bias.  The distribution's argument carries two roundings, which move it by at most
+    2 u (z^2 + 1) of itself, the library's erfc 4 units in the last place, the two products around it
+    one rounding each: u (16 + 2 (z^2 + 1)) of |y|."""
+    n, k, block = 4096 if m > 40 else 4000, 64, 64
+    bias = torch.linspace(-12, 12, n, device=DEV)
+    x, w = torch.zeros((m, k), device=DEV), rnd((n, k), F32, 1)
+    y, z = H.linear_act_fwd(x, w, block, bias=bias, activation="gelu_erf", want_z=True)
+    assert torch.equal(z, bias.expand(m, n))
+    want = bias.double() * torch.special.erfc(-bias.double() * 0.5 ** 0.5) / 2
+    assert ((y.double() - want).abs() <= U * (16 + 2 * (bias.double() ** 2 + 1)) * want.abs()).all()
+    qw, sw = H.fwht_quant(w, H.ROWS, block)
+    assert torch.equal(H.linear_act_q(x, qw, sw, block, bias=bias, activation="gelu_erf"), y)
+    # bf16 operands with fp32 outputs alike
+    y = H.linear_act_fwd(x.bfloat16(), w.bfloat16(), block, bias=bias, activation="gelu_erf", y_dtype=F32)
+    assert ((y.double() - want).abs() <= U * (16 + 2 * (bias.double() ** 2 + 1)) * want.abs()).all()
