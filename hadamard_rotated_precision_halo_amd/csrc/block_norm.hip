@@ -519,10 +519,8 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
     keep_raw(wgate);
     T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
     T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
-    // Without a row (!live) nothing is added: FAST loads gave zeros; else selected, not multiplied
-    // by zero, since the row read in its place may hold infinities (8192 x 4096 bf16: 84.9 us,
-    // with the selects 86.0 us).
-    const bool add = FAST || live;
+    // Without a row (!live) nothing is added: selected, not multiplied by zero, since the row read in
+    // its place, its factors or the weights may hold infinities.
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       keep_raw1(cur[j].g);
@@ -541,9 +539,9 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
       for (int e = 0; e < VEC; ++e) {
         const float rhat = rv[e] * b, yhat = yv[e] * ar;
         g[e] = __builtin_fmaf(-bm, rhat, __builtin_fmaf(b, u[e] * wq[e], g[e]));
-        spre[j][e] = __builtin_fmaf(add ? u[e] : 0.f, rhat, spre[j][e]);
+        spre[j][e] = __builtin_fmaf(live ? u[e] : 0.f, rhat, spre[j][e]);
         const float sG = a.scale * g[e];
-        const float gy = add ? sG * yhat : 0.f;
+        const float gy = live ? sG * yhat : 0.f;
         sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
         spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
         o[e] = ar * __builtin_fmaf(-m2, yhat, sG * wg[e] * wp[e]);
