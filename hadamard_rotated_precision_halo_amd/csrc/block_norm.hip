@@ -519,8 +519,8 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
     keep_raw(wgate);
     T* dr = reinterpret_cast<T*>(a.dr) + t * a.lddr;
     T* dy = reinterpret_cast<T*>(a.dy) + t * a.lddy;
-    // Without a row (!live) nothing is added: selected, not multiplied by zero, since the row read in
-    // its place, its factors or the weights may hold infinities.
+    // Without a row (!live) the sums stay as they are: selected, not multiplied by zero, since the row
+    // read in its place, its factors and the weights may hold infinities.
 #pragma unroll
     for (int j = 0; j < CH; ++j) {
       keep_raw1(cur[j].g);
@@ -539,11 +539,10 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
       for (int e = 0; e < VEC; ++e) {
         const float rhat = rv[e] * b, yhat = yv[e] * ar;
         g[e] = __builtin_fmaf(-bm, rhat, __builtin_fmaf(b, u[e] * wq[e], g[e]));
-        spre[j][e] = __builtin_fmaf(live ? u[e] : 0.f, rhat, spre[j][e]);
-        const float sG = a.scale * g[e];
-        const float gy = live ? sG * yhat : 0.f;
-        sgate[j][e] = __builtin_fmaf(gy, wp[e], sgate[j][e]);
-        spost[j][e] = __builtin_fmaf(gy, wg[e], spost[j][e]);
+        const float sG = a.scale * g[e], gy = sG * yhat;
+        spre[j][e] = live ? __builtin_fmaf(u[e], rhat, spre[j][e]) : spre[j][e];
+        sgate[j][e] = live ? __builtin_fmaf(gy, wp[e], sgate[j][e]) : sgate[j][e];
+        spost[j][e] = live ? __builtin_fmaf(gy, wg[e], spost[j][e]) : spost[j][e];
         o[e] = ar * __builtin_fmaf(-m2, yhat, sG * wg[e] * wp[e]);
       }
       if constexpr (FAST) {
@@ -799,10 +798,10 @@ __global__ __launch_bounds__(64 * kStripTeams) void norm_strip_kernel(NormBwdArg
     for (int e = 0; e < VEC; ++e) {  // !live: see norm_bwd_kernel
       const float rhat = rv[e] * cur.b, yhat = yv[e] * cur.a;
       g[e] = __builtin_fmaf(-cur.bm, rhat, __builtin_fmaf(cur.b, u[e] * wq[e], g[e]));
-      sums[1][e] = __builtin_fmaf(live ? u[e] : 0.f, rhat, sums[1][e]);
-      const float sG = a.scale * g[e], gy = live ? sG * yhat : 0.f;
-      sums[2][e] = __builtin_fmaf(gy, wp[e], sums[2][e]);
-      sums[0][e] = __builtin_fmaf(gy, wg[e], sums[0][e]);
+      const float sG = a.scale * g[e], gy = sG * yhat;
+      sums[1][e] = live ? __builtin_fmaf(u[e], rhat, sums[1][e]) : sums[1][e];
+      sums[2][e] = live ? __builtin_fmaf(gy, wp[e], sums[2][e]) : sums[2][e];
+      sums[0][e] = live ? __builtin_fmaf(gy, wg[e], sums[0][e]) : sums[0][e];
       o[e] = cur.a * __builtin_fmaf(-cur.m2, yhat, sG * wg[e] * wp[e]);
     }
     if (live && pl.in) {

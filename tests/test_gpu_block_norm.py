@@ -347,3 +347,28 @@ def test_in_place_with_a_team_too_many(d, post, pre, dt):
     got = H.block_norm_fwd(r, y, post_weight=wp, pre_weight=wq, scale=0.5, r_out=r, h=y if pre else None)
     for u, v in zip(got, want):
         assert (u is None and v is None) or torch.equal(u, v)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("t,d,groups", [(1, 64, 1), (2, 64, 2), (1, 1000, 1), (2, 513, 2), (3, 8193, 1),
+                                        (3, 8193, 3), (1, 4096, 1), (5, 2049, 5), (9, 300, 3)])
+def test_infinite_inputs_stay_in_their_sums(t, d, groups, dt):
+    """An infinity in r_out, y or a weight reaches the sums whose terms hold it, with its sign, and no
+    others: also where a workgroup has more teams than rows."""
+    print(f"tokens {t} dim {d} gate rows {groups} {dt}", flush=True)
+    col, inf = d // 2, float("inf")
+    ones = torch.ones(t, dtype=torch.float32, device=DEV)
+    base = dict(gate=rnd((groups, d), dt, 3).abs() + 1, post_weight=rnd((d,), dt, 4).abs() + 1,
+                pre_weight=rnd((d,), dt, 5) + 1, rstd_post=ones * 0.5, rstd_pre=ones * 0.5)
+    rows = dict(dr_out=rnd((t, d), dt, 6).abs() + 0.5, dh=rnd((t, d), dt, 7, 1e-4).abs() + 1e-4,
+                r_out=rnd((t, d), dt, 1, 0.1), y=rnd((t, d), dt, 2).abs() + 0.5)
+    for where in ("r_out", "post_weight", "gate", "rstd_pre"):
+        kw = {k: v.clone() for k, v in {**base, **rows}.items()}
+        (kw[where][0] if where in ("r_out", "gate") else kw[where])[col if where != "rstd_pre" else 0] = inf
+        got = dict(zip(("dr", "dy", "dgate", "dpost", "dpre"), H.block_norm_bwd(scale=1.0, **kw)))
+        ref = bwd64(kw["dr_out"], kw["dh"], kw["r_out"], kw["y"], kw["gate"], kw["post_weight"],
+                    kw["pre_weight"], kw["rstd_post"], kw["rstd_pre"], 1.0)
+        for name in ("dgate", "dpost", "dpre"):
+            want = ref[name][0]
+            kind = lambda v: torch.where(v.isnan(), 3, torch.where(v == inf, 2, torch.where(v == -inf, 1, 0)))
+            assert torch.equal(kind(got[name].double()), kind(want)), (where, name)
