@@ -474,14 +474,11 @@ __global__ __launch_bounds__(64 * NW * bwd_teams(NW, VEC)) void norm_bwd_kernel(
       for (int e = 0; e < VEC; ++e) {
         u[e] *= wq[e];
         rv[e] *= b;
-        float cy = (wp[e] * wg[e]) * (yv[e] * ar);
-        if (ODD) {  // the chunk before counts the shared elements
-          u[e] = e >= pl[j].from ? u[e] : 0.f;
-          cy = e >= pl[j].from ? cy : 0.f;
-        }
-        m1 = __builtin_fmaf(u[e], rv[e], m1);
-        sa = __builtin_fmaf(cy, __builtin_fmaf(b, u[e], g[e]), sa);
-        sb = __builtin_fmaf(cy * b, rv[e], sb);
+        const float cy = (wp[e] * wg[e]) * (yv[e] * ar);
+        const bool own = !ODD || e >= pl[j].from;  // the chunk before counts the shared elements
+        m1 = own ? __builtin_fmaf(u[e], rv[e], m1) : m1;
+        sa = own ? __builtin_fmaf(cy, __builtin_fmaf(b, u[e], g[e]), sa) : sa;
+        sb = own ? __builtin_fmaf(cy * b, rv[e], sb) : sb;
       }
     }
     m1 = wave_sum(m1);

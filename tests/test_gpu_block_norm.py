@@ -372,3 +372,26 @@ def test_infinite_inputs_stay_in_their_sums(t, d, groups, dt):
             want = ref[name][0]
             kind = lambda v: torch.where(v.isnan(), 3, torch.where(v == inf, 2, torch.where(v == -inf, 1, 0)))
             assert torch.equal(kind(got[name].double()), kind(want)), (where, name)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("t,d", [(3, 64), (2, 1000), (3, 1003), (2, 2051), (5, 4003), (2, 6003), (2, 9001)])
+def test_an_infinity_reaches_its_rows_gradient_as_the_formula_has_it(t, d, dt):
+    """dr infinite in one place: the other places of dy get the infinity of the mean, not NaN, also where
+    the place is an element that two chunks of a row hold."""
+    print(f"tokens {t} dim {d} {dt}", flush=True)
+    inf, vec = float("inf"), 8 if dt == BF16 else 4
+    ones = torch.ones(t, dtype=torch.float32, device=DEV)
+    base = dict(gate=rnd((1, d), dt, 3).abs() + 1, post_weight=rnd((d,), dt, 4).abs() + 1,
+                pre_weight=rnd((d,), dt, 5) + 1, rstd_post=ones * 0.5, rstd_pre=ones * 0.5,
+                dr_out=rnd((t, d), dt, 6).abs() + 0.5, dh=rnd((t, d), dt, 7, 1e-4),
+                r_out=rnd((t, d), dt, 1, 0.1), y=rnd((t, d), dt, 2).abs() + 0.5)
+    kind = lambda v: torch.where(v.isnan(), 3, torch.where(v == inf, 2, torch.where(v == -inf, 1, 0)))
+    for col in (0, d // 2, max(0, d - vec), d - 1):
+        kw = {k: v.clone() for k, v in base.items()}
+        kw["dr_out"][0, col] = inf
+        got = dict(zip(("dr", "dy", "dgate", "dpost", "dpre"), H.block_norm_bwd(scale=1.0, **kw)))
+        ref = bwd64(kw["dr_out"], kw["dh"], kw["r_out"], kw["y"], kw["gate"], kw["post_weight"],
+                    kw["pre_weight"], kw["rstd_post"], kw["rstd_pre"], 1.0)
+        for name in ("dr", "dy", "dgate", "dpost", "dpre"):
+            assert torch.equal(kind(got[name].double()), kind(ref[name][0])), (col, name)
