@@ -663,10 +663,10 @@ const char* halo_status_str(halo_status s) {
     case HALO_ERR_SHAPE: return "unsupported or inconsistent sizes";
     case HALO_ERR_BLOCK: return "block must be a power of two in [1, 4096]";
     case HALO_ERR_DTYPE: return "unsupported element type";
-    case HALO_ERR_ALIGN: return "pointer or leading dimension not 16-byte aligned";
+    case HALO_ERR_ALIGN: return "pointer or leading dimension not aligned (16 bytes; row operators: the element)";
     case HALO_ERR_WORKSPACE: return "workspace missing or too small";
     case HALO_ERR_HIP: return "HIP launch failed";
-    case HALO_ERR_OPTION: return "invalid rounding option";
+    case HALO_ERR_OPTION: return "invalid option (rounding mode, activation, eps or temperature)";
   }
   return "unknown status";
 }

@@ -331,3 +331,10 @@ def test_workspace_of_a_gradients_own_form(L):
     small = layer + parts - 1
     assert call(L.halo_linear_act_bwd, ACT_BWD, m=m, n=n, k=k, block=128, act=silu,
                 ws_bytes=small) == WORKSPACE
+
+
+def test_status_strings_name_the_operators_options(L):
+    text = L.halo_status_str(OPTION).decode()
+    for word in ("rounding", "activation", "eps", "temperature"):
+        assert word in text
+    assert "element" in L.halo_status_str(ALIGN).decode()   # rows of the row operators start anywhere
