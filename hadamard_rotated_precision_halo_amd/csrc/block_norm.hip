@@ -137,7 +137,7 @@ __global__ __launch_bounds__(64 * FwdGeo<NW>::WAVES) void norm_fwd_kernel(NormFw
   __shared__ float s_post[WAVES], s_pre[WAVES];
   const int wave = threadIdx.x >> 6, team = wave / NW;
   const int tl = threadIdx.x - team * NW * 64;  // thread within the team
-  const int64_t tok = (int64_t)blockIdx.x * TEAMS + team;
+  const int64_t tok = a.first + (int64_t)blockIdx.x * TEAMS + team;
   // a workgroup of several teams may end past the last token; a team of one wave meets no
   // barrier and leaves, one of more waves repeats the last token (its stores write the same)
   if (NW == 1 && tok >= a.tokens) return;
@@ -238,12 +238,17 @@ __global__ __launch_bounds__(64 * FwdGeo<NW>::WAVES) void norm_fwd_kernel(NormFw
 }
 
 template <typename T, int VEC, bool ODD, int NW, int CH>
-hipError_t run_fwd(const NormFwdArgs& a, hipStream_t st) {
+hipError_t run_fwd(NormFwdArgs a, hipStream_t st) {
   constexpr int WAVES = FwdGeo<NW>::WAVES, TEAMS = FwdGeo<NW>::TEAMS;
-  const int64_t grid = (a.tokens + TEAMS - 1) / TEAMS;
-  hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, ODD, NW, CH>), dim3((unsigned)grid),
-                     dim3(64 * WAVES), 0, st, a);
-  return hipGetLastError();
+  const int64_t grid = (a.tokens + TEAMS - 1) / TEAMS, most = max_workgroups(64 * WAVES);
+  for (int64_t g = 0; g < grid; g += most) {
+    a.first = g * TEAMS;
+    hipLaunchKernelGGL((norm_fwd_kernel<T, VEC, ODD, NW, CH>),
+                       dim3((unsigned)(grid - g < most ? grid - g : most)), dim3(64 * WAVES), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Waves per token: so many that a lane holds at most two chunks of r and of y, since few registers
@@ -678,7 +683,7 @@ template <typename T, int VEC, bool ODD>
 __global__ __launch_bounds__(512) void norm_stats_kernel(NormBwdArgs a) {
   constexpr int WAVES = 8;
   __shared__ float s_red[3][WAVES];
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.first + blockIdx.x;
   const T* dr_out = reinterpret_cast<const T*>(a.dr_out) + t * a.lddro;
   const T* dh = reinterpret_cast<const T*>(a.dh) + t * a.lddh;
   const T* r = reinterpret_cast<const T*>(a.r_out) + t * a.ldro;
@@ -838,10 +843,15 @@ __global__ __launch_bounds__(64 * kStripTeams) void norm_strip_kernel(NormBwdArg
 }
 
 template <typename T, int VEC, bool ODD>
-hipError_t run_strips(const NormBwdArgs& a, const NormPlan& pn, hipStream_t st) {
-  hipLaunchKernelGGL((norm_stats_kernel<T, VEC, ODD>), dim3((unsigned)a.tokens), dim3(512), 0, st, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+hipError_t run_strips(NormBwdArgs a, const NormPlan& pn, hipStream_t st) {
+  const int64_t most = max_workgroups(512);
+  for (a.first = 0; a.first < a.tokens; a.first += most) {
+    const int64_t left = a.tokens - a.first;
+    hipLaunchKernelGGL((norm_stats_kernel<T, VEC, ODD>), dim3((unsigned)(left < most ? left : most)),
+                       dim3(512), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const unsigned strips = (unsigned)((a.dim + 64 * VEC - 1) / (64 * VEC));
   hipLaunchKernelGGL((norm_strip_kernel<T, VEC, ODD>), dim3(strips, (unsigned)pn.wgs),
                      dim3(64 * kStripTeams), 0, st, a, pn);

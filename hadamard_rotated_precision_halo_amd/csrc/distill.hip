@@ -136,7 +136,7 @@ void distill_kernel(DistillArgs a) {
   // t, then p [K]; logit [K]; index [K]; with many entries, a table of indices [slots]
   extern __shared__ __attribute__((aligned(16))) float s_top[];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t tok = blockIdx.x;
+  const int64_t tok = a.first + blockIdx.x;
   const int K = a.top;
   const float mul = a.inv_tau * kLog2e;
   const T* row = reinterpret_cast<const T*>(a.logits) + tok * a.ldl;
@@ -392,12 +392,19 @@ void distill_kernel(DistillArgs a) {
 }
 
 template <typename T, int NT, int CH, int MODE>
-hipError_t run(const DistillArgs& a, hipStream_t st) {
+hipError_t run(DistillArgs a, hipStream_t st) {
   constexpr int64_t part = (int64_t)NT * CH * RowType<T>::VEC;
-  const dim3 grid((unsigned)a.tokens, MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
-  hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT),
-                     (size_t)((a.top + 3) & ~3) * 12 + (size_t)entry_slots(a.top) * 4, st, a);
-  return hipGetLastError();
+  const int64_t most = max_workgroups(NT);
+  for (a.first = 0; a.first < a.tokens; a.first += most) {
+    const int64_t left = a.tokens - a.first;
+    const dim3 grid((unsigned)(left < most ? left : most),
+                    MODE == kParts ? (unsigned)((a.vocab + part - 1) / part) : 1u);
+    hipLaunchKernelGGL((distill_kernel<T, NT, CH, MODE>), grid, dim3(NT),
+                       (size_t)((a.top + 3) & ~3) * 12 + (size_t)entry_slots(a.top) * 4, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 // Threads per token, by the vocabulary alone: so few that a compute unit holds several rows, one of

@@ -158,6 +158,11 @@ hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t
 hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
                            int64_t n, float* dz, void* db, float* part, hipStream_t st);
 
+// Workgroups of `threads` along x that one launch may hold: HIP counts a launch's threads along an
+// axis in 32 bits, and what passes them is dropped without an error.  The row operators, whose
+// grids have a team of threads for every token, launch longer calls in pieces.
+constexpr int64_t max_workgroups(int threads) { return (int64_t(1) << 31) / threads; }
+
 // The join between two blocks (block_norm.hip).  Optional tensors are NULL; leading dimensions
 // in elements; group_len = tokens / gate rows.
 struct NormFwdArgs {
@@ -166,6 +171,7 @@ struct NormFwdArgs {
   float *rstd_post, *rstd_pre;
   int64_t ldr, ldy, ldg, ldro, ldh;
   int64_t tokens, group_len;
+  int64_t first;  // set by the launcher: the launch's first token
   int dim;
   float scale, eps, inv_dim;
 };
@@ -177,8 +183,10 @@ struct NormBwdArgs {
   int64_t tokens, group_len;
   int dim;
   float scale, inv_dim;
-  // set by the launcher: partial sums, and the widest rows' statistics [tokens x 2]
+  // set by the launcher: partial sums, and the widest rows' statistics [tokens x 2], of the tokens
+  // from `first` on in a launch
   float *part_post, *part_pre, *part_gate, *stats;
+  int64_t first;
 };
 int64_t norm_max_dim(int in_bf16);
 hipError_t launch_norm_fwd(const NormFwdArgs& a, int in_bf16, hipStream_t st);
@@ -198,6 +206,7 @@ struct DistillArgs {
   void* dlogits;         // [tokens x vocab], ldd; may be logits
   int64_t ldl, ldi, ldt, ldd;
   int64_t tokens;
+  int64_t first;         // set by the launcher: the launch's first token
   int vocab, top;
   int t_bf16;            // tlogits are bf16
   float tau, inv_tau;

@@ -81,3 +81,48 @@ def test_layer(block):
     assert torch.equal(got[0][-rows:], want[0]) and torch.equal(got[1], want[1])
     err = (got[2].float() - want[2].float()).abs()
     assert (err <= 2.0 ** -7 * want[2].float().abs() + 1e-3).all()
+
+
+# HIP counts a launch's threads in 32 bits: a wave per token passes them at 2^26 tokens, 256 threads
+# per token at 2^24
+@pytest.mark.parametrize("t,d", [(2 ** 26 + 5, 8), (2 ** 26 + 4, 5)])
+def test_more_tokens_than_a_launch_has_threads_for(t, d):
+    print(f"{t} x {d} bf16", flush=True)
+    r, rl = tail_only((t, d), 8, 1)
+    r[:-8] = 1
+    w = torch.full((d,), 2.0, dtype=BF16, device=DEV)
+    out, h, a, b = H.block_norm_fwd(r, r, post_weight=w, pre_weight=w, eps=0.0)
+    assert (h[:-8] == 2).all() and (out[:-8] == 3).all()
+    want = H.block_norm_fwd(rl, rl, post_weight=w, pre_weight=w, eps=0.0)
+    for got, ref in zip((out, h, a, b), want):
+        assert torch.equal(got[-8:], ref)
+    del out, h
+    g = H.block_norm_bwd(r, None, r)
+    assert torch.equal(g[0], r)
+    del g
+    idx = torch.zeros((t, 1), dtype=torch.int32, device=DEV)
+    tl, one = torch.zeros((t, 1), device=DEV), torch.ones(t, device=DEV)
+    want = H.distill_fwd_bwd(rl, idx[-8:], tl[-8:], one[-8:])
+    loss, lse, grad = H.distill_fwd_bwd(r, idx, tl, one)
+    first = H.distill_fwd_bwd(r[:1].contiguous(), idx[:1], tl[:1], one[:1])
+    for got, ref, start in zip((loss, lse, grad), want, first):
+        assert torch.equal(got[-8:], ref) and (got[:-8] == start).all()
+    loss, lse = H.distill_fwd(r, idx, tl)
+    assert torch.equal(loss[-8:], want[0]) and (loss[:-8] == first[0]).all()
+    alone = H.distill_bwd(one, r, lse, idx, tl, dlogits=r)
+    assert torch.equal(alone[-8:], want[2]) and (alone[:-8] == first[2]).all()
+
+
+def test_more_rows_than_a_launch_has_threads_for():
+    t, v = 2 ** 24 + 3, 2056
+    print(f"{t} x {v} bf16", flush=True)
+    z, zl = tail_only((t, v), 4, 1)
+    idx = torch.zeros((t, 1), dtype=torch.int32, device=DEV)
+    tl, one = torch.zeros((t, 1), device=DEV), torch.ones(t, device=DEV)
+    want = H.distill_fwd_bwd(zl, idx[-4:], tl[-4:], one[-4:])
+    first = H.distill_fwd_bwd(z[:1].contiguous(), idx[:1], tl[:1], one[:1])
+    loss, lse, grad = H.distill_fwd_bwd(z, idx, tl, one, dlogits=z)
+    assert torch.equal(grad[-4:], want[2]) and torch.equal(loss[-4:], want[0])
+    assert (loss[:-4] == first[0]).all() and (lse[:-4] == first[1]).all()
+    for k in range(0, t - 4, 2 ** 21):
+        assert (grad[k:min(k + 2 ** 21, t - 4)] == first[2]).all()
