@@ -58,10 +58,11 @@ __device__ __forceinline__ uint4 get(const T* row, int at) {
     return load16u(row + at);
   }
 }
-// A row that is read once and not again, past the caches (8192 x 4096 bf16: forward 48.8 us with,
-// 51.8 us without; backward 91.8 and 98.3 us): not where rows start anywhere (ODD), whose boundary
-// lines two rows share (2310 x 2049 fp32 backward: 43.0 us with, 39.6 us without).  The outputs
-// are stored through the caches: the next layer reads them.
+// A row that is read once and not again, past the caches (8192 x 4096 bf16: forward 49.1 us with,
+// 51.7 us without; backward 80.7 and 91.1 us): not where rows start anywhere (ODD), whose boundary
+// lines two rows share (2310 x 2049 fp32 backward: 36.8 us with, 34.1 us without).  The outputs
+// are stored through the caches; past them, a chain of join, layer, layer and join at 8192 x 4096
+// took 371 us for 379 us.
 template <typename T, int VEC, bool ODD>
 __device__ __forceinline__ uint4 get_once(const T* row, int at) {
   if constexpr (VEC == 1 || ODD) return get<T, VEC>(row, at);
@@ -292,8 +293,9 @@ struct NormPlan {
 };
 
 // Waves per token and chunks per lane of the backward for a row of `chunks` chunks: two chunks per
-// lane and as many waves as that takes, so that few lanes idle whatever the width (8192 x 4096
-// and 6500 x 5120 bf16: 91.5 and 93.3 us; one chunk per lane, twice the waves: 90.9 and 101.0 us).
+// lane and as many waves as that takes, so that few lanes idle whatever the width (one chunk per
+// lane and twice the waves, in a form of the loop that had branches: as long at 8192 x 4096 bf16, 8 %
+// longer at 6500 x 5120, which takes 87.7 us).
 // bf16 lanes (256 registers, 8 waves) and fp32 lanes (160 registers, 12 waves) bound the row;
 // longer rows (nw 0) go by column strips, see norm_strip_kernel.
 void bwd_shape(int64_t chunks, int vec, int* nw, int* ch) {
@@ -310,8 +312,7 @@ NormPlan plan_bwd(int64_t tokens, int64_t group_len, int teams, int64_t wgs) {
   NormPlan p{};
   // whole rows: one workgroup per compute unit, whose teams keep enough rows in flight (each
   // prefetches its next row), so that the partial sums, one row per workgroup, stay few (8192 x
-  // 4096 bf16: 96.8 us with 256 workgroups, 103.4 us with 512; without the prefetch 104.8 and 108.9
-  // us, each before the loop lost its branches)
+  // 4096 bf16: 80.7 us with 256 workgroups, 88.1 us with 512; 2310 x 2049 fp32: 34.1 and 43.1 us)
   int64_t rows = (tokens + wgs - 1) / wgs;
   if (rows < teams) rows = teams;
   if (group_len * teams <= rows) {
@@ -677,7 +678,8 @@ BwdLayout bwd_layout(int64_t tokens, int64_t dim, int64_t group_len, int in_bf16
 // The widest rows, which a workgroup's registers do not hold beside their columns' sums: a first
 // launch reduces each row to the two numbers that its gradient needs, bm = b mean(u rhat) and the
 // mean m2 of dy's formula; a second takes strips of 64 chunks, a wave per row of a strip, and does
-// the rest (2048 x 16384 bf16: see the launcher).  Only the second stores, so dr and dy may be
+// the rest (2048 x 16384 bf16: 138 us, everything being read twice; with the row held and registers
+// spilled, more than twice that).  Only the second stores, so dr and dy may be
 // inputs as before; a moved-back chunk's shared elements are another workgroup's and not stored.
 template <typename T, int VEC, bool ODD>
 __global__ __launch_bounds__(512) void norm_stats_kernel(NormBwdArgs a) {

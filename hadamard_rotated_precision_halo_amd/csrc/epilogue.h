@@ -121,7 +121,9 @@ __device__ __forceinline__ void load_cols(const T* p, int cnt, float* o) {
   }
 }
 
-// Whole groups are stored non-temporally: the outputs are not read back here.
+// Whole groups are stored non-temporally, as the bare product's: whether the next operator then finds
+// them in a cache does not show (a chain of join, layer, layer and join at 8192 x 4096: 379 us, with
+// these stores through the caches 378 us).
 template <typename T>
 __device__ __forceinline__ void store_cols(T* p, int cnt, const float* v) {
   if (cnt == 8) {

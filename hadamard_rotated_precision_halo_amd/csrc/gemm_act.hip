@@ -27,8 +27,8 @@ hipError_t run(const GemmArgs& g, hipStream_t st) {
 
 // The largest tile that still gives the 256 compute units a tile each, since a workgroup of the
 // 256 tile needs a whole unit and fewer tiles leave units idle for the whole contraction, while
-// smaller tiles read each operand more often from the L2 (8192 x 11008 x 4096 INT8: 414 us a call
-// against 453 us on 128 x 128 tiles).  Below that 64 x 64 tiles: two
+// smaller tiles read each operand more often from the L2 (8192 x 11008 x 4096 INT8: 403 us a call;
+// on 128 x 128 tiles 9 % longer).  Below that 64 x 64 tiles: two
 // workgroups per unit, or, where there is not even one tile per unit, the kernel whose waves
 // split the contraction (256 x 4096 x 4096 INT8: 16.3 us a call against 18.4 us; but 400 rows:
 // 24.3 against 21.7 us).

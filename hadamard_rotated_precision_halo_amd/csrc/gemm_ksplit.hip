@@ -9,8 +9,8 @@
 // wave waits for another before the end, where the four partial tiles meet in LDS and are added in
 // wave order.  Bound by the loads: a tile reads 128 bytes for each K byte, 1.4 MB per compute unit
 // at 203 x 4096 x 11008 FP8, 12 to 14 us at the 100 to 120 bytes/ns that a unit loads of data in
-// its L2; the product takes 20.6 us (19.7 us with its LDS reads and MFMAs left out; touching the
-// lines of b ahead of their loads made it 30 us).
+// its L2; the product takes 21 us of a call's 26 (4 % less with its LDS reads and MFMAs left out;
+// touching the lines of b ahead of their loads made it half as long again).
 #include "gemm_tile.h"
 
 namespace halo {

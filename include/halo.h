@@ -16,7 +16,8 @@
  *   - Matrices are row-major with an explicit leading dimension (in elements).
  *   - Every pointer is DEVICE memory owned by the caller.  The library never allocates,
  *     frees or synchronises; work is enqueued on `stream` (a hipStream_t; NULL = the
- *     default stream) and the call returns once it is enqueued.
+ *     default stream) and the call returns once it is enqueued.  The calling thread's current
+ *     HIP device is the one that the pointers and the stream belong to.
  *   - A pointer may be NULL only when the matrix it describes is empty (a zero size).
  *   - All arguments are validated on the host before anything is launched.  On any error
  *     the call returns a non-zero status, launches nothing and writes no output.  A failed
