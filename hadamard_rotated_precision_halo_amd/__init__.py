@@ -659,16 +659,10 @@ def _io_2d(t, name):
     return dt, t.device
 
 
-# torch's raw handle of a device's current stream: a twentieth of the time of building the
-# torch.cuda.Stream object for it, where this torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current_stream(device):
-    """The current HIP stream of `device`."""
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+# The handle of the current stream of the device of that index: torch's raw one, a twentieth of the
+# time of building the torch.cuda.Stream object for it, where this torch has it.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _dense_like(t):
@@ -695,7 +689,7 @@ def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scal
     and for the fp32 factors of norms that were not asked for.
     """
     dt, dev = _io_2d(r, "r")
-    if stream is not None or _off_device(r):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, block_norm_fwd, r, y, gate, post_weight, pre_weight, scale, eps,
                    r_out, h)
     t, d = shape = r.shape
@@ -731,7 +725,7 @@ def block_norm_fwd(r, y=None, gate=None, post_weight=None, pre_weight=None, scal
     st = lib().halo_block_norm_fwd(_p(r), ldr, _p(y), ldy, _p(gate), ldg, groups, _p(post_weight),
                                    _p(pre_weight), _TORCH_CODE[dt], t, d, scale, eps, _p(r_out),
                                    ldro, _p(h), ldh, _p(rstd_post), _p(rstd_pre),
-                                   _current_stream(dev))
+                                   _current_stream(dev.index))
     _check(st, "halo_block_norm_fwd")
     return (r if y is None else r_out), h, rstd_post, rstd_pre
 
@@ -749,7 +743,7 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
     [groups, dim].  The parameter gradients are fp32 sums in a fixed order, rounded once."""
     ref = dr_out if dr_out is not None else dh
     dt, dev = _io_2d(ref, "dr_out" if dr_out is not None else "dh")
-    if stream is not None or _off_device(ref):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, block_norm_bwd, dr_out, dh, r_out, y, gate, post_weight,
                    pre_weight, rstd_post, rstd_pre, scale, dr, dy, want_dgate, want_dpost,
                    want_dpre, workspace)
@@ -808,7 +802,7 @@ def block_norm_bwd(dr_out, dh, r_out, y=None, gate=None, post_weight=None, pre_w
                                _p(rstd_post) if post_weight is not None else None, _p(rstd_pre),
                                code, t, d, scale, _p(dr), lddr, _p(dy), lddy, _p(dgate),
                                _p(dpost), _p(dpre), _p(workspace), workspace.numel(),
-                               _current_stream(dev))
+                               _current_stream(dev.index))
     _check(st, "halo_block_norm_bwd")
     return dr, dy, dgate, dpost, dpre
 
@@ -836,13 +830,13 @@ def distill_fwd(logits, idx, tlogits, temperature=1.0, loss=None, lse=None, stre
     vocabulary, such as -1, is no entry) and q the softmax of the student's logits, both at the
     temperature.  Returns (loss, lse), fp32 per token; lse = log sum exp(logits / temperature)."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None or _off_device(logits):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, distill_fwd, logits, idx, tlogits, temperature, loss, lse)
     loss = _out_vec(loss, "loss", t, dev)
     lse = _out_vec(lse, "lse", t, dev)
     st = lib().halo_distill_fwd(_p(logits), _TORCH_CODE[dt], ldl, _p(idx), ldi, _p(tlogits), tc,
                                 ldt, t, v, top, temperature, _p(loss), _p(lse),
-                                _current_stream(dev))
+                                _current_stream(dev.index))
     _check(st, "halo_distill_fwd")
     return loss, lse
 
@@ -858,7 +852,7 @@ def distill_bwd(dloss, logits, lse, idx, tlogits, temperature=1.0, dlogits=None,
     """Gradient of distill_fwd for the logits: dloss[t] * temperature * (q - p) per token, from
     the forward's lse.  dlogits may be logits itself."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None or _off_device(logits):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, distill_bwd, dloss, logits, lse, idx, tlogits, temperature,
                    dlogits)
     _vec(dloss, "dloss", t, torch.float32, dev)
@@ -869,7 +863,7 @@ def distill_bwd(dloss, logits, lse, idx, tlogits, temperature=1.0, dlogits=None,
         ldd = _rows(dlogits, "dlogits", logits.shape, dt, dev)
     st = lib().halo_distill_bwd(_p(dloss), _p(logits), _TORCH_CODE[dt], ldl, _p(lse), _p(idx), ldi,
                                 _p(tlogits), tc, ldt, t, v, top, temperature, _p(dlogits), ldd,
-                                _current_stream(dev))
+                                _current_stream(dev.index))
     _check(st, "halo_distill_bwd")
     return dlogits
 
@@ -880,7 +874,7 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
     token's weight in the loss beforehand (dloss; 0 leaves a token out).  Returns (loss, lse,
     dlogits); dlogits may be logits itself."""
     dt, dev, t, v, top, ldl, ldi, ldt, tc = _distill_args(logits, idx, tlogits)
-    if stream is not None or _off_device(logits):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, distill_fwd_bwd, logits, idx, tlogits, dloss, temperature, loss,
                    lse, dlogits)
     _vec(dloss, "dloss", t, torch.float32, dev)
@@ -892,7 +886,7 @@ def distill_fwd_bwd(logits, idx, tlogits, dloss, temperature=1.0, loss=None, lse
         ldd = _rows(dlogits, "dlogits", logits.shape, dt, dev)
     st = lib().halo_distill_fwd_bwd(_p(logits), _TORCH_CODE[dt], ldl, _p(idx), ldi, _p(tlogits),
                                     tc, ldt, _p(dloss), t, v, top, temperature, _p(loss), _p(lse),
-                                    _p(dlogits), ldd, _current_stream(dev))
+                                    _p(dlogits), ldd, _current_stream(dev.index))
     _check(st, "halo_distill_fwd_bwd")
     return loss, lse, dlogits
 
@@ -942,7 +936,7 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
     (y, z) when the pre-activation is wanted (want_z or a z to write it to): linear_act_bwd takes
     it.  residual may be y itself."""
     dt, dev = _io_2d(x, "x")
-    if stream is not None or _off_device(x):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, linear_act_fwd, x, w, block, q_dtype, bias, activation, residual,
                    y, y_dtype, want_z, z, workspace, signs_k=signs_k)
     if not (isinstance(w, torch.Tensor) and w.dim() == 2):
@@ -969,7 +963,7 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
                   if workspace is None else 0, x)
     st = L.halo_linear_act_fwd(_p(x), _p(w), _TORCH_CODE[dt], m, n, k, int(block), qc, _p(y),
                                _code(yt), ctypes.byref(ep), opts, _p(ws), ws.numel(),
-                               _current_stream(dev))
+                               _current_stream(dev.index))
     _check(st, "halo_linear_act_fwd")
     return y if z is None else (y, z)
 
@@ -985,7 +979,7 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
     least).  Only x is rotated and quantised here; up to 16 rows of x take a kernel bound by
     reading qw once.  Returns y (and z when a z to write it to is given)."""
     dt, dev = _io_2d(x, "x")
-    if stream is not None or _off_device(x):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, linear_act_q, x, qw, sw, block, bias, activation, residual, y,
                    y_dtype, z, workspace, signs_k=signs_k)
     m, k = x.shape
@@ -1018,7 +1012,7 @@ def linear_act_q(x, qw, sw, block, bias=None, activation="none", residual=None, 
                              sw.data_ptr(), m, n, k, block, y.data_ptr(), _code(yt),
                              ctypes.byref(ep), _p(signs_k), _p(workspace),
                              0 if workspace is None else workspace.numel(),
-                             _current_stream(dev))
+                             _current_stream(dev.index))
     _check(st, "halo_linear_act_q")
     return y if z is None else (y, z)
 
@@ -1044,7 +1038,7 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
     activation "none".  The residual's gradient is dy.  Returns (dx, dw, db), None where not
     wanted; options as linear_bwd."""
     dt, dev = _io_2d(dy, "dy")
-    if stream is not None or _off_device(dy):
+    if stream is not None or dev.index != _current_device():
         return _on(stream, dev, linear_act_bwd, dy, z, x, w, block, q_dtype, grad_q_dtype,
                    activation, want_dx, want_dw, want_db, dx, dw, db, workspace, signs_n=signs_n,
                    signs_m=signs_m, grad_rounding=grad_rounding, seed=seed, counter=counter,
@@ -1086,6 +1080,6 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
                                int(block), qc, _code(grad_q_dtype or q_dtype),
                                _p(dx) if want_dx else None, _p(dw) if want_dw else None,
                                _p(db) if want_db else None, opts, _p(ws), ws.numel(),
-                               _current_stream(dev))
+                               _current_stream(dev.index))
     _check(st, "halo_linear_act_bwd")
     return (dx if want_dx else None), (dw if want_dw else None), (db if want_db else None)

@@ -17,7 +17,7 @@ class Machine:
         self.device, self.streams, self.launches, self.switches = 0, {0: 100, 1: 101}, [], 0
         monkeypatch.setattr(H, "lib", lambda: self)
         monkeypatch.setattr(H, "_current_device", lambda: self.device)
-        monkeypatch.setattr(H, "_raw_stream", lambda index: self.streams[index])
+        monkeypatch.setattr(H, "_current_stream", lambda index: self.streams[index])
         monkeypatch.setattr(H, "_ptr", lambda t: None if t is None else 1)
         monkeypatch.setattr(H, "_p", lambda t: None if t is None else 1)
         monkeypatch.setattr(torch.cuda, "current_stream", self.current_stream)
