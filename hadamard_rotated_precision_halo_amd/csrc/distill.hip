@@ -299,17 +299,20 @@ void distill_kernel(DistillArgs a) {
   }
   __syncthreads();
   float tm, ts, lse, m = 0.f, logsum = 0.f;
+  bool none;  // every logit is -inf; lse alone may also be below the range of fp32
   pair_of<TT / 64>(s_tea, mul, tm, ts);
   if (MODE == kParts) {
     lse = a.lse_in[tok];
+    none = lse == -__builtin_inff();
   } else {
     float sum;
     pair_of<NW>(s_row, mul, m, sum);
     logsum = logf(sum);
-    lse = sum == 0.f ? -__builtin_inff() : __builtin_fmaf(m, a.inv_tau, logsum);
+    none = sum == 0.f;
+    lse = none ? -__builtin_inff() : __builtin_fmaf(m, a.inv_tau, logsum);
     if (a.lse && tid == 0) a.lse[tok] = lse;
   }
-  const bool empty = tm == -__builtin_inff() || lse == -__builtin_inff();
+  const bool empty = tm == -__builtin_inff() || none;
 
   // each entry's p, and the loss
   float l = 0.f;

@@ -440,7 +440,8 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
  *   r_out, h     outputs; r_out may be r or y, h may be y or r (with the same leading dimension).
  *   rstd_post, rstd_pre  [tokens] fp32, the factors a and b (the backward takes them); may be NULL.
  * dim is 1 .. 32768 (bf16) or 16384 (fp32).  A row of zeros with eps 0 gives infinities, as the
- * formula does.
+ * formula does.  Rows whose fp32 sum of squares overflows (elements of some 1e19) are outside the
+ * supported range.
  */
 halo_status halo_block_norm_fwd(const void* r, int64_t ldr, const void* y, int64_t ldy,
                                 const void* gate, int64_t ldg, int64_t groups,
@@ -499,7 +500,8 @@ halo_status halo_block_norm_bwd(const void* dr_out, int64_t lddr_out, const void
  *   dlogits  [tokens x vocab] of the logits' type, ldd >= vocab; may be logits (then ldd = ldl).
  * halo_distill_bwd takes the lse that the forward wrote; halo_distill_fwd_bwd does both from one
  * read of the logits.  Their gradients are the same bits while |lse| <= 4096; beyond, the joint
- * call's q comes from the row's sum, and halo_distill_bwd's is as good as lse in fp32 (in [0, 1]).
+ * call's q comes from the row's sum, and halo_distill_bwd's is as good as lse in fp32 (in [0, 1];
+ * an lse of -inf is a row without logits).
  */
 halo_status halo_distill_fwd(const void* logits, halo_dtype logits_type, int64_t ldl,
                              const int32_t* idx, int64_t ldi, const void* tlogits,

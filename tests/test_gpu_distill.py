@@ -322,3 +322,30 @@ def test_rows_of_one_value(v, tau, dt):
     e = U * (400 + 16 * logv + 8 * size)
     tol = by * (e / v * (1 + e) + spread * p_tol) + ROUND[dt] * 1.01 * (want.abs() + by * e / v)
     within(alone[near], want[near], tol[near], "gradient")
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("v", [3, 2000, 140001])
+def test_logits_beyond_the_range_of_lse(v, dt):
+    """At a temperature below 1 the type's extremes scale past fp32: lse is an infinity, loss and
+    gradient of the joint call are still those of q = 1 / vocabulary (tolerances as for rows of one
+    value, without lse), and the gradient from lse alone stays finite."""
+    ext = torch.finfo(dt).max
+    logits = torch.tensor([-ext, ext], dtype=torch.float64, device=DEV)[:, None].expand(2, v).to(dt).contiguous()
+    _, idx, tl, dloss = make(2, v, 9, dt, 51, missing=False)
+    dloss, tau, logv = dloss + 0.25, 0.7, torch.log(torch.tensor(float(v), dtype=torch.float64)).item()
+    p = torch.softmax(tl.double() / tau, 1)
+    p_tol = (U * (64 + 8 * (tl.double() / tau).abs().amax(1) + 9 / 4))[:, None]
+    loss, lse, grad = H.distill_fwd_bwd(logits, idx, tl, dloss, temperature=tau)
+    assert lse.tolist() == [float("-inf"), float("inf")]
+    tol = tau ** 2 * ((p * (p_tol + 16 * U) * (p.log().abs() + logv + 1)).sum(1) + 310 * U)
+    within(loss, tau ** 2 * (p * (p.log() + logv)).sum(1), tol, "loss")
+    by = (dloss.double() * tau)[:, None]
+    spread = torch.zeros((2, v), dtype=torch.float64, device=DEV).scatter_add_(1, idx.long(), p)
+    want = by * (1 / v - spread)
+    tol = by * (U * (400 + 16 * logv) / v + spread * p_tol) + ROUND[dt] * 1.01 * want.abs()
+    within(grad, want, tol, "gradient of the joint call")
+    l2, e2 = H.distill_fwd(logits, idx, tl, temperature=tau)
+    assert torch.equal(l2, loss) and torch.equal(e2, lse)
+    alone = H.distill_bwd(dloss, logits, lse, idx, tl, temperature=tau)
+    assert torch.isfinite(alone).all() and (alone[0] == 0).all()   # of -inf alone: nothing left
