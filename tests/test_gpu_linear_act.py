@@ -412,3 +412,21 @@ def test_gelu_in_fp32_keeps_its_tail(m):
     # bf16 operands with fp32 outputs alike
     y = H.linear_act_fwd(x.bfloat16(), w.bfloat16(), block, bias=bias, activation="gelu_erf", y_dtype=F32)
     assert ((y.double() - want).abs() <= U * (16 + 2 * (bias.double() ** 2 + 1)) * want.abs()).all()
+
+
+@pytest.mark.parametrize("q,gq", [(I8, I8), (E4M3, E5M2)])
+def test_backward_when_tasks_stop_waiting(q, gq):
+    """Columns split over 48 workgroups that exchange their maxima, dz formed inside: with one poll of
+    the bounded wait, tasks stop waiting and the launch behind stores their parts from dy and z again;
+    the gradients are the same bits, and the bias gradient's sums are counted once."""
+    m, n, k, block = 49152, 384, 64, 256
+    x, w = rnd((m, k), BF16, 1), rnd((n, k), BF16, 2, k ** -0.5)
+    z, dy = rnd((m, n), BF16, 3, 1.5), rnd((m, n), BF16, 4, 1e-3)
+    want = H.linear_act_bwd(dy, z, x, w, block, q, gq, activation="silu")
+    dz = dy.double() * slope64(z.double(), "silu")
+    tol = ROUND[BF16] * 1.01 * dz.sum(0).abs() + 2100 * U * dz.abs().sum(0)
+    assert ((want[2].double() - dz.sum(0)).abs() <= tol).all()
+    for _ in range(4):
+        got = H.linear_act_bwd(dy, z, x, w, block, q, gq, activation="silu", exchange_polls=1)
+        for u, v in zip(got, want):
+            assert torch.equal(u, v)
