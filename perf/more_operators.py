@@ -1,0 +1,438 @@
+"""Cases, plain forms and 64-bit values of the gated feed-forward layer and of activations kept in
+8 bits for the backward pass.
+
+Two operators, as the feed-forward half of a block uses them:
+
+  glu      linear_glu_fwd / linear_glu_q / linear_glu_bwd: both projections of a gated feed-forward
+           block as one Hadamard-rotated 8-bit layer, w [2 n, k] (the gate's n rows, then the up
+           projection's), z = X W^T + bias, y = act(z[:, :n]) z[:, n:], the same on weights
+           quantised once (serving), and its gradient.
+  keep     checkpoint_pack / checkpoint_unpack: rows of activations as 8-bit codes with a power of
+           two for each 32 of a row, and back; and linear_act_bwd / linear_glu_bwd, which read the
+           layer's input and pre-activation in that form.
+
+`own` picks the side `run` takes: the plain form in elementary torch operations, or the library's
+entry points.
+"""
+import torch
+
+own = False
+
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+CODES = {"i8": torch.int8, "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+QMAX = {"i8": 127.0, "e4m3": 448.0, "e5m2": 57344.0}
+GRAD_CODES = {"i8": "i8", "e4m3": "e5m2"}   # codes of the gradient beside codes of X and W
+GROUP = 32                                  # values that share a checkpoint's power of two
+
+
+# ---------------------------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------------------------
+
+def listed():
+    return [
+        # serving, one token: both projections on weights quantised once
+        {"name": "glu_q_one_token", "op": "glu", "dir": "q", "m": 1, "n": 11008, "k": 4096,
+         "block": 256, "codes": "i8", "act": "silu", "bias": False, "kept": "none"},
+        # serving, a ragged batch of tokens, FP8 weights
+        {"name": "glu_q_ragged_fp8", "op": "glu", "dir": "q", "m": 203, "n": 5504, "k": 4096,
+         "block": 128, "codes": "e4m3", "act": "gelu_tanh", "bias": True, "kept": "none"},
+        # training forward of the largest layer, pre-activation kept as it is
+        {"name": "glu_fwd_train", "op": "glu", "dir": "fwd", "m": 8192, "n": 11008, "k": 4096,
+         "block": 128, "codes": "i8", "act": "silu", "bias": False, "kept": "bf16"},
+        # training forward that keeps its pre-activation in 8 bits
+        {"name": "glu_fwd_kept8", "op": "glu", "dir": "fwd", "m": 4096, "n": 5504, "k": 4096,
+         "block": 256, "codes": "i8", "act": "silu", "bias": True, "kept": "i8"},
+        # its gradient from bf16 activations
+        {"name": "glu_bwd_train", "op": "glu", "dir": "bwd", "m": 4096, "n": 5504, "k": 4096,
+         "block": 256, "codes": "i8", "act": "silu", "bias": True, "kept": "bf16"},
+        # the same from the layer's input and pre-activation kept in 8 bits
+        {"name": "glu_bwd_kept8", "op": "glu", "dir": "bwd", "m": 4096, "n": 5504, "k": 4096,
+         "block": 256, "codes": "i8", "act": "silu", "bias": True, "kept": "i8"},
+        # a short, ragged batch of a narrow layer, everything in FP8
+        {"name": "glu_bwd_ragged_fp8", "op": "glu", "dir": "bwd", "m": 1000, "n": 1048, "k": 1056,
+         "block": 64, "codes": "e4m3", "act": "gelu_erf", "bias": True, "kept": "e4m3"},
+        # a few rows kept and read back: latency
+        {"name": "keep_few_rows", "op": "keep", "dir": "trip", "m": 16, "k": 4096, "type": "bf16",
+         "kept": "i8"},
+        # a training batch of a wide layer's input
+        {"name": "keep_train", "op": "keep", "dir": "trip", "m": 8192, "k": 11008, "type": "bf16",
+         "kept": "i8"},
+        # full-precision rows of an odd width, in FP8
+        {"name": "keep_f32_odd", "op": "keep", "dir": "trip", "m": 2310, "k": 2049, "type": "f32",
+         "kept": "e4m3"},
+        # the gradient of a feed-forward block's last projection, whose wide input was kept in 8
+        # bits
+        {"name": "linear_bwd_kept8", "op": "keep", "dir": "bwd", "m": 4096, "n": 4096, "k": 11008,
+         "block": 256, "codes": "i8", "act": "none", "bias": True, "kept": "i8"},
+        # the gradient of a layer with an activation, input and pre-activation kept in 8 bits
+        {"name": "linear_act_bwd_kept8", "op": "keep", "dir": "bwd", "m": 2048, "n": 4096,
+         "k": 1024, "block": 128, "codes": "i8", "act": "gelu_tanh", "bias": True, "kept": "i8"},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    """A whole number spread evenly over its logarithm."""
+    return min(hi, max(lo, int(lo * (hi / lo) ** rng.random() + rng.random())))
+
+
+def draw(rng):
+    op = rng.choice(["glu", "glu", "keep"])
+    acts = ["none", "relu", "silu", "silu", "gelu_tanh", "gelu_erf"]
+    if op == "keep" and rng.random() < 0.5:
+        k = _log_int(rng, 1, 16384)
+        return {"op": op, "dir": "trip", "m": _log_int(rng, 1, min(16384, (8192 * 11008) // k)),
+                "k": k, "type": rng.choice(["bf16", "bf16", "f32"]),
+                "kept": rng.choice(["i8", "i8", "e4m3"])}
+    n, k = 8 * _log_int(rng, 32, 1376), 32 * _log_int(rng, 8, 128)
+    case = {"op": op, "n": n, "k": k, "block": rng.choice([64, 128, 256]),
+            "codes": rng.choice(["i8", "i8", "e4m3"]), "act": rng.choice(acts),
+            "bias": rng.random() < 0.5}
+    if op == "keep":
+        return case | {"dir": "bwd", "m": _log_int(rng, 128, 4096),
+                       "kept": rng.choice(["i8", "i8", "e4m3"])}
+    d = rng.choice(["q", "q", "fwd", "bwd"])
+    if d == "q":
+        return case | {"dir": d, "m": _log_int(rng, 1, 512), "kept": "none"}
+    if d == "fwd":   # rotated FP8 products round more than their activations kept in 8 bits show
+        kept = rng.choice(["none", "bf16", "i8", "i8"] if case["codes"] == "i8" else ["none", "bf16"])
+    else:
+        kept = rng.choice(["bf16", "i8", "e4m3"])
+    return case | {"dir": d, "m": _log_int(rng, 128, 4096), "kept": kept}
+
+
+def work(case):
+    m, k = case["m"], case["k"]
+    groups = -(-k // GROUP)
+    if case["dir"] == "trip":   # x -> codes and powers -> x
+        e = 2 if case["type"] == "bf16" else 4
+        return {"bytes": 2 * m * k * e + 2 * m * (k + groups), "flops": 4 * m * k}
+    n = case["n"]
+    rows = 2 * n if case["op"] == "glu" else n      # of the weights
+    bias = 2 * rows * case["bias"]
+    flops = 2 * m * rows * k
+    kept = {"none": 0, "bf16": 2, "i8": 33 / 32, "e4m3": 33 / 32}[case["kept"]]   # bytes a value
+    if case["dir"] == "q":      # x, the weights' codes and scales -> y
+        return {"bytes": 2 * m * k + rows * _padded(k, case["block"]) + 4 * rows + 2 * m * n + bias,
+                "flops": flops}
+    if case["dir"] == "fwd":    # x, w -> y, z
+        return {"bytes": int(2 * (m * k + rows * k + m * n) + kept * m * rows) + bias, "flops": flops}
+    # dy, z, x, w -> dx, dw, db
+    z = kept * m * rows if case["act"] != "none" or case["op"] == "glu" else 0
+    return {"bytes": int(2 * (m * n + 2 * rows * k + m * k) + kept * m * k + z) + bias,
+            "flops": 2 * flops}
+
+
+# ---------------------------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------------------------
+
+def _padded(length, block):
+    """The contraction length: zero padded to a multiple of the block and of 32."""
+    step = max(block, 32)
+    return -(-length // step) * step
+
+
+def _hadamard(b):
+    """The Sylvester matrix of order b: (-1) ** (number of common one bits of row and column)."""
+    i = torch.arange(b, device=DEV)
+    c = i[:, None] & i[None, :]
+    for s in (8, 4, 2, 1):   # parity of the (at most 13) bits
+        c = c ^ (c >> s)
+    return (1 - 2 * (c & 1)).float()
+
+
+def _normal(g, *shape):
+    return torch.randn(*shape, generator=g, device=DEV, dtype=torch.float32)
+
+
+def _activations(g, rows, cols):
+    """Activations as a residual stream has them: a few channels are far larger than the rest."""
+    x = _normal(g, rows, cols)
+    x *= torch.where(torch.rand(cols, generator=g, device=DEV) < 0.004, 30.0, 1.0)
+    return x
+
+
+def _kept_state(s, name, v, kept):
+    """An activation as the forward left it: bf16, or codes and biased exponents."""
+    if kept == "bf16":
+        s[name] = v.to(torch.bfloat16)
+    else:
+        c, e = _packed_plain(v.to(torch.bfloat16).float(), kept)
+        s[name] = (c.to(CODES[kept]), e.to(torch.uint8))
+
+
+def prepare(case, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    s = {"case": case}
+    m, k, bf = case["m"], case["k"], torch.bfloat16
+    if case["dir"] == "trip":
+        s["x"] = _activations(g, m, k).to(TYPES[case["type"]])
+        return s
+    n, block = case["n"], case["block"]
+    rows = 2 * n if case["op"] == "glu" else n
+    x = _activations(g, m, k)
+    w = (k ** -0.5 * _normal(g, rows, k)).to(bf)
+    s["bias"] = (0.1 * _normal(g, rows)).to(bf) if case["bias"] else None
+    if case["dir"] == "bwd":
+        s["w"] = w
+        _kept_state(s, "x", x, case["kept"])
+        _kept_state(s, "z", 1.5 * _normal(g, m, rows), case["kept"])
+        s["dy"] = (1e-3 * _normal(g, m, n) / (0.3 + torch.rand(m, 1, generator=g, device=DEV))).to(bf)
+        return s
+    s["x"] = x.to(bf)
+    if case["dir"] == "q":
+        s["qw"], s["sw"] = _quantised_plain(w.float(), block, case["codes"])
+        s["qw"] = s["qw"].to(CODES[case["codes"]])
+    else:
+        s["w"] = w
+    return s
+
+
+# ---------------------------------------------------------------------------------------------
+# plain forms
+# ---------------------------------------------------------------------------------------------
+
+def _power(e):
+    """2 ** (e - 127) of biased exponents 1 .. 254."""
+    return (e.int() << 23).view(torch.float32)
+
+
+def _packed_plain(v, kept):
+    """Codes (as the numbers they stand for) of the rows of v and the biased exponents of their
+    groups' powers of two: the smallest that brings a group's largest value into the codes' range."""
+    rows, length = v.shape
+    groups = -(-length // GROUP)
+    u = torch.zeros(rows, groups * GROUP, device=v.device)
+    u[:, :length] = v
+    u = u.view(rows, groups, GROUP)
+    frac, e = torch.frexp(u.abs().amax(2))   # largest = frac 2 ** e, frac in [0.5, 1)
+    if kept == "i8":
+        e = torch.where(frac > 127 / 128, e + 1, e) - 7 + 127
+        e = e.clamp(16, 248)
+    else:
+        e = torch.where(frac > 7 / 8, e + 1, e) - 9 + 127
+        e = e.clamp(16, 246)
+    c = torch.clamp(u * _power(254 - e)[:, :, None], -QMAX[kept], QMAX[kept])
+    c = torch.round(c) if kept == "i8" else c.to(CODES[kept]).float()
+    return c.view(rows, groups * GROUP)[:, :length].contiguous(), e
+
+
+def _unpacked_plain(c, e):
+    rows, length = c.shape
+    return c.float() * _power(e).repeat_interleave(GROUP, 1)[:, :length]
+
+
+def _value(a):
+    """A kept activation in 32 bits."""
+    return _unpacked_plain(*a) if isinstance(a, tuple) else a.float()
+
+
+def _quantised_plain(v, block, codes):
+    """The rotated, quantised rows of v (32 bits): codes as the numbers they stand for, scales."""
+    rows, length = v.shape
+    lp = _padded(length, block)
+    if lp != length:
+        v = torch.cat([v, v.new_zeros(rows, lp - length)], 1)
+    b = (v.reshape(-1, block) @ _hadamard(block)).view(rows, lp)
+    top = b.abs().amax(1)
+    mul = torch.where(top > 0, QMAX[codes] / top, 0.0)
+    c = b * mul[:, None]
+    c = torch.round(c) if codes == "i8" else c.to(CODES[codes]).float()
+    return c, top / (QMAX[codes] * block ** 0.5)
+
+
+def _act_plain(z, act):
+    """act(z) and its slope."""
+    if act == "none":
+        return z, torch.ones_like(z)
+    if act == "relu":
+        return torch.clamp(z, min=0), (z > 0).float()
+    if act == "silu":
+        p = 1 / (1 + torch.exp(-z))
+        return z * p, p * (1 + z * (1 - p))
+    if act == "gelu_erf":
+        p = 0.5 * (1 + torch.erf(z * 0.7071067811865476))
+        return z * p, p + z * torch.exp(-0.5 * z * z) * 0.3989422804014327
+    u = torch.tanh(0.7978845608028654 * (z + 0.044715 * z * z * z))
+    return 0.5 * z * (1 + u), \
+        0.5 * (1 + u) + 0.5 * z * (1 - u * u) * 0.7978845608028654 * (1 + 0.134145 * z * z)
+
+
+def _glu_plain(s):
+    c = s["case"]
+    n, block, codes = c["n"], c["block"], c["codes"]
+    qx, sx = _quantised_plain(s["x"].float(), block, codes)
+    qw, sw = (s["qw"].float(), s["sw"]) if c["dir"] == "q" else _quantised_plain(s["w"].float(), block, codes)
+    z = (qx @ qw.t()) * sx[:, None] * sw[None, :]
+    if s["bias"] is not None:
+        z = z + s["bias"].float()
+    y = (_act_plain(z[:, :n], c["act"])[0] * z[:, n:]).to(torch.bfloat16)
+    if c["kept"] == "none":
+        return y
+    if c["kept"] != "bf16":
+        z = _unpacked_plain(*_packed_plain(z, c["kept"]))
+    return y, z.to(torch.bfloat16)
+
+
+def _bwd_plain(s):
+    c = s["case"]
+    n, block, codes, grad = c["n"], c["block"], c["codes"], GRAD_CODES[c["codes"]]
+    dz, x = s["dy"].float(), _value(s["x"])
+    if c["op"] == "glu":
+        z = _value(s["z"])
+        a, slope = _act_plain(z[:, :n], c["act"])
+        dz = torch.cat([dz * z[:, n:] * slope, dz * a], 1)
+    elif c["act"] != "none":
+        dz = dz * _act_plain(_value(s["z"]), c["act"])[1]
+    qa, sa = _quantised_plain(dz, block, grad)
+    qb, sb = _quantised_plain(s["w"].float().t().contiguous(), block, codes)
+    dx = (qa @ qb.t()) * sa[:, None] * sb[None, :]
+    qa, sa = _quantised_plain(dz.t().contiguous(), block, grad)
+    qb, sb = _quantised_plain(x.t().contiguous(), block, codes)
+    dw = (qa @ qb.t()) * sa[:, None] * sb[None, :]
+    out = (dx.to(torch.bfloat16), dw.to(torch.bfloat16))
+    return out + (dz.sum(0).to(torch.bfloat16),) if c["bias"] else out
+
+
+def _plain(s):
+    c = s["case"]
+    if c["dir"] == "trip":
+        return _unpacked_plain(*_packed_plain(s["x"].float(), c["kept"])).to(s["x"].dtype)
+    return _bwd_plain(s) if c["dir"] == "bwd" else _glu_plain(s)
+
+
+# ---------------------------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------------------------
+
+def _library(s):
+    import hadamard_rotated_precision_halo_amd as H
+    c = s["case"]
+    if c["dir"] == "trip":
+        return H.checkpoint_unpack(H.checkpoint_pack(s["x"], CODES[c["kept"]]), s["x"].dtype)
+    if c["dir"] == "q":
+        return H.linear_glu_q(s["x"], s["qw"], s["sw"], c["block"], bias=s["bias"],
+                              activation=c["act"])
+    codes = CODES[c["codes"]]
+    if c["dir"] == "fwd":
+        want = {"none": False, "bf16": True}.get(c["kept"], CODES.get(c["kept"]))
+        out = H.linear_glu_fwd(s["x"], s["w"], c["block"], codes, bias=s["bias"],
+                               activation=c["act"], want_z=want)
+        if isinstance(want, bool):
+            return out
+        return out[0], H.checkpoint_unpack(out[1], torch.bfloat16)
+    bwd = H.linear_glu_bwd if c["op"] == "glu" else H.linear_act_bwd
+    z = s["z"] if c["op"] == "glu" or c["act"] != "none" else None
+    out = bwd(s["dy"], z, s["x"], s["w"], c["block"], codes, CODES[GRAD_CODES[c["codes"]]],
+              activation=c["act"], want_db=c["bias"])
+    return out if c["bias"] else out[:2]
+
+
+def run(state):
+    return _library(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------------------------------------
+# the definition in 64 bits
+# ---------------------------------------------------------------------------------------------
+
+def _on_grid(a, codes):
+    """The nearest numbers of the code type, ties to even."""
+    if codes == "i8":
+        return torch.round(a)
+    bits, lowest = (3, -6) if codes == "e4m3" else (2, -14)   # mantissa bits, least exponent
+    _, e = torch.frexp(a)
+    quantum = torch.exp2((torch.clamp(e - 1, min=lowest) - bits).double())
+    return torch.round(a / quantum) * quantum
+
+
+def _codes64(v, block, codes):
+    """Row codes (as numbers) and scales of v by the definition: orthonormal block transform by
+    butterflies, absmax scale, nearest code."""
+    rows, length = v.shape
+    lp = _padded(length, block)
+    u = v.new_zeros(rows, lp)
+    u[:, :length] = v
+    step = 1
+    while step < block:
+        w = u.view(rows, lp // (2 * step), 2, step)
+        u = torch.stack([w[:, :, 0] + w[:, :, 1], w[:, :, 0] - w[:, :, 1]], 2).view(rows, lp)
+        step *= 2
+    u = u / block ** 0.5
+    top = u.abs().amax(1, keepdim=True)
+    a = torch.where(top > 0, u / torch.where(top > 0, top, 1.0) * QMAX[codes], 0.0)
+    return _on_grid(a, codes), (top / QMAX[codes]).squeeze(1)
+
+
+def _kept64(v, kept):
+    """The values that a checkpoint of v stands for: per 32 of a row, multiples of the least power
+    of two p with p qmax >= max |v|."""
+    out = torch.empty_like(v)
+    for at in range(0, v.shape[1], GROUP):
+        part = v[:, at:at + GROUP]
+        f, e = torch.frexp(part.abs().amax(1, keepdim=True) / QMAX[kept])   # f in [0.5, 1)
+        e = torch.where(f > 0.5, e, e - 1).clamp(-111, 121 if kept == "i8" else 119)
+        p = torch.exp2(e.double())
+        out[:, at:at + GROUP] = _on_grid((part / p).clamp(-QMAX[kept], QMAX[kept]), kept) * p
+    return out
+
+
+def _act64(z, act):
+    """act(z) and its slope."""
+    if act == "none":
+        return z, torch.ones_like(z)
+    if act == "relu":
+        return torch.where(z > 0, z, 0.0), torch.where(z > 0, 1.0, 0.0).to(z.dtype)
+    if act == "silu":
+        p = torch.special.expit(z)
+        return z * p, p + z * p * (1 - p)
+    if act == "gelu_erf":
+        cdf = torch.special.ndtr(z)
+        return z * cdf, cdf + z * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    a, b = (2 / torch.pi) ** 0.5, 0.044715
+    p = torch.special.expit(2 * a * (z + b * z ** 3))   # (1 + tanh u) / 2
+    return z * p, p + z * 2 * p * (1 - p) * a * (1 + 3 * b * z ** 2)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    if case["dir"] == "trip":
+        return _kept64(s["x"].double(), case["kept"])
+
+    def val(a):
+        if not isinstance(a, tuple):
+            return a.double()
+        p = torch.exp2(a[1].double() - 127)
+        return a[0].double() * p.repeat_interleave(GROUP, 1)[:, :a[0].shape[1]]
+
+    def product(a, b):
+        (qa, sa), (qb, sb) = a, b
+        return (qa @ qb.t()) * (sa[:, None] * sb[None, :])
+
+    n, block, codes, grad = case["n"], case["block"], case["codes"], GRAD_CODES[case["codes"]]
+    x = val(s["x"])
+    if case["dir"] == "bwd":
+        dz, w = s["dy"].double(), s["w"].double()
+        if case["op"] == "glu":
+            gate, up = val(s["z"]).split(n, 1)
+            a, slope = _act64(gate, case["act"])
+            dz = torch.cat([dz * slope * up, dz * a], 1)
+        else:
+            dz = dz * _act64(val(s["z"]), case["act"])[1]
+        dx = product(_codes64(dz, block, grad), _codes64(w.t().contiguous(), block, codes))
+        dw = product(_codes64(dz.t().contiguous(), block, grad),
+                     _codes64(x.t().contiguous(), block, codes))
+        return (dx, dw, dz.sum(0)) if case["bias"] else (dx, dw)
+    right = (s["qw"].double(), s["sw"].double()) if case["dir"] == "q" \
+        else _codes64(s["w"].double(), block, codes)
+    z = product(_codes64(x, block, codes), right)
+    if case["bias"]:
+        z = z + s["bias"].double()
+    gate, up = z.split(n, 1)
+    y = _act64(gate, case["act"])[0] * up
+    if case["kept"] == "none":
+        return y
+    return y, (z if case["kept"] == "bf16" else _kept64(z, case["kept"]))
