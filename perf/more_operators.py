@@ -9,7 +9,8 @@ Two operators, as the feed-forward half of a block uses them:
            quantised once (serving), and its gradient.
   keep     checkpoint_pack / checkpoint_unpack: rows of activations as 8-bit codes with a power of
            two for each 32 of a row, and back; and linear_act_bwd / linear_glu_bwd, which read the
-           layer's input and pre-activation in that form.
+           layer's input and pre-activation in that form (the gated layer's z [m, 2 n] as 2 m rows
+           of n).
 
 `own` picks the side `run` takes: the plain form in elementary torch operations, or the library's
 entry points.
@@ -112,7 +113,7 @@ def work(case):
     rows = 2 * n if case["op"] == "glu" else n      # of the weights
     bias = 2 * rows * case["bias"]
     flops = 2 * m * rows * k
-    kept = {"none": 0, "bf16": 2, "i8": 33 / 32, "e4m3": 33 / 32}[case["kept"]]   # bytes a value
+    kept = {"none": 0, "bf16": 2, "i8": 33 / 32, "e4m3": 33 / 32}[case["kept"]]   # bytes for a value
     if case["dir"] == "q":      # x, the weights' codes and scales -> y
         return {"bytes": 2 * m * k + rows * _padded(k, case["block"]) + 4 * rows + 2 * m * n + bias,
                 "flops": flops}
@@ -179,7 +180,8 @@ def prepare(case, seed):
     if case["dir"] == "bwd":
         s["w"] = w
         _kept_state(s, "x", x, case["kept"])
-        _kept_state(s, "z", 1.5 * _normal(g, m, rows), case["kept"])
+        z = 1.5 * _normal(g, m, rows)
+        _kept_state(s, "z", z if case["kept"] == "bf16" else z.view(-1, n), case["kept"])
         s["dy"] = (1e-3 * _normal(g, m, n) / (0.3 + torch.rand(m, 1, generator=g, device=DEV))).to(bf)
         return s
     s["x"] = x.to(bf)
@@ -273,7 +275,7 @@ def _glu_plain(s):
     if c["kept"] == "none":
         return y
     if c["kept"] != "bf16":
-        z = _unpacked_plain(*_packed_plain(z, c["kept"]))
+        z = _unpacked_plain(*_packed_plain(z.view(-1, n), c["kept"]))
     return y, z.to(torch.bfloat16)
 
 
@@ -282,7 +284,7 @@ def _bwd_plain(s):
     n, block, codes, grad = c["n"], c["block"], c["codes"], GRAD_CODES[c["codes"]]
     dz, x = s["dy"].float(), _value(s["x"])
     if c["op"] == "glu":
-        z = _value(s["z"])
+        z = _value(s["z"]).view(-1, 2 * n)
         a, slope = _act_plain(z[:, :n], c["act"])
         dz = torch.cat([dz * z[:, n:] * slope, dz * a], 1)
     elif c["act"] != "none":
@@ -417,7 +419,7 @@ def exact(case, seed):
     if case["dir"] == "bwd":
         dz, w = s["dy"].double(), s["w"].double()
         if case["op"] == "glu":
-            gate, up = val(s["z"]).split(n, 1)
+            gate, up = val(s["z"]).view(-1, 2 * n).split(n, 1)
             a, slope = _act64(gate, case["act"])
             dz = torch.cat([dz * slope * up, dz * a], 1)
         else:
@@ -435,4 +437,4 @@ def exact(case, seed):
     y = _act64(gate, case["act"])[0] * up
     if case["kept"] == "none":
         return y
-    return y, (z if case["kept"] == "bf16" else _kept64(z, case["kept"]))
+    return y, (z if case["kept"] == "bf16" else _kept64(z.view(-1, n), case["kept"]))
