@@ -14,6 +14,7 @@ the zero padding and stochastic rounding of its s5, and the seeded randomised tr
 """
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -38,7 +39,11 @@ EXPORTS = ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
            "halo_distill_fwd", "halo_distill_bwd", "halo_distill_fwd_bwd",
            "halo_linear_act_fwd", "halo_linear_act_q", "halo_linear_act_q_workspace_bytes",
            "halo_linear_act_bwd", "halo_linear_act_bwd_workspace_bytes",
-           "halo_linear_act_bwd_workspace_bytes_ex")
+           "halo_linear_act_bwd_workspace_bytes_ex",
+           "halo_checkpoint_pack", "halo_checkpoint_unpack", "halo_linear_act_fwd_kept",
+           "halo_linear_act_bwd_kept", "halo_linear_act_bwd_kept_workspace_bytes",
+           "halo_linear_glu_fwd", "halo_linear_glu_q", "halo_linear_glu_bwd",
+           "halo_linear_glu_bwd_workspace_bytes")
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu_tanh": 3, "gelu_erf": 4}  # halo_activation
 
 
@@ -61,6 +66,18 @@ class Epilogue(ctypes.Structure):
     """halo_epilogue of include/halo.h."""
     _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("z", ctypes.c_void_p),
                 ("activation", ctypes.c_int32)]
+
+
+class Kept(ctypes.Structure):
+    """halo_kept of include/halo.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("powers", ctypes.c_void_p), ("type", ctypes.c_int)]
+
+
+class Checkpoint(NamedTuple):
+    """Activations kept in 8 bits (checkpoint_pack): codes [rows, cols] (int8 or float8_e4m3fn) and
+    powers [rows, ceil(cols / 32)] (uint8): codes[r, c] * 2 ** (powers[r, c // 32] - 127)."""
+    codes: torch.Tensor
+    powers: torch.Tensor
 
 
 _TORCH_CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8,
@@ -137,6 +154,20 @@ def lib():
         L.halo_linear_act_bwd_workspace_bytes_ex.restype = sz
         L.halo_linear_act_bwd.argtypes = [vp, vp, e, vp, vp, e, i64, i64, i64, i32, e, e, vp, vp,
                                           vp, lo, vp, sz, vp]
+        kp = ctypes.POINTER(Kept)
+        L.halo_checkpoint_pack.argtypes = [vp, e, i64, i64, i64, e, vp, i64, vp, i64, vp]
+        L.halo_checkpoint_unpack.argtypes = [vp, e, i64, vp, i64, i64, i64, vp, e, i64, vp]
+        L.halo_linear_act_fwd_kept.argtypes = [vp, vp, e, i64, i64, i64, i32, e, vp, e, ep, kp, lo,
+                                               vp, sz, vp]
+        L.halo_linear_glu_fwd.argtypes = [vp, vp, e, i64, i64, i64, i32, e, vp, e, vp, e, kp, lo, vp,
+                                          sz, vp]
+        L.halo_linear_glu_q.argtypes = [vp, e, vp, e, vp, i64, i64, i64, i32, vp, e, vp, e, vp, vp,
+                                        sz, vp]
+        for f in (L.halo_linear_act_bwd_kept, L.halo_linear_glu_bwd):
+            f.argtypes = [vp, kp, e, kp, vp, e, i64, i64, i64, i32, e, e, vp, vp, vp, lo, vp, sz, vp]
+        for f in (L.halo_linear_act_bwd_kept_workspace_bytes, L.halo_linear_glu_bwd_workspace_bytes):
+            f.argtypes = [i64, i64, i64, i32, e, e, e, e, e, i32, e]
+            f.restype = sz
         L.halo_status_str.argtypes = [e]
         L.halo_status_str.restype = ctypes.c_char_p
         for f in ("halo_fwht_quant", "halo_fwht_quant_ex", "halo_fwht_quant_noalloc",
@@ -145,7 +176,10 @@ def lib():
                   "halo_linear_bwd_ex", "halo_fwht_quant_dual", "halo_mfma_rate_probe",
                   "halo_block_norm_fwd", "halo_block_norm_bwd", "halo_distill_fwd",
                   "halo_distill_bwd", "halo_distill_fwd_bwd", "halo_linear_act_fwd",
-                  "halo_linear_act_q", "halo_linear_act_bwd"):
+                  "halo_linear_act_q", "halo_linear_act_bwd", "halo_checkpoint_pack",
+                  "halo_checkpoint_unpack", "halo_linear_act_fwd_kept",
+                  "halo_linear_act_bwd_kept", "halo_linear_glu_fwd", "halo_linear_glu_q",
+                  "halo_linear_glu_bwd"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -934,7 +968,8 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
     as linear_fwd), y = act(z) + residual, rounded once.  activation: "none", "relu", "silu",
     "gelu_tanh" or "gelu_erf"; bias [n], residual, y and z [m, n] share y's type.  Returns y, or
     (y, z) when the pre-activation is wanted (want_z or a z to write it to): linear_act_bwd takes
-    it.  residual may be y itself."""
+    it.  want_z=torch.int8 or torch.float8_e4m3fn keeps it in 8 bits: z is then a Checkpoint.
+    residual may be y itself."""
     dt, dev = _io_2d(x, "x")
     if stream is not None or dev.index != _current_device():
         return _on(stream, dev, linear_act_fwd, x, w, block, q_dtype, bias, activation, residual,
@@ -950,9 +985,9 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
         y = torch.empty((m, n), dtype=yt, device=dev)
     else:
         _dense(y, "y", (m, n), yt, dev)
-    if want_z and z is None:
-        z = torch.empty((m, n), dtype=yt, device=dev)
-    ep = _epilogue(bias, activation, residual, z, (m, n), yt, dev)
+    z = _new_kept(want_z, z, m, n, yt, dev)
+    kept = _kept(z, "z", m, n, yt, dev) if isinstance(z, tuple) else None
+    ep = _epilogue(bias, activation, residual, None if kept else z, (m, n), yt, dev)
     opts = None
     if signs_k is not None:
         _vector(signs_k, "signs_k", _sign_words(contraction_len(k, block)), torch.int32)
@@ -961,6 +996,12 @@ def linear_act_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="none"
     L, qc = lib(), _code(q_dtype)
     ws = _scratch(workspace, L.halo_linear_workspace_bytes_ex(m, n, k, int(block), qc, 0)
                   if workspace is None else 0, x)
+    if kept is not None:
+        st = L.halo_linear_act_fwd_kept(_p(x), _p(w), _TORCH_CODE[dt], m, n, k, int(block), qc, _p(y),
+                                        _code(yt), ctypes.byref(ep), ctypes.byref(kept), opts, _p(ws),
+                                        ws.numel(), _current_stream(dev.index))
+        _check(st, "halo_linear_act_fwd_kept")
+        return y, z
     st = L.halo_linear_act_fwd(_p(x), _p(w), _TORCH_CODE[dt], m, n, k, int(block), qc, _p(y),
                                _code(yt), ctypes.byref(ep), opts, _p(ws), ws.numel(),
                                _current_stream(dev.index))
@@ -1035,8 +1076,13 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
                    grad_rounding="nearest", seed=0, counter=0, exchange_polls=0):
     """Gradient of linear_act_fwd: dz = dy act'(z) (fp32 until its codes), then linear_bwd's
     products dX = dz W and dW = dz^T X, and db = dz summed over the rows.  z may be None with
-    activation "none".  The residual's gradient is dy.  Returns (dx, dw, db), None where not
-    wanted; options as linear_bwd."""
+    activation "none".  x and z may each be a Checkpoint (activations kept in 8 bits).  The
+    residual's gradient is dy.  Returns (dx, dw, db), None where not wanted; options as
+    linear_bwd."""
+    if isinstance(x, tuple) or isinstance(z, tuple):
+        return _bwd_kept(False, dy, z, x, w, block, q_dtype, grad_q_dtype, activation, want_dx,
+                         want_dw, want_db, dx, dw, db, workspace, stream, signs_n, signs_m,
+                         grad_rounding, seed, counter, exchange_polls)
     dt, dev = _io_2d(dy, "dy")
     if stream is not None or dev.index != _current_device():
         return _on(stream, dev, linear_act_bwd, dy, z, x, w, block, q_dtype, grad_q_dtype,
@@ -1082,4 +1128,268 @@ def linear_act_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, ac
                                _p(db) if want_db else None, opts, _p(ws), ws.numel(),
                                _current_stream(dev.index))
     _check(st, "halo_linear_act_bwd")
+    return (dx if want_dx else None), (dw if want_dw else None), (db if want_db else None)
+
+
+# ---------------------------------------------------------------------------
+# activations kept in 8 bits, and the gated layer
+# ---------------------------------------------------------------------------
+
+_KEPT_DTYPES = (torch.int8, torch.float8_e4m3fn)
+
+
+def _groups(cols):
+    return -(-cols // 32)
+
+
+def _parts(a, name):
+    if not (isinstance(a, tuple) and len(a) == 2 and all(isinstance(t, torch.Tensor) for t in a)):
+        raise ValueError(f"{name} must be a tensor or a Checkpoint")
+    if a[0].dtype not in _KEPT_DTYPES:
+        raise TypeError(f"unsupported dtype {a[0].dtype}")
+    return a
+
+
+def _kept(a, name, rows, cols, dtype, device, shape=None):
+    """A kept activation, [rows, cols] as a Checkpoint or `shape` (the same by default) as a plain
+    tensor of dtype."""
+    if isinstance(a, torch.Tensor):
+        _dense(a, name, shape or (rows, cols), dtype, device)
+        return Kept(a.data_ptr(), None, _TORCH_CODE[dtype])
+    codes, powers = _parts(a, name)
+    _dense(codes, f"{name}'s codes", (rows, cols), codes.dtype, device)
+    _dense(powers, f"{name}'s powers", (rows, _groups(cols)), torch.uint8, device)
+    return Kept(codes.data_ptr(), powers.data_ptr(), _TORCH_CODE[codes.dtype])
+
+
+def _new_checkpoint(rows, cols, q_dtype, device):
+    if q_dtype not in _KEPT_DTYPES:
+        raise TypeError(f"unsupported dtype {q_dtype}")
+    return Checkpoint(torch.empty((rows, cols), dtype=q_dtype, device=device),
+                      torch.empty((rows, _groups(cols)), dtype=torch.uint8, device=device))
+
+
+def _new_kept(want, a, rows, cols, dtype, device, shape=None):
+    """The place a forward writes z to: the caller's, or a new one in the form wanted."""
+    if a is not None or want is False or want is None:
+        return a
+    if isinstance(want, torch.dtype) and want is not dtype:
+        return _new_checkpoint(rows, cols, want, device)
+    return torch.empty(shape or (rows, cols), dtype=dtype, device=device) if want else None
+
+
+def checkpoint_pack(x, q_dtype=torch.int8, out=None, stream=None):
+    """Activations in 8 bits for the backward pass (halo_checkpoint_pack): every 32 values of a row
+    of x (bf16 or fp32, any row stride) share the least power of two that brings the largest of them
+    to at most 127 (torch.int8) or 448 (torch.float8_e4m3fn), and are rounded once, ties to even.
+    Returns a Checkpoint (`out` to write into, dense or with longer rows).  Its values are bf16 numbers
+    exactly; a group with an infinity or a NaN becomes NaN throughout."""
+    dt, dev = _io_2d(x, "x")
+    if stream is not None or dev.index != _current_device():
+        return _on(stream, dev, checkpoint_pack, x, q_dtype, out)
+    rows, cols = shape = x.shape
+    ldx = _rows(x, "x", shape, dt, dev)
+    if out is None:
+        out = _new_checkpoint(rows, cols, q_dtype, dev)
+    codes, powers = _parts(out, "out")
+    ldc = _rows(codes, "out's codes", shape, q_dtype, dev)
+    ldp = _rows(powers, "out's powers", (rows, _groups(cols)), torch.uint8, dev)
+    st = lib().halo_checkpoint_pack(_p(x), _TORCH_CODE[dt], rows, cols, ldx, _code(q_dtype), _p(codes),
+                                    ldc, _p(powers), ldp, _current_stream(dev.index))
+    _check(st, "halo_checkpoint_pack")
+    return out
+
+
+def checkpoint_unpack(kept, dtype=torch.bfloat16, x=None, stream=None):
+    """The values a Checkpoint stands for, as bf16 or fp32 rows (halo_checkpoint_unpack; `x` to write
+    into)."""
+    codes, powers = _parts(kept, "kept")
+    if codes.dim() != 2 or not codes.is_cuda:
+        raise ValueError("a checkpoint's codes must be a 2-D GPU tensor")
+    dev = codes.device
+    if stream is not None or dev.index != _current_device():
+        return _on(stream, dev, checkpoint_unpack, kept, dtype, x)
+    rows, cols = shape = codes.shape
+    ldc = _rows(codes, "codes", shape, codes.dtype, dev)
+    ldp = _rows(powers, "powers", (rows, _groups(cols)), torch.uint8, dev)
+    if x is None:
+        x = torch.empty(shape, dtype=dtype, device=dev)
+    ldx = _rows(x, "x", shape, dtype, dev)
+    st = lib().halo_checkpoint_unpack(_p(codes), _TORCH_CODE[codes.dtype], ldc, _p(powers), ldp, rows,
+                                      cols, _p(x), _code(dtype), ldx, _current_stream(dev.index))
+    _check(st, "halo_checkpoint_unpack")
+    return x
+
+
+def linear_glu_fwd(x, w, block, q_dtype=torch.int8, bias=None, activation="silu", y=None,
+                   y_dtype=None, want_z=False, z=None, workspace=None, stream=None, signs_k=None):
+    """The gated feed-forward layer (halo_linear_glu_fwd): w [2 n, k] holds the gate's n rows, then
+    the up projection's; z = X W^T + bias (one rotated 8-bit product), y = act(z[:, :n]) z[:, n:],
+    rounded once.  Returns y [m, n], or (y, z) when the pre-activations are wanted for
+    linear_glu_bwd: want_z True for z [m, 2 n] of y's type, torch.int8 or torch.float8_e4m3fn for a
+    Checkpoint of 2 m rows of n (a token's gate half, then its up half), or z to write them to.
+    Workspace as linear_fwd's of 2 n output features."""
+    dt, dev = _io_2d(x, "x")
+    if stream is not None or dev.index != _current_device():
+        return _on(stream, dev, linear_glu_fwd, x, w, block, q_dtype, bias, activation, y, y_dtype,
+                   want_z, z, workspace, signs_k=signs_k)
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2 and w.shape[0] % 2 == 0):
+        raise ValueError("w must be a 2-D tensor of 2 n rows")
+    m, k = x.shape
+    n = w.shape[0] // 2
+    _dense(x, "x", (m, k), dt, dev)
+    _dense(w, "w", (2 * n, k), dt, dev)
+    yt = y.dtype if y is not None else (y_dtype or dt)
+    if y is None:
+        y = torch.empty((m, n), dtype=yt, device=dev)
+    else:
+        _dense(y, "y", (m, n), yt, dev)
+    if bias is not None:
+        _vec(bias, "bias", 2 * n, yt, dev)
+    z = _new_kept(want_z, z, 2 * m, n, yt, dev, (m, 2 * n))
+    kept = None if z is None else _kept(z, "z", 2 * m, n, yt, dev, (m, 2 * n))
+    opts = None
+    if signs_k is not None:
+        _vector(signs_k, "signs_k", _sign_words(contraction_len(k, block)), torch.int32)
+        _same_gpu(x, signs_k=signs_k)
+        opts = ctypes.byref(LinearOpts(_p(signs_k), None, None, NEAREST))
+    L, qc = lib(), _code(q_dtype)
+    ws = _scratch(workspace, L.halo_linear_workspace_bytes_ex(m, 2 * n, k, int(block), qc, 0)
+                  if workspace is None else 0, x)
+    st = L.halo_linear_glu_fwd(_p(x), _p(w), _TORCH_CODE[dt], m, n, k, int(block), qc, _p(y),
+                               _code(yt), _p(bias), _activation(activation),
+                               None if kept is None else ctypes.byref(kept), opts, _p(ws),
+                               ws.numel(), _current_stream(dev.index))
+    _check(st, "halo_linear_glu_fwd")
+    return y if z is None else (y, z)
+
+
+def linear_glu_q(x, qw, sw, block, bias=None, activation="silu", y=None, y_dtype=None,
+                 workspace=None, stream=None, signs_k=None):
+    """linear_glu_fwd on weights quantised once, for serving: (qw, sw) = fwht_quant(w, ROWS, block,
+    q_dtype[, signs=signs_k]) of the stacked weights [2 n, k], as for linear_act_q.  Returns y."""
+    dt, dev = _io_2d(x, "x")
+    if stream is not None or dev.index != _current_device():
+        return _on(stream, dev, linear_glu_q, x, qw, sw, block, bias, activation, y, y_dtype,
+                   workspace, signs_k=signs_k)
+    m, k = x.shape
+    if not (isinstance(qw, torch.Tensor) and qw.dim() == 2 and qw.shape[0] % 2 == 0):
+        raise ValueError("qw must be a 2-D tensor of 2 n rows")
+    n, block = qw.shape[0] // 2, int(block)
+    _dense(x, "x", x.shape, dt, dev)
+    if qw.dtype not in _KEPT_DTYPES:
+        raise TypeError(f"unsupported dtype {qw.dtype}")
+    kq = contraction_len(k, block) if block > 0 else k  # the library refuses a bad block
+    _dense(qw, "qw", (2 * n, kq), qw.dtype, dev)
+    _vec(sw, "sw", 2 * n, torch.float32, dev)
+    yt = y.dtype if y is not None else (y_dtype or dt)
+    if y is None:
+        y = torch.empty((m, n), dtype=yt, device=dev)
+    else:
+        _dense(y, "y", (m, n), yt, dev)
+    if bias is not None:
+        _vec(bias, "bias", 2 * n, yt, dev)
+    if signs_k is not None:
+        _vector(signs_k, "signs_k", _sign_words(kq), torch.int32)
+        _same_gpu(x, signs_k=signs_k)
+    L = lib()
+    if workspace is None:
+        need = L.halo_linear_act_q_workspace_bytes(m, k, block)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _scratch(workspace, 0, x)
+    st = L.halo_linear_glu_q(x.data_ptr(), _TORCH_CODE[dt], qw.data_ptr(), _TORCH_CODE[qw.dtype],
+                             sw.data_ptr(), m, n, k, block, y.data_ptr(), _code(yt), _p(bias),
+                             _activation(activation), _p(signs_k), _p(workspace),
+                             0 if workspace is None else workspace.numel(),
+                             _current_stream(dev.index))
+    _check(st, "halo_linear_glu_q")
+    return y
+
+
+def linear_glu_bwd(dy, z, x, w, block, q_dtype=torch.int8, grad_q_dtype=None, activation="silu",
+                   want_dx=True, want_dw=True, want_db=True, dx=None, dw=None, db=None,
+                   workspace=None, stream=None, signs_n=None, signs_m=None,
+                   grad_rounding="nearest", seed=0, counter=0, exchange_polls=0):
+    """Gradient of linear_glu_fwd for dy [m, n]: with g, u the halves of z,
+    dz = [dy u act'(g), dy act(g)] [m, 2 n] (fp32 until its codes), dX = dz W and dW = dz^T X as
+    linear_bwd's products over 2 n output features, db [2 n] = dz summed over the rows.  x and z are
+    the forward's, each a tensor or a Checkpoint.  Returns (dx, dw, db), None where not wanted;
+    options as linear_bwd (signs_n covers 2 n)."""
+    return _bwd_kept(True, dy, z, x, w, block, q_dtype, grad_q_dtype, activation, want_dx, want_dw,
+                     want_db, dx, dw, db, workspace, stream, signs_n, signs_m, grad_rounding, seed,
+                     counter, exchange_polls)
+
+
+def _type_of(a, dt):
+    """halo_dtype of a kept activation (None: plain)."""
+    return _TORCH_CODE[a[0].dtype if isinstance(a, tuple) else dt]
+
+
+def linear_kept_bwd_workspace_bytes(glu, m, n, k, block, q_dtype=torch.int8, dtype=torch.bfloat16,
+                                    activation="none", z_dtype=None, x_dtype=None, want_dx=True,
+                                    want_dw=True, want_db=True, grad_rounding="nearest"):
+    """Workspace bytes of linear_glu_bwd (glu True; n output features, w [2 n, k]), or of linear_act_bwd
+    with a Checkpoint among x and z, for a call of these types (z_dtype, x_dtype: torch.int8 or
+    torch.float8_e4m3fn for a Checkpoint, None for a tensor of dtype)."""
+    L = lib()
+    f = L.halo_linear_glu_bwd_workspace_bytes if glu else L.halo_linear_act_bwd_kept_workspace_bytes
+    return int(f(m, n, k, int(block), _code(dtype), _code(q_dtype), _activation(activation),
+                 _code(z_dtype or dtype), _code(x_dtype or dtype),
+                 1 * bool(want_dx) + 2 * bool(want_dw) + 4 * bool(want_db), _rounding(grad_rounding)))
+
+
+def _bwd_kept(glu, dy, z, x, w, block, q_dtype, grad_q_dtype, activation, want_dx, want_dw, want_db,
+              dx, dw, db, workspace, stream, signs_n, signs_m, grad_rounding, seed, counter,
+              exchange_polls):
+    dt, dev = _io_2d(dy, "dy")
+    if stream is not None or dev.index != _current_device():
+        return _on(stream, dev, _bwd_kept, glu, dy, z, x, w, block, q_dtype, grad_q_dtype, activation,
+                   want_dx, want_dw, want_db, dx, dw, db, workspace, None, signs_n, signs_m,
+                   grad_rounding, seed, counter, exchange_polls)
+    m, n = dy.shape
+    nz = 2 * n if glu else n
+    if not (isinstance(w, torch.Tensor) and w.dim() == 2):
+        raise ValueError("w must be a 2-D tensor")
+    k = w.shape[1]
+    _dense(dy, "dy", (m, n), dt, dev)
+    _dense(w, "w", (nz, k), dt, dev)
+    kx = _kept(x, "x", m, k, dt, dev)
+    act = _activation(activation)
+    kz = None
+    if glu or act != 0 or z is not None:
+        kz = _kept(z, "z", 2 * m if glu else m, n, dt, dev, (m, nz))
+    if want_dx:
+        dx = torch.empty((m, k), dtype=dt, device=dev) if dx is None else dx
+        _dense(dx, "dx", (m, k), dt, dev)
+    if want_dw:
+        dw = torch.empty((nz, k), dtype=dt, device=dev) if dw is None else dw
+        _dense(dw, "dw", (nz, k), dt, dev)
+    if want_db:
+        db = torch.empty(nz, dtype=dt, device=dev) if db is None else db
+        _vec(db, "db", nz, dt, dev)
+    if signs_n is not None:
+        _vector(signs_n, "signs_n", _sign_words(contraction_len(nz, block)), torch.int32)
+    if signs_m is not None:
+        _vector(signs_m, "signs_m", _sign_words(contraction_len(m, block)), torch.int32)
+    _same_gpu(dy, signs_n=signs_n, signs_m=signs_m)
+    rnd = _rounding(grad_rounding)
+    opts = None
+    if signs_n is not None or signs_m is not None or rnd != NEAREST or exchange_polls:
+        opts = ctypes.byref(LinearOpts(None, _p(signs_n), _p(signs_m), rnd, _u32x2(seed),
+                                       _u32x2(counter), int(exchange_polls)))
+    L, qc, code = lib(), _code(q_dtype), _TORCH_CODE[dt]
+    query, call, name = (
+        (L.halo_linear_glu_bwd_workspace_bytes, L.halo_linear_glu_bwd, "halo_linear_glu_bwd") if glu
+        else (L.halo_linear_act_bwd_kept_workspace_bytes, L.halo_linear_act_bwd_kept,
+              "halo_linear_act_bwd_kept"))
+    ws = _scratch(workspace, query(m, n, k, int(block), code, qc, act, _type_of(z, dt),
+                                   _type_of(x, dt), 1 * bool(want_dx) + 2 * bool(want_dw)
+                                   + 4 * bool(want_db), rnd) if workspace is None else 0, dy)
+    st = call(_p(dy), None if kz is None else ctypes.byref(kz), act, ctypes.byref(kx), _p(w), code, m,
+              n, k, int(block), qc, _code(grad_q_dtype or q_dtype), _p(dx) if want_dx else None,
+              _p(dw) if want_dw else None, _p(db) if want_db else None, opts, _p(ws), ws.numel(),
+              _current_stream(dev.index))
+    _check(st, name)
     return (dx if want_dx else None), (dw if want_dw else None), (db if want_db else None)

@@ -79,6 +79,34 @@ __device__ __forceinline__ float slope_of(float z) {
   return 1.f;
 }
 
+// act(z) and its slope from one exponential, as act_of (without FULL) and slope_of give them.
+template <int ACT>
+__device__ __forceinline__ void act_slope(float z, float* y, float* slope) {
+  *y = act_of<ACT, false>(z);
+  *slope = slope_of<ACT>(z);
+}
+
+// The gradient of a gated pair y = act(g) u for N values: dg = d u act'(g), du = d act(g).
+template <int N>
+__device__ __forceinline__ void gated_grad(int act, const float* d, const float* g, const float* u,
+                                           float* dg, float* du) {
+#define HALO_GATED(A) \
+  _Pragma("unroll") for (int e = 0; e < N; ++e) { \
+    float y, s; \
+    act_slope<A>(g[e], &y, &s); \
+    dg[e] = (d[e] * u[e]) * s; \
+    du[e] = d[e] * y; \
+  }
+  switch (act) {
+    case kActRelu: HALO_GATED(kActRelu) break;
+    case kActSilu: HALO_GATED(kActSilu) break;
+    case kActGeluTanh: HALO_GATED(kActGeluTanh) break;
+    case kActGeluErf: HALO_GATED(kActGeluErf) break;
+    default: HALO_GATED(kActNone) break;
+  }
+#undef HALO_GATED
+}
+
 // The activation (a wave-uniform choice) of 8 values, for outputs of type T.
 template <typename T>
 __device__ __forceinline__ void act8(int act, const float* z, float* y) {

@@ -9,7 +9,7 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
   using CFG = BigTile;
   constexpr int BM = CFG::BT, BN = CFG::BT, NT = 64 * CFG::WM * CFG::WN;
   const hipError_t attr_err =
-      allow_dynamic_lds<&gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, false>>(CFG::LDS);
+      allow_dynamic_lds<&gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, kEpiNone>>(CFG::LDS);
   if (attr_err != hipSuccess) return attr_err;
   GemmPair gp{};
   gp.g[0] = g0;
@@ -20,11 +20,11 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
     gp.g[0] = gp.g[1];
     gp.split = t1;
     if (t1 == 0) return hipSuccess;
-    hipLaunchKernelGGL((gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, false>), dim3((unsigned)t1),
+    hipLaunchKernelGGL((gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, kEpiNone>), dim3((unsigned)t1),
                        dim3(NT), CFG::LDS, st, gp);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, false>),
+  hipLaunchKernelGGL((gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, kEpiNone>),
                      dim3((unsigned)(gp.split + t1)), dim3(NT), CFG::LDS, st, gp);
   return hipGetLastError();
 }

@@ -9,18 +9,21 @@ namespace {
 // 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit.
 using MidTile = TileCfg<128, 2, 2, 2>;
 using SmallTile = TileCfg<64, 2, 2, 4>;
+// the gated layer's smallest: its waves are 64 columns of b wide, 32 of each half
+using SmallGluTile = TileCfg<64, 2, 1, 4>;
 
-template <int KIND, int OUT, bool MASK, typename CFG>
+template <int KIND, int OUT, bool MASK, typename CFG, int EPI>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
   constexpr int BK = GEMM_BK, NT = 64 * CFG::WM * CFG::WN;
   const hipError_t e =
-      allow_dynamic_lds<&gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, true>>(CFG::LDS);
+      allow_dynamic_lds<&gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, EPI>>(CFG::LDS);
   if (e != hipSuccess) return e;
   GemmPair gp{};
   gp.g[0] = gp.g[1] = g;
-  gp.split = ((g.m + CFG::BT - 1) / CFG::BT) * ((g.n + CFG::BT - 1) / CFG::BT);
+  constexpr int YN = EPI == kEpiGlu ? CFG::BT / 2 : CFG::BT;
+  gp.split = ((g.m + CFG::BT - 1) / CFG::BT) * ((g.n + YN - 1) / YN);
   if (gp.split == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, true>), dim3((unsigned)gp.split),
+  hipLaunchKernelGGL((gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, EPI>), dim3((unsigned)gp.split),
                      dim3(NT), CFG::LDS, st, gp);
   return hipGetLastError();
 }
@@ -34,10 +37,17 @@ hipError_t run(const GemmArgs& g, hipStream_t st) {
 // 24.3 against 21.7 us).
 template <int KIND, int OUT, bool MASK>
 hipError_t pick(const GemmArgs& g, hipStream_t st) {
-  auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((g.n + bt - 1) / bt); };
-  if (tiles(256) >= 224) return run<KIND, OUT, MASK, BigTile>(g, st);
-  if (tiles(128) >= 224) return run<KIND, OUT, MASK, MidTile>(g, st);
-  if (tiles(64) > 256) return run<KIND, OUT, MASK, SmallTile>(g, st);
+  const int64_t n = g.glu ? 2 * g.n : g.n;
+  auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((n + bt - 1) / bt); };
+  if (tiles(256) >= 224)
+    return g.glu ? run<KIND, OUT, MASK, BigTile, kEpiGlu>(g, st)
+                 : run<KIND, OUT, MASK, BigTile, kEpiAct>(g, st);
+  if (tiles(128) >= 224)
+    return g.glu ? run<KIND, OUT, MASK, MidTile, kEpiGlu>(g, st)
+                 : run<KIND, OUT, MASK, MidTile, kEpiAct>(g, st);
+  if (tiles(64) > 256)
+    return g.glu ? run<KIND, OUT, MASK, SmallGluTile, kEpiGlu>(g, st)
+                 : run<KIND, OUT, MASK, SmallTile, kEpiAct>(g, st);
   return launch_gemm_ksplit(g, KIND, OUT, st);
 }
 
@@ -50,7 +60,8 @@ hipError_t pick_mask(const GemmArgs& g, hipStream_t st) {
 
 hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
-  if (g.m <= kSkinnyRows) return launch_gemm_skinny(g, kind, out, st);
+  // the few-rows kernel's lanes hold single columns: z kept in 8 bits takes the next larger one
+  if (g.m <= kSkinnyRows && !g.kept) return launch_gemm_skinny(g, kind, out, st);
   if (kind == 0) return out == 1 ? pick_mask<0, 1>(g, st) : pick_mask<0, 2>(g, st);
   return out == 1 ? pick_mask<1, 1>(g, st) : pick_mask<1, 2>(g, st);
 }

@@ -23,7 +23,9 @@ constexpr int kPitch = kT + 4;            // words of a staged row
 constexpr int kLds = 4 * 2 * kSlab;
 static_assert(4 * kT * kPitch * 4 <= kLds, "the partial tiles fit where the rings were");
 
-template <int KIND, int OUT, bool MASK>
+// GLU: the gated layer's epilogue: a tile is 32 columns of the gate and the 32 of the up projection
+// that they meet.
+template <int KIND, int OUT, bool MASK, bool GLU>
 __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
   using SL = Slab<GEMM_BK, kT>;
   using Acc = typename std::conditional<KIND == 0, v16i, v16f>::type;
@@ -39,10 +41,11 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
   // each XCD (workgroup i runs on XCD i % 8) gets a contiguous run of tiles, rows fastest, so its
   // L2 reads a column strip of b once
   const int tiles_m = (int)((g.m + kT - 1) / kT);
-  const int total = tiles_m * (int)((g.n + kT - 1) / kT);
+  constexpr int YN = GLU ? kT / 2 : kT;  // output columns of a tile
+  const int total = tiles_m * (int)((g.n + YN - 1) / YN);
   const int q8 = total / 8, r8 = total % 8, xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
   const int tile = xcd < r8 ? xcd * (q8 + 1) + slot : r8 * (q8 + 1) + (xcd - r8) * q8 + slot;
-  const int64_t m0 = (int64_t)(tile % tiles_m) * kT, n0 = (int64_t)(tile / tiles_m) * kT;
+  const int64_t m0 = (int64_t)(tile % tiles_m) * kT, n0 = (int64_t)(tile / tiles_m) * YN;
 
   const __amdgpu_buffer_rsrc_t ra = raw_rsrc(g.a), rb = raw_rsrc(g.b);
   uint32_t aoff[NI], boff[NI];  // byte offsets of the lane's chunk in slab 0 (operands are < 4 GB)
@@ -52,7 +55,8 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
     const int r = i * SL::RPI + lane / SL::CHUNKS;
     cb[i] = (uint32_t)(((lane % SL::CHUNKS) ^ SL::swz(r)) << 4);
     aoff[i] = (uint32_t)(min(m0 + r, g.m - 1) * g.lda);  // clamped rows feed unused outputs
-    boff[i] = (uint32_t)(min(n0 + r, g.n - 1) * g.ldb);
+    const int64_t br = GLU ? min(n0 + r % YN, g.n - 1) + (r < YN ? 0 : g.n) : min(n0 + r, g.n - 1);
+    boff[i] = (uint32_t)(br * g.ldb);
   }
   const int nk = (int)((g.k + GEMM_BK - 1) / GEMM_BK);
   const int count = nk > wave ? (nk - wave + 3) / 4 : 0;  // slabs of this wave
@@ -148,15 +152,53 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
         *reinterpret_cast<E4*>(part + (wave * kT + y * 32 + fr) * kPitch + x * 32 + q * 8 + fh * 4) = w;
       }
   __syncthreads();
+  if constexpr (GLU) {  // a thread per row and 8 columns of both halves
+    const int cg = (tid & 3) * 8, r = tid >> 2;
+    const int64_t col0 = n0 + cg, row = m0 + r;
+    const int cnt = (int)max((int64_t)0, min((int64_t)8, g.n - col0));
+    const float sar = g.sa[min(row, g.m - 1)];
+    float z[2][8], y[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      E s[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = part[r * kPitch + h * YN + cg + e];
+#pragma unroll
+      for (int w = 1; w < 4; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += part[(w * kT + r) * kPitch + h * YN + cg + e];
+      float sbv[8], bias[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sbv[e] = bias[e] = 0.f;
+      if (cnt > 0) load_cols<float>(g.sb + h * g.n + col0, cnt, sbv);
+      if (g.bias && cnt > 0) load_cols<T>(reinterpret_cast<const T*>(g.bias) + h * g.n + col0, cnt, bias);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[h][e] = __builtin_fmaf((float)s[e] * sar, sbv[e], bias[e]);
+    }
+    act8<T>(g.act, z[0], y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] *= z[1][e];
+    if (g.kept) {
+      keep_cols(g.kept, g.z, g.zp, 2 * row, g.n, col0, row < g.m, z[0]);
+      keep_cols(g.kept, g.z, g.zp, 2 * row + 1, g.n, col0, row < g.m, z[1]);
+    }
+    if (row >= g.m || cnt <= 0) return;
+    store_cols<T>(reinterpret_cast<T*>(g.c) + row * g.ldc + col0, cnt, y);
+    if (g.z && !g.kept) {
+      store_cols<T>(reinterpret_cast<T*>(g.z) + 2 * row * g.n + col0, cnt, z[0]);
+      store_cols<T>(reinterpret_cast<T*>(g.z) + (2 * row + 1) * g.n + col0, cnt, z[1]);
+    }
+    return;
+  }
   const int cg = (tid & 7) * 8;
   const int64_t col0 = n0 + cg;
   const int cnt = (int)max((int64_t)0, min((int64_t)8, g.n - col0));
-  if (cnt <= 0) return;
+  if (cnt <= 0 && !g.kept) return;  // z kept in 8 bits: a quad's lanes stay together
   float sbv[8], bias[8];
-  load_cols<float>(g.sb + col0, cnt, sbv);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) bias[e] = 0.f;
-  if (g.bias) load_cols<T>(reinterpret_cast<const T*>(g.bias) + col0, cnt, bias);
+  for (int e = 0; e < 8; ++e) sbv[e] = bias[e] = 0.f;
+  if (cnt > 0) load_cols<float>(g.sb + col0, cnt, sbv);
+  if (g.bias && cnt > 0) load_cols<T>(reinterpret_cast<const T*>(g.bias) + col0, cnt, bias);
 #pragma unroll
   for (int it = 0; it < 2; ++it) {
     const int r = it * 32 + (tid >> 3);
@@ -164,7 +206,7 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
     if (row >= g.m) continue;
     float res[8];
     const int64_t at = row * g.ldc + col0;
-    if (g.res) load_cols<T>(reinterpret_cast<const T*>(g.res) + at, cnt, res);
+    if (g.res && cnt > 0) load_cols<T>(reinterpret_cast<const T*>(g.res) + at, cnt, res);
     E s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = part[r * kPitch + cg + e];
@@ -181,18 +223,26 @@ __global__ __launch_bounds__(256, 1) void ksplit_kernel(GemmArgs g) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] += res[e];
     }
+    if (g.kept) keep_cols(g.kept, g.z, g.zp, row, g.n, col0, true, z);
+    if (cnt <= 0) continue;
     store_cols<T>(reinterpret_cast<T*>(g.c) + at, cnt, y);
-    if (g.z) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
+    if (g.z && !g.kept) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
   }
+}
+
+template <int KIND, int OUT, bool MASK, bool GLU>
+hipError_t run_form(const GemmArgs& g, hipStream_t st) {
+  const hipError_t e = allow_dynamic_lds<&ksplit_kernel<KIND, OUT, MASK, GLU>>(kLds);
+  if (e != hipSuccess) return e;
+  constexpr int YN = GLU ? kT / 2 : kT;
+  const int64_t tiles = ((g.m + kT - 1) / kT) * ((g.n + YN - 1) / YN);
+  hipLaunchKernelGGL((ksplit_kernel<KIND, OUT, MASK, GLU>), dim3((unsigned)tiles), dim3(256), kLds, st, g);
+  return hipGetLastError();
 }
 
 template <int KIND, int OUT, bool MASK>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
-  const hipError_t e = allow_dynamic_lds<&ksplit_kernel<KIND, OUT, MASK>>(kLds);
-  if (e != hipSuccess) return e;
-  const int64_t tiles = ((g.m + kT - 1) / kT) * ((g.n + kT - 1) / kT);
-  hipLaunchKernelGGL((ksplit_kernel<KIND, OUT, MASK>), dim3((unsigned)tiles), dim3(256), kLds, st, g);
-  return hipGetLastError();
+  return g.glu ? run_form<KIND, OUT, MASK, true>(g, st) : run_form<KIND, OUT, MASK, false>(g, st);
 }
 
 template <int KIND, int OUT>

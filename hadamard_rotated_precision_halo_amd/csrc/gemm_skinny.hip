@@ -9,7 +9,8 @@
 // of b is asked for at the start; the codes go from memory into MFMA operands directly (16 rows x
 // 64 bytes per load, no LDS), since no other wave uses them.  The rows of a (up to 16) are read from
 // the L2.  The waves' partial sums meet in LDS and are added in wave order.  For the fewest rows
-// the rotation and quantisation of a run in the same kernel (skinny_fused_kernel).
+// the rotation and quantisation of a run in the same kernel (skinny_fused_kernel).  The gated layer
+// (y = act(zg) zu) takes 8 rows of the gate and the 8 of the up projection that they meet.
 #include "epilogue.h"
 #include "halo_kernels.h"
 
@@ -46,22 +47,53 @@ struct Step<1> {
   }
 };
 
-// The epilogue of one element.
+// The row of b that lane row r16 of a workgroup holds (clamped rows feed unused outputs), and the
+// output columns of a workgroup.
+template <bool GLU>
+constexpr int kCols = GLU ? 8 : 16;
+template <bool GLU>
+__device__ __forceinline__ int64_t brow(const GemmArgs& g, int64_t n0, int r16) {
+  if constexpr (GLU) return min(n0 + (r16 & 7), g.n - 1) + (r16 < 8 ? 0 : g.n);
+  return min(n0 + r16, g.n - 1);
+}
+
+// z of column col of b.
+template <typename T>
+__device__ __forceinline__ float z_of(const GemmArgs& g, float acc, float sa, int64_t col) {
+  float z = (acc * sa) * g.sb[col];
+  if (g.bias) z += elem_f32<T>(reinterpret_cast<const T*>(g.bias) + col);
+  return z;
+}
+template <typename T>
+__device__ __forceinline__ float act1(int act, float z) {
+  constexpr bool FULL = sizeof(T) == 4;
+  switch (act) {
+    case kActRelu: return act_of<kActRelu, FULL>(z);
+    case kActSilu: return act_of<kActSilu, FULL>(z);
+    case kActGeluTanh: return act_of<kActGeluTanh, FULL>(z);
+    case kActGeluErf: return act_of<kActGeluErf, FULL>(z);
+    default: return z;
+  }
+}
+
+// The epilogue of one element, and of one gated pair.
+template <typename T>
+__device__ __forceinline__ void finish_pair(const GemmArgs& g, float gate, float up, float sa,
+                                            int64_t row, int64_t col) {
+  const float zg = z_of<T>(g, gate, sa, col), zu = z_of<T>(g, up, sa, g.n + col);
+  elem_store<T>(reinterpret_cast<T*>(g.c) + row * g.ldc + col, act1<T>(g.act, zg) * zu);
+  if (g.z) {
+    T* z = reinterpret_cast<T*>(g.z) + 2 * row * g.n + col;
+    elem_store<T>(z, zg);
+    elem_store<T>(z + g.n, zu);
+  }
+}
 template <typename T>
 __device__ __forceinline__ void finish(const GemmArgs& g, float acc, float sa, int64_t row,
                                        int64_t col) {
   const int64_t at = row * g.ldc + col;
-  float z = (acc * sa) * g.sb[col];
-  if (g.bias) z += elem_f32<T>(reinterpret_cast<const T*>(g.bias) + col);
-  constexpr bool FULL = sizeof(T) == 4;
-  float y;
-  switch (g.act) {
-    case kActRelu: y = act_of<kActRelu, FULL>(z); break;
-    case kActSilu: y = act_of<kActSilu, FULL>(z); break;
-    case kActGeluTanh: y = act_of<kActGeluTanh, FULL>(z); break;
-    case kActGeluErf: y = act_of<kActGeluErf, FULL>(z); break;
-    default: y = z;
-  }
+  const float z = z_of<T>(g, acc, sa, col);
+  float y = act1<T>(g.act, z);
   if (g.res) y += elem_f32<T>(reinterpret_cast<const T*>(g.res) + at);
   elem_store<T>(reinterpret_cast<T*>(g.c) + at, y);
   if (g.z) elem_store<T>(reinterpret_cast<T*>(g.z) + at, z);
@@ -85,20 +117,26 @@ __device__ __forceinline__ void load_steps(v4i (&f)[UN][Step<KIND>::CH], const c
 
 // The waves' partial tiles, added in wave order, and the epilogue: element (row i % 16, column
 // i / 16) of thread i is value column % 4 of lane (row, column / 4).
-template <typename T, int KIND, typename Scale>
+template <typename T, int KIND, bool GLU, typename Scale>
 __device__ __forceinline__ void join(const GemmArgs& g, const typename Step<KIND>::Acc (*s_acc)[64],
                                      int64_t n0, Scale scale) {
   using E = typename std::conditional<KIND == 0, int, float>::type;
   const int i = threadIdx.x, row = i & 15, cl = i >> 4;
   const int64_t col = n0 + cl;
-  if (i >= 256 || row >= g.m || col >= g.n) return;
+  if (cl >= kCols<GLU> || row >= g.m || col >= g.n) return;
   E sum = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) sum += s_acc[w][(cl >> 2) * 16 + row][cl & 3];
+  if constexpr (GLU) {
+    E up = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) up += s_acc[w][((cl + 8) >> 2) * 16 + row][cl & 3];
+    return finish_pair<T>(g, (float)sum, (float)up, scale(row), row, col);
+  }
   finish<T>(g, (float)sum, scale(row), row, col);
 }
 
-template <int KIND, int OUT>
+template <int KIND, int OUT, bool GLU>
 __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
   using S = Step<KIND>;
   using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
@@ -106,8 +144,8 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
   __shared__ typename S::Acc s_acc[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q16 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const char* pb = static_cast<const char*>(g.b) + min(n0 + r16, g.n - 1) * g.ldb + q16 * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * kCols<GLU>;
+  const char* pb = static_cast<const char*>(g.b) + brow<GLU>(g, n0, r16) * g.ldb + q16 * 16;
   const char* pa = static_cast<const char*>(g.a) + min((int64_t)r16, g.m - 1) * g.lda + q16 * 16;
 
   typename S::Acc acc = {};
@@ -131,7 +169,7 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
   }
   s_acc[wave][lane] = acc;
   __syncthreads();
-  join<T, KIND>(g, s_acc, n0, [&](int row) { return g.sa[row]; });
+  join<T, KIND, GLU>(g, s_acc, n0, [&](int row) { return g.sa[row]; });
 }
 
 // Butterflies of one stage across lanes at distance 2^S where the block spans them.
@@ -175,7 +213,7 @@ __device__ __forceinline__ void rotate8(float* v, int lane, int block) {
 // own).  A wave takes 512-element slices of the rows, kUnits at most.
 constexpr int kUnits = 4;
 
-template <typename TX, int KIND, int OUT>
+template <typename TX, int KIND, int OUT, bool GLU>
 __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, FqArgs f) {
   using S = Step<KIND>;
   using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
@@ -188,8 +226,8 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   const int r16 = lane & 15, q16 = lane >> 4;
   const int kq = (int)g.k, m = (int)g.m;
   const int pitch = kq + 16;  // rows 16 bytes apart in the banks
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const char* pb = static_cast<const char*>(g.b) + min(n0 + r16, g.n - 1) * g.ldb + q16 * 16;
+  const int64_t n0 = (int64_t)blockIdx.x * kCols<GLU>;
+  const char* pb = static_cast<const char*>(g.b) + brow<GLU>(g, n0, r16) * g.ldb + q16 * 16;
   const int steps = (kq + S::K - 1) / S::K;
   const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
   v4i fb[UN][S::CH];
@@ -263,14 +301,18 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   }
   s_acc[wave][lane] = acc;
   __syncthreads();
-  join<T, KIND>(g, s_acc, n0, [&](int row) { return s_sa[row]; });
+  join<T, KIND, GLU>(g, s_acc, n0, [&](int row) { return s_sa[row]; });
 }
 
 template <typename TX, int KIND, int OUT>
 hipError_t run_fused(const GemmArgs& g, const FqArgs& f, hipStream_t st) {
   const int lds = (int)(g.m * (g.k + 16));
-  hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT>), dim3((unsigned)((g.n + 15) / 16)),
-                     dim3(64 * kWaves), lds, st, g, f);
+  if (g.glu)
+    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, true>), dim3((unsigned)((g.n + 7) / 8)),
+                       dim3(64 * kWaves), lds, st, g, f);
+  else
+    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, false>), dim3((unsigned)((g.n + 15) / 16)),
+                       dim3(64 * kWaves), lds, st, g, f);
   return hipGetLastError();
 }
 
@@ -282,8 +324,12 @@ hipError_t run_fused_x(const GemmArgs& g, const FqArgs& f, int kind, int out, hi
 
 template <int KIND, int OUT>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
-  hipLaunchKernelGGL((skinny_kernel<KIND, OUT>), dim3((unsigned)((g.n + 15) / 16)),
-                     dim3(64 * kWaves), 0, st, g);
+  if (g.glu)
+    hipLaunchKernelGGL((skinny_kernel<KIND, OUT, true>), dim3((unsigned)((g.n + 7) / 8)),
+                       dim3(64 * kWaves), 0, st, g);
+  else
+    hipLaunchKernelGGL((skinny_kernel<KIND, OUT, false>), dim3((unsigned)((g.n + 15) / 16)),
+                       dim3(64 * kWaves), 0, st, g);
   return hipGetLastError();
 }
 

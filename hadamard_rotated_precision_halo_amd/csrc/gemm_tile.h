@@ -34,6 +34,7 @@
 // contiguous run of tiles, rastered in groups of 4 tile rows, for L2 reuse of both operands.
 #pragma once
 
+#include "checkpoint.h"
 #include "epilogue.h"
 #include "halo_device.h"
 #include "halo_kernels.h"
@@ -143,8 +144,12 @@ struct GemmPair {
 };
 
 // EPI: the layer's epilogue (bias, activation, residual, the pre-activation kept) in place of
-// the bare dequant; OUT is then 1 or 2 and also the type of bias, residual and z.
-template <int KIND, int AF, int BF, int OUT, bool MASK, int BK, typename CFG, bool EPI>
+// the bare dequant; OUT is then 1 or 2 and also the type of bias, residual and z.  kEpiGlu: the gated
+// layer's, y = act(zg) zu: a tile's columns of b are BT / 2 of the gate and the BT / 2 of the up
+// projection that they meet, side by side in every wave, so that the pair never leaves it.
+enum Epi { kEpiNone = 0, kEpiAct = 1, kEpiGlu = 2 };
+
+template <int KIND, int AF, int BF, int OUT, bool MASK, int BK, typename CFG, int EPI>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPair gp) {
   constexpr int BM = CFG::BT, BN = CFG::BT, WN = CFG::WN;
   using SL = Slab<BK, CFG::BT>;
@@ -161,7 +166,9 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   // ---- product and tile of this workgroup ---------------------------------------------
   const bool second = (int64_t)blockIdx.x >= gp.split;
   const GemmArgs g = second ? gp.g[1] : gp.g[0];
-  const int tiles_m = (int)((g.m + BM - 1) / BM), tiles_n = (int)((g.n + BN - 1) / BN);
+  constexpr int YN = EPI == kEpiGlu ? BN / 2 : BN;  // output columns per tile
+  static_assert(EPI != kEpiGlu || FB % 2 == 0, "a wave holds both halves of a gated pair");
+  const int tiles_m = (int)((g.m + BM - 1) / BM), tiles_n = (int)((g.n + YN - 1) / YN);
   const int T = tiles_m * tiles_n;
   const int bid = (int)(blockIdx.x - (second ? gp.split : 0));
   const int q8 = T / 8, r8 = T % 8, xcd = bid % 8, slot = bid / 8;
@@ -172,7 +179,13 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   const int gm = min(tiles_m - first_m, GROUP_M);
   const int in_grp = tile % per_group;
   const int64_t m0 = (int64_t)(first_m + in_grp % gm) * BM;
-  const int64_t n0 = (int64_t)(in_grp / gm) * BN;
+  const int64_t n0 = (int64_t)(in_grp / gm) * YN;
+  // b's row of the tile's column r (clamped rows feed unused outputs)
+  auto brow = [&](int r) __attribute__((always_inline)) -> int64_t {
+    if constexpr (EPI != kEpiGlu) return min(n0 + r, g.n - 1);
+    const int64_t c = min(n0 + (r / TN) * (TN / 2) + r % (TN / 2), g.n - 1);
+    return r % TN < TN / 2 ? c : g.n + c;
+  };
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform: LDS bases in SGPRs
@@ -183,7 +196,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   if constexpr (OUT != 0) {
     if (tid < BM) {
       my_sa = g.sa[min(m0 + tid, g.m - 1)];
-      my_sb = g.sb[min(n0 + tid, g.n - 1)];
+      my_sb = g.sb[brow(tid)];
     }
   }
 
@@ -199,7 +212,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
     const int r = wave * WROWS + i * RPI + lane / SL::CHUNKS;
     cbo[i] = (uint32_t)(((lane % SL::CHUNKS) ^ SL::swz(r)) << 4);
     aoff[i] = (uint32_t)(min(m0 + r, g.m - 1) * g.lda);  // clamped rows feed unused outputs
-    boff[i] = (uint32_t)(min(n0 + r, g.n - 1) * g.ldb);
+    boff[i] = (uint32_t)(brow(r) * g.ldb);
   }
   const int nk = (int)((g.k + BK - 1) / BK);
   constexpr int KS = BK / (KIND == 0 ? 32 : 64);  // MFMA K sub-steps per slab
@@ -336,7 +349,75 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   // columns wn * TN + i * 32 + g * 8 + fh * 4 + [0, 4), g = 0..3.  Each wave stages its
   // results in LDS 32 rows at a time and reads them back row-contiguous, 16 bytes per lane.
   __syncthreads();  // every wave is done with the K slabs
-  if constexpr (EPI) {
+  if constexpr (EPI == kEpiGlu) {
+    // The gated layer's epilogue, in the same way: a lane reads back 8 columns of the gate and the 8
+    // of the up projection beside them.
+    using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
+    constexpr int PITCH = TN + 4, HN = TN / 2;
+    constexpr int LPR = HN / 8, RPIT = 64 / LPR, NIT = 32 / RPIT;
+    uint32_t* stile = reinterpret_cast<uint32_t*>(smem) + wave * (32 * PITCH);
+    const int ecol = (lane % LPR) * 8, erow = lane / LPR;
+    const int64_t col0 = n0 + wn * HN + ecol;
+    const int cnt = (int)max((int64_t)0, min((int64_t)8, g.n - col0));  // columns of this lane
+    float sbv[2][8], bias[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sbv[h][e] = s_sb[wn * TN + h * HN + ecol + e];
+        bias[h][e] = 0.f;
+      }
+      if (g.bias && cnt > 0)
+        load_cols<T>(reinterpret_cast<const T*>(g.bias) + h * g.n + col0, cnt, bias[h]);
+    }
+#pragma unroll
+    for (int j = 0; j < FA; ++j) {
+#pragma unroll
+      for (int i = 0; i < FB; ++i)
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+          float4 w;
+          if constexpr (KIND == 0)
+            w = make_float4((float)acc[i][j][gq * 4 + 0], (float)acc[i][j][gq * 4 + 1],
+                            (float)acc[i][j][gq * 4 + 2], (float)acc[i][j][gq * 4 + 3]);
+          else
+            w = make_float4(acc[i][j][gq * 4 + 0], acc[i][j][gq * 4 + 1], acc[i][j][gq * 4 + 2],
+                            acc[i][j][gq * 4 + 3]);
+          *reinterpret_cast<float4*>(stile + fr * PITCH + i * 32 + gq * 8 + fh * 4) = w;
+        }
+      // the wave reads back only what it wrote: program order plus the LDS wait suffice
+#pragma unroll
+      for (int t = 0; t < NIT; ++t) {
+        const int r = t * RPIT + erow;
+        const int64_t row = m0 + wm * TM + j * 32 + r;
+        const float sar = s_sa[wm * TM + j * 32 + r];
+        float z[2][8], y[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 lo = *reinterpret_cast<const float4*>(stile + r * PITCH + h * HN + ecol);
+          const float4 hi = *reinterpret_cast<const float4*>(stile + r * PITCH + h * HN + ecol + 4);
+          const float a[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[h][e] = __builtin_fmaf(a[e] * sar, sbv[h][e], bias[h][e]);
+        }
+        act8<T>(g.act, z[0], y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= z[1][e];
+        if (g.kept) {
+          keep_cols(g.kept, g.z, g.zp, 2 * row, g.n, col0, row < g.m, z[0]);
+          keep_cols(g.kept, g.z, g.zp, 2 * row + 1, g.n, col0, row < g.m, z[1]);
+        }
+        if (row >= g.m || cnt <= 0) continue;
+        store_cols<T>(reinterpret_cast<T*>(g.c) + row * g.ldc + col0, cnt, y);
+        if (g.z && !g.kept) {
+          store_cols<T>(reinterpret_cast<T*>(g.z) + 2 * row * g.n + col0, cnt, z[0]);
+          store_cols<T>(reinterpret_cast<T*>(g.z) + (2 * row + 1) * g.n + col0, cnt, z[1]);
+        }
+      }
+    }
+    return;
+  }
+  if constexpr (EPI == kEpiAct) {
     // The layer's epilogue: the raw accumulators are staged as for fp32 output and read back 8
     // columns per lane; z = (acc * sa) * sb + bias, y = act(z) + residual, each rounded once on
     // its store.  The residual of a 32-row strip is loaded before the strip is staged, so its
@@ -397,10 +478,11 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] += res[t][e];
         }
+        if (g.kept) keep_cols(g.kept, g.z, g.zp, row, g.n, col0, row < g.m, z);
         if (row >= g.m || cnt <= 0) continue;
         const int64_t at = row * g.ldc + col0;
         store_cols<T>(reinterpret_cast<T*>(g.c) + at, cnt, y);
-        if (g.z) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
+        if (g.z && !g.kept) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
       }
     }
     return;

@@ -8,6 +8,7 @@
 // product in low precision): each product's two operands are rotated and quantised along
 // that product's contraction dimension.
 #include "../../include/halo.h"
+#include "checkpoint.h"
 #include "halo_kernels.h"
 
 #include <atomic>
@@ -307,21 +308,59 @@ halo_status check_epilogue(const halo_epilogue* ep) {
   return HALO_OK;
 }
 
+// The form of an activation that the forward kept for the backward.
+int kept_form(halo_dtype t) { return t == HALO_I8 ? kKeptI8 : t == HALO_E4M3 ? kKeptE4M3 : kKeptPlain; }
+
+// Validation of a kept activation; plain: the type of plain elements.
+halo_status check_kept(const halo_kept* a, halo_dtype plain) {
+  if (!dtype_ok(a->type)) return HALO_ERR_DTYPE;
+  if (kept_form(a->type) == kKeptPlain ? a->type != plain || a->powers : false) return HALO_ERR_DTYPE;
+  if (!a->data || (kept_form(a->type) != kKeptPlain && !a->powers)) return HALO_ERR_NULL;
+  return aligned16(a->data) ? HALO_OK : HALO_ERR_ALIGN;
+}
+
+// A validated epilogue: the caller's, with the form z is kept in and the gated layer's pairing.
+struct Ep {
+  const void* bias = nullptr;
+  const void* residual = nullptr;
+  void* z = nullptr;
+  uint8_t* zp = nullptr;
+  int act = 0, kept = kKeptPlain, glu = 0;
+  Ep() = default;
+  explicit Ep(const halo_epilogue* e) {
+    if (!e) return;
+    bias = e->bias;
+    residual = e->residual;
+    z = e->z;
+    act = e->activation;
+  }
+  void keep(const halo_kept* to) {
+    if (!to) return;
+    z = to->data;
+    zp = to->powers;
+    kept = kept_form(to->type);
+  }
+};
+
+// n: rows of b (the gated layer's 2 n).
 GemmArgs act_args(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
-                  const float* sb, int64_t m, int64_t n, int64_t k, void* y,
-                  const halo_epilogue* ep) {
-  GemmArgs g{a, lda, b, ldb, sa, sb, y, n, m, n, k};
-  g.bias = ep->bias;
-  g.res = ep->residual;
-  g.z = ep->z;
-  g.act = ep->activation;
+                  const float* sb, int64_t m, int64_t n, int64_t k, void* y, const Ep& ep) {
+  const int64_t yn = ep.glu ? n / 2 : n;
+  GemmArgs g{a, lda, b, ldb, sa, sb, y, yn, m, yn, k};
+  g.bias = ep.bias;
+  g.res = ep.residual;
+  g.z = ep.z;
+  g.act = ep.act;
+  g.glu = ep.glu;
+  g.kept = ep.kept;
+  g.zp = ep.zp;
   return g;
 }
 
 // The product with its epilogue.
 halo_status act_product(const void* a, int64_t lda, const float* sa, const void* b, int64_t ldb,
                         const float* sb, int64_t m, int64_t n, int64_t k, halo_dtype qt, void* y,
-                        halo_dtype yt, const halo_epilogue* ep, hipStream_t st) {
+                        halo_dtype yt, const Ep& ep, hipStream_t st) {
   return from_hip(launch_gemm_act(act_args(a, lda, sa, b, ldb, sb, m, n, k, y, ep),
                                   qt == HALO_I8 ? 0 : 1, yt == HALO_F32 ? 1 : 2, st));
 }
@@ -352,8 +391,7 @@ halo_status check_fwd(const void* x, const void* w, halo_dtype io_type, int64_t 
 // (NULL: the bare product).  ws holds plan_ws(m, n, k, 0, block).total bytes.
 halo_status run_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m, int64_t n,
                     int64_t k, int32_t block, halo_dtype q_type, void* y, halo_dtype y_type,
-                    const halo_epilogue* ep, const halo_linear_opts* opts, void* ws,
-                    hipStream_t st) {
+                    const Ep* ep, const halo_linear_opts* opts, void* ws, hipStream_t st) {
   const WsPlan p = plan_ws(m, n, k, 0, block);
   const int64_t kq = contraction_len(k, block);
   char* base = static_cast<char*>(ws);
@@ -377,7 +415,7 @@ halo_status run_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
     if (s == HALO_OK) s = run_fa(aw, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
   }
   if (s == HALO_OK && ep)
-    return act_product(qx, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep, st);
+    return act_product(qx, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, *ep, st);
   if (s == HALO_OK)
     s = gemm_any(qx, q_type, kq, sx, qw, q_type, kq, sw, m, n, kq, y, y_type, n, st);
   return s;
@@ -1018,8 +1056,30 @@ halo_status halo_linear_act_fwd(const void* x, const void* w, halo_dtype io_type
   if (s != HALO_OK) return s;
   if (!ws || ws_bytes < plan_ws(m, n, k, 0, block).total) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
-  const halo_epilogue none{};
-  return run_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, ep ? ep : &none, opts, ws,
+  const Ep e(ep);
+  return run_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, &e, opts, ws,
+                 (hipStream_t)stream);
+}
+
+halo_status halo_linear_act_fwd_kept(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                     int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                     void* y, halo_dtype y_type, const halo_epilogue* ep,
+                                     const halo_kept* z, const halo_linear_opts* opts, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  if (!z) return halo_linear_act_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, ep, opts, ws,
+                                     ws_bytes, stream);
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, opts);
+  if (s == HALO_OK) s = check_epilogue(ep);
+  if (s == HALO_OK && ep && ep->z) s = HALO_ERR_OPTION;
+  if (s == HALO_OK && m > 0 && n > 0) s = check_kept(z, y_type);
+  if (s != HALO_OK) return s;
+  if (m > 0 && n > 0 && kept_form(z->type) != kKeptPlain && n % 8 != 0) return HALO_ERR_SHAPE;
+  if (!ws || ws_bytes < plan_ws(m, n, k, 0, block).total) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  Ep e(ep);
+  if (m > 0 && n > 0) e.keep(z);
+  return run_fwd(x, w, io_type, m, n, k, block, q_type, y, y_type, &e, opts, ws,
                  (hipStream_t)stream);
 }
 
@@ -1029,14 +1089,14 @@ size_t halo_linear_act_q_workspace_bytes(int64_t m, int64_t k, int32_t block) {
   return round256((size_t)m * contraction_len(k, block)) + round256((size_t)m * 4);
 }
 
-halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
-                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
-                              void* y, halo_dtype y_type, const halo_epilogue* ep,
-                              const uint32_t* signs_k, void* ws, size_t ws_bytes, void* stream) {
-  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
-  halo_status s = check_fwd(x, qw, io_type, m, n, k, block, q_type, y, y_type, nullptr);
-  if (s == HALO_OK) s = check_epilogue(ep);
-  if (s != HALO_OK) return s;
+namespace {
+
+// A layer on weights quantised once, after check_fwd and the epilogue's checks; n: rows of qw.
+halo_status run_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                  const float* sw, int64_t m, int64_t n, int64_t k, int32_t block, void* y,
+                  halo_dtype y_type, const Ep& ep, const uint32_t* signs_k, void* ws,
+                  size_t ws_bytes, void* stream) {
+  halo_status s = HALO_OK;
   const int64_t kq = contraction_len(k, block);
   if (kq != padded_len(k, block)) return HALO_ERR_SHAPE;
   if (n > 0 && !sw) return HALO_ERR_NULL;
@@ -1051,15 +1111,28 @@ halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw,
   PassOpts po;
   po.signs = signs_k;
   const FqArgs ax = make_fq(x, m, k, k, HALO_ALONG_ROWS, block, q_type, base, kq, sx, po, kq);
-  const halo_epilogue none{};
   if (need == 0) {
-    const GemmArgs g = act_args(nullptr, kq, nullptr, qw, kq, sw, m, n, kq, y, ep ? ep : &none);
+    const GemmArgs g = act_args(nullptr, kq, nullptr, qw, kq, sw, m, n, kq, y, ep);
     return from_hip(launch_skinny_fused(g, ax, io_type == HALO_BF16 ? 1 : 0, q_type == HALO_I8 ? 0 : 1,
                                         y_type == HALO_F32 ? 1 : 2, st));
   }
   s = run_fa(ax, io_type, HALO_ALONG_ROWS, q_type, nullptr, 0, st);
   if (s != HALO_OK) return s;
-  return act_product(base, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep ? ep : &none, st);
+  return act_product(base, kq, sx, qw, kq, sw, m, n, kq, q_type, y, y_type, ep, st);
+}
+
+}  // namespace
+
+halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
+                              void* y, halo_dtype y_type, const halo_epilogue* ep,
+                              const uint32_t* signs_k, void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_fwd(x, qw, io_type, m, n, k, block, q_type, y, y_type, nullptr);
+  if (s == HALO_OK) s = check_epilogue(ep);
+  if (s != HALO_OK) return s;
+  return run_q(x, io_type, qw, q_type, sw, m, n, k, block, y, y_type, Ep(ep), signs_k, ws, ws_bytes,
+               stream);
 }
 
 size_t halo_linear_act_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
@@ -1121,6 +1194,219 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
   }
   return run_bwd(act ? dz : dy, act ? HALO_F32 : io_type, x, w, io_type, m, n, k, block, q_type,
                  grad_q_type, dx, dw, opts, ws, st);
+}
+
+// ---- activations kept in 8 bits ---------------------------------------------------------------
+
+namespace {
+
+halo_status check_keep(const void* x, const halo_dtype& x_type, int64_t rows, int64_t cols,
+                       int64_t ldx, const halo_dtype& q_type, const void* codes, int64_t ldc,
+                       const uint8_t* powers, int64_t ldp) {
+  if (!dtype_ok(x_type) || !dtype_ok(q_type)) return HALO_ERR_DTYPE;
+  if ((x_type != HALO_F32 && x_type != HALO_BF16) || (q_type != HALO_I8 && q_type != HALO_E4M3))
+    return HALO_ERR_DTYPE;
+  if (rows < 0 || cols < 0 || rows >= kMaxDim || cols >= kMaxDim) return HALO_ERR_SHAPE;
+  if (rows == 0 || cols == 0) return HALO_OK;  // empty tensors may come with NULL pointers
+  if (!x || !codes || !powers) return HALO_ERR_NULL;
+  if (ldx < cols || ldc < cols || ldp < (cols + kGroup - 1) / kGroup) return HALO_ERR_SHAPE;
+  return aligned_to(x, esize(x_type)) ? HALO_OK : HALO_ERR_ALIGN;
+}
+
+}  // namespace
+
+halo_status halo_checkpoint_pack(const void* x, halo_dtype x_type, int64_t rows, int64_t cols,
+                                 int64_t ldx, halo_dtype q_type, void* codes, int64_t ldc,
+                                 uint8_t* powers, int64_t ldp, void* stream) {
+  const halo_status s = check_keep(x, x_type, rows, cols, ldx, q_type, codes, ldc, powers, ldp);
+  if (s != HALO_OK || rows == 0 || cols == 0) return s;
+  const KeepArgs a{x, nullptr, codes, powers, ldx, ldc, ldp, rows, cols, 0, 0};
+  return from_hip(launch_keep(a, x_type == HALO_BF16 ? 1 : 0, qt_index(q_type), true,
+                              (hipStream_t)stream));
+}
+
+halo_status halo_checkpoint_unpack(const void* codes, halo_dtype q_type, int64_t ldc,
+                                   const uint8_t* powers, int64_t ldp, int64_t rows, int64_t cols,
+                                   void* x, halo_dtype x_type, int64_t ldx, void* stream) {
+  const halo_status s = check_keep(x, x_type, rows, cols, ldx, q_type, codes, ldc, powers, ldp);
+  if (s != HALO_OK || rows == 0 || cols == 0) return s;
+  const KeepArgs a{nullptr, x, const_cast<void*>(codes), const_cast<uint8_t*>(powers), ldx, ldc, ldp,
+                   rows, cols, 0, 0};
+  return from_hip(launch_keep(a, x_type == HALO_BF16 ? 1 : 0, qt_index(q_type), false,
+                              (hipStream_t)stream));
+}
+
+// ---- the gated layer, and gradients from kept activations ---------------------------------------
+
+namespace {
+
+// The gated layer's checks beside check_fwd's over 2 n rows of w.
+halo_status check_glu(const halo_dtype& y_type, int64_t n, const void* bias,
+                      const halo_activation& activation) {
+  if (n < 0 || n >= kMaxDim / 2 || (n * esize(y_type)) % 16 != 0) return HALO_ERR_SHAPE;
+  if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return HALO_ERR_OPTION;
+  return aligned16(bias) ? HALO_OK : HALO_ERR_ALIGN;
+}
+
+void glu_ep(Ep& e, const void* bias, halo_activation activation) {
+  e.bias = bias;
+  e.act = (int)activation;
+  e.glu = 1;
+}
+
+// Workspace of a layer backward from kept activations: the layer's (of nz output features), the
+// stored dz, the bias gradient's partial rows and x read back, where the call has them.
+struct KeptBwdWs {
+  size_t dz, part, x, total;  // byte offsets, and the whole
+};
+
+KeptBwdWs kept_bwd_ws(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block, bool glu,
+                      bool act, halo_dtype x_type, bool dw, bool db) {
+  const int64_t nz = glu ? 2 * n : n;
+  KeptBwdWs w{};
+  w.dz = plan_ws(m, nz, k, 1, block).total;
+  w.part = w.dz + (act || glu ? round256((size_t)m * nz * 4) : 0);
+  w.x = w.part + (db ? round256((size_t)act_grad_parts(m, n) * nz * 4) : 0);
+  w.total = w.x + (dw && kept_form(x_type) != kKeptPlain ? round256((size_t)m * k * esize(io_type)) : 0);
+  return w;
+}
+
+size_t kept_bwd_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t block, const halo_dtype& io_type,
+                         const halo_dtype& q_type, const halo_activation& activation,
+                         const halo_dtype& z_type, const halo_dtype& x_type, int32_t gradients,
+                         const halo_rounding& rounding, bool glu) {
+  if (!dtype_ok(io_type) || (io_type != HALO_F32 && io_type != HALO_BF16)) return 0;
+  if (!dtype_ok(x_type) || !dtype_ok(z_type) || !dtype_ok(q_type)) return 0;
+  if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return 0;
+  if (!enum_in(rounding, HALO_ROUND_NEAREST_EVEN, HALO_ROUND_STOCHASTIC)) return 0;
+  if (gradients & ~(HALO_GRAD_DX | HALO_GRAD_DW | HALO_GRAD_DB)) return 0;
+  if (n < 0 || n >= kMaxDim / 2 ||
+      halo_linear_workspace_bytes_ex(m, glu ? 2 * n : n, k, block, q_type, 1) == 0)
+    return 0;
+  return kept_bwd_ws(io_type, m, n, k, block, glu, activation != HALO_ACT_NONE, x_type,
+                     gradients & HALO_GRAD_DW, gradients & HALO_GRAD_DB)
+      .total;
+}
+
+halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& activation,
+                     const halo_kept* x, const void* w, const halo_dtype& io_type, int64_t m,
+                     int64_t n, int64_t k, int32_t block, const halo_dtype& q_type,
+                     const halo_dtype& grad_q_type, void* dx, void* dw, void* db,
+                     const halo_linear_opts* opts, void* ws, size_t ws_bytes, hipStream_t st,
+                     bool glu) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
+  if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return HALO_ERR_OPTION;
+  const bool act = activation != HALO_ACT_NONE, has_dz = act || glu;
+  if (!x || (has_dz && !z)) return HALO_ERR_NULL;
+  if (n < 0 || n >= kMaxDim / 2 || n % 8 != 0) return HALO_ERR_SHAPE;
+  const int64_t nz = glu ? 2 * n : n;
+  halo_status s = check_bwd(dy, has_dz ? HALO_F32 : io_type, x->data, w, io_type, m, nz, k, block,
+                            q_type, grad_q_type, dx, dw, opts);
+  if (s == HALO_OK) s = check_kept(x, io_type);
+  if (s == HALO_OK && has_dz) s = check_kept(z, io_type);
+  if (s != HALO_OK) return s;
+  if (!aligned16(db)) return HALO_ERR_ALIGN;
+  const KeptBwdWs wl = kept_bwd_ws(io_type, m, n, k, block, glu, act, x->type, dw, db);
+  if (!ws || ws_bytes < wl.total) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  const int inb = io_type == HALO_BF16 ? 1 : 0;
+  char* base = static_cast<char*>(ws);
+  float* dz = reinterpret_cast<float*>(base + wl.dz);
+  float* part = reinterpret_cast<float*>(base + wl.part);
+  hipError_t e = hipSuccess;
+  if (has_dz) {
+    const DzArgs a{dy, z->data, z->powers, kept_form(z->type), (int)activation, glu ? 1 : 0, m, n, dz,
+                   db, part};
+    e = launch_dz(a, inb, st);
+  } else if (db) {
+    e = launch_act_grad(dy, nullptr, (int)HALO_ACT_NONE, inb, m, n, nullptr, db, part, st);
+  }
+  const void* xv = x->data;
+  if (e == hipSuccess && dw && kept_form(x->type) != kKeptPlain) {
+    const KeepArgs a{nullptr, base + wl.x, x->data, x->powers, k, k, (k + kGroup - 1) / kGroup, m, k,
+                     0, 0};
+    e = launch_keep(a, inb, qt_index(x->type), false, st);
+    xv = base + wl.x;
+  }
+  if (e != hipSuccess) return HALO_ERR_HIP;
+  if (!dx && !dw) return HALO_OK;
+  return run_bwd(has_dz ? dz : dy, has_dz ? HALO_F32 : io_type, xv, w, io_type, m, nz, k, block,
+                 q_type, grad_q_type, dx, dw, opts, ws, st);
+}
+
+}  // namespace
+
+halo_status halo_linear_glu_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type, void* y,
+                                halo_dtype y_type, const void* bias, halo_activation activation,
+                                const halo_kept* z, const halo_linear_opts* opts, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_glu(y_type, n, bias, activation);
+  if (s == HALO_OK) s = check_fwd(x, w, io_type, m, 2 * n, k, block, q_type, y, y_type, opts);
+  if (s == HALO_OK && z && m > 0 && n > 0) s = check_kept(z, y_type);
+  if (s != HALO_OK) return s;
+  if (z && m > 0 && n > 0 && kept_form(z->type) != kKeptPlain && n % 8 != 0) return HALO_ERR_SHAPE;
+  if (!ws || ws_bytes < plan_ws(m, 2 * n, k, 0, block).total) return HALO_ERR_WORKSPACE;
+  if (!aligned16(ws)) return HALO_ERR_ALIGN;
+  Ep e;
+  glu_ep(e, bias, activation);
+  if (m > 0 && n > 0) e.keep(z);
+  return run_fwd(x, w, io_type, m, 2 * n, k, block, q_type, y, y_type, &e, opts, ws,
+                 (hipStream_t)stream);
+}
+
+halo_status halo_linear_glu_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
+                              void* y, halo_dtype y_type, const void* bias,
+                              halo_activation activation, const uint32_t* signs_k, void* ws,
+                              size_t ws_bytes, void* stream) {
+  if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(y_type)) return HALO_ERR_DTYPE;
+  halo_status s = check_glu(y_type, n, bias, activation);
+  if (s == HALO_OK) s = check_fwd(x, qw, io_type, m, 2 * n, k, block, q_type, y, y_type, nullptr);
+  if (s != HALO_OK) return s;
+  Ep e;
+  glu_ep(e, bias, activation);
+  return run_q(x, io_type, qw, q_type, sw, m, 2 * n, k, block, y, y_type, e, signs_k, ws, ws_bytes,
+               stream);
+}
+
+size_t halo_linear_act_bwd_kept_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                                halo_dtype io_type, halo_dtype q_type,
+                                                halo_activation activation, halo_dtype z_type,
+                                                halo_dtype x_type, int32_t gradients,
+                                                halo_rounding grad_rounding) {
+  return kept_bwd_ws_bytes(m, n, k, block, io_type, q_type, activation, z_type, x_type, gradients,
+                           grad_rounding, false);
+}
+
+halo_status halo_linear_act_bwd_kept(const void* dy, const halo_kept* z,
+                                     halo_activation activation, const halo_kept* x, const void* w,
+                                     halo_dtype io_type, int64_t m, int64_t n, int64_t k,
+                                     int32_t block, halo_dtype q_type, halo_dtype grad_q_type,
+                                     void* dx, void* dw, void* db, const halo_linear_opts* opts,
+                                     void* ws, size_t ws_bytes, void* stream) {
+  return kept_bwd(dy, z, activation, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw, db,
+                  opts, ws, ws_bytes, (hipStream_t)stream, false);
+}
+
+size_t halo_linear_glu_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                           halo_dtype io_type, halo_dtype q_type,
+                                           halo_activation activation, halo_dtype z_type,
+                                           halo_dtype x_type, int32_t gradients,
+                                           halo_rounding grad_rounding) {
+  return kept_bwd_ws_bytes(m, n, k, block, io_type, q_type, activation, z_type, x_type, gradients,
+                           grad_rounding, true);
+}
+
+halo_status halo_linear_glu_bwd(const void* dy, const halo_kept* z, halo_activation activation,
+                                const halo_kept* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                halo_dtype grad_q_type, void* dx, void* dw, void* db,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream) {
+  return kept_bwd(dy, z, activation, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw, db,
+                  opts, ws, ws_bytes, (hipStream_t)stream, true);
 }
 
 }  // extern "C"

@@ -128,6 +128,13 @@ struct GemmArgs {
   const void* res = nullptr;
   void* z = nullptr;
   int act = 0;
+  // glu: the gated layer: b holds 2 n rows (gate, then up), sb and bias 2 n entries, y = act(zg) zu
+  // is [m x n] and z [m x 2 n]; no residual
+  int glu = 0;
+  // kept: z's form (a Kept of checkpoint.h); its codes go to z and its powers to zp (the gated
+  // layer's z as 2 m rows of n)
+  int kept = 0;
+  uint8_t* zp = nullptr;
 };
 
 // kind: 0 INT8, 1 FP8.  afmt/bfmt (FP8 only): 0 E4M3, 1 E5M2.  out: 0 int32, 1 fp32, 2 bf16.
@@ -157,6 +164,33 @@ hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t
                            hipStream_t st);
 hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
                            int64_t n, float* dz, void* db, float* part, hipStream_t st);
+
+// The general form: dz in fp32 of a layer whose z is plain (kept 0) or a checkpoint (kept: a Kept of
+// checkpoint.h, zp its powers), or of the gated layer (glu: z is 2 m rows of n, dz [m x 2 n], db
+// [2 n], part act_grad_parts(m, n) x 2 n).
+struct DzArgs {
+  const void *dy, *z;
+  const uint8_t* zp;
+  int kept, act, glu;
+  int64_t m, n;
+  float* dz;
+  void* db;     // or NULL
+  float* part;
+};
+hipError_t launch_dz(const DzArgs& a, int in_bf16, hipStream_t st);
+
+// Rows to 8-bit checkpoints (pack: x is read) and back (x_out is written); see checkpoint.h.  qt: 0
+// INT8, 1 E4M3.  Any leading dimension of at least a row, any alignment of whole elements.
+struct KeepArgs {
+  const void* x;
+  void* x_out;
+  void* codes;      // [rows x cols], ldc
+  uint8_t* powers;  // [rows x ceil(cols / 32)], ldp
+  int64_t ldx, ldc, ldp, rows, cols;
+  int64_t rows_per_wg;  // set by the launcher, as tpr
+  int tpr;
+};
+hipError_t launch_keep(const KeepArgs& a, int in_bf16, int qt, bool pack, hipStream_t st);
 
 // Workgroups of `threads` along x that one launch may hold: HIP counts a launch's threads along an
 // axis in 32 bits, and what passes them is dropped without an error.  The row operators, whose

@@ -421,6 +421,108 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
                                 void* stream);
 
 /*
+ * Activations kept in 8 bits for the backward pass (checkpoints).  A row is cut into groups of 32
+ * values (the last may be shorter); group g has one byte s and stands for
+ *   v = code 2^(s - 127),   2^(s - 127) the least power of two with max |v| <= qmax 2^(s - 127),
+ * qmax 127 (HALO_I8) or 448 (HALO_E4M3), s in [16, 248] (HALO_E4M3: [16, 246]); the codes are
+ * v / 2^(s - 127) rounded once, ties to even, and kept within +-qmax.  Every value that a checkpoint
+ * stands for is a bf16 number, so all readers see the same one.  Magnitudes below 2^-112 are kept to
+ * within 2^-112.  A group that holds an infinity or a NaN has s = 255 and stands for NaN throughout.
+ */
+typedef struct {
+    void* data;      /* [rows x cols] dense: elements of `type`, or codes of it with `powers`       */
+    uint8_t* powers; /* [rows x ceil(cols / 32)] dense: s of every group; NULL for plain elements   */
+    halo_dtype type; /* HALO_I8 or HALO_E4M3 with powers; HALO_F32 or HALO_BF16 (the call's) without */
+} halo_kept;
+
+/*
+ * Rows of x to a checkpoint, and a checkpoint to rows.
+ *   x        HALO_F32 or HALO_BF16 [rows x cols], any leading dimension >= cols, any pointer aligned
+ *            to its element.  Reading a checkpoint as bf16 or as fp32 gives the same numbers.
+ *   q_type   HALO_I8 or HALO_E4M3;  codes [rows x cols], ldc >= cols;
+ *   powers   [rows x ceil(cols / 32)], ldp >= ceil(cols / 32).
+ */
+halo_status halo_checkpoint_pack(const void* x, halo_dtype x_type, int64_t rows, int64_t cols,
+                                 int64_t ldx, halo_dtype q_type, void* codes, int64_t ldc,
+                                 uint8_t* powers, int64_t ldp, void* stream);
+halo_status halo_checkpoint_unpack(const void* codes, halo_dtype q_type, int64_t ldc,
+                                   const uint8_t* powers, int64_t ldp, int64_t rows, int64_t cols,
+                                   void* x, halo_dtype x_type, int64_t ldx, void* stream);
+
+/*
+ * halo_linear_act_fwd whose z goes to `z` (plain elements of y_type or a checkpoint, taken from the
+ * fp32 z; NULL: not kept).  ep->z must be NULL beside it (HALO_ERR_OPTION).  For a checkpoint n is a
+ * multiple of 8.
+ */
+halo_status halo_linear_act_fwd_kept(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                     int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                     void* y, halo_dtype y_type, const halo_epilogue* ep,
+                                     const halo_kept* z, const halo_linear_opts* opts, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/*
+ * halo_linear_act_bwd from kept activations: x [m x k] and z [m x n], each plain elements of io_type
+ * or a checkpoint (z NULL with HALO_ACT_NONE).  The gradients are those of the values kept.
+ *   ws   at least halo_linear_act_bwd_kept_workspace_bytes(...) bytes for the call's own types.
+ */
+size_t halo_linear_act_bwd_kept_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                                halo_dtype io_type, halo_dtype q_type,
+                                                halo_activation activation, halo_dtype z_type,
+                                                halo_dtype x_type, int32_t gradients,
+                                                halo_rounding grad_rounding);
+halo_status halo_linear_act_bwd_kept(const void* dy, const halo_kept* z,
+                                     halo_activation activation, const halo_kept* x, const void* w,
+                                     halo_dtype io_type, int64_t m, int64_t n, int64_t k,
+                                     int32_t block, halo_dtype q_type, halo_dtype grad_q_type,
+                                     void* dx, void* dw, void* db, const halo_linear_opts* opts,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The gated feed-forward layer: both projections as one rotated 8-bit product, the activation and
+ * the product of the two in its epilogue.  w [2 n x k] holds the gate's n rows, then the up
+ * projection's; bias [2 n] or NULL:
+ *   z = X W^T + bias  [m x 2 n],   y = act(z[:, :n]) z[:, n:]  [m x n],
+ * fp32 until the stores; y and z are rounded once each.
+ *   z    receives z (plain elements of y_type [m x 2 n], or a checkpoint of 2 m rows of n: a token's
+ *        gate half, then its up half; n a multiple of 8), or NULL.
+ * Other arguments, workspace (of 2 n output features) and errors as halo_linear_act_fwd; n a
+ * multiple of 16 bytes of y_type.  halo_linear_glu_q: on weights quantised once, as
+ * halo_linear_act_q (qw [2 n x kq], sw [2 n]; workspace halo_linear_act_q_workspace_bytes).
+ */
+halo_status halo_linear_glu_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type, void* y,
+                                halo_dtype y_type, const void* bias, halo_activation activation,
+                                const halo_kept* z, const halo_linear_opts* opts, void* ws,
+                                size_t ws_bytes, void* stream);
+halo_status halo_linear_glu_q(const void* x, halo_dtype io_type, const void* qw, halo_dtype q_type,
+                              const float* sw, int64_t m, int64_t n, int64_t k, int32_t block,
+                              void* y, halo_dtype y_type, const void* bias,
+                              halo_activation activation, const uint32_t* signs_k, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the gated layer for dy [m x n] of y: with g, u the halves of z,
+ *   dz = [dy u act'(g), dy act(g)]  [m x 2 n],   dX = dz W,   dW = dz^T X,   db = sum over rows of dz,
+ * the products as halo_linear_bwd's over 2 n output features (signs_n covers 2 n).  dz is fp32 from
+ * the activation to its rotation.
+ *   z, x   the forward's, each plain elements of io_type or a checkpoint (z as halo_linear_glu_fwd
+ *          writes it).  dx [m x k], dw [2 n x k], db [2 n]: each may be NULL.
+ *   ws     at least halo_linear_glu_bwd_workspace_bytes(...) bytes for the call's own types.
+ * n and k are multiples of 8; everything else as halo_linear_act_bwd with an activation.
+ */
+size_t halo_linear_glu_bwd_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t block,
+                                           halo_dtype io_type, halo_dtype q_type,
+                                           halo_activation activation, halo_dtype z_type,
+                                           halo_dtype x_type, int32_t gradients,
+                                           halo_rounding grad_rounding);
+halo_status halo_linear_glu_bwd(const void* dy, const halo_kept* z, halo_activation activation,
+                                const halo_kept* x, const void* w, halo_dtype io_type, int64_t m,
+                                int64_t n, int64_t k, int32_t block, halo_dtype q_type,
+                                halo_dtype grad_q_type, void* dx, void* dw, void* db,
+                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/*
  * Row operators: the join between two blocks of a model and the distillation loss.  Unlike the
  * rotation and the products they take any leading dimension (at least the row's width) and any
  * pointer aligned to its own element.
