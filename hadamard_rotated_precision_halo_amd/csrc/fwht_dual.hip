@@ -32,6 +32,7 @@ namespace halo {
 namespace {
 
 constexpr int kTile = 256;
+constexpr int kDualLdsBytes = 16 * 512 * 16;  // 16 waves x 512 chunks of 16 bytes
 constexpr uint32_t kLateMark = 0x80000000u;
 
 struct DualProb {
@@ -153,7 +154,7 @@ __device__ __forceinline__ void dual_task(const DualProb& dp, int64_t ltask, uin
     const int64_t row = r0 + w * (4096 / kTile) + rseg;
     const int64_t pos0 = c0 - (int64_t)rseg * kTile;    // + off(lane, j): column index
     const uint16_t* xr = reinterpret_cast<const uint16_t*>(dp.ar.x) + row * dp.ar.ldx;
-    load_slice<uint16_t, B>(dp.ar, xr, pos0, lane, true, v);
+    load_slice<uint16_t, B>(dp.ar, xr, pos0, lane, true, 0, v);
     const float sgn = rotate64<B>(v, lane);
     float mx = lane_max(absmax64(v), row_lanes_log2);
     bool late = false;
@@ -194,9 +195,9 @@ size_t dual_scratch_bytes(int64_t rows, int64_t cols) {
 template <int B, int QT, bool SR>
 hipError_t launch_dual_t(const FqArgs& ar, const FqArgs& ac, void* ws, int prezeroed,
                          hipStream_t st) {
-  hipError_t e = allow_dynamic_lds<&fq_dual_kernel<B, QT, SR, false>>(kColsLdsBytes);
+  hipError_t e = allow_dynamic_lds<&fq_dual_kernel<B, QT, SR, false>>(kDualLdsBytes);
   if (e != hipSuccess) return e;
-  e = allow_dynamic_lds<&fq_dual_kernel<B, QT, SR, true>>(kColsLdsBytes);
+  e = allow_dynamic_lds<&fq_dual_kernel<B, QT, SR, true>>(kDualLdsBytes);
   if (e != hipSuccess) return e;
   const int64_t rows = ar.nvec, cols = ac.nvec;
   DualProb dp{};
@@ -227,7 +228,7 @@ hipError_t launch_dual_t(const FqArgs& ar, const FqArgs& ac, void* ws, int preze
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((fq_dual_kernel<B, QT, SR, false>), dim3((unsigned)tiles), dim3(1024),
-                     kColsLdsBytes, st, dp);
+                     kDualLdsBytes, st, dp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   // the repair launch: its workgroups (at most one per compute unit) return at once unless a
@@ -235,7 +236,7 @@ hipError_t launch_dual_t(const FqArgs& ar, const FqArgs& ac, void* ws, int preze
   const int cap = cols2_capacity(reinterpret_cast<const void*>(&fq_dual_kernel<B, QT, SR, false>));
   const int64_t rgrid = tiles < cap ? tiles : (cap > 0 ? cap : 1);
   hipLaunchKernelGGL((fq_dual_kernel<B, QT, SR, true>), dim3((unsigned)rgrid), dim3(1024),
-                     kColsLdsBytes, st, dp);
+                     kDualLdsBytes, st, dp);
   return hipGetLastError();
 }
 

@@ -46,11 +46,13 @@
 // a template parameter, instantiated in fwht_wave_sr.hip).
 #pragma once
 
+#include "checkpoint.h"
 #include "epilogue.h"
 #include "halo_device.h"
 #include "halo_kernels.h"
 
 #include <atomic>
+#include <type_traits>
 
 namespace halo {
 
@@ -232,12 +234,23 @@ __device__ __forceinline__ void store_chunk8_sr(void* q, int64_t idx, const floa
 // Store the 8 chunks of a lane: codes of vector vec, whose chunk j sits at position
 // pos0 + off(lane, j) of the vector and at element base + off(lane, j) of the code array.
 // SR: stochastic rounding (a separate instantiation, so that the nearest-even kernels keep
-// their register budget).
-template <int B, int QT, bool SR>
+// their register budget).  END: positions from a.len on are not stored (a lane of blocks of 64 and
+// more is whole on one side: its caller leaves it out).
+template <int B, int QT, bool SR, bool END = false>
 __device__ __forceinline__ void store_slice(const FqArgs& a, const float* v, float mul,
                                             int64_t base, int lane, int64_t vec, int64_t pos0) {
   using S = Slice<B>;
-  if constexpr (SR && QT != 3) {
+  if constexpr (END && B < 64) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (pos0 + S::off(lane, j) >= a.len) continue;
+      if constexpr (SR && QT != 3)
+        store_chunk8_sr<QT>(a.q, base + S::off(lane, j), &v[j * 8], mul, a, vec,
+                            pos0 + S::off(lane, j));
+      else
+        store_chunk8<QT>(a.q, base + S::off(lane, j), &v[j * 8], mul);
+    }
+  } else if constexpr (SR && QT != 3) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       store_chunk8_sr<QT>(a.q, base + S::off(lane, j), &v[j * 8], mul, a, vec,
@@ -299,17 +312,63 @@ __device__ __forceinline__ void store_slice_staged(const FqArgs& a, const float*
   }
 }
 
+// Chunk of 8 of z in its kept form: 16 bytes of bf16, or 8 codes and their power.
+struct ZChunk {
+  uint4 w;
+  __device__ __forceinline__ void load(const FqArgs& a, int64_t row, int64_t width, int64_t col) {
+    if (a.zk == kKeptPlain) {
+      w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.z) + row * width + col);
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.z) +
+                                                      row * width + col);
+      w.x = q.x;
+      w.y = q.y;
+      w.z = a.zw[row * ((width + kGroup - 1) / kGroup) + col / kGroup];
+    }
+  }
+  __device__ __forceinline__ void get(int zk, float* o) const {
+    if (zk == kKeptPlain) unpack_bf16x8(w, o);
+    else if (zk == kKeptI8) kept8<0>(make_uint2(w.x, w.y), w.z, o);
+    else kept8<1>(make_uint2(w.x, w.y), w.z, o);
+  }
+};
+
+// The 8 chunks of a lane of dz = dy act'(z), z in any kept form.
+template <int B>
+__device__ __forceinline__ void load_dz_slice(const FqArgs& a, const uint16_t* vp, int64_t pos0,
+                                              int lane, bool valid, int64_t row, float* v) {
+  using S = Slice<B>;
+  uint4 d[8];
+  ZChunk z[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int64_t pos = pos0 + S::off(lane, j);
+    const int64_t at = valid && pos < a.in_len ? pos : 0;
+    d[j] = *reinterpret_cast<const uint4*>(vp + at);
+    z[j].load(a, row, a.in_len, at);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float zv[8];
+    unpack_bf16x8(d[j], &v[j * 8]);
+    z[j].get(a.zk, zv);
+    slope_mul<8>(a.act, zv, &v[j * 8]);
+  }
+}
+
 // Load the 8 chunks of a lane: chunk j at position pos0 + off(lane, j) of the vector whose
 // element 0 is at vp.  The loads are unconditional (a chunk of the zero padding, at and past
 // in_len, reads chunk 0 instead), so they issue back to back; only passes with padding then
-// zero those chunks.  Then the transform's signs.  ACT: the vector is dz = dy act'(z), z at the
-// same place of a.z as dy of a.x.
-template <typename Tin, int B, bool ACT = false>
+// zero those chunks.  Then the transform's signs.  ACT: the vector is dz (a DyForm), z at the
+// same place of a.z as dy of a.x, or, kept, at its own of vector `row`.
+template <typename Tin, int B, int ACT = kDyPlain>
 __device__ __forceinline__ void load_slice(const FqArgs& a, const Tin* vp, int64_t pos0, int lane,
-                                           bool valid, float* v) {
+                                           bool valid, int64_t row, float* v) {
   using S = Slice<B>;
-  if constexpr (ACT) {
-    const Tin* zp = a.z + (vp - reinterpret_cast<const Tin*>(a.x));
+  if constexpr (ACT == kDyKept) {
+    load_dz_slice<B>(a, vp, pos0, lane, valid, row, v);
+  } else if constexpr (ACT == kDyAct) {
+    const Tin* zp = reinterpret_cast<const Tin*>(a.z) + (vp - reinterpret_cast<const Tin*>(a.x));
     uint4 d[8], z[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -374,7 +433,7 @@ __device__ __forceinline__ float stored_scale(const FqArgs& a, float mx) {
 
 // One wave's slice of a rows pass with L <= 4096 and 4096 % L == 0: wave `gw` of the pass owns
 // rows [gw * 4096 / L, (gw + 1) * 4096 / L).  Lanes past the last row idle.
-template <typename Tin, int B, int QT, bool SR, bool ACT = false>
+template <typename Tin, int B, int QT, bool SR, int ACT = kDyPlain>
 __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane) {
   using S = Slice<B>;
   const int L = (int)a.len;
@@ -388,7 +447,7 @@ __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane)
   // idle lanes read the first chunk of row 0
   const Tin* rp = xin + (valid ? row : 0) * a.ldx;
   float v[64];
-  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, v);
+  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, valid ? row : 0, v);
   const float sgn = rotate64<B>(v, lane);
   float mx = valid ? absmax64(v) : 0.f;
   mx = lane_max(mx, row_lanes_log2);
@@ -400,11 +459,12 @@ __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane)
 }
 
 // QT: 0 INT8, 1 E4M3, 2 E5M2, 3 fp32 rotated values.
-// multi = 1: one row per workgroup, wave w owns columns [4096 w, 4096 (w + 1)).
+// multi = 1: one row per workgroup, wave w owns columns [4096 w, 4096 (w + 1)) (also for rows of
+// less than 4096 that do not divide it).
 // multi = 0: 4096 % L == 0, each wave owns 4096 / L whole rows.
 // One launch serves up to two passes of the same geometry (workgroups below pp.split run the
 // first), and can clear a scratch range for the column passes that follow it on the stream.
-template <typename Tin, int B, int QT, bool SR, bool ACT = false>
+template <typename Tin, int B, int QT, bool SR, int ACT = kDyPlain>
 __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   using S = Slice<B>;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, nw = blockDim.x >> 6;
@@ -427,7 +487,7 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
       if (row >= a.nvec) return;
       const Tin* rp = reinterpret_cast<const Tin*>(a.x) + row * a.ldx;
       float v[64];
-      load_slice<Tin, B, ACT>(a, rp, 0, lane, true, v);
+      load_slice<Tin, B, ACT>(a, rp, 0, lane, true, row, v);
       const float sgn = rotate64<B>(v, lane);
       const float mx = lane_max(absmax64(v), 6);
       if (lane == 0) a.scale[row] = stored_scale<QT>(a, mx);
@@ -444,7 +504,7 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   const Tin* __restrict__ xin = reinterpret_cast<const Tin*>(a.x);
   const Tin* rp = xin + row * a.ldx;
   float v[64];
-  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, v);
+  load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, row, v);
   const float sgn = rotate64<B>(v, lane);
   float mx = valid ? absmax64(v) : 0.f;
   mx = lane_max(mx, 6);
@@ -473,15 +533,16 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
 }
 
 // Workgroups of one rows pass (0 for an empty one).
+static bool rows2_multi(int64_t len) { return len > 4096 || 4096 % len != 0; }
 static int64_t rows2_grid(const FqArgs& a) {
   if (a.nvec == 0) return 0;
-  if (a.len > 4096) return a.nvec;
+  if (rows2_multi(a.len)) return a.nvec;
   const int64_t rpw = 4096 / a.len;
   const int64_t waves = (a.nvec + rpw - 1) / rpw;
   return (waves + 3) / 4;
 }
 
-template <typename Tin, int B, int QT, bool SR, bool ACT = false>
+template <typename Tin, int B, int QT, bool SR, int ACT = kDyPlain>
 static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
   const int64_t L = pp.p0.len;
   const int64_t g0 = rows2_grid(pp.p0), g1 = pp.has1 ? rows2_grid(pp.p1) : 0;
@@ -493,7 +554,7 @@ static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
   }
   // rows of up to 4096 elements: whole rows per wave in 4-wave workgroups (for 4096, this
   // beat one single-wave workgroup per row: 11.74 against 11.43 us per 4096^2 pass)
-  const int multi = L > 4096 ? 1 : 0;
+  const int multi = rows2_multi(L) ? 1 : 0;
   const int nw = multi ? (int)((L + 4095) / 4096) : 4;
   const int lds = QT != 3 && (multi || L == 4096) ? nw * kStageBytes : 0;
   if (lds > 65536) {
@@ -509,7 +570,10 @@ static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
 // columns kernel
 // ---------------------------------------------------------------------------
 
-constexpr int kColsLdsBytes = 16 * 512 * 16;  // 16 waves x 512 chunks of 16 bytes
+constexpr int kColsWaves = 16;                      // waves of a task
+constexpr int kColsThreads = 64 * kColsWaves;
+constexpr int kColsTile = 4096 * kColsWaves;         // values of a task
+constexpr int kColsLdsBytes = kColsWaves * 512 * 16;  // 512 chunks of 16 bytes a wave
 
 // LDS chunk (16-byte slot) of chunk j of `lane` in wave w: lane-major per wave, so the compute
 // reads are contiguous; the XOR on the low 4 lane bits spreads the transposing writes over all
@@ -538,10 +602,45 @@ struct ColsProb {
   uint32_t spins;  // polls of a waiting task before it stops waiting (see cols_task)
 };
 
+// The signs of the 8 rows from r0 on (bits 0 .. 7); none behind the rotated length, where the last
+// part of a column may reach.
+__device__ __forceinline__ uint32_t row_signs(const FqArgs& a, int64_t r0) {
+  return r0 < a.len ? a.signs[r0 >> 5] >> (r0 & 31) : 0u;
+}
+
+// 8 rows of 8 adjacent columns of x kept in 8 bits, as bf16 (exact): 8 bytes of codes and a power
+// per row; rows of the zero padding, at and past in_len, read row 0 instead.
+template <int QT>
+__device__ __forceinline__ void cols_kept_rows(const FqArgs& a, int64_t r0, int64_t col,
+                                               uint4 (&raw)[8]) {
+  const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.x) + col;
+  const int64_t groups = (a.ldx + kGroup - 1) / kGroup;
+  const uint8_t* powers = a.xw + col / kGroup;
+  uint2 q[8];
+  uint32_t s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t row = r0 + i < a.in_len ? r0 + i : 0;
+    q[i] = *reinterpret_cast<const uint2*>(codes + row * a.ldx);
+    s[i] = powers[row * groups];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float v[8];
+    kept8<QT>(q[i], s[i], v);
+    uint32_t h[4];  // the values' high halves: exact, they are bf16 numbers
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      h[e] = __builtin_amdgcn_perm(__float_as_uint(v[2 * e + 1]), __float_as_uint(v[2 * e]), 0x07060302u);
+    raw[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+}
+
 // Load part `part` (rows [part R, (part + 1) R)) of the column strip starting at column c0
 // into the LDS tile: each thread reads 8 rows of 8 adjacent columns (16 bytes per row),
-// transposes them in registers and writes 8 words of 8 rows of one column each.
-template <int B>
+// transposes them in registers and writes 8 words of 8 rows of one column each.  PK: x may be kept
+// in 8 bits (a.xk).
+template <int B, bool PK = false>
 __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int part, int t,
                                           uint4* lds) {
   using S = Slice<B>;
@@ -559,16 +658,23 @@ __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int pa
   // unconditional loads (a row of the zero padding, at and past in_len, reads row 0 instead);
   // only passes with padding then zero those rows
   const uint16_t* p0 = xin + (cvalid ? col : 0);
+  const bool padded = a.in_len < a.len || (int64_t)pr.P * R > a.len;
+  if (PK && a.xk == kKeptI8) {
+    cols_kept_rows<0>(a, r0, cvalid ? col : 0, raw);
+  } else if (PK && a.xk == kKeptE4M3) {
+    cols_kept_rows<1>(a, r0, cvalid ? col : 0, raw);
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    raw[i] = *reinterpret_cast<const uint4*>(r0 + i < a.in_len ? p + i * a.ldx : p0);
-  if (a.in_len < a.len) {
+    for (int i = 0; i < 8; ++i)
+      raw[i] = *reinterpret_cast<const uint4*>(r0 + i < a.in_len ? p + i * a.ldx : p0);
+  }
+  if (padded) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (r0 + i >= a.in_len) raw[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (a.signs) {  // the transform's signs: one bit per row, on the bf16 sign bits
-    const uint32_t b = a.signs[r0 >> 5] >> (r0 & 31);
+    const uint32_t b = row_signs(a, r0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t f = ((b >> i) & 1u) ? 0x80008000u : 0u;
@@ -626,9 +732,10 @@ __device__ __forceinline__ int lds_unit_f32(int w, int lane, int j, int half) {
 
 // Both rounds' loads of part `part` of the strip at column c0: in round h each thread reads 8
 // rows (row group f32_group(i, h)) of 4 adjacent columns, 16 bytes per row.
-template <int B>
+// SUM: the sums over the thread's rows are added to sum (before the signs).
+template <int B, bool SUM>
 __device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, int part, int t,
-                                              uint4 (&raw)[2][8]) {
+                                              float (&sum)[4], uint4 (&raw)[2][8]) {
   const FqArgs& a = pr.a;
   const int R = pr.R, CC = pr.C / 4;         // 16-byte (4-column) chunks per tile row
   const int cc = t % CC, i = t / CC;         // column chunk, row-group index of a round
@@ -643,13 +750,22 @@ __device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, in
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       raw[h][e] = *reinterpret_cast<const uint4*>(r0 + e < a.in_len ? p + e * a.ldx : p0);
-    if (a.in_len < a.len) {
+    if (a.in_len < a.len || (int64_t)pr.P * R > a.len) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (r0 + e >= a.in_len) raw[h][e] = make_uint4(0u, 0u, 0u, 0u);
     }
+    if constexpr (SUM) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sum[0] += __uint_as_float(raw[h][e].x);
+        sum[1] += __uint_as_float(raw[h][e].y);
+        sum[2] += __uint_as_float(raw[h][e].z);
+        sum[3] += __uint_as_float(raw[h][e].w);
+      }
+    }
     if (a.signs) {  // the transform's signs: one bit per row, on the fp32 sign bits
-      const uint32_t b = a.signs[r0 >> 5] >> (r0 & 31);
+      const uint32_t b = row_signs(a, r0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const uint32_t f = ((b >> e) & 1u) ? 0x80000000u : 0u;
@@ -671,32 +787,80 @@ __device__ __forceinline__ void cols_load_act(const ColsProb& pr, int64_t c0, in
   const int64_t col = c0 + cc * 4;
   const int64_t p0 = col < a.nvec ? col : 0;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+  const uint16_t* zin = reinterpret_cast<const uint16_t*>(a.z);
   const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int64_t at = p0 + (r0 + e < a.in_len ? (r0 + e) * a.ldx : 0);
     d[e] = *reinterpret_cast<const uint2*>(x + at);
-    z[e] = *reinterpret_cast<const uint2*>(a.z + at);
+    z[e] = *reinterpret_cast<const uint2*>(zin + at);
+  }
+}
+
+// The same for a z in any kept form: 4 columns of a row of z, as 8 bytes of bf16, or 4 codes and their
+// power.
+struct Z4 {
+  uint2 w;
+  __device__ __forceinline__ void load(const FqArgs& a, int64_t row, int64_t width, int64_t col) {
+    if (a.zk == kKeptPlain) {
+      w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.z) + row * width + col);
+    } else {
+      w.x = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(a.z) + row * width + col);
+      w.y = a.zw[row * ((width + kGroup - 1) / kGroup) + col / kGroup];
+    }
+  }
+};
+
+// The 4 values.
+__device__ __forceinline__ void z4_values(const uint2& z, int, float* o) {
+  o[0] = __uint_as_float(z.x << 16);
+  o[1] = __uint_as_float(z.x & 0xffff0000u);
+  o[2] = __uint_as_float(z.y << 16);
+  o[3] = __uint_as_float(z.y & 0xffff0000u);
+}
+__device__ __forceinline__ void z4_values(const Z4& z, int zk, float* o) {
+  if (zk == kKeptPlain) return z4_values(z.w, 0, o);
+  if (zk == kKeptI8) codes4<0>(z.w.x, o);
+  else codes4<1>(z.w.x, o);
+  const float p = power_of(z.w.y);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] *= p;
+}
+
+template <int B>
+__device__ __forceinline__ void cols_load_kept(const ColsProb& pr, int64_t c0, int part, int t, int h,
+                                               uint2 (&d)[8], Z4 (&z)[8]) {
+  const FqArgs& a = pr.a;
+  const int R = pr.R, CC = pr.C / 4;
+  const int cc = t % CC, i = t / CC;
+  const int64_t col = c0 + cc * 4 < a.nvec ? c0 + cc * 4 : 0;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(a.x);
+  const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t row = r0 + e < a.in_len ? r0 + e : 0;
+    d[e] = *reinterpret_cast<const uint2*>(x + row * a.ldx + col);
+    z[e].load(a, row, a.nvec, col);
   }
 }
 
 // One round's dz (8 rows of 4 columns), its sums over the rows added to sum, the transform's signs
-// last.
-template <int B>
+// last.  Z: uint2 (4 bf16) or Z4.
+template <int B, typename Z>
 __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, int h,
-                                         const uint2 (&d)[8], const uint2 (&z)[8], float (&sum)[4],
+                                         const uint2 (&d)[8], const Z (&z)[8], float (&sum)[4],
                                          uint4 (&raw)[8]) {
   const FqArgs& a = pr.a;
   const int i = t / (pr.C / 4);
   const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(i, h) * 8;
-  const uint32_t flip = a.signs ? a.signs[r0 >> 5] >> (r0 & 31) : 0u;
+  const uint32_t flip = a.signs ? row_signs(a, r0) : 0u;
   // a row at a time: few values live beside the tile's
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float v[4] = {__uint_as_float(d[e].x << 16), __uint_as_float(d[e].x & 0xffff0000u),
                   __uint_as_float(d[e].y << 16), __uint_as_float(d[e].y & 0xffff0000u)};
-    const float zv[4] = {__uint_as_float(z[e].x << 16), __uint_as_float(z[e].x & 0xffff0000u),
-                         __uint_as_float(z[e].y << 16), __uint_as_float(z[e].y & 0xffff0000u)};
+    float zv[4];
+    z4_values(z[e], a.zk, zv);
     slope_mul<4>(a.act, zv, v);
     const bool in = r0 + e < a.in_len;  // rows of the zero padding
     const uint32_t f = ((flip >> e) & 1u) ? 0x80000000u : 0u;
@@ -715,7 +879,7 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
 // then the waves in order, into row `part` of db_part or db itself.
 __device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
                                         float (&sum)[4]) {
-  __shared__ float s_db[16][256];
+  __shared__ float s_db[kColsWaves][256];
   const FqArgs& a = pr.a;
   const int CC = pr.C / 4, lane = t & 63, w = t >> 6;
 #pragma unroll
@@ -737,7 +901,7 @@ __device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part
   const int same = CC <= 64 ? 1 : CC / 64;
   if (t < pr.C && c0 + t < a.nvec) {
     float v = 0.f;
-    for (int i = t / 256; i < 16; i += same) v += s_db[i][t & 255];
+    for (int i = t / 256; i < kColsWaves; i += same) v += s_db[i][t & 255];
     if (a.db) a.db[c0 + t] = (uint16_t)bf16x2_of(v, 0.f);
     else if (a.db_part) a.db_part[(int64_t)part * a.nvec + c0 + t] = v;
   }
@@ -773,8 +937,9 @@ __device__ __forceinline__ void cols_stage_f32(const ColsProb& pr, int t, int h,
 // REPAIR: the second launch of an exchanging pass (see below): only the tasks of strips marked
 // late run, with the column maxima complete by then.
 // F32: fp32 input (two LDS rounds, see cols_load_f32); else bf16.
-// ACT: the activation-gradient pass (see cols_load_act; F32 with it).
-template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false, bool ACT = false>
+// ACT: the activation-gradient pass (see cols_load_act; F32 with it).  PK: see cols_load.
+template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false, int ACT = kDyPlain,
+          bool PK = false>
 __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uint4* lds) {
   using S = Slice<B>;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -820,18 +985,24 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   // ---- load R rows x C columns, transposed into LDS, into the wave's slices ---------------
   float v[64];
   if constexpr (F32) {
-    uint4 raw[ACT ? 1 : 2][8];
-    uint2 ad[8], az[8];
+    constexpr bool kForm = ACT == kDyAct || ACT == kDyKept;  // dz is formed here
+    uint4 raw[kForm ? 1 : 2][8];
+    uint2 ad[8];
+    typename std::conditional<ACT == kDyKept, Z4, uint2>::type az[8];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (ACT) cols_load_act<B>(pr, c0, part, t, 0, ad, az);
-    else cols_load_f32<B>(pr, c0, part, t, raw);
+    if constexpr (ACT == kDyKept) cols_load_kept<B>(pr, c0, part, t, 0, ad, az);
+    else if constexpr (ACT == kDyAct) cols_load_act<B>(pr, c0, part, t, 0, ad, az);
+    else cols_load_f32<B, ACT == kDyStored>(pr, c0, part, t, sum, raw);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if constexpr (ACT) {
+      if constexpr (ACT == kDyKept) {
+        cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
+        if (h == 0) cols_load_kept<B>(pr, c0, part, t, 1, ad, az);
+      } else if constexpr (ACT == kDyAct) {
         cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
         if (h == 0) cols_load_act<B>(pr, c0, part, t, 1, ad, az);
       }
-      cols_stage_f32<B>(pr, t, h, raw[ACT ? 0 : h], lds);
+      cols_stage_f32<B>(pr, t, h, raw[kForm ? 0 : h], lds);
       __syncthreads();
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
@@ -845,9 +1016,9 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       }
       if (h == 0) __syncthreads();  // round 1 overwrites the LDS tile
     }
-    if constexpr (ACT && !REPAIR) cols_db(pr, c0, part, t, sum);
+    if constexpr (ACT != kDyPlain && !REPAIR) cols_db(pr, c0, part, t, sum);
   } else {
-    cols_load<B>(pr, c0, part, t, lds);
+    cols_load<B, PK>(pr, c0, part, t, lds);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 8; ++j) unpack_bf16x8(lds[lds_slot<B>(w, lane, j)], &v[j * 8]);
@@ -869,7 +1040,7 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   // task in and waits for all P; one thread per column reads the final maximum back with an
   // atomic load and shares it through LDS.  No cache-wide fence is needed.
   if (P > 1) {
-    __shared__ float s_cmax[1024];
+    __shared__ float s_cmax[kColsThreads];
     uint32_t* cm = reinterpret_cast<uint32_t*>(colmax);
     if constexpr (!REPAIR) {
       __shared__ uint32_t s_late;
@@ -920,7 +1091,8 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   if (valid) {
     if (part == 0 && writer) a.scale[col] = stored_scale<QT>(a, mx);
     const float mul = quant_mul_v<QT>(a, mx, v) * sgn;
-    store_slice<B, QT, SR>(a, v, mul, col * a.ldq + pos0, lane, col, pos0);
+    if (pos0 + S::off(lane, 0) < a.len)  // the last part may reach past the column's end
+      store_slice<B, QT, SR, true>(a, v, mul, col * a.ldq + pos0, lane, col, pos0);
   }
 }
 
@@ -942,7 +1114,7 @@ __device__ __forceinline__ bool any_late(const uint32_t* a, const uint32_t* b, c
 }
 
 template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false>
-__global__ __launch_bounds__(1024) void fq_cols2_kernel(ColsProb c0, ColsProb c1, int64_t split,
+__global__ __launch_bounds__(kColsThreads) void fq_cols2_kernel(ColsProb c0, ColsProb c1, int64_t split,
                                                         int64_t tasks) {
   extern __shared__ __attribute__((aligned(16))) uint4 lds[];
   if constexpr (REPAIR) {
@@ -969,9 +1141,9 @@ struct FqBatch {
 
 // SR: stochastic rounding of the dY codes (the W and X codes are rounded to nearest).
 // REPAIR: the follow-up launch of the column passes (rows tasks excluded from its grid).
-// ACT: dY's passes take dz = dy act'(z).
-template <int B, int QG, int QW, bool SR, bool REPAIR = false, bool ACT = false>
-__global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
+// ACT: what dY's passes take (a DyForm).  PK: x may be kept in 8 bits.
+template <int B, int QG, int QW, bool SR, bool REPAIR = false, int ACT = kDyPlain, bool PK = false>
+__global__ __launch_bounds__(kColsThreads) void fq_batch_kernel(FqBatch fb) {
   extern __shared__ __attribute__((aligned(16))) uint4 lds[];
   if constexpr (REPAIR) {
     // a grid of at most one workgroup per compute unit, striding over the column tasks
@@ -983,11 +1155,11 @@ __global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
       __syncthreads();  // the next task overwrites the LDS tile
     }
     for (int64_t t = blockIdx.x; t < fb.end_dy - fb.end_w; t += gridDim.x) {
-      cols_task<B, QG, SR, true, ACT, ACT>(fb.cdy, t, lds);
+      cols_task<B, QG, SR, true, ACT != kDyPlain, ACT>(fb.cdy, t, lds);
       __syncthreads();
     }
     for (int64_t t = blockIdx.x; t < fb.end_x - fb.end_dy; t += gridDim.x) {
-      cols_task<B, QW, false, true>(fb.cx, t, lds);
+      cols_task<B, QW, false, true, false, kDyPlain, PK>(fb.cx, t, lds);
       __syncthreads();
     }
     return;
@@ -996,30 +1168,30 @@ __global__ __launch_bounds__(1024) void fq_batch_kernel(FqBatch fb) {
   if (bid < fb.end_w) {
     cols_task<B, QW, false>(fb.cw, bid, lds);
   } else if (bid < fb.end_dy) {
-    cols_task<B, QG, SR, false, ACT, ACT>(fb.cdy, bid - fb.end_w, lds);
+    cols_task<B, QG, SR, false, ACT != kDyPlain, ACT>(fb.cdy, bid - fb.end_w, lds);
   } else if (bid < fb.end_x) {
-    cols_task<B, QW, false>(fb.cx, bid - fb.end_dy, lds);
+    cols_task<B, QW, false, false, false, kDyPlain, PK>(fb.cx, bid - fb.end_dy, lds);
   } else {
-    rows_wave<uint16_t, B, QG, SR, ACT>(fb.rows, (bid - fb.end_x) * 16 + (threadIdx.x >> 6),
+    rows_wave<uint16_t, B, QG, SR, ACT == kDyStored ? kDyPlain : ACT>(fb.rows, (bid - fb.end_x) * kColsWaves + (threadIdx.x >> 6),
                                    threadIdx.x & 63);
   }
 }
 
-// Rows per task for a column of `rows` elements (a power of two in [64, 4096] dividing rows
-// and divisible by the block; 0 when the shape is not covered).  Columns of up to 4096 rows go
-// whole into one task (4096 x 16 columns, or a wider tile for shorter columns): no exchange of
-// partial maxima at all, and the strips' XCD-aware order keeps their 32-byte row segments
-// fetched once per 128-byte line.  Longer columns take 1024-row tasks (64-column strips, full
-// 128-byte row segments) and exchange their partial maxima.
+// Rows per task for a column of `rows` elements (a power of two in [64, 4096], at least the block;
+// 0 when the shape is not covered).  Columns of up to 4096 rows go whole into one task (4096 x 16
+// columns, or a wider tile for shorter columns): no exchange of partial maxima at all, and the
+// strips' XCD-aware order keeps their 32-byte row segments fetched once per 128-byte line.  Longer
+// columns take 1024-row tasks (64-column strips, full 128-byte row segments) and exchange their
+// partial maxima.  Lengths that the tasks do not divide leave part of the last one idle: smaller
+// tasks that divide them exchange among more parts (11008 x 4096 bf16, 43 parts of 256: 77.8 us).
 static int cols2_rows_per_task(int64_t rows, int block) {
-  int R = rows <= 4096 ? 4096 : 1024;
-  if (block > R) R = block;
-  while (R > rows) R >>= 1;
-  while (R >= 64 && rows % R != 0) R >>= 1;
-  if (R < 64 || R > 4096 || (R & (R - 1)) != 0) return 0;
-  if (rows % R != 0 || R % block != 0) return 0;
-  return R;
+  if (rows < 64 || block > 4096) return 0;
+  int R = 64;
+  while (R < rows && R < 4096) R *= 2;
+  if (rows > 4096) R = 1024;
+  return R > block ? R : block;
 }
+static int64_t cols2_parts(int64_t rows, int R) { return (rows + R - 1) / R; }
 
 // Workgroups that can be resident at once (one per compute unit: the tile takes 128 KB of
 // LDS), queried once per device.  Every kernel asking has the same 1024-thread, 128 KB LDS
@@ -1034,7 +1206,7 @@ static int cols2_capacity(const void* fn) {
   int cus = 0, per_cu = 0;
   if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
     return 0;
-  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, 1024, kColsLdsBytes) != hipSuccess)
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, kColsThreads, kColsLdsBytes) != hipSuccess)
     return 0;
   cap[dev].store(cus * per_cu, std::memory_order_relaxed);
   return cus * per_cu;
@@ -1064,8 +1236,8 @@ static ColsProb cols2_prob(const FqArgs& a, void* ws, int64_t* tasks, int64_t* s
   ColsProb pr{};
   pr.a = a;
   pr.R = cols2_rows_per_task(a.len, a.block);
-  pr.P = (int)(a.len / pr.R);
-  pr.C = 65536 / pr.R;
+  pr.P = (int)cols2_parts(a.len, pr.R);
+  pr.C = kColsTile / pr.R;
   pr.gs = 1;
   const int64_t strips = (a.nvec + pr.C - 1) / pr.C;
   *tasks = (a.nvec == 0 || a.len == 0) ? 0 : strips * pr.P;
@@ -1110,7 +1282,7 @@ static hipError_t launch_cols2_t(const FqArgs& a0, void* ws0, const FqArgs* a1, 
     if (cap < P) return hipErrorInvalidConfiguration;
     p0.gs = p1.gs = cols2_group(P, cap);
   }
-  hipLaunchKernelGGL((fq_cols2_kernel<B, QT, SR, false, F32>), dim3((unsigned)tasks), dim3(1024),
+  hipLaunchKernelGGL((fq_cols2_kernel<B, QT, SR, false, F32>), dim3((unsigned)tasks), dim3(kColsThreads),
                      kColsLdsBytes, st, p0, p1, t0, tasks);
   e = hipGetLastError();
   if (e != hipSuccess || P == 1) return e;
@@ -1121,7 +1293,7 @@ static hipError_t launch_cols2_t(const FqArgs& a0, void* ws0, const FqArgs* a1, 
   if (e != hipSuccess) return e;
   const int cap = cols2_capacity(reinterpret_cast<const void*>(fn));
   const int64_t rgrid = tasks < cap ? tasks : cap;
-  hipLaunchKernelGGL((fq_cols2_kernel<B, QT, SR, true, F32>), dim3((unsigned)rgrid), dim3(1024),
+  hipLaunchKernelGGL((fq_cols2_kernel<B, QT, SR, true, F32>), dim3((unsigned)rgrid), dim3(kColsThreads),
                      kColsLdsBytes, st, p0, p1, t0, tasks);
   return hipGetLastError();
 }
@@ -1144,19 +1316,19 @@ static hipError_t cols2_block(const FqArgs& a0, void* ws0, const FqArgs* a1, voi
 // backward batch
 // ---------------------------------------------------------------------------
 
-template <int B, int QG, int QW, bool SR, bool ACT = false>
+template <int B, int QG, int QW, bool SR, int ACT = kDyPlain, bool PK = false>
 static hipError_t launch_batch_t(const FqArgs* rows, const FqArgs& cw, void* ws_w,
                                  const FqArgs& cdy, void* ws_dy, const FqArgs& cx, void* ws_x,
                                  hipStream_t st) {
-  auto* fn = &fq_batch_kernel<B, QG, QW, SR, false, ACT>;
-  hipError_t e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, false, ACT>>(kColsLdsBytes);
+  auto* fn = &fq_batch_kernel<B, QG, QW, SR, false, ACT, PK>;
+  hipError_t e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, false, ACT, PK>>(kColsLdsBytes);
   if (e != hipSuccess) return e;
   FqBatch fb{};
   int64_t tw = 0, tdy = 0, tx = 0, scratch = 0;
   if (rows) {
     fb.rows = *rows;
     const int64_t waves = (rows->nvec * rows->len + 4095) / 4096;
-    fb.rows_wg = rows->nvec == 0 ? 0 : (waves + 15) / 16;
+    fb.rows_wg = rows->nvec == 0 ? 0 : (waves + kColsWaves - 1) / kColsWaves;
   }
   fb.cw = cols2_prob(cw, ws_w, &tw, &scratch);
   fb.cdy = cols2_prob(cdy, ws_dy, &tdy, &scratch);
@@ -1176,17 +1348,17 @@ static hipError_t launch_batch_t(const FqArgs* rows, const FqArgs& cw, void* ws_
     fb.cdy.gs = cols2_group(fb.cdy.P, cap);
     fb.cx.gs = cols2_group(fb.cx.P, cap);
   }
-  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, false, ACT>), dim3((unsigned)grid), dim3(1024),
+  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, false, ACT, PK>), dim3((unsigned)grid), dim3(kColsThreads),
                      kColsLdsBytes, st, fb);
   e = hipGetLastError();
   if (e != hipSuccess || P == 1) return e;
   // the repair launch over the column tasks (see launch_cols2_t)
-  e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, true, ACT>>(kColsLdsBytes);
+  e = allow_dynamic_lds<&fq_batch_kernel<B, QG, QW, SR, true, ACT, PK>>(kColsLdsBytes);
   if (e != hipSuccess) return e;
   const int cap = cols2_capacity(reinterpret_cast<const void*>(fn));
   const int64_t rgrid = fb.end_x < cap ? fb.end_x : cap;
-  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, true, ACT>), dim3((unsigned)rgrid),
-                     dim3(1024), kColsLdsBytes, st, fb);
+  hipLaunchKernelGGL((fq_batch_kernel<B, QG, QW, SR, true, ACT, PK>), dim3((unsigned)rgrid),
+                     dim3(kColsThreads), kColsLdsBytes, st, fb);
   return hipGetLastError();
 }
 

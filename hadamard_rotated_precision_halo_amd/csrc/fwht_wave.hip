@@ -7,16 +7,15 @@ namespace halo {
 
 bool fq_rows2_supported(int64_t len, int block) {
   if (len <= 0 || len % 64 != 0 || len > 16 * 4096) return false;
-  if (len < 4096 && 4096 % len != 0) return false;
   return block >= 1 && block <= 4096 && len % block == 0;
 }
 
 size_t fq_cols2_ws_bytes(int64_t rows, int64_t cols, int block) {
   const int R = cols2_rows_per_task(rows, block);
   if (R == 0) return 0;
-  const int64_t P = rows / R;
+  const int64_t P = cols2_parts(rows, R);
   if (P <= 1) return 0;
-  const int64_t C = 65536 / R;
+  const int64_t C = kColsTile / R;
   const int64_t strips = (cols + C - 1) / C;
   const size_t cnt = ((size_t)strips * 4 + 255) & ~(size_t)255;
   return kColsLateBytes + cnt + (size_t)cols * 4;
@@ -28,11 +27,12 @@ bool fq_cols2_supported(int64_t rows, int64_t cols, int block, int in_bf16, bool
   if ((!in_bf16 && sr) || rows <= 0 || cols <= 0) return false;
   const int R = cols2_rows_per_task(rows, block);
   if (R == 0) return false;
-  if (rows / R == 1) return true;
+  const int64_t P = cols2_parts(rows, R);
+  if (P == 1) return true;
   // the parts of a strip wait for each other, so all of them must fit on the device at once;
   // longer columns take the two-sweep kernel, which never waits
   const int cap = cols2_capacity(reinterpret_cast<const void*>(&fq_cols2_kernel<256, 0, false>));
-  return rows / R <= cap && ws_bytes >= fq_cols2_ws_bytes(rows, cols, block);
+  return P <= cap && ws_bytes >= fq_cols2_ws_bytes(rows, cols, block);
 }
 
 bool fq_batch_rows_ok(int64_t len) { return len >= 64 && len <= 4096 && 4096 % len == 0; }

@@ -10,7 +10,7 @@ bool fq_act_block_ok(int block) { return block >= 64 && block <= 1024; }
 
 int64_t fq_act_parts(int64_t rows, int block) {
   const int R = cols2_rows_per_task(rows, block);
-  return R == 0 ? 0 : rows / R;
+  return R == 0 ? 0 : cols2_parts(rows, R);
 }
 
 namespace {
@@ -19,7 +19,7 @@ template <int QG, int QW>
 hipError_t batch_act(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
                      void* ws_dy, const FqArgs& cx, void* ws_x, hipStream_t st) {
 #define HALO_A_CASE(BB) \
-  case BB: return launch_batch_t<BB, QG, QW, false, true>(rows, cw, ws_w, cdy, ws_dy, cx, ws_x, st);
+  case BB: return launch_batch_t<BB, QG, QW, false, kDyAct>(rows, cw, ws_w, cdy, ws_dy, cx, ws_x, st);
   switch (cw.block) {
     HALO_A_CASE(64) HALO_A_CASE(128) HALO_A_CASE(256) HALO_A_CASE(512) HALO_A_CASE(1024)
     default: return hipErrorInvalidValue;
@@ -30,7 +30,7 @@ hipError_t batch_act(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqA
 template <int QT>
 hipError_t rows_act(const FqPair& a, hipStream_t st) {
 #define HALO_A_CASE(BB) \
-  case BB: return launch_rows2_t<uint16_t, BB, QT, false, true>(a, st);
+  case BB: return launch_rows2_t<uint16_t, BB, QT, false, kDyAct>(a, st);
   switch (a.p0.block) {
     HALO_A_CASE(64) HALO_A_CASE(128) HALO_A_CASE(256) HALO_A_CASE(512) HALO_A_CASE(1024)
     default: return hipErrorInvalidValue;

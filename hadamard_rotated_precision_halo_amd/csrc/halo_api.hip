@@ -460,6 +460,12 @@ struct ActGrad {
   int act = 0;
   void* db = nullptr;    // bf16 [n] or NULL
   float* part = nullptr; // scratch of its partial sums
+  // from kept activations: the forms of z and x; dz: dY's passes take dz, else dY as it is; glu: dY's
+  // rows are the gated layer's (of n / 2 columns each half), dz is stored here
+  bool kept = false, dz = true;
+  int zk = kKeptPlain, xk = kKeptPlain;
+  const uint8_t *zw = nullptr, *xw = nullptr;
+  float* glu = nullptr;
 };
 
 // Whether the backward forms dz = dy act'(z) inside its rotation passes: the one-launch batch of
@@ -474,6 +480,17 @@ bool act_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t b
          fq_cols2_supported(mq, n, block, 1, false, p.scr_dy) &&
          fq_cols2_supported(mq, k, block, 1, false, p.scr_x) &&
          act_grad_parts(m, n) >= (fq_act_parts(mq, block) > 1 ? fq_act_parts(mq, block) : 1);
+}
+
+// The same for the passes from kept activations and the gated layer's (n: columns of dz).
+bool kept_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block, bool glu,
+                   bool dx, bool dw, bool stochastic) {
+  const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
+  const WsPlan p = plan_ws(m, n, k, 1, block);
+  return dx && dw && io_type == HALO_BF16 && fq_act_block_ok(block) && !stochastic &&
+         (glu ? glu_rows_ok(n / 2, block) : fq_rows2_supported(nq, block)) && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
+         fq_cols2_supported(mq, n, block, 1, false, p.scr_dy) &&
+         fq_cols2_supported(mq, k, block, 1, false, p.scr_x);
 }
 
 // Workspace of a layer backward with its activation: the layer's, then a stored dz (where the
@@ -536,12 +553,20 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
   // dX = dY W: rows of dY and columns of W along n; dW = dY^T X: columns of dY and X along m
   FqArgs rows = make_fq(dy, m, n, n, HALO_ALONG_ROWS, block, grad_q_type, qdy, nq, sdy, gn, nq);
   const FqArgs cw = make_fq(w, n, k, k, HALO_ALONG_COLS, block, q_type, qwt, nq, swt, on, nq);
-  FqArgs cdy = make_fq(dy, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
-  const FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
+  const void* dy_cols = act && act->glu ? act->glu : dy;
+  FqArgs cdy = make_fq(dy_cols, m, n, n, HALO_ALONG_COLS, block, grad_q_type, qdyt, mq, sdyt, gm, mq);
+  FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
 
-  const int64_t db_parts = act ? fq_act_parts(mq, block) : 0;
-  if (act) {
-    rows.z = cdy.z = static_cast<const uint16_t*>(act->z);
+  const bool has_dz = act && act->dz;
+  const int64_t db_parts = has_dz ? fq_act_parts(mq, block) : 0;
+  if (act && act->kept) {
+    rows.zk = cdy.zk = act->zk;
+    rows.zw = cdy.zw = act->zw;
+    cx.xk = act->xk;
+    cx.xw = act->xw;
+  }
+  if (has_dz) {
+    rows.z = cdy.z = act->z;
     rows.act = cdy.act = act->act;
     if (act->db && db_parts == 1) cdy.db = static_cast<uint16_t*>(act->db);
     if (act->db && db_parts > 1) cdy.db_part = act->part;
@@ -567,6 +592,31 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
   // the rows pass of dY, clearing the scratch as a side job when it runs as the wave kernel
   auto rows_pass = [&]() {
     if (s != HALO_OK) return;
+    if (act && act->glu) {
+      GluRowsArgs g{};
+      g.dy = static_cast<const uint16_t*>(dy);
+      g.z = act->z;
+      g.zw = act->zw;
+      g.zk = act->zk;
+      g.act = act->act;
+      g.rows = m;
+      g.n = n / 2;
+      g.dz = act->glu;
+      g.q = static_cast<uint8_t*>(qdy);
+      g.nq = nq;
+      g.scale = sdy;
+      g.block = block;
+      g.qmax = rows.qmax;
+      g.denom = rows.denom;
+      g.signs = rows.signs;
+      if (zero_pending) {
+        g.zero = reinterpret_cast<uint32_t*>(scr);
+        g.nzero = (int64_t)(p.scratch_bytes / 4);
+        zero_pending = false;
+      }
+      s = from_hip(launch_glu_rows(g, qt_index(grad_q_type), st));
+      return;
+    }
     if (fq_rows2_supported(nq, block) && (inb_dy || !rows.sr)) {
       FqPair pp{};
       pp.p0 = rows;
@@ -575,8 +625,9 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
         pp.nzero = (int64_t)(p.scratch_bytes / 4);
         zero_pending = false;
       }
-      s = from_hip(act ? launch_fq_rows2_act(pp, qt_index(grad_q_type), st)
-                       : launch_fq_rows2_pair(pp, inb_dy, qt_index(grad_q_type), st));
+      s = from_hip(!has_dz      ? launch_fq_rows2_pair(pp, inb_dy, qt_index(grad_q_type), st)
+                   : act->kept ? launch_fq_rows2_kept(pp, qt_index(grad_q_type), st)
+                               : launch_fq_rows2_act(pp, qt_index(grad_q_type), st));
     } else {
       s = run_fa(rows, dy_type, HALO_ALONG_ROWS, grad_q_type, nullptr, 0, st);
     }
@@ -588,16 +639,20 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
       fq_cols2_supported(mq, k, block, 1, false, p.scr_x)) {
     // every rotation pass of the backward in one launch (or two, when the dY rows are long):
     // the passes overlap on the device, then the two products
-    const bool rows_in = fq_batch_rows_ok(nq);
+    const bool rows_in = fq_batch_rows_ok(nq) && !(act && act->glu);
     if (rows_in) {
       clear_scratch();
     } else {
       rows_pass();
       clear_scratch();
     }
-    if (s == HALO_OK)
-      s = from_hip((act ? launch_fq_batch_act : launch_fq_batch)(
-          rows_in ? &rows : nullptr, cw, scr_w, cdy, scr_dy, cx, scr_x, qg, qw, st));
+    const FqArgs* in = rows_in ? &rows : nullptr;
+    if (s == HALO_OK && act && act->kept)
+      s = from_hip(launch_fq_batch_kept(in, cw, scr_w, cdy, scr_dy, cx, scr_x, qg, qw,
+                                        act->glu ? kDyStored : has_dz ? kDyKept : kDyPlain, st));
+    else if (s == HALO_OK)
+      s = from_hip((act ? launch_fq_batch_act : launch_fq_batch)(in, cw, scr_w, cdy, scr_dy, cx, scr_x,
+                                                                 qg, qw, st));
     if (s == HALO_OK && cdy.db_part)
       s = from_hip(launch_part_sum(cdy.db_part, db_parts, n, static_cast<uint16_t*>(act->db), st));
   } else {
@@ -1257,17 +1312,23 @@ void glu_ep(Ep& e, const void* bias, halo_activation activation) {
 // Workspace of a layer backward from kept activations: the layer's (of nz output features), the
 // stored dz, the bias gradient's partial rows and x read back, where the call has them.
 struct KeptBwdWs {
+  bool fused;                 // dz is formed (the gated layer's: and stored), and x read, inside the
+                              // rotation passes
   size_t dz, part, x, total;  // byte offsets, and the whole
 };
 
 KeptBwdWs kept_bwd_ws(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block, bool glu,
-                      bool act, halo_dtype x_type, bool dw, bool db) {
+                      bool act, halo_dtype x_type, bool dx, bool dw, bool db, bool stochastic) {
   const int64_t nz = glu ? 2 * n : n;
   KeptBwdWs w{};
+  w.fused = kept_fused_ok(io_type, m, nz, k, block, glu, dx, dw, stochastic);
   w.dz = plan_ws(m, nz, k, 1, block).total;
-  w.part = w.dz + (act || glu ? round256((size_t)m * nz * 4) : 0);
-  w.x = w.part + (db ? round256((size_t)act_grad_parts(m, n) * nz * 4) : 0);
-  w.total = w.x + (dw && kept_form(x_type) != kKeptPlain ? round256((size_t)m * k * esize(io_type)) : 0);
+  w.part = w.dz + (glu || (act && !w.fused) ? round256((size_t)m * nz * 4) : 0);
+  const int64_t parts = w.fused && (act || glu) ? fq_act_parts(contraction_len(m, block), block)
+                                                : act_grad_parts(m, n);
+  w.x = w.part + (db ? round256((size_t)parts * nz * 4) : 0);
+  w.total = w.x + (dw && !w.fused && kept_form(x_type) != kKeptPlain
+                       ? round256((size_t)m * k * esize(io_type)) : 0);
   return w;
 }
 
@@ -1284,7 +1345,8 @@ size_t kept_bwd_ws_bytes(int64_t m, int64_t n, int64_t k, int32_t block, const h
       halo_linear_workspace_bytes_ex(m, glu ? 2 * n : n, k, block, q_type, 1) == 0)
     return 0;
   return kept_bwd_ws(io_type, m, n, k, block, glu, activation != HALO_ACT_NONE, x_type,
-                     gradients & HALO_GRAD_DW, gradients & HALO_GRAD_DB)
+                     gradients & HALO_GRAD_DX, gradients & HALO_GRAD_DW, gradients & HALO_GRAD_DB,
+                     rounding == HALO_ROUND_STOCHASTIC)
       .total;
 }
 
@@ -1306,7 +1368,8 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
   if (s == HALO_OK && has_dz) s = check_kept(z, io_type);
   if (s != HALO_OK) return s;
   if (!aligned16(db)) return HALO_ERR_ALIGN;
-  const KeptBwdWs wl = kept_bwd_ws(io_type, m, n, k, block, glu, act, x->type, dw, db);
+  const KeptBwdWs wl = kept_bwd_ws(io_type, m, n, k, block, glu, act, x->type, dx, dw, db,
+                                   opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC);
   if (!ws || ws_bytes < wl.total) return HALO_ERR_WORKSPACE;
   if (!aligned16(ws)) return HALO_ERR_ALIGN;
   const int inb = io_type == HALO_BF16 ? 1 : 0;
@@ -1314,6 +1377,27 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
   float* dz = reinterpret_cast<float*>(base + wl.dz);
   float* part = reinterpret_cast<float*>(base + wl.part);
   hipError_t e = hipSuccess;
+  if (wl.fused) {
+    ActGrad ag;
+    ag.kept = true;
+    ag.dz = has_dz;
+    ag.xk = kept_form(x->type);
+    ag.xw = x->powers;
+    if (has_dz) {
+      ag.z = z->data;
+      ag.zk = kept_form(z->type);
+      ag.zw = z->powers;
+      ag.act = (int)activation;
+      ag.glu = glu ? dz : nullptr;
+      ag.db = db;
+      ag.part = part;
+    } else if (db && launch_act_grad(dy, nullptr, (int)HALO_ACT_NONE, inb, m, n, nullptr, db, part,
+                                     st) != hipSuccess) {
+      return HALO_ERR_HIP;
+    }
+    return run_bwd(dy, io_type, x->data, w, io_type, m, nz, k, block, q_type, grad_q_type, dx, dw, opts,
+                   ws, st, &ag);
+  }
   if (has_dz) {
     const DzArgs a{dy, z->data, z->powers, kept_form(z->type), (int)activation, glu ? 1 : 0, m, n, dz,
                    db, part};

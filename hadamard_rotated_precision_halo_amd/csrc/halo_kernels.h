@@ -34,10 +34,17 @@ struct FqArgs {
   // are those of dz = dy act'(z), z [rows x cols] with x's leading dimension (bf16); db_part: the
   // columns pass's sums of dz over each task's rows, [parts x nvec] fp32, or, where a task holds
   // whole columns and db is not NULL, db [nvec] bf16 itself
-  const uint16_t* z;
+  const void* z;
   int act;
   float* db_part;
   uint16_t* db;
+  // the general form of these passes (launch_fq_*_kept): z's form (zk: a Kept of checkpoint.h) and
+  // its powers
+  int zk;
+  const uint8_t* zw;
+  // x itself kept in 8 bits (columns passes of launch_fq_batch_kept): its form and powers
+  int xk;
+  const uint8_t* xw;
 };
 
 // in_bf16: 1 for bf16 input, 0 for fp32.  qt: 0 INT8, 1 E4M3, 2 E5M2, 3 fp32 values.
@@ -54,6 +61,10 @@ size_t fq_cols2_ws_bytes(int64_t rows, int64_t cols, int block);
 bool fq_cols2_supported(int64_t rows, int64_t cols, int block, int in_bf16, bool sr,
                         size_t ws_bytes);
 hipError_t launch_fq_cols2(const FqArgs& a, int in_bf16, int qt, void* ws, hipStream_t st);
+
+// What a layer backward's dY passes take: dY as it is, dz = dY act'(z) of a bf16 z or of a z in any
+// kept form, or a dz that is stored in fp32 (columns passes, which then sum it over the rows too).
+enum DyForm { kDyPlain = 0, kDyAct = 1, kDyKept = 2, kDyStored = 3 };
 
 // The rotation passes of a layer backward in one launch (bf16 input): the rows of dY (codes
 // qg; may be NULL, else fq_batch_rows_ok(len) must hold) and the single-read column passes of
@@ -72,6 +83,34 @@ int64_t fq_act_parts(int64_t rows, int block);
 hipError_t launch_fq_batch_act(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
                                void* ws_dy, const FqArgs& cx, void* ws_x, int qg, int qw,
                                hipStream_t st);
+
+// The same from kept activations: x (cx.xk) and z (zk) in any form; form: what dY's passes take (a
+// DyForm; a stored dz is fp32, and its rows are another pass's).
+hipError_t launch_fq_batch_kept(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
+                                void* ws_dy, const FqArgs& cx, void* ws_x, int qg, int qw, int form,
+                                hipStream_t st);
+
+// The rows pass of the gated layer's gradient (glu_rows.hip): dz = [dy u act'(g), dy act(g)] formed in
+// fp32, stored, rotated and quantised in one pass.  dy [rows x n] and z [2 rows x n] (any kept form);
+// n as glu_rows_ok; nearest rounding.
+struct GluRowsArgs {
+  const uint16_t* dy;
+  const void* z;
+  const uint8_t* zw;
+  int zk, act;
+  int64_t rows, n;
+  float* dz;             // [rows x 2 n]
+  uint8_t* q;            // codes [rows x nq], nq = 2 n padded to a multiple of the block
+  int64_t nq;
+  float* scale;          // [rows]
+  int block;
+  float qmax, denom;     // as FqArgs
+  const uint32_t* signs; // along 2 n, or NULL
+  uint32_t* zero;        // words to clear beside the pass (may be NULL)
+  int64_t nzero;
+};
+bool glu_rows_ok(int64_t n, int block);
+hipError_t launch_glu_rows(const GluRowsArgs& a, int qt, hipStream_t st);
 
 // Both passes of one bf16 matrix from a single read (fwht_dual.hip): the rows pass ar and
 // the columns pass ac of the same x (same block and code type qt), with one scratch whose
@@ -102,6 +141,7 @@ struct FqPair {
 };
 hipError_t launch_fq_rows2_pair(const FqPair& a, int in_bf16, int qt, hipStream_t st);
 hipError_t launch_fq_rows2_act(const FqPair& a, int qt, hipStream_t st);
+hipError_t launch_fq_rows2_kept(const FqPair& a, int qt, hipStream_t st);
 
 // Up to two single-read column passes over columns of the same length, block, input type
 // (in_bf16) and code type in one launch (a1 may be NULL).  prezeroed: the scratch of both was
