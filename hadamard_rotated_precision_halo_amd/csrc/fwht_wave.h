@@ -730,47 +730,52 @@ __device__ __forceinline__ int lds_unit_f32(int w, int lane, int j, int half) {
   return w * 512 + (j & 3) * 128 + half * 64 + (lane ^ (((j * JA) ^ w) & 15));
 }
 
-// Both rounds' loads of part `part` of the strip at column c0: in round h each thread reads 8
-// rows (row group f32_group(i, h)) of 4 adjacent columns, 16 bytes per row.
-// SUM: the sums over the thread's rows are added to sum (before the signs).
-template <int B, bool SUM>
-__device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, int part, int t,
-                                              float (&sum)[4], uint4 (&raw)[2][8]) {
+// Loads of round h of part `part` of the strip at column c0: each thread reads 8 rows (row group
+// f32_group(i, h)) of 4 adjacent columns, 16 bytes per row.
+template <int B>
+__device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, int part, int t, int h,
+                                              uint4 (&raw)[8]) {
   const FqArgs& a = pr.a;
   const int R = pr.R, CC = pr.C / 4;         // 16-byte (4-column) chunks per tile row
   const int cc = t % CC, i = t / CC;         // column chunk, row-group index of a round
   const float* __restrict__ xin = reinterpret_cast<const float*>(a.x);
   const int64_t col = c0 + cc * 4;
   const float* p0 = xin + (col < a.nvec ? col : 0);
+  const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
+  const float* p = p0 + r0 * a.ldx;
+  // rows of the zero padding read row 0 instead and are zeroed by cols_rows_f32
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t r0 = (int64_t)part * R + f32_group<B>(i, h) * 8;
-    const float* p = p0 + r0 * a.ldx;
-    // rows of the zero padding read row 0 instead and are zeroed below
+  for (int e = 0; e < 8; ++e)
+    raw[e] = *reinterpret_cast<const uint4*>(r0 + e < a.in_len ? p + e * a.ldx : p0);
+}
+
+// Round h's rows once they are there: the padding's zeros, the sums over the thread's rows (SUM,
+// added to sum), the transform's signs.
+template <int B, bool SUM>
+__device__ __forceinline__ void cols_rows_f32(const ColsProb& pr, int part, int t, int h,
+                                              float (&sum)[4], uint4 (&raw)[8]) {
+  const FqArgs& a = pr.a;
+  const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(t / (pr.C / 4), h) * 8;
+  if (a.in_len < a.len || (int64_t)pr.P * pr.R > a.len) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      raw[h][e] = *reinterpret_cast<const uint4*>(r0 + e < a.in_len ? p + e * a.ldx : p0);
-    if (a.in_len < a.len || (int64_t)pr.P * R > a.len) {
+      if (r0 + e >= a.in_len) raw[e] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if constexpr (SUM) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (r0 + e >= a.in_len) raw[h][e] = make_uint4(0u, 0u, 0u, 0u);
+    for (int e = 0; e < 8; ++e) {
+      sum[0] += __uint_as_float(raw[e].x);
+      sum[1] += __uint_as_float(raw[e].y);
+      sum[2] += __uint_as_float(raw[e].z);
+      sum[3] += __uint_as_float(raw[e].w);
     }
-    if constexpr (SUM) {
+  }
+  if (a.signs) {  // the transform's signs: one bit per row, on the fp32 sign bits
+    const uint32_t b = row_signs(a, r0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[0] += __uint_as_float(raw[h][e].x);
-        sum[1] += __uint_as_float(raw[h][e].y);
-        sum[2] += __uint_as_float(raw[h][e].z);
-        sum[3] += __uint_as_float(raw[h][e].w);
-      }
-    }
-    if (a.signs) {  // the transform's signs: one bit per row, on the fp32 sign bits
-      const uint32_t b = row_signs(a, r0);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t f = ((b >> e) & 1u) ? 0x80000000u : 0u;
-        raw[h][e].x ^= f; raw[h][e].y ^= f; raw[h][e].z ^= f; raw[h][e].w ^= f;
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t f = ((b >> e) & 1u) ? 0x80000000u : 0u;
+      raw[e].x ^= f; raw[e].y ^= f; raw[e].z ^= f; raw[e].w ^= f;
     }
   }
 }
@@ -875,12 +880,10 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
   }
 }
 
-// The task's column sums from its threads' (4 columns each): lanes of the same columns first,
-// then the waves in order, into row `part` of db_part or db itself.
-__device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
-                                        float (&sum)[4]) {
-  __shared__ float s_db[kColsWaves][256];
-  const FqArgs& a = pr.a;
+// The task's column sums from its threads' (4 columns each): lanes of the same columns first, into
+// s_db (before a barrier), then the waves in order, into row `part` of db_part or db itself.
+__device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&sum)[4],
+                                            float (*s_db)[256]) {
   const int CC = pr.C / 4, lane = t & 63, w = t >> 6;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -896,7 +899,11 @@ __device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part
 #pragma unroll
     for (int c = 0; c < 4; ++c) s_db[w][lane * 4 + c] = sum[c];
   }
-  __syncthreads();
+}
+__device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
+                                        const float (*s_db)[256]) {
+  const FqArgs& a = pr.a;
+  const int CC = pr.C / 4;
   // waves w, w + CC / 64, .. hold the same columns where a row of the tile spans several waves
   const int same = CC <= 64 ? 1 : CC / 64;
   if (t < pr.C && c0 + t < a.nvec) {
@@ -985,14 +992,19 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   // ---- load R rows x C columns, transposed into LDS, into the wave's slices ---------------
   float v[64];
   if constexpr (F32) {
-    constexpr bool kForm = ACT == kDyAct || ACT == kDyKept;  // dz is formed here
-    uint4 raw[kForm ? 1 : 2][8];
+    // a plain fp32 tile's loads of both rounds are under way together; beside the sums of a stored
+    // dz their registers would spill, and its second round is loaded when the first is staged
+    constexpr bool kBoth = ACT == kDyPlain;
+    uint4 raw[kBoth ? 2 : 1][8];
     uint2 ad[8];
     typename std::conditional<ACT == kDyKept, Z4, uint2>::type az[8];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr bool kSum = ACT != kDyPlain && !REPAIR;  // the bias gradient beside the codes
+    __shared__ float s_db[kSum ? kColsWaves : 1][256];
     if constexpr (ACT == kDyKept) cols_load_kept<B>(pr, c0, part, t, 0, ad, az);
     else if constexpr (ACT == kDyAct) cols_load_act<B>(pr, c0, part, t, 0, ad, az);
-    else cols_load_f32<B, ACT == kDyStored>(pr, c0, part, t, sum, raw);
+    else cols_load_f32<B>(pr, c0, part, t, 0, raw[0]);
+    if constexpr (kBoth) cols_load_f32<B>(pr, c0, part, t, 1, raw[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (ACT == kDyKept) {
@@ -1001,9 +1013,17 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       } else if constexpr (ACT == kDyAct) {
         cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
         if (h == 0) cols_load_act<B>(pr, c0, part, t, 1, ad, az);
+      } else {
+        cols_rows_f32<B, ACT == kDyStored>(pr, part, t, h, sum, raw[kBoth ? h : 0]);
       }
-      cols_stage_f32<B>(pr, t, h, raw[kForm ? 0 : h], lds);
+      cols_stage_f32<B>(pr, t, h, raw[kBoth ? h : 0], lds);
+      if constexpr (ACT == kDyStored)
+        if (h == 0) cols_load_f32<B>(pr, c0, part, t, 1, raw[0]);
+      if constexpr (kSum)
+        if (h == 1) cols_db_put(pr, t, sum, s_db);
       __syncthreads();
+      if constexpr (kSum)
+        if (h == 1) cols_db(pr, c0, part, t, s_db);
 #pragma unroll
       for (int jj = 0; jj < 4; ++jj) {
         const int j = 4 * h + jj;
@@ -1016,7 +1036,6 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       }
       if (h == 0) __syncthreads();  // round 1 overwrites the LDS tile
     }
-    if constexpr (ACT != kDyPlain && !REPAIR) cols_db(pr, c0, part, t, sum);
   } else {
     cols_load<B, PK>(pr, c0, part, t, lds);
     __syncthreads();
