@@ -1,12 +1,10 @@
-// gemm.hip -- the layer's 8-bit products: the kernel of gemm_tile.h on 256 x 256 tiles, one or two
-// products per launch.
+// gemm.hip -- the layer's 8-bit products: the kernel of gemm_tile.h, one or two products per launch.
 #include "gemm_tile.h"
 
 namespace halo {
 
-template <int KIND, int AF, int BF, int OUT, bool MASK, int BK>
+template <int KIND, int AF, int BF, int OUT, bool MASK, int BK, typename CFG>
 static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t st) {
-  using CFG = BigTile;
   constexpr int BM = CFG::BT, BN = CFG::BT, NT = 64 * CFG::WM * CFG::WN;
   const hipError_t attr_err =
       allow_dynamic_lds<&gemm_kernel<KIND, AF, BF, OUT, MASK, BK, CFG, kEpiNone>>(CFG::LDS);
@@ -29,12 +27,24 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
   return hipGetLastError();
 }
 
+// The largest tile that still gives the 256 compute units a tile each (see pick of gemm_act.hip; each
+// output's sum runs in the same order in all of them, so the choice changes no result).
+template <int KIND, int AF, int BF, int OUT, bool MASK>
+static hipError_t pick(const GemmArgs& g, const GemmArgs* g1, hipStream_t st) {
+  constexpr int BK = GEMM_BK;
+  auto tiles = [&](int64_t bt) {
+    auto of = [&](const GemmArgs& p) { return ((p.m + bt - 1) / bt) * ((p.n + bt - 1) / bt); };
+    return of(g) + (g1 ? of(*g1) : 0);
+  };
+  if (tiles(256) >= 224) return launch_cfg<KIND, AF, BF, OUT, MASK, BK, BigTile>(g, g1, st);
+  if (tiles(128) >= 224) return launch_cfg<KIND, AF, BF, OUT, MASK, BK, MidTile>(g, g1, st);
+  return launch_cfg<KIND, AF, BF, OUT, MASK, BK, SmallTile>(g, g1, st);
+}
+
 template <int KIND, int AF, int BF, int OUT>
 static hipError_t launch_t(const GemmArgs& g, const GemmArgs* g1, hipStream_t st) {
-  constexpr int BK = GEMM_BK;
-  const bool mask = needs_mask<KIND, BK>(g) || (g1 && needs_mask<KIND, BK>(*g1));
-  return mask ? launch_cfg<KIND, AF, BF, OUT, true, BK>(g, g1, st)
-              : launch_cfg<KIND, AF, BF, OUT, false, BK>(g, g1, st);
+  const bool mask = needs_mask<KIND, GEMM_BK>(g) || (g1 && needs_mask<KIND, GEMM_BK>(*g1));
+  return mask ? pick<KIND, AF, BF, OUT, true>(g, g1, st) : pick<KIND, AF, BF, OUT, false>(g, g1, st);
 }
 
 hipError_t launch_gemm_pair(const GemmArgs& g_in, const GemmArgs* g1_in, int kind, int afmt,

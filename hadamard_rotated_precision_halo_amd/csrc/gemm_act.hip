@@ -6,9 +6,6 @@ namespace halo {
 
 namespace {
 
-// 128 x 128 and 64 x 64 tiles of 4 waves, two workgroups per compute unit.
-using MidTile = TileCfg<128, 2, 2, 2>;
-using SmallTile = TileCfg<64, 2, 2, 4>;
 // the gated layer's smallest: its waves are 64 columns of b wide, 32 of each half
 using SmallGluTile = TileCfg<64, 2, 1, 4>;
 

@@ -53,8 +53,11 @@ struct TileCfg {
   static constexpr int RING = NSTAGE * 2 * BT * GEMM_BK;
   static constexpr int LDS = RING + 2 * BT * 4;
 };
-// The layer's products: 256 x 256 tiles, 8 waves (2 x 4), a 2-slab ring of 128 KB.
+// The layer's products: 256 x 256 tiles, 8 waves (2 x 4), a 2-slab ring of 128 KB; for fewer tiles
+// 128 x 128 and 64 x 64 ones of 4 waves, two workgroups per compute unit.
 using BigTile = TileCfg<256, 2, 4, 2>;
+using MidTile = TileCfg<128, 2, 2, 2>;
+using SmallTile = TileCfg<64, 2, 2, 4>;
 
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
