@@ -639,10 +639,10 @@ __device__ __forceinline__ void cols_kept_rows(const FqArgs& a, int64_t r0, int6
 // Load part `part` (rows [part R, (part + 1) R)) of the column strip starting at column c0
 // into the LDS tile: each thread reads 8 rows of 8 adjacent columns (16 bytes per row),
 // transposes them in registers and writes 8 words of 8 rows of one column each.  PK: x may be kept
-// in 8 bits (a.xk).
-template <int B, bool PK = false>
+// in 8 bits (a.xk).  SUM: the sums over the thread's rows are added to sum (before the signs).
+template <int B, bool PK = false, bool SUM = false>
 __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int part, int t,
-                                          uint4* lds) {
+                                          uint4* lds, float* sum = nullptr) {
   using S = Slice<B>;
   const FqArgs& a = pr.a;
   const int R = pr.R, C = pr.C;
@@ -672,6 +672,15 @@ __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int pa
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (r0 + i >= a.in_len) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if constexpr (SUM) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v[8];
+      unpack_bf16x8(raw[i], v);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] += v[c];
+    }
   }
   if (a.signs) {  // the transform's signs: one bit per row, on the bf16 sign bits
     const uint32_t b = row_signs(a, r0);
@@ -880,13 +889,15 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
   }
 }
 
-// The task's column sums from its threads' (4 columns each): lanes of the same columns first, into
-// s_db (before a barrier), then the waves in order, into row `part` of db_part or db itself.
-__device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&sum)[4],
+// The task's column sums from its threads' (NC columns each): lanes of the same columns first, into
+// s_db (before a barrier), then the waves in order, into row `part` of db_part or db itself.  (8
+// columns a thread: tiles of up to 256 columns.)
+template <int NC>
+__device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&sum)[NC],
                                             float (*s_db)[256]) {
-  const int CC = pr.C / 4, lane = t & 63, w = t >> 6;
+  const int CC = pr.C / NC, lane = t & 63, w = t >> 6;
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < NC; ++c) {
     if (CC <= 1) sum[c] += partner<0>(sum[c]);
     if (CC <= 2) sum[c] += partner<1>(sum[c]);
     if (CC <= 4) sum[c] += partner<2>(sum[c]);
@@ -897,7 +908,7 @@ __device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&s
   const int width = CC < 64 ? CC : 64;  // column chunks of a wave
   if (lane < width) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s_db[w][lane * 4 + c] = sum[c];
+    for (int c = 0; c < NC; ++c) s_db[w][lane * NC + c] = sum[c];
   }
 }
 __device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
@@ -944,9 +955,10 @@ __device__ __forceinline__ void cols_stage_f32(const ColsProb& pr, int t, int h,
 // REPAIR: the second launch of an exchanging pass (see below): only the tasks of strips marked
 // late run, with the column maxima complete by then.
 // F32: fp32 input (two LDS rounds, see cols_load_f32); else bf16.
-// ACT: the activation-gradient pass (see cols_load_act; F32 with it).  PK: see cols_load.
+// ACT: the activation-gradient pass (see cols_load_act; F32 with it).  PK: see cols_load.  SUM: a
+// bf16 pass that also gives the sums of its columns (a.db or a.db_part, either may be NULL).
 template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false, int ACT = kDyPlain,
-          bool PK = false>
+          bool PK = false, bool SUM = false>
 __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uint4* lds) {
   using S = Slice<B>;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
@@ -1037,8 +1049,16 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       if (h == 0) __syncthreads();  // round 1 overwrites the LDS tile
     }
   } else {
-    cols_load<B, PK>(pr, c0, part, t, lds);
+    constexpr bool kSum = SUM && !REPAIR;
+    float sum[8] = {};
+    cols_load<B, PK, kSum>(pr, c0, part, t, lds, sum);
+    __shared__ float s_db[kSum ? kColsWaves : 1][256];
+    const bool sums = kSum && (a.db || a.db_part);
+    if constexpr (kSum)
+      if (sums) cols_db_put(pr, t, sum, s_db);
     __syncthreads();
+    if constexpr (kSum)
+      if (sums) cols_db(pr, c0, part, t, s_db);
 #pragma unroll
     for (int j = 0; j < 8; ++j) unpack_bf16x8(lds[lds_slot<B>(w, lane, j)], &v[j * 8]);
   }
@@ -1187,7 +1207,8 @@ __global__ __launch_bounds__(kColsThreads) void fq_batch_kernel(FqBatch fb) {
   if (bid < fb.end_w) {
     cols_task<B, QW, false>(fb.cw, bid, lds);
   } else if (bid < fb.end_dy) {
-    cols_task<B, QG, SR, false, ACT != kDyPlain, ACT>(fb.cdy, bid - fb.end_w, lds);
+    cols_task<B, QG, SR, false, ACT != kDyPlain, ACT, false, PK && ACT == kDyPlain>(
+        fb.cdy, bid - fb.end_w, lds);
   } else if (bid < fb.end_x) {
     cols_task<B, QW, false, false, false, kDyPlain, PK>(fb.cx, bid - fb.end_dy, lds);
   } else {

@@ -6,8 +6,13 @@ namespace halo {
 
 namespace {
 
-// the gated layer's smallest: its waves are 64 columns of b wide, 32 of each half
+// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.  And its tile for
+// at most one workgroup per compute unit: four slabs on their way instead of two, since no second
+// workgroup covers the loads (203 x 2 x 5504 x 4096 FP8 with the rows pass: 23.2 us a call, 28.7 with
+// two slabs or on the 64 tile; 17 rows of 2 x 11008: 29.7 against 39.6; from 257 tiles on two
+// workgroups of two slabs are as good: 300 x 2 x 5504 29.7).
 using SmallGluTile = TileCfg<64, 2, 1, 4>;
+using DeepGluTile = TileCfg<128, 2, 2, 4>;
 
 template <int KIND, int OUT, bool MASK, typename CFG, int EPI>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
@@ -39,6 +44,8 @@ hipError_t pick(const GemmArgs& g, hipStream_t st) {
   if (tiles(256) >= 224)
     return g.glu ? run<KIND, OUT, MASK, BigTile, kEpiGlu>(g, st)
                  : run<KIND, OUT, MASK, BigTile, kEpiAct>(g, st);
+  if (g.glu && tiles(128) >= 128 && tiles(128) <= 256)
+    return run<KIND, OUT, MASK, DeepGluTile, kEpiGlu>(g, st);
   if (tiles(128) >= 224)
     return g.glu ? run<KIND, OUT, MASK, MidTile, kEpiGlu>(g, st)
                  : run<KIND, OUT, MASK, MidTile, kEpiAct>(g, st);

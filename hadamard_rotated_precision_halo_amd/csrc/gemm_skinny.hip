@@ -210,15 +210,18 @@ __device__ __forceinline__ void rotate8(float* v, int lane, int block) {
 // pass (x, block, signs), whose codes stay in LDS.  Every workgroup repeats that pass; it runs
 // while the workgroup's first reads of b are on their way, and the call is one launch without a
 // scratch (one token, 4096 x 4096 INT8: 10.2 us a call, 14.3 us with the pass in a launch of its
-// own).  A wave takes 512-element slices of the rows, kUnits at most.
+// own).  A wave takes 512-element slices of the rows, kUnits at most.  More output columns than
+// kFusedGrid workgroups hold are dealt to them in turn: a workgroup keeps its codes of a, and reads
+// its next rows of b while it joins the last ones' sums.
 constexpr int kUnits = 4;
+constexpr int kFusedGrid = 512;  // two workgroups per compute unit
 
 template <typename TX, int KIND, int OUT, bool GLU>
 __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, FqArgs f) {
   using S = Step<KIND>;
   using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
   constexpr int UN = 8 / S::CH;
-  __shared__ typename S::Acc s_acc[kWaves][64];
+  __shared__ typename S::Acc s_acc[2][kWaves][64];
   __shared__ float s_unit[kWaves * kUnits], s_sa[16];
   extern __shared__ __attribute__((aligned(16))) char s_codes[];  // [m][pitch]
   const int lane = threadIdx.x & 63;
@@ -226,8 +229,12 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   const int r16 = lane & 15, q16 = lane >> 4;
   const int kq = (int)g.k, m = (int)g.m;
   const int pitch = kq + 16;  // rows 16 bytes apart in the banks
-  const int64_t n0 = (int64_t)blockIdx.x * kCols<GLU>;
-  const char* pb = static_cast<const char*>(g.b) + brow<GLU>(g, n0, r16) * g.ldb + q16 * 16;
+  const int tiles = (int)((g.n + kCols<GLU> - 1) / kCols<GLU>);
+  auto rows_of_b = [&](int tile) __attribute__((always_inline)) {
+    return static_cast<const char*>(g.b) + brow<GLU>(g, (int64_t)tile * kCols<GLU>, r16) * g.ldb +
+           q16 * 16;
+  };
+  const char* pb = rows_of_b(blockIdx.x);
   const int steps = (kq + S::K - 1) / S::K;
   const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
   v4i fb[UN][S::CH];
@@ -280,39 +287,49 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
   __syncthreads();
 
   // ---- the product -----------------------------------------------------------------------
-  typename S::Acc acc = {};
   const char* la = s_codes + min(r16, m - 1) * pitch + q16 * 16;
-  for (int s = s0; s < s1; s += UN) {
-    if (s > s0) load_steps<KIND, UN>(fb, pb, s, s1, g.k, q16);
+  int turn = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    typename S::Acc acc = {};
+    for (int s = s0; s < s1; s += UN) {
+      if (s > s0) load_steps<KIND, UN>(fb, pb, s, s1, g.k, q16);
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      v4i fa[S::CH];
+      for (int u = 0; u < UN; ++u) {
+        v4i fa[S::CH];
 #pragma unroll
-      for (int h = 0; h < S::CH; ++h) {
-        const int k = (s + u) * S::K + h * 64;
-        const bool in = s + u < s1 && k + q16 * 16 < kq;
-        const v4i zero = {0, 0, 0, 0};
-        fa[h] = *reinterpret_cast<const v4i*>(la + (in ? k : -q16 * 16));
-        fa[h] = in ? fa[h] : zero;
-        if constexpr (KIND == 1) fb[u][h] = in ? fb[u][h] : zero;  // 0 x NaN is not 0
+        for (int h = 0; h < S::CH; ++h) {
+          const int k = (s + u) * S::K + h * 64;
+          const bool in = s + u < s1 && k + q16 * 16 < kq;
+          const v4i zero = {0, 0, 0, 0};
+          fa[h] = *reinterpret_cast<const v4i*>(la + (in ? k : -q16 * 16));
+          fa[h] = in ? fa[h] : zero;
+          if constexpr (KIND == 1) fb[u][h] = in ? fb[u][h] : zero;  // 0 x NaN is not 0
+        }
+        acc = S::mul(fb[u], fa, acc);
       }
-      acc = S::mul(fb[u], fa, acc);
     }
+    if (tile + (int)gridDim.x < tiles) {
+      pb = rows_of_b(tile + gridDim.x);
+      load_steps<KIND, UN>(fb, pb, s0, s1, g.k, q16);
+    }
+    // the turns alternate between two areas: a barrier lies between a join and the next sums there
+    s_acc[turn][wave][lane] = acc;
+    __syncthreads();
+    join<T, KIND, GLU>(g, s_acc[turn], (int64_t)tile * kCols<GLU>, [&](int row) { return s_sa[row]; });
   }
-  s_acc[wave][lane] = acc;
-  __syncthreads();
-  join<T, KIND, GLU>(g, s_acc, n0, [&](int row) { return s_sa[row]; });
 }
 
 template <typename TX, int KIND, int OUT>
 hipError_t run_fused(const GemmArgs& g, const FqArgs& f, hipStream_t st) {
   const int lds = (int)(g.m * (g.k + 16));
+  const int64_t tiles = g.glu ? (g.n + 7) / 8 : (g.n + 15) / 16;
+  const dim3 grid((unsigned)(tiles < kFusedGrid ? tiles : kFusedGrid));
   if (g.glu)
-    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, true>), dim3((unsigned)((g.n + 7) / 8)),
-                       dim3(64 * kWaves), lds, st, g, f);
+    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, true>), grid, dim3(64 * kWaves), lds, st, g,
+                       f);
   else
-    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, false>), dim3((unsigned)((g.n + 15) / 16)),
-                       dim3(64 * kWaves), lds, st, g, f);
+    hipLaunchKernelGGL((skinny_fused_kernel<TX, KIND, OUT, false>), grid, dim3(64 * kWaves), lds, st, g,
+                       f);
   return hipGetLastError();
 }
 

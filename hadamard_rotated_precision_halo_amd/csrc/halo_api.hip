@@ -558,7 +558,7 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
   FqArgs cx = make_fq(x, m, k, k, HALO_ALONG_COLS, block, q_type, qxt, mq, sxt, om, mq);
 
   const bool has_dz = act && act->dz;
-  const int64_t db_parts = has_dz ? fq_act_parts(mq, block) : 0;
+  const int64_t db_parts = act ? fq_act_parts(mq, block) : 0;
   if (act && act->kept) {
     rows.zk = cdy.zk = act->zk;
     rows.zw = cdy.zw = act->zw;
@@ -568,6 +568,8 @@ halo_status run_bwd(const void* dy, halo_dtype dy_type, const void* x, const voi
   if (has_dz) {
     rows.z = cdy.z = act->z;
     rows.act = cdy.act = act->act;
+  }
+  if (act) {
     if (act->db && db_parts == 1) cdy.db = static_cast<uint16_t*>(act->db);
     if (act->db && db_parts > 1) cdy.db_part = act->part;
   }
@@ -1314,6 +1316,7 @@ void glu_ep(Ep& e, const void* bias, halo_activation activation) {
 struct KeptBwdWs {
   bool fused;                 // dz is formed (the gated layer's: and stored), and x read, inside the
                               // rotation passes
+  bool sums;                  // so is the bias gradient
   size_t dz, part, x, total;  // byte offsets, and the whole
 };
 
@@ -1324,8 +1327,9 @@ KeptBwdWs kept_bwd_ws(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32
   w.fused = kept_fused_ok(io_type, m, nz, k, block, glu, dx, dw, stochastic);
   w.dz = plan_ws(m, nz, k, 1, block).total;
   w.part = w.dz + (glu || (act && !w.fused) ? round256((size_t)m * nz * 4) : 0);
-  const int64_t parts = w.fused && (act || glu) ? fq_act_parts(contraction_len(m, block), block)
-                                                : act_grad_parts(m, n);
+  const int64_t mq = contraction_len(m, block);
+  w.sums = w.fused && (act || glu || fq_col_sums_ok(mq, block));
+  const int64_t parts = w.sums ? fq_act_parts(mq, block) : act_grad_parts(m, n);
   w.x = w.part + (db ? round256((size_t)parts * nz * 4) : 0);
   w.total = w.x + (dw && !w.fused && kept_form(x_type) != kKeptPlain
                        ? round256((size_t)m * k * esize(io_type)) : 0);
@@ -1389,6 +1393,8 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
       ag.zw = z->powers;
       ag.act = (int)activation;
       ag.glu = glu ? dz : nullptr;
+    }
+    if (wl.sums) {
       ag.db = db;
       ag.part = part;
     } else if (db && launch_act_grad(dy, nullptr, (int)HALO_ACT_NONE, inb, m, n, nullptr, db, part,
