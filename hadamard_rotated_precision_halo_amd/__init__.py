@@ -1143,7 +1143,8 @@ def _groups(cols):
 
 
 def _parts(a, name):
-    if not (isinstance(a, tuple) and len(a) == 2 and all(isinstance(t, torch.Tensor) for t in a)):
+    if not (isinstance(a, tuple) and len(a) == 2 and isinstance(a[0], torch.Tensor)
+            and isinstance(a[1], torch.Tensor)):
         raise ValueError(f"{name} must be a tensor or a Checkpoint")
     if a[0].dtype not in _KEPT_DTYPES:
         raise TypeError(f"unsupported dtype {a[0].dtype}")
@@ -1166,7 +1167,7 @@ def _new_checkpoint(rows, cols, q_dtype, device):
     if q_dtype not in _KEPT_DTYPES:
         raise TypeError(f"unsupported dtype {q_dtype}")
     return Checkpoint(torch.empty((rows, cols), dtype=q_dtype, device=device),
-                      torch.empty((rows, _groups(cols)), dtype=torch.uint8, device=device))
+                      torch.empty((rows, -(-cols // 32)), dtype=torch.uint8, device=device))
 
 
 def _new_kept(want, a, rows, cols, dtype, device, shape=None):
@@ -1189,13 +1190,16 @@ def checkpoint_pack(x, q_dtype=torch.int8, out=None, stream=None):
         return _on(stream, dev, checkpoint_pack, x, q_dtype, out)
     rows, cols = shape = x.shape
     ldx = _rows(x, "x", shape, dt, dev)
+    ldc, ldp = cols, _groups(cols)
     if out is None:
-        out = _new_checkpoint(rows, cols, q_dtype, dev)
-    codes, powers = _parts(out, "out")
-    ldc = _rows(codes, "out's codes", shape, q_dtype, dev)
-    ldp = _rows(powers, "out's powers", (rows, _groups(cols)), torch.uint8, dev)
-    st = lib().halo_checkpoint_pack(_p(x), _TORCH_CODE[dt], rows, cols, ldx, _code(q_dtype), _p(codes),
-                                    ldc, _p(powers), ldp, _current_stream(dev.index))
+        out = codes, powers = _new_checkpoint(rows, cols, q_dtype, dev)
+    else:
+        codes, powers = _parts(out, "out")
+        ldc = _rows(codes, "out's codes", shape, q_dtype, dev)
+        ldp = _rows(powers, "out's powers", (rows, ldp), torch.uint8, dev)
+    st = lib().halo_checkpoint_pack(x.data_ptr(), _TORCH_CODE[dt], rows, cols, ldx, _code(q_dtype),
+                                    codes.data_ptr(), ldc, powers.data_ptr(), ldp,
+                                    _current_stream(dev.index))
     _check(st, "halo_checkpoint_pack")
     return out
 
@@ -1213,10 +1217,12 @@ def checkpoint_unpack(kept, dtype=torch.bfloat16, x=None, stream=None):
     ldc = _rows(codes, "codes", shape, codes.dtype, dev)
     ldp = _rows(powers, "powers", (rows, _groups(cols)), torch.uint8, dev)
     if x is None:
-        x = torch.empty(shape, dtype=dtype, device=dev)
-    ldx = _rows(x, "x", shape, dtype, dev)
-    st = lib().halo_checkpoint_unpack(_p(codes), _TORCH_CODE[codes.dtype], ldc, _p(powers), ldp, rows,
-                                      cols, _p(x), _code(dtype), ldx, _current_stream(dev.index))
+        x, ldx = torch.empty(shape, dtype=dtype, device=dev), cols
+    else:
+        ldx = _rows(x, "x", shape, dtype, dev)
+    st = lib().halo_checkpoint_unpack(codes.data_ptr(), _TORCH_CODE[codes.dtype], ldc,
+                                      powers.data_ptr(), ldp, rows, cols, x.data_ptr(), _code(dtype),
+                                      ldx, _current_stream(dev.index))
     _check(st, "halo_checkpoint_unpack")
     return x
 

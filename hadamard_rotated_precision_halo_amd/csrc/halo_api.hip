@@ -1277,7 +1277,7 @@ halo_status halo_checkpoint_pack(const void* x, halo_dtype x_type, int64_t rows,
                                  uint8_t* powers, int64_t ldp, void* stream) {
   const halo_status s = check_keep(x, x_type, rows, cols, ldx, q_type, codes, ldc, powers, ldp);
   if (s != HALO_OK || rows == 0 || cols == 0) return s;
-  const KeepArgs a{x, nullptr, codes, powers, ldx, ldc, ldp, rows, cols, 0, 0};
+  const KeepArgs a{x, nullptr, codes, powers, ldx, ldc, ldp, rows, cols, 0};
   return from_hip(launch_keep(a, x_type == HALO_BF16 ? 1 : 0, qt_index(q_type), true,
                               (hipStream_t)stream));
 }
@@ -1288,7 +1288,7 @@ halo_status halo_checkpoint_unpack(const void* codes, halo_dtype q_type, int64_t
   const halo_status s = check_keep(x, x_type, rows, cols, ldx, q_type, codes, ldc, powers, ldp);
   if (s != HALO_OK || rows == 0 || cols == 0) return s;
   const KeepArgs a{nullptr, x, const_cast<void*>(codes), const_cast<uint8_t*>(powers), ldx, ldc, ldp,
-                   rows, cols, 0, 0};
+                   rows, cols, 0};
   return from_hip(launch_keep(a, x_type == HALO_BF16 ? 1 : 0, qt_index(q_type), false,
                               (hipStream_t)stream));
 }
@@ -1414,7 +1414,7 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
   const void* xv = x->data;
   if (e == hipSuccess && dw && kept_form(x->type) != kKeptPlain) {
     const KeepArgs a{nullptr, base + wl.x, x->data, x->powers, k, k, (k + kGroup - 1) / kGroup, m, k,
-                     0, 0};
+                     0};
     e = launch_keep(a, inb, qt_index(x->type), false, st);
     xv = base + wl.x;
   }

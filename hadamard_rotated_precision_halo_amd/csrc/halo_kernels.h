@@ -230,8 +230,7 @@ struct KeepArgs {
   void* codes;      // [rows x cols], ldc
   uint8_t* powers;  // [rows x ceil(cols / 32)], ldp
   int64_t ldx, ldc, ldp, rows, cols;
-  int64_t rows_per_wg;  // set by the launcher, as tpr
-  int tpr;
+  int chunks;  // set by the launcher: chunks of 8 a row, whole groups
 };
 hipError_t launch_keep(const KeepArgs& a, int in_bf16, int qt, bool pack, hipStream_t st);
 
