@@ -205,6 +205,17 @@ __device__ __forceinline__ float lane_max(float v, int lane_bits) {
   return v;
 }
 
+// The same for sums (every lane of the vector receives it, in a fixed order).
+__device__ __forceinline__ float lane_sum(float v, int lane_bits) {
+  if (lane_bits > 0) v += partner<0>(v);
+  if (lane_bits > 1) v += partner<1>(v);
+  if (lane_bits > 2) v += partner<2>(v);
+  if (lane_bits > 3) v += partner<3>(v);
+  if (lane_bits > 4) v += partner<4>(v);
+  if (lane_bits > 5) v += partner<5>(v);
+  return v;
+}
+
 // Store chunk j of the lane (8 values y) at element `idx` of the code array: 8 code bytes, or
 // 8 fp32 rotated values for the value mode (QT 3).
 template <int QT>
@@ -639,10 +650,10 @@ __device__ __forceinline__ void cols_kept_rows(const FqArgs& a, int64_t r0, int6
 // Load part `part` (rows [part R, (part + 1) R)) of the column strip starting at column c0
 // into the LDS tile: each thread reads 8 rows of 8 adjacent columns (16 bytes per row),
 // transposes them in registers and writes 8 words of 8 rows of one column each.  PK: x may be kept
-// in 8 bits (a.xk).  SUM: the sums over the thread's rows are added to sum (before the signs).
-template <int B, bool PK = false, bool SUM = false>
+// in 8 bits (a.xk).  SIGNS: with the transform's signs.
+template <int B, bool PK = false, bool SIGNS = true>
 __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int part, int t,
-                                          uint4* lds, float* sum = nullptr) {
+                                          uint4* lds) {
   using S = Slice<B>;
   const FqArgs& a = pr.a;
   const int R = pr.R, C = pr.C;
@@ -673,16 +684,7 @@ __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int pa
     for (int i = 0; i < 8; ++i)
       if (r0 + i >= a.in_len) raw[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if constexpr (SUM) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v[8];
-      unpack_bf16x8(raw[i], v);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] += v[c];
-    }
-  }
-  if (a.signs) {  // the transform's signs: one bit per row, on the bf16 sign bits
+  if (SIGNS && a.signs) {  // the transform's signs: one bit per row, on the bf16 sign bits
     const uint32_t b = row_signs(a, r0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -758,11 +760,10 @@ __device__ __forceinline__ void cols_load_f32(const ColsProb& pr, int64_t c0, in
     raw[e] = *reinterpret_cast<const uint4*>(r0 + e < a.in_len ? p + e * a.ldx : p0);
 }
 
-// Round h's rows once they are there: the padding's zeros, the sums over the thread's rows (SUM,
-// added to sum), the transform's signs.
-template <int B, bool SUM>
+// Round h's rows once they are there: the padding's zeros and (SIGNS) the transform's signs.
+template <int B, bool SIGNS>
 __device__ __forceinline__ void cols_rows_f32(const ColsProb& pr, int part, int t, int h,
-                                              float (&sum)[4], uint4 (&raw)[8]) {
+                                              uint4 (&raw)[8]) {
   const FqArgs& a = pr.a;
   const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(t / (pr.C / 4), h) * 8;
   if (a.in_len < a.len || (int64_t)pr.P * pr.R > a.len) {
@@ -770,16 +771,7 @@ __device__ __forceinline__ void cols_rows_f32(const ColsProb& pr, int part, int 
     for (int e = 0; e < 8; ++e)
       if (r0 + e >= a.in_len) raw[e] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if constexpr (SUM) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      sum[0] += __uint_as_float(raw[e].x);
-      sum[1] += __uint_as_float(raw[e].y);
-      sum[2] += __uint_as_float(raw[e].z);
-      sum[3] += __uint_as_float(raw[e].w);
-    }
-  }
-  if (a.signs) {  // the transform's signs: one bit per row, on the fp32 sign bits
+  if (SIGNS && a.signs) {  // one bit per row, on the fp32 sign bits
     const uint32_t b = row_signs(a, r0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -858,16 +850,16 @@ __device__ __forceinline__ void cols_load_kept(const ColsProb& pr, int64_t c0, i
   }
 }
 
-// One round's dz (8 rows of 4 columns), its sums over the rows added to sum, the transform's signs
-// last.  Z: uint2 (4 bf16) or Z4.
-template <int B, typename Z>
+// One round's dz (8 rows of 4 columns); HERE: its sums over the rows are added to sum, and the
+// transform's signs come last.  Z: uint2 (4 bf16) or Z4.
+template <int B, bool HERE, typename Z>
 __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, int h,
                                          const uint2 (&d)[8], const Z (&z)[8], float (&sum)[4],
                                          uint4 (&raw)[8]) {
   const FqArgs& a = pr.a;
   const int i = t / (pr.C / 4);
   const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(i, h) * 8;
-  const uint32_t flip = a.signs ? row_signs(a, r0) : 0u;
+  const uint32_t flip = HERE && a.signs ? row_signs(a, r0) : 0u;
   // a row at a time: few values live beside the tile's
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -881,7 +873,7 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       v[c] = in ? v[c] : 0.f;
-      sum[c] += v[c];
+      if constexpr (HERE) sum[c] += v[c];
     }
     raw[e] = make_uint4(__float_as_uint(v[0]) ^ f, __float_as_uint(v[1]) ^ f,
                         __float_as_uint(v[2]) ^ f, __float_as_uint(v[3]) ^ f);
@@ -889,15 +881,13 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
   }
 }
 
-// The task's column sums from its threads' (NC columns each): lanes of the same columns first, into
-// s_db (before a barrier), then the waves in order, into row `part` of db_part or db itself.  (8
-// columns a thread: tiles of up to 256 columns.)
-template <int NC>
-__device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&sum)[NC],
+// The task's column sums from its threads' (4 columns each): lanes of the same columns first, into
+// s_db (before a barrier), then the waves in order, into row `part` of db_part or db itself.
+__device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&sum)[4],
                                             float (*s_db)[256]) {
-  const int CC = pr.C / NC, lane = t & 63, w = t >> 6;
+  const int CC = pr.C / 4, lane = t & 63, w = t >> 6;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < 4; ++c) {
     if (CC <= 1) sum[c] += partner<0>(sum[c]);
     if (CC <= 2) sum[c] += partner<1>(sum[c]);
     if (CC <= 4) sum[c] += partner<2>(sum[c]);
@@ -908,7 +898,7 @@ __device__ __forceinline__ void cols_db_put(const ColsProb& pr, int t, float (&s
   const int width = CC < 64 ? CC : 64;  // column chunks of a wave
   if (lane < width) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) s_db[w][lane * NC + c] = sum[c];
+    for (int c = 0; c < 4; ++c) s_db[w][lane * 4 + c] = sum[c];
   }
 }
 __device__ __forceinline__ void cols_db(const ColsProb& pr, int64_t c0, int part, int t,
@@ -955,8 +945,9 @@ __device__ __forceinline__ void cols_stage_f32(const ColsProb& pr, int t, int h,
 // REPAIR: the second launch of an exchanging pass (see below): only the tasks of strips marked
 // late run, with the column maxima complete by then.
 // F32: fp32 input (two LDS rounds, see cols_load_f32); else bf16.
-// ACT: the activation-gradient pass (see cols_load_act; F32 with it).  PK: see cols_load.  SUM: a
-// bf16 pass that also gives the sums of its columns (a.db or a.db_part, either may be NULL).
+// ACT: the activation-gradient pass (see cols_load_act; F32 with it).  PK: see cols_load.  SUM: the
+// pass also gives the sums of its columns (a.db or a.db_part, either may be NULL) from its slices; with
+// ACT always, kDyAct's as its inputs are loaded.
 template <int B, int QT, bool SR, bool REPAIR = false, bool F32 = false, int ACT = kDyPlain,
           bool PK = false, bool SUM = false>
 __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uint4* lds) {
@@ -1002,16 +993,16 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   }
 
   // ---- load R rows x C columns, transposed into LDS, into the wave's slices ---------------
+  constexpr bool kLate = SUM || ACT == kDyKept || ACT == kDyStored;  // sums, then signs, from the slices
   float v[64];
   if constexpr (F32) {
-    // a plain fp32 tile's loads of both rounds are under way together; beside the sums of a stored
-    // dz their registers would spill, and its second round is loaded when the first is staged
-    constexpr bool kBoth = ACT == kDyPlain;
+    constexpr bool kBoth = ACT == kDyPlain || ACT == kDyStored;  // both rounds' loads at once
     uint4 raw[kBoth ? 2 : 1][8];
     uint2 ad[8];
     typename std::conditional<ACT == kDyKept, Z4, uint2>::type az[8];
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr bool kSum = ACT != kDyPlain && !REPAIR;  // the bias gradient beside the codes
+    constexpr bool kHere = ACT == kDyAct;  // the bias gradient's sums as the inputs are loaded
+    constexpr bool kSum = kHere && !REPAIR;
     __shared__ float s_db[kSum ? kColsWaves : 1][256];
     if constexpr (ACT == kDyKept) cols_load_kept<B>(pr, c0, part, t, 0, ad, az);
     else if constexpr (ACT == kDyAct) cols_load_act<B>(pr, c0, part, t, 0, ad, az);
@@ -1020,17 +1011,15 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if constexpr (ACT == kDyKept) {
-        cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
+        cols_act<B, kHere>(pr, part, t, h, ad, az, sum, raw[0]);
         if (h == 0) cols_load_kept<B>(pr, c0, part, t, 1, ad, az);
       } else if constexpr (ACT == kDyAct) {
-        cols_act<B>(pr, part, t, h, ad, az, sum, raw[0]);
+        cols_act<B, kHere>(pr, part, t, h, ad, az, sum, raw[0]);
         if (h == 0) cols_load_act<B>(pr, c0, part, t, 1, ad, az);
       } else {
-        cols_rows_f32<B, ACT == kDyStored>(pr, part, t, h, sum, raw[kBoth ? h : 0]);
+        cols_rows_f32<B, !kLate>(pr, part, t, h, raw[kBoth ? h : 0]);
       }
       cols_stage_f32<B>(pr, t, h, raw[kBoth ? h : 0], lds);
-      if constexpr (ACT == kDyStored)
-        if (h == 0) cols_load_f32<B>(pr, c0, part, t, 1, raw[0]);
       if constexpr (kSum)
         if (h == 1) cols_db_put(pr, t, sum, s_db);
       __syncthreads();
@@ -1049,16 +1038,8 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
       if (h == 0) __syncthreads();  // round 1 overwrites the LDS tile
     }
   } else {
-    constexpr bool kSum = SUM && !REPAIR;
-    float sum[8] = {};
-    cols_load<B, PK, kSum>(pr, c0, part, t, lds, sum);
-    __shared__ float s_db[kSum ? kColsWaves : 1][256];
-    const bool sums = kSum && (a.db || a.db_part);
-    if constexpr (kSum)
-      if (sums) cols_db_put(pr, t, sum, s_db);
+    cols_load<B, PK, !kLate>(pr, c0, part, t, lds);
     __syncthreads();
-    if constexpr (kSum)
-      if (sums) cols_db(pr, c0, part, t, s_db);
 #pragma unroll
     for (int j = 0; j < 8; ++j) unpack_bf16x8(lds[lds_slot<B>(w, lane, j)], &v[j * 8]);
   }
@@ -1066,11 +1047,33 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   // ---- rotate the wave's column segments --------------------------------------------------
   const int seg = S::off(lane, 0) / R;       // column segment of this lane within the wave
   const int64_t pos0 = (int64_t)part * R - (int64_t)seg * R;  // + off(lane, j): row index
-  const float sgn = rotate64<B>(v, lane);
   const int64_t col = c0 + w * cpw + seg;
   const bool valid = col < ncols;
-  float mx = lane_max(absmax64(v), row_lanes_log2);
   const bool writer = (lane & ((1 << row_lanes_log2) - 1)) == 0;
+  if constexpr (kLate) {
+    // the sum of a column (a part of it) is its lanes' own, and the signs come after it.  (The sums of a
+    // thread's columns as they are loaded took 34 more registers of a stored dz's pass, spills among
+    // them, and 15 of 179 us at 4096 x 11008.)
+    if (!REPAIR && (a.db || a.db_part)) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) s += (v[i] + v[i + 1]) + (v[i + 2] + v[i + 3]);
+      s = lane_sum(s, row_lanes_log2);
+      if (valid && writer) {
+        if (a.db) a.db[col] = (uint16_t)bf16x2_of(s, 0.f);
+        else a.db_part[(int64_t)part * ncols + col] = s;
+      }
+    }
+    if (a.signs) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t pos = pos0 + S::off(lane, j);
+        apply_signs8(&v[j * 8], a.signs, pos < a.len ? pos : 0);
+      }
+    }
+  }
+  const float sgn = rotate64<B>(v, lane);
+  float mx = lane_max(absmax64(v), row_lanes_log2);
 
   // ---- column maxima of a strip split over P tasks -----------------------------------------
   // Device-scope atomics only (they are performed at the device's coherence point, across
@@ -1194,7 +1197,7 @@ __global__ __launch_bounds__(kColsThreads) void fq_batch_kernel(FqBatch fb) {
       __syncthreads();  // the next task overwrites the LDS tile
     }
     for (int64_t t = blockIdx.x; t < fb.end_dy - fb.end_w; t += gridDim.x) {
-      cols_task<B, QG, SR, true, ACT != kDyPlain, ACT>(fb.cdy, t, lds);
+      cols_task<B, QG, SR, true, ACT != kDyPlain, ACT, false, PK && ACT == kDyPlain>(fb.cdy, t, lds);
       __syncthreads();
     }
     for (int64_t t = blockIdx.x; t < fb.end_x - fb.end_dy; t += gridDim.x) {

@@ -13,11 +13,6 @@ int64_t fq_act_parts(int64_t rows, int block) {
   return R == 0 ? 0 : cols2_parts(rows, R);
 }
 
-bool fq_col_sums_ok(int64_t rows, int block) {
-  const int R = cols2_rows_per_task(rows, block);
-  return R >= kColsTile / 256;
-}
-
 namespace {
 
 template <int QG, int QW>

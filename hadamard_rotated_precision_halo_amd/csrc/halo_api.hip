@@ -1314,9 +1314,8 @@ void glu_ep(Ep& e, const void* bias, halo_activation activation) {
 // Workspace of a layer backward from kept activations: the layer's (of nz output features), the
 // stored dz, the bias gradient's partial rows and x read back, where the call has them.
 struct KeptBwdWs {
-  bool fused;                 // dz is formed (the gated layer's: and stored), and x read, inside the
-                              // rotation passes
-  bool sums;                  // so is the bias gradient
+  bool fused;                 // dz is formed (the gated layer's: and stored), x read and the bias
+                              // gradient summed inside the rotation passes
   size_t dz, part, x, total;  // byte offsets, and the whole
 };
 
@@ -1327,9 +1326,7 @@ KeptBwdWs kept_bwd_ws(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32
   w.fused = kept_fused_ok(io_type, m, nz, k, block, glu, dx, dw, stochastic);
   w.dz = plan_ws(m, nz, k, 1, block).total;
   w.part = w.dz + (glu || (act && !w.fused) ? round256((size_t)m * nz * 4) : 0);
-  const int64_t mq = contraction_len(m, block);
-  w.sums = w.fused && (act || glu || fq_col_sums_ok(mq, block));
-  const int64_t parts = w.sums ? fq_act_parts(mq, block) : act_grad_parts(m, n);
+  const int64_t parts = w.fused ? fq_act_parts(contraction_len(m, block), block) : act_grad_parts(m, n);
   w.x = w.part + (db ? round256((size_t)parts * nz * 4) : 0);
   w.total = w.x + (dw && !w.fused && kept_form(x_type) != kKeptPlain
                        ? round256((size_t)m * k * esize(io_type)) : 0);
@@ -1394,13 +1391,8 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
       ag.act = (int)activation;
       ag.glu = glu ? dz : nullptr;
     }
-    if (wl.sums) {
-      ag.db = db;
-      ag.part = part;
-    } else if (db && launch_act_grad(dy, nullptr, (int)HALO_ACT_NONE, inb, m, n, nullptr, db, part,
-                                     st) != hipSuccess) {
-      return HALO_ERR_HIP;
-    }
+    ag.db = db;
+    ag.part = part;
     return run_bwd(dy, io_type, x->data, w, io_type, m, nz, k, block, q_type, grad_q_type, dx, dw, opts,
                    ws, st, &ag);
   }

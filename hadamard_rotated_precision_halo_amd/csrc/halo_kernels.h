@@ -80,9 +80,6 @@ hipError_t launch_fq_batch(const FqArgs* rows, const FqArgs& cw, void* ws_w, con
 // in one launch; and the rows of dz alone.  fq_act_parts: rows of db_part (1: whole columns).
 bool fq_act_block_ok(int block);
 int64_t fq_act_parts(int64_t rows, int block);
-// Whether the columns pass of a plain dY (launch_fq_batch_kept) can give its sums: tiles of up to 256
-// columns, so columns of more than 128 rows.
-bool fq_col_sums_ok(int64_t rows, int block);
 hipError_t launch_fq_batch_act(const FqArgs* rows, const FqArgs& cw, void* ws_w, const FqArgs& cdy,
                                void* ws_dy, const FqArgs& cx, void* ws_x, int qg, int qw,
                                hipStream_t st);
