@@ -323,9 +323,17 @@ __device__ __forceinline__ void store_slice_staged(const FqArgs& a, const float*
   }
 }
 
-// Chunk of 8 of z in its kept form: 16 bytes of bf16, or 8 codes and their power.
+// The value of lane K of a lane's quad.
+template <int K>
+__device__ __forceinline__ uint32_t quad_lane(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, K * 0x55, 0xF, 0xF, false);
+}
+
+// Chunk of 8 of z in its kept form: 16 bytes of bf16, or 8 codes and their power.  NO_POWER: the
+// caller sets the power (w.z).
 struct ZChunk {
   uint4 w;
+  template <bool NO_POWER = false>
   __device__ __forceinline__ void load(const FqArgs& a, int64_t row, int64_t width, int64_t col) {
     if (a.zk == kKeptPlain) {
       w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.z) + row * width + col);
@@ -334,7 +342,7 @@ struct ZChunk {
                                                       row * width + col);
       w.x = q.x;
       w.y = q.y;
-      w.z = a.zw[row * ((width + kGroup - 1) / kGroup) + col / kGroup];
+      if (!NO_POWER) w.z = a.zw[row * ((width + kGroup - 1) / kGroup) + col / kGroup];
     }
   }
   __device__ __forceinline__ void get(int zk, float* o) const {
@@ -619,22 +627,59 @@ __device__ __forceinline__ uint32_t row_signs(const FqArgs& a, int64_t r0) {
   return r0 < a.len ? a.signs[r0 >> 5] >> (r0 & 31) : 0u;
 }
 
+// The powers of 8 rows (r0 ..) of the group of 32 columns that a lane's columns are in.  The lanes
+// beside it on the same rows are in the same group (4 of them, or 2 in a tile of 16 columns, cc the
+// lane's place): each reads its share of the rows' bytes and hands it round (4096 rows of 11008 with a
+// byte load per row and lane: 157 us for 146).  col0: the first of these lanes' columns; pw: the powers
+// of rows of nvec values.
+__device__ __forceinline__ void cols_powers(const FqArgs& a, const uint8_t* pw, int64_t r0, int64_t col0,
+                                            int CC, int cc, uint32_t (&s)[8]) {
+  const int64_t groups = (a.nvec + kGroup - 1) / kGroup;
+  const uint8_t* powers = pw + (col0 < a.nvec ? col0 : 0) / kGroup;
+  if (CC >= 4) {
+    uint32_t own[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = r0 + (cc & 3) * 2 + i;
+      own[i] = powers[(row < a.in_len ? row : 0) * groups];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = quad_lane<0>(own[i]);
+      s[2 + i] = quad_lane<1>(own[i]);
+      s[4 + i] = quad_lane<2>(own[i]);
+      s[6 + i] = quad_lane<3>(own[i]);
+    }
+  } else {
+    uint32_t own[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = r0 + (cc & 1) * 4 + i;
+      own[i] = powers[(row < a.in_len ? row : 0) * groups];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)own[i], 0xB1, 0xF, 0xF, false);
+      s[i] = cc & 1 ? other : own[i];
+      s[4 + i] = cc & 1 ? own[i] : other;
+    }
+  }
+}
+
 // 8 rows of 8 adjacent columns of x kept in 8 bits, as bf16 (exact): 8 bytes of codes and a power
 // per row; rows of the zero padding, at and past in_len, read row 0 instead.
 template <int QT>
-__device__ __forceinline__ void cols_kept_rows(const FqArgs& a, int64_t r0, int64_t col,
-                                               uint4 (&raw)[8]) {
+__device__ __forceinline__ void cols_kept_rows(const FqArgs& a, int64_t r0, int64_t col, int64_t c0,
+                                               int CC, int cc, uint4 (&raw)[8]) {
   const uint8_t* codes = reinterpret_cast<const uint8_t*>(a.x) + col;
-  const int64_t groups = (a.ldx + kGroup - 1) / kGroup;
-  const uint8_t* powers = a.xw + col / kGroup;
   uint2 q[8];
   uint32_t s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + i < a.in_len ? r0 + i : 0;
     q[i] = *reinterpret_cast<const uint2*>(codes + row * a.ldx);
-    s[i] = powers[row * groups];
   }
+  cols_powers(a, a.xw, r0, c0 + (cc & ~3) * 8, CC, cc, s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float v[8];
@@ -671,9 +716,9 @@ __device__ __forceinline__ void cols_load(const ColsProb& pr, int64_t c0, int pa
   const uint16_t* p0 = xin + (cvalid ? col : 0);
   const bool padded = a.in_len < a.len || (int64_t)pr.P * R > a.len;
   if (PK && a.xk == kKeptI8) {
-    cols_kept_rows<0>(a, r0, cvalid ? col : 0, raw);
+    cols_kept_rows<0>(a, r0, cvalid ? col : 0, c0, CC, cc, raw);
   } else if (PK && a.xk == kKeptE4M3) {
-    cols_kept_rows<1>(a, r0, cvalid ? col : 0, raw);
+    cols_kept_rows<1>(a, r0, cvalid ? col : 0, c0, CC, cc, raw);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -808,12 +853,10 @@ __device__ __forceinline__ void cols_load_act(const ColsProb& pr, int64_t c0, in
 struct Z4 {
   uint2 w;
   __device__ __forceinline__ void load(const FqArgs& a, int64_t row, int64_t width, int64_t col) {
-    if (a.zk == kKeptPlain) {
+    if (a.zk == kKeptPlain)
       w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.z) + row * width + col);
-    } else {
+    else  // w.y: the power, by its loader
       w.x = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(a.z) + row * width + col);
-      w.y = a.zw[row * ((width + kGroup - 1) / kGroup) + col / kGroup];
-    }
   }
 };
 
@@ -847,6 +890,12 @@ __device__ __forceinline__ void cols_load_kept(const ColsProb& pr, int64_t c0, i
     const int64_t row = r0 + e < a.in_len ? r0 + e : 0;
     d[e] = *reinterpret_cast<const uint2*>(x + row * a.ldx + col);
     z[e].load(a, row, a.nvec, col);
+  }
+  if (a.zk != kKeptPlain) {  // a quad's lanes hold 16 columns of one group
+    uint32_t s[8];
+    cols_powers(a, a.zw, r0, c0 + (cc & ~3) * 4, CC, cc, s);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e].w.y = s[e];
   }
 }
 

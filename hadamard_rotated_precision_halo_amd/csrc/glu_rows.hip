@@ -122,8 +122,22 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
   for (int j = 0; j < 4; ++j) {
     const int at = col0 + S::off(lane, j), col = at < n ? at : 0;
     d[j] = *reinterpret_cast<const uint4*>(a.dy + row * n + col);
-    g[j].load(zf, 2 * row, n, col);
-    u[j].load(zf, 2 * row + 1, n, col);
+    g[j].load<B >= 128>(zf, 2 * row, n, col);
+    u[j].load<B >= 128>(zf, 2 * row + 1, n, col);
+  }
+  if (B >= 128 && a.zk != kKeptPlain) {
+    // a quad's lanes are one group in every chunk: each reads one chunk's two powers
+    const int at = col0 + S::off(lane & ~3, lane & 3), groups = (n + kGroup - 1) / kGroup;
+    const uint8_t* p = a.zw + 2 * row * groups + (at < n ? at : 0) / kGroup;
+    const uint32_t pg = p[0], pu = p[groups];
+    g[0].w.z = quad_lane<0>(pg);
+    g[1].w.z = quad_lane<1>(pg);
+    g[2].w.z = quad_lane<2>(pg);
+    g[3].w.z = quad_lane<3>(pg);
+    u[0].w.z = quad_lane<0>(pu);
+    u[1].w.z = quad_lane<1>(pu);
+    u[2].w.z = quad_lane<2>(pu);
+    u[3].w.z = quad_lane<3>(pu);
   }
   float v[2][32];
 #pragma unroll
