@@ -3,13 +3,13 @@
 // its 2 n columns as the rows kernel of fwht_wave.h does it (natural-order butterflies over blocks of B
 // contiguous indices, one absmax scale per row).
 //
-// A workgroup owns a row.  A wave holds 2048 columns of the gate's half and the same 2048 of the up
-// half, 32 + 32 values per lane, so that dy, g and u are read once and the activation is evaluated once for
-// both: the pass is bound by the vector ALU and by memory alike, and evaluating it for each half, with dz
-// formed again by the columns pass in place of the store, took no less.  Half a slice: chunk j (of 8) of lane
-// lo of a block's G = B / 32 lanes sits at block offset (j G + lo) 8, so the 3 low and the 2 high
-// index bits are butterflied in registers and log2(G) stages cross lanes, in increasing bit order and
-// with the operand order of a sequential fp32 butterfly.
+// A workgroup owns a row.  A lane holds CH chunks of 8 columns of the gate's half and the same of the up
+// half, so that dy, g and u are read once and the activation is evaluated once for both.  The pass moves
+// 360 MB in 66 us at 4096 x 2 x 5504 bf16 (5.4 TB/s); forming dz in the columns pass again in place of the
+// store moved less and took longer (each half evaluates the activation for itself there: 222 against 165 us
+// of all columns).  Chunk j of lane lo of a block's G = B / (8 CH) lanes sits at block offset
+// (j G + lo) 8, so the 3 low and the top index bits are butterflied in registers and log2(G) stages cross
+// lanes, in increasing bit order and with the operand order of a sequential fp32 butterfly.
 //
 // Where the block does not divide n, a block spans both halves and the up half's blocks start at other
 // columns than the gate's: what lies behind the gate's whole blocks (its last columns, the up half, the
@@ -20,12 +20,16 @@ namespace halo {
 
 namespace {
 
-constexpr int kHalf = 2048;                              // columns of a half per wave
-constexpr int kHalfStage = kHalf + kHalf / 256 * 32;     // its codes in LDS (stage_off)
+constexpr int kMaxColumns = 16 * 2048;  // of a half: 16 waves of the widest slices
 
-template <int B>
+// CH: as few chunks a lane as 16 waves hold of a row, so that a row's waves are many and short (4096 x 2
+// x 5504, k 512: 234 us a call with one, 239 with two, 244 with four; 1000 x 2 x 1048: 41.1, 41.6, 42.9).
+template <int B, int CH>
 struct HalfSlice {
-  static constexpr int G = B / 32;  // lanes per block
+  static constexpr int G = B / (8 * CH);  // lanes per block
+  static constexpr int N = 8 * CH;        // values of a half per lane
+  static constexpr int kHalf = 64 * N;    // columns of a half per wave
+  static constexpr int kStage = kHalf + kHalf / 256 * 32;  // its codes in LDS (stage_off)
   __device__ static __forceinline__ int off(int lane, int j) {
     return (lane / G) * B + (j * G + lane % G) * 8;
   }
@@ -36,10 +40,10 @@ __device__ __forceinline__ void put8(uint8_t* p, const float* v) {
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-template <int D>
-__device__ __forceinline__ void reg_stage32(float* v) {
+template <int D, int N>
+__device__ __forceinline__ void reg_stage_n(float* v) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2 * D)
+  for (int i = 0; i < N; i += 2 * D)
 #pragma unroll
     for (int t = i; t < i + D; ++t) {
       const float p = v[t], q = v[t + D];
@@ -48,41 +52,43 @@ __device__ __forceinline__ void reg_stage32(float* v) {
     }
 }
 
-template <int S>
-__device__ __forceinline__ void lane_stage32(float* v, float c) {
+template <int S, int N>
+__device__ __forceinline__ void lane_stage_n(float* v, float c) {
   if constexpr (S < 2) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) dpp_fmac8<S>(&v[i], c);
+    for (int i = 0; i < N; i += 8) dpp_fmac8<S>(&v[i], c);
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = xbutterfly<S>(v[i], c);
+    for (int i = 0; i < N; ++i) v[i] = xbutterfly<S>(v[i], c);
   }
 }
 
-// Rotates a lane's 32 values in place; returns the sign the DPP stages left on them.
-template <int B>
-__device__ __forceinline__ float rotate32(float* v, int lane) {
-  constexpr int G = HalfSlice<B>::G;
+// Rotates a lane's values of a half in place; returns the sign the DPP stages left on them.
+template <int B, int CH>
+__device__ __forceinline__ float rotate_half(float* v, int lane) {
+  constexpr int G = HalfSlice<B, CH>::G, N = HalfSlice<B, CH>::N;
+  static_assert(G <= 64, "a block within a wave");
   const int lo = lane % G;
-  reg_stage32<1>(v);
-  reg_stage32<2>(v);
-  reg_stage32<4>(v);
+  reg_stage_n<1, N>(v);
+  reg_stage_n<2, N>(v);
+  reg_stage_n<4, N>(v);
   float sgn = 1.f;
   if constexpr (G >= 2) {
     const float c = (lo & 1) ? -1.f : 1.f;
-    lane_stage32<0>(v, c);
+    lane_stage_n<0, N>(v, c);
     sgn *= c;
   }
   if constexpr (G >= 4) {
     const float c = (lo & 2) ? -1.f : 1.f;
-    lane_stage32<1>(v, c);
+    lane_stage_n<1, N>(v, c);
     sgn *= c;
   }
-  if constexpr (G >= 8) lane_stage32<2>(v, (lo & 4) ? -1.f : 1.f);
-  if constexpr (G >= 16) lane_stage32<3>(v, (lo & 8) ? -1.f : 1.f);
-  if constexpr (G >= 32) lane_stage32<4>(v, (lo & 16) ? -1.f : 1.f);
-  reg_stage32<8>(v);
-  reg_stage32<16>(v);
+  if constexpr (G >= 8) lane_stage_n<2, N>(v, (lo & 4) ? -1.f : 1.f);
+  if constexpr (G >= 16) lane_stage_n<3, N>(v, (lo & 8) ? -1.f : 1.f);
+  if constexpr (G >= 32) lane_stage_n<4, N>(v, (lo & 16) ? -1.f : 1.f);
+  if constexpr (G >= 64) lane_stage_n<5, N>(v, (lo & 32) ? -1.f : 1.f);
+  if constexpr (CH >= 2) reg_stage_n<8, N>(v);
+  if constexpr (CH >= 4) reg_stage_n<16, N>(v);
   return sgn;
 }
 
@@ -91,9 +97,11 @@ __device__ __forceinline__ float rotate32(float* v, int lane) {
 __device__ __forceinline__ int shift_off(int i) { return i * 4 + (i >> 6) * 32; }
 inline int shift_bytes(int64_t len) { return (int)(len * 4 + (len + 63) / 64 * 32); }
 
-template <int B, int QT, bool SHIFT>
+template <int B, int QT, bool SHIFT, int CH>
 __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
-  using S = HalfSlice<B>;
+  using S = HalfSlice<B, CH>;
+  constexpr int N = S::N;
+  constexpr bool kShare = B >= 128 && CH == 4;  // a quad's lanes are one group of z in every chunk
   extern __shared__ __attribute__((aligned(16))) uint8_t s_stage[];
   __shared__ float s_max[16];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
@@ -104,7 +112,7 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
       a.zero[i] = 0u;
   }
   const int64_t row = blockIdx.x;
-  const int n = (int)a.n, col0 = w * kHalf;
+  const int n = (int)a.n, col0 = w * S::kHalf;
   // the first part's length (whole blocks of the gate) and the second's
   const int len0 = SHIFT ? n - n % B : n, len1 = SHIFT ? (int)a.nq - len0 : n;
   bool in[2];  // whole blocks, so whole lanes
@@ -116,32 +124,33 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
   zf.z = a.z;
   zf.zw = a.zw;
   zf.zk = a.zk;
-  uint4 d[4];
-  ZChunk g[4], u[4];
+  uint4 d[CH];
+  ZChunk g[CH], u[CH];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < CH; ++j) {
     const int at = col0 + S::off(lane, j), col = at < n ? at : 0;
     d[j] = *reinterpret_cast<const uint4*>(a.dy + row * n + col);
-    g[j].load<B >= 128>(zf, 2 * row, n, col);
-    u[j].load<B >= 128>(zf, 2 * row + 1, n, col);
+    g[j].template load<kShare>(zf, 2 * row, n, col);
+    u[j].template load<kShare>(zf, 2 * row + 1, n, col);
   }
-  if (B >= 128 && a.zk != kKeptPlain) {
-    // a quad's lanes are one group in every chunk: each reads one chunk's two powers
-    const int at = col0 + S::off(lane & ~3, lane & 3), groups = (n + kGroup - 1) / kGroup;
-    const uint8_t* p = a.zw + 2 * row * groups + (at < n ? at : 0) / kGroup;
-    const uint32_t pg = p[0], pu = p[groups];
-    g[0].w.z = quad_lane<0>(pg);
-    g[1].w.z = quad_lane<1>(pg);
-    g[2].w.z = quad_lane<2>(pg);
-    g[3].w.z = quad_lane<3>(pg);
-    u[0].w.z = quad_lane<0>(pu);
-    u[1].w.z = quad_lane<1>(pu);
-    u[2].w.z = quad_lane<2>(pu);
-    u[3].w.z = quad_lane<3>(pu);
+  if constexpr (kShare) {
+    if (a.zk != kKeptPlain) {  // each lane reads one chunk's two powers
+      const int at = col0 + S::off(lane & ~3, lane & 3), groups = (n + kGroup - 1) / kGroup;
+      const uint8_t* p = a.zw + 2 * row * groups + (at < n ? at : 0) / kGroup;
+      const uint32_t pg = p[0], pu = p[groups];
+      g[0].w.z = quad_lane<0>(pg);
+      g[1].w.z = quad_lane<1>(pg);
+      g[2].w.z = quad_lane<2>(pg);
+      g[3].w.z = quad_lane<3>(pg);
+      u[0].w.z = quad_lane<0>(pu);
+      u[1].w.z = quad_lane<1>(pu);
+      u[2].w.z = quad_lane<2>(pu);
+      u[3].w.z = quad_lane<3>(pu);
+    }
   }
-  float v[2][32];
+  float v[2][N];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < CH; ++j) {
     float dv[8], gv[8], uv[8];
     unpack_bf16x8(d[j], dv);
     g[j].get(a.zk, gv);
@@ -172,7 +181,7 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
   if constexpr (SHIFT) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < CH; ++j) {
       const int i = in[1] ? col0 + S::off(lane, j) : 0;
       load8<float>(reinterpret_cast<const float*>(s_stage + shift_off(i)), &v[1][j * 8]);
     }
@@ -183,16 +192,16 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < CH; ++j)
         apply_signs8(&v[h][j * 8], a.signs, in[h] ? h * len0 + col0 + S::off(lane, j) : 0);
   }
   float sgn = 1.f, mx = 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    sgn = rotate32<B>(v[h], lane);
+    sgn = rotate_half<B, CH>(v[h], lane);
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; i += 2)
+    for (int i = 0; i < N; i += 2)
       top = __builtin_fmaxf(__builtin_fmaxf(top, fabsf(v[h][i])), fabsf(v[h][i + 1]));
     mx = in[h] ? __builtin_fmaxf(mx, top) : mx;
   }
@@ -209,16 +218,16 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
   // (where the shifted part was: every wave has read it, the maxima's barrier lies between)
   float pre;
   const float mul = code_mul(a.qmax, mx, &pre) * sgn;
-  uint8_t* st = s_stage + w * 2 * kHalfStage;
+  uint8_t* st = s_stage + w * 2 * S::kStage;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if (pre != 1.f) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[h][i] *= pre;
+      for (int i = 0; i < N; ++i) v[h][i] *= pre;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint2*>(st + h * kHalfStage + stage_off(S::off(lane, j))) =
+    for (int j = 0; j < CH; ++j)
+      *reinterpret_cast<uint2*>(st + h * S::kStage + stage_off(S::off(lane, j))) =
           encode8<QT>(&v[h][j * 8], mul);
   }
   // the wave's LDS accesses complete in order: the reads see every lane's writes
@@ -227,34 +236,44 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
     const int rest = (h ? len1 : len0) - col0;
     uint8_t* q = a.q + row * a.nq + h * len0 + col0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < (S::kHalf + 1023) / 1024; ++i) {
       const int b = i * 1024 + lane * 16;
-      if (b < rest)
+      if (b < rest && b < S::kHalf)
         *reinterpret_cast<uint4*>(q + b) =
-            *reinterpret_cast<const uint4*>(st + h * kHalfStage + stage_off(b));
+            *reinterpret_cast<const uint4*>(st + h * S::kStage + stage_off(b));
     }
   }
 }
 
-template <int B, int QT, bool SHIFT>
+template <int B, int QT, bool SHIFT, int CH>
 hipError_t run_form(const GluRowsArgs& a, hipStream_t st) {
+  using S = HalfSlice<B, CH>;
   const int64_t len1 = SHIFT ? a.nq - (a.n - a.n % B) : a.n;  // the longer part
-  const int nw = (int)((len1 + kHalf - 1) / kHalf);
-  int lds = nw * 2 * kHalfStage;
+  const int nw = (int)((len1 + S::kHalf - 1) / S::kHalf);
+  int lds = nw * 2 * S::kStage;
   if (SHIFT && shift_bytes(len1) > lds) lds = shift_bytes(len1);
   if (lds > 65536) {
     const hipError_t e =
-        allow_dynamic_lds<&glu_rows_kernel<B, QT, SHIFT>>(shift_bytes(16 * kHalf));
+        allow_dynamic_lds<&glu_rows_kernel<B, QT, SHIFT, CH>>(shift_bytes(kMaxColumns));
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((glu_rows_kernel<B, QT, SHIFT>), dim3((unsigned)a.rows), dim3(64 * nw), lds, st,
-                     a);
+  hipLaunchKernelGGL((glu_rows_kernel<B, QT, SHIFT, CH>), dim3((unsigned)a.rows), dim3(64 * nw), lds,
+                     st, a);
   return hipGetLastError();
+}
+
+template <int B, int QT, int CH>
+hipError_t run_shift(const GluRowsArgs& a, hipStream_t st) {
+  return a.n % B != 0 ? run_form<B, QT, true, CH>(a, st) : run_form<B, QT, false, CH>(a, st);
 }
 
 template <int B, int QT>
 hipError_t run(const GluRowsArgs& a, hipStream_t st) {
-  return a.n % B != 0 ? run_form<B, QT, true>(a, st) : run_form<B, QT, false>(a, st);
+  // the second part of a row, with a block's rest and the padding, fits 16 waves; a block fits a wave
+  if constexpr (B <= 512)
+    if (a.n + 2 * B <= kMaxColumns / 4) return run_shift<B, QT, 1>(a, st);
+  if (a.n + 2 * B <= kMaxColumns / 2) return run_shift<B, QT, 2>(a, st);
+  return run_shift<B, QT, 4>(a, st);
 }
 
 template <int QT>
@@ -273,7 +292,7 @@ hipError_t run_block(const GluRowsArgs& a, hipStream_t st) {
 
 bool glu_rows_ok(int64_t n, int block) {
   // the second part, with a block's rest and the padding, fits 16 waves
-  return fq_act_block_ok(block) && n > 0 && n % 8 == 0 && n + 2 * block <= 16 * kHalf;
+  return fq_act_block_ok(block) && n > 0 && n % 8 == 0 && n + 2 * block <= kMaxColumns;
 }
 
 hipError_t launch_glu_rows(const GluRowsArgs& a, int qt, hipStream_t st) {
