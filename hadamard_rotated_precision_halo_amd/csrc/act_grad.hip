@@ -72,21 +72,21 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
   __shared__ float s[3][kCols];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t n = a.n, col = (int64_t)blockIdx.x * kCols + lane * 8;
-  const int cnt = (int)max((int64_t)0, min((int64_t)8, n - col));
+  const bool in = col < n;  // n is a multiple of 8: a lane's columns are whole
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_wg, r1 = min(a.m, r0 + rows_per_wg);
   const int64_t groups = (n + kGroup - 1) / kGroup;
   float sum[H][8] = {};
-  if (cnt > 0) {
+  if (in) {
     for (int64_t r = r0 + w; r < r1; r += 4) {
       float d[8], z[H][8], g[H][8];
-      load_cols<T>(static_cast<const T*>(a.dy) + r * n + col, cnt, d);
+      load_cols<T>(static_cast<const T*>(a.dy) + r * n + col, 8, d);
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const int64_t zr = r * H + h;
         if (a.act == kActNone && !GLU) continue;
         if (a.kept == kKeptPlain) {
-          load_cols<T>(static_cast<const T*>(a.z) + zr * n + col, cnt, z[h]);
-        } else {  // n is a multiple of 8: a chunk of 8 codes is whole
+          load_cols<T>(static_cast<const T*>(a.z) + zr * n + col, 8, z[h]);
+        } else {
           const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.z) + zr * n + col);
           const uint32_t p = a.zp[zr * groups + col / kGroup];
           if (a.kept == kKeptI8) kept8<0>(q, p, z[h]);
@@ -105,12 +105,8 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
         float* o = a.dz + r * (n * H) + h * n + col;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[h][e] += g[h][e];
-        if (cnt == 8) {
-          reinterpret_cast<float4*>(o)[0] = make_float4(g[h][0], g[h][1], g[h][2], g[h][3]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(g[h][4], g[h][5], g[h][6], g[h][7]);
-        } else {
-          for (int e = 0; e < cnt; ++e) o[e] = g[h][e];
-        }
+        reinterpret_cast<float4*>(o)[0] = make_float4(g[h][0], g[h][1], g[h][2], g[h][3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(g[h][4], g[h][5], g[h][6], g[h][7]);
       }
     }
   }
@@ -123,12 +119,11 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
       for (int e = 0; e < 8; ++e) s[w - 1][e * 64 + lane] = sum[h][e];
     }
     __syncthreads();
-    if (w == 0 && cnt > 0) {
+    if (w == 0 && in) {
       float* o = part + (int64_t)blockIdx.y * (n * H) + h * n + col;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float v = ((sum[h][e] + s[0][e * 64 + lane]) + s[1][e * 64 + lane]) + s[2][e * 64 + lane];
-        if (e < cnt) o[e] = v;
+        o[e] = ((sum[h][e] + s[0][e * 64 + lane]) + s[1][e * 64 + lane]) + s[2][e * 64 + lane];
       }
     }
   }

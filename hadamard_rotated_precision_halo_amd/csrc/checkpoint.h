@@ -3,9 +3,10 @@
 //
 // A group's power 2^(s - 127) is the least with max |v| <= qmax 2^(s - 127) (qmax 127 for INT8, 448
 // for E4M3), s in [16, 248 or 246], and its codes are v / 2^(s - 127) rounded once, ties to even, and
-// kept within +-qmax.  A power of two rather than max / qmax: the division and every code times its power are then
-// exact, in bf16 too (8 significant bits), so a kept value means the same number to every reader and the
-// rotation passes take it as they take a bf16 one; it costs INT8 half a bit on average.  The lower
+// kept within +-qmax.  A power of two rather than max / qmax: the division and every code times its
+// power are then exact, in bf16 too (8 significant bits), so a kept value means the same number to
+// every reader and the rotation passes take it as they take a bf16 one; it costs INT8 half a bit on
+// average.  The lower
 // bound on s keeps values and products out of the subnormals (what is below 2^-112 is lost), the
 // upper one keeps the largest finite ones finite.  A group with an infinity or a NaN has s = 255 and
 // stands for NaN throughout.

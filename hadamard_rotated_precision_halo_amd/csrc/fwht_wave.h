@@ -17,19 +17,20 @@
 // All stages run in increasing index-bit order with the same operand order as a sequential
 // fp32 butterfly, so the values are bit-identical to it.
 //
-// Rows kernel.  A wave reads its slice straight from HBM: 4096 / L whole rows when L <= 4096
+// Rows kernel.  A wave reads its slice straight from HBM: 4096 / L whole rows when L divides 4096
 // (no barrier), or a workgroup of ceil(L / 4096) waves per row with one LDS exchange of wave
-// maxima.
+// maxima (any L that is a multiple of 64; a wave's lanes behind the row's end idle).
 //
 // Columns kernel.  A workgroup of 16 waves owns a tile of C = 65536 / R columns by R rows:
-// whole columns (R = 4096, C = 16: 32-byte row segments, no exchange) for columns of up to
-// 4096 rows, R = 1024 (C = 64: full 128-byte row segments) for longer ones.  Each lane loads 8
+// whole columns (R the least power of two that holds them; 4096 rows, C = 16: 32-byte row
+// segments, no exchange) for columns of up to 4096 rows, R = 1024 (C = 64: full 128-byte row
+// segments) for longer ones.  Each lane loads 8
 // consecutive rows of 8 adjacent columns, transposes them in registers with v_perm_b32 (8 rows
 // of one column in one 16-byte word) and writes them to LDS in the order the compute waves
 // read them (bank-conflict-free by an XOR swizzle); the waves then run the slice computation
 // on column segments of R rows.  fp32 input keeps the tile's geometry and passes it through
-// the LDS in two rounds of half the rows each (see cols_load_f32).  When a column is longer than R, the P = rows / R workgroups
-// of one column strip combine their partial maxima through device-scope atomics: each
+// the LDS in two rounds of half the rows each (see cols_load_f32).  When a column is longer than
+// R, the P = ceil(rows / R) workgroups of one column strip combine their partial maxima through device-scope atomics: each
 // max-reduces its maxima into the strip's column maxima, increments the strip's arrival
 // counter, and waits until all P have arrived.  The tasks of a group of up to 8 strips are
 // consecutive workgroups, the parts of each strip 8 apart (one XCD), so the parts of a strip
@@ -551,9 +552,11 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   }
 }
 
-// Workgroups of one rows pass (0 for an empty one).
+// Rows that do not divide 4096 take a wave of their own: a 1000 x 2112 bf16 pass took 7 us, 13 in
+// the staged kernel of fwht_quant.hip.
 static bool rows2_multi(int64_t len) { return len > 4096 || 4096 % len != 0; }
-static int64_t rows2_grid(const FqArgs& a) {
+// Workgroups of one rows pass (0 for an empty one).
+static inline int64_t rows2_grid(const FqArgs& a) {
   if (a.nvec == 0) return 0;
   if (rows2_multi(a.len)) return a.nvec;
   const int64_t rpw = 4096 / a.len;
@@ -1263,9 +1266,9 @@ __global__ __launch_bounds__(kColsThreads) void fq_batch_kernel(FqBatch fb) {
         fb.cdy, bid - fb.end_w, lds);
   } else if (bid < fb.end_x) {
     cols_task<B, QW, false, false, false, kDyPlain, PK>(fb.cx, bid - fb.end_dy, lds);
-  } else {
-    rows_wave<uint16_t, B, QG, SR, ACT == kDyStored ? kDyPlain : ACT>(fb.rows, (bid - fb.end_x) * kColsWaves + (threadIdx.x >> 6),
-                                   threadIdx.x & 63);
+  } else if constexpr (ACT != kDyStored) {
+    rows_wave<uint16_t, B, QG, SR, ACT>(fb.rows, (bid - fb.end_x) * kColsWaves + (threadIdx.x >> 6),
+                                        threadIdx.x & 63);
   }
 }
 
@@ -1289,7 +1292,7 @@ static int64_t cols2_parts(int64_t rows, int R) { return (rows + R - 1) / R; }
 // LDS), queried once per device.  Every kernel asking has the same 1024-thread, 128 KB LDS
 // shape, so one cache serves them; concurrent first calls may both query and store the same
 // value.
-static int cols2_capacity(const void* fn) {
+static inline int cols2_capacity(const void* fn) {
   static std::atomic<int> cap[64];
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
@@ -1307,7 +1310,7 @@ static int cols2_capacity(const void* fn) {
 // Strips per task group of a pass with P parts per strip: 8 (one XCD per strip) when 8 P
 // workgroups fit on the device at once, so that a group's waits can all end (the argument of
 // the launchers below, with groups in place of strips); else 1.
-static int cols2_group(int P, int capacity) { return P > 1 && 8 * P <= capacity ? 8 : 1; }
+static inline int cols2_group(int P, int capacity) { return P > 1 && 8 * P <= capacity ? 8 : 1; }
 
 // Scratch layout of one pass: the count of tasks that stopped waiting for the other parts of
 // their strip (one word, padded to 256 bytes), the arrival counters (padded to 256 bytes),
@@ -1324,7 +1327,7 @@ static void cols2_scratch(void* ws, int64_t strips, float** colmax, uint32_t** a
 }
 
 // Geometry and scratch of one column pass (rows = a.len); tasks = 0 for an empty pass.
-static ColsProb cols2_prob(const FqArgs& a, void* ws, int64_t* tasks, int64_t* scratch_words) {
+static inline ColsProb cols2_prob(const FqArgs& a, void* ws, int64_t* tasks, int64_t* scratch_words) {
   ColsProb pr{};
   pr.a = a;
   pr.R = cols2_rows_per_task(a.len, a.block);

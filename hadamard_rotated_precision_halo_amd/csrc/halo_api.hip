@@ -488,7 +488,8 @@ bool kept_fused_ok(halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t 
   const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
   const WsPlan p = plan_ws(m, n, k, 1, block);
   return dx && dw && io_type == HALO_BF16 && fq_act_block_ok(block) && !stochastic &&
-         (glu ? glu_rows_ok(n / 2, block) : fq_rows2_supported(nq, block)) && fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
+         (glu ? glu_rows_ok(n / 2, block) : fq_rows2_supported(nq, block)) &&
+         fq_cols2_supported(nq, k, block, 1, false, p.scr_w) &&
          fq_cols2_supported(mq, n, block, 1, false, p.scr_dy) &&
          fq_cols2_supported(mq, k, block, 1, false, p.scr_x);
 }

@@ -126,7 +126,7 @@ hipError_t launch_fq_dual(const FqArgs& ar, const FqArgs& ac, void* ws, int qt, 
 // Zero n floats (also used for 32-bit counters).
 hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st);
 
-// Wave-per-slice rows kernel: rows of L = 64 j elements with 4096 % L == 0 or 4096 <= L <= 65536.
+// Wave-per-slice rows kernel: rows of L = 64 j elements, L <= 65536.
 bool fq_rows2_supported(int64_t len, int block);
 hipError_t launch_fq_rows2(const FqArgs& a, int in_bf16, int qt, hipStream_t st);
 

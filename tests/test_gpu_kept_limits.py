@@ -220,3 +220,15 @@ def test_two_captured_graphs():
             torch.cuda.synchronize()
             want = H.linear_glu_bwd(d, z, H.checkpoint_pack(x), w, block)
             assert all(torch.equal(u, v) for u, v in zip(out, want))
+
+
+# a product of few tiles and a long contraction beside one of many tiles and a short one, and products
+# alike: both gradients of one call are those of a call for each, bit for bit
+@pytest.mark.parametrize("m,n,k", [(128, 22016, 256), (1000, 14336, 512), (40, 11008, 1024), (4096, 64, 11008),
+                                   (2048, 4096, 1024)])
+@pytest.mark.parametrize("q,gq", [(I8, I8), (E4M3, E5M2)])
+def test_both_gradients_are_each_ones(m, n, k, q, gq):
+    x, w, dy = rnd((m, k), BF16, 1), rnd((n, k), BF16, 2, 0.1), rnd((m, n), BF16, 3)
+    dx, dw = H.linear_bwd(dy, x, w, 64, q, gq)
+    assert torch.equal(dx, H.linear_bwd(dy, x, w, 64, q, gq, want_dw=False)[0])
+    assert torch.equal(dw, H.linear_bwd(dy, x, w, 64, q, gq, want_dx=False)[1])
