@@ -27,14 +27,14 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
   return hipGetLastError();
 }
 
-// The largest tile that still gives the 256 compute units a tile each (see pick of gemm_act.hip; each
-// output's sum runs in the same order in all of them, so the choice changes no result).
+// The tile (see big_tiles, and pick of gemm_act.hip).  Each output's sum runs in the same order in all
+// of them, so the choice changes no result.
 static int tile_of(const GemmArgs& g, const GemmArgs* g1) {
   auto tiles = [&](int64_t bt) {
     auto of = [&](const GemmArgs& p) { return ((p.m + bt - 1) / bt) * ((p.n + bt - 1) / bt); };
     return of(g) + (g1 ? of(*g1) : 0);
   };
-  return tiles(256) >= 224 ? 256 : tiles(128) >= 224 ? 128 : 64;
+  return big_tiles(tiles(256), tiles(128)) ? 256 : tiles(64) > 512 ? 128 : 64;
 }
 
 // Microseconds of a launch on tiles of bt, to choose between launches: the device's rate with all

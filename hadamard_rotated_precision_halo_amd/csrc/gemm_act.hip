@@ -6,13 +6,11 @@ namespace halo {
 
 namespace {
 
-// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.  And its tile for
+// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.  And the tile for
 // at most one workgroup per compute unit: four slabs on their way instead of two, since no second
-// workgroup covers the loads (203 x 2 x 5504 x 4096 FP8 with the rows pass: 23.2 us a call, 28.7 with
-// two slabs or on the 64 tile; 17 rows of 2 x 11008: 29.7 against 39.6; from 257 tiles on two
-// workgroups of two slabs are as good: 300 x 2 x 5504 29.7).
+// workgroup covers the loads.
 using SmallGluTile = TileCfg<64, 2, 1, 4>;
-using DeepGluTile = TileCfg<128, 2, 2, 4>;
+using DeepTile = TileCfg<128, 2, 2, 4>;
 
 template <int KIND, int OUT, bool MASK, typename CFG, int EPI>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
@@ -30,25 +28,25 @@ hipError_t run(const GemmArgs& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// The largest tile that still gives the 256 compute units a tile each, since a workgroup of the
-// 256 tile needs a whole unit and fewer tiles leave units idle for the whole contraction, while
-// smaller tiles read each operand more often from the L2 (8192 x 11008 x 4096 INT8: 403 us a call;
-// on 128 x 128 tiles 9 % longer).  Below that 64 x 64 tiles: two
-// workgroups per unit, or, where there is not even one tile per unit, the kernel whose waves
-// split the contraction (256 x 4096 x 4096 INT8: 16.3 us a call against 18.4 us; but 400 rows:
-// 24.3 against 21.7 us).
+// The largest tile that fills the device (see big_tiles), since smaller ones read each operand more
+// often from the L2 (8192 x 11008 x 4096 INT8: 403 us a call; on 128 x 128 tiles 9 % longer).  64 x 64
+// tiles while two of them per unit are enough, and below one tile per unit the kernel whose waves
+// split the contraction.  INT8, 4096 long, with a rows pass, us on 128 tiles of four slabs, of two, on 64
+// tiles, and split: 256 x 4096: 24.4, 28.5, 19.0, 16.4; 512 x 4096 26.2, 30.2, 23.4, 25.1; 700 x 4096
+// 27.7, 30.6, 34.4, 33.4; 256 x 11008 26.2, 29.7, 32.8, 31.8; 300 x 11008 42.4, 30.6, 38.1, 38.5.
 template <int KIND, int OUT, bool MASK>
 hipError_t pick(const GemmArgs& g, hipStream_t st) {
   const int64_t n = g.glu ? 2 * g.n : g.n;
   auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((n + bt - 1) / bt); };
-  if (tiles(256) >= 224)
+  if (big_tiles(tiles(256), tiles(128)))
     return g.glu ? run<KIND, OUT, MASK, BigTile, kEpiGlu>(g, st)
                  : run<KIND, OUT, MASK, BigTile, kEpiAct>(g, st);
-  if (g.glu && tiles(128) >= 128 && tiles(128) <= 256)
-    return run<KIND, OUT, MASK, DeepGluTile, kEpiGlu>(g, st);
-  if (tiles(128) >= 224)
+  if (tiles(128) > 256)
     return g.glu ? run<KIND, OUT, MASK, MidTile, kEpiGlu>(g, st)
                  : run<KIND, OUT, MASK, MidTile, kEpiAct>(g, st);
+  if (tiles(64) > 512)
+    return g.glu ? run<KIND, OUT, MASK, DeepTile, kEpiGlu>(g, st)
+                 : run<KIND, OUT, MASK, DeepTile, kEpiAct>(g, st);
   if (tiles(64) > 256)
     return g.glu ? run<KIND, OUT, MASK, SmallGluTile, kEpiGlu>(g, st)
                  : run<KIND, OUT, MASK, SmallTile, kEpiAct>(g, st);

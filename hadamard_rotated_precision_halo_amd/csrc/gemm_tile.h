@@ -59,6 +59,18 @@ using BigTile = TileCfg<256, 2, 4, 2>;
 using MidTile = TileCfg<128, 2, 2, 2>;
 using SmallTile = TileCfg<64, 2, 2, 4>;
 
+// Whether a product of so many 256 and 128 tiles is faster on the 256 ones: where the 128 ones need
+// more than one round of the device (512 at once), unless they fill their rounds much better.  At equal
+// filling the 256 tile, which reads its operands less often from the L2, is faster by a fifth (INT8, 4096
+// long, with a rows pass; tiles of 256: us on them and on those of 128: 128: 53.3, 46.3; 129: 49.7, 61.9;
+// 172: 52.3, 58.5; 258: 102.5, 93.8; 344: 105.5, 103.3; 516: 165.3, 161.3; 688: 169, 197; 1376: 335, 374).
+static inline bool big_tiles(int64_t t256, int64_t t128) {
+  auto fill = [](int64_t t, int64_t slots) {
+    return (double)t / (double)((t + slots - 1) / slots * slots);
+  };
+  return t128 > 512 && 1.2 * fill(t256, 256) >= fill(t128, 512);
+}
+
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));

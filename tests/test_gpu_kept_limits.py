@@ -232,3 +232,42 @@ def test_both_gradients_are_each_ones(m, n, k, q, gq):
     dx, dw = H.linear_bwd(dy, x, w, 64, q, gq)
     assert torch.equal(dx, H.linear_bwd(dy, x, w, 64, q, gq, want_dw=False)[0])
     assert torch.equal(dw, H.linear_bwd(dy, x, w, 64, q, gq, want_dx=False)[1])
+
+
+# every tile the products run on: the same sums, so the rows of a batch are those of its parts
+@pytest.mark.parametrize("n,k", [(2048, 160), (5504, 96), (504, 640)])
+@pytest.mark.parametrize("q", [I8, E4M3])
+def test_rows_do_not_depend_on_the_batch(n, k, q):
+    w, x = rnd((2 * n, k), BF16, 2, k ** -0.5), rnd((4500, k), BF16, 1)
+    qw, sw = H.fwht_quant(w, H.ROWS, 32, q)
+    y, z = H.linear_glu_fwd(x, w, 32, q, want_z=True)
+    for m in (1, 3, 17, 100, 203, 300, 700, 1500, 2310, 4100):
+        part = H.linear_glu_fwd(x[:m].contiguous(), w, 32, q, want_z=True)
+        served = H.linear_glu_q(x[:m].contiguous(), qw, sw, 32)
+        if q == I8:   # integer sums
+            assert torch.equal(part[0], y[:m]) and torch.equal(part[1], z[:m]) and torch.equal(served, y[:m])
+        else:         # fp32 sums in another order where the contraction is split between waves
+            G.check_fwd(x[:m].contiguous(), w, 32, q, "silu", None, *part, BF16)
+
+
+@pytest.mark.parametrize("act", ["none", "gelu_tanh"])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_one_of_the_two_kept(act, dt):
+    """x or z kept, the other plain: the gradient of the values, bit for bit as with both kept."""
+    m, n, k = 260, 136, 72
+    x, w, dy, z = rnd((m, k), dt, 1), rnd((n, k), dt, 2, 0.1), rnd((m, n), dt, 3), rnd((m, n), dt, 4)
+    ck, cz = H.checkpoint_pack(x, E4M3), H.checkpoint_pack(z)
+    xv, zv = H.checkpoint_unpack(ck, dt), H.checkpoint_unpack(cz, dt)
+    # (the call with neither kept is another kernel, whose slopes may differ in the last bit of fp32:
+    # test_backward_from_checkpoints compares the two)
+    want = H.linear_act_bwd(dy, cz, ck, w, 64, activation=act)
+    for xi, zi in ((ck, zv), (xv, cz)):
+        for u, v in zip(H.linear_act_bwd(dy, zi, xi, w, 64, activation=act), want):
+            assert torch.equal(u, v)
+    z2 = rnd((m, 2 * n), dt, 5)
+    c2 = H.checkpoint_pack(z2.view(2 * m, n))
+    v2, w2 = H.checkpoint_unpack(c2, dt).view(m, 2 * n), rnd((2 * n, k), dt, 6, 0.1)
+    want = H.linear_glu_bwd(dy, v2, xv, w2, 64, activation=act)
+    for xi, zi in ((ck, v2), (xv, c2), (ck, c2)):
+        for u, v in zip(H.linear_glu_bwd(dy, zi, xi, w2, 64, activation=act), want):
+            assert torch.equal(u, v)
