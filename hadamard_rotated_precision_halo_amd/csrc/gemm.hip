@@ -29,20 +29,22 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
 
 // The tile (see big_tiles, and pick of gemm_act.hip).  Each output's sum runs in the same order in all
 // of them, so the choice changes no result.
-static int tile_of(const GemmArgs& g, const GemmArgs* g1) {
+enum Tile { kBig, kMid, kDeep, kSmall };
+static Tile tile_of(const GemmArgs& g, const GemmArgs* g1) {
   auto tiles = [&](int64_t bt) {
     auto of = [&](const GemmArgs& p) { return ((p.m + bt - 1) / bt) * ((p.n + bt - 1) / bt); };
     return of(g) + (g1 ? of(*g1) : 0);
   };
-  return big_tiles(tiles(256), tiles(128)) ? 256 : tiles(64) > 512 ? 128 : 64;
+  if (big_tiles(tiles(256), tiles(128))) return kBig;
+  return tiles(128) > 256 ? kMid : tiles(64) > 512 ? kDeep : kSmall;
 }
 
-// Microseconds of a launch on tiles of bt, to choose between launches: the device's rate with all
-// compute units busy (2.4, 1.7 and 1.2 POP/s), or its longest tile's slabs one after the other
-// (128 bytes of the contraction each: 1.3, 0.6 and 0.22 us).
-static double launch_us(const GemmArgs& g, const GemmArgs* g1, int bt) {
-  const double rate = bt == 256 ? 2.4e9 : bt == 128 ? 1.7e9 : 1.2e9;
-  const double slab = bt == 256 ? 1.3 : bt == 128 ? 0.6 : 0.22;
+// Microseconds of a launch on a tile, to choose between launches: the device's rate with all compute
+// units busy, or its longest tile's slabs (128 bytes of the contraction) one after the other.
+static double launch_us(const GemmArgs& g, const GemmArgs* g1, Tile t) {
+  constexpr double kRate[] = {2.4e9, 1.7e9, 1.9e9, 1.2e9};  // operations per us
+  constexpr double kSlab[] = {1.3, 0.6, 0.5, 0.22};
+  const double rate = kRate[t], slab = kSlab[t];
   auto ops = [](const GemmArgs& p) { return 2.0 * (double)p.m * (double)p.n * (double)p.k; };
   const int64_t k = g1 && g1->k > g.k ? g1->k : g.k;
   const double work = (ops(g) + (g1 ? ops(*g1) : 0.0)) / rate, chain = (double)k / 128 * slab;
@@ -52,7 +54,8 @@ static double launch_us(const GemmArgs& g, const GemmArgs* g1, int bt) {
 // Two products with tiles of their own, one launch after the other, against one launch on common
 // tiles: a few tiles of a long contraction beside many of a short one keep their compute units long
 // after the others' are done (gradients of few tokens: 128 x 4096 over 22016 beside 22016 x 4096 over
-// 128 takes 186 us in one launch, 44 + 55 in two; 512 tokens 266 and 91 + 80, 1024 tokens 281 and 154 + 117).
+// 128 takes 186 us in one launch, 44 + 55 in two; 512 tokens 266 and 91 + 80; a gated layer's gradient of
+// 1024 tokens 507 a call and 459).
 static bool apart(const GemmArgs& g, const GemmArgs& g1) {
   constexpr double kLaunch = 5.0;  // of a second launch
   return launch_us(g, nullptr, tile_of(g, nullptr)) + launch_us(g1, nullptr, tile_of(g1, nullptr)) +
@@ -63,10 +66,11 @@ template <int KIND, int AF, int BF, int OUT, bool MASK>
 static hipError_t pick(const GemmArgs& g, const GemmArgs* g1, hipStream_t st) {
   constexpr int BK = GEMM_BK;
   switch (tile_of(g, g1)) {
-    case 256: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, BigTile>(g, g1, st);
-    case 128: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, MidTile>(g, g1, st);
+    case kBig: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, BigTile>(g, g1, st);
+    case kMid: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, MidTile>(g, g1, st);
+    case kDeep: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, DeepTile>(g, g1, st);
+    default: return launch_cfg<KIND, AF, BF, OUT, MASK, BK, SmallTile>(g, g1, st);
   }
-  return launch_cfg<KIND, AF, BF, OUT, MASK, BK, SmallTile>(g, g1, st);
 }
 
 template <int KIND, int AF, int BF, int OUT>

@@ -6,11 +6,8 @@ namespace halo {
 
 namespace {
 
-// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.  And the tile for
-// at most one workgroup per compute unit: four slabs on their way instead of two, since no second
-// workgroup covers the loads.
+// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.
 using SmallGluTile = TileCfg<64, 2, 1, 4>;
-using DeepTile = TileCfg<128, 2, 2, 4>;
 
 template <int KIND, int OUT, bool MASK, typename CFG, int EPI>
 hipError_t run(const GemmArgs& g, hipStream_t st) {

@@ -58,6 +58,9 @@ struct TileCfg {
 using BigTile = TileCfg<256, 2, 4, 2>;
 using MidTile = TileCfg<128, 2, 2, 2>;
 using SmallTile = TileCfg<64, 2, 2, 4>;
+// For at most one 128 x 128 workgroup per unit: four slabs on their way instead of two, since no second
+// workgroup covers the loads.
+using DeepTile = TileCfg<128, 2, 2, 4>;
 
 // Whether a product of so many 256 and 128 tiles is faster on the 256 ones: where the 128 ones need
 // more than one round of the device (512 at once), unless they fill their rounds much better.  At equal
