@@ -271,3 +271,17 @@ def test_one_of_the_two_kept(act, dt):
     for xi, zi in ((ck, v2), (xv, c2), (ck, c2)):
         for u, v in zip(H.linear_glu_bwd(dy, zi, xi, w2, 64, activation=act), want):
             assert torch.equal(u, v)
+
+
+# few rows of narrow and wide layers: the kernel that reads the codes straight, and the tiles
+@pytest.mark.parametrize("m", [1, 3, 5, 9, 16])
+@pytest.mark.parametrize("n,k", [(4088, 640), (4096, 640), (4104, 9216)])
+@pytest.mark.parametrize("q", [I8, E4M3])
+def test_few_rows_of_wide_layers(m, n, k, q):
+    x, w, bias = rnd((m, k), BF16, 1), rnd((2 * n, k), BF16, 2, k ** -0.5), rnd((2 * n,), BF16, 3, 0.1)
+    y, z = H.linear_glu_fwd(x, w, 64, q, bias=bias, want_z=True)
+    G.check_fwd(x, w, 64, q, "silu", bias, y, z, BF16)
+    qw, sw = H.fwht_quant(w, H.ROWS, 64, q)
+    served = H.linear_glu_q(x, qw, sw, 64, bias=bias)
+    G.check_fwd(x, w, 64, q, "silu", bias, served, z, BF16)
+    assert torch.equal(served, y)
