@@ -238,6 +238,17 @@ halo_status check_gemm(const void* a, int64_t lda, const void* b, int64_t ldb, i
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
+// Room of one columns pass in the layer's workspace: its scratch, and for columns of up to 4096 rows,
+// which go whole into one task and exchange nothing, what parts that divide them would exchange: the
+// size of a workspace for a given layer stays what it was with such parts, and callers hold it.
+size_t cols_room(int64_t len, int64_t nvec, int32_t block) {
+  if (len > 4096 || len < 64) return round256(fq_ws_bytes_len(len, nvec, HALO_ALONG_COLS, block));
+  int64_t part = 4096;
+  while (part > len || len % part != 0) part >>= 1;
+  if (part < 64 || part % block != 0 || part == len) return 0;
+  const int64_t strips = (nvec + 65536 / part - 1) / (65536 / part);
+  return round256(256 + round256((size_t)strips * 4) + (size_t)nvec * 4);
+}
 
 // Region sizes of the layer workspace, in carve order; the backward's last region is the
 // scratch of its three column passes (W, dY, X: one sub-region each, cleared together by the
@@ -282,7 +293,9 @@ WsPlan plan_ws(int64_t m, int64_t n, int64_t k, int backward, int32_t block) {
   }
   p.scratch_off = o;
   p.scratch_bytes = p.scr_w + p.scr_dy + p.scr_x;
-  p.total = o + p.scratch_bytes;
+  p.total = o;
+  if (backward)
+    p.total += cols_room(nq, k, block) + cols_room(mq, n, block) + cols_room(mq, k, block);
   return p;
 }
 
