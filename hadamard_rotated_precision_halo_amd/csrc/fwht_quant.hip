@@ -474,9 +474,19 @@ hipError_t launch_fill_zero(float* p, int64_t n, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Whether a rows pass that the wave kernel covers is faster in the one above: fp32 rows whose blocks
+// (up to 64) a lane holds alone, that do not divide a wave and pass the caches.  A lane then reads 256
+// bytes of its own 16 at a time, and the waves' lines push each other out of the L1 before they are
+// used up; here neighbouring lanes read neighbouring chunks.  Block 64: 131072 x 1536 218 us here, 267
+// there; 131072 x 3584 483, 531; 32768 x 3584 131, 138; 8192 x 3584 35, 34; 1000 x 2112 11, 7.
+static bool staged_rows(const FqArgs& a, int in_bf16) {
+  return !in_bf16 && a.block <= 64 && a.len < 4096 && 4096 % a.len != 0 &&
+         a.len <= fq_rows_max_len(a.block) && a.nvec > (int64_t(1) << 25) / a.len;
+}
+
 hipError_t launch_fwht_quant(const FqArgs& a, int in_bf16, int qt, int axis, void* ws,
                              size_t ws_bytes, hipStream_t st) {
-  if (axis == 0 && fq_rows2_supported(a.len, a.block) && (in_bf16 || !a.sr))
+  if (axis == 0 && fq_rows2_supported(a.len, a.block) && (in_bf16 || !a.sr) && !staged_rows(a, in_bf16))
     return launch_fq_rows2(a, in_bf16, qt, st);
   if (axis == 1 && fq_cols2_supported(a.len, a.nvec, a.block, in_bf16, a.sr != 0, ws_bytes))
     return launch_fq_cols2(a, in_bf16, qt, ws, st);

@@ -17,9 +17,9 @@
 // All stages run in increasing index-bit order with the same operand order as a sequential
 // fp32 butterfly, so the values are bit-identical to it.
 //
-// Rows kernel.  A wave reads its slice straight from HBM: 4096 / L whole rows when L divides 4096
-// (no barrier), or a workgroup of ceil(L / 4096) waves per row with one LDS exchange of wave
-// maxima (any L that is a multiple of 64; a wave's lanes behind the row's end idle).
+// Rows kernel (L a multiple of 64).  A wave reads its slice straight from HBM: floor(4096 / L) whole
+// rows of up to 4096 (no barrier; the lanes behind the last one idle), or a workgroup of
+// ceil(L / 4096) waves per longer row with one LDS exchange of wave maxima.
 //
 // Columns kernel.  A workgroup of 16 waves owns a tile of C = 65536 / R columns by R rows:
 // whole columns (R the least power of two that holds them; 4096 rows, C = 16: 32-byte row
@@ -451,18 +451,28 @@ __device__ __forceinline__ float stored_scale(const FqArgs& a, float mx) {
 // rows kernel
 // ---------------------------------------------------------------------------
 
-// One wave's slice of a rows pass with L <= 4096 and 4096 % L == 0: wave `gw` of the pass owns
-// rows [gw * 4096 / L, (gw + 1) * 4096 / L).  Lanes past the last row idle.
+// Max over the `lanes` consecutive lanes of a row, whose first is `first`; every lane of the row
+// receives it.  `lanes` is the same for the whole wave.
+__device__ __forceinline__ float row_max(float v, int lane, int first, int lanes) {
+  if ((lanes & (lanes - 1)) == 0) return lane_max(v, 31 - __builtin_clz((unsigned)lanes));
+  for (int d = 1; d < lanes; d *= 2) {  // then of the lanes [lane, lane + 2 d) of the row
+    const float o = __shfl(v, lane + d);
+    if (lane + d < first + lanes) v = __builtin_fmaxf(v, o);
+  }
+  return __shfl(v, first);
+}
+
+// One wave's slice of a rows pass with L <= 4096: wave `gw` of the pass owns rows [gw r, (gw + 1) r),
+// r = floor(4096 / L).  Rows start at whole lanes and hold whole blocks (L is a multiple of 64 and
+// of B); the lanes past the last row idle.
 template <typename Tin, int B, int QT, bool SR, int ACT = kDyPlain>
 __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane) {
-  using S = Slice<B>;
-  const int L = (int)a.len;
-  const int64_t rpw = 4096 / L;              // rows per wave
-  const int r_in_wave = S::off(lane, 0) / L;
+  const int L = (int)a.len, lanes = L / 64;  // lanes per row
+  const int rpw = 4096 / L;                  // rows per wave
+  const int r_in_wave = lane / lanes;
   const int64_t row = gw * rpw + r_in_wave;
   const int col0 = -r_in_wave * L;           // so that col0 + off(lane, j) is the column
-  const int row_lanes_log2 = 31 - __builtin_clz((unsigned)(L / 64));
-  const bool valid = row < a.nvec;
+  const bool valid = r_in_wave < rpw && row < a.nvec;
   const Tin* __restrict__ xin = reinterpret_cast<const Tin*>(a.x);
   // idle lanes read the first chunk of row 0
   const Tin* rp = xin + (valid ? row : 0) * a.ldx;
@@ -470,20 +480,32 @@ __device__ __forceinline__ void rows_wave(const FqArgs& a, int64_t gw, int lane)
   load_slice<Tin, B, ACT>(a, rp, col0, lane, valid, valid ? row : 0, v);
   const float sgn = rotate64<B>(v, lane);
   float mx = valid ? absmax64(v) : 0.f;
-  mx = lane_max(mx, row_lanes_log2);
-  const bool writer = (lane & ((1 << row_lanes_log2) - 1)) == 0;
+  mx = row_max(mx, lane, r_in_wave * lanes, lanes);
   if (!valid) return;
-  if (writer) a.scale[row] = stored_scale<QT>(a, mx);
+  if (lane == r_in_wave * lanes) a.scale[row] = stored_scale<QT>(a, mx);
   const float mul = quant_mul_v<QT>(a, mx, v) * sgn;
   store_slice<B, QT, SR>(a, v, mul, row * a.ldq + col0, lane, row, col0);
 }
 
+// The row at rp, of 2049 to 4096 elements, in one wave (code types).
+template <typename Tin, int B, int QT, bool SR, int ACT>
+__device__ __forceinline__ void row_alone(const FqArgs& a, const Tin* rp, int64_t row, int lane,
+                                          bool valid, uint8_t* st) {
+  float v[64];
+  load_slice<Tin, B, ACT>(a, rp, 0, lane, valid, row, v);
+  const float sgn = rotate64<B>(v, lane);
+  const float mx = lane_max(valid ? absmax64(v) : 0.f, 6);
+  if (lane == 0) a.scale[row] = stored_scale<QT>(a, mx);
+  const float mul = quant_mul_v<QT>(a, mx, v) * sgn;
+  store_slice_staged<B, QT, SR>(a, v, mul, row * a.ldq, lane, row, 0, (int)a.len, st);
+}
+
 // QT: 0 INT8, 1 E4M3, 2 E5M2, 3 fp32 rotated values.
-// multi = 1: one row per workgroup, wave w owns columns [4096 w, 4096 (w + 1)) (also for rows of
-// less than 4096 that do not divide it).
-// multi = 0: 4096 % L == 0, each wave owns 4096 / L whole rows.
+// multi = 1: L > 4096, one row per workgroup, wave w owns columns [4096 w, 4096 (w + 1)).
+// multi = 0: L <= 4096, each wave owns floor(4096 / L) whole rows.
 // One launch serves up to two passes of the same geometry (workgroups below pp.split run the
-// first), and can clear a scratch range for the column passes that follow it on the stream.
+// first; this launch's start at pp.first), and can clear a scratch range for the column passes that
+// follow it on the stream.
 template <typename Tin, int B, int QT, bool SR, int ACT = kDyPlain>
 __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   using S = Slice<B>;
@@ -497,22 +519,20 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < pp.nzero; i += stride)
       pp.zero[i] = 0u;
   }
-  const bool second = (int64_t)blockIdx.x >= pp.split;
+  const int64_t gid = pp.first + blockIdx.x;
+  const bool second = gid >= pp.split;
   const FqArgs a = second ? pp.p1 : pp.p0;
-  const int bid = (int)(blockIdx.x - (second ? pp.split : 0));
+  const int bid = (int)(gid - (second ? pp.split : 0));
   if (!multi) {
-    if (QT != 3 && a.len == 4096) {
-      // one whole row per wave: its codes are one contiguous run of 4096 bytes
+    if (QT != 3 && a.len > 2048) {
+      // one row per wave: its codes are one contiguous run.  Whole waves (rows of 4096) are a branch of
+      // their own: with selects for lanes behind the row's end in it, 65536 x 4096 fp32 at block 64
+      // took 291 us for 263.
       const int64_t row = (int64_t)bid * nw + w;
       if (row >= a.nvec) return;
       const Tin* rp = reinterpret_cast<const Tin*>(a.x) + row * a.ldx;
-      float v[64];
-      load_slice<Tin, B, ACT>(a, rp, 0, lane, true, row, v);
-      const float sgn = rotate64<B>(v, lane);
-      const float mx = lane_max(absmax64(v), 6);
-      if (lane == 0) a.scale[row] = stored_scale<QT>(a, mx);
-      const float mul = quant_mul_v<QT>(a, mx, v) * sgn;
-      store_slice_staged<B, QT, SR>(a, v, mul, row * a.ldq, lane, row, 0, 4096, st);
+      if (a.len == 4096) row_alone<Tin, B, QT, SR, ACT>(a, rp, row, lane, true, st);
+      else row_alone<Tin, B, QT, SR, ACT>(a, rp, row, lane, S::off(lane, 0) < a.len, st);
       return;
     }
     rows_wave<Tin, B, QT, SR, ACT>(a, (int64_t)bid * nw + w, lane);
@@ -552,13 +572,10 @@ __global__ __launch_bounds__(1024) void fq_rows2_kernel(FqPair pp, int multi) {
   }
 }
 
-// Rows that do not divide 4096 take a wave of their own: a 1000 x 2112 bf16 pass took 7 us, 13 in
-// the staged kernel of fwht_quant.hip.
-static bool rows2_multi(int64_t len) { return len > 4096 || 4096 % len != 0; }
 // Workgroups of one rows pass (0 for an empty one).
 static inline int64_t rows2_grid(const FqArgs& a) {
   if (a.nvec == 0) return 0;
-  if (rows2_multi(a.len)) return a.nvec;
+  if (a.len > 4096) return a.nvec;
   const int64_t rpw = 4096 / a.len;
   const int64_t waves = (a.nvec + rpw - 1) / rpw;
   return (waves + 3) / 4;
@@ -576,16 +593,24 @@ static hipError_t launch_rows2_t(FqPair pp, hipStream_t st) {
   }
   // rows of up to 4096 elements: whole rows per wave in 4-wave workgroups (for 4096, this
   // beat one single-wave workgroup per row: 11.74 against 11.43 us per 4096^2 pass)
-  const int multi = rows2_multi(L) ? 1 : 0;
+  const int multi = L > 4096 ? 1 : 0;
   const int nw = multi ? (int)((L + 4095) / 4096) : 4;
-  const int lds = QT != 3 && (multi || L == 4096) ? nw * kStageBytes : 0;
+  const int lds = QT != 3 && L > 2048 ? nw * kStageBytes : 0;
   if (lds > 65536) {
     const hipError_t e = allow_dynamic_lds<&fq_rows2_kernel<Tin, B, QT, SR, ACT>>(16 * kStageBytes);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((fq_rows2_kernel<Tin, B, QT, SR, ACT>), dim3((unsigned)grid), dim3(64 * nw), lds,
-                     st, pp, multi);
-  return hipGetLastError();
+  // more rows than a launch has threads for go in pieces
+  const int64_t most = max_workgroups(64 * nw);
+  for (pp.first = 0; pp.first < grid; pp.first += most) {
+    const int64_t now = grid - pp.first < most ? grid - pp.first : most;
+    hipLaunchKernelGGL((fq_rows2_kernel<Tin, B, QT, SR, ACT>), dim3((unsigned)now), dim3(64 * nw), lds,
+                       st, pp, multi);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    pp.zero = nullptr;
+  }
+  return hipSuccess;
 }
 
 // ---------------------------------------------------------------------------

@@ -135,7 +135,7 @@ hipError_t launch_fq_rows2(const FqArgs& a, int in_bf16, int qt, hipStream_t st)
 struct FqPair {
   FqArgs p0, p1;
   int has1;
-  int64_t split;  // set by the launcher
+  int64_t split, first;  // set by the launcher
   uint32_t* zero;
   int64_t nzero;
 };
