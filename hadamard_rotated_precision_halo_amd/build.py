@@ -11,9 +11,9 @@ LIB = os.path.join(HERE, "libhalo.so")
 SOURCES = ["halo_api.hip", "fwht_quant.hip", "fwht_wave.hip", "fwht_wave_sr.hip", "fwht_wave_act.hip",
            "fwht_wave_kept.hip", "fwht_wave_kept_e5m2.hip", "fwht_wave_kept_e4m3.hip", "glu_rows.hip",
            "fwht_dual.hip",
-           "gemm.hip", "gemm_act.hip", "gemm_skinny.hip", "gemm_ksplit.hip", "act_grad.hip", "checkpoint.hip", "block_norm.hip",
-           "distill.hip", "mfma_probe.hip"]
-HEADERS = ["halo_device.h", "halo_kernels.h", "fwht_wave.h", "rowops.h", "gemm_tile.h", "epilogue.h",
+           "gemm.hip", "gemm_act.hip", "gemm_act_kept.hip", "gemm_skinny.hip", "gemm_ksplit.hip",
+           "act_grad.hip", "checkpoint.hip", "block_norm.hip", "distill.hip", "mfma_probe.hip"]
+HEADERS = ["halo_device.h", "halo_kernels.h", "fwht_wave.h", "rowops.h", "gemm_tile.h", "gemm_act.h", "epilogue.h",
            "checkpoint.h", "fwht_wave_kept.h"]
 
 # -packed-fp32-ops off: hipcc -O3 would otherwise form v_pk_*_f32 from scalar float code.

@@ -1,68 +1,14 @@
-// gemm_act.hip -- the layer's product with its epilogue (bias, activation, residual, the kept
-// pre-activation): the kernel of gemm_tile.h with EPI, on the tile that fills the device.
-#include "gemm_tile.h"
+// gemm_act.hip -- launch interface of the layer's product with its epilogue (gemm_act.h), and the
+// kernels that keep z as plain elements or not at all.
+#include "gemm_act.h"
 
 namespace halo {
-
-namespace {
-
-// The gated layer's smallest: its waves are 64 columns of b wide, 32 of each half.
-using SmallGluTile = TileCfg<64, 2, 1, 4>;
-
-template <int KIND, int OUT, bool MASK, typename CFG, int EPI>
-hipError_t run(const GemmArgs& g, hipStream_t st) {
-  constexpr int BK = GEMM_BK, NT = 64 * CFG::WM * CFG::WN;
-  const hipError_t e =
-      allow_dynamic_lds<&gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, EPI>>(CFG::LDS);
-  if (e != hipSuccess) return e;
-  GemmPair gp{};
-  gp.g[0] = gp.g[1] = g;
-  constexpr int YN = EPI == kEpiGlu ? CFG::BT / 2 : CFG::BT;
-  gp.split = ((g.m + CFG::BT - 1) / CFG::BT) * ((g.n + YN - 1) / YN);
-  if (gp.split == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm_kernel<KIND, 0, 0, OUT, MASK, BK, CFG, EPI>), dim3((unsigned)gp.split),
-                     dim3(NT), CFG::LDS, st, gp);
-  return hipGetLastError();
-}
-
-// The largest tile that fills the device (see big_tiles), since smaller ones read each operand more
-// often from the L2 (8192 x 11008 x 4096 INT8: 403 us a call; on 128 x 128 tiles 9 % longer).  64 x 64
-// tiles while two of them per unit are enough, and below one tile per unit the kernel whose waves
-// split the contraction.  INT8, 4096 long, with a rows pass, us on 128 tiles of four slabs, of two, on 64
-// tiles, and split: 256 x 4096: 24.4, 28.5, 19.0, 16.4; 512 x 4096 26.2, 30.2, 23.4, 25.1; 700 x 4096
-// 27.7, 30.6, 34.4, 33.4; 256 x 11008 26.2, 29.7, 32.8, 31.8; 300 x 11008 42.4, 30.6, 38.1, 38.5.
-template <int KIND, int OUT, bool MASK>
-hipError_t pick(const GemmArgs& g, hipStream_t st) {
-  const int64_t n = g.glu ? 2 * g.n : g.n;
-  auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((n + bt - 1) / bt); };
-  if (big_tiles(tiles(256), tiles(128)))
-    return g.glu ? run<KIND, OUT, MASK, BigTile, kEpiGlu>(g, st)
-                 : run<KIND, OUT, MASK, BigTile, kEpiAct>(g, st);
-  if (tiles(128) > 256)
-    return g.glu ? run<KIND, OUT, MASK, MidTile, kEpiGlu>(g, st)
-                 : run<KIND, OUT, MASK, MidTile, kEpiAct>(g, st);
-  if (tiles(64) > 512)
-    return g.glu ? run<KIND, OUT, MASK, DeepTile, kEpiGlu>(g, st)
-                 : run<KIND, OUT, MASK, DeepTile, kEpiAct>(g, st);
-  if (tiles(64) > 256)
-    return g.glu ? run<KIND, OUT, MASK, SmallGluTile, kEpiGlu>(g, st)
-                 : run<KIND, OUT, MASK, SmallTile, kEpiAct>(g, st);
-  return launch_gemm_ksplit(g, KIND, OUT, st);
-}
-
-template <int KIND, int OUT>
-hipError_t pick_mask(const GemmArgs& g, hipStream_t st) {
-  return needs_mask<KIND, GEMM_BK>(g) ? pick<KIND, OUT, true>(g, st) : pick<KIND, OUT, false>(g, st);
-}
-
-}  // namespace
 
 hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
   // the few-rows kernel's lanes hold single columns: z kept in 8 bits takes the next larger one
   if (g.m <= kSkinnyRows && !g.kept) return launch_gemm_skinny(g, kind, out, st);
-  if (kind == 0) return out == 1 ? pick_mask<0, 1>(g, st) : pick_mask<0, 2>(g, st);
-  return out == 1 ? pick_mask<1, 1>(g, st) : pick_mask<1, 2>(g, st);
+  return g.kept ? launch_gemm_act_kept(g, kind, out, st) : launch_act<false>(g, kind, out, st);
 }
 
 }  // namespace halo

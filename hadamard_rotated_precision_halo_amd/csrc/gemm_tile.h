@@ -164,8 +164,10 @@ struct GemmPair {
 // EPI: the layer's epilogue (bias, activation, residual, the pre-activation kept) in place of
 // the bare dequant; OUT is then 1 or 2 and also the type of bias, residual and z.  kEpiGlu: the gated
 // layer's, y = act(zg) zu: a tile's columns of b are BT / 2 of the gate and the BT / 2 of the up
-// projection that they meet, side by side in every wave, so that the pair never leaves it.
-enum Epi { kEpiNone = 0, kEpiAct = 1, kEpiGlu = 2 };
+// projection that they meet, side by side in every wave, so that the pair never leaves it.  The Kept
+// ones code z in 8 bits: kernels of their own, since that branch beside the plain stores cost every
+// tile 2 to 4 us (8192 x 4096 x 4096 INT8 144 -> 151 us a call, 4096 x 4096 x 1024 FP8 33 -> 38).
+enum Epi { kEpiNone = 0, kEpiAct = 1, kEpiGlu = 2, kEpiActKept = 3, kEpiGluKept = 4 };
 
 template <int KIND, int AF, int BF, int OUT, bool MASK, int BK, typename CFG, int EPI>
 __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPair gp) {
@@ -184,8 +186,10 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   // ---- product and tile of this workgroup ---------------------------------------------
   const bool second = (int64_t)blockIdx.x >= gp.split;
   const GemmArgs g = second ? gp.g[1] : gp.g[0];
-  constexpr int YN = EPI == kEpiGlu ? BN / 2 : BN;  // output columns per tile
-  static_assert(EPI != kEpiGlu || FB % 2 == 0, "a wave holds both halves of a gated pair");
+  constexpr bool GLU = EPI == kEpiGlu || EPI == kEpiGluKept;
+  constexpr bool KEEP = EPI == kEpiActKept || EPI == kEpiGluKept;
+  constexpr int YN = GLU ? BN / 2 : BN;  // output columns per tile
+  static_assert(!GLU || FB % 2 == 0, "a wave holds both halves of a gated pair");
   const int tiles_m = (int)((g.m + BM - 1) / BM), tiles_n = (int)((g.n + YN - 1) / YN);
   const int T = tiles_m * tiles_n;
   const int bid = (int)(blockIdx.x - (second ? gp.split : 0));
@@ -200,7 +204,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   const int64_t n0 = (int64_t)(in_grp / gm) * YN;
   // b's row of the tile's column r (clamped rows feed unused outputs)
   auto brow = [&](int r) __attribute__((always_inline)) -> int64_t {
-    if constexpr (EPI != kEpiGlu) return min(n0 + r, g.n - 1);
+    if constexpr (!GLU) return min(n0 + r, g.n - 1);
     const int64_t c = min(n0 + (r / TN) * (TN / 2) + r % (TN / 2), g.n - 1);
     return r % TN < TN / 2 ? c : g.n + c;
   };
@@ -367,7 +371,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
   // columns wn * TN + i * 32 + g * 8 + fh * 4 + [0, 4), g = 0..3.  Each wave stages its
   // results in LDS 32 rows at a time and reads them back row-contiguous, 16 bytes per lane.
   __syncthreads();  // every wave is done with the K slabs
-  if constexpr (EPI == kEpiGlu) {
+  if constexpr (GLU) {
     // The gated layer's epilogue, in the same way: a lane reads back 8 columns of the gate and the 8
     // of the up projection beside them.
     using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
@@ -421,13 +425,13 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
         act8<T>(g.act, z[0], y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] *= z[1][e];
-        if (g.kept) {
+        if constexpr (KEEP) {
           keep_cols(g.kept, g.z, g.zp, 2 * row, g.n, col0, row < g.m, z[0]);
           keep_cols(g.kept, g.z, g.zp, 2 * row + 1, g.n, col0, row < g.m, z[1]);
         }
         if (row >= g.m || cnt <= 0) continue;
         store_cols<T>(reinterpret_cast<T*>(g.c) + row * g.ldc + col0, cnt, y);
-        if (g.z && !g.kept) {
+        if (!KEEP && g.z) {
           store_cols<T>(reinterpret_cast<T*>(g.z) + 2 * row * g.n + col0, cnt, z[0]);
           store_cols<T>(reinterpret_cast<T*>(g.z) + (2 * row + 1) * g.n + col0, cnt, z[1]);
         }
@@ -435,7 +439,7 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
     }
     return;
   }
-  if constexpr (EPI == kEpiAct) {
+  if constexpr (EPI != kEpiNone) {
     // The layer's epilogue: the raw accumulators are staged as for fp32 output and read back 8
     // columns per lane; z = (acc * sa) * sb + bias, y = act(z) + residual, each rounded once on
     // its store.  The residual of a 32-row strip is loaded before the strip is staged, so its
@@ -496,11 +500,11 @@ __global__ __launch_bounds__(64 * CFG::WM * CFG::WN, 1) void gemm_kernel(GemmPai
 #pragma unroll
           for (int e = 0; e < 8; ++e) y[e] += res[t][e];
         }
-        if (g.kept) keep_cols(g.kept, g.z, g.zp, row, g.n, col0, row < g.m, z);
+        if constexpr (KEEP) keep_cols(g.kept, g.z, g.zp, row, g.n, col0, row < g.m, z);
         if (row >= g.m || cnt <= 0) continue;
         const int64_t at = row * g.ldc + col0;
         store_cols<T>(reinterpret_cast<T*>(g.c) + at, cnt, y);
-        if (g.z && !g.kept) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
+        if (!KEEP && g.z) store_cols<T>(reinterpret_cast<T*>(g.z) + at, cnt, z);
       }
     }
     return;
