@@ -1210,7 +1210,11 @@ __device__ __forceinline__ void cols_task(const ColsProb& pr, int64_t ltask, uin
   if (valid) {
     if (part == 0 && writer) a.scale[col] = stored_scale<QT>(a, mx);
     const float mul = quant_mul_v<QT>(a, mx, v) * sgn;
-    if (pos0 + S::off(lane, 0) < a.len)  // the last part may reach past the column's end
+    // the last part may reach past the column's end; the others keep the stores without checks (a
+    // check per chunk took blocks below 64 from 7.9 to 9.8 us at 128 x 1024)
+    if ((int64_t)(part + 1) * R <= a.len)
+      store_slice<B, QT, SR>(a, v, mul, col * a.ldq + pos0, lane, col, pos0);
+    else if (pos0 + S::off(lane, 0) < a.len)
       store_slice<B, QT, SR, true>(a, v, mul, col * a.ldq + pos0, lane, col, pos0);
   }
 }
