@@ -6,8 +6,7 @@ namespace halo {
 
 hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st) {
   if (g.m == 0 || g.n == 0) return hipSuccess;
-  // the few-rows kernel's lanes hold single columns: z kept in 8 bits takes the next larger one
-  if (g.m <= kSkinnyRows && !g.kept) return launch_gemm_skinny(g, kind, out, st);
+  if (g.m <= kSkinnyRows) return launch_gemm_skinny(g, kind, out, st);
   return g.kept ? launch_gemm_act_kept(g, kind, out, st) : launch_act<false>(g, kind, out, st);
 }
 

@@ -10,7 +10,9 @@
 // 64 bytes per load, no LDS), since no other wave uses them.  The rows of a (up to 16) are read from
 // the L2.  The waves' partial sums meet in LDS and are added in wave order.  For the fewest rows
 // the rotation and quantisation of a run in the same kernel (skinny_fused_kernel).  The gated layer
-// (y = act(zg) zu) takes 8 rows of the gate and the 8 of the up projection that they meet.
+// (y = act(zg) zu) takes 8 rows of the gate and the 8 of the up projection that they meet; with z kept
+// in 8 bits a workgroup takes the 32 columns of a group (skinny_kept_kernel).
+#include "checkpoint.h"
 #include "epilogue.h"
 #include "halo_kernels.h"
 
@@ -76,27 +78,35 @@ __device__ __forceinline__ float act1(int act, float z) {
   }
 }
 
-// The epilogue of one element, and of one gated pair.
-template <typename T>
+// z of a workgroup's group of 32 columns until it is coded: [half x 16 + row][column].
+constexpr int kZPitch = kGroup + 4;
+typedef float ZTile[kZPitch];
+
+// The epilogue of one element, and of one gated pair; KEEP: z goes to column zc of the tile.
+template <typename T, bool KEEP>
 __device__ __forceinline__ void finish_pair(const GemmArgs& g, float gate, float up, float sa,
-                                            int64_t row, int64_t col) {
+                                            int64_t row, int64_t col, ZTile* s_z, int zc) {
   const float zg = z_of<T>(g, gate, sa, col), zu = z_of<T>(g, up, sa, g.n + col);
   elem_store<T>(reinterpret_cast<T*>(g.c) + row * g.ldc + col, act1<T>(g.act, zg) * zu);
-  if (g.z) {
+  if constexpr (KEEP) {
+    s_z[row][zc] = zg;
+    s_z[16 + row][zc] = zu;
+  } else if (g.z) {
     T* z = reinterpret_cast<T*>(g.z) + 2 * row * g.n + col;
     elem_store<T>(z, zg);
     elem_store<T>(z + g.n, zu);
   }
 }
-template <typename T>
+template <typename T, bool KEEP>
 __device__ __forceinline__ void finish(const GemmArgs& g, float acc, float sa, int64_t row,
-                                       int64_t col) {
+                                       int64_t col, ZTile* s_z, int zc) {
   const int64_t at = row * g.ldc + col;
   const float z = z_of<T>(g, acc, sa, col);
   float y = act1<T>(g.act, z);
   if (g.res) y += elem_f32<T>(reinterpret_cast<const T*>(g.res) + at);
   elem_store<T>(reinterpret_cast<T*>(g.c) + at, y);
-  if (g.z) elem_store<T>(reinterpret_cast<T*>(g.z) + at, z);
+  if constexpr (KEEP) s_z[row][zc] = z;
+  else if (g.z) elem_store<T>(reinterpret_cast<T*>(g.z) + at, z);
 }
 
 // An operand's fragments of UN steps from s on; chunks past the contraction or the wave's steps
@@ -117,11 +127,12 @@ __device__ __forceinline__ void load_steps(v4i (&f)[UN][Step<KIND>::CH], const c
 
 // The waves' partial tiles, added in wave order, and the epilogue: element (row i % 16, column
 // i / 16) of thread i is value column % 4 of lane (row, column / 4).
-template <typename T, int KIND, bool GLU, typename Scale>
+template <typename T, int KIND, bool GLU, bool KEEP, typename Scale>
 __device__ __forceinline__ void join(const GemmArgs& g, const typename Step<KIND>::Acc (*s_acc)[64],
-                                     int64_t n0, Scale scale) {
+                                     int64_t n0, Scale scale, int i, ZTile* s_z = nullptr,
+                                     int z0 = 0) {
   using E = typename std::conditional<KIND == 0, int, float>::type;
-  const int i = threadIdx.x, row = i & 15, cl = i >> 4;
+  const int row = i & 15, cl = i >> 4;
   const int64_t col = n0 + cl;
   if (cl >= kCols<GLU> || row >= g.m || col >= g.n) return;
   E sum = 0;
@@ -131,9 +142,9 @@ __device__ __forceinline__ void join(const GemmArgs& g, const typename Step<KIND
     E up = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) up += s_acc[w][((cl + 8) >> 2) * 16 + row][cl & 3];
-    return finish_pair<T>(g, (float)sum, (float)up, scale(row), row, col);
+    return finish_pair<T, KEEP>(g, (float)sum, (float)up, scale(row), row, col, s_z, z0 + cl);
   }
-  finish<T>(g, (float)sum, scale(row), row, col);
+  finish<T, KEEP>(g, (float)sum, scale(row), row, col, s_z, z0 + cl);
 }
 
 template <int KIND, int OUT, bool GLU>
@@ -169,7 +180,68 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
   }
   s_acc[wave][lane] = acc;
   __syncthreads();
-  join<T, KIND, GLU>(g, s_acc, n0, [&](int row) { return g.sa[row]; });
+  join<T, KIND, GLU, false>(g, s_acc, n0, [&](int row) { return g.sa[row]; }, threadIdx.x);
+}
+
+// The same with z kept in 8 bits: a workgroup holds the 2 (gated: 4) runs of columns that make a group
+// of 32.  Every sum runs as above, so y and z have the same bits however z is kept.  LOADS: 64-byte loads
+// of a row in flight together, as many as a wave has (steps behind its last would read it again: gated, 16
+// x 2 x 2048 x 1024 a call with 8 of them 20.2 us, with 2 13.6).
+template <int KIND, int OUT, bool GLU, int LOADS>
+__global__ __launch_bounds__(64 * kWaves) void skinny_kept_kernel(GemmArgs g) {
+  using S = Step<KIND>;
+  using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
+  constexpr int UN = LOADS / S::CH, RUNS = kGroup / kCols<GLU>, H = GLU ? 2 : 1;
+  static_assert(RUNS * 16 * kCols<GLU> == 64 * kWaves, "a thread per element of the group's rows");
+  __shared__ typename S::Acc s_acc[RUNS][kWaves][64];
+  __shared__ ZTile s_z[16 * H];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r16 = lane & 15, q16 = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * kGroup;
+  const char* pa = static_cast<const char*>(g.a) + min((int64_t)r16, g.m - 1) * g.lda + q16 * 16;
+  const char* pb[RUNS];
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r)  // (a run behind the last column reads the last one: unused)
+    pb[r] = static_cast<const char*>(g.b) + brow<GLU>(g, n0 + r * kCols<GLU>, r16) * g.ldb + q16 * 16;
+
+  typename S::Acc acc[RUNS] = {};
+  const int steps = (int)((g.k + S::K - 1) / S::K);
+  const int s0 = (int)((int64_t)steps * wave / kWaves), s1 = (int)((int64_t)steps * (wave + 1) / kWaves);
+  for (int s = s0; s < s1; s += UN) {
+    v4i fb[RUNS][UN][S::CH], fa[UN][S::CH];
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) load_steps<KIND, UN>(fb[r], pb[r], s, s1, g.k, q16);
+    load_steps<KIND, UN>(fa, pa, s, s1, g.k, q16);
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+#pragma unroll
+      for (int h = 0; h < S::CH; ++h) {
+        const int64_t k = (int64_t)(s + u) * S::K + h * 64;
+        const int keep = s + u < s1 && k + q16 * 16 < g.k ? -1 : 0;
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) fb[r][u][h] &= keep;
+        if constexpr (KIND == 1) fa[u][h] &= keep;  // 0 x NaN is not 0
+      }
+#pragma unroll
+      for (int r = 0; r < RUNS; ++r) acc[r] = S::mul(fb[r][u], fa[u], acc[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RUNS; ++r) s_acc[r][wave][lane] = acc[r];
+  __syncthreads();
+  const int t = threadIdx.x, run = t / (16 * kCols<GLU>);
+  join<T, KIND, GLU, true>(g, s_acc[run], n0 + run * kCols<GLU>, [&](int row) { return g.sa[row]; },
+                           t % (16 * kCols<GLU>), s_z, run * kCols<GLU>);
+  __syncthreads();
+  // a quad per row and half, 8 columns a lane (n is a multiple of 8: a lane's columns are whole)
+  const int part = (t & 3) * 8, row = (t >> 2) & 15, h = t >> 6;
+  if (h >= H) return;
+  const int64_t col = n0 + part;
+  const bool in = row < g.m && col < g.n;
+  float z[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = in ? s_z[h * 16 + row][part + e] : 0.f;
+  keep_cols(g.kept, g.z, g.zp, (int64_t)row * H + h, g.n, col, in, z);
 }
 
 // Butterflies of one stage across lanes at distance 2^S where the block spans them.
@@ -315,7 +387,8 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_fused_kernel(GemmArgs g, F
     // the turns alternate between two areas: a barrier lies between a join and the next sums there
     s_acc[turn][wave][lane] = acc;
     __syncthreads();
-    join<T, KIND, GLU>(g, s_acc[turn], (int64_t)tile * kCols<GLU>, [&](int row) { return s_sa[row]; });
+    join<T, KIND, GLU, false>(g, s_acc[turn], (int64_t)tile * kCols<GLU>,
+                              [&](int row) { return s_sa[row]; }, threadIdx.x);
   }
 }
 
@@ -339,15 +412,22 @@ hipError_t run_fused_x(const GemmArgs& g, const FqArgs& f, int kind, int out, hi
   return out == 1 ? run_fused<TX, 1, 1>(g, f, st) : run_fused<TX, 1, 2>(g, f, st);
 }
 
+template <int KIND, int OUT, bool GLU>
+hipError_t run_form(const GemmArgs& g, hipStream_t st) {
+  const dim3 groups((unsigned)((g.n + kGroup - 1) / kGroup));
+  if (g.kept && g.k <= 2 * 64 * kWaves)
+    hipLaunchKernelGGL((skinny_kept_kernel<KIND, OUT, GLU, 2>), groups, dim3(64 * kWaves), 0, st, g);
+  else if (g.kept)
+    hipLaunchKernelGGL((skinny_kept_kernel<KIND, OUT, GLU, 8>), groups, dim3(64 * kWaves), 0, st, g);
+  else
+    hipLaunchKernelGGL((skinny_kernel<KIND, OUT, GLU>),
+                       dim3((unsigned)((g.n + kCols<GLU> - 1) / kCols<GLU>)), dim3(64 * kWaves), 0, st, g);
+  return hipGetLastError();
+}
+
 template <int KIND, int OUT>
 hipError_t run(const GemmArgs& g, hipStream_t st) {
-  if (g.glu)
-    hipLaunchKernelGGL((skinny_kernel<KIND, OUT, true>), dim3((unsigned)((g.n + 7) / 8)),
-                       dim3(64 * kWaves), 0, st, g);
-  else
-    hipLaunchKernelGGL((skinny_kernel<KIND, OUT, false>), dim3((unsigned)((g.n + 15) / 16)),
-                       dim3(64 * kWaves), 0, st, g);
-  return hipGetLastError();
+  return g.glu ? run_form<KIND, OUT, true>(g, st) : run_form<KIND, OUT, false>(g, st);
 }
 
 }  // namespace

@@ -452,7 +452,7 @@ halo_status halo_checkpoint_unpack(const void* codes, halo_dtype q_type, int64_t
 /*
  * halo_linear_act_fwd whose z goes to `z` (plain elements of y_type or a checkpoint, taken from the
  * fp32 z; NULL: not kept).  ep->z must be NULL beside it (HALO_ERR_OPTION).  For a checkpoint n is a
- * multiple of 8.
+ * multiple of 8.  y has the same bits however z is kept (so has halo_linear_glu_fwd's).
  */
 halo_status halo_linear_act_fwd_kept(const void* x, const void* w, halo_dtype io_type, int64_t m,
                                      int64_t n, int64_t k, int32_t block, halo_dtype q_type,
