@@ -27,27 +27,46 @@ static hipError_t launch_cfg(const GemmArgs& g0, const GemmArgs* g1, hipStream_t
   return hipGetLastError();
 }
 
-// The tile (see big_tiles, and pick of gemm_act.hip).  Each output's sum runs in the same order in all
+static int64_t tiles_of(const GemmArgs& p, int64_t bt) {
+  return ((p.m + bt - 1) / bt) * ((p.n + bt - 1) / bt);
+}
+
+// fill_of a launch of one or two products: the second one's tiles, of the shorter contraction, run on
+// the units that the first one's last round leaves idle, and behind it (2048 x 4096 over 4096 beside 4096 x
+// 4096 over 2048: 384 tiles of 256 fill two rounds of the longer's half length, 109.7 us of a gradient
+// against 114.9 in two launches and 118 on 128 tiles).
+static double pair_fill(const GemmArgs& g, const GemmArgs* g1, int64_t bt, int64_t slots) {
+  const int64_t t0 = tiles_of(g, bt);
+  if (!g1 || tiles_of(*g1, bt) == 0) return fill_of(t0, slots);
+  const int64_t t1 = tiles_of(*g1, bt), rest = t0 % slots;
+  const double p = (double)g.k / (double)g1->k;  // rounds of the second in one of the first
+  const int64_t beside = rest ? (slots - rest) * (int64_t)p : 0;
+  const int64_t behind = t1 > beside ? t1 - beside : 0;
+  const double rounds = (double)((t0 + slots - 1) / slots) * p + (double)((behind + slots - 1) / slots);
+  return ((double)t0 * p + (double)t1) / ((double)slots * rounds);
+}
+
+// The tile (see big_tiles, and pick_act of gemm_act.h).  Each output's sum runs in the same order in all
 // of them, so the choice changes no result.
 enum Tile { kBig, kMid, kDeep, kSmall };
 static Tile tile_of(const GemmArgs& g, const GemmArgs* g1) {
-  auto tiles = [&](int64_t bt) {
-    auto of = [&](const GemmArgs& p) { return ((p.m + bt - 1) / bt) * ((p.n + bt - 1) / bt); };
-    return of(g) + (g1 ? of(*g1) : 0);
-  };
-  if (big_tiles(tiles(256), tiles(128))) return kBig;
-  return tiles(128) > 256 ? kMid : tiles(64) > 512 ? kDeep : kSmall;
+  auto tiles = [&](int64_t bt) { return tiles_of(g, bt) + (g1 ? tiles_of(*g1, bt) : 0); };
+  if (big_tiles(tiles(128), pair_fill(g, g1, 256, 256), pair_fill(g, g1, 128, 512), g.k)) return kBig;
+  if (tiles(128) > 256) return kMid;
+  return tiles(64) > 512 ? kDeep : kSmall;
 }
 
 // Microseconds of a launch on a tile, to choose between launches: the device's rate with all compute
-// units busy, or its longest tile's slabs (128 bytes of the contraction) one after the other.
+// units busy, or its longest tile's slabs (128 bytes of the contraction) one after the other.  The
+// constants are INT8's; FP8's rates lie within a tenth of them (22016 x 4096 x 4096 on 256 tiles 379 and
+// 346 us) and favour the same launch.  Over 476 gradients the choice lies 2 % above the best of one launch
+// on any tile and two, and none over 3 % behind one launch on 256 tiles.
 static double launch_us(const GemmArgs& g, const GemmArgs* g1, Tile t) {
-  constexpr double kRate[] = {2.4e9, 1.7e9, 1.9e9, 1.2e9};  // operations per us
-  constexpr double kSlab[] = {1.3, 0.6, 0.5, 0.22};
-  const double rate = kRate[t], slab = kSlab[t];
+  constexpr double kRate[] = {2.2e9, 1.8e9, 1.9e9, 1.2e9};  // operations per us
+  constexpr double kSlab[] = {1.3, 0.75, 0.5, 0.22};
   auto ops = [](const GemmArgs& p) { return 2.0 * (double)p.m * (double)p.n * (double)p.k; };
-  const int64_t k = g1 && g1->k > g.k ? g1->k : g.k;
-  const double work = (ops(g) + (g1 ? ops(*g1) : 0.0)) / rate, chain = (double)k / 128 * slab;
+  const double work = (ops(g) + (g1 ? ops(*g1) : 0.0)) / kRate[t];
+  const double chain = (double)g.k / 128 * kSlab[t];  // g's contraction is the longer one
   return work > chain ? work : chain;
 }
 
@@ -57,7 +76,7 @@ static double launch_us(const GemmArgs& g, const GemmArgs* g1, Tile t) {
 // 128 takes 186 us in one launch, 44 + 55 in two; 512 tokens 266 and 91 + 80; a gated layer's gradient of
 // 1024 tokens 507 a call and 459).
 static bool apart(const GemmArgs& g, const GemmArgs& g1) {
-  constexpr double kLaunch = 5.0;  // of a second launch
+  constexpr double kLaunch = 8.0;  // of a second launch and the first one's tail
   return launch_us(g, nullptr, tile_of(g, nullptr)) + launch_us(g1, nullptr, tile_of(g1, nullptr)) +
              kLaunch < launch_us(g, &g1, tile_of(g, &g1));
 }

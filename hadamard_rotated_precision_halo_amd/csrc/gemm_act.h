@@ -31,16 +31,17 @@ static hipError_t run_act(const GemmArgs& g, hipStream_t st) {
 // tiles while two of them per unit are enough, and below one tile per unit the kernel whose waves
 // split the contraction.  INT8, 4096 long, with a rows pass, us on 128 tiles of four slabs, of two, on 64
 // tiles, and split: 256 x 4096: 24.4, 28.5, 19.0, 16.4; 512 x 4096 26.2, 30.2, 23.4, 25.1; 700 x 4096
-// 27.7, 30.6, 34.4, 33.4; 256 x 11008 26.2, 29.7, 32.8, 31.8; 300 x 11008 42.4, 30.6, 38.1, 38.5.
+// 27.7, 30.6, 34.4, 33.4; 256 x 11008 26.2, 29.7, 32.8, 31.8; 300 x 11008 42.4, 30.6, 38.1, 38.5.  Up to
+// 512 long two slabs do (1024 x 4096, 256 long: 14.1, 13.6).
 template <int KIND, int OUT, bool MASK, bool KEPT>
 static hipError_t pick_act(const GemmArgs& g, hipStream_t st) {
   constexpr int ACT = KEPT ? kEpiActKept : kEpiAct, GLU = KEPT ? kEpiGluKept : kEpiGlu;
   const int64_t n = g.glu ? 2 * g.n : g.n;
   auto tiles = [&](int64_t bt) { return ((g.m + bt - 1) / bt) * ((n + bt - 1) / bt); };
-  if (big_tiles(tiles(256), tiles(128)))
+  if (big_tiles(tiles(128), fill_of(tiles(256), 256), fill_of(tiles(128), 512), g.k))
     return g.glu ? run_act<KIND, OUT, MASK, BigTile, GLU>(g, st)
                  : run_act<KIND, OUT, MASK, BigTile, ACT>(g, st);
-  if (tiles(128) > 256)
+  if (tiles(128) > 256 || (tiles(64) > 512 && g.k <= 4 * GEMM_BK))
     return g.glu ? run_act<KIND, OUT, MASK, MidTile, GLU>(g, st)
                  : run_act<KIND, OUT, MASK, MidTile, ACT>(g, st);
   if (tiles(64) > 512)

@@ -62,16 +62,21 @@ using SmallTile = TileCfg<64, 2, 2, 4>;
 // workgroup covers the loads.
 using DeepTile = TileCfg<128, 2, 2, 4>;
 
-// Whether a product of so many 256 and 128 tiles is faster on the 256 ones: where the 128 ones need
-// more than one round of the device (512 at once), unless they fill their rounds much better.  At equal
-// filling the 256 tile, which reads its operands less often from the L2, is faster by a fifth (INT8, 4096
-// long, with a rows pass; tiles of 256: us on them and on those of 128: 128: 53.3, 46.3; 129: 49.7, 61.9;
-// 172: 52.3, 58.5; 258: 102.5, 93.8; 344: 105.5, 103.3; 516: 165.3, 161.3; 688: 169, 197; 1376: 335, 374).
-static inline bool big_tiles(int64_t t256, int64_t t128) {
-  auto fill = [](int64_t t, int64_t slots) {
-    return (double)t / (double)((t + slots - 1) / slots * slots);
-  };
-  return t128 > 512 && 1.2 * fill(t256, 256) >= fill(t128, 512);
+// Share of the device's time that a launch of `tiles` fills, of which `slots` run at once.
+static inline double fill_of(int64_t tiles, int64_t slots) {
+  return (double)tiles / (double)((tiles + slots - 1) / slots * slots);
+}
+
+// Whether a launch of t128 128 tiles, which fill the device to f128, is faster on 256 ones, which fill it
+// to f256; k: its longest contraction.  It is where the 128 ones need more than one round of the device
+// (512 at once), unless they fill their rounds much better.  At equal filling the 256 tile, which reads its
+// operands less often from the L2, is faster, and by more the longer the contraction (INT8, with a rows
+// pass; us on tiles of 256 and of 128, tiles of 256: 1024 long 256: 35.0, 36.9; 344: 51.5, 46.8; 4096 long
+// 128: 53.3, 46.3; 129: 49.7, 61.9; 172: 52.3, 58.5; 258: 102.5, 93.8; 344: 105.5, 103.3; 688: 169, 197;
+// 11008 long 256: 182, 210; 384: 303, 304).
+static inline bool big_tiles(int64_t t128, double f256, double f128, int64_t k) {
+  const double gain = 1.0 + (double)(k < 12288 ? k : 12288) / 25600;
+  return t128 > 512 && (gain > 1.2 ? gain : 1.2) * f256 >= f128;
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
