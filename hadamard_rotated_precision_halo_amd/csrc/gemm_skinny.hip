@@ -151,7 +151,9 @@ template <int KIND, int OUT, bool GLU>
 __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
   using S = Step<KIND>;
   using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
-  constexpr int UN = 8 / S::CH;  // steps whose loads are in flight together
+  // steps whose loads are in flight together: 8 of 64 codes, 2 of 128, so that the registers leave 7 and 8
+  // waves per SIMD (FP8 with 4 of them: 4 waves, 16 x 14336 x 4096 24.8 us a call for 22.8)
+  constexpr int UN = KIND == 0 ? 8 : 2;
   __shared__ typename S::Acc s_acc[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int r16 = lane & 15, q16 = lane >> 4;
