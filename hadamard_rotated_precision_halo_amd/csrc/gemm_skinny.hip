@@ -435,10 +435,12 @@ hipError_t run(const GemmArgs& g, hipStream_t st) {
 }  // namespace
 
 // Up to 16 rows of 512 and more codes whose slices (of 512) the 8 waves hold at once, in blocks
-// that a slice holds whole, and whose codes fit the default LDS limit.
+// that a slice holds whole.
 bool skinny_fused_ok(int64_t m, int64_t kq, int block) {
-  return m >= 1 && m <= 16 && kq >= 512 && block <= 512 &&
-         m * ((kq + 511) / 512) <= kWaves * kUnits && m * (kq + 16) <= 48 * 1024;
+  // their codes then fit the default LDS limit beside the sums, the slices' maxima and the scales
+  static_assert(kWaves * kUnits * 512 + 16 * 16 + (int)sizeof(v4i) * 2 * kWaves * 64 +
+                        4 * (kWaves * kUnits + 16) <= 64 * 1024, "LDS of skinny_fused_kernel");
+  return m >= 1 && m <= 16 && kq >= 512 && block <= 512 && m * ((kq + 511) / 512) <= kWaves * kUnits;
 }
 
 hipError_t launch_skinny_fused(const GemmArgs& g, const FqArgs& f, int in_bf16, int kind, int out,
