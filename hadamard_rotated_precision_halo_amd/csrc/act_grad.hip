@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
         }
       }
       if constexpr (GLU) {
-        gated_grad<8>(a.act, d, z[0], z[1], g[0], g[1]);
+        gated_grad<8, sizeof(T) == 4>(a.act, d, z[0], z[1], g[0], g[1]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[0][e] = d[e];

@@ -79,23 +79,16 @@ __device__ __forceinline__ float slope_of(float z) {
   return 1.f;
 }
 
-// act(z) and its slope from one exponential, as act_of (without FULL) and slope_of give them.
-template <int ACT>
-__device__ __forceinline__ void act_slope(float z, float* y, float* slope) {
-  *y = act_of<ACT, false>(z);
-  *slope = slope_of<ACT>(z);
-}
-
-// The gradient of a gated pair y = act(g) u for N values: dg = d u act'(g), du = d act(g).
-template <int N>
+// The gradient of a gated pair y = act(g) u for N values: dg = d u act'(g), du = d act(g); FULL: for fp32
+// rows, whose du shows the activation's tail as an fp32 output does.  The slope meets u first: where it
+// is 0 (a gate far below it), d u may pass the largest fp32 value, and 0 times that is NaN.
+template <int N, bool FULL>
 __device__ __forceinline__ void gated_grad(int act, const float* d, const float* g, const float* u,
                                            float* dg, float* du) {
 #define HALO_GATED(A) \
   _Pragma("unroll") for (int e = 0; e < N; ++e) { \
-    float y, s; \
-    act_slope<A>(g[e], &y, &s); \
-    dg[e] = (d[e] * u[e]) * s; \
-    du[e] = d[e] * y; \
+    dg[e] = d[e] * (u[e] * slope_of<A>(g[e])); \
+    du[e] = d[e] * act_of<A, FULL>(g[e]); \
   }
   switch (act) {
     case kActRelu: HALO_GATED(kActRelu) break;

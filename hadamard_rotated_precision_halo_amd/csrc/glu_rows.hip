@@ -155,7 +155,7 @@ __global__ __launch_bounds__(1024) void glu_rows_kernel(GluRowsArgs a) {
     unpack_bf16x8(d[j], dv);
     g[j].get(a.zk, gv);
     u[j].get(a.zk, uv);
-    gated_grad<8>(a.act, dv, gv, uv, &v[0][j * 8], &v[1][j * 8]);
+    gated_grad<8, false>(a.act, dv, gv, uv, &v[0][j * 8], &v[1][j * 8]);
     const int col = col0 + S::off(lane, j);
     if (col < n) {
       float* o = a.dz + row * 2 * n + col;
