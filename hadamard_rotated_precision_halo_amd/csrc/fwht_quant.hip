@@ -486,7 +486,9 @@ static bool staged_rows(const FqArgs& a, int in_bf16) {
 
 hipError_t launch_fwht_quant(const FqArgs& a, int in_bf16, int qt, int axis, void* ws,
                              size_t ws_bytes, hipStream_t st) {
-  if (axis == 0 && fq_rows2_supported(a.len, a.block) && (in_bf16 || !a.sr) && !staged_rows(a, in_bf16))
+  // (fp32 rows with stochastic rounding as far as they fit: the kernels above)
+  if (axis == 0 && fq_rows2_supported(a.len, a.block) && !staged_rows(a, in_bf16) &&
+      (in_bf16 || !a.sr || a.len > fq_rows_max_len(a.block)))
     return launch_fq_rows2(a, in_bf16, qt, st);
   if (axis == 1 && fq_cols2_supported(a.len, a.nvec, a.block, in_bf16, a.sr != 0, ws_bytes))
     return launch_fq_cols2(a, in_bf16, qt, ws, st);

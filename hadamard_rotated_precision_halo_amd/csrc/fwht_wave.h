@@ -1525,5 +1525,6 @@ hipError_t batch_dispatch_sr(int qg, int qw, const FqArgs* rows, const FqArgs& c
                              const FqArgs& cdy, void* ws_dy, const FqArgs& cx, void* ws_x,
                              hipStream_t st);
 hipError_t rows2_dispatch_sr(const FqPair& a, int qt, hipStream_t st);
+hipError_t rows2_dispatch_sr_f32(const FqPair& a, int qt, hipStream_t st);
 
 }  // namespace halo

@@ -1,6 +1,6 @@
 // fwht_wave.hip -- launch interface of the wave-slice rotation kernels (fwht_wave.h): shape
 // support, scratch sizes, and the nearest-even instantiations.  The stochastic-rounding
-// instantiations live in fwht_wave_sr.hip, so the two halves compile in parallel.
+// instantiations live in fwht_wave_sr.hip and fwht_wave_sr_f32.hip, so that they compile in parallel.
 #include "fwht_wave.h"
 
 namespace halo {
@@ -80,10 +80,7 @@ hipError_t launch_fq_batch(const FqArgs* rows, const FqArgs& cw, void* ws_w, con
 hipError_t launch_fq_rows2_pair(const FqPair& a, int in_bf16, int qt, hipStream_t st) {
   // the two passes of one launch share the rounding mode
   if (a.has1 && a.p1.sr != a.p0.sr) return hipErrorInvalidValue;
-  if (a.p0.sr && qt != 3) {  // stochastic rounding: bf16 input (fp32 takes the older kernel)
-    if (!in_bf16) return hipErrorInvalidValue;
-    return rows2_dispatch_sr(a, qt, st);
-  }
+  if (a.p0.sr && qt != 3) return in_bf16 ? rows2_dispatch_sr(a, qt, st) : rows2_dispatch_sr_f32(a, qt, st);
   if (in_bf16) {
     switch (qt) {
       case 0: return rows2_block<uint16_t, 0, false>(a, st);

@@ -99,9 +99,10 @@ halo_status check_signs(const uint32_t* signs) {
 }
 
 // Whether a rows pass over vectors of Lp rotated positions has a kernel: the wave kernel
-// (Lp a multiple of 64, one wave per 4096 positions and up to 16 per row; its stochastic
-// rounding takes bf16 input), else the older kernel, whose workgroup holds a whole row of up
-// to fq_rows_max_len(block) positions.
+// (Lp a multiple of 64, one wave per 4096 positions and up to 16 per row), else the older kernel,
+// whose workgroup holds a whole row of up to fq_rows_max_len(block) positions.  A call of
+// halo_fwht_quant takes the wave kernel for stochastic rounding of bf16 input only; the layer's dY
+// and dz of any type.
 bool rows_len_ok(int64_t Lp, int32_t block, bool in_bf16, bool sr) {
   return (fq_rows2_supported(Lp, block) && (in_bf16 || !sr)) || Lp <= fq_rows_max_len(block);
 }
@@ -434,9 +435,8 @@ halo_status run_fwd(const void* x, const void* w, halo_dtype io_type, int64_t m,
   return s;
 }
 
-// Validation of a layer backward; rot_type: the type dY's rows are rotated in.
-halo_status check_bwd(const void* dy, halo_dtype rot_type, const void* x, const void* w,
-                      halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
+// Validation of a layer backward.
+halo_status check_bwd(const void* dy, const void* x, const void* w, halo_dtype io_type, int64_t m, int64_t n, int64_t k, int32_t block,
                       halo_dtype q_type, halo_dtype grad_q_type, const void* dx, const void* dw,
                       const halo_linear_opts* opts) {
   if (!dy || !x || !w) return HALO_ERR_NULL;
@@ -452,8 +452,7 @@ halo_status check_bwd(const void* dy, halo_dtype rot_type, const void* x, const 
   if (!valid_block(block)) return HALO_ERR_BLOCK;
   const int64_t nq = contraction_len(n, block), mq = contraction_len(m, block);
   if (n % 8 != 0 || k % 8 != 0) return HALO_ERR_SHAPE;
-  const bool sr_dy = opts && opts->grad_rounding == HALO_ROUND_STOCHASTIC;
-  if (dx && !rows_len_ok(nq, block, rot_type == HALO_BF16, sr_dy)) return HALO_ERR_SHAPE;
+  if (dx && !rows_len_ok(nq, block, true, false)) return HALO_ERR_SHAPE;
   if (!operand_fits(m, nq, nq) || !operand_fits(k, nq, nq) || !operand_fits(n, mq, mq) ||
       !operand_fits(k, mq, mq))
     return HALO_ERR_SHAPE;
@@ -1096,7 +1095,7 @@ halo_status halo_linear_bwd_ex(const void* dy, const void* x, const void* w, hal
                                const halo_linear_opts* opts, void* ws, size_t ws_bytes,
                                void* stream) {
   if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
-  const halo_status s = check_bwd(dy, io_type, x, w, io_type, m, n, k, block, q_type, grad_q_type,
+  const halo_status s = check_bwd(dy, x, w, io_type, m, n, k, block, q_type, grad_q_type,
                                   dx, dw, opts);
   if (s != HALO_OK) return s;
   if (!ws || ws_bytes < plan_ws(m, n, k, 1, block).total) return HALO_ERR_WORKSPACE;
@@ -1237,8 +1236,7 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
   if (!dtype_ok(io_type) || !dtype_ok(q_type) || !dtype_ok(grad_q_type)) return HALO_ERR_DTYPE;
   if (!enum_in(activation, HALO_ACT_NONE, HALO_ACT_GELU_ERF)) return HALO_ERR_OPTION;
   const bool act = activation != HALO_ACT_NONE;
-  halo_status s = check_bwd(dy, act ? HALO_F32 : io_type, x, w, io_type, m, n, k, block, q_type,
-                            grad_q_type, dx, dw, opts);
+  halo_status s = check_bwd(dy, x, w, io_type, m, n, k, block, q_type, grad_q_type, dx, dw, opts);
   if (s != HALO_OK) return s;
   if (act && !z) return HALO_ERR_NULL;
   if (!aligned16(z) || !aligned16(db)) return HALO_ERR_ALIGN;
@@ -1377,8 +1375,7 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
   if (!x || (has_dz && !z)) return HALO_ERR_NULL;
   if (n < 0 || n >= kMaxDim / 2 || n % 8 != 0) return HALO_ERR_SHAPE;
   const int64_t nz = glu ? 2 * n : n;
-  halo_status s = check_bwd(dy, has_dz ? HALO_F32 : io_type, x->data, w, io_type, m, nz, k, block,
-                            q_type, grad_q_type, dx, dw, opts);
+  halo_status s = check_bwd(dy, x->data, w, io_type, m, nz, k, block, q_type, grad_q_type, dx, dw, opts);
   if (s == HALO_OK) s = check_kept(x, io_type);
   if (s == HALO_OK && has_dz) s = check_kept(z, io_type);
   if (s != HALO_OK) return s;

@@ -208,8 +208,8 @@ halo_status halo_linear_fwd(const void* x, const void* w, halo_dtype io_type, in
  *   ws           at least halo_linear_workspace_bytes(m, n, k, q_type, 1) bytes.
  * n and k must be multiples of 8, m >= 1; block as for halo_fwht_quant.  Contraction
  * dimensions that block does not divide are zero-padded as in halo_linear_fwd; when dx is
- * computed the padded n is a rows-axis length as in halo_fwht_quant (with stochastic rounding
- * of fp32 dY: at most 16384), and each code matrix spans less than 4 GiB.
+ * computed the padded n is a rows-axis length as in halo_fwht_quant for nearest rounding (whatever
+ * the call's types and rounding), and each code matrix spans less than 4 GiB.
  * With INT8 codes, dW's int32 sums run over the padded m: exact while every partial sum
  * stays within int32, which |codes| <= 127 guarantee up to 133144 terms (as halo_gemm_i8).
  */
@@ -401,8 +401,7 @@ halo_status halo_linear_act_q(const void* x, halo_dtype io_type, const void* qw,
  *   ws           at least halo_linear_act_bwd_workspace_bytes_ex(...) bytes for the call's own
  *                types, activation, gradients and rounding;
  *                halo_linear_act_bwd_workspace_bytes(...) is enough for every form.
- * Everything else as halo_linear_bwd_ex (with an activation, the dX product's padded n is limited
- * under stochastic rounding as for fp32 dY).
+ * Everything else as halo_linear_bwd_ex.
  */
 #define HALO_GRAD_DX 1 /* the gradients a call asks for, as bits */
 #define HALO_GRAD_DW 2
