@@ -17,55 +17,8 @@ namespace {
 
 constexpr int kCols = 512;
 
-template <typename T>
-__global__ __launch_bounds__(256) void act_grad_kernel(const T* dy, const T* z, int act, int64_t m,
-                                                       int64_t n, int64_t rows_per_wg, float* dz,
-                                                       float* part) {
-  __shared__ float s[3][kCols];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * kCols + lane * 8;
-  const int cnt = (int)max((int64_t)0, min((int64_t)8, n - col));
-  const int64_t r0 = (int64_t)blockIdx.y * rows_per_wg, r1 = min(m, r0 + rows_per_wg);
-  float sum[8] = {};
-  if (cnt > 0) {
-    for (int64_t r = r0 + w; r < r1; r += 4) {
-      float d[8], zv[8];
-      load_cols<T>(dy + r * n + col, cnt, d);
-      if (act != kActNone) {
-        load_cols<T>(z + r * n + col, cnt, zv);
-        slope_mul<8>(act, zv, d);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += d[e];
-      if (dz) {
-        float* o = dz + r * n + col;
-        if (cnt == 8) {
-          reinterpret_cast<float4*>(o)[0] = make_float4(d[0], d[1], d[2], d[3]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(d[4], d[5], d[6], d[7]);
-        } else {
-          for (int e = 0; e < cnt; ++e) o[e] = d[e];
-        }
-      }
-    }
-  }
-  if (!part) return;
-  if (w > 0) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[w - 1][e * 64 + lane] = sum[e];
-  }
-  __syncthreads();
-  if (w == 0 && cnt > 0) {
-    float* o = part + (int64_t)blockIdx.y * n + col;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = ((sum[e] + s[0][e * 64 + lane]) + s[1][e * 64 + lane]) + s[2][e * 64 + lane];
-      if (e < cnt) o[e] = v;
-    }
-  }
-}
-
-// The general form: z plain or kept in 8 bits, and the gated layer's pair of halves from one read
-// of dy (dz and db are then 2 n wide, z is 2 m rows of n).
+// z plain or kept in 8 bits; GLU: the gated layer's pair of halves from one read of dy (dz and db are
+// then 2 n wide, z is 2 m rows of n).
 template <typename T, bool GLU>
 __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, float* part) {
   constexpr int H = GLU ? 2 : 1;
@@ -80,17 +33,19 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
     for (int64_t r = r0 + w; r < r1; r += 4) {
       float d[8], z[H][8], g[H][8];
       load_cols<T>(static_cast<const T*>(a.dy) + r * n + col, 8, d);
+      if (GLU || a.act != kActNone) {
 #pragma unroll
-      for (int h = 0; h < H; ++h) {
-        const int64_t zr = r * H + h;
-        if (a.act == kActNone && !GLU) continue;
-        if (a.kept == kKeptPlain) {
-          load_cols<T>(static_cast<const T*>(a.z) + zr * n + col, 8, z[h]);
-        } else {
-          const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.z) + zr * n + col);
-          const uint32_t p = a.zp[zr * groups + col / kGroup];
-          if (a.kept == kKeptI8) kept8<0>(q, p, z[h]);
-          else kept8<1>(q, p, z[h]);
+        for (int h = 0; h < H; ++h) {
+          const int64_t zr = r * H + h;
+          if (a.kept == kKeptPlain) {
+            load_cols<T>(static_cast<const T*>(a.z) + zr * n + col, 8, z[h]);
+          } else {
+            const uint2 q =
+                *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.z) + zr * n + col);
+            const uint32_t p = a.zp[zr * groups + col / kGroup];
+            if (a.kept == kKeptI8) kept8<0>(q, p, z[h]);
+            else kept8<1>(q, p, z[h]);
+          }
         }
       }
       if constexpr (GLU) {
@@ -98,13 +53,14 @@ __global__ __launch_bounds__(256) void dz_kernel(DzArgs a, int64_t rows_per_wg, 
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) g[0][e] = d[e];
-        slope_mul<8>(a.act, z[0], g[0]);
+        if (a.act != kActNone) slope_mul<8>(a.act, z[0], g[0]);
       }
 #pragma unroll
       for (int h = 0; h < H; ++h) {
-        float* o = a.dz + r * (n * H) + h * n + col;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[h][e] += g[h][e];
+        if (!a.dz) continue;
+        float* o = a.dz + r * (n * H) + h * n + col;
         reinterpret_cast<float4*>(o)[0] = make_float4(g[h][0], g[h][1], g[h][2], g[h][3]);
         reinterpret_cast<float4*>(o)[1] = make_float4(g[h][4], g[h][5], g[h][6], g[h][7]);
       }
@@ -153,21 +109,7 @@ int64_t rows_per(int64_t m, int64_t n) {
 }
 
 template <typename T>
-hipError_t run(const void* dy, const void* z, int act, int64_t m, int64_t n, float* dz, void* db,
-               float* part, hipStream_t st) {
-  const int64_t rows = rows_per(m, n), parts = (m + rows - 1) / rows;
-  hipLaunchKernelGGL((act_grad_kernel<T>), dim3((unsigned)((n + kCols - 1) / kCols), (unsigned)parts),
-                     dim3(256), 0, st, static_cast<const T*>(dy), static_cast<const T*>(z), act, m,
-                     n, rows, dz, db ? part : nullptr);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !db) return e;
-  hipLaunchKernelGGL((part_sum_kernel<T>), dim3((unsigned)((n + 63) / 64)), dim3(256), 0, st, part,
-                     parts, n, static_cast<T*>(db));
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t run_dz(const DzArgs& a, hipStream_t st) {
+hipError_t run(const DzArgs& a, hipStream_t st) {
   const int64_t rows = rows_per(a.m, a.n), parts = (a.m + rows - 1) / rows;
   const int64_t width = a.glu ? 2 * a.n : a.n;
   const dim3 grid((unsigned)((a.n + kCols - 1) / kCols), (unsigned)parts);
@@ -184,7 +126,7 @@ hipError_t run_dz(const DzArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_dz(const DzArgs& a, int in_bf16, hipStream_t st) {
-  return in_bf16 ? run_dz<uint16_t>(a, st) : run_dz<float>(a, st);
+  return in_bf16 ? run<uint16_t>(a, st) : run<float>(a, st);
 }
 
 hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t* db,
@@ -197,12 +139,6 @@ hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t
 int64_t act_grad_parts(int64_t m, int64_t n) {
   const int64_t rows = rows_per(m, n);
   return (m + rows - 1) / rows;
-}
-
-hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
-                           int64_t n, float* dz, void* db, float* part, hipStream_t st) {
-  return in_bf16 ? run<uint16_t>(dy, z, act, m, n, dz, db, part, st)
-                 : run<float>(dy, z, act, m, n, dz, db, part, st);
 }
 
 }  // namespace halo

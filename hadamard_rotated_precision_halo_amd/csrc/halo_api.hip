@@ -1257,8 +1257,8 @@ halo_status halo_linear_act_bwd(const void* dy, const void* z, halo_activation a
                    st, &ag);
   }
   if (act || db) {
-    const hipError_t e = launch_act_grad(dy, z, (int)activation, io_type == HALO_BF16 ? 1 : 0, m, n,
-                                         act ? dz : nullptr, db, part, st);
+    const DzArgs a{dy, z, nullptr, kKeptPlain, (int)activation, 0, m, n, act ? dz : nullptr, db, part};
+    const hipError_t e = launch_dz(a, io_type == HALO_BF16 ? 1 : 0, st);
     if (e != hipSuccess) return HALO_ERR_HIP;
   }
   return run_bwd(act ? dz : dy, act ? HALO_F32 : io_type, x, w, io_type, m, n, k, block, q_type,
@@ -1412,7 +1412,8 @@ halo_status kept_bwd(const void* dy, const halo_kept* z, const halo_activation& 
                    db, part};
     e = launch_dz(a, inb, st);
   } else if (db) {
-    e = launch_act_grad(dy, nullptr, (int)HALO_ACT_NONE, inb, m, n, nullptr, db, part, st);
+    const DzArgs a{dy, nullptr, nullptr, kKeptPlain, (int)HALO_ACT_NONE, 0, m, n, nullptr, db, part};
+    e = launch_dz(a, inb, st);
   }
   const void* xv = x->data;
   if (e == hipSuccess && dw && kept_form(x->type) != kKeptPlain) {

@@ -196,26 +196,23 @@ bool skinny_fused_ok(int64_t m, int64_t kq, int block);
 hipError_t launch_skinny_fused(const GemmArgs& g, const FqArgs& f, int in_bf16, int kind, int out,
                                hipStream_t st);
 
-// dz = dy act'(z) in fp32 and, when db is not NULL, db = its sums over the m rows (bias type:
-// that of dy).  part: act_grad_parts(m, n) x n floats of scratch (db only).
+// Rows of partial sums that launch_dz makes for its db.
 int64_t act_grad_parts(int64_t m, int64_t n);
 // db (bf16) = the sum of `parts` rows of part, in order.
 hipError_t launch_part_sum(const float* part, int64_t parts, int64_t n, uint16_t* db,
                            hipStream_t st);
-hipError_t launch_act_grad(const void* dy, const void* z, int act, int in_bf16, int64_t m,
-                           int64_t n, float* dz, void* db, float* part, hipStream_t st);
 
-// The general form: dz in fp32 of a layer whose z is plain (kept 0) or a checkpoint (kept: a Kept of
-// checkpoint.h, zp its powers), or of the gated layer (glu: z is 2 m rows of n, dz [m x 2 n], db
-// [2 n], part act_grad_parts(m, n) x 2 n).
+// dz = dy act'(z) in fp32 of a layer whose z is plain (kept 0) or a checkpoint (kept: a Kept of
+// checkpoint.h, zp its powers), or of the gated layer (glu: z is 2 m rows of n, dz [m x 2 n], db [2 n]),
+// and its sums db over the rows (bias type: that of dy).  n is a multiple of 8.
 struct DzArgs {
-  const void *dy, *z;
+  const void *dy, *z;  // z is not read without an activation or a gate
   const uint8_t* zp;
   int kept, act, glu;
   int64_t m, n;
-  float* dz;
-  void* db;     // or NULL
-  float* part;
+  float* dz;           // or NULL
+  void* db;            // or NULL
+  float* part;         // scratch of db: act_grad_parts(m, n) x (glu ? 2 n : n)
 };
 hipError_t launch_dz(const DzArgs& a, int in_bf16, hipStream_t st);
 
