@@ -186,14 +186,15 @@ __global__ __launch_bounds__(64 * kWaves) void skinny_kernel(GemmArgs g) {
 }
 
 // The same with z kept in 8 bits: a workgroup holds the 2 (gated: 4) runs of columns that make a group
-// of 32.  Every sum runs as above, so y and z have the same bits however z is kept.  LOADS: 64-byte loads
-// of a row in flight together, as many as a wave has (steps behind its last would read it again: gated, 16
-// x 2 x 2048 x 1024 a call with 8 of them 20.2 us, with 2 13.6).
-template <int KIND, int OUT, bool GLU, int LOADS>
+// of 32.  Every sum runs as above, so y and z have the same bits however z is kept.  Two 64-byte loads of
+// every run are in flight together: with eight, steps behind a wave's last are read again (gated, 16 x 2 x
+// 512 x 2048 a call 18.7 us for 14.5).  Another kernel whose waves split the contraction through the LDS took
+// 13.8 there, and 66 us for 75 at 16 x 2 x 4096 x 11008, with other last bits.
+template <int KIND, int OUT, bool GLU>
 __global__ __launch_bounds__(64 * kWaves) void skinny_kept_kernel(GemmArgs g) {
   using S = Step<KIND>;
   using T = typename std::conditional<OUT == 2, uint16_t, float>::type;
-  constexpr int UN = LOADS / S::CH, RUNS = kGroup / kCols<GLU>, H = GLU ? 2 : 1;
+  constexpr int UN = 2 / S::CH, RUNS = kGroup / kCols<GLU>, H = GLU ? 2 : 1;
   static_assert(RUNS * 16 * kCols<GLU> == 64 * kWaves, "a thread per element of the group's rows");
   __shared__ typename S::Acc s_acc[RUNS][kWaves][64];
   __shared__ ZTile s_z[16 * H];
@@ -416,11 +417,9 @@ hipError_t run_fused_x(const GemmArgs& g, const FqArgs& f, int kind, int out, hi
 
 template <int KIND, int OUT, bool GLU>
 hipError_t run_form(const GemmArgs& g, hipStream_t st) {
-  const dim3 groups((unsigned)((g.n + kGroup - 1) / kGroup));
-  if (g.kept && g.k <= 2 * 64 * kWaves)
-    hipLaunchKernelGGL((skinny_kept_kernel<KIND, OUT, GLU, 2>), groups, dim3(64 * kWaves), 0, st, g);
-  else if (g.kept)
-    hipLaunchKernelGGL((skinny_kept_kernel<KIND, OUT, GLU, 8>), groups, dim3(64 * kWaves), 0, st, g);
+  if (g.kept)
+    hipLaunchKernelGGL((skinny_kept_kernel<KIND, OUT, GLU>), dim3((unsigned)((g.n + kGroup - 1) / kGroup)),
+                       dim3(64 * kWaves), 0, st, g);
   else
     hipLaunchKernelGGL((skinny_kernel<KIND, OUT, GLU>),
                        dim3((unsigned)((g.n + kCols<GLU> - 1) / kCols<GLU>)), dim3(64 * kWaves), 0, st, g);

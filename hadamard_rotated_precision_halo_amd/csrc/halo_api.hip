@@ -239,9 +239,11 @@ halo_status check_gemm(const void* a, int64_t lda, const void* b, int64_t ldb, i
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Room of one columns pass in the layer's workspace: its scratch, and for columns of up to 4096 rows,
-// which go whole into one task and exchange nothing, what parts that divide them would exchange: the
-// size of a workspace for a given layer stays what it was with such parts, and callers hold it.
+// Room of one columns pass in the layer's workspace: its scratch.  Columns of up to 4096 rows go whole
+// into one task and use none; the size keeps for them what parts that divide them would exchange (768 rows
+// of block 256: counters and a maximum per column), so that a size once computed for such a layer stays
+// enough.  Longer columns need what the query says now: their strips of 64 columns have more counters than
+// the wider strips of parts that divided them (13824 x 5120 at block 128: 21248 bytes for 20992).
 size_t cols_room(int64_t len, int64_t nvec, int32_t block) {
   if (len > 4096 || len < 64) return round256(fq_ws_bytes_len(len, nvec, HALO_ALONG_COLS, block));
   int64_t part = 4096;

@@ -188,7 +188,10 @@ hipError_t launch_gemm_pair(const GemmArgs& g, const GemmArgs* g1, int kind, int
 hipError_t launch_gemm_act(const GemmArgs& g, int kind, int out, hipStream_t st);
 // The same with the contraction split over a workgroup's waves, for few tiles (gemm_ksplit.hip).
 hipError_t launch_gemm_ksplit(const GemmArgs& g, int kind, int out, hipStream_t st);
-// The same for up to kSkinnyRows rows of a (gemm_skinny.hip).
+// The same for up to kSkinnyRows rows of a (gemm_skinny.hip).  From 5 rows on wide layers would be faster
+// on the 64 tiles (INT8, 2 x 11008 x 4096, 16 rows 29.0 us a call, 23.6 there; 11008 x 4096 18.4, 18.0;
+// 4096 x 4096 11.3, 15.4), whose z is rounded once and not twice: the fewest rows, quantised inside, and the
+// forward of the same rows would then differ in last bits.
 constexpr int kSkinnyRows = 16;
 hipError_t launch_gemm_skinny(const GemmArgs& g, int kind, int out, hipStream_t st);
 // The same with the rows pass f (its codes and scales stay inside) of m rows in one launch.
