@@ -937,6 +937,11 @@ __device__ __forceinline__ void cols_act(const ColsProb& pr, int part, int t, in
   const int i = t / (pr.C / 4);
   const int64_t r0 = (int64_t)part * pr.R + f32_group<B>(i, h) * 8;
   const uint32_t flip = HERE && a.signs ? row_signs(a, r0) : 0u;
+  if (r0 >= a.in_len) {  // 8 rows of the padding, or behind the column's end
+#pragma unroll
+    for (int e = 0; e < 8; ++e) raw[e] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
   // a row at a time: few values live beside the tile's
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -1306,8 +1311,11 @@ __global__ __launch_bounds__(kColsThreads) void fq_batch_kernel(FqBatch fb) {
 // columns, or a wider tile for shorter columns): no exchange of partial maxima at all, and the
 // strips' XCD-aware order keeps their 32-byte row segments fetched once per 128-byte line.  Longer
 // columns take 1024-row tasks (64-column strips, full 128-byte row segments) and exchange their
-// partial maxima.  Lengths that the tasks do not divide leave part of the last one idle: smaller
-// tasks that divide them exchange among more parts (11008 x 4096 bf16, 43 parts of 256: 77.8 us).
+// partial maxima.  Lengths that the tasks do not divide leave part of the last one idle; smaller tasks
+// that divide them exchange, among more parts.  bf16, us here and in parts that divide the length:
+// 1088 x 4096 9.5, 17.8; 3584 x 11008 40, 56; 5504 x 4096 37.7, 39.8; 11008 x 4096 68.0, 73.3; but 5504 x 64
+// 14.8, 13.4, 22016 x 1024 43.1, 40.7, 22016 x 4096 139, 144.  The gradient of 3000 tokens, whole and in parts of
+// 1024: 14336 x 4096 507, 491, 4096 x 1024 63, 82.
 static int cols2_rows_per_task(int64_t rows, int block) {
   if (rows < 64 || block > 4096) return 0;
   int R = 64;
