@@ -85,3 +85,20 @@ def test_more_rows_than_a_launch_has_threads():
     if torch.cuda.mem_get_info()[0] < 150 * 2 ** 30:
         pytest.skip("137 GB of codes")
     _long_call(rows, 8, 4096)
+
+
+@pytest.mark.parametrize("cols,block", [(320, 64), (1088, 16), (3136, 64)])
+def test_large_fp32_calls_have_the_bits_of_small_ones(cols, block):
+    # past 2^25 elements such rows take another kernel
+    rows = 2 ** 25 // cols + 40
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    x = torch.randn((rows, cols), generator=g, device=DEV)
+    signs = H.hadamard_signs(cols, 3, DEV)
+    for kw in ({}, dict(signs=signs, q_dtype=torch.float8_e4m3fn)):
+        q, s = H.fwht_quant(x, H.ROWS, block, **kw)
+        for at in (0, rows // 2):
+            part = x[at:at + rows // 2]
+            want = H.fwht_quant(part, H.ROWS, block, **kw)
+            assert torch.equal(q[at:at + rows // 2].view(torch.uint8), want[0].view(torch.uint8))
+            assert torch.equal(s[at:at + rows // 2], want[1])
