@@ -66,6 +66,7 @@ KERNEL_SOURCES = ["hadamard_rotated_precision_halo_amd/csrc/gemm.hip",
                   "hadamard_rotated_precision_halo_amd/csrc/fwht_quant.hip",
                   "hadamard_rotated_precision_halo_amd/csrc/fwht_wave.h",
                   "hadamard_rotated_precision_halo_amd/csrc/fwht_wave.hip",
+                  "hadamard_rotated_precision_halo_amd/csrc/fwht_wave_rows.hip",
                   "hadamard_rotated_precision_halo_amd/csrc/fwht_wave_sr.hip",
                   "hadamard_rotated_precision_halo_amd/csrc/halo_device.h",
                   "hadamard_rotated_precision_halo_amd/csrc/halo_kernels.h"]

@@ -8,7 +8,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libhalo.so")
-SOURCES = ["halo_api.hip", "fwht_quant.hip", "fwht_wave.hip", "fwht_wave_sr.hip", "fwht_wave_sr_f32.hip",
+SOURCES = ["halo_api.hip", "fwht_quant.hip", "fwht_wave.hip", "fwht_wave_rows.hip", "fwht_wave_sr.hip",
+           "fwht_wave_sr_rows.hip", "fwht_wave_sr_f32.hip",
            "fwht_wave_act.hip",
            "fwht_wave_kept.hip", "fwht_wave_kept_e5m2.hip", "fwht_wave_kept_e4m3.hip", "glu_rows.hip",
            "fwht_dual.hip",

@@ -44,7 +44,7 @@
 // one bit per element, applied before the butterflies), zero padding of vectors whose length
 // the block does not divide ("QWHA方法：基于Walsh-Hadamard变换的高效大模型微调技术" s5: in_len
 // input elements, len rotated positions), and stochastic rounding of the codes (the same s5;
-// a template parameter, instantiated in fwht_wave_sr.hip).
+// a template parameter, instantiated in fwht_wave_sr*.hip).
 #pragma once
 
 #include "checkpoint.h"
@@ -1526,12 +1526,14 @@ static hipError_t rows2_block(const FqPair& a, hipStream_t st) {
 #undef HALO_R2_CASE
 }
 
-// Stochastic-rounding instantiations of the launches (compiled in fwht_wave_sr.hip).
+// Stochastic-rounding instantiations of the launches (compiled in fwht_wave_sr*.hip), and the rows
+// launch of nearest codes and rotated values (fwht_wave_rows.hip).
 hipError_t cols2_dispatch_sr(const FqArgs& a0, void* ws0, const FqArgs* a1, void* ws1, int qt,
                              int prezeroed, hipStream_t st);
 hipError_t batch_dispatch_sr(int qg, int qw, const FqArgs* rows, const FqArgs& cw, void* ws_w,
                              const FqArgs& cdy, void* ws_dy, const FqArgs& cx, void* ws_x,
                              hipStream_t st);
+hipError_t rows2_dispatch(const FqPair& a, int in_bf16, int qt, hipStream_t st);
 hipError_t rows2_dispatch_sr(const FqPair& a, int qt, hipStream_t st);
 hipError_t rows2_dispatch_sr_f32(const FqPair& a, int qt, hipStream_t st);
 

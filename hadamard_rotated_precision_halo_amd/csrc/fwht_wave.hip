@@ -1,6 +1,7 @@
 // fwht_wave.hip -- launch interface of the wave-slice rotation kernels (fwht_wave.h): shape
-// support, scratch sizes, and the nearest-even instantiations.  The stochastic-rounding
-// instantiations live in fwht_wave_sr.hip and fwht_wave_sr_f32.hip, so that they compile in parallel.
+// support, scratch sizes, and the nearest-even instantiations of the columns and batch kernels.  The
+// rows kernels (fwht_wave_rows.hip) and those with stochastic rounding (fwht_wave_sr*.hip) are files of
+// their own, so that they compile in parallel.
 #include "fwht_wave.h"
 
 namespace halo {
@@ -81,22 +82,7 @@ hipError_t launch_fq_rows2_pair(const FqPair& a, int in_bf16, int qt, hipStream_
   // the two passes of one launch share the rounding mode
   if (a.has1 && a.p1.sr != a.p0.sr) return hipErrorInvalidValue;
   if (a.p0.sr && qt != 3) return in_bf16 ? rows2_dispatch_sr(a, qt, st) : rows2_dispatch_sr_f32(a, qt, st);
-  if (in_bf16) {
-    switch (qt) {
-      case 0: return rows2_block<uint16_t, 0, false>(a, st);
-      case 1: return rows2_block<uint16_t, 1, false>(a, st);
-      case 2: return rows2_block<uint16_t, 2, false>(a, st);
-      case 3: return rows2_block<uint16_t, 3, false>(a, st);
-    }
-  } else {
-    switch (qt) {
-      case 0: return rows2_block<float, 0, false>(a, st);
-      case 1: return rows2_block<float, 1, false>(a, st);
-      case 2: return rows2_block<float, 2, false>(a, st);
-      case 3: return rows2_block<float, 3, false>(a, st);
-    }
-  }
-  return hipErrorInvalidValue;
+  return rows2_dispatch(a, in_bf16, qt, st);
 }
 
 hipError_t launch_fq_rows2(const FqArgs& a, int in_bf16, int qt, hipStream_t st) {

@@ -1,4 +1,4 @@
-// fwht_wave_sr.hip -- the stochastic-rounding instantiations of the wave-slice rotation
+// fwht_wave_sr.hip -- the stochastic-rounding instantiations of the wave-slice columns and batch
 // kernels (fwht_wave.h), for the code types INT8, E4M3 and E5M2 and bf16 input.  Stochastic
 // rounding ("QWHA方法：基于Walsh-Hadamard变换的高效大模型微调技术" s5) draws one Philox4x32-10
 // uniform per element; see store_chunk8_sr.
@@ -22,15 +22,6 @@ hipError_t batch_dispatch_sr(int qg, int qw, const FqArgs* rows, const FqArgs& c
   if (qg == 0 && qw == 0) return batch_block<0, 0, true>(cw.block, rows, cw, ws_w, cdy, ws_dy, cx, ws_x, st);
   if (qg == 2 && qw == 1) return batch_block<2, 1, true>(cw.block, rows, cw, ws_w, cdy, ws_dy, cx, ws_x, st);
   if (qg == 1 && qw == 1) return batch_block<1, 1, true>(cw.block, rows, cw, ws_w, cdy, ws_dy, cx, ws_x, st);
-  return hipErrorInvalidValue;
-}
-
-hipError_t rows2_dispatch_sr(const FqPair& a, int qt, hipStream_t st) {
-  switch (qt) {
-    case 0: return rows2_block<uint16_t, 0, true>(a, st);
-    case 1: return rows2_block<uint16_t, 1, true>(a, st);
-    case 2: return rows2_block<uint16_t, 2, true>(a, st);
-  }
   return hipErrorInvalidValue;
 }
 
