@@ -86,13 +86,13 @@ TRAFFIC_JSON = os.path.join(ROOT, "profiles", "traffic_4096.json")
 GEMM_GRID = 256 * 512
 PASSES = {
     "gemm_i8_4096": (["halo::gemm_kernel<0"], GEMM_GRID),
-    "fq_rows_4096": (["halo::fq_rows2_kernel<unsigned short, 256, 0, false>"], None),
+    "fq_rows_4096": (["halo::fq_rows2_kernel<unsigned short, 256, 0, false, 0>"], None),
     "fq_cols_4096": (["halo::fq_cols2_kernel<256, 0, false, false, false>"], None),
     "gemm_fp8_4096": (["halo::gemm_kernel<1"], GEMM_GRID),
-    "fq_rows_opt_4096": (["halo::fq_rows2_kernel<unsigned short, 256, 0, true>"], None),
+    "fq_rows_opt_4096": (["halo::fq_rows2_kernel<unsigned short, 256, 0, true, 0>"], None),
     "fq_cols_opt_4096": (["halo::fq_cols2_kernel<256, 0, true, false, false>"], None),
     "copy_neg": (["neg_kernel"], None),  # 64 MiB calibration, or the 512 MiB copy reference
-    "fq_batch_4096": (["halo::fq_batch_kernel<256, 0, 0, false, false>"], None),
+    "fq_batch_4096": (["halo::fq_batch_kernel<256, 0, 0, false, false, 0, false>"], None),
     "gemm_i8_pair_4096": (["halo::gemm_kernel<0"], 2 * GEMM_GRID),
     "fq_dual_4096": (["fq_dual_kernel<256, 0, false, false>"], None),
     "fq_cols_f32_4096": (["halo::fq_cols2_kernel<256, 0, false, false, true>"], None),
